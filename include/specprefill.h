@@ -327,6 +327,159 @@ sp_status sp_gather_kept(const int32_t* token_ids, int B, const int64_t* cu_M_ho
                          void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Positions, the paged cache, and attention over it                        */
+/* ------------------------------------------------------------------------ */
+
+/* Rows of a tensor [rows, heads, d]: entry i of (row, head) is at
+ * data[row * stride_row + head * stride_head + i] (strides in entries).  data
+ * is 16-byte aligned and both strides are multiples of 16 bytes, so a slice
+ * of a fused projection is taken as it lies. */
+typedef struct {
+    void*   data;
+    int64_t stride_row, stride_head;
+} sp_rows;
+
+/* Rotary frequencies.  Filled by sp_rotary_plan_init and then read only;
+ * `turns` holds each pair's turns per position as a 64-bit fraction. */
+typedef struct {
+    int32_t  rot;             /* entries of a head that are rotated (the first ones) */
+    int32_t  interleaved;
+    int32_t  axes;
+    uint64_t turns[128];
+    uint8_t  axis[128];
+} sp_rotary_plan;
+
+/* Fills `plan` (host memory).  rot: even, 2 .. 256, a multiple of 16.  Pair i
+ * (i < rot / 2) is entries (i, i + rot / 2) of a head, or (2i, 2i + 1) if
+ * `interleaved`; it turns by inv_freq_host[i] radians a position (finite) of
+ * axis axis_of_pair_host[i] (< axes <= 8; NULL: axis 0).  Several axes are the
+ * positions of image and video tokens: time, height, width. */
+sp_status sp_rotary_plan_init(sp_rotary_plan* plan, int rot, const double* inv_freq_host,
+                              const uint8_t* axis_of_pair_host, int axes, int interleaved);
+
+/* Rotates queries and keys at their original positions (paper review,
+ * "position ID recovery": the kept tokens keep their positions): each pair
+ * (x0, x1) becomes (x0 cos a - x1 sin a, x1 cos a + x0 sin a), a = position *
+ * frequency, or -a if `inverse` != 0 (which undoes the rotation and is its
+ * gradient).  Entries past plan->rot are copied.
+ *
+ *   positions   device int32 [axes, T], axis a at positions[a * pos_stride]; any int32 value, the
+ *               angle is exact to fp32 rounding at all of them (sp_gather_kept's out_positions)
+ *   q, q_out    [T, H, d]     in and out may be the same rows, and must not overlap otherwise
+ *   k, k_out    [T, H_kv, d]  H or H_kv may be 0: that pair of tensors is left out
+ *
+ * Requirements: T >= 0, 8 <= d <= 256, d % 8 == 0, rot <= d.  No workspace.
+ * Products and sums are fp32, rounded once. */
+sp_status sp_rotary(const sp_rotary_plan* plan, const int32_t* positions, int64_t pos_stride, int64_t T, int d,
+                    sp_dtype dtype, int inverse, const sp_rows* q, const sp_rows* q_out, int H, const sp_rows* k,
+                    const sp_rows* k_out, int H_kv, void* stream);
+
+/* How a cache holds its rows.  A row is one token's d entries of one head.
+ *   SP_CACHE_SAME  as they are, in `dtype`
+ *   SP_CACHE_E4M3  8-bit floats (4 exponent bits, 3 mantissa bits), largest 448
+ *   SP_CACHE_INT8  8-bit integers in [-127, 127]
+ * The 8-bit kinds divide each row by its own scale, a power of two: the
+ * smallest 2^k, k >= -100, with max|x| / 2^k <= 448 or 127 (1 for a row of
+ * zeros), and round x / 2^k to the nearest code, ties to even.  With a power
+ * of two the division is exact, and code * scale is a bf16 value, so reading
+ * a cache back rounds nothing (for codes * scale above bf16's smallest normal).  A row that holds a NaN or an infinity gets
+ * the scale NaN and reads back as NaN. */
+typedef enum { SP_CACHE_SAME = 0, SP_CACHE_E4M3 = 1, SP_CACHE_INT8 = 2 } sp_cache_kind;
+
+/* One layer's keys and values in pages of `page` tokens: the row of (page p,
+ * head h, slot s) starts at entry p * stride_page + h * stride_head + s *
+ * stride_slot of k and of v (entries of `dtype`, or bytes of the 8-bit kinds);
+ * 16-byte aligned (8-byte for the 8-bit kinds), strides likewise.  So
+ * [pages, H_kv, page, d] and [pages, page, H_kv, d] are both taken. */
+typedef struct {
+    void*         k;
+    void*         v;
+    float*        k_scale;     /* 8-bit kinds: [pages, H_kv, page], contiguous; else NULL */
+    float*        v_scale;
+    int64_t       stride_page, stride_head, stride_slot;
+    int64_t       pages;
+    int32_t       page, H_kv, d;
+    sp_dtype      dtype;       /* of the rows written, read back and attended */
+    sp_cache_kind kind;
+} sp_cache;
+
+/* The new tokens of B sequences, and where they stand.  Sequence b's new
+ * tokens are rows cu_new[b] .. cu_new[b+1] - 1 of the call's tensors and the
+ * last ones of its kv_len[b] tokens: row cu_new[b] + t is token
+ * kv_len[b] - (cu_new[b+1] - cu_new[b]) + t.  Token i of the sequence is in
+ * slot i % page of page table[b * table_stride + i / page].  All arrays are on
+ * the device and read when the work runs, so a captured call follows their
+ * contents; sp_gather_kept's cu_kept and sp_select_varlen's n_kept are such
+ * arrays.  Rows before cu_new[0] and from cu_new[B] on are not touched.
+ *
+ * What the device arrays say is checked when the work runs.  A sequence is
+ * left out, and SP_EDEVICE recorded in the workspace, unless
+ * 0 <= cu_new[b] <= cu_new[b+1] <= T, cu_new[b+1] - cu_new[b] <= max_new and
+ * 0 <= kv_len[b] <= table_width * page (and <= 2^31 - 1 - page).  A page index outside
+ * [0, pages) is never followed: SP_EDEVICE is recorded, its tokens are not
+ * written, read back as zeros, and are attended as if they were zeros or left out. */
+typedef struct {
+    int32_t        B;          /* >= 1 */
+    int32_t        max_new;    /* at least the largest number of new tokens of a sequence */
+    int64_t        T;          /* rows of the call's tensors, at most 2^31 - 1 */
+    const int64_t* cu_new;     /* device [B + 1] */
+    const int64_t* kv_len;     /* device [B] */
+    const int32_t* table;      /* device [B, table_width] */
+    int32_t        table_width;
+    int64_t        table_stride;
+} sp_batch;
+
+/* Workspace bytes of sp_cache_write and sp_cache_read (they keep their status there). */
+size_t sp_cache_workspace_size(void);
+
+/* Writes the new tokens' keys and values, k_new and v_new [T, H_kv, d], to
+ * their places in the cache, quantising as the cache's kind says.  A new
+ * token whose place would be negative (kv_len below the number of new tokens) is
+ * skipped.  No other slot of the cache is touched. */
+sp_status sp_cache_write(const sp_cache* cache, const sp_batch* batch, const sp_rows* k_new, const sp_rows* v_new,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* Reads the batch's "new" tokens back into out_k and out_v [T, H_kv, d] in the
+ * cache's dtype; either may be NULL.  With cu_new the prompts' offsets, kv_len
+ * their lengths and the rows of layer l of a [L, H_kv, T, d] tensor
+ * (stride_row d, stride_head T * d) this makes sp_score's K_prompt, or
+ * sp_score_varlen's, from a paged cache.  A token whose place would be
+ * negative reads as zeros. */
+sp_status sp_cache_read(const sp_cache* cache, const sp_batch* batch, const sp_rows* out_k, const sp_rows* out_v,
+                        void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes sp_attend needs for this cache, batch and number of query
+ * heads on the current device (0 if they are invalid).  Depends on T, max_new,
+ * B, H, H_kv and d, not on the contents of the batch's device arrays. */
+size_t sp_attend_workspace_size(const sp_cache* cache, const sp_batch* batch, int H);
+
+/* Causal attention of the new tokens over their sequences' cached tokens (the
+ * new tokens' own keys and values are already in the cache):
+ *
+ *   out[r, h] = sum_i softmax_i(scale * q[r, h] . k_i) v_i,  lse[r, h] = ln sum_i exp(scale * q[r, h] . k_i)
+ *
+ * over the tokens i <= p of the row's sequence, p its own place, and i > p -
+ * window if window > 0.  Query head h reads KV head h / (H / H_kv).  A row
+ * that sees no token (p < 0) gets out = 0 and lse = -inf.  One call is a
+ * prefill chunk, a decode step, or a mixture of them.  The lse of the
+ * look-ahead decode steps is what sp_score_lse takes.
+ *
+ *   q, out   [T, H, d] in the cache's dtype
+ *   lse      fp32, lse[r * lse_stride_row + h * lse_stride_head], or NULL.  Step j of N
+ *            look-ahead steps of one request (T = 1, layer l of sp_score_lse's lse [L, H, N]):
+ *            pointer lse + l * H * N + j, lse_stride_head = N
+ *
+ * Requirements: 8 <= d <= 256, d % 8 == 0, H % H_kv == 0, scale > 0 and
+ * finite.  What unwritten slots hold (NaN too) has no effect, nor have rows
+ * that are not a token of the batch.  A NaN or an infinity in a key or value of a token that
+ * some rows of the sequence see may reach its other rows as well.
+ * Statistics and sums are fp32; bf16 softmax weights are rounded to bf16 for
+ * the product with the values. */
+sp_status sp_attend(const sp_rows* q, const sp_cache* cache, const sp_batch* batch, int H, double scale,
+                    int64_t window, const sp_rows* out, float* lse, int64_t lse_stride_row,
+                    int64_t lse_stride_head, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Status                                                                   */
 /* ------------------------------------------------------------------------ */
 

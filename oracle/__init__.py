@@ -40,3 +40,4 @@ from .select import (  # noqa: F401
     mass_chunks, kept_positions, select, select_varlen, keep_rules, select_mask, select_rules,
 )
 from .gather import gather_kept  # noqa: F401,E402
+from . import paged  # noqa: F401,E402

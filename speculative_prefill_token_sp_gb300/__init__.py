@@ -26,11 +26,17 @@ __all__ = [
     "sp_gather_kept", "sp_workspace_status", "sp_last_error", "sp_status_string", "sp_version",
     "sp_kernel_launches", "sp_test_set_exchange_wait_ns", "sp_test_score_plan",
     "score", "score_lse", "score_prefill", "score_varlen", "score_lse_varlen", "select", "select_rules", "select_varlen", "gather_kept", "V3_BOOST",
+    "SP_CACHE_SAME", "SP_CACHE_E4M3", "SP_CACHE_INT8", "SpRows", "SpRotaryPlan", "SpCache", "SpBatch",
+    "sp_rotary_plan_init", "sp_rotary", "sp_cache_workspace_size", "sp_cache_write", "sp_cache_read",
+    "sp_attend_workspace_size", "sp_attend",
+    "rotary_plan", "rotary", "Cache", "Batch", "cache_alloc", "cache_write", "cache_read", "attend_workspace_size",
+    "attend",
 ]
 
 SP_OK, SP_EINVAL, SP_ENOMEM, SP_ECUDA, SP_EDEVICE, SP_ETIMEOUT, SP_EUNSUPPORTED = range(7)
 SP_BF16, SP_F32 = 0, 1
 SP_SELECT_TOPK, SP_SELECT_MASS = 0, 1
+SP_CACHE_SAME, SP_CACHE_E4M3, SP_CACHE_INT8 = 0, 1, 2
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libspecprefill.so")
@@ -54,6 +60,32 @@ class SpKeepRules(ctypes.Structure):
 
 # The rules the llama.cpp guide runs with: min_tok 128, always-kept tokens, SP_MAX_KEEP 2000.
 GUIDE_RULES = (128, 1, 2000)
+
+
+class SpRows(ctypes.Structure):
+    """sp_rows: a tensor [rows, heads, d] by its address and strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_row", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
+
+
+class SpRotaryPlan(ctypes.Structure):
+    """sp_rotary_plan: frequencies, filled by sp_rotary_plan_init."""
+    _fields_ = [("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("turns", ctypes.c_uint64 * 128), ("axis", ctypes.c_uint8 * 128)]
+
+
+class SpCache(ctypes.Structure):
+    """sp_cache: one layer's paged keys and values."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("stride_page", ctypes.c_int64), ("stride_head", ctypes.c_int64),
+                ("stride_slot", ctypes.c_int64), ("pages", ctypes.c_int64), ("page", ctypes.c_int32),
+                ("H_kv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("kind", ctypes.c_int32)]
+
+
+class SpBatch(ctypes.Structure):
+    """sp_batch: the new tokens of B sequences and where they stand."""
+    _fields_ = [("B", ctypes.c_int32), ("max_new", ctypes.c_int32), ("T", ctypes.c_int64), ("cu_new", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("table", ctypes.c_void_p), ("table_width", ctypes.c_int32),
+                ("table_stride", ctypes.c_int64)]
 
 
 class SpError(RuntimeError):
@@ -86,6 +118,13 @@ _SIGS = {
     "sp_select_rules_workspace_size": (_sz, [_i64, _i32]),
     "sp_select_rules": (_i32, [_vp, _i64, _i32, _i32, _i32, _dbl, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "sp_gather_kept": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "sp_rotary_plan_init": (_i32, [_vp, _i32, _vp, _vp, _i32, _i32]),
+    "sp_rotary": (_i32, [_vp, _vp, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _i32, _vp]),
+    "sp_cache_workspace_size": (_sz, []),
+    "sp_cache_write": (_i32, [_vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "sp_cache_read": (_i32, [_vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "sp_attend_workspace_size": (_sz, [_vp, _vp, _i32]),
+    "sp_attend": (_i32, [_vp, _vp, _vp, _i32, _dbl, _i64, _vp, _vp, _i64, _i64, _vp, _sz, _vp]),
     "sp_workspace_status": (_i32, [_vp, _vp]),
     "sp_last_error": (_c.c_char_p, []),
     "sp_status_string": (_c.c_char_p, [_i32]),
@@ -259,6 +298,45 @@ def sp_gather_kept(token_ids, B, cu_M_host, kept_pos, n_kept, out_tokens, out_po
     cu = _i64_array(cu_M_host)
     return lib().sp_gather_kept(_ptr(token_ids), B, ctypes.addressof(cu), _ptr(kept_pos), _ptr(n_kept),
                                 _ptr(out_tokens), _ptr(out_positions), _ptr(cu_kept), _stream(stream))
+
+
+def _struct(x):
+    return None if x is None else ctypes.addressof(x)
+
+
+def sp_rotary_plan_init(plan, rot, inv_freq_host, axis_of_pair_host, axes, interleaved) -> int:
+    freq = (ctypes.c_double * max(len(inv_freq_host), 1))(*inv_freq_host) if inv_freq_host is not None else None
+    axis = (ctypes.c_uint8 * max(len(axis_of_pair_host), 1))(*axis_of_pair_host) if axis_of_pair_host is not None else None
+    return lib().sp_rotary_plan_init(_struct(plan), rot, _ptr(freq), _ptr(axis), axes, interleaved)
+
+
+def sp_rotary(plan, positions, pos_stride, T, d, dtype, inverse, q, q_out, H, k, k_out, H_kv, stream=None) -> int:
+    return lib().sp_rotary(_struct(plan), _ptr(positions), pos_stride, T, d, dtype, inverse, _struct(q),
+                           _struct(q_out), H, _struct(k), _struct(k_out), H_kv, _stream(stream))
+
+
+def sp_cache_workspace_size() -> int:
+    return lib().sp_cache_workspace_size()
+
+
+def sp_cache_write(cache, batch, k_new, v_new, ws, ws_bytes, stream=None) -> int:
+    return lib().sp_cache_write(_struct(cache), _struct(batch), _struct(k_new), _struct(v_new), _ptr(ws), ws_bytes,
+                                _stream(stream))
+
+
+def sp_cache_read(cache, batch, out_k, out_v, ws, ws_bytes, stream=None) -> int:
+    return lib().sp_cache_read(_struct(cache), _struct(batch), _struct(out_k), _struct(out_v), _ptr(ws), ws_bytes,
+                               _stream(stream))
+
+
+def sp_attend_workspace_size(cache, batch, H) -> int:
+    return lib().sp_attend_workspace_size(_struct(cache), _struct(batch), H)
+
+
+def sp_attend(q, cache, batch, H, scale, window, out, lse, lse_stride_row, lse_stride_head, ws, ws_bytes,
+              stream=None) -> int:
+    return lib().sp_attend(_struct(q), _struct(cache), _struct(batch), H, scale, window, _struct(out), _ptr(lse),
+                           lse_stride_row, lse_stride_head, _ptr(ws), ws_bytes, _stream(stream))
 
 
 def sp_workspace_status(ws, stream=None) -> int:
@@ -486,3 +564,238 @@ def gather_kept(token_ids, cu_M, kept_pos, n_kept, *, stream=None):
     cu_kept = torch.empty(B + 1, dtype=torch.int64, device=dev)
     _check(sp_gather_kept(token_ids, B, cu, kept_pos, n_kept, tokens, positions, cu_kept, stream))
     return tokens, positions, cu_kept
+
+
+# ----------------------------------------------------------------------------
+# Positions, the paged cache, and attention over it
+# ----------------------------------------------------------------------------
+
+def rotary_plan(rot, *, base=10000.0, inv_freq=None, sections=None, axis_of_pair=None, interleaved=False):
+    """Rotary frequencies for `rotary`: base ** (-2 i / rot), or the given inv_freq (rot / 2 values).
+    sections: how many consecutive pairs each position axis has (time, height, width, say), or
+    axis_of_pair: each pair's axis.  interleaved: pair i is entries 2i, 2i + 1, not i, i + rot / 2."""
+    rot = int(rot)
+    pairs = rot // 2
+    freq = [float(base) ** (-i / pairs) for i in range(pairs)] if inv_freq is None else [float(f) for f in inv_freq]
+    if sections is not None:
+        if axis_of_pair is not None:
+            raise ValueError("give sections or axis_of_pair, not both")
+        axis_of_pair = [a for a, n in enumerate(sections) for _ in range(n)]
+    axis = [0] * pairs if axis_of_pair is None else [int(a) for a in axis_of_pair]
+    if len(freq) != pairs or len(axis) != pairs:
+        raise ValueError(f"a plan of {rot} entries has {pairs} pairs: got {len(freq)} frequencies, {len(axis)} axes")
+    if any(not 0 <= a < 8 for a in axis):
+        raise ValueError("axes are numbered 0 to 7")
+    plan = SpRotaryPlan()
+    axes = max(len(sections) if sections is not None else 0, max(axis, default=0) + 1)
+    _check(sp_rotary_plan_init(plan, rot, freq, axis, axes, int(bool(interleaved))))
+    return plan
+
+
+def _rows(t, heads_first=False):
+    """sp_rows of a tensor [rows, heads, d] (heads_first: [heads, rows, d]) whose last axis is contiguous."""
+    st = t.stride()
+    if st[2] != 1 and t.shape[2] > 1:
+        raise ValueError("the last axis must be contiguous")
+    return SpRows(t.data_ptr(), st[1], st[0]) if heads_first else SpRows(t.data_ptr(), st[0], st[1])
+
+
+class _On:
+    """For a call on `device` and `stream` (None: the current one): makes both current, where they are not, so that
+    what the call allocates belongs to the stream that uses it."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guards = []
+        if device.type != "cuda":
+            raise ValueError(f"the tensors must be on a GPU (got {device})")
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on different devices: {device} and {t.device}")
+
+
+def rotary(q, k, positions, plan, *, inverse=False, q_out=None, k_out=None, stream=None):
+    """Rotates q [T, H, d] and k [T, H_kv, d] (either may be None) at positions [T] or [axes, T] (int32) and returns
+    (q_out, k_out).  q_out=q rotates in place.  inverse=True undoes the rotation (and is its gradient)."""
+    import torch
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("neither q nor k")
+    T, d = some.shape[0], some.shape[2]
+    dt = _dtype_code(some)
+    for t in (q, k):
+        if t is not None and (t.dim() != 3 or t.shape[0] != T or t.shape[2] != d or t.dtype != some.dtype):
+            raise ValueError("q and k must be [T, heads, d] of the same T, d and dtype")
+    if positions.dtype != torch.int32 or positions.shape[-1] != T or positions.dim() > 2:
+        raise ValueError("positions must be int32, [T] or [axes, T]")
+    if (positions.shape[0] if positions.dim() == 2 else 1) < plan.axes:
+        raise ValueError(f"the plan has {plan.axes} axes: positions must be [{plan.axes}, T]")
+    if T and positions.stride(-1) != 1:
+        positions = positions.contiguous()
+    _same_device(some.device, q, k, positions, q_out, k_out)
+    for t, o in ((q, q_out), (k, k_out)):
+        if t is not None and o is not None and (o.shape != t.shape or o.dtype != t.dtype):
+            raise ValueError("q_out and k_out must have the shape and dtype of q and k")
+    with _On(some.device, stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        _check(sp_rotary(plan, positions, positions.stride(0) if positions.dim() == 2 else 0, T, d, dt, int(inverse),
+                         None if q is None else _rows(q), None if q is None else _rows(q_out),
+                         0 if q is None else q.shape[1], None if k is None else _rows(k),
+                         None if k is None else _rows(k_out), 0 if k is None else k.shape[1], stream))
+    return q_out if q is not None else None, k_out if k is not None else None
+
+
+class Cache:
+    """One layer's paged keys and values: k and v [pages, H_kv, page, d] (any strides with the last axis contiguous;
+    the same for both), of `dtype` (bf16 or f32) or, for an 8-bit cache, float8_e4m3fn or int8 with k_scale and
+    v_scale fp32 [pages, H_kv, page].  dtype: of the rows that are written and read (default: k's)."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None, *, dtype=None):
+        import torch
+        kinds = {torch.float8_e4m3fn: SP_CACHE_E4M3, torch.int8: SP_CACHE_INT8}
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+            raise ValueError("k and v must be [pages, H_kv, page, d] of the same shape, dtype and strides")
+        if k.stride(3) != 1:
+            raise ValueError("the last axis of k and v must be contiguous")
+        kind = kinds.get(k.dtype, SP_CACHE_SAME)
+        dtype = dtype or (k.dtype if kind == SP_CACHE_SAME else torch.bfloat16)
+        if kind == SP_CACHE_SAME:
+            if dtype != k.dtype or k_scale is not None or v_scale is not None:
+                raise ValueError(f"a cache of {k.dtype} holds rows of that dtype and has no scales")
+        else:
+            for s in (k_scale, v_scale):
+                if s is None or s.dtype != torch.float32 or s.shape != k.shape[:3] or not s.is_contiguous():
+                    raise ValueError("an 8-bit cache needs k_scale and v_scale, contiguous fp32 [pages, H_kv, page]")
+        _same_device(k.device, v, k_scale, v_scale)
+        code = {torch.bfloat16: SP_BF16, torch.float32: SP_F32}.get(dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {dtype}")
+        self.k, self.v, self.k_scale, self.v_scale, self.dtype, self.kind = k, v, k_scale, v_scale, dtype, kind
+        self.device = k.device
+        self.pages, self.H_kv, self.page, self.d = k.shape
+        sp_, sh, ss, _ = k.stride()
+        self.c = SpCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), sp_, sh, ss, self.pages, self.page,
+                         self.H_kv, self.d, code, kind)
+
+
+def cache_alloc(pages, H_kv, page, d, *, dtype=None, kind="same", device="cuda"):
+    """A Cache of uninitialised pages.  kind: "same" (rows held in dtype), "e4m3" or "int8"."""
+    import torch
+    dtype = dtype or torch.bfloat16
+    held = {"same": dtype, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}[kind]
+    new = lambda: torch.empty(pages, H_kv, page, d, dtype=held, device=device)          # noqa: E731
+    scale = lambda: None if kind == "same" else torch.empty(pages, H_kv, page, dtype=torch.float32, device=device)  # noqa: E731
+    return Cache(new(), new(), scale(), scale(), dtype=dtype)
+
+
+class Batch:
+    """The new tokens of B sequences: cu_new int64 [B + 1] (offsets of their rows), kv_len int64 [B] (tokens in the
+    cache, the new ones included) and table int32 [B, width] (page of each `page` tokens), on the device, read when
+    the work runs.  rows: rows of the calls' tensors; max_new: at least the largest number of new tokens of a
+    sequence (default: rows)."""
+
+    def __init__(self, cu_new, kv_len, table, *, rows, max_new=None):
+        import torch
+        B = kv_len.shape[0]
+        if cu_new.dtype != torch.int64 or kv_len.dtype != torch.int64 or table.dtype != torch.int32:
+            raise TypeError("cu_new and kv_len must be int64, table int32")
+        if cu_new.shape != (B + 1,) or kv_len.dim() != 1 or table.dim() != 2 or table.shape[0] != B:
+            raise ValueError("cu_new must be [B + 1], kv_len [B] and table [B, width]")
+        if not cu_new.is_contiguous() or not kv_len.is_contiguous() or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("cu_new, kv_len and the rows of table must be contiguous")
+        _same_device(cu_new.device, kv_len, table)
+        self.cu_new, self.kv_len, self.table, self.rows = cu_new, kv_len, table, int(rows)
+        self.device = cu_new.device
+        self.max_new = self.rows if max_new is None else int(max_new)
+        self.c = SpBatch(B, self.max_new, self.rows, _ptr(cu_new), _ptr(kv_len), _ptr(table), table.shape[1],
+                         table.stride(0) if B > 1 else 0)
+
+
+def _check_rows_of(t, name, rows, heads, d, dtype, device):
+    if tuple(t.shape) != (rows, heads, d) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} [{rows}, {heads}, {d}] on {device}: "
+                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+def cache_write(cache, batch, k_new, v_new, *, ws=None, stream=None, check=False):
+    """Writes the batch's new tokens, k_new and v_new [rows, H_kv, d], into the cache."""
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        _check_rows_of(t, name, batch.rows, cache.H_kv, cache.d, cache.dtype, cache.device)
+    _same_device(cache.device, batch)
+    with _On(cache.device, stream):
+        ws = _workspace(sp_cache_workspace_size(), cache.device, ws)
+        _check(sp_cache_write(cache.c, batch.c, _rows(k_new), _rows(v_new), ws, ws.numel() * ws.element_size(), stream))
+        _check_device(ws, stream, check)
+
+
+def cache_read(cache, batch, *, out_k=None, out_v=None, ws=None, stream=None, check=False):
+    """Reads the batch's tokens back: (out_k, out_v) [H_kv, rows, d], a layer of score's K_prompt each.  Given
+    outputs are written in place (any strides with the last axis contiguous), and one that is not given while the
+    other is stays out.  With neither given both are made, and rows that are not a token of the batch are not set."""
+    import torch
+    for t, name in ((out_k, "out_k"), (out_v, "out_v")):
+        if t is not None and (tuple(t.shape) != (cache.H_kv, batch.rows, cache.d) or t.dtype != cache.dtype or
+                              t.device != cache.device):
+            raise ValueError(f"{name} must be {cache.dtype} [{cache.H_kv}, {batch.rows}, {cache.d}] on {cache.device}")
+    _same_device(cache.device, batch)
+    with _On(cache.device, stream):
+        if out_k is None and out_v is None:
+            out_k, out_v = (torch.empty(cache.H_kv, batch.rows, cache.d, dtype=cache.dtype, device=cache.device)
+                            for _ in range(2))
+        ws = _workspace(sp_cache_workspace_size(), cache.device, ws)
+        _check(sp_cache_read(cache.c, batch.c, None if out_k is None else _rows(out_k, True),
+                             None if out_v is None else _rows(out_v, True), ws, ws.numel() * ws.element_size(),
+                             stream))
+        _check_device(ws, stream, check)
+    return out_k, out_v
+
+
+def attend_workspace_size(q, cache, batch):
+    """Workspace bytes of attend for these arguments."""
+    with _On(cache.device, None):
+        return sp_attend_workspace_size(cache.c, batch.c, q.shape[1])
+
+
+def attend(q, cache, batch, *, scale=None, window=0, out=None, lse=None, ws=None, stream=None, check=False):
+    """Causal attention of the batch's new tokens, q [rows, H, d], over their sequences' cached tokens (their own
+    among them): (out [rows, H, d], lse fp32 [H, rows]).  scale: default 1 / sqrt(d).  window > 0: each token sees
+    itself and the window - 1 tokens before it.  lse may be any strided fp32 [H, rows], such as [l, :, j:j+1] of
+    score_lse's [L, H, N].  Rows that are not a token of the batch are not written."""
+    import torch
+    H = q.shape[1] if q.dim() == 3 else 0
+    _check_rows_of(q, "q", batch.rows, H, cache.d, cache.dtype, cache.device)
+    if out is not None:
+        _check_rows_of(out, "out", batch.rows, H, cache.d, cache.dtype, cache.device)
+    if lse is not None and (tuple(lse.shape) != (H, batch.rows) or lse.dtype != torch.float32 or lse.device != q.device):
+        raise ValueError(f"lse must be fp32 [{H}, {batch.rows}] on {q.device}")
+    _same_device(cache.device, batch)
+    with _On(cache.device, stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty(H, batch.rows, dtype=torch.float32, device=q.device)
+        ws = _workspace(sp_attend_workspace_size(cache.c, batch.c, H), cache.device, ws)
+        _check(sp_attend(_rows(q), cache.c, batch.c, H, cache.d ** -0.5 if scale is None else float(scale), int(window),
+                         _rows(out), lse, lse.stride(1), lse.stride(0), ws, ws.numel() * ws.element_size(), stream))
+        _check_device(ws, stream, check)
+    return out, lse

@@ -1,0 +1,116 @@
+// Rotary positions of queries and keys, with one or several position axes.
+//
+// Pair i at position p turns by p * f_i.  The angle needs p * f_i / 2 pi only
+// modulo 1, so the plan holds f_i / 2 pi as a 64-bit fraction F of a turn and
+// the kernel takes p * F modulo 2^64: an integer product that is exact for
+// every int32 position, where an fp32 product would be off by p * 2^-25
+// radians.  The upper 32 bits, as a signed number of half turns, go to sincospi.
+//
+// Bound by memory: each entry is read once and written once.  A block takes a
+// few tokens, works out their sines and cosines once into shared memory, and
+// then runs over all the heads of q and k with 16-byte loads and stores.
+#include "paged.cuh"
+
+namespace sp {
+namespace {
+
+constexpr int kRotThreads = 256;
+
+struct RotArgs {
+    sp_rotary_plan plan;
+    const int32_t* pos;
+    int64_t pos_stride, T;
+    int d, H, Hk;
+    int tokens;             // tokens a block takes
+    float sign;             // -1: inverse
+    sp_rows q, qo, k, ko;
+};
+
+// Rotates eight pairs: x0/x1 hold the pairs' entries (half layout: the two
+// halves' entries; interleaved: 16 consecutive entries).
+__device__ __forceinline__ void rotate8(float (&x0)[8], float (&x1)[8], const float2* cs, float sign, bool inter) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float c = cs[i].x, s = cs[i].y * sign;
+        float& a = inter ? (i < 4 ? x0[(2 * i) & 7] : x1[(2 * i) & 7]) : x0[i];
+        float& b = inter ? (i < 4 ? x0[(2 * i + 1) & 7] : x1[(2 * i + 1) & 7]) : x1[i];
+        const float u = a, v = b;
+        a = u * c - v * s;
+        b = v * c + u * s;
+    }
+}
+
+template <typename T, bool kInter>
+__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotArgs p) {
+    extern __shared__ float2 cs[];      // [tokens][pairs]: cosine, sine
+    const int pairs = p.plan.rot / 2;
+    const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
+    const int nt = (int)min((int64_t)p.tokens, p.T - t0);
+    for (int i = threadIdx.x; i < nt * pairs; i += kRotThreads) {
+        const int t = i / pairs, j = i - t * pairs;
+        const int64_t at = p.pos[p.plan.axis[j] * p.pos_stride + t0 + t];
+        const int32_t half_turns = (int32_t)(((uint64_t)at * p.plan.turns[j]) >> 32);
+        float s, c;
+        sincospif((float)half_turns * 0x1p-31f, &s, &c);
+        cs[i] = make_float2(c, s);
+    }
+    __syncthreads();
+    // an item: one head's chunk of eight pairs, or of eight entries past rot
+    const int rc = pairs / 8, chunks = rc + (p.d - p.plan.rot) / 8;
+    const int heads = p.H + p.Hk, per = heads * chunks;
+    for (int i = blockIdx.y * kRotThreads + threadIdx.x; i < nt * per; i += gridDim.y * kRotThreads) {
+        const int t = i / per, r = i - t * per;
+        int h = r / chunks;
+        const int c = r - h * chunks;
+        const bool isq = h < p.H;
+        if (!isq) h -= p.H;
+        const sp_rows& in = isq ? p.q : p.k;
+        const sp_rows& out = isq ? p.qo : p.ko;
+        const T* src = static_cast<const T*>(in.data) + (t0 + t) * in.stride_row + h * in.stride_head;
+        T* dst = static_cast<T*>(out.data) + (t0 + t) * out.stride_row + h * out.stride_head;
+        float x0[8], x1[8];
+        if (c >= rc) {
+            const int e = p.plan.rot + (c - rc) * 8;
+            load8(src + e, x0);
+            store8(dst + e, x0);
+            continue;
+        }
+        const int e0 = kInter ? c * 16 : c * 8, e1 = kInter ? c * 16 + 8 : pairs + c * 8;
+        load8(src + e0, x0);
+        load8(src + e1, x1);
+        rotate8(x0, x1, cs + t * pairs + c * 8, p.sign, kInter);
+        store8(dst + e0, x0);
+        store8(dst + e1, x1);
+    }
+}
+
+}  // namespace
+
+sp_status rotary_launch(const sp_rotary_plan& plan, const int32_t* pos, int64_t pos_stride, int64_t T, int d,
+                        sp_dtype dtype, bool inverse, const sp_rows& q, const sp_rows& qo, int H, const sp_rows& k,
+                        const sp_rows& ko, int Hk, cudaStream_t st) {
+    if (T == 0 || H + Hk == 0) return SP_OK;
+    RotArgs a;
+    a.plan = plan;
+    a.pos = pos; a.pos_stride = pos_stride; a.T = T; a.d = d; a.H = H; a.Hk = Hk;
+    a.sign = inverse ? -1.f : 1.f;
+    a.q = q; a.qo = qo; a.k = k; a.ko = ko;
+    a.tokens = 4;
+    const int64_t blocks = (T + a.tokens - 1) / a.tokens;
+    const int per = (H + Hk) * (plan.rot / 16 + (d - plan.rot) / 8) * a.tokens;
+    // few tokens: several blocks share a token's heads
+    const int split = blocks >= 608 ? 1 : (int)std::min<int64_t>((per + kRotThreads - 1) / kRotThreads, (608 + blocks - 1) / blocks);
+    const size_t smem = (size_t)a.tokens * (plan.rot / 2) * sizeof(float2);
+    const dim3 grid((unsigned)blocks, (unsigned)std::max(1, split));
+    if (dtype == SP_BF16) {
+        if (plan.interleaved) rotary_kernel<__nv_bfloat16, true><<<grid, kRotThreads, smem, st>>>(a);
+        else rotary_kernel<__nv_bfloat16, false><<<grid, kRotThreads, smem, st>>>(a);
+    } else {
+        if (plan.interleaved) rotary_kernel<float, true><<<grid, kRotThreads, smem, st>>>(a);
+        else rotary_kernel<float, false><<<grid, kRotThreads, smem, st>>>(a);
+    }
+    SP_LAUNCH_CHECK();
+    return SP_OK;
+}
+
+}  // namespace sp

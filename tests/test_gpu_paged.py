@@ -1,0 +1,551 @@
+"""Rotary positions, the paged cache and the attention over it on the GPU, against the 64-bit oracle."""
+import numpy as np
+import pytest
+
+import oracle
+from paged_helpers import attend_bounds, make_batch, make_cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sp():
+    import torch
+    assert torch.cuda.is_available(), "the GPU tests need a CUDA device"
+    from speculative_prefill_token_sp_gb300 import build
+    build.build()
+    import speculative_prefill_token_sp_gb300 as m
+    m.lib()
+    return m
+
+
+def torch_dtype(name):
+    import torch
+    return {"bf16": torch.bfloat16, "f32": torch.float32}[name]
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+# ----------------------------------------------------------------------------
+# Rotary positions
+# ----------------------------------------------------------------------------
+
+# a pair's result is two products and a sum of fp32 values rounded to the type: half a step of the type, plus the
+# sine and cosine (fp32: 2 units of 2^-24, and 2^-24 * pi from the angle's fp32 conversion) and the fp32 products and sum (2 more)
+def rotary_bound(x, dtype, pairs, interleaved):
+    turned = x[..., :2 * pairs]
+    a, b = (turned[..., 0::2], turned[..., 1::2]) if interleaved else (turned[..., :pairs], turned[..., pairs:])
+    size = np.abs(a) + np.abs(b)
+    size = np.stack([size, size], -1).reshape(turned.shape) if interleaved else np.concatenate([size, size], -1)
+    full = np.abs(x).copy()
+    full[..., :2 * pairs] = size
+    return full * ((2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) + 8 * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,H,H_kv,d,rot,sections", [
+    (1, 4, 2, 64, 64, None), (5, 32, 8, 128, 128, (16, 24, 24)), (131, 3, 1, 96, 32, None), (33, 2, 2, 16, 16, (1, 3, 4)),
+    (3, 1, 1, 256, 256, None), (700, 16, 4, 64, 64, (8, 12, 12)), (2, 5, 0, 24, 16, None), (9, 0, 3, 40, 32, None),
+])
+def test_rotary_matches_the_oracle(sp, dtype, interleaved, T, H, H_kv, d, rot, sections):
+    import torch
+    rng = np.random.default_rng(T * 1000 + d)
+    axes = len(sections) if sections else 1
+    pos = rng.integers(-(1 << 31), 1 << 31, (axes, T)).astype(np.int32)
+    pos[:, : T // 2] = rng.integers(0, 131072, (axes, T // 2))
+    plan = sp.rotary_plan(rot, base=500000.0, sections=sections, interleaved=interleaved)
+    freq = [500000.0 ** (-i / (rot // 2)) for i in range(rot // 2)]
+    axis = [a for a, n in enumerate(sections) for _ in range(n)] if sections else [0] * (rot // 2)
+    mk = lambda h: torch.from_numpy(rng.standard_normal((T, h, d))).to(torch_dtype(dtype)).cuda() if h else None  # noqa: E731
+    q, k = mk(H), mk(H_kv)
+    p = torch.from_numpy(pos if axes > 1 else pos[0]).cuda()
+    for inverse in (False, True):
+        for x, got in zip((q, k), sp.rotary(q, k, p, plan, inverse=inverse)):
+            if x is None:
+                assert got is None
+                continue
+            ref = oracle.paged.rotary(f64(x), pos, freq, axis, interleaved, inverse)
+            # 2^31 * 2^-53 of a turn from the 64-bit fraction's own double: below 2^-24
+            assert np.all(np.abs(f64(got) - ref) <= rotary_bound(f64(x), dtype, rot // 2, interleaved) + 1e-30)
+            assert np.array_equal(f64(got)[..., rot:], f64(x)[..., rot:])
+
+
+def test_rotary_in_place_on_slices_of_a_fused_projection(sp):
+    import torch
+    T, H, H_kv, d = 77, 6, 2, 64
+    g = torch.Generator().manual_seed(3)
+    qkv = torch.randn(T, H + 2 * H_kv, d, generator=g).to(torch.bfloat16).cuda()
+    pos = torch.arange(1000, 1000 + T, dtype=torch.int32).cuda()
+    plan = sp.rotary_plan(d)
+    want_q, want_k = sp.rotary(qkv[:, :H].contiguous(), qkv[:, H:H + H_kv].contiguous(), pos, plan)
+    before = qkv.clone()
+    q, k = qkv[:, :H], qkv[:, H:H + H_kv]
+    sp.rotary(q, k, pos, plan, q_out=q, k_out=k)
+    assert torch.equal(qkv[:, :H], want_q) and torch.equal(qkv[:, H:H + H_kv], want_k)
+    assert torch.equal(qkv[:, H + H_kv:], before[:, H + H_kv:])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_inverse_is_its_gradient(sp, interleaved):
+    import torch
+    T, H, d = 9, 3, 32
+    rng = np.random.default_rng(5)
+    pos = rng.integers(0, 5000, (1, T)).astype(np.int32)
+    x, g, e = (torch.from_numpy(rng.standard_normal((T, H, d))).float().cuda() for _ in range(3))
+    plan = sp.rotary_plan(d, interleaved=interleaved)
+    p = torch.from_numpy(pos).cuda()
+    grad, _ = sp.rotary(g, None, p, plan, inverse=True)
+    # the formula's gradient: the transpose of the rotation, by its matrix' columns
+    freq, axis = [10000.0 ** (-i / (d // 2)) for i in range(d // 2)], [0] * (d // 2)
+    columns = np.stack([oracle.paged.rotary(np.broadcast_to(np.eye(d)[j], (T, 1, d)), pos, freq, axis, interleaved)[:, 0]
+                        for j in range(d)], -1)                          # [T, out, in]
+    want = np.einsum("toi,tho->thi", columns, f64(g))
+    assert np.all(np.abs(f64(grad) - want) <= rotary_bound(f64(g), "f32", d // 2, interleaved))
+    # differences: the map is linear, so a difference of any size has the gradient's product.  Each result is off
+    # by 9 * 2^-24 of at most sqrt(2) * |pair|: summed over T H d entries against g, in quadrature and six times that
+    up, _ = sp.rotary(x + e, None, p, plan)
+    down, _ = sp.rotary(x, None, p, plan)
+    lhs = ((f64(up) - f64(down)) * f64(g)).sum()
+    rhs = (f64(x + e) - f64(x)).ravel() @ f64(grad).ravel()
+    assert abs(lhs - rhs) <= 6 * np.sqrt(T * H * d) * 3 * 9 * 2.0 ** -24 * 10
+
+
+def test_rotary_of_no_tokens(sp):
+    import torch
+    q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    out, k = sp.rotary(q, None, torch.empty(0, dtype=torch.int32, device="cuda"), sp.rotary_plan(64))
+    assert out.shape == q.shape and k is None
+
+
+# ----------------------------------------------------------------------------
+# The cache
+# ----------------------------------------------------------------------------
+
+SHAPES = [  # H_kv, d, page, new, kv, rows before and behind
+    (2, 64, 16, [1], [1], 0, 0), (8, 128, 64, [70, 0, 1], [200, 0, 64], 0, 3), (3, 72, 7, [20, 5], [20, 33], 2, 1),
+    (1, 256, 1, [9], [12], 0, 0), (4, 8, 48, [100], [100], 0, 0), (2, 40, 128, [5, 6, 7], [3, 300, 7], 1, 0),
+]
+
+
+def rows_with_edges(rng, T, H_kv, d, dtype):
+    """Rows of all sizes: normal ones, zeros, tiny and huge ones, halfway values, and some that hold NaN and infinity."""
+    import torch
+    x = rng.standard_normal((T, H_kv, d)) * 2.0 ** rng.integers(-8, 8, (T, H_kv, 1))
+    for i in range(T):
+        kind = i % 9
+        if kind == 1:
+            x[i] = 0
+        elif kind == 2:
+            x[i] *= 2.0 ** -110
+        elif kind == 3:
+            x[i] *= 2.0 ** 110
+        elif kind == 4:
+            x[i] = rng.integers(-254, 255, (H_kv, d)) / 2       # half steps of the 8-bit integers
+            x[i, :, 0] = 127
+        elif kind == 5:
+            x[i, 0, d // 2] = np.nan
+        elif kind == 6:
+            x[i, -1, d - 1] = -np.inf
+        elif kind == 7:
+            x[i, :, 0] = 448 * 2.0 ** -3                        # the largest code exactly, and one step above
+            x[i, :, 1:] = np.clip(x[i, :, 1:], -50, 50)
+    return torch.from_numpy(x).to(torch_dtype(dtype))
+
+
+@pytest.mark.parametrize("layout", ["hnd", "nhd"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["same", "e4m3", "int8"])
+@pytest.mark.parametrize("H_kv,d,page,new,kv,before,behind", SHAPES)
+def test_cache_write_and_read(sp, H_kv, d, page, new, kv, before, behind, kind, dtype, layout):
+    import torch
+    rng = np.random.default_rng(d * page)
+    cache, table, kval, vval = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=kv, kind=kind, dtype=torch_dtype(dtype),
+                                          layout=layout)
+    T = before + sum(new) + behind
+    batch, cu = make_batch(sp, new, kv, table, rows=T, first=before, max_new=max(new))
+    k_new, v_new = (rows_with_edges(rng, T, H_kv, d, dtype) for _ in range(2))
+    raw = lambda t: t.contiguous().view(torch.uint8 if kind != "same" else t.dtype).cpu()        # noqa: E731
+    sides = [(cache.k, cache.k_scale), (cache.v, cache.v_scale)]
+    old = [(raw(t), None if s is None else s.cpu()) for t, s in sides]
+    sp.cache_write(cache, batch, k_new.cuda(), v_new.cuda(), check=True)
+    places = oracle.paged.places(cu, kv)
+    read = sp.cache_read(cache, batch, out_k=torch.full((H_kv, T, d), 7.0, dtype=torch_dtype(dtype), device="cuda"),
+                         out_v=torch.full((H_kv, T, d), 7.0, dtype=torch_dtype(dtype), device="cuda"), check=True)
+    for x, (t, s), (was, was_scale), got in zip((k_new, v_new), sides, old, read):
+        now = raw(t)
+        touched = torch.zeros(t.shape[:3], dtype=torch.bool)
+        for r, (b, i) in enumerate(places):
+            row = x[before + r].double().numpy()
+            back = f64(got[:, before + r])
+            if i < 0:
+                assert np.all(back == 0)
+                continue
+            pg, slot = table[b, i // page], i % page
+            touched[pg, :, slot] = True
+            if kind == "same":
+                assert np.array_equal(f64(t[pg, :, slot]), row, equal_nan=True)
+                assert np.array_equal(back, row, equal_nan=True)
+                continue
+            codes, scale = oracle.paged.quantise(row, kind)
+            held = f64(t[pg, :, slot].float())
+            assert np.array_equal(f64(s[pg, :, slot]), scale, equal_nan=True)
+            assert np.array_equal(held, codes)
+            with np.errstate(invalid="ignore"):
+                assert np.array_equal(back, f64(torch.from_numpy(codes * scale[:, None]).to(torch_dtype(dtype))), equal_nan=True)
+        assert torch.equal(now[~touched], was[~touched])
+        if s is not None:
+            assert torch.equal(s.cpu()[~touched], was_scale[~touched])
+        left = f64(got)
+        assert np.all(left[:, :before] == 7) and np.all(left[:, before + sum(new):] == 7)
+
+
+def test_cache_read_one_side_into_a_layer_of_k_prompt(sp):
+    import torch
+    rng = np.random.default_rng(8)
+    kv = [37, 64, 5]
+    cache, table, kval, _ = make_cache(sp, rng, H_kv=2, d=64, page=16, kv=kv, kind="e4m3")
+    batch, cu = make_batch(sp, kv, kv, table)
+    K = torch.zeros(3, 2, sum(kv), 64, dtype=torch.bfloat16, device="cuda")
+    k, v = sp.cache_read(cache, batch, out_k=K[1], check=True)
+    assert v is None and k.data_ptr() == K[1].data_ptr()
+    for b in range(3):
+        assert np.array_equal(f64(K[1][:, cu[b]:cu[b + 1]]), kval[b])
+    assert not K[0].any() and not K[2].any()
+
+
+def test_every_code_reads_back_as_its_value(sp):
+    import torch
+    codes = torch.arange(256, dtype=torch.uint8).view(1, 1, 2, 128)
+    for held in (torch.float8_e4m3fn, torch.int8):
+        for scale in (1.0, 2.0 ** -100, 2.0 ** 119):
+            k = codes.view(held).cuda()
+            s = torch.full((1, 1, 2), scale, device="cuda")
+            cache = sp.Cache(k, k.clone(), s, s.clone())
+            batch, _ = make_batch(sp, [2], [2], np.zeros((1, 1), np.int32))
+            got, _ = sp.cache_read(cache, batch, check=True)
+            want = (codes.view(held).double() * scale).view(1, 2, 128)
+            assert np.array_equal(f64(got), want.numpy(), equal_nan=True)
+
+
+def test_rows_of_a_cache_beyond_2_31_entries(sp):
+    import torch
+    # two pages, 5 * 2^30 bytes apart
+    far = 5 * (1 << 30)
+    buf = torch.zeros(far + 4096, dtype=torch.int8, device="cuda")
+    k = buf.as_strided((2, 1, 16, 64), (far, 1024, 64, 1))
+    v = buf.as_strided((2, 1, 16, 64), (far, 1024, 64, 1), 2048)
+    s = [torch.zeros(2, 1, 16, device="cuda") for _ in range(2)]
+    cache = sp.Cache(k, v, *s, dtype=torch.bfloat16)
+    batch, _ = make_batch(sp, [20], [20], np.array([[1, 0]], np.int32))
+    x = torch.randn(20, 1, 64, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    sp.cache_write(cache, batch, x.cuda(), (-x).cuda(), check=True)
+    got, gotv = sp.cache_read(cache, batch, check=True)
+    codes, scale = oracle.paged.quantise(x[:, 0].double().numpy(), "int8")
+    assert np.array_equal(f64(got)[0], codes * scale[:, None]) and np.array_equal(f64(gotv)[0], -codes * scale[:, None])
+    out, lse = sp.attend(x.cuda(), cache, batch, check=True)
+    ref = oracle.paged.attend(x.double().numpy(), f64(got), f64(gotv), 0.125)
+    bound, lse_bound = attend_bounds("bf16", 64, 20, ref[0], ref[3], ref[2], ref[1])
+    assert np.all(np.abs(f64(out) - ref[0]) <= bound) and np.all(np.abs(f64(lse) - ref[1]) <= lse_bound)
+
+
+# ----------------------------------------------------------------------------
+# Attention
+# ----------------------------------------------------------------------------
+
+def check_attend(sp, *, H, H_kv, d, page, new, kv, dtype="bf16", kind="same", window=0, layout="hnd", before=0, behind=0,
+                 scale=None, seed=0, junk=float("nan"), q_gain=1.0):
+    import torch
+    rng = np.random.default_rng(seed + 17 * d + page)
+    td = torch_dtype(dtype)
+    cache, table, kval, vval = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=kv, kind=kind, dtype=td, layout=layout,
+                                          junk=junk)
+    T = before + sum(new) + behind
+    batch, cu = make_batch(sp, new, kv, table, rows=T, first=before, max_new=max(new))
+    q = torch.from_numpy(rng.standard_normal((T, H, d)) * q_gain).to(td)
+    # rows of no token hold NaN, and what they would write to must stay
+    real = np.zeros(T, dtype=bool)
+    real[before:before + sum(new)] = True
+    q[~torch.from_numpy(real)] = float("nan")
+    out = torch.full((T, H, d), 7.0, dtype=td, device="cuda")
+    lse = torch.full((H, T), 7.0, dtype=torch.float32, device="cuda")
+    sp.attend(q.cuda(), cache, batch, scale=scale, window=window, out=out, lse=lse, check=True)
+    got, got_lse = f64(out), f64(lse)
+    assert np.all(got[~real] == 7) and np.all(got_lse[:, ~real] == 7)
+    qd = q.double().numpy()
+    for b in range(len(new)):
+        lo, hi = int(cu[b]), int(cu[b + 1])
+        if lo == hi:
+            continue
+        ref, ref_lse, top, spread = oracle.paged.attend(qd[lo:hi], kval[b], vval[b], d ** -0.5 if scale is None else scale,
+                                                        window)
+        bound, lse_bound = attend_bounds(dtype, d, kv[b], ref, spread, top, ref_lse)
+        err = np.abs(got[lo:hi] - ref)
+        assert np.all(err <= bound), f"sequence {b}: out off by {np.nanmax(err / bound)} of its bound"
+        empty = np.isneginf(ref_lse)
+        assert np.array_equal(np.isneginf(got_lse[:, lo:hi]), empty)
+        assert np.all(got[lo:hi][empty.T] == 0)
+        with np.errstate(invalid="ignore"):
+            assert np.all((np.abs(got_lse[:, lo:hi] - ref_lse) <= lse_bound) | empty)
+
+
+@pytest.mark.parametrize("kind", ["same", "e4m3", "int8"])
+@pytest.mark.parametrize("H,H_kv,d,page", [
+    (4, 2, 64, 16), (32, 8, 128, 64), (7, 7, 64, 32), (6, 2, 128, 128), (8, 1, 64, 48), (5, 1, 40, 7), (2, 1, 256, 16),
+    (16, 1, 128, 1), (3, 3, 8, 5), (24, 1, 64, 256),
+])
+@pytest.mark.parametrize("new,kv", [
+    ([1], [1]), ([1, 1, 0, 1, 1], [17, 300, 0, 128, 129]), ([2, 3, 1], [2, 5, 1023]),
+])
+def test_attend_decode_steps(sp, H, H_kv, d, page, new, kv, kind):
+    check_attend(sp, H=H, H_kv=H_kv, d=d, page=page, new=new, kv=kv, kind=kind, behind=2)
+
+
+@pytest.mark.parametrize("kind", ["same", "e4m3", "int8"])
+@pytest.mark.parametrize("H,H_kv,d,page", [
+    (4, 2, 64, 16), (8, 2, 128, 64), (3, 1, 64, 32), (6, 2, 128, 128), (7, 1, 64, 48), (2, 2, 40, 7), (2, 1, 128, 8),
+    (12, 1, 128, 256),
+])
+@pytest.mark.parametrize("new,kv,window", [
+    ([33], [33], 0), ([64, 1, 65, 0], [64, 400, 200, 0], 0), ([129, 5], [300, 2], 0), ([100, 40], [260, 40], 37),
+    ([1, 70], [500, 128], 128),
+])
+def test_attend_chunks(sp, H, H_kv, d, page, new, kv, window, kind):
+    check_attend(sp, H=H, H_kv=H_kv, d=d, page=page, new=new, kv=kv, kind=kind, window=window, before=1, behind=3)
+
+
+@pytest.mark.parametrize("kind", ["same", "e4m3", "int8"])
+@pytest.mark.parametrize("new,kv,window", [
+    ([1], [512], 0), ([1, 1], [1, 700], 9), ([5, 0, 40], [3, 0, 90], 0), ([130], [131], 64),
+])
+@pytest.mark.parametrize("H,H_kv,d,page", [(4, 2, 64, 16), (3, 1, 128, 5), (2, 2, 256, 32)])
+def test_attend_single_precision(sp, H, H_kv, d, page, new, kv, window, kind):
+    check_attend(sp, H=H, H_kv=H_kv, d=d, page=page, new=new, kv=kv, kind=kind, window=window, dtype="f32", behind=1)
+
+
+@pytest.mark.parametrize("new,kv", [([1, 1], [5000, 40]), ([300, 1, 20], [1300, 2000, 30])])
+@pytest.mark.parametrize("layout,q_gain,scale", [("nhd", 1.0, None), ("hnd", 12.0, None), ("nhd", 1.0, 3.0), ("hnd", 1.0, 1e-4)])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("kind", ["same", "int8"])
+def test_attend_layouts_and_scales(sp, new, kv, layout, q_gain, scale, d, page, kind):
+    check_attend(sp, H=4, H_kv=2, d=d, page=page, new=new, kv=kv, layout=layout, q_gain=q_gain, scale=scale, kind=kind)
+
+
+@pytest.mark.parametrize("fill", [float("inf"), float("-inf"), 3e38])
+@pytest.mark.parametrize("new", [[1], [200]])
+def test_unwritten_slots_have_no_effect(sp, fill, new):
+    check_attend(sp, H=4, H_kv=2, d=128, page=64, new=new, kv=[205], junk=fill)
+
+
+def test_a_long_cache(sp):
+    check_attend(sp, H=2, H_kv=1, d=64, page=16, new=[1, 17], kv=[70001, 9001])
+
+
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (48, "bf16"), (64, "f32")])
+@pytest.mark.parametrize("n", [1, 150])
+def test_strided_queries_and_outputs(sp, d, dtype, n):
+    import torch
+    rng = np.random.default_rng(4)
+    td = torch_dtype(dtype)
+    H, H_kv, page, kv = 4, 2, 16, [n + 20]
+    cache, table, kval, vval = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=kv, dtype=td)
+    batch, _ = make_batch(sp, [n], kv, table)
+    qkv = torch.from_numpy(rng.standard_normal((n, H + 2 * H_kv, d))).to(td).cuda()
+    q = qkv[:, :H]
+    want, want_lse = sp.attend(q.contiguous(), cache, batch, check=True)
+    out = torch.zeros(H, n, d, dtype=td, device="cuda").transpose(0, 1)
+    lse = torch.zeros(3, n, 5, H, device="cuda")[1, :, 2].T
+    sp.attend(q, cache, batch, out=out, lse=lse, check=True)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 40), ("f32", 64)])
+@pytest.mark.parametrize("n", [1, 140])
+def test_what_the_arrays_get_wrong_is_reported_and_does_no_harm(sp, dtype, d, n):
+    import torch
+    rng = np.random.default_rng(6)
+    td = torch_dtype(dtype)
+    H, H_kv, page = 4, 2, 16
+    new, kv = [n, n, n], [n + 50, n + 40, n + 30]
+    cache, table, _, _ = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=kv, dtype=td)
+    good, cu = make_batch(sp, new, kv, table)
+    T = 3 * n
+    q = torch.from_numpy(rng.standard_normal((T, H, d))).to(td).cuda()
+    x = torch.from_numpy(rng.standard_normal((T, H_kv, d))).to(td).cuda()
+    want, _ = sp.attend(q, cache, good, check=True)
+    bad_page = table.copy()
+    bad_page[1, 1] = cache.pages
+    negative = table.copy()
+    negative[1, 0] = -1
+    far = torch.tensor([n + 50, 16 * table.shape[1] + 1, n + 30]).cuda()
+    cases = [make_batch(sp, new, kv, bad_page)[0], sp.Batch(good.cu_new, good.kv_len, torch.from_numpy(np.where(negative < 0, -1, negative)).cuda(), rows=T),
+             sp.Batch(good.cu_new, far, good.table, rows=T), sp.Batch(good.cu_new, -good.kv_len, good.table, rows=T),
+             sp.Batch(good.cu_new, good.kv_len, good.table, rows=T, max_new=n - 1),
+             sp.Batch(good.cu_new + 1, good.kv_len, good.table, rows=T)]
+    for i, batch in enumerate(cases):
+        out = torch.full((T, H, d), 7.0, dtype=td, device="cuda")
+        ws = torch.empty(sp.attend_workspace_size(q, cache, batch), dtype=torch.uint8, device="cuda")
+        sp.attend(q, cache, batch, out=out, ws=ws)
+        assert sp.sp_workspace_status(ws) == sp.SP_EDEVICE, i
+        if i < 3:           # the sequences around the bad one are right
+            assert torch.equal(out[:n], want[:n]) and torch.equal(out[2 * n:], want[2 * n:])
+        if i in (2, 3, 4):
+            assert torch.all(out[n:2 * n] == 7)
+    # writing and reading: a bad page among the new tokens' own
+    tail = table.copy()
+    tail[1, (kv[1] - 1) // page] = 0x7ffffff0
+    batch = make_batch(sp, new, kv, tail)[0]
+    before = cache.k.clone()
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    sp.cache_write(cache, batch, x, x, ws=ws)
+    assert sp.sp_workspace_status(ws) == sp.SP_EDEVICE
+    for r, (b, i) in enumerate(oracle.paged.places(cu, kv)):
+        pg = tail[b, i // page]
+        if pg < cache.pages:
+            before[pg, :, i % page] = x[r]
+    assert torch.equal(cache.k, before)
+    k, _ = sp.cache_read(cache, batch, ws=ws)
+    assert sp.sp_workspace_status(ws) == sp.SP_EDEVICE
+    gone = [r for r, (b, i) in enumerate(oracle.paged.places(cu, kv)) if tail[b, i // page] >= cache.pages]
+    assert gone and torch.all(k[:, gone] == 0)
+    sp.cache_read(cache, good, ws=ws)
+    assert sp.sp_workspace_status(ws) == sp.SP_OK
+
+
+@pytest.mark.parametrize("n,dtype", [(1, "bf16"), (200, "bf16"), (1, "f32")])
+def test_a_captured_call_follows_the_arrays_and_two_of_them_do_not_meet(sp, n, dtype):
+    import torch
+    rng = np.random.default_rng(9)
+    td = torch_dtype(dtype)
+    H, H_kv, d, page = 4, 2, 64, 16
+    cap = [n + 600, n + 300]
+    cache, table, kval, vval = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=cap, dtype=td)
+    runs = []
+    for g in range(2):
+        batch, cu = make_batch(sp, [n, n], cap, table)
+        q = torch.from_numpy(rng.standard_normal((2 * n, H, d))).to(td).cuda()
+        out = torch.zeros_like(q)
+        lse = torch.zeros(H, 2 * n, device="cuda")
+        ws = torch.empty(sp.attend_workspace_size(q, cache, batch), dtype=torch.uint8, device="cuda")
+        sp.attend(q, cache, batch, out=out, lse=lse, ws=ws)
+        torch.cuda.synchronize()
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=stream):
+            sp.attend(q, cache, batch, out=out, lse=lse, ws=ws)
+        runs.append((graph, stream, batch, q, out, lse, ws))
+    torch.cuda.synchronize()
+    for lens in ([n + 600, n + 300], [n + 13, n], [n - 1, n + 299]):
+        for graph, stream, batch, q, out, lse, ws in runs:
+            batch.kv_len.copy_(torch.tensor(lens))
+            out.fill_(7)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for graph, stream, *_ in runs:
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for graph, stream, batch, q, out, lse, ws in runs:
+            assert sp.sp_workspace_status(ws) == sp.SP_OK
+            want, want_lse = sp.attend(q, cache, batch, check=True)
+            assert torch.equal(out, want) and torch.equal(lse, want_lse)
+            for b in range(2):
+                ref = oracle.paged.attend(f64(q[b * n:(b + 1) * n]), kval[b][:, :lens[b]], vval[b][:, :lens[b]], d ** -0.5)
+                bound, _ = attend_bounds(dtype, d, max(lens[b], 1), ref[0], ref[3], ref[2], ref[1])
+                assert np.all(np.abs(f64(out[b * n:(b + 1) * n]) - ref[0]) <= bound)
+
+
+def test_calls_on_another_stream(sp):
+    import torch
+    rng = np.random.default_rng(10)
+    cache, table, kval, vval = make_cache(sp, rng, H_kv=2, d=64, page=16, kv=[300])
+    batch, _ = make_batch(sp, [1], [300], table)
+    q = torch.from_numpy(rng.standard_normal((1, 4, 64))).to(torch.bfloat16).cuda()
+    want, _ = sp.attend(q, cache, batch, check=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for handle in (s, s.cuda_stream):
+        out, _ = sp.attend(q, cache, batch, stream=handle)
+        s.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_the_same_call_gives_the_same_bits(sp):
+    import torch
+    rng = np.random.default_rng(11)
+    for d, new, kv in ((64, [1, 1, 1], [9000, 20, 3000]), (128, [900, 3], [5000, 8000])):
+        cache, table, _, _ = make_cache(sp, rng, H_kv=2, d=d, page=16, kv=kv)
+        batch, _ = make_batch(sp, new, kv, table)
+        q = torch.from_numpy(rng.standard_normal((sum(new), 8, d))).to(torch.bfloat16).cuda()
+        first = sp.attend(q, cache, batch)
+        for _ in range(3):
+            again = sp.attend(q, cache, batch)
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+# ----------------------------------------------------------------------------
+# Together
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["same", "e4m3"])
+def test_from_the_speculators_cache_to_the_targets_sparse_prefill(sp, kind):
+    """Chunked prefill into a paged cache, look-ahead steps whose lse goes to score_lse, selection, and the target's
+    attention of the kept tokens at their original positions."""
+    import torch
+    rng = np.random.default_rng(12)
+    L, H, H_kv, d, M, N, page = 2, 8, 2, 64, 700, 3, 16
+    plan = sp.rotary_plan(d)
+    freq, axis = [10000.0 ** (-i / (d // 2)) for i in range(d // 2)], [0] * (d // 2)
+    dev = lambda *s: torch.from_numpy(rng.standard_normal(s)).to(torch.bfloat16).cuda()          # noqa: E731
+    pages = -(-(M + N) // page)
+    table = torch.from_numpy(rng.permutation(pages).astype(np.int32))[None].cuda()
+    i64 = lambda *v: torch.tensor(v, dtype=torch.int64, device="cuda")                          # noqa: E731
+    caches = [sp.cache_alloc(pages, H_kv, page, d, kind=kind) for _ in range(L)]
+    Q_la = torch.zeros(N, L, H, d, dtype=torch.bfloat16, device="cuda")
+    K_prompt = torch.zeros(L, H_kv, M, d, dtype=torch.bfloat16, device="cuda")
+    K_la = torch.zeros(L, H_kv, N, d, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(L, H, N, device="cuda")
+    for layer in range(L):
+        for lo, hi in ((0, 400), (400, M)):
+            pos = torch.arange(lo, hi, dtype=torch.int32, device="cuda")
+            q, k = sp.rotary(dev(hi - lo, H, d), dev(hi - lo, H_kv, d), pos, plan)
+            batch = sp.Batch(i64(0, hi - lo), i64(hi), table, rows=hi - lo)
+            sp.cache_write(caches[layer], batch, k, dev(hi - lo, H_kv, d), check=True)
+            sp.attend(q, caches[layer], batch, check=True)
+        for j in range(N):
+            pos = torch.tensor([M + j], dtype=torch.int32, device="cuda")
+            q, k = sp.rotary(dev(1, H, d), dev(1, H_kv, d), pos, plan)
+            step = sp.Batch(i64(0, 1), i64(M + j + 1), table, rows=1)
+            sp.cache_write(caches[layer], step, k, dev(1, H_kv, d), check=True)
+            sp.attend(q, caches[layer], step, lse=lse[layer, :, j:j + 1], check=True)
+            Q_la[j, layer] = q[0]
+        sp.cache_read(caches[layer], sp.Batch(i64(0, M), i64(M), table, rows=M), out_k=K_prompt[layer], check=True)
+        sp.cache_read(caches[layer], sp.Batch(i64(0, N), i64(M + N), table, rows=N), out_k=K_la[layer], check=True)
+    ref_lse = oracle.row_lse(f64(Q_la), f64(K_prompt), f64(K_la))
+    assert np.all(np.abs(f64(lse) - np.asarray(ref_lse).reshape(L, H, N)) <= 1e-4)
+    imp = sp.score_lse(Q_la, K_prompt, lse, check=True)
+    full = sp.score(Q_la, K_prompt, K_la, check=True)
+    ref = oracle.importance(f64(Q_la), f64(K_prompt), f64(K_la))
+    for got in (imp, full):         # the scoring's own tolerance
+        assert np.all(np.abs(f64(got) - ref) <= np.minimum(1e-3, 1e-2 * np.abs(ref) + 1e-9))
+    kept, n_kept = sp.select(imp, 32, 3, "topk", 0.3, trim=False)
+    tokens, positions, cu_kept = sp.gather_kept(torch.arange(M, dtype=torch.int32, device="cuda"), [0, M], kept, n_kept)
+    # the target: the kept tokens' rows, packed, with capacity for the whole prompt
+    q0, k0, v0 = dev(M, H, d), dev(M, H_kv, d), dev(M, H_kv, d)
+    batch = sp.Batch(cu_kept, n_kept, table, rows=M)
+    q, k = sp.rotary(q0, k0, positions, plan)
+    target = sp.cache_alloc(pages, H_kv, page, d, kind=kind)
+    sp.cache_write(target, batch, k, v0, check=True)
+    out, _ = sp.attend(q, target, batch, check=True)
+    n = int(n_kept.item())
+    assert 0 < n < M
+    pos = positions[:n].cpu().numpy()[None]
+    qr = f64(torch.from_numpy(oracle.paged.rotary(f64(q0[:n]), pos, freq, axis)).to(torch.bfloat16))
+    assert np.all(np.abs(f64(q[:n]) - qr) <= 2.0 ** -7 * np.abs(qr) + 1e-6)     # a rounding may fall the other way
+    kk, vv = (f64(t).transpose(1, 0, 2) for t in (k[:n], v0[:n]))
+    if kind != "same":
+        kk, vv = (c * s[..., None] for c, s in (oracle.paged.quantise(t, kind) for t in (kk, vv)))
+    ref, ref_l, top, spread = oracle.paged.attend(f64(q[:n]), kk, vv, d ** -0.5)
+    bound, _ = attend_bounds("bf16", d, n, ref, spread, top, ref_l)
+    assert np.all(np.abs(f64(out[:n]) - ref) <= bound)
