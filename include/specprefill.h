@@ -415,7 +415,8 @@ typedef struct {
  * What the device arrays say is checked when the work runs.  A sequence is
  * left out, and SP_EDEVICE recorded in the workspace, unless
  * 0 <= cu_new[b] <= cu_new[b+1] <= T, cu_new[b+1] - cu_new[b] <= max_new and
- * 0 <= kv_len[b] <= table_width * page (and <= 2^31 - 1 - page).  A page index outside
+ * 0 <= kv_len[b] <= table_width * page (and <= 2^30).  Table entries of tokens that a
+ * call does not touch (outside every row's window, say) are not read.  A page index outside
  * [0, pages) is never followed: SP_EDEVICE is recorded, its tokens are not
  * written, read back as zeros, and are attended as if they were zeros or left out. */
 typedef struct {

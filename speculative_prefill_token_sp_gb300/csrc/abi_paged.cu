@@ -16,6 +16,9 @@ sp_status cache_write_launch(const sp_cache& c, const sp_batch& b, const sp_rows
 sp_status cache_read_launch(const sp_cache& c, const sp_batch& b, const sp_rows& k, const sp_rows& v, void* ws,
                             cudaStream_t st);
 sp_status attend_simple_launch(const AttendProblem& p, void* ws, cudaStream_t st);
+bool attend_step_supported(const sp_cache& c);
+size_t attend_step_ws_bytes(const sp_cache& c);
+sp_status attend_step_launch(const AttendProblem& p, void* ws, cudaStream_t st);
 
 namespace {
 
@@ -57,6 +60,11 @@ sp_status check_workspace(const char* fn, const void* ws, size_t have, size_t ne
         return SP_ENOMEM;
     }
     return SP_OK;
+}
+
+// Few rows per KV head in every sequence: at most the 16 of the step kernel.
+bool use_step(const sp_cache& c, const sp_batch& b, int H) {
+    return attend_step_supported(c) && (int64_t)b.max_new * (H / c.H_kv) <= 16;
 }
 
 }  // namespace
@@ -243,7 +251,7 @@ size_t sp_attend_workspace_size(const sp_cache* cache, const sp_batch* batch, in
         set_error("%s: H (%d) must be a multiple of H_kv (%d)", fn, H, cache->H_kv);
         return 0;
     }
-    return sizeof(WsHeader);
+    return use_step(*cache, *batch, H) ? attend_step_ws_bytes(*cache) : sizeof(WsHeader);
 }
 
 sp_status sp_attend(const sp_rows* q, const sp_cache* cache, const sp_batch* batch, int H, double scale,
@@ -276,7 +284,8 @@ sp_status sp_attend(const sp_rows* q, const sp_cache* cache, const sp_batch* bat
     p.q = *q; p.out = *out; p.cache = *cache; p.batch = *batch; p.H = H; p.scale = (float)scale;
     p.window = (int)std::min<int64_t>(window, INT32_MAX);
     p.lse = lse; p.lse_stride_row = lse_stride_row; p.lse_stride_head = lse_stride_head;
-    s = attend_simple_launch(p, ws, static_cast<cudaStream_t>(stream));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    s = use_step(*cache, *batch, H) ? attend_step_launch(p, ws, st) : attend_simple_launch(p, ws, st);
     if (s == SP_OK) clear_error();
     return s;
 }

@@ -34,7 +34,7 @@ __device__ __forceinline__ float warp_sum(float x) {
 template <typename T, int kKind>
 __global__ void __launch_bounds__(128) attend_simple_kernel(const __grid_constant__ AttendProblem p, WsHeader* hdr) {
     if (blockIdx.x == gridDim.x - 1) {
-        check_batch(p.batch, p.cache, true, hdr);
+        check_batch(p.batch, p.cache, p.window, hdr);
         return;
     }
     const int lane = threadIdx.x & 31;

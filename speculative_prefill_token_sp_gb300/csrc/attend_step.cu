@@ -1,0 +1,638 @@
+// Attention of few new tokens (decode and look-ahead steps) over the paged
+// cache: bf16, head dimension 64 or 128, sequences of at most 16 query rows
+// per KV head (a row is a new token's query head of the group).
+//
+// One pass over the keys with the running maximum and sum of each row's
+// softmax (base 2).  The work is bound by the cache's bytes: K and V are read
+// once, straight from global memory into the registers that mma.sync takes,
+// with no shared memory between.  Both products are taken transposed, so that
+// the query rows (8 a tile, few) are the narrow side and the accumulators are
+// small, and both sum over an index whose order does not matter (the entries of
+// a head, the tokens), so the order is chosen such that a lane's operand
+// registers are 16 consecutive bytes of a row.  Lane (n, q) = (lane / 4, lane % 4):
+//  * S^T = K Q^T: of tokens n and n + 8 the entries [j * 4E + q * E, + E) for
+//    each 16-byte load j of E entries; Q is laid out the same way;
+//  * O^T = V^T P^T: of tokens 2q, 2q + 1, 2q + 8, 2q + 9 the entries [c * 8E +
+//    n * E, + E); a byte permute pairs two tokens' entries.  P^T needs its 8 x 8
+//    tiles transposed (movmatrix).  A lane's sums are runs of E consecutive
+//    entries of rows 2q and 2q + 1.
+// The tensor cores' time at these row counts is a fraction of the loads'.
+//
+// A warp takes 16 tokens (32 where a row has at most 128 bytes) at a time and
+// keeps its own statistics; the four warps of a CTA take consecutive pieces of a
+// unit of 64 (128) tokens.  K of the next piece is requested when this piece's logits are
+// done, V when its product is, so a warp has 4 to 8 KB in flight all the time.
+// The units of all (sequence, KV head) pairs are laid end to end and cut into
+// equal runs, one per resident CTA, so a batch of any mixture of lengths keeps
+// every SM busy to the end; a pair that is cut leaves partial sums in the
+// workspace, and a second kernel, launched early, joins them in a fixed order.
+#include "paged.cuh"
+
+#include <algorithm>
+#include <atomic>
+
+namespace sp {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRows = 16;          // rows of a slot of partial sums
+
+struct StepArgs {
+    AttendProblem a;
+    int G;
+    int rows;               // most query rows of a sequence that is taken (8 or 16)
+    int P;                  // CTAs of the main kernel
+    WsHeader* hdr;
+    int* err;               // [P] what each CTA found wrong (0: nothing)
+    float* part_o;          // [P][2][kRows][d]
+    float2* part_ml;        // [P][2][kRows] maximum and sum
+};
+
+template <int D, int kKind>
+constexpr int warp_tokens() { return kKind == SP_CACHE_SAME && D == 128 ? 16 : 32; }
+template <int D, int kKind>
+constexpr int unit_tokens() { return kWarps * warp_tokens<D, kKind>(); }
+
+// Tokens [first, kv) that the rows of a sequence see, and their units.
+struct Span {
+    int first, units;
+};
+__device__ __forceinline__ Span span_of(const Seq& s, int window, int unit) {
+    Span r;
+    r.first = first_seen(s, window);
+    r.units = max(1, (s.kv - r.first + unit - 1) / unit);
+    return r;
+}
+
+__device__ __forceinline__ bool is_step(const StepArgs& p, const Seq& s) {
+    return s.n > 0 && (int64_t)s.n * p.G <= p.rows;
+}
+
+// Units of sequence i's pairs for one KV head (0: not taken here).
+__device__ __forceinline__ int seq_units(const StepArgs& p, int i, int unit, bool& bad) {
+    const Seq s = load_seq(p.a.batch, p.a.cache.page, i);
+    if (!s.ok) bad = true;
+    return is_step(p, s) ? span_of(s, p.a.window, unit).units : 0;
+}
+
+// Sum over all sequences, by one warp.
+__device__ __forceinline__ int64_t total_units(const StepArgs& p, int unit, bool& bad) {
+    int64_t sum = 0;
+    for (int i = threadIdx.x & 31; i < p.a.batch.B; i += 32) sum += seq_units(p, i, unit, bad);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    bad = __any_sync(0xffffffffu, bad);
+    return sum * p.a.cache.H_kv;
+}
+
+// The sequence whose units hold unit u (< total), and the unit at which it
+// begins, by one warp.
+__device__ __forceinline__ int find_unit(const StepArgs& p, int unit, int64_t u, int64_t& begin) {
+    int64_t base = 0;
+    const int lane = threadIdx.x & 31;
+    bool bad = false;
+    for (int i0 = 0; i0 < p.a.batch.B; i0 += 32) {
+        const int64_t mine = i0 + lane < p.a.batch.B ? (int64_t)seq_units(p, i0 + lane, unit, bad) * p.a.cache.H_kv : 0;
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, base + incl > u);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            begin = base + __shfl_sync(0xffffffffu, incl - mine, l);
+            return i0 + l;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    begin = base;
+    return p.a.batch.B;
+}
+
+// CTA c takes units [c * U / P, (c + 1) * U / P); the CTA of a unit:
+__device__ __forceinline__ int64_t cut(int64_t c, int64_t U, int P) { return c * U / P; }
+__device__ __forceinline__ int cta_of(int64_t u, int64_t U, int P) { return (int)(((u + 1) * P - 1) / U); }
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two 8-bit codes, in bits 8-15 and 24-31 of y (the other bits are ignored),
+// as a pair of bf16 (their values before the scale, exactly).
+template <int kKind>
+__device__ __forceinline__ uint32_t pair_of(uint32_t y) {
+    uint32_t r;
+    if (kKind == SP_CACHE_E4M3) {
+        // exponent and mantissa moved to bf16's place mean the value * 2^-120 (biases 7 and 127), also
+        // for e4m3's subnormals; the product with 2^120 is exact.  0x7f is NaN in e4m3, never written, and 480 here
+        const uint32_t b = ((y >> 4) & 0x07f007f0u) | (y & 0x80008000u);
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(0x7b807b80u));
+    } else {
+        // 0x4300 + (7 bits) is 128 + those bits; minus 128, or minus 256 (0x4380) where the sign bit is set
+        const uint32_t lo = ((y >> 8) & 0x007f007fu) | 0x43004300u, off = ((y >> 8) & 0x00800080u) | 0x43004300u;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(lo), "r"(off));
+    }
+    return r;
+}
+
+template <int kBytes>
+struct Chunk {
+    uint32_t w[kBytes / 4];
+};
+template <int kBytes>
+__device__ __forceinline__ Chunk<kBytes> fetch(const void* p, bool there) {
+    Chunk<kBytes> c;
+    if constexpr (kBytes == 16) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (there) v = __ldg(static_cast<const uint4*>(p));
+        c.w[0] = v.x; c.w[1] = v.y; c.w[2] = v.z; c.w[3] = v.w;
+    } else {
+        uint2 v = make_uint2(0, 0);
+        if (there) v = __ldg(static_cast<const uint2*>(p));
+        c.w[0] = v.x; c.w[1] = v.y;
+    }
+    return c;
+}
+
+// Transpose of an 8 x 8 tile of 16-bit values: lane (n, q) gives row n's columns 2q, 2q + 1 and gets column n's rows 2q, 2q + 1.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// kN: tiles of 8 query rows (1 or 2).  Registers bound the resident warps, and those the bytes in flight.
+template <int D, int kKind, int kN>
+__global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const __grid_constant__ StepArgs p) {
+    constexpr bool kSame = kKind == SP_CACHE_SAME;
+    constexpr int kSize = kSame ? 2 : 1;                    // bytes of an entry in the cache
+    constexpr int kTok = warp_tokens<D, kKind>(), kUnit = unit_tokens<D, kKind>();
+    constexpr int kT = kTok / 16;                           // tiles of 16 tokens
+    constexpr int kE = 16 / kSize;                          // entries of a K load
+    constexpr int kJ = D / (4 * kE);                        // K loads of a token
+    constexpr int kEv = D / 8 < kE ? D / 8 : kE;            // entries of a V load
+    constexpr int kC = D / (8 * kEv);                       // V loads of a token
+    constexpr int kVB = kEv * kSize;                        // bytes of a V load
+    constexpr int kO = kC * kEv / 2;                        // tiles of 16 entries of the sums
+    __shared__ float sm_o[kWarps][8 * kN][D + 4];
+    __shared__ float2 sm_ml[kWarps][8 * kN];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = lane >> 2, q4 = lane & 3;
+    const sp_cache& c = p.a.cache;
+    const sp_batch& bt = p.a.batch;
+    bool bad_seq = false, bad_page = false;
+    cudaTriggerProgrammaticLaunchCompletion();      // the joining kernel may line up: it waits for this one's end
+    const int64_t U = total_units(p, kUnit, bad_seq);
+    int64_t u = cut(blockIdx.x, U, p.P);
+    const int64_t u_end = cut(blockIdx.x + 1, U, p.P);
+    int64_t begin = 0;
+    int b = u < u_end ? find_unit(p, kUnit, u, begin) : 0;
+    const float f = p.a.scale * 1.4426950408889634f;
+
+    while (u < u_end) {
+        const Seq s = load_seq(bt, c.page, b);
+        if (!is_step(p, s)) {
+            ++b;
+            continue;
+        }
+        const Span span = span_of(s, p.a.window, kUnit);
+        const int64_t in_seq = u - begin;
+        if (in_seq >= (int64_t)span.units * c.H_kv) {
+            begin += (int64_t)span.units * c.H_kv;
+            ++b;
+            continue;
+        }
+        const int g = (int)(in_seq / span.units), from = (int)(in_seq - (int64_t)g * span.units);
+        const int to = (int)min((int64_t)span.units, from + (u_end - u));
+        const int rows = s.n * p.G;
+
+        // query row n (and n + 8) as operands, and the tokens that rows 2q, 2q + 1 (+ 8) see
+        uint32_t qb[kN][2 * kJ * (kE / 8)][2];
+        int last[kN][2], first[kN][2];
+#pragma unroll
+        for (int h = 0; h < kN; ++h) {
+            const int r = n + 8 * h, t = r / p.G;
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.a.q.data) + (s.row0 + t) * p.a.q.stride_row +
+                                       (g * p.G + r - t * p.G) * p.a.q.stride_head;
+#pragma unroll
+            for (int j = 0; j < kJ; ++j)
+#pragma unroll
+                for (int e = 0; e < kE / 8; ++e) {
+                    const Chunk<16> x = fetch<16>(src + j * 4 * kE + q4 * kE + e * 8, r < rows);
+                    const int k = (j * (kE / 8) + e) * 2;
+                    qb[h][k][0] = x.w[0]; qb[h][k][1] = x.w[1];
+                    qb[h][k + 1][0] = x.w[2]; qb[h][k + 1][1] = x.w[3];
+                }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int ry = 8 * h + 2 * q4 + y;
+                last[h][y] = ry < rows ? s.kv - s.n + ry / p.G : -1;
+                first[h][y] = p.a.window ? last[h][y] - p.a.window + 1 : 0;
+            }
+        }
+        const int all_last = s.kv - s.n, all_first = p.a.window ? s.kv - p.a.window : 0;  // tokens that every row sees
+
+        float o[kN][kO][4];
+        float m[kN][2], z[kN][2];
+#pragma unroll
+        for (int h = 0; h < kN; ++h) {
+            m[h][0] = m[h][1] = -INFINITY;
+            z[h][0] = z[h][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kO; ++i)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[h][i][x] = 0.f;
+        }
+
+        // this lane's token (lane % kTok) of a piece: where its rows are (entries; -1: nowhere) and its scales
+        const int32_t* table = bt.table + (int64_t)b * bt.table_stride;
+        const int tok_lane = lane & (kTok - 1);
+        auto page_of = [&](int tok) { return tok < s.kv ? table[(unsigned)tok / (unsigned)c.page] : 0; };
+        struct Where {
+            int64_t at;
+            float ks, vs;
+        };
+        auto place = [&](int tok, int pg) {
+            Where w{-1, 1.f, 1.f};
+            if (tok < s.kv) {
+                if ((unsigned)pg < (unsigned)c.pages) {
+                    const int slot = (int)((unsigned)tok % (unsigned)c.page);
+                    w.at = row_offset(c, pg, g, slot);
+                    if (!kSame) {
+                        const int64_t sc = scale_offset(c, pg, g, slot);
+                        w.ks = __ldg(c.k_scale + sc);
+                        w.vs = __ldg(c.v_scale + sc);
+                    }
+                } else {
+                    bad_page = true;
+                }
+            }
+            return w;
+        };
+        Chunk<16> kr[2 * kT][kJ];
+        Chunk<kVB> vr[4 * kT][kC];
+        auto load_k = [&](const Where& w) {
+#pragma unroll
+            for (int t = 0; t < 2 * kT; ++t) {
+                const int64_t at = __shfl_sync(0xffffffffu, w.at, t * 8 + n);
+                const char* src = static_cast<const char*>(c.k) + (at + q4 * kE) * kSize;
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) kr[t][j] = fetch<16>(src + j * 64, at >= 0);
+            }
+        };
+        auto load_v = [&](const Where& w) {
+#pragma unroll
+            for (int t = 0; t < 4 * kT; ++t) {
+                const int tok = (t >> 1) * 8 + 2 * q4 + (t & 1);
+                const int64_t at = __shfl_sync(0xffffffffu, w.at, tok);
+                const char* src = static_cast<const char*>(c.v) + (at + n * kEv) * kSize;
+#pragma unroll
+                for (int i = 0; i < kC; ++i) vr[t][i] = fetch<kVB>(src + i * 8 * kVB, at >= 0);
+            }
+        };
+
+        const int tok0 = span.first + warp * kTok;
+        Where cur = place(tok0 + from * kUnit + tok_lane, page_of(tok0 + from * kUnit + tok_lane));
+        load_k(cur);
+        load_v(cur);
+        int next_page = page_of(tok0 + (from + 1) * kUnit + tok_lane);
+        for (int i = from; i < to; ++i) {
+            const int base = tok0 + i * kUnit;
+            const bool more = i + 1 < to;
+            Where nxt{-1, 1.f, 1.f};
+            if (more) {
+                nxt = place(base + kUnit + tok_lane, next_page);
+                next_page = page_of(base + 2 * kUnit + tok_lane);
+            }
+            // logits: x[h][t] holds tokens 16t + n (first two) and 16t + n + 8, rows 8h + 2q and 8h + 2q + 1
+            float x[kN][kT][4];
+#pragma unroll
+            for (int t = 0; t < kT; ++t) {
+#pragma unroll
+                for (int h = 0; h < kN; ++h)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) x[h][t][y] = 0.f;
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    const Chunk<16>&lo = kr[2 * t][j], &hi = kr[2 * t + 1][j];
+#pragma unroll
+                    for (int k = 0; k < kE / 4; ++k) {
+                        uint32_t a[4];
+                        if constexpr (kSame) {
+                            a[0] = lo.w[2 * k]; a[1] = hi.w[2 * k];
+                            a[2] = lo.w[2 * k + 1]; a[3] = hi.w[2 * k + 1];
+                        } else {
+                            a[0] = pair_of<kKind>(__byte_perm(lo.w[k], 0, 0x1404));
+                            a[1] = pair_of<kKind>(__byte_perm(hi.w[k], 0, 0x1404));
+                            a[2] = pair_of<kKind>(__byte_perm(lo.w[k], 0, 0x3424));
+                            a[3] = pair_of<kKind>(__byte_perm(hi.w[k], 0, 0x3424));
+                        }
+#pragma unroll
+                        for (int h = 0; h < kN; ++h) {
+                            const int kk = j * (kE / 4) + k;
+                            mma16816(x[h][t], a, qb[h][kk][0], qb[h][kk][1]);
+                        }
+                    }
+                }
+            }
+            if (more) load_k(nxt);
+            const bool masked = base + kTok - 1 > all_last || base < all_first;
+            float vs[kSame ? 1 : kT][2];
+            float top[kN][2];
+#pragma unroll
+            for (int h = 0; h < kN; ++h) top[h][0] = m[h][0], top[h][1] = m[h][1];
+#pragma unroll
+            for (int t = 0; t < kT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int tl = 16 * t + 8 * e + n, tok = base + tl;
+                    float ft = f;
+                    if constexpr (!kSame) {
+                        ft *= __shfl_sync(0xffffffffu, cur.ks, tl);
+                        vs[t][e] = __shfl_sync(0xffffffffu, cur.vs, tl);
+                    }
+#pragma unroll
+                    for (int h = 0; h < kN; ++h)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            float& v = x[h][t][2 * e + y];
+                            v *= ft;
+                            if (masked && (tok > last[h][y] || tok < first[h][y])) v = -INFINITY;
+                            top[h][y] = fmaxf(top[h][y], v);
+                        }
+                }
+            // a NaN logit is not a maximum, but its weight is NaN and spreads to the row's sums
+            bool grows = false;
+#pragma unroll
+            for (int h = 0; h < kN; ++h)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                    for (int w = 4; w < 32; w <<= 1)
+                        top[h][y] = fmaxf(top[h][y], __shfl_xor_sync(0xffffffffu, top[h][y], w));
+                    grows |= top[h][y] > m[h][y];
+                }
+            if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+                for (int h = 0; h < kN; ++h)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float a = top[h][y] == -INFINITY ? 1.f : ex2(m[h][y] - top[h][y]);
+                        m[h][y] = top[h][y];
+                        z[h][y] *= a;
+#pragma unroll
+                        for (int k = 0; k < kO; ++k) {
+                            o[h][k][y] *= a;
+                            o[h][k][2 + y] *= a;
+                        }
+                    }
+            }
+            uint32_t pb[kN][kT][2];
+#pragma unroll
+            for (int h = 0; h < kN; ++h) {
+                const float r0 = m[h][0] == -INFINITY ? 0.f : m[h][0], r1 = m[h][1] == -INFINITY ? 0.f : m[h][1];
+#pragma unroll
+                for (int t = 0; t < kT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float w0 = ex2(x[h][t][2 * e] - r0), w1 = ex2(x[h][t][2 * e + 1] - r1);
+                        z[h][0] += w0;
+                        z[h][1] += w1;
+                        if constexpr (!kSame) {
+                            // a masked token's weight stays 0 whatever its scale is
+                            w0 = w0 == 0.f ? 0.f : w0 * vs[t][e];
+                            w1 = w1 == 0.f ? 0.f : w1 * vs[t][e];
+                        }
+                        pb[h][t][e] = transpose8(pack_bf16(w0, w1));
+                    }
+            }
+#pragma unroll
+            for (int t = 0; t < kT; ++t)
+#pragma unroll
+                for (int cc = 0; cc < kC; ++cc)
+#pragma unroll
+                    for (int e = 0; e < kEv; e += 2) {
+                        uint32_t a[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {       // entry e + (y & 1) of tokens 2q, 2q + 1 (+ 8 for y >= 2)
+                            const int w = (e + (y & 1)) * kSize / 4, at = 4 * t + (y >> 1) * 2;
+                            if constexpr (kSame) {
+                                a[y] = __byte_perm(vr[at][cc].w[w], vr[at + 1][cc].w[w], y & 1 ? 0x7632 : 0x5410);
+                            } else {
+                                // the first token's byte to bits 8-15, the second's to bits 24-31
+                                const uint32_t i4 = (e + (y & 1)) & 3, sel = 0x4000u + (i4 << 12) + (i4 << 4);
+                                a[y] = pair_of<kKind>(__byte_perm(vr[at][cc].w[w], vr[at + 1][cc].w[w], sel));
+                            }
+                        }
+#pragma unroll
+                        for (int h = 0; h < kN; ++h) mma16816(o[h][(cc * kEv + e) / 2], a, pb[h][t][0], pb[h][t][1]);
+                    }
+            if (more) load_v(nxt);
+            cur = nxt;
+        }
+
+        // join the four warps: lane (n, q) holds entries cc * 8 kEv + n * kEv + e of rows 2q, 2q + 1
+#pragma unroll
+        for (int h = 0; h < kN; ++h)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int r = 8 * h + 2 * q4 + y;
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) z[h][y] += __shfl_xor_sync(0xffffffffu, z[h][y], w);
+                if (n == 0) sm_ml[warp][r] = make_float2(m[h][y], z[h][y]);
+#pragma unroll
+                for (int k = 0; k < kO; ++k) {
+                    const int e = 2 * k, at = (e / kEv) * 8 * kEv + n * kEv + e % kEv;
+                    sm_o[warp][r][at] = o[h][k][y];
+                    sm_o[warp][r][at + 1] = o[h][k][2 + y];
+                }
+            }
+        __syncthreads();
+        const bool whole = from == 0 && to == span.units;
+        for (int i = threadIdx.x; i < rows * (D / 8); i += kThreads) {
+            const int r = i / (D / 8), e = (i % (D / 8)) * 8;
+            float mm = -INFINITY, zz = 0.f, v[8] = {};
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_ml[w][r].x);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 ml = sm_ml[w][r];
+                if (ml.x == -INFINITY && ml.y == 0.f) continue;         // saw no token of the row
+                // without a maximum but with a sum: all its logits were NaN, and so is the sum
+                const float a = ml.x == -INFINITY ? 1.f : ex2(ml.x - mm);
+                zz += ml.y * a;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] += sm_o[w][r][e + k] * a;
+            }
+            if (whole) {
+                const float inv = zz == 0.f ? 0.f : 1.f / zz;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = zz == 0.f ? 0.f : v[k] * inv;
+                const int t = r / p.G, h = g * p.G + r - t * p.G;
+                store8(static_cast<__nv_bfloat16*>(p.a.out.data) + (s.row0 + t) * p.a.out.stride_row +
+                           h * p.a.out.stride_head + e, v);
+                if (p.a.lse && e == 0)
+                    p.a.lse[(s.row0 + t) * p.a.lse_stride_row + h * p.a.lse_stride_head] =
+                        zz == 0.f ? -INFINITY : (mm + log2f(zz)) * 0.6931471805599453f;
+            } else {
+                const int64_t slot = ((int64_t)blockIdx.x * 2 + (from == 0 ? 1 : 0)) * kRows + r;
+                store8(p.part_o + slot * D + e, v);
+                if (e == 0) p.part_ml[slot] = make_float2(mm, zz);
+            }
+        }
+        __syncthreads();
+        u += to - from;
+    }
+    const int any = (__syncthreads_or(bad_seq) ? 1 : 0) | (__syncthreads_or(bad_page) ? 2 : 0);
+    if (threadIdx.x == 0) p.err[blockIdx.x] = any;
+}
+
+// Joins the parts of the pairs that were cut: block (i, r) takes row r of pair
+// i = (sequence, KV head), a thread one entry.  Block (0, 0) also gathers the status.
+template <int D, int kKind>
+__global__ void __launch_bounds__(D) step_join_kernel(const __grid_constant__ StepArgs p) {
+    constexpr int kUnit = unit_tokens<D, kKind>();
+    bool bad = false;
+    const int i = blockIdx.x, b = i / p.a.cache.H_kv, g = i - b * p.a.cache.H_kv, r = blockIdx.y;
+    const Seq s = load_seq(p.a.batch, p.a.cache.page, b);
+    const bool mine = is_step(p, s) && r < s.n * p.G;
+    int64_t U = 0, begin = 0;
+    if (mine) {
+        for (int k = threadIdx.x & 31; k < p.a.batch.B; k += 32) {
+            const int64_t units = seq_units(p, k, kUnit, bad);
+            U += units;
+            if (k < b) begin += units;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            U += __shfl_xor_sync(0xffffffffu, U, o);
+            begin += __shfl_xor_sync(0xffffffffu, begin, o);
+        }
+    }
+    cudaGridDependencySynchronize();        // the main kernel's partial sums
+    if (i == 0 && r == 0) {
+        int code = 0;
+        for (int k = threadIdx.x; k < p.P; k += D) code |= p.err[k];
+        code = __syncthreads_or(code);
+        if (threadIdx.x == 0) {
+            p.hdr->status = code ? SP_EDEVICE : SP_OK;
+            p.hdr->where = code;            // 1: impossible lengths or offsets, 2: a page index out of range
+        }
+    }
+    if (!mine) return;
+    U *= p.a.cache.H_kv;
+    const int units = span_of(s, p.a.window, kUnit).units;
+    begin = begin * p.a.cache.H_kv + (int64_t)g * units;
+    const int c0 = cta_of(begin, U, p.P), c1 = cta_of(begin + units - 1, U, p.P);
+    if (c0 == c1) return;                   // written by the main kernel
+    const int e = threadIdx.x;
+    float m = -INFINITY;
+    for (int k = c0; k <= c1; ++k) {
+        if (cut(k, U, p.P) == cut(k + 1, U, p.P)) continue;     // a CTA without units
+        m = fmaxf(m, p.part_ml[((int64_t)k * 2 + (cut(k, U, p.P) <= begin ? 1 : 0)) * kRows + r].x);
+    }
+    float z = 0.f, v = 0.f;
+    for (int k = c0; k <= c1; ++k) {
+        if (cut(k, U, p.P) == cut(k + 1, U, p.P)) continue;
+        const int64_t slot = ((int64_t)k * 2 + (cut(k, U, p.P) <= begin ? 1 : 0)) * kRows + r;
+        const float2 ml = p.part_ml[slot];
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;
+        const float a = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
+        z += ml.y * a;
+        v += p.part_o[slot * D + e] * a;
+    }
+    const int t = r / p.G, h = g * p.G + r - t * p.G;
+    static_cast<__nv_bfloat16*>(p.a.out.data)[(s.row0 + t) * p.a.out.stride_row + h * p.a.out.stride_head + e] =
+        __float2bfloat16_rn(z == 0.f ? 0.f : v / z);
+    if (p.a.lse && e == 0)
+        p.a.lse[(s.row0 + t) * p.a.lse_stride_row + h * p.a.lse_stride_head] =
+            z == 0.f ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
+}
+
+int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+int ctas(int rows) { return sm_count() * (rows <= 8 ? 3 : 2); }
+
+template <int D, int kKind>
+sp_status launch(const StepArgs& p, cudaStream_t st) {
+    if (p.rows <= 8) step_kernel<D, kKind, 1><<<p.P, kThreads, 0, st>>>(p);
+    else step_kernel<D, kKind, 2><<<p.P, kThreads, 0, st>>>(p);
+    SP_LAUNCH_CHECK();
+    const int64_t rows = std::min<int64_t>(p.rows, (int64_t)p.a.batch.max_new * p.G);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.a.batch.B * p.a.cache.H_kv), (unsigned)std::max<int64_t>(1, rows));
+    cfg.blockDim = dim3(D);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    SP_CUDA_TRY(cudaLaunchKernelEx(&cfg, step_join_kernel<D, kKind>, p));
+    SP_LAUNCH_CHECK();
+    return SP_OK;
+}
+
+template <int D>
+sp_status launch_kind(const StepArgs& p, cudaStream_t st) {
+    switch (p.a.cache.kind) {
+        case SP_CACHE_SAME: return launch<D, SP_CACHE_SAME>(p, st);
+        case SP_CACHE_E4M3: return launch<D, SP_CACHE_E4M3>(p, st);
+        default: return launch<D, SP_CACHE_INT8>(p, st);
+    }
+}
+
+}  // namespace
+
+bool attend_step_supported(const sp_cache& c) {
+    if (c.dtype != SP_BF16 || (c.d != 64 && c.d != 128)) return false;
+    // the 8-bit kinds are read 16 bytes at a time
+    return c.kind == SP_CACHE_SAME ||
+           ((reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v) | (uintptr_t)c.stride_page |
+             (uintptr_t)c.stride_head | (uintptr_t)c.stride_slot) % 16 == 0);
+}
+
+size_t attend_step_ws_bytes(const sp_cache& c) {
+    const size_t P = (size_t)ctas(8);       // the larger of the two grids
+    Carve w;
+    w.take(P * sizeof(int));
+    w.take(P * 2 * kRows * c.d * sizeof(float));
+    w.take(P * 2 * kRows * sizeof(float2));
+    return w.off;
+}
+
+sp_status attend_step_launch(const AttendProblem& a, void* ws, cudaStream_t st) {
+    StepArgs p;
+    p.a = a;
+    p.G = a.H / a.cache.H_kv;
+    p.rows = (int64_t)a.batch.max_new * p.G <= 8 ? 8 : 16;
+    p.P = ctas(p.rows);
+    Carve w;
+    char* base = static_cast<char*>(ws);
+    p.hdr = reinterpret_cast<WsHeader*>(base);
+    p.err = reinterpret_cast<int*>(base + w.take(p.P * sizeof(int)));
+    p.part_o = reinterpret_cast<float*>(base + w.take((size_t)p.P * 2 * kRows * a.cache.d * sizeof(float)));
+    p.part_ml = reinterpret_cast<float2*>(base + w.take((size_t)p.P * 2 * kRows * sizeof(float2)));
+    return a.cache.d == 64 ? launch_kind<64>(p, st) : launch_kind<128>(p, st);
+}
+
+}  // namespace sp

@@ -20,11 +20,16 @@ __device__ __forceinline__ Seq load_seq(const sp_batch& b, int page, int i) {
     const int64_t lo = b.cu_new[i], hi = b.cu_new[i + 1], kv = b.kv_len[i];
     Seq s;
     s.ok = lo >= 0 && hi >= lo && hi <= b.T && hi - lo <= b.max_new && kv >= 0 &&
-           kv <= (int64_t)b.table_width * page && kv <= (int64_t)INT32_MAX - page;
+           kv <= (int64_t)b.table_width * page && kv <= (int64_t)1 << 30;
     s.row0 = lo;
     s.n = s.ok ? (int)(hi - lo) : 0;
     s.kv = s.ok ? (int)kv : 0;
     return s;
+}
+
+// The first token that a row of the sequence sees.
+__device__ __forceinline__ int first_seen(const Seq& s, int window) {
+    return window ? (int)max((int64_t)0, (int64_t)s.kv - s.n - window + 1) : 0;
 }
 
 // The sequence that row r is a new token of: the last b with cu_new[b] <= r
@@ -153,9 +158,9 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
 }
 
 // One block's check of everything the batch's device arrays say about the
-// tokens [first, kv) of each sequence, `first` being the first new token or,
-// with `all`, the first token.  Writes the status: the only writer of the call.
-__device__ __forceinline__ void check_batch(const sp_batch& b, const sp_cache& c, bool all, WsHeader* hdr) {
+// tokens [first, kv) of each sequence, `first` being the first new token or, with
+// window >= 0, the first one that a row sees.  Writes the status: the only writer of the call.
+__device__ __forceinline__ void check_batch(const sp_batch& b, const sp_cache& c, int window, WsHeader* hdr) {
     __shared__ int bad;
     if (threadIdx.x == 0) bad = 0;
     __syncthreads();
@@ -165,7 +170,7 @@ __device__ __forceinline__ void check_batch(const sp_batch& b, const sp_cache& c
         const Seq s = load_seq(b, c.page, i);
         if (!s.ok) mine = 1;
         if (s.n == 0 || s.kv == 0) continue;
-        const int first = all ? 0 : max(0, s.kv - s.n) / c.page, last = (s.kv - 1) / c.page;
+        const int first = (window < 0 ? max(0, s.kv - s.n) : first_seen(s, window)) / c.page, last = (s.kv - 1) / c.page;
         for (int q = first + lane; q <= last; q += 32) {
             const int pg = b.table[(int64_t)i * b.table_stride + q];
             if (pg < 0 || pg >= c.pages) mine = 2;

@@ -339,6 +339,25 @@ def test_unwritten_slots_have_no_effect(sp, fill, new):
     check_attend(sp, H=4, H_kv=2, d=128, page=64, new=new, kv=[205], junk=fill)
 
 
+@pytest.mark.parametrize("d,dtype,n", [(64, "bf16", 1), (128, "bf16", 3), (64, "f32", 2), (128, "bf16", 90), (40, "bf16", 5)])
+def test_pages_behind_the_window_may_be_gone(sp, d, dtype, n):
+    import torch
+    rng = np.random.default_rng(13)
+    td = torch_dtype(dtype)
+    H, H_kv, page, kv, window = 4, 2, 16, 700, 100
+    cache, table, kval, vval = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=[kv], dtype=td)
+    first = kv - n - window + 1
+    cache.k[table[0, first // page], :, :first % page] = float("nan")       # in the window's first page, before it
+    cache.v[table[0, first // page], :, :first % page] = float("nan")
+    table[0, :first // page] = -1
+    batch, _ = make_batch(sp, [n], [kv], table)
+    q = torch.from_numpy(rng.standard_normal((n, H, d))).to(td).cuda()
+    out, lse = sp.attend(q, cache, batch, window=window, check=True)
+    ref, ref_lse, top, spread = oracle.paged.attend(f64(q), kval[0], vval[0], d ** -0.5, window)
+    bound, lse_bound = attend_bounds(dtype, d, window, ref, spread, top, ref_lse)
+    assert np.all(np.abs(f64(out) - ref) <= bound) and np.all(np.abs(f64(lse) - ref_lse) <= lse_bound)
+
+
 def test_a_long_cache(sp):
     check_attend(sp, H=2, H_kv=1, d=64, page=16, new=[1, 17], kv=[70001, 9001])
 
