@@ -5,6 +5,9 @@
 
 #include <string.h>
 
+#include <algorithm>
+#include <atomic>
+
 namespace sp {
 
 // Implemented in rotary.cu, cache.cu and attend_*.cu.
@@ -19,6 +22,9 @@ sp_status attend_simple_launch(const AttendProblem& p, void* ws, cudaStream_t st
 bool attend_step_supported(const sp_cache& c);
 size_t attend_step_ws_bytes(const sp_cache& c);
 sp_status attend_step_launch(const AttendProblem& p, void* ws, cudaStream_t st);
+bool attend_tc_supported(const sp_cache& c, int G);
+size_t attend_tc_ws_bytes(const sp_cache& c, const sp_batch& b, int G);
+sp_status attend_tc_launch(const AttendProblem& p, int min_rows, void* ws, cudaStream_t st);
 
 namespace {
 
@@ -62,12 +68,41 @@ sp_status check_workspace(const char* fn, const void* ws, size_t have, size_t ne
     return SP_OK;
 }
 
-// Few rows per KV head in every sequence: at most the 16 of the step kernel.
-bool use_step(const sp_cache& c, const sp_batch& b, int H) {
-    return attend_step_supported(c) && (int64_t)b.max_new * (H / c.H_kv) <= 16;
+// Which kernels a call takes.
+enum Path {
+    kSimple,        // the general one
+    kStep,          // every sequence has at most the 16 rows per KV head of the step kernel
+    kChunks,        // one sequence with more, or a cache that the step kernel does not take
+    kMixed          // the step kernel for the sequences with few rows, the tensor-core one for the others
+};
+Path path_of(const sp_cache& c, const sp_batch& b, int H) {
+    const int G = H / c.H_kv;
+    const bool step = attend_step_supported(c);
+    if (step && (int64_t)b.max_new * G <= 16) return kStep;
+    if (!attend_tc_supported(c, G)) return kSimple;
+    return step && b.B > 1 ? kMixed : kChunks;
+}
+
+size_t path_bytes(Path path, const sp_cache& c, const sp_batch& b, int H) {
+    switch (path) {
+        case kStep: return attend_step_ws_bytes(c);
+        case kChunks: return attend_tc_ws_bytes(c, b, H / c.H_kv);
+        case kMixed: return std::max(attend_step_ws_bytes(c), attend_tc_ws_bytes(c, b, H / c.H_kv));
+        default: return sizeof(WsHeader);
+    }
 }
 
 }  // namespace
+
+int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
 
 sp_status check_cache(const char* fn, const sp_cache* c) {
     if (!c || !c->k || !c->v) {
@@ -251,7 +286,7 @@ size_t sp_attend_workspace_size(const sp_cache* cache, const sp_batch* batch, in
         set_error("%s: H (%d) must be a multiple of H_kv (%d)", fn, H, cache->H_kv);
         return 0;
     }
-    return use_step(*cache, *batch, H) ? attend_step_ws_bytes(*cache) : sizeof(WsHeader);
+    return path_bytes(path_of(*cache, *batch, H), *cache, *batch, H);
 }
 
 sp_status sp_attend(const sp_rows* q, const sp_cache* cache, const sp_batch* batch, int H, double scale,
@@ -282,10 +317,18 @@ sp_status sp_attend(const sp_rows* q, const sp_cache* cache, const sp_batch* bat
     if ((s = check_workspace(fn, ws, ws_bytes, need)) != SP_OK) return s;
     AttendProblem p;
     p.q = *q; p.out = *out; p.cache = *cache; p.batch = *batch; p.H = H; p.scale = (float)scale;
-    p.window = (int)std::min<int64_t>(window, INT32_MAX);
+    p.window = window >= (int64_t)1 << 30 ? 0 : (int)window;       // kv_len is at most 2^30: no limit at all
     p.lse = lse; p.lse_stride_row = lse_stride_row; p.lse_stride_head = lse_stride_head;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    s = use_step(*cache, *batch, H) ? attend_step_launch(p, ws, st) : attend_simple_launch(p, ws, st);
+    switch (path_of(*cache, *batch, H)) {
+        case kSimple: s = attend_simple_launch(p, ws, st); break;
+        case kStep: s = attend_step_launch(p, ws, st); break;
+        case kChunks: s = attend_tc_launch(p, 0, ws, st); break;
+        case kMixed:
+            s = attend_step_launch(p, ws, st);
+            if (s == SP_OK) s = attend_tc_launch(p, 16, ws, st);
+            break;
+    }
     if (s == SP_OK) clear_error();
     return s;
 }

@@ -29,7 +29,6 @@
 #include "paged.cuh"
 
 #include <algorithm>
-#include <atomic>
 
 namespace sp {
 namespace {
@@ -558,16 +557,6 @@ __global__ void __launch_bounds__(D) step_join_kernel(const __grid_constant__ St
     if (p.a.lse && e == 0)
         p.a.lse[(s.row0 + t) * p.a.lse_stride_row + h * p.a.lse_stride_head] =
             z == 0.f ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
-}
-
-int sm_count() {
-    static std::atomic<int> known[64];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
-    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
-    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
-    return n;
 }
 
 int ctas(int rows) { return sm_count() * (rows <= 8 ? 3 : 2); }

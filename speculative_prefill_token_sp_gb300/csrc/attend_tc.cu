@@ -1,0 +1,890 @@
+// Attention of chunks of new tokens over the paged cache on tensor cores:
+// tcgen05.mma + TMA + TMEM.  bf16, head dimension 64 or 128.
+//
+// Query rows are packed by KV head: row r of a tile is token r / G, head r % G
+// of the group, so the keys and values of a KV head are read once for all its
+// query heads.  An item is 2 tiles of 128 rows (A and B) of one sequence and KV
+// head against tiles of 128 keys; one pass over the keys, with the running
+// maximum and sum of each row's softmax (base 2):
+//   S = Q K^T (TMEM)  ->  P = 2^(f S - m) (registers, back to TMEM as bf16)  ->  O += P V (TMEM)
+//
+// The three steps of one tile depend on each other, so the two row tiles take
+// turns: while the softmax of A runs, the tensor cores do P V and the next S of
+// B.  Per 256 x 128 logits the MMAs take 2048 cycles (d = 128) and each
+// softmax warpgroup has as long for its 128 x 128 logits: one thread a row, so
+// that maximum and sum need no exchange between threads.  O stays in TMEM; it
+// is scaled only when a row's maximum grows by more than 2^8 over the one it
+// is held by (P is then at most 2^8, and bf16 has the same precision there).
+//
+// Warp roles of a CTA (one per SM; 512 threads):
+//  * warps 0-3, 4-7: softmax of tiles A and B, the scaling of O, and the output;
+//  * warps 8-11: convert the rows of an 8-bit cache to bf16 into the shared-
+//    memory tiles (unused for a cache of bf16);
+//  * warp 12: issues the MMAs;
+//  * warp 13: TMA loads of K and V tiles, page by page (boxes of the largest
+//    power of two that divides the page), and of Q;
+//  * warp 14: zeroes what a V tile holds of slots without a token, as 0 * NaN
+//    in P V would be NaN.  (K needs none: masked logits are replaced.)
+//
+// The items of the call, longest part first within a sequence, are laid end to
+// end, and each CTA takes an equal run of key tiles, so that the SMs end
+// together whatever the lengths.  An item that is cut leaves its sums in the
+// workspace and a joining kernel adds them up in a fixed order.
+#include "paged.cuh"
+#include "tc_ptx.cuh"
+
+#include <algorithm>
+
+namespace sp {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kRowsItem = 256;
+constexpr int kKeys = 128;              // keys of a tile
+constexpr int kSmem = 227 * 1024;
+constexpr int kPlanThreads = 1024;
+
+struct Item {
+    int b, t0;              // sequence, first new token
+    int lo, tiles;          // first key tile, number of key tiles (at least 1)
+};
+
+struct TcArgs {
+    AttendProblem a;
+    int G, tpt;             // query heads of a KV head; new tokens of a row tile
+    int min_rows;           // sequences with at most this many rows per KV head are left to the step kernel
+    int P;                  // CTAs
+    int box;                // rows of a TMA box
+    int clear;              // 1: the plan clears the status
+    int max_items;
+    WsHeader* hdr;
+    int* n_items;           // [1]
+    Item* items;            // [max_items]
+    int64_t* pre;           // [max_items + 1] key tiles before an item, for one KV head
+    float* part_o;          // [P][2][d / 4][256][4]
+    float2* part_ml;        // [P][2][256]
+};
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+__device__ __forceinline__ bool is_tc(const TcArgs& p, const Seq& s) {
+    return s.n > 0 && (int64_t)s.n * p.G > p.min_rows;
+}
+
+__device__ __forceinline__ Item item_of(const TcArgs& p, const Seq& s, int b, int qt) {
+    Item it;
+    it.b = b;
+    it.t0 = qt * 2 * p.tpt;
+    const int last = min(s.n, it.t0 + 2 * p.tpt) - 1 + s.kv - s.n;      // place of the item's last token
+    const int first = p.a.window ? max(0, s.kv - s.n + it.t0 - p.a.window + 1) : 0;
+    it.lo = first / kKeys;
+    it.tiles = last < 0 ? 1 : last / kKeys + 1 - it.lo;
+    return it;
+}
+
+// Inclusive sum over the block's threads.
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* warp_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t w = warp_sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        warp_sums[lane] = w;
+    }
+    __syncthreads();
+    const int64_t r = x + (warp ? warp_sums[warp - 1] : 0);
+    __syncthreads();
+    return r;
+}
+
+// Lists the items (all sequences, one KV head) and their key tiles' running sum.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ TcArgs p) {
+    __shared__ int64_t sums[32];
+    __shared__ int64_t at_item, at_tile;
+    cudaTriggerProgrammaticLaunchCompletion();
+    if (threadIdx.x == 0) at_item = 0, at_tile = 0;
+    if (threadIdx.x == 0 && p.clear) p.hdr->status = SP_OK, p.hdr->where = 0;
+    __syncthreads();
+    const int tpi = 2 * p.tpt;
+    for (int b0 = 0; b0 < p.a.batch.B; b0 += kPlanThreads) {
+        const int b = b0 + threadIdx.x;
+        int mine = 0;
+        if (b < p.a.batch.B) {
+            const Seq s = load_seq(p.a.batch, p.a.cache.page, b);
+            if (!s.ok) record_error(p.hdr, SP_EDEVICE, 1);
+            if (is_tc(p, s)) mine = (s.n + tpi - 1) / tpi;
+        }
+        const int64_t incl = block_scan(mine, sums);
+        // the order within a sequence is from its last tokens, which see most keys, to its first
+        const int64_t base = at_item + incl - mine;
+        for (int i = 0; i < mine; ++i)
+            if (base + i < p.max_items) p.items[base + i] = Item{b, mine - 1 - i, 0, 0};
+        __syncthreads();
+        if (threadIdx.x == kPlanThreads - 1) at_item += incl;
+        __syncthreads();
+    }
+    const int n = (int)min(at_item, (int64_t)p.max_items);
+    for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+        const int i = i0 + threadIdx.x;
+        Item it{0, 0, 0, 0};
+        if (i < n) {
+            const Item raw = p.items[i];
+            it = item_of(p, load_seq(p.a.batch, p.a.cache.page, raw.b), raw.b, raw.t0);
+            p.items[i] = it;
+        }
+        const int64_t incl = block_scan(it.tiles, sums);
+        if (i < n) p.pre[i] = at_tile + incl - it.tiles;
+        __syncthreads();
+        if (threadIdx.x == kPlanThreads - 1) at_tile += incl;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        p.pre[n] = at_tile;
+        *p.n_items = n;
+    }
+}
+
+// A CTA's run of key tiles, item by item.  Every role walks it by itself.
+struct Segment {
+    Item it;
+    Seq s;
+    int g, from, to;        // KV head; tiles [from, to) of the item, counted from its last keys to its first
+};
+
+struct Walk {
+    int64_t u, u_end, per_head;
+    int n, i, g;
+
+    __device__ __forceinline__ Walk(const TcArgs& p, int c) {
+        n = *p.n_items;
+        per_head = p.pre[n];
+        const int64_t U = per_head * p.a.cache.H_kv;
+        u = c * U / p.P;
+        u_end = (c + 1) * U / p.P;
+        if (u < u_end) {
+            g = (int)(u / per_head);
+            i = find(p, u - g * per_head);
+        }
+    }
+    // the item that holds tile r of a head
+    __device__ __forceinline__ int find(const TcArgs& p, int64_t r) const {
+        int lo = 0, hi = n - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.pre[mid] <= r) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    }
+    __device__ __forceinline__ bool next(const TcArgs& p, Segment& o) {
+        if (u >= u_end) return false;
+        o.it = p.items[i];
+        o.s = load_seq(p.a.batch, p.a.cache.page, o.it.b);
+        o.g = g;
+        o.from = (int)(u - g * per_head - p.pre[i]);
+        o.to = (int)min((int64_t)o.it.tiles, o.from + (u_end - u));
+        u += o.to - o.from;
+        if (o.to == o.it.tiles && ++i == n) i = 0, ++g;
+        return true;
+    }
+};
+
+__device__ __forceinline__ int tile_of(const Segment& s, int x) { return s.it.lo + s.it.tiles - 1 - x; }
+__device__ __forceinline__ bool two_tiles(const TcArgs& p, const Segment& s) { return s.it.t0 + p.tpt < s.s.n; }
+
+// Whether the tile of keys from `base` holds slots without a token of the
+// sequence, or with one that no row of the sequence sees.
+__device__ __forceinline__ bool ragged(const TcArgs& p, const Segment& s, int base) {
+    return base + kKeys > s.s.kv || base < first_seen(s.s, p.a.window);
+}
+
+constexpr uint32_t instr_desc(int n, bool b_mn) {
+    return (1u << 4)                                // fp32 accumulator
+           | (1u << 7) | (1u << 10)                 // bf16 operands
+           | (b_mn ? 1u << 16 : 0u)                 // B stored with its N index contiguous (V), or its K index (K)
+           | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+// V's tile as operand B: [64-entry column blocks][128 keys][64 entries], 128-byte swizzle, N contiguous:
+// column blocks are 128 rows apart, groups of 8 keys 1024 bytes.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
+    uint64_t d = smem_desc(saddr);
+    d &= ~((uint64_t)0x3FFFu << 16);
+    return d | (uint64_t)((kKeys * 128) >> 4) << 16;
+}
+
+// mbar_wait in line: a call would cost the roles registers that their shares do not have.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, WsHeader* hdr, int where) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try_wait_suspend(bar, parity, 1000u)) {
+        if (*abort_flag) return false;
+        if (global_ns() - t0 > kTimeoutNs) {
+            record_error(hdr, SP_ETIMEOUT, where);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// For a warp whose lanes go on together.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, WsHeader* hdr, int where) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, hdr, where));
+}
+
+// A from TMEM.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+#define TMEM_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
+#define TMEM_W8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
+
+// 32 columns of this thread's TMEM lane; the registers may be used after tmem_wait32 (16).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : TMEM_R8(r, 0), TMEM_R8(r, 8), TMEM_R8(r, 16), TMEM_R8(r, 24)
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : TMEM_R8(r, 0), TMEM_R8(r, 8)
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+        ::TMEM_W8(r, 0), TMEM_W8(r, 8), "r"(taddr)
+        : "memory");
+}
+// Waits for this thread's TMEM loads; taking the registers as operands keeps their uses below it.
+__device__ __forceinline__ void tmem_wait32(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+__device__ __forceinline__ void tmem_wait16(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// (a, b) * (x, x) + (y, y), two fp32 at once
+__device__ __forceinline__ void fma2(float& a, float& b, float x, float y) {
+    asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %2};\n\tmov.b64 w, {%3, %3};\n\t"
+        "fma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
+    asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\t"
+        "add.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+
+template <int D>
+struct Layout {
+    static constexpr int kChunks = D / 64;                      // 128-byte column blocks of a row
+    static constexpr int kTileBytes = kKeys * D * 2;            // a tile of Q, K or V
+    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr int kQ = 0, kRing = 2 * kTileBytes, kBars = kRing + kStages * kTileBytes;
+    // TMEM columns
+    static constexpr int kS(int w) { return w * 128; }
+    static constexpr int kO(int w) { return 256 + w * D; }
+};
+
+template <int D, int kKind>
+__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_constant__ Maps maps,
+                                                                const __grid_constant__ TcArgs p) {
+    using L = Layout<D>;
+    constexpr bool kSame = kKind == SP_CACHE_SAME;
+    constexpr int NS = L::kStages;
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+    uint64_t* full = bars;                  // [NS] a K or V tile is ready
+    uint64_t* empty = full + NS;            // [NS] the MMAs have read it
+    uint64_t* landed = empty + NS;          // [NS] a V tile has arrived and waits to be cleaned
+    uint64_t* q_full = landed + NS;
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* s_full = q_empty + 1;         // [2] S is in TMEM (and all earlier P V done)
+    uint64_t* p_full = s_full + 2;          // [2] P is in TMEM, O is scaled
+    uint64_t* o_full = p_full + 2;          // [2] O is final
+    uint64_t* final_bar = o_full + 2;
+    volatile uint32_t* tmem_sh = reinterpret_cast<volatile uint32_t*>(final_bar + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_sh + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(smem_u32(&full[i]), kSame ? 1 : 4);
+            mbar_init(smem_u32(&empty[i]), 1);
+            mbar_init(smem_u32(&landed[i]), 1);
+        }
+        mbar_init(smem_u32(q_full), 1);
+        mbar_init(smem_u32(q_empty), 1);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(smem_u32(&s_full[w]), 1);
+            mbar_init(smem_u32(&p_full[w]), 4);
+            mbar_init(smem_u32(&o_full[w]), 1);
+        }
+        mbar_init(smem_u32(final_bar), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32((const void*)tmem_sh)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_sh;
+    cudaGridDependencySynchronize();        // the plan
+    cudaTriggerProgrammaticLaunchCompletion();
+    Walk walk(p, blockIdx.x);
+    Segment sg;
+    const int rows_tile = p.G * p.tpt;
+
+    if (warp < 8) {
+        // ------------------------------ softmax and output ------------------------------
+        // 512 threads are launched with 128 registers each: 256 * 192 + 128 * (64 + 64 or 80 + 48) is all of them
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        const int w = warp >> 2, row = (warp & 3) * 32 + lane;          // row tile; row = TMEM lane
+        const uint32_t lane_at = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + lane_at + L::kS(w), o_at = tmem + lane_at + L::kO(w);
+        const int t_row = row / p.G, h_row = row - t_row * p.G;
+        const float f = p.a.scale * 1.4426950408889634f;
+        uint32_t ph = 0, ph_o = 0;
+        bool ok = true;
+        while (ok && walk.next(p, sg)) {
+            if (w == 1 && !two_tiles(p, sg)) continue;
+            const int t = sg.it.t0 + w * p.tpt + t_row;                  // this row's new token
+            const bool real = row < rows_tile && t < sg.s.n;
+            const int pos = real ? sg.s.kv - sg.s.n + t : -1;
+            // places of the tile's first and last rows, for whether a key tile needs a mask at all
+            const int p_first = sg.s.kv - sg.s.n + sg.it.t0 + w * p.tpt;
+            const int p_last = sg.s.kv - sg.s.n + min(sg.s.n, sg.it.t0 + (w + 1) * p.tpt) - 1;
+            float m = -INFINITY, z = 0.f;
+            for (int x = sg.from; x < sg.to; ++x) {
+                const int base = tile_of(sg, x) * kKeys;
+                ok = wait_warp(smem_u32(&s_full[w]), ph, abort_flag, p.hdr, 21);
+                ph ^= 1;
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t sr[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, sr + 32 * c);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_wait32(sr + 32 * c);
+                float* sv = reinterpret_cast<float*>(sr);
+                if (base + kKeys - 1 > p_first || (p.a.window && base <= p_last - p.a.window)) {
+                    const int hi = pos - base, lo = p.a.window ? hi - p.a.window + 1 : -1;      // columns this row sees
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        if (i > hi || i < lo) sv[i] = -INFINITY;
+                }
+                float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+                for (int i = 4; i < 124; i += 8)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) mx[c] = fmax3(mx[c], sv[i + 2 * c], sv[i + 2 * c + 1]);
+                mx[0] = fmax3(mx[0], sv[124], sv[125]);
+                mx[1] = fmax3(mx[1], sv[126], sv[127]);
+                const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * f;
+                // f > 0, so the largest logit is f times the largest product
+                const bool grows = m != -INFINITY && top > m + 8.f;
+                if (__any_sync(0xffffffffu, grows)) {
+                    const float a = grows ? ex2_approx(m - top) : 1.f;
+                    if (grows) m = top;
+                    z *= a;
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t ov[16];
+                        tmem_ld16(o_at + 16 * c, ov);
+                        tmem_wait16(ov);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * a);
+                        tmem_st16(o_at + 16 * c, ov);
+                    }
+                }
+                if (m == -INFINITY) m = top;            // nothing summed so far
+                const float nm = m == -INFINITY ? 0.f : -m;
+                float zs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float a = sv[32 * c + i], b = sv[32 * c + i + 1];
+                        fma2(a, b, f, nm);
+                        a = ex2_approx(a);
+                        b = ex2_approx(b);
+                        add2(zs[(i & 2)], zs[(i & 2) + 1], a, b);
+                        pk[i >> 1] = pack_bf16(a, b);
+                    }
+                    tmem_st16(s_at + 16 * c, pk);
+                }
+                z += (zs[0] + zs[1]) + (zs[2] + zs[3]);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&p_full[w]));
+            }
+            if (!ok) break;
+            ok = wait_warp(smem_u32(&o_full[w]), ph_o, abort_flag, p.hdr, 22);
+            ph_o ^= 1;
+            if (!ok) break;
+            tc_fence_after();
+            const bool whole = sg.from == 0 && sg.to == sg.it.tiles;
+            const float inv = z == 0.f ? 0.f : 1.f / z;
+            const int64_t r = sg.s.row0 + t;
+            const int h = sg.g * p.G + h_row;
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.a.out.data) + r * p.a.out.stride_row + h * p.a.out.stride_head;
+            const int64_t slot = (int64_t)blockIdx.x * 2 + (sg.from == 0 ? 1 : 0);
+            float* po = p.part_o + slot * kRowsItem * D + (w * 128 + row) * 4;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t ov[32];
+                tmem_ld32(o_at + 32 * c, ov);
+                tmem_wait32(ov);
+                if (whole) {
+                    if (real) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            float v[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) v[k] = z == 0.f ? 0.f : __uint_as_float(ov[i + k]) * inv;
+                            store8(dst + 32 * c + i, v);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<uint4*>(po + (int64_t)(8 * c + i / 4) * (kRowsItem * 4)) =
+                            make_uint4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
+                }
+            }
+            if (whole) {
+                if (real && p.a.lse)
+                    p.a.lse[r * p.a.lse_stride_row + h * p.a.lse_stride_head] =
+                        z == 0.f ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
+            } else {
+                p.part_ml[slot * kRowsItem + w * 128 + row] = make_float2(m, z);
+            }
+            tc_fence_before();          // O is read before this thread's next hand-off of P
+        }
+    } else if (warp < 12) {
+        // ------------------------------ conversion of 8-bit rows ------------------------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSame ? 64 : 80));
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSame ? 64 : 48));
+        if (warp == 12) {
+            // ------------------------------ MMAs ------------------------------
+            if (lane == 0) {
+                constexpr uint32_t kIdS = instr_desc(kKeys, false), kIdO = instr_desc(D, true);
+                const uint32_t ring = smem_u32(smem + L::kRing), qs = smem_u32(smem + L::kQ);
+                int st = 0;
+                uint32_t ph = 0, ph_q = 0, ph_p = 0;
+                bool ok = true;
+                auto step = [&](int& s, uint32_t& h) {
+                    if (++s == NS) s = 0, h ^= 1;
+                };
+                auto s_mma = [&](int w, int stage) {
+                    const uint64_t a = smem_desc(qs + w * L::kTileBytes), b = smem_desc(ring + stage * L::kTileBytes);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t off = (uint64_t)(((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4);
+                        tc_mma(tmem + L::kS(w), a + off, b + off, kIdS, k > 0);
+                    }
+                    tc_commit(smem_u32(&s_full[w]));
+                };
+                while (ok && walk.next(p, sg)) {
+                    const int nw = two_tiles(p, sg) ? 2 : 1, nt = sg.to - sg.from;
+                    ok = wait_bar(smem_u32(q_full), ph_q, abort_flag, p.hdr, 31);
+                    ph_q ^= 1;
+                    ok = ok && wait_bar(smem_u32(&full[st]), ph, abort_flag, p.hdr, 32);
+                    if (!ok) break;
+                    tc_fence_after();
+                    for (int w = 0; w < nw; ++w) s_mma(w, st);
+                    tc_commit(smem_u32(&empty[st]));
+                    if (nt == 1) tc_commit(smem_u32(q_empty));
+                    step(st, ph);
+                    for (int i = 0; i < nt && ok; ++i) {
+                        const int sv = st;              // V of tile i, then K of tile i + 1
+                        ok = wait_bar(smem_u32(&full[sv]), ph, abort_flag, p.hdr, 33);
+                        if (!ok) break;
+                        step(st, ph);
+                        for (int w = 0; w < nw; ++w) {
+                            ok = wait_bar(smem_u32(&p_full[w]), (ph_p >> w) & 1, abort_flag, p.hdr, 34);
+                            ph_p ^= 1u << w;
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t b = smem_desc_mn(ring + sv * L::kTileBytes);
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                tc_mma_ts(tmem + L::kO(w), tmem + L::kS(w) + k * 8, b + (uint64_t)((k * 16 * 128) >> 4), kIdO,
+                                          i > 0 || k > 0);
+                            if (i + 1 == nt) {
+                                tc_commit(smem_u32(&o_full[w]));
+                            } else {
+                                if (w == 0) {
+                                    ok = wait_bar(smem_u32(&full[st]), ph, abort_flag, p.hdr, 35);
+                                    if (!ok) break;
+                                    tc_fence_after();
+                                }
+                                s_mma(w, st);
+                            }
+                        }
+                        if (!ok) break;
+                        tc_commit(smem_u32(&empty[sv]));
+                        if (i + 1 < nt) {
+                            tc_commit(smem_u32(&empty[st]));
+                            if (i + 2 == nt) tc_commit(smem_u32(q_empty));
+                            step(st, ph);
+                        }
+                    }
+                }
+                // nothing of this CTA's MMAs is in flight when TMEM is freed
+                tc_commit(smem_u32(final_bar));
+                const unsigned long long t0 = global_ns();
+                while (!mbar_try_wait_suspend(smem_u32(final_bar), 0, 1000u))
+                    if (global_ns() - t0 > kTimeoutNs) {
+                        record_error(p.hdr, SP_ETIMEOUT, 36);
+                        break;
+                    }
+            }
+            __syncwarp();
+        } else if (warp == 13) {
+            // ------------------------------ TMA ------------------------------
+            const uint32_t ring = smem_u32(smem + L::kRing), qs = smem_u32(smem + L::kQ);
+            const sp_cache& c = p.a.cache;
+            int st = 0, loads = 0;
+            uint32_t ph = 1, ph_q = 1;          // a fresh barrier counts as completed for the odd parity
+            uint32_t dirty = 0;                 // stages whose last load went to `landed`
+            bool ok = true;
+            const int boxes = kKeys / p.box;
+            while (ok && walk.next(p, sg)) {
+                const int nw = two_tiles(p, sg) ? 2 : 1;
+                const int32_t* table = p.a.batch.table + (int64_t)sg.it.b * p.a.batch.table_stride;
+                const int seen = first_seen(sg.s, p.a.window);
+                ok = wait_warp(smem_u32(q_empty), ph_q, abort_flag, p.hdr, 41);
+                ph_q ^= 1;
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_expect_tx(smem_u32(q_full), (uint32_t)(nw * rows_tile * D * 2));
+                    for (int w = 0; w < nw; ++w)
+                        for (int ch = 0; ch < L::kChunks; ++ch)
+                            tma_load_3d(qs + w * L::kTileBytes + ch * (kKeys * 128), &maps.q, ch * 64, sg.g * p.G,
+                                        (int)(sg.s.row0 + sg.it.t0 + w * p.tpt), smem_u32(q_full));
+                }
+                if constexpr (!kSame) continue;
+                // this lane's box of a tile: its page (pages: none, which loads zeros) and its first slot
+                auto page_of = [&](int x, int& slot) {
+                    const int tok = tile_of(sg, x) * kKeys + lane * p.box;
+                    slot = 0;
+                    if (lane >= boxes || tok >= sg.s.kv || tok + p.box <= seen) return (int)c.pages;
+                    const int q = (int)((unsigned)tok / (unsigned)c.page), pg = table[q];
+                    if (pg < 0 || pg >= c.pages) {
+                        record_error(p.hdr, SP_EDEVICE, 2);
+                        return (int)c.pages;
+                    }
+                    slot = tok - q * c.page;
+                    return pg;
+                };
+                int slot, pg = page_of(sg.from, slot);
+                for (int x = sg.from; x < sg.to && ok; ++x) {
+                    int slot2 = 0, pg2 = 0;
+                    if (x + 1 < sg.to) pg2 = page_of(x + 1, slot2);
+                    const bool clean = !ragged(p, sg, tile_of(sg, x) * kKeys);
+                    for (int v = 0; v < 2; ++v) {
+                        ok = wait_warp(smem_u32(&empty[st]), ph, abort_flag, p.hdr, 42);
+                        if (!ok) break;
+                        const bool wash = v == 1 && !clean;
+                        const uint32_t bar = smem_u32(wash ? &landed[st] : &full[st]);
+                        if (lane == 0) mbar_expect_tx(bar, L::kTileBytes);
+                        __syncwarp();
+                        if (lane < boxes)
+#pragma unroll
+                            for (int ch = 0; ch < L::kChunks; ++ch)
+                                tma_load_4d(ring + st * L::kTileBytes + ch * (kKeys * 128) + lane * p.box * 128,
+                                            v ? &maps.v : &maps.k, ch * 64, slot, sg.g, pg, bar);
+                        if (wash) dirty |= 1u << st;
+                        else dirty &= ~(1u << st);
+                        ++loads;
+                        if (++st == NS) st = 0, ph ^= 1;
+                    }
+                    pg = pg2;
+                    slot = slot2;
+                }
+            }
+            (void)dirty; (void)loads;
+            // an aborted CTA's copies land before it leaves
+            if (kSame && lane == 0 && *abort_flag) {
+                const unsigned long long t0 = global_ns();
+                for (int k = 1; k <= min(loads, NS); ++k) {
+                    const int s1 = (st - k + NS) % NS;
+                    const uint32_t parity = (uint32_t)(((loads - k) / NS) & 1);
+                    // a load that waits to be cleaned is followed on a barrier of its own, whose phase is not known here
+                    if (dirty >> s1 & 1) {
+                        const unsigned long long t1 = global_ns();
+                        while (global_ns() - t1 < 1000000ull) {}
+                        continue;
+                    }
+                    while (!mbar_try_wait_suspend(smem_u32(&full[s1]), parity, 1000u) && global_ns() - t0 < kTimeoutNs) {}
+                }
+            }
+            __syncwarp();
+        } else if (warp == 14 && kSame) {
+            // ------------------------------ cleaning of V ------------------------------
+            int st = 0;
+            uint32_t ph = 0;                    // per stage
+            bool ok = true;
+            while (ok && walk.next(p, sg)) {
+                const int seen = first_seen(sg.s, p.a.window);
+                for (int x = sg.from; x < sg.to && ok; ++x) {
+                    const int base = tile_of(sg, x) * kKeys, sv = st + 1 == NS ? 0 : st + 1;
+                    st = sv + 1 == NS ? 0 : sv + 1;
+                    if (!ragged(p, sg, base)) continue;
+                    ok = wait_warp(smem_u32(&landed[sv]), (ph >> sv) & 1, abort_flag, p.hdr, 51);
+                    ph ^= 1u << sv;
+                    if (!ok) break;
+                    uint8_t* tile = smem + L::kRing + sv * L::kTileBytes;
+                    // a row is 128 bytes in each column block, wherever the swizzle puts its pieces
+                    for (int i = lane; i < kKeys * L::kChunks * 8; i += 32) {
+                        const int rr = i >> 3, tok = base + (rr & (kKeys - 1));
+                        if (tok >= sg.s.kv || tok < seen) *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&full[sv]));
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+// Adds up the parts of the items that were cut: block (c, y) takes the item
+// whose first cut is the one before CTA c, and 16 of its columns; a thread one row.
+template <int D>
+__global__ void __launch_bounds__(kRowsItem) tc_join_kernel(const __grid_constant__ TcArgs p) {
+    cudaGridDependencySynchronize();
+    const int c = blockIdx.x + 1, row = threadIdx.x;
+    const int n = *p.n_items;
+    const int64_t per_head = p.pre[n], U = per_head * p.a.cache.H_kv;
+    const int64_t u = c * U / p.P;
+    if (U == 0 || u >= U) return;
+    const int g = (int)(u / per_head);
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.pre[mid] <= u - g * per_head) lo = mid;
+        else hi = mid - 1;
+    }
+    const int64_t begin = g * per_head + p.pre[lo];
+    if (u == begin || (c - 1) * U / p.P > begin || (c - 1) * U / p.P == u) return;
+    const Item it = p.items[lo];
+    const Seq s = load_seq(p.a.batch, p.a.cache.page, it.b);
+    const int64_t end = begin + it.tiles;
+    const int w = row >> 7, r = row & 127, t_row = r / p.G, t = it.t0 + w * p.tpt + t_row;
+    if (r >= p.G * p.tpt || t >= s.n) return;
+    float m = -INFINITY;
+    for (int k = c - 1; k < p.P && k * U / p.P < end; ++k) {
+        if (k * U / p.P == (k + 1) * U / p.P) continue;
+        m = fmaxf(m, p.part_ml[((int64_t)k * 2 + (k == c - 1 ? 1 : 0)) * kRowsItem + row].x);
+    }
+    float z = 0.f, v[16] = {};
+    for (int k = c - 1; k < p.P && k * U / p.P < end; ++k) {
+        if (k * U / p.P == (k + 1) * U / p.P) continue;
+        const int64_t slot = (int64_t)k * 2 + (k == c - 1 ? 1 : 0);
+        const float2 ml = p.part_ml[slot * kRowsItem + row];
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;
+        const float a = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);
+        z += ml.y * a;
+        const float4* src = reinterpret_cast<const float4*>(p.part_o) + (slot * (D / 4) + blockIdx.y * 4) * kRowsItem + row;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 o = src[i * kRowsItem];
+            v[4 * i] += o.x * a; v[4 * i + 1] += o.y * a; v[4 * i + 2] += o.z * a; v[4 * i + 3] += o.w * a;
+        }
+    }
+    const float inv = z == 0.f ? 0.f : 1.f / z;
+    const int h = g * p.G + r - t_row * p.G;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.a.out.data) + (s.row0 + t) * p.a.out.stride_row +
+                         h * p.a.out.stride_head + blockIdx.y * 16;
+    float o0[8], o1[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        o0[i] = z == 0.f ? 0.f : v[i] * inv;
+        o1[i] = z == 0.f ? 0.f : v[8 + i] * inv;
+    }
+    store8(dst, o0);
+    store8(dst + 8, o1);
+    if (p.a.lse && blockIdx.y == 0)
+        p.a.lse[(s.row0 + t) * p.a.lse_stride_row + h * p.a.lse_stride_head] =
+            z == 0.f ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
+}
+
+struct Space {
+    size_t n_items, items, pre, part_o, part_ml, total;
+};
+
+int max_items(const sp_batch& b, int tpt) {
+    return (int)std::min<int64_t>((int64_t)b.B + b.T / (2 * tpt), INT32_MAX / 2);
+}
+
+Space carve(const sp_batch& b, int d, int tpt, int P) {
+    Space s;
+    Carve c;
+    const size_t n = (size_t)max_items(b, tpt);
+    s.n_items = c.take(sizeof(int));
+    s.items = c.take(n * sizeof(Item));
+    s.pre = c.take((n + 1) * sizeof(int64_t));
+    s.part_o = c.take((size_t)P * 2 * kRowsItem * d * sizeof(float));
+    s.part_ml = c.take((size_t)P * 2 * kRowsItem * sizeof(float2));
+    s.total = c.off;
+    return s;
+}
+
+// A tensor map of bf16 rows; strides in entries.  An extent of 1 has no stride of its own.
+sp_status encode(CUtensorMap* map, const void* data, int rank, const int64_t* extent, const int64_t* stride, const int* box) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    if (!enc) {
+        set_error("sp_attend: cuTensorMapEncodeTiled is unavailable from the driver");
+        return SP_ECUDA;
+    }
+    cuuint64_t dim[4], step[3];
+    cuuint32_t bx[4], one[4] = {1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        dim[i] = (cuuint64_t)extent[i];
+        bx[i] = (cuuint32_t)box[i];
+        if (i) step[i - 1] = extent[i] == 1 ? 16 : (cuuint64_t)stride[i] * 2;
+    }
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(data), dim, step, bx, one,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        set_error("sp_attend: cuTensorMapEncodeTiled failed (%d)", (int)r);
+        return SP_ECUDA;
+    }
+    return SP_OK;
+}
+
+// Launch that may begin while the kernel before it ends (the kernel waits for that by itself).
+template <typename... A>
+sp_status launch_early(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    SP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, args...));
+    SP_LAUNCH_CHECK();
+    return SP_OK;
+}
+
+template <int D, int kKind>
+sp_status launch(const Maps& maps, const TcArgs& p, cudaStream_t st) {
+    SP_CUDA_TRY(cudaFuncSetAttribute(attend_tc_kernel<D, kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+    plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
+    SP_LAUNCH_CHECK();
+    sp_status s = launch_early(attend_tc_kernel<D, kKind>, dim3((unsigned)p.P), kThreads, (size_t)kSmem, st, maps, p);
+    if (s != SP_OK || p.P == 1) return s;
+    return launch_early(tc_join_kernel<D>, dim3((unsigned)p.P - 1, D / 16), kRowsItem, (size_t)0, st, p);
+}
+
+}  // namespace
+
+// Whether the cache and the group of heads are within the kernel's layouts.
+bool attend_tc_supported(const sp_cache& c, int G) {
+    if (c.dtype != SP_BF16 || (c.d != 64 && c.d != 128) || G > 128 || c.kind != SP_CACHE_SAME) return false;
+    if (c.page % 8 != 0) return false;                                  // boxes of 8 rows at least
+    const int64_t limit = (int64_t)1 << 39;                             // tensor-map strides are below 2^40 bytes
+    if (c.stride_slot >= limit / 2 || c.stride_head >= limit / 2 || c.stride_page >= limit / 2) return false;
+    return !(c.H_kv > 1 && c.stride_head == 0) && !(c.pages > 1 && c.stride_page == 0);
+}
+
+size_t attend_tc_ws_bytes(const sp_cache& c, const sp_batch& b, int G) {
+    return carve(b, c.d, 128 / G, sm_count()).total;
+}
+
+// min_rows: sequences of at most that many rows per KV head have been taken by another kernel
+sp_status attend_tc_launch(const AttendProblem& a, int min_rows, void* ws, cudaStream_t st) {
+    TcArgs p;
+    p.a = a;
+    p.G = a.H / a.cache.H_kv;
+    p.tpt = 128 / p.G;
+    p.min_rows = min_rows;
+    p.P = sm_count();
+    p.box = std::min(128, a.cache.page & -a.cache.page);
+    p.clear = min_rows == 0;
+    p.max_items = max_items(a.batch, p.tpt);
+    char* base = static_cast<char*>(ws);
+    const Space s = carve(a.batch, a.cache.d, p.tpt, p.P);
+    p.hdr = reinterpret_cast<WsHeader*>(base);
+    p.n_items = reinterpret_cast<int*>(base + s.n_items);
+    p.items = reinterpret_cast<Item*>(base + s.items);
+    p.pre = reinterpret_cast<int64_t*>(base + s.pre);
+    p.part_o = reinterpret_cast<float*>(base + s.part_o);
+    p.part_ml = reinterpret_cast<float2*>(base + s.part_ml);
+    Maps maps;
+    const int64_t q_ext[3] = {a.cache.d, a.H, std::max<int64_t>(a.batch.T, 1)}, q_str[3] = {1, a.q.stride_head, a.q.stride_row};
+    const int q_box[3] = {64, p.G, p.tpt};
+    const int64_t c_ext[4] = {a.cache.d, a.cache.page, a.cache.H_kv, a.cache.pages};
+    const int64_t c_str[4] = {1, a.cache.stride_slot, a.cache.stride_head, a.cache.stride_page};
+    const int c_box[4] = {64, p.box, 1, 1};
+    sp_status e;
+    if ((e = encode(&maps.q, a.q.data, 3, q_ext, q_str, q_box)) != SP_OK ||
+        (e = encode(&maps.k, a.cache.k, 4, c_ext, c_str, c_box)) != SP_OK ||
+        (e = encode(&maps.v, a.cache.v, 4, c_ext, c_str, c_box)) != SP_OK)
+        return e;
+    return a.cache.d == 64 ? launch<64, SP_CACHE_SAME>(maps, p, st) : launch<128, SP_CACHE_SAME>(maps, p, st);
+}
+
+}  // namespace sp

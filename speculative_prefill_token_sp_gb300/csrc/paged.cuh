@@ -188,6 +188,9 @@ __device__ __forceinline__ void check_batch(const sp_batch& b, const sp_cache& c
 sp_status check_cache(const char* fn, const sp_cache* c);
 sp_status check_batch_args(const char* fn, const sp_batch* b);
 
+// SMs of the current device (defined in abi_paged.cu).
+int sm_count();
+
 struct AttendProblem {
     sp_rows q, out;
     sp_cache cache;
