@@ -394,7 +394,7 @@ typedef enum { SP_CACHE_SAME = 0, SP_CACHE_E4M3 = 1, SP_CACHE_INT8 = 2 } sp_cach
 typedef struct {
     void*         k;
     void*         v;
-    float*        k_scale;     /* 8-bit kinds: [pages, H_kv, page], contiguous; else NULL */
+    float*        k_scale;     /* 8-bit kinds: [pages, H_kv, page], contiguous, powers of two or NaN; else NULL */
     float*        v_scale;
     int64_t       stride_page, stride_head, stride_slot;
     int64_t       pages;

@@ -33,6 +33,8 @@
 #include "paged.cuh"
 #include "tc_ptx.cuh"
 
+#include <string.h>
+
 #include <algorithm>
 
 namespace sp {
@@ -304,6 +306,12 @@ __device__ __forceinline__ void tmem_wait16(uint32_t* r) {
     for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // (a, b) * (x, x) + (y, y), two fp32 at once
 __device__ __forceinline__ void fma2(float& a, float& b, float x, float y) {
     asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %2};\n\tmov.b64 w, {%3, %3};\n\t"
@@ -512,7 +520,97 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         }
     } else if (warp < 12) {
         // ------------------------------ conversion of 8-bit rows ------------------------------
+        // A warp takes 32 rows of each tile; a lane 16 entries of a row, so that a row's lanes read it whole.  A
+        // piece is requested for the next tile as soon as it is converted for this one.
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSame ? 64 : 80));
+        if constexpr (!kSame) {
+            constexpr int kLanes = D / 16, kPass = kLanes;              // lanes of a row; rows of a warp / rows at a time
+            const sp_cache& c = p.a.cache;
+            const int r0 = (warp - 8) * 32, lp = lane % kLanes, rl = lane / kLanes;
+            const uint32_t swap = D == 128 ? (lp >> 2) & 1 : 0;        // the two column blocks' stores take other banks
+            int st = 0;
+            uint32_t ph = 1;
+            bool ok = true;
+            while (ok && walk.next(p, sg)) {
+                const int32_t* table = p.a.batch.table + (int64_t)sg.it.b * p.a.batch.table_stride;
+                const int seen = first_seen(sg.s, p.a.window);
+                // this lane's row of a tile: where it is (-1: nowhere) and its scales as pairs of bf16
+                struct Where {
+                    int64_t at;
+                    uint32_t ks, vs;
+                };
+                auto page_of = [&](int x) {
+                    const int tok = tile_of(sg, x) * kKeys + r0 + lane;
+                    return tok < sg.s.kv && tok >= seen ? table[(unsigned)tok / (unsigned)c.page] : -1;
+                };
+                auto place = [&](int x, int pg) {
+                    Where w{-1, 0x3f803f80u, 0x3f803f80u};
+                    const int tok = tile_of(sg, x) * kKeys + r0 + lane;
+                    if (tok >= sg.s.kv || tok < seen) return w;
+                    if ((unsigned)pg >= (unsigned)c.pages) {
+                        record_error(p.hdr, SP_EDEVICE, 2);
+                        return w;
+                    }
+                    const int slot = (int)((unsigned)tok % (unsigned)c.page);
+                    w.at = row_offset(c, pg, sg.g, slot);
+                    const int64_t sc = scale_offset(c, pg, sg.g, slot);
+                    // a power of two (or NaN) is its upper half
+                    w.ks = __byte_perm(__float_as_uint(__ldg(c.k_scale + sc)), 0, 0x3232);
+                    w.vs = __byte_perm(__float_as_uint(__ldg(c.v_scale + sc)), 0, 0x3232);
+                    return w;
+                };
+                auto fetch = [&](const void* data, int64_t at_lane, int ps) {
+                    const int64_t at = __shfl_sync(0xffffffffu, at_lane, ps * (32 / kLanes) + rl);
+                    return at >= 0 ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(data) + at + lp * 16))
+                                   : make_uint4(0, 0, 0, 0);
+                };
+                Where cur = place(sg.from, page_of(sg.from));
+                uint4 raw_codes[kPass];
+#pragma unroll
+                for (int ps = 0; ps < kPass; ++ps) raw_codes[ps] = fetch(c.k, cur.at, ps);
+                for (int x = sg.from; x < sg.to && ok; ++x) {
+                    const bool more = x + 1 < sg.to;
+                    const int next_page = more ? page_of(x + 1) : -1;
+                    Where nxt = cur;
+#pragma unroll 1
+                    for (int v = 0; v < 2; ++v) {
+                        if (v == 1) {
+                            if (more) nxt = place(x + 1, next_page);
+                            else nxt.at = -1;
+                        }
+                        ok = wait_warp(smem_u32(&empty[st]), ph, abort_flag, p.hdr, 61);
+                        if (!ok) break;
+                        uint8_t* tile = smem + L::kRing + st * L::kTileBytes;
+                        const uint32_t scale_lane = v ? cur.vs : cur.ks;
+                        const void* next_data = v ? c.k : c.v;
+                        const int64_t next_at = v ? nxt.at : cur.at;
+#pragma unroll
+                        for (int ps = 0; ps < kPass; ++ps) {
+                            const int rr = ps * (32 / kLanes) + rl, row = r0 + rr;
+                            const uint32_t scale = __shfl_sync(0xffffffffu, scale_lane, rr);
+                            const uint32_t w4[4] = {raw_codes[ps].x, raw_codes[ps].y, raw_codes[ps].z, raw_codes[ps].w};
+                            uint32_t o[8];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                o[2 * i] = mul_bf16x2(pair_of<kKind>(__byte_perm(w4[i], 0, 0x1404)), scale);
+                                o[2 * i + 1] = mul_bf16x2(pair_of<kKind>(__byte_perm(w4[i], 0, 0x3424)), scale);
+                            }
+                            raw_codes[ps] = fetch(next_data, next_at, ps);
+                            uint8_t* at = tile + (lp >> 2) * (kKeys * 128) + row * 128;
+                            const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
+                            const uint32_t p0 = (lp & 3) * 2;
+                            *reinterpret_cast<uint4*>(at + (((p0 + swap) ^ (row & 7)) << 4)) = swap ? b : a;
+                            *reinterpret_cast<uint4*>(at + (((p0 + 1 - swap) ^ (row & 7)) << 4)) = swap ? a : b;
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&full[st]));
+                        if (++st == NS) st = 0, ph ^= 1;
+                    }
+                    cur = nxt;
+                }
+            }
+        }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSame ? 64 : 48));
         if (warp == 12) {
@@ -839,11 +937,19 @@ sp_status launch(const Maps& maps, const TcArgs& p, cudaStream_t st) {
     return launch_early(tc_join_kernel<D>, dim3((unsigned)p.P - 1, D / 16), kRowsItem, (size_t)0, st, p);
 }
 
+template <int D>
+sp_status launch_codes(const Maps& maps, const TcArgs& p, cudaStream_t st) {
+    return p.a.cache.kind == SP_CACHE_E4M3 ? launch<D, SP_CACHE_E4M3>(maps, p, st) : launch<D, SP_CACHE_INT8>(maps, p, st);
+}
+
 }  // namespace
 
 // Whether the cache and the group of heads are within the kernel's layouts.
 bool attend_tc_supported(const sp_cache& c, int G) {
-    if (c.dtype != SP_BF16 || (c.d != 64 && c.d != 128) || G > 128 || c.kind != SP_CACHE_SAME) return false;
+    if (c.dtype != SP_BF16 || (c.d != 64 && c.d != 128) || G > 128) return false;
+    if (c.kind != SP_CACHE_SAME)                                        // rows of codes are read 16 bytes at a time
+        return (reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v) | (uintptr_t)c.stride_page |
+                (uintptr_t)c.stride_head | (uintptr_t)c.stride_slot) % 16 == 0;
     if (c.page % 8 != 0) return false;                                  // boxes of 8 rows at least
     const int64_t limit = (int64_t)1 << 39;                             // tensor-map strides are below 2^40 bytes
     if (c.stride_slot >= limit / 2 || c.stride_head >= limit / 2 || c.stride_page >= limit / 2) return false;
@@ -880,8 +986,11 @@ sp_status attend_tc_launch(const AttendProblem& a, int min_rows, void* ws, cudaS
     const int64_t c_str[4] = {1, a.cache.stride_slot, a.cache.stride_head, a.cache.stride_page};
     const int c_box[4] = {64, p.box, 1, 1};
     sp_status e;
-    if ((e = encode(&maps.q, a.q.data, 3, q_ext, q_str, q_box)) != SP_OK ||
-        (e = encode(&maps.k, a.cache.k, 4, c_ext, c_str, c_box)) != SP_OK ||
+    memset(&maps, 0, sizeof(maps));
+    if ((e = encode(&maps.q, a.q.data, 3, q_ext, q_str, q_box)) != SP_OK) return e;
+    if (a.cache.kind != SP_CACHE_SAME)
+        return a.cache.d == 64 ? launch_codes<64>(maps, p, st) : launch_codes<128>(maps, p, st);
+    if ((e = encode(&maps.k, a.cache.k, 4, c_ext, c_str, c_box)) != SP_OK ||
         (e = encode(&maps.v, a.cache.v, 4, c_ext, c_str, c_box)) != SP_OK)
         return e;
     return a.cache.d == 64 ? launch<64, SP_CACHE_SAME>(maps, p, st) : launch<128, SP_CACHE_SAME>(maps, p, st);

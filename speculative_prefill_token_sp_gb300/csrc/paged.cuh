@@ -116,6 +116,24 @@ __device__ __forceinline__ void decode8(uint2 u, float (&x)[8]) {
     }
 }
 
+// Two 8-bit codes, in bits 8-15 and 24-31 of y (the other bits are ignored),
+// as a pair of bf16 (their values before the scale, exactly).
+template <int kKind>
+__device__ __forceinline__ uint32_t pair_of(uint32_t y) {
+    uint32_t r;
+    if (kKind == SP_CACHE_E4M3) {
+        // exponent and mantissa moved to bf16's place mean the value * 2^-120 (biases 7 and 127), also
+        // for e4m3's subnormals; the product with 2^120 is exact.  0x7f is NaN in e4m3, never written, and 480 here
+        const uint32_t b = ((y >> 4) & 0x07f007f0u) | (y & 0x80008000u);
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(0x7b807b80u));
+    } else {
+        // 0x4300 + (7 bits) is 128 + those bits; minus 128, or minus 256 (0x4380) where the sign bit is set
+        const uint32_t lo = ((y >> 8) & 0x007f007fu) | 0x43004300u, off = ((y >> 8) & 0x00800080u) | 0x43004300u;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(lo), "r"(off));
+    }
+    return r;
+}
+
 // The scale of a row whose largest magnitude is `top` (NaN or infinite if an
 // entry is): 2^k with the smallest k >= -100 such that top / 2^k is at most
 // the largest code.  448 = 0.875 * 2^9 and 127 = 0.9921875 * 2^7: with top = m
