@@ -462,10 +462,11 @@ size_t sp_attend_workspace_size(const sp_cache* cache, const sp_batch* batch, in
  * over the tokens i <= p of the row's sequence, p its own place, and i > p -
  * window if window > 0.  Query head h reads KV head h / (H / H_kv).  A row
  * that sees no token (p < 0) gets out = 0 and lse = -inf.  One call is a
- * prefill chunk, a decode step, or a mixture of them.  The lse of the
+ * prefill chunk, a decode step, or a mixture of them.  The same call gives the
+ * same bits; in another batch a sequence's sums may be added in another order.  The lse of the
  * look-ahead decode steps is what sp_score_lse takes.
  *
- *   q, out   [T, H, d] in the cache's dtype
+ *   q, out   [T, H, d] in the cache's dtype; out must not overlap q
  *   lse      fp32, lse[r * lse_stride_row + h * lse_stride_head], or NULL.  Step j of N
  *            look-ahead steps of one request (T = 1, layer l of sp_score_lse's lse [L, H, N]):
  *            pointer lse + l * H * N + j, lse_stride_head = N

@@ -594,35 +594,40 @@ def rotary_plan(rot, *, base=10000.0, inv_freq=None, sections=None, axis_of_pair
 
 def _rows(t, heads_first=False):
     """sp_rows of a tensor [rows, heads, d] (heads_first: [heads, rows, d]) whose last axis is contiguous."""
-    st = t.stride()
-    if st[2] != 1 and t.shape[2] > 1:
+    s0, s1, s2 = t.stride()
+    if s2 != 1:
         raise ValueError("the last axis must be contiguous")
-    return SpRows(t.data_ptr(), st[1], st[0]) if heads_first else SpRows(t.data_ptr(), st[0], st[1])
+    return SpRows(t.data_ptr(), s1, s0) if heads_first else SpRows(t.data_ptr(), s0, s1)
 
 
-class _On:
-    """For a call on `device` and `stream` (None: the current one): makes both current, where they are not, so that
-    what the call allocates belongs to the stream that uses it."""
+# The helpers below are called for every layer of every step, so their own time on the host counts: torch is looked
+# up once, and a call for the current device and stream (nearly all of them) enters no context.
+_torch = None
 
-    def __init__(self, device, stream):
-        import torch
-        self.guards = []
-        if device.type != "cuda":
-            raise ValueError(f"the tensors must be on a GPU (got {device})")
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
-            self.guards.append(torch.cuda.stream(stream))
 
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
 
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+
+def _on(device, stream, call):
+    """call(stream handle) with `device` and `stream` (None: its current one) current, so that what the call
+    allocates belongs to the stream that uses it."""
+    torch = _torch
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be on a GPU (got {device})")
+    index = device.index
+    if stream is None and index == torch._C._cuda_getDevice():
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
 def _same_device(device, *tensors):
@@ -631,38 +636,62 @@ def _same_device(device, *tensors):
             raise ValueError(f"tensors on different devices: {device} and {t.device}")
 
 
+def _space(nbytes, device, ws):
+    """(workspace, its bytes): the caller's, or a new one."""
+    if ws is None:
+        return _torch.empty(nbytes or 256, dtype=_torch.uint8, device=device), nbytes
+    if ws.device != device:
+        raise ValueError(f"the workspace is on {ws.device}, the tensors on {device}")
+    return ws, ws.numel() * ws.element_size()
+
+
 def rotary(q, k, positions, plan, *, inverse=False, q_out=None, k_out=None, stream=None):
     """Rotates q [T, H, d] and k [T, H_kv, d] (either may be None) at positions [T] or [axes, T] (int32) and returns
     (q_out, k_out).  q_out=q rotates in place.  inverse=True undoes the rotation (and is its gradient)."""
-    import torch
-    some = q if q is not None else k
+    torch = _torch or _load_torch()
+    some = k if q is None else q
     if some is None:
         raise ValueError("neither q nor k")
-    T, d = some.shape[0], some.shape[2]
-    dt = _dtype_code(some)
-    for t in (q, k):
-        if t is not None and (t.dim() != 3 or t.shape[0] != T or t.shape[2] != d or t.dtype != some.dtype):
-            raise ValueError("q and k must be [T, heads, d] of the same T, d and dtype")
-    if positions.dtype != torch.int32 or positions.shape[-1] != T or positions.dim() > 2:
-        raise ValueError("positions must be int32, [T] or [axes, T]")
-    if (positions.shape[0] if positions.dim() == 2 else 1) < plan.axes:
+    T, H, d = some.shape
+    H_kv, dtype, device, code = 0, some.dtype, some.device, _dtype_code(some)
+    if q is None:
+        H, H_kv = 0, H
+    elif k is not None:
+        T2, H_kv, d2 = k.shape
+        if T2 != T or d2 != d or k.dtype != dtype or k.device != device:
+            raise ValueError("q and k must be [T, heads, d] of the same T, d, dtype and device")
+    per_axis = positions.stride()
+    axes = positions.shape[0] if len(per_axis) == 2 else 1
+    if positions.dtype != torch.int32 or positions.shape[-1] != T or len(per_axis) > 2 or positions.device != device:
+        raise ValueError("positions must be int32, [T] or [axes, T], on the device of q and k")
+    if axes < plan.axes:
         raise ValueError(f"the plan has {plan.axes} axes: positions must be [{plan.axes}, T]")
-    if T and positions.stride(-1) != 1:
-        positions = positions.contiguous()
-    _same_device(some.device, q, k, positions, q_out, k_out)
     for t, o in ((q, q_out), (k, k_out)):
-        if t is not None and o is not None and (o.shape != t.shape or o.dtype != t.dtype):
-            raise ValueError("q_out and k_out must have the shape and dtype of q and k")
-    with _On(some.device, stream):
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        _check(sp_rotary(plan, positions, positions.stride(0) if positions.dim() == 2 else 0, T, d, dt, int(inverse),
-                         None if q is None else _rows(q), None if q is None else _rows(q_out),
-                         0 if q is None else q.shape[1], None if k is None else _rows(k),
-                         None if k is None else _rows(k_out), 0 if k is None else k.shape[1], stream))
-    return q_out if q is not None else None, k_out if k is not None else None
+        if o is not None and (t is None or o.shape != t.shape or o.dtype != dtype or o.device != device):
+            raise ValueError("q_out and k_out must have the shape, dtype and device of q and k")
+
+    def call(handle):
+        p, qo, ko = positions, q_out, k_out
+        if per_axis[-1] != 1 and T > 1:
+            p = p.contiguous()
+        qr = kr = qor = kor = None
+        if q is not None:
+            if qo is None:
+                qo = torch.empty((T, H, d), dtype=dtype, device=device)
+            qr, qor = _rows(q), _rows(qo)
+        if k is not None:
+            if ko is None:
+                ko = torch.empty((T, H_kv, d), dtype=dtype, device=device)
+            kr, kor = _rows(k), _rows(ko)
+        at = ctypes.addressof
+        status = lib().sp_rotary(at(plan), p.data_ptr(), p.stride(0) if len(per_axis) == 2 else 0, T, d, code,
+                                 1 if inverse else 0, qr and at(qr), qor and at(qor), H, kr and at(kr), kor and at(kor),
+                                 H_kv, handle)
+        if status:
+            _check(status)
+        return qo, ko
+
+    return _on(device, stream, call)
 
 
 class Cache:
@@ -671,7 +700,7 @@ class Cache:
     v_scale fp32 [pages, H_kv, page].  dtype: of the rows that are written and read (default: k's)."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None, *, dtype=None):
-        import torch
+        torch = _torch or _load_torch()
         kinds = {torch.float8_e4m3fn: SP_CACHE_E4M3, torch.int8: SP_CACHE_INT8}
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
             raise ValueError("k and v must be [pages, H_kv, page, d] of the same shape, dtype and strides")
@@ -692,10 +721,12 @@ class Cache:
             raise TypeError(f"unsupported dtype {dtype}")
         self.k, self.v, self.k_scale, self.v_scale, self.dtype, self.kind = k, v, k_scale, v_scale, dtype, kind
         self.device = k.device
+        self.ws_bytes = sp_cache_workspace_size()
         self.pages, self.H_kv, self.page, self.d = k.shape
         sp_, sh, ss, _ = k.stride()
         self.c = SpCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), sp_, sh, ss, self.pages, self.page,
                          self.H_kv, self.d, code, kind)
+        self.at = ctypes.addressof(self.c)
 
 
 def cache_alloc(pages, H_kv, page, d, *, dtype=None, kind="same", device="cuda"):
@@ -715,7 +746,7 @@ class Batch:
     sequence (default: rows)."""
 
     def __init__(self, cu_new, kv_len, table, *, rows, max_new=None):
-        import torch
+        torch = _torch or _load_torch()
         B = kv_len.shape[0]
         if cu_new.dtype != torch.int64 or kv_len.dtype != torch.int64 or table.dtype != torch.int32:
             raise TypeError("cu_new and kv_len must be int64, table int32")
@@ -729,73 +760,97 @@ class Batch:
         self.max_new = self.rows if max_new is None else int(max_new)
         self.c = SpBatch(B, self.max_new, self.rows, _ptr(cu_new), _ptr(kv_len), _ptr(table), table.shape[1],
                          table.stride(0) if B > 1 else 0)
+        self.at = ctypes.addressof(self.c)
 
 
 def _check_rows_of(t, name, rows, heads, d, dtype, device):
-    if tuple(t.shape) != (rows, heads, d) or t.dtype != dtype or t.device != device:
+    if t.shape != (rows, heads, d) or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be {dtype} [{rows}, {heads}, {d}] on {device}: "
                          f"got {t.dtype} {list(t.shape)} on {t.device}")
 
 
 def cache_write(cache, batch, k_new, v_new, *, ws=None, stream=None, check=False):
     """Writes the batch's new tokens, k_new and v_new [rows, H_kv, d], into the cache."""
-    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-        _check_rows_of(t, name, batch.rows, cache.H_kv, cache.d, cache.dtype, cache.device)
-    _same_device(cache.device, batch)
-    with _On(cache.device, stream):
-        ws = _workspace(sp_cache_workspace_size(), cache.device, ws)
-        _check(sp_cache_write(cache.c, batch.c, _rows(k_new), _rows(v_new), ws, ws.numel() * ws.element_size(), stream))
-        _check_device(ws, stream, check)
+    device = cache.device
+    _check_rows_of(k_new, "k_new", batch.rows, cache.H_kv, cache.d, cache.dtype, device)
+    _check_rows_of(v_new, "v_new", batch.rows, cache.H_kv, cache.d, cache.dtype, device)
+    _same_device(device, batch)
+
+    def call(handle):
+        w, size = _space(cache.ws_bytes, device, ws)
+        kr, vr = _rows(k_new), _rows(v_new)
+        status = lib().sp_cache_write(cache.at, batch.at, ctypes.addressof(kr), ctypes.addressof(vr), w.data_ptr(), size,
+                                      handle)
+        if status:
+            _check(status)
+        if check:
+            _check(sp_workspace_status(w, handle))
+
+    _on(device, stream, call)
 
 
 def cache_read(cache, batch, *, out_k=None, out_v=None, ws=None, stream=None, check=False):
     """Reads the batch's tokens back: (out_k, out_v) [H_kv, rows, d], a layer of score's K_prompt each.  Given
     outputs are written in place (any strides with the last axis contiguous), and one that is not given while the
     other is stays out.  With neither given both are made, and rows that are not a token of the batch are not set."""
-    import torch
+    device = cache.device
     for t, name in ((out_k, "out_k"), (out_v, "out_v")):
-        if t is not None and (tuple(t.shape) != (cache.H_kv, batch.rows, cache.d) or t.dtype != cache.dtype or
-                              t.device != cache.device):
-            raise ValueError(f"{name} must be {cache.dtype} [{cache.H_kv}, {batch.rows}, {cache.d}] on {cache.device}")
-    _same_device(cache.device, batch)
-    with _On(cache.device, stream):
-        if out_k is None and out_v is None:
-            out_k, out_v = (torch.empty(cache.H_kv, batch.rows, cache.d, dtype=cache.dtype, device=cache.device)
-                            for _ in range(2))
-        ws = _workspace(sp_cache_workspace_size(), cache.device, ws)
-        _check(sp_cache_read(cache.c, batch.c, None if out_k is None else _rows(out_k, True),
-                             None if out_v is None else _rows(out_v, True), ws, ws.numel() * ws.element_size(),
-                             stream))
-        _check_device(ws, stream, check)
-    return out_k, out_v
+        if t is not None:
+            _check_rows_of(t, name, cache.H_kv, batch.rows, cache.d, cache.dtype, device)
+    _same_device(device, batch)
+
+    def call(handle):
+        k, v = out_k, out_v
+        if k is None and v is None:
+            k, v = (_torch.empty(cache.H_kv, batch.rows, cache.d, dtype=cache.dtype, device=device) for _ in range(2))
+        w, size = _space(cache.ws_bytes, device, ws)
+        kr, vr = None if k is None else _rows(k, True), None if v is None else _rows(v, True)
+        status = lib().sp_cache_read(cache.at, batch.at, kr and ctypes.addressof(kr), vr and ctypes.addressof(vr),
+                                     w.data_ptr(), size, handle)
+        if status:
+            _check(status)
+        if check:
+            _check(sp_workspace_status(w, handle))
+        return k, v
+
+    return _on(device, stream, call)
 
 
 def attend_workspace_size(q, cache, batch):
     """Workspace bytes of attend for these arguments."""
-    with _On(cache.device, None):
-        return sp_attend_workspace_size(cache.c, batch.c, q.shape[1])
+    return _on(cache.device, None, lambda handle: sp_attend_workspace_size(cache.c, batch.c, q.shape[1]))
 
 
 def attend(q, cache, batch, *, scale=None, window=0, out=None, lse=None, ws=None, stream=None, check=False):
     """Causal attention of the batch's new tokens, q [rows, H, d], over their sequences' cached tokens (their own
     among them): (out [rows, H, d], lse fp32 [H, rows]).  scale: default 1 / sqrt(d).  window > 0: each token sees
     itself and the window - 1 tokens before it.  lse may be any strided fp32 [H, rows], such as [l, :, j:j+1] of
-    score_lse's [L, H, N].  Rows that are not a token of the batch are not written."""
-    import torch
+    score_lse's [L, H, N].  out must not overlap q.  Rows that are not a token of the batch are not written."""
+    device, rows = cache.device, batch.rows
     H = q.shape[1] if q.dim() == 3 else 0
-    _check_rows_of(q, "q", batch.rows, H, cache.d, cache.dtype, cache.device)
+    _check_rows_of(q, "q", rows, H, cache.d, cache.dtype, device)
     if out is not None:
-        _check_rows_of(out, "out", batch.rows, H, cache.d, cache.dtype, cache.device)
-    if lse is not None and (tuple(lse.shape) != (H, batch.rows) or lse.dtype != torch.float32 or lse.device != q.device):
-        raise ValueError(f"lse must be fp32 [{H}, {batch.rows}] on {q.device}")
-    _same_device(cache.device, batch)
-    with _On(cache.device, stream):
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty(H, batch.rows, dtype=torch.float32, device=q.device)
-        ws = _workspace(sp_attend_workspace_size(cache.c, batch.c, H), cache.device, ws)
-        _check(sp_attend(_rows(q), cache.c, batch.c, H, cache.d ** -0.5 if scale is None else float(scale), int(window),
-                         _rows(out), lse, lse.stride(1), lse.stride(0), ws, ws.numel() * ws.element_size(), stream))
-        _check_device(ws, stream, check)
-    return out, lse
+        _check_rows_of(out, "out", rows, H, cache.d, cache.dtype, device)
+    if lse is not None and (lse.shape != (H, rows) or lse.dtype != _torch.float32 or lse.device != device):
+        raise ValueError(f"lse must be fp32 [{H}, {rows}] on {device}")
+    _same_device(device, batch)
+
+    def call(handle):
+        o, z = out, lse
+        if o is None:
+            o = _torch.empty((rows, H, cache.d), dtype=cache.dtype, device=device)
+        if z is None:
+            z = _torch.empty(H, rows, dtype=_torch.float32, device=device)
+        w, size = _space(sp_attend_workspace_size(cache.c, batch.c, H) if ws is None else 0, device, ws)
+        zh, zr = z.stride()
+        qr, outr = _rows(q), _rows(o)
+        status = lib().sp_attend(ctypes.addressof(qr), cache.at, batch.at, H,
+                                 cache.d ** -0.5 if scale is None else float(scale), int(window),
+                                 ctypes.addressof(outr), z.data_ptr(), zr, zh, w.data_ptr(), size, handle)
+        if status:
+            _check(status)
+        if check:
+            _check(sp_workspace_status(w, handle))
+        return o, z
+
+    return _on(device, stream, call)

@@ -18,7 +18,8 @@ sp_status cache_write_launch(const sp_cache& c, const sp_batch& b, const sp_rows
                              cudaStream_t st);
 sp_status cache_read_launch(const sp_cache& c, const sp_batch& b, const sp_rows& k, const sp_rows& v, void* ws,
                             cudaStream_t st);
-sp_status attend_simple_launch(const AttendProblem& p, void* ws, cudaStream_t st);
+size_t attend_general_ws_bytes(const sp_cache& c);
+sp_status attend_general_launch(const AttendProblem& p, void* ws, cudaStream_t st);
 bool attend_step_supported(const sp_cache& c);
 size_t attend_step_ws_bytes(const sp_cache& c);
 sp_status attend_step_launch(const AttendProblem& p, void* ws, cudaStream_t st);
@@ -70,7 +71,7 @@ sp_status check_workspace(const char* fn, const void* ws, size_t have, size_t ne
 
 // Which kernels a call takes.
 enum Path {
-    kSimple,        // the general one
+    kGeneral,       // the general one
     kStep,          // every sequence has at most the 16 rows per KV head of the step kernel
     kChunks,        // one sequence with more, or a cache that the step kernel does not take
     kMixed          // the step kernel for the sequences with few rows, the tensor-core one for the others
@@ -79,7 +80,7 @@ Path path_of(const sp_cache& c, const sp_batch& b, int H) {
     const int G = H / c.H_kv;
     const bool step = attend_step_supported(c);
     if (step && (int64_t)b.max_new * G <= 16) return kStep;
-    if (!attend_tc_supported(c, G)) return kSimple;
+    if (!attend_tc_supported(c, G)) return kGeneral;
     return step && b.B > 1 ? kMixed : kChunks;
 }
 
@@ -88,7 +89,7 @@ size_t path_bytes(Path path, const sp_cache& c, const sp_batch& b, int H) {
         case kStep: return attend_step_ws_bytes(c);
         case kChunks: return attend_tc_ws_bytes(c, b, H / c.H_kv);
         case kMixed: return std::max(attend_step_ws_bytes(c), attend_tc_ws_bytes(c, b, H / c.H_kv));
-        default: return sizeof(WsHeader);
+        default: return attend_general_ws_bytes(c);
     }
 }
 
@@ -321,7 +322,7 @@ sp_status sp_attend(const sp_rows* q, const sp_cache* cache, const sp_batch* bat
     p.lse = lse; p.lse_stride_row = lse_stride_row; p.lse_stride_head = lse_stride_head;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (path_of(*cache, *batch, H)) {
-        case kSimple: s = attend_simple_launch(p, ws, st); break;
+        case kGeneral: s = attend_general_launch(p, ws, st); break;
         case kStep: s = attend_step_launch(p, ws, st); break;
         case kChunks: s = attend_tc_launch(p, 0, ws, st); break;
         case kMixed:

@@ -26,7 +26,7 @@
 // equal runs, one per resident CTA, so a batch of any mixture of lengths keeps
 // every SM busy to the end; a pair that is cut leaves partial sums in the
 // workspace, and a second kernel, launched early, joins them in a fixed order.
-#include "paged.cuh"
+#include "attend_split.cuh"
 
 #include <algorithm>
 
@@ -35,96 +35,17 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRows = 16;          // rows of a slot of partial sums
-
-struct StepArgs {
-    AttendProblem a;
-    int G;
-    int rows;               // most query rows of a sequence that is taken (8 or 16)
-    int P;                  // CTAs of the main kernel
-    WsHeader* hdr;
-    int* err;               // [P] what each CTA found wrong (0: nothing)
-    float* part_o;          // [P][2][kRows][d]
-    float2* part_ml;        // [P][2][kRows] maximum and sum
-};
 
 template <int D, int kKind>
 constexpr int warp_tokens() { return kKind == SP_CACHE_SAME && D == 128 ? 16 : 32; }
 template <int D, int kKind>
 constexpr int unit_tokens() { return kWarps * warp_tokens<D, kKind>(); }
 
-// Tokens [first, kv) that the rows of a sequence see, and their units.
-struct Span {
-    int first, units;
-};
-__device__ __forceinline__ Span span_of(const Seq& s, int window, int unit) {
-    Span r;
-    r.first = first_seen(s, window);
-    r.units = max(1, (s.kv - r.first + unit - 1) / unit);
-    return r;
-}
-
-__device__ __forceinline__ bool is_step(const StepArgs& p, const Seq& s) {
-    return s.n > 0 && (int64_t)s.n * p.G <= p.rows;
-}
-
-// Units of sequence i's pairs for one KV head (0: not taken here).
-__device__ __forceinline__ int seq_units(const StepArgs& p, int i, int unit, bool& bad) {
-    const Seq s = load_seq(p.a.batch, p.a.cache.page, i);
-    if (!s.ok) bad = true;
-    return is_step(p, s) ? span_of(s, p.a.window, unit).units : 0;
-}
-
-// Sum over all sequences, by one warp.
-__device__ __forceinline__ int64_t total_units(const StepArgs& p, int unit, bool& bad) {
-    int64_t sum = 0;
-    for (int i = threadIdx.x & 31; i < p.a.batch.B; i += 32) sum += seq_units(p, i, unit, bad);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    bad = __any_sync(0xffffffffu, bad);
-    return sum * p.a.cache.H_kv;
-}
-
-// The sequence whose units hold unit u (< total), and the unit at which it
-// begins, by one warp.
-__device__ __forceinline__ int find_unit(const StepArgs& p, int unit, int64_t u, int64_t& begin) {
-    int64_t base = 0;
-    const int lane = threadIdx.x & 31;
-    bool bad = false;
-    for (int i0 = 0; i0 < p.a.batch.B; i0 += 32) {
-        const int64_t mine = i0 + lane < p.a.batch.B ? (int64_t)seq_units(p, i0 + lane, unit, bad) * p.a.cache.H_kv : 0;
-        int64_t incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, base + incl > u);
-        if (past) {
-            const int l = __ffs(past) - 1;
-            begin = base + __shfl_sync(0xffffffffu, incl - mine, l);
-            return i0 + l;
-        }
-        base += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    begin = base;
-    return p.a.batch.B;
-}
-
-// CTA c takes units [c * U / P, (c + 1) * U / P); the CTA of a unit:
-__device__ __forceinline__ int64_t cut(int64_t c, int64_t U, int P) { return c * U / P; }
-__device__ __forceinline__ int cta_of(int64_t u, int64_t U, int P) { return (int)(((u + 1) * P - 1) / U); }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 template <int kBytes>
@@ -155,7 +76,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 
 // kN: tiles of 8 query rows (1 or 2).  Registers bound the resident warps, and those the bytes in flight.
 template <int D, int kKind, int kN>
-__global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const __grid_constant__ StepArgs p) {
+__global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const __grid_constant__ SplitArgs p) {
     constexpr bool kSame = kKind == SP_CACHE_SAME;
     constexpr int kSize = kSame ? 2 : 1;                    // bytes of an entry in the cache
     constexpr int kTok = warp_tokens<D, kKind>(), kUnit = unit_tokens<D, kKind>();
@@ -175,15 +96,16 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
     bool bad_seq = false, bad_page = false;
     cudaTriggerProgrammaticLaunchCompletion();      // the joining kernel may line up: it waits for this one's end
     const int64_t U = total_units(p, kUnit, bad_seq);
-    int64_t u = cut(blockIdx.x, U, p.P);
-    const int64_t u_end = cut(blockIdx.x + 1, U, p.P);
+    const int P = parts_of(p, U);
+    int64_t u = cut(blockIdx.x, U, P);
+    const int64_t u_end = cut(blockIdx.x + 1, U, P);
     int64_t begin = 0;
     int b = u < u_end ? find_unit(p, kUnit, u, begin) : 0;
     const float f = p.a.scale * 1.4426950408889634f;
 
     while (u < u_end) {
         const Seq s = load_seq(bt, c.page, b);
-        if (!is_step(p, s)) {
+        if (row_blocks(p, s) == 0) {
             ++b;
             continue;
         }
@@ -482,12 +404,12 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
 // Joins the parts of the pairs that were cut: block (i, r) takes row r of pair
 // i = (sequence, KV head), a thread one entry.  Block (0, 0) also gathers the status.
 template <int D, int kKind>
-__global__ void __launch_bounds__(D) step_join_kernel(const __grid_constant__ StepArgs p) {
+__global__ void __launch_bounds__(D) step_join_kernel(const __grid_constant__ SplitArgs p) {
     constexpr int kUnit = unit_tokens<D, kKind>();
     bool bad = false;
     const int i = blockIdx.x, b = i / p.a.cache.H_kv, g = i - b * p.a.cache.H_kv, r = blockIdx.y;
     const Seq s = load_seq(p.a.batch, p.a.cache.page, b);
-    const bool mine = is_step(p, s) && r < s.n * p.G;
+    const bool mine = row_blocks(p, s) > 0 && r < s.n * p.G;
     int64_t U = 0, begin = 0;
     if (mine) {
         for (int k = threadIdx.x & 31; k < p.a.batch.B; k += 32) {
@@ -502,36 +424,27 @@ __global__ void __launch_bounds__(D) step_join_kernel(const __grid_constant__ St
         }
     }
     cudaGridDependencySynchronize();        // the main kernel's partial sums
-    if (i == 0 && r == 0) {
-        int code = 0;
-        for (int k = threadIdx.x; k < p.P; k += D) code |= p.err[k];
-        code = __syncthreads_or(code);
-        if (threadIdx.x == 0) {
-            p.hdr->status = code ? SP_EDEVICE : SP_OK;
-            p.hdr->where = code;            // 1: impossible lengths or offsets, 2: a page index out of range
-        }
-    }
+    if (i == 0 && r == 0) gather_status(p);
     if (!mine) return;
     U *= p.a.cache.H_kv;
     const int units = span_of(s, p.a.window, kUnit).units;
     begin = begin * p.a.cache.H_kv + (int64_t)g * units;
-    const int c0 = cta_of(begin, U, p.P), c1 = cta_of(begin + units - 1, U, p.P);
+    const int P = parts_of(p, U), c0 = cta_of(begin, U, P), c1 = cta_of(begin + units - 1, U, P);
     if (c0 == c1) return;                   // written by the main kernel
+    // the first part begins with the pair's first unit (slot 2 c0 + 1), the others do not (slot 2 k)
     const int e = threadIdx.x;
     float m = -INFINITY;
-    for (int k = c0; k <= c1; ++k) {
-        if (cut(k, U, p.P) == cut(k + 1, U, p.P)) continue;     // a CTA without units
-        m = fmaxf(m, p.part_ml[((int64_t)k * 2 + (cut(k, U, p.P) <= begin ? 1 : 0)) * kRows + r].x);
-    }
+    for (int k = c0; k <= c1; ++k) m = fmaxf(m, p.part_ml[((int64_t)k * 2 + (k == c0)) * kRows + r].x);
     float z = 0.f, v = 0.f;
+#pragma unroll 4
     for (int k = c0; k <= c1; ++k) {
-        if (cut(k, U, p.P) == cut(k + 1, U, p.P)) continue;
-        const int64_t slot = ((int64_t)k * 2 + (cut(k, U, p.P) <= begin ? 1 : 0)) * kRows + r;
+        const int64_t slot = ((int64_t)k * 2 + (k == c0)) * kRows + r;
         const float2 ml = p.part_ml[slot];
-        if (ml.x == -INFINITY && ml.y == 0.f) continue;
+        const float o = p.part_o[slot * D + e];
+        // without a maximum the part has summed nothing, or NaN alone: it counts as it is
         const float a = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
         z += ml.y * a;
-        v += p.part_o[slot * D + e] * a;
+        v += o * a;
     }
     const int t = r / p.G, h = g * p.G + r - t * p.G;
     static_cast<__nv_bfloat16*>(p.a.out.data)[(s.row0 + t) * p.a.out.stride_row + h * p.a.out.stride_head + e] =
@@ -544,27 +457,17 @@ __global__ void __launch_bounds__(D) step_join_kernel(const __grid_constant__ St
 int ctas(int rows) { return sm_count() * (rows <= 8 ? 3 : 2); }
 
 template <int D, int kKind>
-sp_status launch(const StepArgs& p, cudaStream_t st) {
+sp_status launch(const SplitArgs& p, cudaStream_t st) {
     if (p.rows <= 8) step_kernel<D, kKind, 1><<<p.P, kThreads, 0, st>>>(p);
     else step_kernel<D, kKind, 2><<<p.P, kThreads, 0, st>>>(p);
     SP_LAUNCH_CHECK();
     const int64_t rows = std::min<int64_t>(p.rows, (int64_t)p.a.batch.max_new * p.G);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.a.batch.B * p.a.cache.H_kv), (unsigned)std::max<int64_t>(1, rows));
-    cfg.blockDim = dim3(D);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    SP_CUDA_TRY(cudaLaunchKernelEx(&cfg, step_join_kernel<D, kKind>, p));
-    SP_LAUNCH_CHECK();
-    return SP_OK;
+    const dim3 grid((unsigned)(p.a.batch.B * p.a.cache.H_kv), (unsigned)std::max<int64_t>(1, rows));
+    return launch_early(step_join_kernel<D, kKind>, grid, D, (size_t)0, st, p);
 }
 
 template <int D>
-sp_status launch_kind(const StepArgs& p, cudaStream_t st) {
+sp_status launch_kind(const SplitArgs& p, cudaStream_t st) {
     switch (p.a.cache.kind) {
         case SP_CACHE_SAME: return launch<D, SP_CACHE_SAME>(p, st);
         case SP_CACHE_E4M3: return launch<D, SP_CACHE_E4M3>(p, st);
@@ -582,27 +485,11 @@ bool attend_step_supported(const sp_cache& c) {
              (uintptr_t)c.stride_head | (uintptr_t)c.stride_slot) % 16 == 0);
 }
 
-size_t attend_step_ws_bytes(const sp_cache& c) {
-    const size_t P = (size_t)ctas(8);       // the larger of the two grids
-    Carve w;
-    w.take(P * sizeof(int));
-    w.take(P * 2 * kRows * c.d * sizeof(float));
-    w.take(P * 2 * kRows * sizeof(float2));
-    return w.off;
-}
+size_t attend_step_ws_bytes(const sp_cache& c) { return split_ws_bytes((size_t)ctas(8), c.d); }   // the larger grid's
 
 sp_status attend_step_launch(const AttendProblem& a, void* ws, cudaStream_t st) {
-    StepArgs p;
-    p.a = a;
-    p.G = a.H / a.cache.H_kv;
-    p.rows = (int64_t)a.batch.max_new * p.G <= 8 ? 8 : 16;
-    p.P = ctas(p.rows);
-    Carve w;
-    char* base = static_cast<char*>(ws);
-    p.hdr = reinterpret_cast<WsHeader*>(base);
-    p.err = reinterpret_cast<int*>(base + w.take(p.P * sizeof(int)));
-    p.part_o = reinterpret_cast<float*>(base + w.take((size_t)p.P * 2 * kRows * a.cache.d * sizeof(float)));
-    p.part_ml = reinterpret_cast<float2*>(base + w.take((size_t)p.P * 2 * kRows * sizeof(float2)));
+    const int rows = (int64_t)a.batch.max_new * (a.H / a.cache.H_kv) <= 8 ? 8 : 16;
+    const SplitArgs p = split_args(a, rows, false, ctas(rows), ws);
     return a.cache.d == 64 ? launch_kind<64>(p, st) : launch_kind<128>(p, st);
 }
 

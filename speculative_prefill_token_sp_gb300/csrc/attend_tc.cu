@@ -158,6 +158,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
 }
 
+// CTA c takes the key tiles from cut(c) to cut(c + 1) of all U; P is the CTAs, or the tiles if those are fewer.
+__device__ __forceinline__ int64_t cut(int64_t c, int64_t U, int P) { return min(c, (int64_t)P) * U / max(P, 1); }
+
 // A CTA's run of key tiles, item by item.  Every role walks it by itself.
 struct Segment {
     Item it;
@@ -173,8 +176,9 @@ struct Walk {
         n = *p.n_items;
         per_head = p.pre[n];
         const int64_t U = per_head * p.a.cache.H_kv;
-        u = c * U / p.P;
-        u_end = (c + 1) * U / p.P;
+        const int P = (int)min((int64_t)p.P, U);
+        u = cut(c, U, P);
+        u_end = cut(c + 1, U, P);
         if (u < u_end) {
             g = (int)(u / per_head);
             i = find(p, u - g * per_head);
@@ -811,8 +815,9 @@ __global__ void __launch_bounds__(kRowsItem) tc_join_kernel(const __grid_constan
     const int c = blockIdx.x + 1, row = threadIdx.x;
     const int n = *p.n_items;
     const int64_t per_head = p.pre[n], U = per_head * p.a.cache.H_kv;
-    const int64_t u = c * U / p.P;
-    if (U == 0 || u >= U) return;
+    const int P = (int)min((int64_t)p.P, U);
+    const int64_t u = cut(c, U, P);
+    if (u >= U) return;
     const int g = (int)(u / per_head);
     int lo = 0, hi = n - 1;
     while (lo < hi) {
@@ -821,23 +826,19 @@ __global__ void __launch_bounds__(kRowsItem) tc_join_kernel(const __grid_constan
         else hi = mid - 1;
     }
     const int64_t begin = g * per_head + p.pre[lo];
-    if (u == begin || (c - 1) * U / p.P > begin || (c - 1) * U / p.P == u) return;
+    if (u == begin || cut(c - 1, U, P) > begin) return;
     const Item it = p.items[lo];
     const Seq s = load_seq(p.a.batch, p.a.cache.page, it.b);
-    const int64_t end = begin + it.tiles;
+    const int c1 = (int)(((begin + it.tiles) * P - 1) / U);        // the CTA of the item's last tile
     const int w = row >> 7, r = row & 127, t_row = r / p.G, t = it.t0 + w * p.tpt + t_row;
     if (r >= p.G * p.tpt || t >= s.n) return;
     float m = -INFINITY;
-    for (int k = c - 1; k < p.P && k * U / p.P < end; ++k) {
-        if (k * U / p.P == (k + 1) * U / p.P) continue;
-        m = fmaxf(m, p.part_ml[((int64_t)k * 2 + (k == c - 1 ? 1 : 0)) * kRowsItem + row].x);
-    }
+    for (int k = c - 1; k <= c1; ++k) m = fmaxf(m, p.part_ml[((int64_t)k * 2 + (k == c - 1)) * kRowsItem + row].x);
     float z = 0.f, v[16] = {};
-    for (int k = c - 1; k < p.P && k * U / p.P < end; ++k) {
-        if (k * U / p.P == (k + 1) * U / p.P) continue;
-        const int64_t slot = (int64_t)k * 2 + (k == c - 1 ? 1 : 0);
+    for (int k = c - 1; k <= c1; ++k) {
+        const int64_t slot = (int64_t)k * 2 + (k == c - 1);     // the first part begins with the item's first tile
         const float2 ml = p.part_ml[slot * kRowsItem + row];
-        if (ml.x == -INFINITY && ml.y == 0.f) continue;
+        // without a maximum the part has summed nothing, or NaN alone: it counts as it is
         const float a = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);
         z += ml.y * a;
         const float4* src = reinterpret_cast<const float4*>(p.part_o) + (slot * (D / 4) + blockIdx.y * 4) * kRowsItem + row;
@@ -906,24 +907,6 @@ sp_status encode(CUtensorMap* map, const void* data, int rank, const int64_t* ex
         set_error("sp_attend: cuTensorMapEncodeTiled failed (%d)", (int)r);
         return SP_ECUDA;
     }
-    return SP_OK;
-}
-
-// Launch that may begin while the kernel before it ends (the kernel waits for that by itself).
-template <typename... A>
-sp_status launch_early(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    SP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, args...));
-    SP_LAUNCH_CHECK();
     return SP_OK;
 }
 

@@ -44,7 +44,7 @@ __device__ __forceinline__ void write_row(const MoveArgs& p, const float (&x)[8]
 template <typename T, int kKind>
 __global__ void __launch_bounds__(kCacheThreads) write_kernel(const __grid_constant__ MoveArgs p) {
     if (blockIdx.x == gridDim.x - 1) {
-        check_batch(p.b, p.c, -1, p.hdr);
+        check_batch(p.b, p.c, p.hdr);
         return;
     }
     const int64_t i = ((int64_t)blockIdx.x * kCacheThreads + threadIdx.x) >> p.lg;
@@ -84,7 +84,7 @@ __device__ __forceinline__ void read_row(const void* data, const float* scales, 
 template <typename T, int kKind>
 __global__ void __launch_bounds__(kCacheThreads) read_kernel(const __grid_constant__ MoveArgs p) {
     if (blockIdx.x == gridDim.x - 1) {
-        if (blockIdx.y == 0) check_batch(p.b, p.c, -1, p.hdr);
+        if (blockIdx.y == 0) check_batch(p.b, p.c, p.hdr);
         return;
     }
     const int64_t r = ((int64_t)blockIdx.x * kCacheThreads + threadIdx.x) >> p.lg;

@@ -175,10 +175,9 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
     return make_uint2(w[0], w[1]);
 }
 
-// One block's check of everything the batch's device arrays say about the
-// tokens [first, kv) of each sequence, `first` being the first new token or, with
-// window >= 0, the first one that a row sees.  Writes the status: the only writer of the call.
-__device__ __forceinline__ void check_batch(const sp_batch& b, const sp_cache& c, int window, WsHeader* hdr) {
+// One block's check of everything the batch's device arrays say about the new
+// tokens of each sequence.  Writes the status: the only writer of the call.
+__device__ __forceinline__ void check_batch(const sp_batch& b, const sp_cache& c, WsHeader* hdr) {
     __shared__ int bad;
     if (threadIdx.x == 0) bad = 0;
     __syncthreads();
@@ -188,7 +187,7 @@ __device__ __forceinline__ void check_batch(const sp_batch& b, const sp_cache& c
         const Seq s = load_seq(b, c.page, i);
         if (!s.ok) mine = 1;
         if (s.n == 0 || s.kv == 0) continue;
-        const int first = (window < 0 ? max(0, s.kv - s.n) : first_seen(s, window)) / c.page, last = (s.kv - 1) / c.page;
+        const int first = max(0, s.kv - s.n) / c.page, last = (s.kv - 1) / c.page;
         for (int q = first + lane; q <= last; q += 32) {
             const int pg = b.table[(int64_t)i * b.table_stride + q];
             if (pg < 0 || pg >= c.pages) mine = 2;
@@ -208,6 +207,24 @@ sp_status check_batch_args(const char* fn, const sp_batch* b);
 
 // SMs of the current device (defined in abi_paged.cu).
 int sm_count();
+
+// Launch that may begin while the kernel before it ends (the kernel waits for that by itself).
+template <typename... A>
+sp_status launch_early(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    SP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, args...));
+    SP_LAUNCH_CHECK();
+    return SP_OK;
+}
 
 struct AttendProblem {
     sp_rows q, out;

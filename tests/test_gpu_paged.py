@@ -388,12 +388,11 @@ def test_what_the_arrays_get_wrong_is_reported_and_does_no_harm(sp, dtype, d, n)
     td = torch_dtype(dtype)
     H, H_kv, page = 4, 2, 16
     new, kv = [n, n, n], [n + 50, n + 40, n + 30]
-    cache, table, _, _ = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=kv, dtype=td)
+    cache, table, kval, vval = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=kv, dtype=td)
     good, cu = make_batch(sp, new, kv, table)
     T = 3 * n
     q = torch.from_numpy(rng.standard_normal((T, H, d))).to(td).cuda()
     x = torch.from_numpy(rng.standard_normal((T, H_kv, d))).to(td).cuda()
-    want, _ = sp.attend(q, cache, good, check=True)
     bad_page = table.copy()
     bad_page[1, 1] = cache.pages
     negative = table.copy()
@@ -408,8 +407,12 @@ def test_what_the_arrays_get_wrong_is_reported_and_does_no_harm(sp, dtype, d, n)
         ws = torch.empty(sp.attend_workspace_size(q, cache, batch), dtype=torch.uint8, device="cuda")
         sp.attend(q, cache, batch, out=out, ws=ws)
         assert sp.sp_workspace_status(ws) == sp.SP_EDEVICE, i
-        if i < 3:           # the sequences around the bad one are right
-            assert torch.equal(out[:n], want[:n]) and torch.equal(out[2 * n:], want[2 * n:])
+        for b in (0, 2) if i < 3 else ():
+            # the sequences around the bad one are right.  (Not to the bit what they are without it: where the keys are
+            # cut, and so the order of the sums, goes by the whole batch.  The bound holds for every order.)
+            ref, ref_lse, top, spread = oracle.paged.attend(f64(q[b * n:(b + 1) * n]), kval[b], vval[b], d ** -0.5)
+            bound, _ = attend_bounds(dtype, d, kv[b], ref, spread, top, ref_lse)
+            assert np.all(np.abs(f64(out[b * n:(b + 1) * n]) - ref) <= bound)
         if i in (2, 3, 4):
             assert torch.all(out[n:2 * n] == 7)
     # writing and reading: a bad page among the new tokens' own
