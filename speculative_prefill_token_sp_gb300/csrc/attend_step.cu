@@ -3,25 +3,27 @@
 // per KV head (a row is a new token's query head of the group).
 //
 // One pass over the keys with the running maximum and sum of each row's
-// softmax (base 2).  The work is bound by the cache's bytes: K and V are read
-// once, straight from global memory into the registers that mma.sync takes,
-// with no shared memory between.  Both products are taken transposed, so that
-// the query rows (8 a tile, few) are the narrow side and the accumulators are
-// small, and both sum over an index whose order does not matter (the entries of
-// a head, the tokens), so the order is chosen such that a lane's operand
-// registers are 16 consecutive bytes of a row.  Lane (n, q) = (lane / 4, lane % 4):
-//  * S^T = K Q^T: of tokens n and n + 8 the entries [j * 4E + q * E, + E) for
-//    each 16-byte load j of E entries; Q is laid out the same way;
+// softmax (base 2).  The work is bound by the cache's bytes, so what counts is
+// that enough of them are under way: each warp copies the rows of its next piece
+// (16 tokens, 32 where a row has at most 128 bytes) into its own ring in shared
+// memory with cp.async while it works on the piece before, with no barrier with
+// another warp; the four warps of a CTA take consecutive pieces of a unit of 64
+// (128) tokens.  Rows in the ring are 16 bytes apart from a multiple of 64, so
+// that the operand reads meet no bank twice.
+//
+// The products are mma.sync, transposed, so that the query rows (8 a tile, few)
+// are the narrow side and the accumulators are small.  Both sum over an index
+// whose order does not matter (the entries of a head, the tokens), so the order
+// is chosen such that a lane's operand registers are 16 consecutive bytes of a
+// row.  Lane (n, q) = (lane / 4, lane % 4):
+//  * S^T = K Q^T: of tokens n and n + 8 the 16-byte pieces 2q, 2q + 1 of each
+//    eight; Q is laid out the same way;
 //  * O^T = V^T P^T: of tokens 2q, 2q + 1, 2q + 8, 2q + 9 the entries [c * 8E +
 //    n * E, + E); a byte permute pairs two tokens' entries.  P^T needs its 8 x 8
 //    tiles transposed (movmatrix).  A lane's sums are runs of E consecutive
 //    entries of rows 2q and 2q + 1.
 // The tensor cores' time at these row counts is a fraction of the loads'.
 //
-// A warp takes 16 tokens (32 where a row has at most 128 bytes) at a time and
-// keeps its own statistics; the four warps of a CTA take consecutive pieces of a
-// unit of 64 (128) tokens.  K of the next piece is requested when this piece's logits are
-// done, V when its product is, so a warp has 4 to 8 KB in flight all the time.
 // The units of all (sequence, KV head) pairs are laid end to end and cut into
 // equal runs, one per resident CTA, so a batch of any mixture of lengths keeps
 // every SM busy to the end; a pair that is cut leaves partial sums in the
@@ -53,19 +55,42 @@ struct Chunk {
     uint32_t w[kBytes / 4];
 };
 template <int kBytes>
-__device__ __forceinline__ Chunk<kBytes> fetch(const void* p, bool there) {
+__device__ __forceinline__ Chunk<kBytes> read_chunk(const uint8_t* p) {
     Chunk<kBytes> c;
     if constexpr (kBytes == 16) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (there) v = __ldg(static_cast<const uint4*>(p));
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
         c.w[0] = v.x; c.w[1] = v.y; c.w[2] = v.z; c.w[3] = v.w;
     } else {
-        uint2 v = make_uint2(0, 0);
-        if (there) v = __ldg(static_cast<const uint2*>(p));
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
         c.w[0] = v.x; c.w[1] = v.y;
     }
     return c;
 }
+
+// Copies kBytes (16 or 4) to shared memory in the background; zeros where `there` is false.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
+    const int size = there ? kBytes : 0;
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
+
+// The ring of a warp: kStages pieces, each its tokens' K rows, V rows and scales.
+template <int D, int kKind, int kN>
+struct Ring {
+    static constexpr int kTok = warp_tokens<D, kKind>();
+    static constexpr int kRow = D * (kKind == SP_CACHE_SAME ? 2 : 1), kPitch = kRow + 16;
+    static constexpr int kV = kTok * kPitch, kScales = 2 * kV;
+    static constexpr int kStage = kScales + (kKind == SP_CACHE_SAME ? 0 : kTok * 8);
+    static constexpr int kCtas = kN == 1 ? 3 : 2;                       // resident on an SM
+    static constexpr int kStages = kN == 1 ? 2 : 3;
+    static constexpr int kBytes = kWarps * kStages * kStage;
+    static constexpr int kJoin = kWarps * 8 * kN * (D + 4) * 4;         // the warps' sums, in the ring's place at the end
+    static constexpr int kSmem = kBytes > kJoin ? kBytes : kJoin;
+    static_assert(kCtas * (kSmem + 1024 + kWarps * 8 * kN * 8) <= 228 * 1024, "the resident CTAs fit (1 KB of each is the system's)");
+};
 
 // Transpose of an 8 x 8 tile of 16-bit values: lane (n, q) gives row n's columns 2q, 2q + 1 and gets column n's rows 2q, 2q + 1.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -74,23 +99,27 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// kN: tiles of 8 query rows (1 or 2).  Registers bound the resident warps, and those the bytes in flight.
+// kN: tiles of 8 query rows (1 or 2).
 template <int D, int kKind, int kN>
 __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const __grid_constant__ SplitArgs p) {
     constexpr bool kSame = kKind == SP_CACHE_SAME;
+    using R = Ring<D, kKind, kN>;
     constexpr int kSize = kSame ? 2 : 1;                    // bytes of an entry in the cache
-    constexpr int kTok = warp_tokens<D, kKind>(), kUnit = unit_tokens<D, kKind>();
+    constexpr int kTok = R::kTok, kUnit = unit_tokens<D, kKind>(), kPitch = R::kPitch;
     constexpr int kT = kTok / 16;                           // tiles of 16 tokens
-    constexpr int kE = 16 / kSize;                          // entries of a K load
-    constexpr int kJ = D / (4 * kE);                        // K loads of a token
-    constexpr int kEv = D / 8 < kE ? D / 8 : kE;            // entries of a V load
-    constexpr int kC = D / (8 * kEv);                       // V loads of a token
-    constexpr int kVB = kEv * kSize;                        // bytes of a V load
+    constexpr int kE = 16 / kSize;                          // entries of a 16-byte piece
+    constexpr int kJ = D / (4 * kE);                        // pieces of a K row that a lane reads
+    constexpr int kEv = D / 8 < kE ? D / 8 : kE;            // entries of a V read
+    constexpr int kC = D / (8 * kEv);                       // V reads of a token
+    constexpr int kVB = kEv * kSize;                        // bytes of a V read
     constexpr int kO = kC * kEv / 2;                        // tiles of 16 entries of the sums
-    __shared__ float sm_o[kWarps][8 * kN][D + 4];
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float2 sm_ml[kWarps][8 * kN];
+    float (*sm_o)[8 * kN][D + 4] = reinterpret_cast<float (*)[8 * kN][D + 4]>(smem);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = lane >> 2, q4 = lane & 3;
+    uint8_t* ring = smem + warp * R::kStages * R::kStage;
+    const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
     const sp_cache& c = p.a.cache;
     const sp_batch& bt = p.a.batch;
     bool bad_seq = false, bad_page = false;
@@ -102,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
     int64_t begin = 0;
     int b = u < u_end ? find_unit(p, kUnit, u, begin) : 0;
     const float f = p.a.scale * 1.4426950408889634f;
+    auto piece = [&](int j) { return kJ == 1 ? q4 : (j >> 1) * 8 + 2 * q4 + (j & 1); };
 
     while (u < u_end) {
         const Seq s = load_seq(bt, c.page, b);
@@ -120,6 +150,51 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
         const int to = (int)min((int64_t)span.units, from + (u_end - u));
         const int rows = s.n * p.G;
 
+        // this lane's token (lane % kTok) of a piece: its page, a piece ahead, and where its rows are
+        const int32_t* table = bt.table + (int64_t)b * bt.table_stride;
+        const int tok0 = span.first + warp * kTok + (lane & (kTok - 1));
+        auto page_of = [&](int i) {
+            const int tok = tok0 + i * kUnit;
+            return i < to && tok < s.kv ? table[(unsigned)tok / (unsigned)c.page] : 0;
+        };
+        // requests piece i of the run into its place in the ring
+        auto request = [&](int i, int pg) {
+            if (i < to) {
+                const int tok = tok0 + i * kUnit;
+                const uint32_t at = ring_at + ((i - from) % R::kStages) * R::kStage;
+                int64_t mine = -1;
+                if (tok < s.kv) {
+                    if ((unsigned)pg < (unsigned)c.pages) mine = row_offset(c, pg, g, (int)((unsigned)tok % (unsigned)c.page));
+                    else bad_page = true;
+                }
+                if constexpr (!kSame) {
+                    if (lane < kTok) {
+                        const int64_t sc = mine >= 0 ? scale_offset(c, pg, g, (int)((unsigned)tok % (unsigned)c.page)) : 0;
+                        copy_async<4>(at + R::kScales + lane * 8, c.k_scale + sc, mine >= 0);
+                        copy_async<4>(at + R::kScales + lane * 8 + 4, c.v_scale + sc, mine >= 0);
+                    }
+                }
+                constexpr int kLanes = R::kRow / 16, kAtOnce = 32 / kLanes;    // lanes of a row, rows of a request
+#pragma unroll
+                for (int t = 0; t < kTok; t += kAtOnce) {
+                    const int row = t + lane / kLanes;
+                    const int64_t w = __shfl_sync(0xffffffffu, mine, row);
+                    const int64_t src = w * kSize + (lane % kLanes) * 16;
+                    const uint32_t dst = at + row * kPitch + (lane % kLanes) * 16;
+                    copy_async<16>(dst, static_cast<const char*>(c.k) + (w >= 0 ? src : 0), w >= 0);
+                    copy_async<16>(dst + R::kV, static_cast<const char*>(c.v) + (w >= 0 ? src : 0), w >= 0);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        int page0 = page_of(from), page1 = page_of(from + 1);
+#pragma unroll
+        for (int i = 0; i < R::kStages - 1; ++i) {
+            request(from + i, page0);
+            page0 = page1;
+            page1 = page_of(from + i + 2);
+        }
+
         // query row n (and n + 8) as operands, and the tokens that rows 2q, 2q + 1 (+ 8) see
         uint32_t qb[kN][2 * kJ * (kE / 8)][2];
         int last[kN][2], first[kN][2];
@@ -132,10 +207,11 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
             for (int j = 0; j < kJ; ++j)
 #pragma unroll
                 for (int e = 0; e < kE / 8; ++e) {
-                    const Chunk<16> x = fetch<16>(src + j * 4 * kE + q4 * kE + e * 8, r < rows);
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (r < rows) x = __ldg(reinterpret_cast<const uint4*>(src + piece(j) * kE + e * 8));
                     const int k = (j * (kE / 8) + e) * 2;
-                    qb[h][k][0] = x.w[0]; qb[h][k][1] = x.w[1];
-                    qb[h][k + 1][0] = x.w[2]; qb[h][k + 1][1] = x.w[3];
+                    qb[h][k][0] = x.x; qb[h][k][1] = x.y;
+                    qb[h][k + 1][0] = x.z; qb[h][k + 1][1] = x.w;
                 }
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
@@ -158,66 +234,14 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
                 for (int x = 0; x < 4; ++x) o[h][i][x] = 0.f;
         }
 
-        // this lane's token (lane % kTok) of a piece: where its rows are (entries; -1: nowhere) and its scales
-        const int32_t* table = bt.table + (int64_t)b * bt.table_stride;
-        const int tok_lane = lane & (kTok - 1);
-        auto page_of = [&](int tok) { return tok < s.kv ? table[(unsigned)tok / (unsigned)c.page] : 0; };
-        struct Where {
-            int64_t at;
-            float ks, vs;
-        };
-        auto place = [&](int tok, int pg) {
-            Where w{-1, 1.f, 1.f};
-            if (tok < s.kv) {
-                if ((unsigned)pg < (unsigned)c.pages) {
-                    const int slot = (int)((unsigned)tok % (unsigned)c.page);
-                    w.at = row_offset(c, pg, g, slot);
-                    if (!kSame) {
-                        const int64_t sc = scale_offset(c, pg, g, slot);
-                        w.ks = __ldg(c.k_scale + sc);
-                        w.vs = __ldg(c.v_scale + sc);
-                    }
-                } else {
-                    bad_page = true;
-                }
-            }
-            return w;
-        };
-        Chunk<16> kr[2 * kT][kJ];
-        Chunk<kVB> vr[4 * kT][kC];
-        auto load_k = [&](const Where& w) {
-#pragma unroll
-            for (int t = 0; t < 2 * kT; ++t) {
-                const int64_t at = __shfl_sync(0xffffffffu, w.at, t * 8 + n);
-                const char* src = static_cast<const char*>(c.k) + (at + q4 * kE) * kSize;
-#pragma unroll
-                for (int j = 0; j < kJ; ++j) kr[t][j] = fetch<16>(src + j * 64, at >= 0);
-            }
-        };
-        auto load_v = [&](const Where& w) {
-#pragma unroll
-            for (int t = 0; t < 4 * kT; ++t) {
-                const int tok = (t >> 1) * 8 + 2 * q4 + (t & 1);
-                const int64_t at = __shfl_sync(0xffffffffu, w.at, tok);
-                const char* src = static_cast<const char*>(c.v) + (at + n * kEv) * kSize;
-#pragma unroll
-                for (int i = 0; i < kC; ++i) vr[t][i] = fetch<kVB>(src + i * 8 * kVB, at >= 0);
-            }
-        };
-
-        const int tok0 = span.first + warp * kTok;
-        Where cur = place(tok0 + from * kUnit + tok_lane, page_of(tok0 + from * kUnit + tok_lane));
-        load_k(cur);
-        load_v(cur);
-        int next_page = page_of(tok0 + (from + 1) * kUnit + tok_lane);
         for (int i = from; i < to; ++i) {
-            const int base = tok0 + i * kUnit;
-            const bool more = i + 1 < to;
-            Where nxt{-1, 1.f, 1.f};
-            if (more) {
-                nxt = place(base + kUnit + tok_lane, next_page);
-                next_page = page_of(base + 2 * kUnit + tok_lane);
-            }
+            const int base = span.first + warp * kTok + i * kUnit;
+            request(i + R::kStages - 1, page0);
+            page0 = page1;
+            page1 = page_of(i + R::kStages + 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(R::kStages - 1) : "memory");
+            __syncwarp();
+            const uint8_t* at = ring + ((i - from) % R::kStages) * R::kStage;
             // logits: x[h][t] holds tokens 16t + n (first two) and 16t + n + 8, rows 8h + 2q and 8h + 2q + 1
             float x[kN][kT][4];
 #pragma unroll
@@ -228,7 +252,8 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
                     for (int y = 0; y < 4; ++y) x[h][t][y] = 0.f;
 #pragma unroll
                 for (int j = 0; j < kJ; ++j) {
-                    const Chunk<16>&lo = kr[2 * t][j], &hi = kr[2 * t + 1][j];
+                    const uint8_t* src = at + (16 * t + n) * kPitch + piece(j) * 16;
+                    const Chunk<16> lo = read_chunk<16>(src), hi = read_chunk<16>(src + 8 * kPitch);
 #pragma unroll
                     for (int k = 0; k < kE / 4; ++k) {
                         uint32_t a[4];
@@ -249,7 +274,6 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
                     }
                 }
             }
-            if (more) load_k(nxt);
             const bool masked = base + kTok - 1 > all_last || base < all_first;
             float vs[kSame ? 1 : kT][2];
             float top[kN][2];
@@ -262,8 +286,9 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
                     const int tl = 16 * t + 8 * e + n, tok = base + tl;
                     float ft = f;
                     if constexpr (!kSame) {
-                        ft *= __shfl_sync(0xffffffffu, cur.ks, tl);
-                        vs[t][e] = __shfl_sync(0xffffffffu, cur.vs, tl);
+                        const float2 sc = *reinterpret_cast<const float2*>(at + R::kScales + tl * 8);
+                        ft *= sc.x;
+                        vs[t][e] = sc.y;
                     }
 #pragma unroll
                     for (int h = 0; h < kN; ++h)
@@ -313,9 +338,13 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
                         z[h][0] += w0;
                         z[h][1] += w1;
                         if constexpr (!kSame) {
-                            // a masked token's weight stays 0 whatever its scale is
-                            w0 = w0 == 0.f ? 0.f : w0 * vs[t][e];
-                            w1 = w1 == 0.f ? 0.f : w1 * vs[t][e];
+                            if (masked) {       // a masked token's weight stays 0 whatever its scale is
+                                w0 = w0 == 0.f ? 0.f : w0 * vs[t][e];
+                                w1 = w1 == 0.f ? 0.f : w1 * vs[t][e];
+                            } else {
+                                w0 *= vs[t][e];
+                                w1 *= vs[t][e];
+                            }
                         }
                         pb[h][t][e] = transpose8(pack_bf16(w0, w1));
                     }
@@ -323,27 +352,34 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
 #pragma unroll
             for (int t = 0; t < kT; ++t)
 #pragma unroll
-                for (int cc = 0; cc < kC; ++cc)
+                for (int cc = 0; cc < kC; ++cc) {
+                    Chunk<kVB> vr[4];           // tokens 2q, 2q + 1, 2q + 8, 2q + 9 of the tile
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        vr[y] = read_chunk<kVB>(at + R::kV + (16 * t + 8 * (y >> 1) + 2 * q4 + (y & 1)) * kPitch +
+                                                (cc * 8 + n) * kVB);
 #pragma unroll
                     for (int e = 0; e < kEv; e += 2) {
                         uint32_t a[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {       // entry e + (y & 1) of tokens 2q, 2q + 1 (+ 8 for y >= 2)
-                            const int w = (e + (y & 1)) * kSize / 4, at = 4 * t + (y >> 1) * 2;
+                            const int w = (e + (y & 1)) * kSize / 4, i2 = (y >> 1) * 2;
                             if constexpr (kSame) {
-                                a[y] = __byte_perm(vr[at][cc].w[w], vr[at + 1][cc].w[w], y & 1 ? 0x7632 : 0x5410);
+                                a[y] = __byte_perm(vr[i2].w[w], vr[i2 + 1].w[w], y & 1 ? 0x7632 : 0x5410);
                             } else {
                                 // the first token's byte to bits 8-15, the second's to bits 24-31
                                 const uint32_t i4 = (e + (y & 1)) & 3, sel = 0x4000u + (i4 << 12) + (i4 << 4);
-                                a[y] = pair_of<kKind>(__byte_perm(vr[at][cc].w[w], vr[at + 1][cc].w[w], sel));
+                                a[y] = pair_of<kKind>(__byte_perm(vr[i2].w[w], vr[i2 + 1].w[w], sel));
                             }
                         }
 #pragma unroll
                         for (int h = 0; h < kN; ++h) mma16816(o[h][(cc * kEv + e) / 2], a, pb[h][t][0], pb[h][t][1]);
                     }
-            if (more) load_v(nxt);
-            cur = nxt;
+                }
+            __syncwarp();           // the piece has been read by all lanes: its place may be filled again
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();            // every warp is done with its ring, which takes the sums now
 
         // join the four warps: lane (n, q) holds entries cc * 8 kEv + n * kEv + e of rows 2q, 2q + 1
 #pragma unroll
@@ -458,8 +494,10 @@ int ctas(int rows) { return sm_count() * (rows <= 8 ? 3 : 2); }
 
 template <int D, int kKind>
 sp_status launch(const SplitArgs& p, cudaStream_t st) {
-    if (p.rows <= 8) step_kernel<D, kKind, 1><<<p.P, kThreads, 0, st>>>(p);
-    else step_kernel<D, kKind, 2><<<p.P, kThreads, 0, st>>>(p);
+    const int smem = p.rows <= 8 ? Ring<D, kKind, 1>::kSmem : Ring<D, kKind, 2>::kSmem;
+    void (*kern)(SplitArgs) = p.rows <= 8 ? step_kernel<D, kKind, 1> : step_kernel<D, kKind, 2>;
+    SP_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    kern<<<p.P, kThreads, smem, st>>>(p);
     SP_LAUNCH_CHECK();
     const int64_t rows = std::min<int64_t>(p.rows, (int64_t)p.a.batch.max_new * p.G);
     const dim3 grid((unsigned)(p.a.batch.B * p.a.cache.H_kv), (unsigned)std::max<int64_t>(1, rows));
