@@ -22,6 +22,9 @@
 //    n * E, + E); a byte permute pairs two tokens' entries.  P^T needs its 8 x 8
 //    tiles transposed (movmatrix).  A lane's sums are runs of E consecutive
 //    entries of rows 2q and 2q + 1.
+// Codes of an 8-bit cache become fp16 for the first product, one instruction a pair (the query rows too, each times a
+// power of two that brings its largest entry near 2^10: an entry is exact unless it is below 2^-27 of that one, and then off by at
+// most 2^-35 of it).  For the second they become bf16, as its weights carry the values' scales, whose range fp16 does not have.
 // The tensor cores' time at these row counts is a fraction of the loads'.
 //
 // The units of all (sequence, KV head) pairs are laid end to end and cut into
@@ -29,6 +32,8 @@
 // every SM busy to the end; a pair that is cut leaves partial sums in the
 // workspace, and a second kernel, launched early, joins them in a fixed order.
 #include "attend_split.cuh"
+
+#include <cuda_fp16.h>
 
 #include <algorithm>
 
@@ -91,6 +96,33 @@ struct Ring {
     static constexpr int kSmem = kBytes > kJoin ? kBytes : kJoin;
     static_assert(kCtas * (kSmem + 1024 + kWarps * 8 * kN * 8) <= 228 * 1024, "the resident CTAs fit (1 KB of each is the system's)");
 };
+
+// The same with fp16 operands.
+__device__ __forceinline__ void mma16816h(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four codes as two pairs of fp16 (their values before the scale, exactly).
+template <int kKind>
+__device__ __forceinline__ void half_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if constexpr (kKind == SP_CACHE_E4M3) {
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(w));
+    } else {
+        // 0x6400 + (8 bits) is 1024 + those bits; with the sign bit flipped they are the code + 128
+        const uint32_t u = w ^ 0x80808080u;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
+    }
+}
+
+// A pair of bf16, times a power of two, as a pair of fp16.
+__device__ __forceinline__ uint32_t half_of(uint32_t w, float scale) {
+    const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * scale, __uint_as_float(w & 0xffff0000u) * scale);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
 
 // Transpose of an 8 x 8 tile of 16-bit values: lane (n, q) gives row n's columns 2q, 2q + 1 and gets column n's rows 2q, 2q + 1.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -197,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
 
         // query row n (and n + 8) as operands, and the tokens that rows 2q, 2q + 1 (+ 8) see
         uint32_t qb[kN][2 * kJ * (kE / 8)][2];
+        float fq[kN][2];            // the logits' factor (8-bit caches: with the query rows' own)
         int last[kN][2], first[kN][2];
 #pragma unroll
         for (int h = 0; h < kN; ++h) {
@@ -213,6 +246,25 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
                     qb[h][k][0] = x.x; qb[h][k][1] = x.y;
                     qb[h][k + 1][0] = x.z; qb[h][k + 1][1] = x.w;
                 }
+            if constexpr (!kSame) {
+                // the row's largest exponent; without a finite one (zeros, infinities, NaN) the row stays as it is
+                uint32_t top = 0;
+#pragma unroll
+                for (int k = 0; k < 2 * kJ * (kE / 8); ++k)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        top = max(top, max(qb[h][k][y] & 0x7f80u, (qb[h][k][y] >> 16) & 0x7f80u));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int shift = top == 0 || top == 0x7f80u ? 0 : min(max(137 - (int)(top >> 7), -100), 100);
+                const float up = __int_as_float((127 + shift) << 23), down = __int_as_float((127 - shift) << 23);
+#pragma unroll
+                for (int k = 0; k < 2 * kJ * (kE / 8); ++k)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) qb[h][k][y] = half_of(qb[h][k][y], up);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) fq[h][y] = f * __shfl_sync(0xffffffffu, down, 4 * (2 * q4 + y));
+            }
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 const int ry = 8 * h + 2 * q4 + y;
@@ -261,15 +313,14 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
                             a[0] = lo.w[2 * k]; a[1] = hi.w[2 * k];
                             a[2] = lo.w[2 * k + 1]; a[3] = hi.w[2 * k + 1];
                         } else {
-                            a[0] = pair_of<kKind>(__byte_perm(lo.w[k], 0, 0x1404));
-                            a[1] = pair_of<kKind>(__byte_perm(hi.w[k], 0, 0x1404));
-                            a[2] = pair_of<kKind>(__byte_perm(lo.w[k], 0, 0x3424));
-                            a[3] = pair_of<kKind>(__byte_perm(hi.w[k], 0, 0x3424));
+                            half_pairs<kKind>(lo.w[k], a[0], a[2]);
+                            half_pairs<kKind>(hi.w[k], a[1], a[3]);
                         }
 #pragma unroll
                         for (int h = 0; h < kN; ++h) {
                             const int kk = j * (kE / 4) + k;
-                            mma16816(x[h][t], a, qb[h][kk][0], qb[h][kk][1]);
+                            if constexpr (kSame) mma16816(x[h][t], a, qb[h][kk][0], qb[h][kk][1]);
+                            else mma16816h(x[h][t], a, qb[h][kk][0], qb[h][kk][1]);
                         }
                     }
                 }
@@ -284,10 +335,9 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int tl = 16 * t + 8 * e + n, tok = base + tl;
-                    float ft = f;
+                    float2 sc = make_float2(1.f, 1.f);
                     if constexpr (!kSame) {
-                        const float2 sc = *reinterpret_cast<const float2*>(at + R::kScales + tl * 8);
-                        ft *= sc.x;
+                        sc = *reinterpret_cast<const float2*>(at + R::kScales + tl * 8);
                         vs[t][e] = sc.y;
                     }
 #pragma unroll
@@ -295,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
                             float& v = x[h][t][2 * e + y];
-                            v *= ft;
+                            v *= kSame ? f : fq[h][y] * sc.x;
                             if (masked && (tok > last[h][y] || tok < first[h][y])) v = -INFINITY;
                             top[h][y] = fmaxf(top[h][y], v);
                         }
@@ -437,11 +487,16 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
     if (threadIdx.x == 0) p.err[blockIdx.x] = any;
 }
 
-// Joins the parts of the pairs that were cut: block (i, r) takes row r of pair
-// i = (sequence, KV head), a thread one entry.  Block (0, 0) also gathers the status.
+constexpr int kJoinThreads = 256;
+
+// Joins the parts of the pairs that were cut: block (i, r) takes row r of pair i = (sequence, KV head).  A thread
+// has four entries of every kGroups-th part, several of them under way at once: a pair may be cut into hundreds.
+// Block (0, 0) also gathers the status.
 template <int D, int kKind>
-__global__ void __launch_bounds__(D) step_join_kernel(const __grid_constant__ SplitArgs p) {
-    constexpr int kUnit = unit_tokens<D, kKind>();
+__global__ void __launch_bounds__(kJoinThreads) step_join_kernel(const __grid_constant__ SplitArgs p) {
+    constexpr int kUnit = unit_tokens<D, kKind>(), kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+    __shared__ float4 sm_o[kGroups][kLanes];
+    __shared__ float2 sm_mz[kJoinThreads / 32];
     bool bad = false;
     const int i = blockIdx.x, b = i / p.a.cache.H_kv, g = i - b * p.a.cache.H_kv, r = blockIdx.y;
     const Seq s = load_seq(p.a.batch, p.a.cache.page, b);
@@ -459,33 +514,55 @@ __global__ void __launch_bounds__(D) step_join_kernel(const __grid_constant__ Sp
             begin += __shfl_xor_sync(0xffffffffu, begin, o);
         }
     }
-    cudaGridDependencySynchronize();        // the main kernel's partial sums
-    if (i == 0 && r == 0) gather_status(p);
-    if (!mine) return;
     U *= p.a.cache.H_kv;
     const int units = span_of(s, p.a.window, kUnit).units;
     begin = begin * p.a.cache.H_kv + (int64_t)g * units;
-    const int P = parts_of(p, U), c0 = cta_of(begin, U, P), c1 = cta_of(begin + units - 1, U, P);
-    if (c0 == c1) return;                   // written by the main kernel
+    const int P = parts_of(p, U), c0 = mine ? cta_of(begin, U, P) : 0, c1 = mine ? cta_of(begin + units - 1, U, P) : 0;
+    cudaGridDependencySynchronize();        // the main kernel's partial sums
+    if (i == 0 && r == 0) gather_status(p);
+    if (c0 == c1) return;                   // not taken here, or written by the main kernel
     // the first part begins with the pair's first unit (slot 2 c0 + 1), the others do not (slot 2 k)
-    const int e = threadIdx.x;
-    float m = -INFINITY;
-    for (int k = c0; k <= c1; ++k) m = fmaxf(m, p.part_ml[((int64_t)k * 2 + (k == c0)) * kRows + r].x);
-    float z = 0.f, v = 0.f;
+    const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+    float m = -INFINITY, z = 0.f;
+    for (int k = c0 + threadIdx.x; k <= c1; k += kJoinThreads)
+        m = fmaxf(m, p.part_ml[((int64_t)k * 2 + (k == c0)) * kRows + r].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((threadIdx.x & 31) == 0) sm_mz[threadIdx.x >> 5].x = m;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kJoinThreads / 32; ++k) m = fmaxf(m, sm_mz[k].x);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int k = c0; k <= c1; ++k) {
+    for (int k = c0 + grp; k <= c1; k += kGroups) {
         const int64_t slot = ((int64_t)k * 2 + (k == c0)) * kRows + r;
         const float2 ml = p.part_ml[slot];
-        const float o = p.part_o[slot * D + e];
+        const float4 o = *reinterpret_cast<const float4*>(p.part_o + slot * D + lane * 4);
         // without a maximum the part has summed nothing, or NaN alone: it counts as it is
         const float a = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
         z += ml.y * a;
-        v += o * a;
+        v.x += o.x * a; v.y += o.y * a; v.z += o.z * a; v.w += o.w * a;
+    }
+    sm_o[grp][lane] = v;
+    __shared__ float sm_z[kGroups];
+    if (lane == 0) sm_z[grp] = z;
+    __syncthreads();
+    if (grp > 0) return;
+    z = 0.f;
+    v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+        const float4 o = sm_o[k][lane];
+        z += sm_z[k];
+        v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
     }
     const int t = r / p.G, h = g * p.G + r - t * p.G;
-    static_cast<__nv_bfloat16*>(p.a.out.data)[(s.row0 + t) * p.a.out.stride_row + h * p.a.out.stride_head + e] =
-        __float2bfloat16_rn(z == 0.f ? 0.f : v / z);
-    if (p.a.lse && e == 0)
+    const float inv = z == 0.f ? 0.f : 1.f / z;
+    if (z == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out.data) + (s.row0 + t) * p.a.out.stride_row +
+                              h * p.a.out.stride_head + lane * 4) =
+        make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+    if (p.a.lse && lane == 0)
         p.a.lse[(s.row0 + t) * p.a.lse_stride_row + h * p.a.lse_stride_head] =
             z == 0.f ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
 }
@@ -501,7 +578,7 @@ sp_status launch(const SplitArgs& p, cudaStream_t st) {
     SP_LAUNCH_CHECK();
     const int64_t rows = std::min<int64_t>(p.rows, (int64_t)p.a.batch.max_new * p.G);
     const dim3 grid((unsigned)(p.a.batch.B * p.a.cache.H_kv), (unsigned)std::max<int64_t>(1, rows));
-    return launch_early(step_join_kernel<D, kKind>, grid, D, (size_t)0, st, p);
+    return launch_early(step_join_kernel<D, kKind>, grid, kJoinThreads, (size_t)0, st, p);
 }
 
 template <int D>
