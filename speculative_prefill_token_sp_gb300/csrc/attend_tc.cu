@@ -16,14 +16,18 @@
 // is scaled only when a row's maximum grows by more than 2^8 over the one it
 // is held by (P is then at most 2^8, and bf16 has the same precision there).
 //
-// Warp roles of a CTA (one per SM; 512 threads):
+// Warp roles of a CTA (one per SM):
 //  * warps 0-3, 4-7: softmax of tiles A and B, the scaling of O, and the output;
-//  * warps 8-11: convert the rows of an 8-bit cache to bf16 into the shared-
-//    memory tiles (unused for a cache of bf16);
-//  * warp 12: issues the MMAs;
-//  * warp 13: TMA loads of K and V tiles, page by page (boxes of the largest
+//  * four warps, for an 8-bit cache only: convert its rows to bf16 into the
+//    shared-memory tiles;
+//  * two warps issue the MMAs of A and B: a thread that issues them is held up
+//    until the tensor cores are nearly done with them, so what it does in between
+//    (some 1000 cycles a tile for one thread) is only hidden by the other's MMAs.
+//    They hand a turn to and fro, or the tiles' MMAs would mix and both tiles'
+//    softmax fall into the same time (chunk of 4096 over 32768: 1.80 ms);
+//  * one makes the TMA loads of K and V tiles, page by page (boxes of the largest
 //    power of two that divides the page), and of Q;
-//  * warp 14: zeroes what a V tile holds of slots without a token, as 0 * NaN
+//  * one zeroes what a V tile holds of slots without a token, as 0 * NaN
 //    in P V would be NaN.  (K needs none: masked logits are replaced.)
 //
 // The items of the call, longest part first within a sequence, are laid end to
@@ -40,7 +44,15 @@
 namespace sp {
 namespace {
 
-constexpr int kThreads = 512;
+// Warpgroups: two of softmax, one that converts 8-bit rows (if there are any), one of single-warp roles.
+template <int kKind>
+constexpr int tc_threads() { return kKind == SP_CACHE_SAME ? 384 : 512; }
+// Registers of a thread in each.  setmaxnreg shares out what the block was launched with: 384 threads of 168 (256 * 216 + 128 *
+// 72), or 512 of 128 (256 * 192 + 128 * 80 + 128 * 48).
+template <int kKind>
+struct Regs {
+    static constexpr int kSoftmax = kKind == SP_CACHE_SAME ? 216 : 192, kConvert = 80, kSingle = kKind == SP_CACHE_SAME ? 72 : 48;
+};
 constexpr int kRowsItem = 256;
 constexpr int kKeys = 128;              // keys of a tile
 constexpr int kSmem = 227 * 1024;
@@ -168,41 +180,42 @@ struct Segment {
     int g, from, to;        // KV head; tiles [from, to) of the item, counted from its last keys to its first
 };
 
+// The item that holds tile r of a head.
+__device__ __forceinline__ int find_item(const TcArgs& p, int n, int64_t r) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.pre[mid] <= r) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
 struct Walk {
-    int64_t u, u_end, per_head;
-    int n, i, g;
+    int left, n, i, g, from;        // tiles left; items of a head; the next item, its head and first tile
 
     __device__ __forceinline__ Walk(const TcArgs& p, int c) {
         n = *p.n_items;
-        per_head = p.pre[n];
-        const int64_t U = per_head * p.a.cache.H_kv;
+        const int64_t per_head = p.pre[n], U = per_head * p.a.cache.H_kv;
         const int P = (int)min((int64_t)p.P, U);
-        u = cut(c, U, P);
-        u_end = cut(c + 1, U, P);
-        if (u < u_end) {
-            g = (int)(u / per_head);
-            i = find(p, u - g * per_head);
-        }
-    }
-    // the item that holds tile r of a head
-    __device__ __forceinline__ int find(const TcArgs& p, int64_t r) const {
-        int lo = 0, hi = n - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.pre[mid] <= r) lo = mid;
-            else hi = mid - 1;
-        }
-        return lo;
+        const int64_t u = cut(c, U, P);
+        left = (int)(cut(c + 1, U, P) - u);
+        i = g = from = 0;
+        if (left == 0) return;
+        g = (int)(u / per_head);
+        i = find_item(p, n, u - g * per_head);
+        from = (int)(u - g * per_head - p.pre[i]);
     }
     __device__ __forceinline__ bool next(const TcArgs& p, Segment& o) {
-        if (u >= u_end) return false;
+        if (left == 0) return false;
         o.it = p.items[i];
         o.s = load_seq(p.a.batch, p.a.cache.page, o.it.b);
         o.g = g;
-        o.from = (int)(u - g * per_head - p.pre[i]);
-        o.to = (int)min((int64_t)o.it.tiles, o.from + (u_end - u));
-        u += o.to - o.from;
-        if (o.to == o.it.tiles && ++i == n) i = 0, ++g;
+        o.from = from;
+        o.to = min(o.it.tiles, from + left);
+        left -= o.to - from;
+        from = 0;
+        if (++i == n) i = 0, ++g;
         return true;
     }
 };
@@ -340,7 +353,7 @@ struct Layout {
 };
 
 template <int D, int kKind>
-__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_constant__ Maps maps,
+__global__ void __launch_bounds__(tc_threads<kKind>(), 1) attend_tc_kernel(const __grid_constant__ Maps maps,
                                                                 const __grid_constant__ TcArgs p) {
     using L = Layout<D>;
     constexpr bool kSame = kKind == SP_CACHE_SAME;
@@ -356,29 +369,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     uint64_t* s_full = q_empty + 1;         // [2] S is in TMEM (and all earlier P V done)
     uint64_t* p_full = s_full + 2;          // [2] P is in TMEM, O is scaled
     uint64_t* o_full = p_full + 2;          // [2] O is final
-    uint64_t* final_bar = o_full + 2;
+    uint64_t* turn = o_full + 2;            // [2] this row tile's MMAs may be issued
+    uint64_t* final_bar = turn + 2;
     volatile uint32_t* tmem_sh = reinterpret_cast<volatile uint32_t*>(final_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_sh + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kMma = kSame ? 8 : 12, kTma = kMma + 2, kClean = kMma + 3;     // the single-warp roles
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(smem_u32(&full[i]), kSame ? 1 : 4);
-            mbar_init(smem_u32(&empty[i]), 1);
+            mbar_init(smem_u32(&empty[i]), 2);          // the two MMA warps
             mbar_init(smem_u32(&landed[i]), 1);
         }
         mbar_init(smem_u32(q_full), 1);
-        mbar_init(smem_u32(q_empty), 1);
+        mbar_init(smem_u32(q_empty), 2);
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_u32(&s_full[w]), 1);
             mbar_init(smem_u32(&p_full[w]), 4);
             mbar_init(smem_u32(&o_full[w]), 1);
+            mbar_init(smem_u32(&turn[w]), 1);
         }
-        mbar_init(smem_u32(final_bar), 1);
+        mbar_init(smem_u32(final_bar), 2);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 12) {
+    if (warp == kMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_u32((const void*)tmem_sh)), "r"(512)
                      : "memory");
@@ -396,8 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
 
     if (warp < 8) {
         // ------------------------------ softmax and output ------------------------------
-        // 512 threads are launched with 128 registers each: 256 * 192 + 128 * (64 + 64 or 80 + 48) is all of them
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<kKind>::kSoftmax));
         const int w = warp >> 2, row = (warp & 3) * 32 + lane;          // row tile; row = TMEM lane
         const uint32_t lane_at = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lane_at + L::kS(w), o_at = tmem + lane_at + L::kO(w);
@@ -522,12 +537,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
             }
             tc_fence_before();          // O is read before this thread's next hand-off of P
         }
-    } else if (warp < 12) {
+    } else if (!kSame && warp < 12) {
+      if constexpr (!kSame) {
         // ------------------------------ conversion of 8-bit rows ------------------------------
         // A warp takes 32 rows of each tile; a lane 16 entries of a row, so that a row's lanes read it whole.  A
         // piece is requested for the next tile as soon as it is converted for this one.
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSame ? 64 : 80));
-        if constexpr (!kSame) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kKind>::kConvert));
+        {
             constexpr int kLanes = D / 16, kPass = kLanes;              // lanes of a row; rows of a warp / rows at a time
             const sp_cache& c = p.a.cache;
             const int r0 = (warp - 8) * 32, lp = lane % kLanes, rl = lane / kLanes;
@@ -615,75 +631,85 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 }
             }
         }
+      }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSame ? 64 : 48));
-        if (warp == 12) {
-            // ------------------------------ MMAs ------------------------------
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kKind>::kSingle));
+        if (warp == kMma || warp == kMma + 1) {
+            // ------------------------------ MMAs of one row tile ------------------------------
             if (lane == 0) {
                 constexpr uint32_t kIdS = instr_desc(kKeys, false), kIdO = instr_desc(D, true);
-                const uint32_t ring = smem_u32(smem + L::kRing), qs = smem_u32(smem + L::kQ);
+                const int w = warp - kMma;
+                const uint32_t s_at = tmem + L::kS(w), o_at = tmem + L::kO(w);
+                const uint32_t ring = smem_u32(smem + L::kRing);
+                const uint64_t q_desc = smem_desc(smem_u32(smem + L::kQ) + w * L::kTileBytes);
+                const uint64_t k_desc = smem_desc(ring), v_desc = smem_desc_mn(ring);
                 int st = 0;
-                uint32_t ph = 0, ph_q = 0, ph_p = 0;
+                uint32_t ph = 0, ph_q = 0, ph_p = 0, ph_t = 1 - w;     // the first turn is A's
                 bool ok = true;
-                auto step = [&](int& s, uint32_t& h) {
-                    if (++s == NS) s = 0, h ^= 1;
+                auto step = [&] {
+                    if (++st == NS) st = 0, ph ^= 1;
                 };
-                auto s_mma = [&](int w, int stage) {
-                    const uint64_t a = smem_desc(qs + w * L::kTileBytes), b = smem_desc(ring + stage * L::kTileBytes);
+                auto s_mma = [&](bool hand_on) {
+                    const uint64_t b = k_desc + (uint64_t)(st * (L::kTileBytes >> 4));
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint64_t off = (uint64_t)(((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4);
-                        tc_mma(tmem + L::kS(w), a + off, b + off, kIdS, k > 0);
+                        tc_mma(s_at, q_desc + off, b + off, kIdS, k > 0);
                     }
+                    if (hand_on) mbar_arrive(smem_u32(&turn[1 - w]));
                     tc_commit(smem_u32(&s_full[w]));
+                    tc_commit(smem_u32(&empty[st]));
                 };
                 while (ok && walk.next(p, sg)) {
-                    const int nw = two_tiles(p, sg) ? 2 : 1, nt = sg.to - sg.from;
+                    const int nt = sg.to - sg.from;
+                    const bool two = two_tiles(p, sg);
                     ok = wait_bar(smem_u32(q_full), ph_q, abort_flag, p.hdr, 31);
                     ph_q ^= 1;
-                    ok = ok && wait_bar(smem_u32(&full[st]), ph, abort_flag, p.hdr, 32);
+                    if (!ok) break;
+                    if (w == 1 && !two) {
+                        // no rows of this tile: the stages are handed back as they come
+                        mbar_arrive(smem_u32(q_empty));
+                        for (int i = 0; i < 2 * nt && ok; ++i) {
+                            ok = wait_bar(smem_u32(&full[st]), ph, abort_flag, p.hdr, 37);
+                            if (ok) mbar_arrive(smem_u32(&empty[st]));
+                            step();
+                        }
+                        continue;
+                    }
+                    ok = wait_bar(smem_u32(&full[st]), ph, abort_flag, p.hdr, 32);
                     if (!ok) break;
                     tc_fence_after();
-                    for (int w = 0; w < nw; ++w) s_mma(w, st);
-                    tc_commit(smem_u32(&empty[st]));
+                    s_mma(false);
                     if (nt == 1) tc_commit(smem_u32(q_empty));
-                    step(st, ph);
-                    for (int i = 0; i < nt && ok; ++i) {
-                        const int sv = st;              // V of tile i, then K of tile i + 1
-                        ok = wait_bar(smem_u32(&full[sv]), ph, abort_flag, p.hdr, 33);
+                    step();
+                    for (int i = 0; i < nt; ++i) {
+                        ok = wait_bar(smem_u32(&full[st]), ph, abort_flag, p.hdr, 33) &&
+                             wait_bar(smem_u32(&p_full[w]), ph_p, abort_flag, p.hdr, 34) &&
+                             (!two || wait_bar(smem_u32(&turn[w]), ph_t, abort_flag, p.hdr, 38));
+                        ph_p ^= 1;
+                        if (two) ph_t ^= 1;
                         if (!ok) break;
-                        step(st, ph);
-                        for (int w = 0; w < nw; ++w) {
-                            ok = wait_bar(smem_u32(&p_full[w]), (ph_p >> w) & 1, abort_flag, p.hdr, 34);
-                            ph_p ^= 1u << w;
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint64_t b = smem_desc_mn(ring + sv * L::kTileBytes);
+                        tc_fence_after();
+                        const uint64_t b = v_desc + (uint64_t)(st * (L::kTileBytes >> 4));
 #pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)
-                                tc_mma_ts(tmem + L::kO(w), tmem + L::kS(w) + k * 8, b + (uint64_t)((k * 16 * 128) >> 4), kIdO,
-                                          i > 0 || k > 0);
-                            if (i + 1 == nt) {
-                                tc_commit(smem_u32(&o_full[w]));
-                            } else {
-                                if (w == 0) {
-                                    ok = wait_bar(smem_u32(&full[st]), ph, abort_flag, p.hdr, 35);
-                                    if (!ok) break;
-                                    tc_fence_after();
-                                }
-                                s_mma(w, st);
-                            }
+                        for (int k = 0; k < kKeys / 16; ++k)
+                            tc_mma_ts(o_at, s_at + k * 8, b + (uint64_t)((k * 16 * 128) >> 4), kIdO, i > 0 || k > 0);
+                        tc_commit(smem_u32(&empty[st]));
+                        step();
+                        if (i + 1 == nt) {
+                            if (two) mbar_arrive(smem_u32(&turn[1 - w]));
+                            tc_commit(smem_u32(&o_full[w]));
+                            break;
                         }
+                        ok = wait_bar(smem_u32(&full[st]), ph, abort_flag, p.hdr, 35);
                         if (!ok) break;
-                        tc_commit(smem_u32(&empty[sv]));
-                        if (i + 1 < nt) {
-                            tc_commit(smem_u32(&empty[st]));
-                            if (i + 2 == nt) tc_commit(smem_u32(q_empty));
-                            step(st, ph);
-                        }
+                        tc_fence_after();
+                        s_mma(two);
+                        if (i + 2 == nt) tc_commit(smem_u32(q_empty));
+                        step();
                     }
                 }
-                // nothing of this CTA's MMAs is in flight when TMEM is freed
+                // nothing of this thread's MMAs is in flight when TMEM is freed
                 tc_commit(smem_u32(final_bar));
                 const unsigned long long t0 = global_ns();
                 while (!mbar_try_wait_suspend(smem_u32(final_bar), 0, 1000u))
@@ -693,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                     }
             }
             __syncwarp();
-        } else if (warp == 13) {
+        } else if (warp == kTma) {
             // ------------------------------ TMA ------------------------------
             const uint32_t ring = smem_u32(smem + L::kRing), qs = smem_u32(smem + L::kQ);
             const sp_cache& c = p.a.cache;
@@ -773,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 }
             }
             __syncwarp();
-        } else if (warp == 14 && kSame) {
+        } else if (warp == kClean && kSame) {
             // ------------------------------ cleaning of V ------------------------------
             int st = 0;
             uint32_t ph = 0;                    // per stage
@@ -803,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 12)
+    if (warp == kMma)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
@@ -819,12 +845,7 @@ __global__ void __launch_bounds__(kRowsItem) tc_join_kernel(const __grid_constan
     const int64_t u = cut(c, U, P);
     if (u >= U) return;
     const int g = (int)(u / per_head);
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.pre[mid] <= u - g * per_head) lo = mid;
-        else hi = mid - 1;
-    }
+    const int lo = find_item(p, n, u - g * per_head);
     const int64_t begin = g * per_head + p.pre[lo];
     if (u == begin || cut(c - 1, U, P) > begin) return;
     const Item it = p.items[lo];
@@ -915,7 +936,7 @@ sp_status launch(const Maps& maps, const TcArgs& p, cudaStream_t st) {
     SP_CUDA_TRY(cudaFuncSetAttribute(attend_tc_kernel<D, kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
     plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
     SP_LAUNCH_CHECK();
-    sp_status s = launch_early(attend_tc_kernel<D, kKind>, dim3((unsigned)p.P), kThreads, (size_t)kSmem, st, maps, p);
+    sp_status s = launch_early(attend_tc_kernel<D, kKind>, dim3((unsigned)p.P), tc_threads<kKind>(), (size_t)kSmem, st, maps, p);
     if (s != SP_OK || p.P == 1) return s;
     return launch_early(tc_join_kernel<D>, dim3((unsigned)p.P - 1, D / 16), kRowsItem, (size_t)0, st, p);
 }
