@@ -11,14 +11,16 @@
 // The three steps of one tile depend on each other, so the two row tiles take
 // turns: while the softmax of A runs, the tensor cores do P V and the next S of
 // B.  Per 256 x 128 logits the MMAs take 2048 cycles (d = 128) and each
-// softmax warpgroup has as long for its 128 x 128 logits: one thread a row, so
-// that maximum and sum need no exchange between threads.  O stays in TMEM; it
+// softmax half as long for its 128 x 128 logits, from one hand-over to the next:
+// one thread a row, so that maximum and sum need no exchange between threads.  (Two a row were slower, 1.55 ms
+// for 1.40 ms, a chunk of 4096 over 32768: the exponentials are bound by their unit, and the registers did not suffice.)
+// The first 96 weights of a row are handed over before the last 32.  O stays in TMEM; it
 // is scaled only when a row's maximum grows by more than 2^8 over the one it
 // is held by (P is then at most 2^8, and bf16 has the same precision there).
 //
 // Warp roles of a CTA (one per SM):
-//  * warps 0-3, 4-7: softmax of tiles A and B, the scaling of O, and the output;
-//  * four warps, for an 8-bit cache only: convert its rows to bf16 into the
+//  * four warps each for tiles A and B: softmax, the scaling of O, and the output;
+//  * eight warps, for an 8-bit cache only: convert its rows to bf16 into the
 //    shared-memory tiles;
 //  * two warps issue the MMAs of A and B: a thread that issues them is held up
 //    until the tensor cores are nearly done with them, so what it does in between
@@ -44,14 +46,16 @@
 namespace sp {
 namespace {
 
-// Warpgroups: two of softmax, one that converts 8-bit rows (if there are any), one of single-warp roles.
+// Warps of a CTA by role: eight of softmax, for an 8-bit cache eight that convert, and the four single ones.  setmaxnreg shares
+// out the registers that the block was launched with: 384 threads of 168, or 640 of 96.
 template <int kKind>
-constexpr int tc_threads() { return kKind == SP_CACHE_SAME ? 384 : 512; }
-// Registers of a thread in each.  setmaxnreg shares out what the block was launched with: 384 threads of 168 (256 * 216 + 128 *
-// 72), or 512 of 128 (256 * 192 + 128 * 80 + 128 * 48).
-template <int kKind>
-struct Regs {
-    static constexpr int kSoftmax = kKind == SP_CACHE_SAME ? 216 : 192, kConvert = 80, kSingle = kKind == SP_CACHE_SAME ? 72 : 48;
+struct Roles {
+    static constexpr bool kSame = kKind == SP_CACHE_SAME;
+    static constexpr int kSoftmax = 8, kMma = kSame ? 8 : 16, kTma = kMma + 2, kClean = kMma + 3;
+    static constexpr int kThreads = 32 * (kMma + 4);
+    static constexpr int kSoftmaxRegs = kSame ? 216 : 168, kConvertRegs = 48, kSingleRegs = kSame ? 72 : 48;
+    static_assert(kSoftmax * kSoftmaxRegs + (kMma - kSoftmax) * kConvertRegs + 4 * kSingleRegs <= (kMma + 4) * (kSame ? 168 : 96),
+                  "the roles' registers");
 };
 constexpr int kRowsItem = 256;
 constexpr int kKeys = 128;              // keys of a tile
@@ -194,6 +198,7 @@ __device__ __forceinline__ int find_item(const TcArgs& p, int n, int64_t r) {
 struct Walk {
     int left, n, i, g, from;        // tiles left; items of a head; the next item, its head and first tile
 
+    Walk() = default;
     __device__ __forceinline__ Walk(const TcArgs& p, int c) {
         n = *p.n_items;
         const int64_t per_head = p.pre[n], U = per_head * p.a.cache.H_kv;
@@ -218,6 +223,11 @@ struct Walk {
         if (++i == n) i = 0, ++g;
         return true;
     }
+};
+
+struct Kept {
+    Walk walk;
+    Segment sg;
 };
 
 __device__ __forceinline__ int tile_of(const Segment& s, int x) { return s.it.lo + s.it.tiles - 1 - x; }
@@ -262,29 +272,6 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
 // For a warp whose lanes go on together.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, WsHeader* hdr, int where) {
     return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, hdr, where));
-}
-
-// A from TMEM.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
 }
 
 #define TMEM_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
@@ -341,25 +328,106 @@ __device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
         : "+f"(a), "+f"(b) : "f"(x), "f"(y));
 }
 
+// The largest of a thread's logits and mx, in four chains.
+template <int N>
+__device__ __forceinline__ void max_cols(const float* v, float (&mx)[4]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx[c] = fmax3(mx[c], v[i + 2 * c], v[i + 2 * c + 1]);
+}
+
+// Weights 2^(f v - m) (nm = -m) of 32 logits as pairs of bf16, and their sums.
+__device__ __forceinline__ void weights32(const float* v, float f, float nm, float (&zs)[4], uint32_t* pk) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        float a = v[i], b = v[i + 1];
+        fma2(a, b, f, nm);
+        a = ex2_approx(a);
+        b = ex2_approx(b);
+        add2(zs[i & 2], zs[(i & 2) + 1], a, b);
+        pk[i >> 1] = pack_bf16(a, b);
+    }
+}
+
+// Scales this thread's row of O.
+template <int D>
+__device__ __forceinline__ void scale_o(uint32_t o_at, float a) {
+#pragma unroll 1
+    for (int c = 0; c < D / 16; ++c) {
+        uint32_t ov[16];
+        tmem_ld16(o_at + 16 * c, ov);
+        tmem_wait16(ov);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * a);
+        tmem_st16(o_at + 16 * c, ov);
+    }
+}
+
+// A warp's TMEM stores are done: tells the MMAs.
+__device__ __forceinline__ void hand_over(uint64_t* bar) {
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(bar));
+}
+
+// Takes out the columns from `first` on that the row does not see.
+template <int N>
+__device__ __forceinline__ void mask_cols(float* v, int first, int hi, int lo) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (first + i > hi || first + i < lo) v[i] = -INFINITY;
+}
+
+// A from TMEM.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
 template <int D>
 struct Layout {
     static constexpr int kChunks = D / 64;                      // 128-byte column blocks of a row
     static constexpr int kTileBytes = kKeys * D * 2;            // a tile of Q, K or V
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr int kQ = 0, kRing = 2 * kTileBytes, kBars = kRing + kStages * kTileBytes;
+    static constexpr int kKeep = kBars + 8 * (3 * kStages + 14), kEnd = kKeep + 8 * (int)sizeof(Kept);
+    static_assert(kEnd <= kSmem, "");
     // TMEM columns
     static constexpr int kS(int w) { return w * 128; }
     static constexpr int kO(int w) { return 256 + w * D; }
 };
 
 template <int D, int kKind>
-__global__ void __launch_bounds__(tc_threads<kKind>(), 1) attend_tc_kernel(const __grid_constant__ Maps maps,
+__global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(const __grid_constant__ Maps maps,
                                                                 const __grid_constant__ TcArgs p) {
     using L = Layout<D>;
     constexpr bool kSame = kKind == SP_CACHE_SAME;
     constexpr int NS = L::kStages;
-    extern __shared__ uint8_t raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t raw[];
+    uint8_t* smem = raw;
+    if (smem_u32(smem) & 1023) {            // the swizzle goes by addresses: not met, as there is no other shared memory
+        if (threadIdx.x == 0) record_error(p.hdr, SP_EDEVICE, 9);
+        return;
+    }
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
     uint64_t* full = bars;                  // [NS] a K or V tile is ready
     uint64_t* empty = full + NS;            // [NS] the MMAs have read it
@@ -367,18 +435,20 @@ __global__ void __launch_bounds__(tc_threads<kKind>(), 1) attend_tc_kernel(const
     uint64_t* q_full = landed + NS;
     uint64_t* q_empty = q_full + 1;
     uint64_t* s_full = q_empty + 1;         // [2] S is in TMEM (and all earlier P V done)
-    uint64_t* p_full = s_full + 2;          // [2] P is in TMEM, O is scaled
-    uint64_t* o_full = p_full + 2;          // [2] O is final
+    uint64_t* p_full = s_full + 2;          // [2][2] P's first 96 columns are in TMEM and O is scaled; all of P is
+    uint64_t* o_full = p_full + 4;          // [2] O is final
     uint64_t* turn = o_full + 2;            // [2] this row tile's MMAs may be issued
     uint64_t* final_bar = turn + 2;
     volatile uint32_t* tmem_sh = reinterpret_cast<volatile uint32_t*>(final_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_sh + 1);
+    Kept* keep = reinterpret_cast<Kept*>(smem + L::kKeep);      // [8] a softmax warp's place in its run
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kMma = kSame ? 8 : 12, kTma = kMma + 2, kClean = kMma + 3;     // the single-warp roles
+    using W = Roles<kKind>;
+    constexpr int kMma = W::kMma, kTma = W::kTma, kClean = W::kClean;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(smem_u32(&full[i]), kSame ? 1 : 4);
+            mbar_init(smem_u32(&full[i]), kSame ? 1 : W::kMma - W::kSoftmax);
             mbar_init(smem_u32(&empty[i]), 2);          // the two MMA warps
             mbar_init(smem_u32(&landed[i]), 1);
         }
@@ -386,7 +456,8 @@ __global__ void __launch_bounds__(tc_threads<kKind>(), 1) attend_tc_kernel(const
         mbar_init(smem_u32(q_empty), 2);
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_u32(&s_full[w]), 1);
-            mbar_init(smem_u32(&p_full[w]), 4);
+            mbar_init(smem_u32(&p_full[2 * w]), 4);
+            mbar_init(smem_u32(&p_full[2 * w + 1]), 4);
             mbar_init(smem_u32(&o_full[w]), 1);
             mbar_init(smem_u32(&turn[w]), 1);
         }
@@ -410,103 +481,112 @@ __global__ void __launch_bounds__(tc_threads<kKind>(), 1) attend_tc_kernel(const
     Segment sg;
     const int rows_tile = p.G * p.tpt;
 
-    if (warp < 8) {
+    if (warp < W::kSoftmax) {
         // ------------------------------ softmax and output ------------------------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<kKind>::kSoftmax));
-        const int w = warp >> 2, row = (warp & 3) * 32 + lane;          // row tile; row = TMEM lane
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(W::kSoftmaxRegs));
+        const int w = warp >> 2, row = (warp & 3) * 32 + lane;             // row tile; row = TMEM lane
         const uint32_t lane_at = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lane_at + L::kS(w), o_at = tmem + lane_at + L::kO(w);
-        const int t_row = row / p.G, h_row = row - t_row * p.G;
         const float f = p.a.scale * 1.4426950408889634f;
         uint32_t ph = 0, ph_o = 0;
         bool ok = true;
         while (ok && walk.next(p, sg)) {
             if (w == 1 && !two_tiles(p, sg)) continue;
-            const int t = sg.it.t0 + w * p.tpt + t_row;                  // this row's new token
-            const bool real = row < rows_tile && t < sg.s.n;
-            const int pos = real ? sg.s.kv - sg.s.n + t : -1;
-            // places of the tile's first and last rows, for whether a key tile needs a mask at all
+            // What the loop over the keys does not need stays in shared memory meanwhile: 128 logits take most of the registers
+            if (lane == 0) keep[warp] = Kept{walk, sg};
+            __syncwarp();
+            // places of the tile's first and last rows, for whether a key tile needs a mask at all, and of this one
             const int p_first = sg.s.kv - sg.s.n + sg.it.t0 + w * p.tpt;
             const int p_last = sg.s.kv - sg.s.n + min(sg.s.n, sg.it.t0 + (w + 1) * p.tpt) - 1;
-            float m = -INFINITY, z = 0.f;
-            for (int x = sg.from; x < sg.to; ++x) {
-                const int base = tile_of(sg, x) * kKeys;
+            const int pos = row < rows_tile ? min(p_first + row / p.G, p_last) : -1;
+            // z and O are sums of 2^(logit - m).  m is the row's maximum as it was some tiles ago: a tile's weights are worked out by
+            // it while its maximum is still being looked for, and m follows before the next tile if that is more than 2^8 above.
+            // Only if it is more than 2^24 above (or the row has no m yet) is the tile done again.
+            float m = -INFINITY, z = 0.f, next_m = -INFINITY;
+            bool follow = false;
+            const int n_tiles = sg.to - sg.from;
+            int base = tile_of(sg, sg.from) * kKeys;
+            for (int x = 0; x < n_tiles; ++x, base -= kKeys) {
                 ok = wait_warp(smem_u32(&s_full[w]), ph, abort_flag, p.hdr, 21);
                 ph ^= 1;
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t sr[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, sr + 32 * c);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_wait32(sr + 32 * c);
-                float* sv = reinterpret_cast<float*>(sr);
-                if (base + kKeys - 1 > p_first || (p.a.window && base <= p_last - p.a.window)) {
-                    const int hi = pos - base, lo = p.a.window ? hi - p.a.window + 1 : -1;      // columns this row sees
-#pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        if (i > hi || i < lo) sv[i] = -INFINITY;
-                }
-                float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
-#pragma unroll
-                for (int i = 4; i < 124; i += 8)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) mx[c] = fmax3(mx[c], sv[i + 2 * c], sv[i + 2 * c + 1]);
-                mx[0] = fmax3(mx[0], sv[124], sv[125]);
-                mx[1] = fmax3(mx[1], sv[126], sv[127]);
-                const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * f;
-                // f > 0, so the largest logit is f times the largest product
-                const bool grows = m != -INFINITY && top > m + 8.f;
-                if (__any_sync(0xffffffffu, grows)) {
-                    const float a = grows ? ex2_approx(m - top) : 1.f;
-                    if (grows) m = top;
+                const bool masked = base + kKeys - 1 > p_first || (p.a.window && base <= p_last - p.a.window);
+                const int hi = pos - base, lo = p.a.window ? hi - p.a.window + 1 : -1;      // columns this row sees
+                if (follow) {
+                    const float a = next_m > m ? ex2_approx(m - next_m) : 1.f;
+                    m = next_m;
                     z *= a;
-#pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint32_t ov[16];
-                        tmem_ld16(o_at + 16 * c, ov);
-                        tmem_wait16(ov);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * a);
-                        tmem_st16(o_at + 16 * c, ov);
-                    }
+                    scale_o<D>(o_at, a);
                 }
-                if (m == -INFINITY) m = top;            // nothing summed so far
-                const float nm = m == -INFINITY ? 0.f : -m;
-                float zs[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t sr[kSame ? 128 : 32], pk[48];
+                float* sv = reinterpret_cast<float*>(sr);
+                float nm, top, zs[4];
+                for (;;) {
+                    nm = m == -INFINITY ? 0.f : -m;
+                    zs[0] = zs[1] = zs[2] = zs[3] = 0.f;
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    if constexpr (kSame) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
+                        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, sr + 32 * c);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        float a = sv[32 * c + i], b = sv[32 * c + i + 1];
-                        fma2(a, b, f, nm);
-                        a = ex2_approx(a);
-                        b = ex2_approx(b);
-                        add2(zs[(i & 2)], zs[(i & 2) + 1], a, b);
-                        pk[i >> 1] = pack_bf16(a, b);
+                        for (int c = 0; c < 4; ++c) tmem_wait32(sr + 32 * c);
+                        if (masked) mask_cols<128>(sv, 0, hi, lo);
+                        max_cols<32>(sv + 96, mx);
                     }
-                    tmem_st16(s_at + 16 * c, pk);
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) {
+                        float* v = kSame ? sv + 32 * c : sv;
+                        if constexpr (!kSame) {
+                            tmem_ld32(s_at + 32 * c, sr);
+                            tmem_wait32(sr);
+                            if (masked) mask_cols<32>(sv, 32 * c, hi, lo);
+                        }
+                        max_cols<32>(v, mx);
+                        weights32(v, f, nm, zs, pk + 16 * c);
+                    }
+                    if constexpr (!kSame) {
+                        tmem_ld32(s_at + 96, sr);
+                        tmem_wait32(sr);
+                        if (masked) mask_cols<32>(sv, 96, hi, lo);
+                        max_cols<32>(sv, mx);
+                    }
+                    top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * f;     // f > 0: f times the largest product
+                    const bool lost = pos >= 0 && (m == -INFINITY ? top > -INFINITY : top > m + 24.f);
+                    if (!__any_sync(0xffffffffu, lost)) break;
+                    const float a = lost && m != -INFINITY ? ex2_approx(m - top) : 1.f;
+                    if (__any_sync(0xffffffffu, a != 1.f)) scale_o<D>(o_at, a);
+                    z *= a;
+                    if (lost) m = top;
                 }
+#pragma unroll
+                for (int c = 0; c < 3; ++c) tmem_st16(s_at + 16 * c, pk + 16 * c);
+                hand_over(&p_full[2 * w]);          // 96 keys' weights, then the last 32: the product with V begins meanwhile
+                weights32(kSame ? sv + 96 : sv, f, nm, zs, pk);
+                tmem_st16(s_at + 48, pk);
+                hand_over(&p_full[2 * w + 1]);
                 z += (zs[0] + zs[1]) + (zs[2] + zs[3]);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&p_full[w]));
+                const bool grows = pos >= 0 && top > m + 8.f;
+                next_m = grows ? top : m;
+                follow = __any_sync(0xffffffffu, grows);
             }
             if (!ok) break;
             ok = wait_warp(smem_u32(&o_full[w]), ph_o, abort_flag, p.hdr, 22);
             ph_o ^= 1;
             if (!ok) break;
             tc_fence_after();
+            walk = keep[warp].walk;
+            sg = keep[warp].sg;
+            const int t_row = row / p.G, t = sg.it.t0 + w * p.tpt + t_row;      // this row's new token
+            const bool real = row < rows_tile && t < sg.s.n;
             const bool whole = sg.from == 0 && sg.to == sg.it.tiles;
             const float inv = z == 0.f ? 0.f : 1.f / z;
             const int64_t r = sg.s.row0 + t;
-            const int h = sg.g * p.G + h_row;
+            const int h = sg.g * p.G + row - t_row * p.G;
             __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.a.out.data) + r * p.a.out.stride_row + h * p.a.out.stride_head;
             const int64_t slot = (int64_t)blockIdx.x * 2 + (sg.from == 0 ? 1 : 0);
             float* po = p.part_o + slot * kRowsItem * D + (w * 128 + row) * 4;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t ov[32];
                 tmem_ld32(o_at + 32 * c, ov);
@@ -536,17 +616,18 @@ __global__ void __launch_bounds__(tc_threads<kKind>(), 1) attend_tc_kernel(const
                 p.part_ml[slot * kRowsItem + w * 128 + row] = make_float2(m, z);
             }
             tc_fence_before();          // O is read before this thread's next hand-off of P
+            __syncwarp();               // and `keep` by all lanes
         }
-    } else if (!kSame && warp < 12) {
+    } else if (!kSame && warp < kMma) {
       if constexpr (!kSame) {
         // ------------------------------ conversion of 8-bit rows ------------------------------
-        // A warp takes 32 rows of each tile; a lane 16 entries of a row, so that a row's lanes read it whole.  A
+        // A warp takes 16 rows of each tile; a lane 16 entries of a row, so that a row's lanes read it whole.  A
         // piece is requested for the next tile as soon as it is converted for this one.
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kKind>::kConvert));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kConvertRegs));
         {
-            constexpr int kLanes = D / 16, kPass = kLanes;              // lanes of a row; rows of a warp / rows at a time
+            constexpr int kLanes = D / 16, kPass = kLanes / 2;          // lanes of a row; times to have 16 rows
             const sp_cache& c = p.a.cache;
-            const int r0 = (warp - 8) * 32, lp = lane % kLanes, rl = lane / kLanes;
+            const int r0 = (warp - W::kSoftmax) * 16, lp = lane % kLanes, rl = lane / kLanes;
             const uint32_t swap = D == 128 ? (lp >> 2) & 1 : 0;        // the two column blocks' stores take other banks
             int st = 0;
             uint32_t ph = 1;
@@ -560,12 +641,12 @@ __global__ void __launch_bounds__(tc_threads<kKind>(), 1) attend_tc_kernel(const
                     uint32_t ks, vs;
                 };
                 auto page_of = [&](int x) {
-                    const int tok = tile_of(sg, x) * kKeys + r0 + lane;
+                    const int tok = tile_of(sg, x) * kKeys + r0 + (lane & 15);
                     return tok < sg.s.kv && tok >= seen ? table[(unsigned)tok / (unsigned)c.page] : -1;
                 };
                 auto place = [&](int x, int pg) {
                     Where w{-1, 0x3f803f80u, 0x3f803f80u};
-                    const int tok = tile_of(sg, x) * kKeys + r0 + lane;
+                    const int tok = tile_of(sg, x) * kKeys + r0 + (lane & 15);
                     if (tok >= sg.s.kv || tok < seen) return w;
                     if ((unsigned)pg >= (unsigned)c.pages) {
                         record_error(p.hdr, SP_EDEVICE, 2);
@@ -633,7 +714,7 @@ __global__ void __launch_bounds__(tc_threads<kKind>(), 1) attend_tc_kernel(const
         }
       }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kKind>::kSingle));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kSingleRegs));
         if (warp == kMma || warp == kMma + 1) {
             // ------------------------------ MMAs of one row tile ------------------------------
             if (lane == 0) {
@@ -655,8 +736,9 @@ __global__ void __launch_bounds__(tc_threads<kKind>(), 1) attend_tc_kernel(const
                     for (int k = 0; k < D / 16; ++k) {
                         const uint64_t off = (uint64_t)(((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4);
                         tc_mma(s_at, q_desc + off, b + off, kIdS, k > 0);
+                        // the other warp needs about as long to see it as the rest of these take
+                        if (k == D / 16 - 3 && hand_on) mbar_arrive(smem_u32(&turn[1 - w]));
                     }
-                    if (hand_on) mbar_arrive(smem_u32(&turn[1 - w]));
                     tc_commit(smem_u32(&s_full[w]));
                     tc_commit(smem_u32(&empty[st]));
                 };
@@ -683,17 +765,25 @@ __global__ void __launch_bounds__(tc_threads<kKind>(), 1) attend_tc_kernel(const
                     if (nt == 1) tc_commit(smem_u32(q_empty));
                     step();
                     for (int i = 0; i < nt; ++i) {
+                        const int sk = st + 1 == NS ? 0 : st + 1;       // the next K tile's stage
                         ok = wait_bar(smem_u32(&full[st]), ph, abort_flag, p.hdr, 33) &&
-                             wait_bar(smem_u32(&p_full[w]), ph_p, abort_flag, p.hdr, 34) &&
+                             (i + 1 == nt || wait_bar(smem_u32(&full[sk]), ph ^ (sk == 0), abort_flag, p.hdr, 35)) &&
+                             wait_bar(smem_u32(&p_full[2 * w]), ph_p, abort_flag, p.hdr, 34) &&
                              (!two || wait_bar(smem_u32(&turn[w]), ph_t, abort_flag, p.hdr, 38));
-                        ph_p ^= 1;
                         if (two) ph_t ^= 1;
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t b = v_desc + (uint64_t)(st * (L::kTileBytes >> 4));
 #pragma unroll
-                        for (int k = 0; k < kKeys / 16; ++k)
+                        for (int k = 0; k < 6; ++k)
                             tc_mma_ts(o_at, s_at + k * 8, b + (uint64_t)((k * 16 * 128) >> 4), kIdO, i > 0 || k > 0);
+                        ok = wait_bar(smem_u32(&p_full[2 * w + 1]), ph_p, abort_flag, p.hdr, 39);
+                        ph_p ^= 1;
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 6; k < 8; ++k)
+                            tc_mma_ts(o_at, s_at + k * 8, b + (uint64_t)((k * 16 * 128) >> 4), kIdO, 1);
                         tc_commit(smem_u32(&empty[st]));
                         step();
                         if (i + 1 == nt) {
@@ -701,9 +791,6 @@ __global__ void __launch_bounds__(tc_threads<kKind>(), 1) attend_tc_kernel(const
                             tc_commit(smem_u32(&o_full[w]));
                             break;
                         }
-                        ok = wait_bar(smem_u32(&full[st]), ph, abort_flag, p.hdr, 35);
-                        if (!ok) break;
-                        tc_fence_after();
                         s_mma(two);
                         if (i + 2 == nt) tc_commit(smem_u32(q_empty));
                         step();
@@ -936,7 +1023,7 @@ sp_status launch(const Maps& maps, const TcArgs& p, cudaStream_t st) {
     SP_CUDA_TRY(cudaFuncSetAttribute(attend_tc_kernel<D, kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
     plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
     SP_LAUNCH_CHECK();
-    sp_status s = launch_early(attend_tc_kernel<D, kKind>, dim3((unsigned)p.P), tc_threads<kKind>(), (size_t)kSmem, st, maps, p);
+    sp_status s = launch_early(attend_tc_kernel<D, kKind>, dim3((unsigned)p.P), Roles<kKind>::kThreads, (size_t)kSmem, st, maps, p);
     if (s != SP_OK || p.P == 1) return s;
     return launch_early(tc_join_kernel<D>, dim3((unsigned)p.P - 1, D / 16), kRowsItem, (size_t)0, st, p);
 }
