@@ -380,13 +380,44 @@ __device__ __forceinline__ void mask_cols(float* v, int first, int hi, int lo) {
         if (first + i > hi || first + i < lo) v[i] = -INFINITY;
 }
 
-// A from TMEM.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The MMA warps run with all lanes and issue from one (`lead`): descriptors, addresses and loop counters are then warp-uniform for
+// the compiler, which keeps them in uniform registers.  Issued from inside `if (lane == 0)`, an MMA took so many instructions
+// that the softmax warps beside it on the scheduler held the tensor cores up (chunk of 4096 over 32768: 1.35 ms).
+// A descriptor's upper half is constant, its lower half an address that no stage carries out of.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ void mma_ss(bool lead, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}\n"
+        ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)acc), "r"((uint32_t)lead)
+        : "memory");
+}
+// A from TMEM.
+__device__ __forceinline__ void mma_ts(bool lead, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}\n"
+        ::"r"(d), "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)acc), "r"((uint32_t)lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(bool lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar), "r"((uint32_t)lead)
+        : "memory");
+}
+__device__ __forceinline__ void arrive_if(bool lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}\n" ::"r"(bar), "r"((uint32_t)lead)
         : "memory");
 }
 
@@ -717,87 +748,92 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kSingleRegs));
         if (warp == kMma || warp == kMma + 1) {
             // ------------------------------ MMAs of one row tile ------------------------------
-            if (lane == 0) {
-                constexpr uint32_t kIdS = instr_desc(kKeys, false), kIdO = instr_desc(D, true);
-                const int w = warp - kMma;
-                const uint32_t s_at = tmem + L::kS(w), o_at = tmem + L::kO(w);
-                const uint32_t ring = smem_u32(smem + L::kRing);
-                const uint64_t q_desc = smem_desc(smem_u32(smem + L::kQ) + w * L::kTileBytes);
-                const uint64_t k_desc = smem_desc(ring), v_desc = smem_desc_mn(ring);
-                int st = 0;
-                uint32_t ph = 0, ph_q = 0, ph_p = 0, ph_t = 1 - w;     // the first turn is A's
-                bool ok = true;
-                auto step = [&] {
-                    if (++st == NS) st = 0, ph ^= 1;
-                };
-                auto s_mma = [&](bool hand_on) {
-                    const uint64_t b = k_desc + (uint64_t)(st * (L::kTileBytes >> 4));
+            constexpr uint32_t kIdS = instr_desc(kKeys, false), kIdO = instr_desc(D, true);
+            const int w = __shfl_sync(0xffffffffu, warp - kMma, 0);
+            const bool lead = elect_one();
+            const uint32_t s_at = L::kS(0) + w * 128, o_at = L::kO(0) + w * D;      // all of TMEM is this CTA's: it begins at 0
+            const uint32_t ring = smem_u32(smem + L::kRing);
+            const uint64_t q_desc = smem_desc(smem_u32(smem + L::kQ)), k_desc = smem_desc(ring), v_desc = smem_desc_mn(ring);
+            const uint32_t q_lo = (uint32_t)q_desc + w * (L::kTileBytes >> 4), k_lo = (uint32_t)k_desc, v_lo = (uint32_t)v_desc;
+            const uint32_t s_hi = (uint32_t)(k_desc >> 32), v_hi = (uint32_t)(v_desc >> 32);
+            const uint32_t full_at = smem_u32(full), empty_at = smem_u32(empty), s_bar = smem_u32(s_full) + 8 * w,
+                           p_bar = smem_u32(p_full) + 16 * w, o_bar = smem_u32(o_full) + 8 * w, my_turn = smem_u32(turn) + 8 * w,
+                           other_turn = smem_u32(turn) + 8 * (1 - w);
+            int st = 0;
+            uint32_t ph = 0, ph_q = 0, ph_p = 0, ph_t = 1 - w;     // the first turn is A's
+            bool ok = tmem == 0;
+            auto wait = [&](uint32_t bar, uint32_t parity, int where) { return wait_warp(bar, parity, abort_flag, p.hdr, where); };
+            auto step = [&] {
+                if (++st == NS) st = 0, ph ^= 1;
+            };
+            auto s_mma = [&](bool hand_on) {
+                const uint32_t b = k_lo + st * (L::kTileBytes >> 4);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t off = (uint64_t)(((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4);
-                        tc_mma(s_at, q_desc + off, b + off, kIdS, k > 0);
-                        // the other warp needs about as long to see it as the rest of these take
-                        if (k == D / 16 - 3 && hand_on) mbar_arrive(smem_u32(&turn[1 - w]));
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
+                    mma_ss(lead, s_at, q_lo + off, b + off, s_hi, kIdS, k > 0);
+                    // the other warp needs about as long to see it as the rest of these take
+                    if (k == D / 16 - 3 && hand_on) arrive_if(lead, other_turn);
+                }
+                commit_if(lead, s_bar);
+                commit_if(lead, empty_at + 8 * st);
+            };
+            while (ok && walk.next(p, sg)) {
+                const int nt = sg.to - sg.from;
+                const bool two = two_tiles(p, sg);
+                ok = wait(smem_u32(q_full), ph_q, 31);
+                ph_q ^= 1;
+                if (!ok) break;
+                if (w == 1 && !two) {
+                    // no rows of this tile: the stages are handed back as they come
+                    arrive_if(lead, smem_u32(q_empty));
+                    for (int i = 0; i < 2 * nt && ok; ++i) {
+                        ok = wait(full_at + 8 * st, ph, 37);
+                        if (ok) arrive_if(lead, empty_at + 8 * st);
+                        step();
                     }
-                    tc_commit(smem_u32(&s_full[w]));
-                    tc_commit(smem_u32(&empty[st]));
-                };
-                while (ok && walk.next(p, sg)) {
-                    const int nt = sg.to - sg.from;
-                    const bool two = two_tiles(p, sg);
-                    ok = wait_bar(smem_u32(q_full), ph_q, abort_flag, p.hdr, 31);
-                    ph_q ^= 1;
-                    if (!ok) break;
-                    if (w == 1 && !two) {
-                        // no rows of this tile: the stages are handed back as they come
-                        mbar_arrive(smem_u32(q_empty));
-                        for (int i = 0; i < 2 * nt && ok; ++i) {
-                            ok = wait_bar(smem_u32(&full[st]), ph, abort_flag, p.hdr, 37);
-                            if (ok) mbar_arrive(smem_u32(&empty[st]));
-                            step();
-                        }
-                        continue;
-                    }
-                    ok = wait_bar(smem_u32(&full[st]), ph, abort_flag, p.hdr, 32);
+                    continue;
+                }
+                ok = wait(full_at + 8 * st, ph, 32);
+                if (!ok) break;
+                tc_fence_after();
+                s_mma(false);
+                if (nt == 1) commit_if(lead, smem_u32(q_empty));
+                step();
+                for (int i = 0; i < nt; ++i) {
+                    const int sk = st + 1 == NS ? 0 : st + 1;       // the next K tile's stage
+                    ok = wait(full_at + 8 * st, ph, 33) && (i + 1 == nt || wait(full_at + 8 * sk, ph ^ (sk == 0), 35)) &&
+                         wait(p_bar, ph_p, 34) && (!two || wait(my_turn, ph_t, 38));
+                    if (two) ph_t ^= 1;
                     if (!ok) break;
                     tc_fence_after();
-                    s_mma(false);
-                    if (nt == 1) tc_commit(smem_u32(q_empty));
+                    const uint32_t b = v_lo + st * (L::kTileBytes >> 4);
+#pragma unroll
+                    for (int k = 0; k < 6; ++k)
+                        mma_ts(lead, o_at, s_at + k * 8, b + ((k * 16 * 128) >> 4), v_hi, kIdO, i > 0 || k > 0);
+                    ok = wait(p_bar + 8, ph_p, 39);
+                    ph_p ^= 1;
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 6; k < 8; ++k) mma_ts(lead, o_at, s_at + k * 8, b + ((k * 16 * 128) >> 4), v_hi, kIdO, true);
+                    commit_if(lead, empty_at + 8 * st);
                     step();
-                    for (int i = 0; i < nt; ++i) {
-                        const int sk = st + 1 == NS ? 0 : st + 1;       // the next K tile's stage
-                        ok = wait_bar(smem_u32(&full[st]), ph, abort_flag, p.hdr, 33) &&
-                             (i + 1 == nt || wait_bar(smem_u32(&full[sk]), ph ^ (sk == 0), abort_flag, p.hdr, 35)) &&
-                             wait_bar(smem_u32(&p_full[2 * w]), ph_p, abort_flag, p.hdr, 34) &&
-                             (!two || wait_bar(smem_u32(&turn[w]), ph_t, abort_flag, p.hdr, 38));
-                        if (two) ph_t ^= 1;
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t b = v_desc + (uint64_t)(st * (L::kTileBytes >> 4));
-#pragma unroll
-                        for (int k = 0; k < 6; ++k)
-                            tc_mma_ts(o_at, s_at + k * 8, b + (uint64_t)((k * 16 * 128) >> 4), kIdO, i > 0 || k > 0);
-                        ok = wait_bar(smem_u32(&p_full[2 * w + 1]), ph_p, abort_flag, p.hdr, 39);
-                        ph_p ^= 1;
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int k = 6; k < 8; ++k)
-                            tc_mma_ts(o_at, s_at + k * 8, b + (uint64_t)((k * 16 * 128) >> 4), kIdO, 1);
-                        tc_commit(smem_u32(&empty[st]));
-                        step();
-                        if (i + 1 == nt) {
-                            if (two) mbar_arrive(smem_u32(&turn[1 - w]));
-                            tc_commit(smem_u32(&o_full[w]));
-                            break;
-                        }
-                        s_mma(two);
-                        if (i + 2 == nt) tc_commit(smem_u32(q_empty));
-                        step();
+                    if (i + 1 == nt) {
+                        if (two) arrive_if(lead, other_turn);
+                        commit_if(lead, o_bar);
+                        break;
                     }
+                    s_mma(two);
+                    if (i + 2 == nt) commit_if(lead, smem_u32(q_empty));
+                    step();
                 }
-                // nothing of this thread's MMAs is in flight when TMEM is freed
-                tc_commit(smem_u32(final_bar));
+            }
+            if (tmem != 0 && lead) record_error(p.hdr, SP_EDEVICE, 8);
+            // nothing of this warp's MMAs is in flight when TMEM is freed
+            commit_if(lead, smem_u32(final_bar));
+            if (lead) {
+                if (!ok) *abort_flag = 1;
                 const unsigned long long t0 = global_ns();
                 while (!mbar_try_wait_suspend(smem_u32(final_bar), 0, 1000u))
                     if (global_ns() - t0 > kTimeoutNs) {
