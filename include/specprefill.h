@@ -450,8 +450,8 @@ sp_status sp_cache_read(const sp_cache* cache, const sp_batch* batch, const sp_r
                         void* ws, size_t ws_bytes, void* stream);
 
 /* Workspace bytes sp_attend needs for this cache, batch and number of query
- * heads on the current device (0 if they are invalid).  Depends on T, max_new,
- * B, H, H_kv and d, not on the contents of the batch's device arrays. */
+ * heads on the current device (0 if they are invalid).  Does not depend on the
+ * contents of the batch's device arrays. */
 size_t sp_attend_workspace_size(const sp_cache* cache, const sp_batch* batch, int H);
 
 /* Causal attention of the new tokens over their sequences' cached tokens (the

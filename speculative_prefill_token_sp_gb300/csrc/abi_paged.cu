@@ -23,9 +23,9 @@ sp_status attend_general_launch(const AttendProblem& p, void* ws, cudaStream_t s
 bool attend_step_supported(const sp_cache& c);
 size_t attend_step_ws_bytes(const sp_cache& c);
 sp_status attend_step_launch(const AttendProblem& p, void* ws, cudaStream_t st);
-bool attend_tc_supported(const sp_cache& c, int G);
-size_t attend_tc_ws_bytes(const sp_cache& c, const sp_batch& b, int G);
-sp_status attend_tc_launch(const AttendProblem& p, int min_rows, void* ws, cudaStream_t st);
+bool attend_tc_supported(const sp_cache& c, const sp_batch& b, int G);
+size_t attend_tc_ws_bytes(const sp_cache& c);
+sp_status attend_tc_launch(const AttendProblem& p, int min_rows, void* ws, size_t offset, cudaStream_t st);
 
 namespace {
 
@@ -80,15 +80,15 @@ Path path_of(const sp_cache& c, const sp_batch& b, int H) {
     const int G = H / c.H_kv;
     const bool step = attend_step_supported(c);
     if (step && (int64_t)b.max_new * G <= 16) return kStep;
-    if (!attend_tc_supported(c, G)) return kGeneral;
+    if (!attend_tc_supported(c, b, G)) return kGeneral;
     return step && b.B > 1 ? kMixed : kChunks;
 }
 
-size_t path_bytes(Path path, const sp_cache& c, const sp_batch& b, int H) {
+size_t path_bytes(Path path, const sp_cache& c) {
     switch (path) {
         case kStep: return attend_step_ws_bytes(c);
-        case kChunks: return attend_tc_ws_bytes(c, b, H / c.H_kv);
-        case kMixed: return std::max(attend_step_ws_bytes(c), attend_tc_ws_bytes(c, b, H / c.H_kv));
+        case kChunks: return attend_tc_ws_bytes(c);
+        case kMixed: return attend_step_ws_bytes(c) + attend_tc_ws_bytes(c);
         default: return attend_general_ws_bytes(c);
     }
 }
@@ -287,7 +287,7 @@ size_t sp_attend_workspace_size(const sp_cache* cache, const sp_batch* batch, in
         set_error("%s: H (%d) must be a multiple of H_kv (%d)", fn, H, cache->H_kv);
         return 0;
     }
-    return path_bytes(path_of(*cache, *batch, H), *cache, *batch, H);
+    return path_bytes(path_of(*cache, *batch, H), *cache);
 }
 
 sp_status sp_attend(const sp_rows* q, const sp_cache* cache, const sp_batch* batch, int H, double scale,
@@ -324,10 +324,10 @@ sp_status sp_attend(const sp_rows* q, const sp_cache* cache, const sp_batch* bat
     switch (path_of(*cache, *batch, H)) {
         case kGeneral: s = attend_general_launch(p, ws, st); break;
         case kStep: s = attend_step_launch(p, ws, st); break;
-        case kChunks: s = attend_tc_launch(p, 0, ws, st); break;
+        case kChunks: s = attend_tc_launch(p, 0, ws, 0, st); break;
         case kMixed:
             s = attend_step_launch(p, ws, st);
-            if (s == SP_OK) s = attend_tc_launch(p, 16, ws, st);
+            if (s == SP_OK) s = attend_tc_launch(p, 16, ws, attend_step_ws_bytes(*cache), st);
             break;
     }
     if (s == SP_OK) clear_error();

@@ -498,6 +498,7 @@ __global__ void __launch_bounds__(kJoinThreads) step_join_kernel(const __grid_co
     __shared__ float4 sm_o[kGroups][kLanes];
     __shared__ float2 sm_mz[kJoinThreads / 32];
     bool bad = false;
+    cudaTriggerProgrammaticLaunchCompletion();      // of a mixed batch: the kernel of the other sequences may begin
     const int i = blockIdx.x, b = i / p.a.cache.H_kv, g = i - b * p.a.cache.H_kv, r = blockIdx.y;
     const Seq s = load_seq(p.a.batch, p.a.cache.page, b);
     const bool mine = row_blocks(p, s) > 0 && r < s.n * p.G;

@@ -60,11 +60,17 @@ struct Roles {
 constexpr int kRowsItem = 256;
 constexpr int kKeys = 128;              // keys of a tile
 constexpr int kSmem = 227 * 1024;
-constexpr int kPlanThreads = 1024;
+constexpr int kMaxSeqs = 16384;         // their item counts are laid out in the (still empty) ring of key tiles
 
 struct Item {
     int b, t0;              // sequence, first new token
     int lo, tiles;          // first key tile, number of key tiles (at least 1)
+};
+
+// What the joining kernel has to know of CTA c: whether its run begins inside an item that no CTA before has cut.
+struct Cut {
+    int first, b, g, t0;
+    int last;               // the CTA of the item's last tile
 };
 
 struct TcArgs {
@@ -73,12 +79,9 @@ struct TcArgs {
     int min_rows;           // sequences with at most this many rows per KV head are left to the step kernel
     int P;                  // CTAs
     int box;                // rows of a TMA box
-    int clear;              // 1: the plan clears the status
-    int max_items;
     WsHeader* hdr;
-    int* n_items;           // [1]
-    Item* items;            // [max_items]
-    int64_t* pre;           // [max_items + 1] key tiles before an item, for one KV head
+    int* err;               // [P] what each CTA found wrong: bits 1, 2 as in SplitArgs, 4 a wait that gave up (in bits 8-15)
+    Cut* cuts;              // [P]
     float* part_o;          // [P][2][d / 4][256][4]
     float2* part_ml;        // [P][2][256]
 };
@@ -89,6 +92,10 @@ struct Maps {
 
 __device__ __forceinline__ bool is_tc(const TcArgs& p, const Seq& s) {
     return s.n > 0 && (int64_t)s.n * p.G > p.min_rows;
+}
+
+__device__ __forceinline__ int blocks_of(const TcArgs& p, const Seq& s) {
+    return is_tc(p, s) ? (s.n + 2 * p.tpt - 1) / (2 * p.tpt) : 0;
 }
 
 __device__ __forceinline__ Item item_of(const TcArgs& p, const Seq& s, int b, int qt) {
@@ -102,9 +109,10 @@ __device__ __forceinline__ Item item_of(const TcArgs& p, const Seq& s, int b, in
     return it;
 }
 
-// Inclusive sum over the block's threads.
-__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* warp_sums) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Sum over the block's threads before this one's; `total` over all of them.
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* warp_sums, int64_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t mine = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -112,118 +120,128 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* warp_sums) {
     }
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
-    if (warp == 0) {
-        int64_t w = warp_sums[lane];
+    int64_t w = lane < warps ? warp_sums[lane] : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += y;
-        }
-        warp_sums[lane] = w;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
     }
+    total = __shfl_sync(0xffffffffu, w, 31);
+    const int64_t before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
     __syncthreads();
-    const int64_t r = x + (warp ? warp_sums[warp - 1] : 0);
-    __syncthreads();
-    return r;
-}
-
-// Lists the items (all sequences, one KV head) and their key tiles' running sum.
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ TcArgs p) {
-    __shared__ int64_t sums[32];
-    __shared__ int64_t at_item, at_tile;
-    cudaTriggerProgrammaticLaunchCompletion();
-    if (threadIdx.x == 0) at_item = 0, at_tile = 0;
-    if (threadIdx.x == 0 && p.clear) p.hdr->status = SP_OK, p.hdr->where = 0;
-    __syncthreads();
-    const int tpi = 2 * p.tpt;
-    for (int b0 = 0; b0 < p.a.batch.B; b0 += kPlanThreads) {
-        const int b = b0 + threadIdx.x;
-        int mine = 0;
-        if (b < p.a.batch.B) {
-            const Seq s = load_seq(p.a.batch, p.a.cache.page, b);
-            if (!s.ok) record_error(p.hdr, SP_EDEVICE, 1);
-            if (is_tc(p, s)) mine = (s.n + tpi - 1) / tpi;
-        }
-        const int64_t incl = block_scan(mine, sums);
-        // the order within a sequence is from its last tokens, which see most keys, to its first
-        const int64_t base = at_item + incl - mine;
-        for (int i = 0; i < mine; ++i)
-            if (base + i < p.max_items) p.items[base + i] = Item{b, mine - 1 - i, 0, 0};
-        __syncthreads();
-        if (threadIdx.x == kPlanThreads - 1) at_item += incl;
-        __syncthreads();
-    }
-    const int n = (int)min(at_item, (int64_t)p.max_items);
-    for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
-        const int i = i0 + threadIdx.x;
-        Item it{0, 0, 0, 0};
-        if (i < n) {
-            const Item raw = p.items[i];
-            it = item_of(p, load_seq(p.a.batch, p.a.cache.page, raw.b), raw.b, raw.t0);
-            p.items[i] = it;
-        }
-        const int64_t incl = block_scan(it.tiles, sums);
-        if (i < n) p.pre[i] = at_tile + incl - it.tiles;
-        __syncthreads();
-        if (threadIdx.x == kPlanThreads - 1) at_tile += incl;
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) {
-        p.pre[n] = at_tile;
-        *p.n_items = n;
-    }
+    return x - mine + (warp ? before : 0);
 }
 
 // CTA c takes the key tiles from cut(c) to cut(c + 1) of all U; P is the CTAs, or the tiles if those are fewer.
 __device__ __forceinline__ int64_t cut(int64_t c, int64_t U, int P) { return min(c, (int64_t)P) * U / max(P, 1); }
 
-// A CTA's run of key tiles, item by item.  Every role walks it by itself.
+// A CTA's run of key tiles, item by item: KV head, sequence, row block (from the last tokens, which see most keys, to the first),
+// key tile.  Every role walks it by itself; all lanes of a warp together.
 struct Segment {
     Item it;
     Seq s;
     int g, from, to;        // KV head; tiles [from, to) of the item, counted from its last keys to its first
 };
 
-// The item that holds tile r of a head.
-__device__ __forceinline__ int find_item(const TcArgs& p, int n, int64_t r) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.pre[mid] <= r) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
-
 struct Walk {
-    int left, n, i, g, from;        // tiles left; items of a head; the next item, its head and first tile
+    int left, g, b, qt, from;       // tiles left; the next item and its first tile
 
-    Walk() = default;
-    __device__ __forceinline__ Walk(const TcArgs& p, int c) {
-        n = *p.n_items;
-        const int64_t per_head = p.pre[n], U = per_head * p.a.cache.H_kv;
-        const int P = (int)min((int64_t)p.P, U);
-        const int64_t u = cut(c, U, P);
-        left = (int)(cut(c + 1, U, P) - u);
-        i = g = from = 0;
-        if (left == 0) return;
-        g = (int)(u / per_head);
-        i = find_item(p, n, u - g * per_head);
-        from = (int)(u - g * per_head - p.pre[i]);
-    }
     __device__ __forceinline__ bool next(const TcArgs& p, Segment& o) {
         if (left == 0) return false;
-        o.it = p.items[i];
-        o.s = load_seq(p.a.batch, p.a.cache.page, o.it.b);
+        o.s = load_seq(p.a.batch, p.a.cache.page, b);
+        o.it = item_of(p, o.s, b, qt);
         o.g = g;
         o.from = from;
         o.to = min(o.it.tiles, from + left);
         left -= o.to - from;
         from = 0;
-        if (++i == n) i = 0, ++g;
+        if (left > 0 && --qt < 0) next_seq(p);
         return true;
     }
+    // the next sequence that has rows here (there is one, as tiles are left), 32 of them at a time
+    __device__ __forceinline__ void next_seq(const TcArgs& p) {
+        const int lane = threadIdx.x & 31;
+        for (int first = b + 1;; first += 32) {
+            if (first >= p.a.batch.B) {
+                first = 0;
+                ++g;
+            }
+            int n = 0;
+            if (first + lane < p.a.batch.B) n = blocks_of(p, load_seq(p.a.batch, p.a.cache.page, first + lane));
+            const unsigned some = __ballot_sync(0xffffffffu, n > 0);
+            if (some) {
+                const int l = __ffs(some) - 1;
+                b = first + l;
+                qt = __shfl_sync(0xffffffffu, n, l) - 1;
+                return;
+            }
+        }
+    }
 };
+
+// Where this CTA's run begins, worked out by all its threads: the row blocks of every sequence are counted, then each thread adds
+// up the key tiles of an equal share of them, and the one whose share holds the first tile finds it.  `starts` [B + 1] and `sums`
+// [32] are scratch in shared memory.
+__device__ __forceinline__ void plan(const TcArgs& p, int* starts, int64_t* sums, Walk* out, int* bad) {
+    const int t = threadIdx.x, threads = blockDim.x, B = p.a.batch.B;
+    int64_t total, base = 0;
+    for (int b0 = 0; b0 < B; b0 += threads) {
+        int n = 0;
+        if (b0 + t < B) {
+            const Seq s = load_seq(p.a.batch, p.a.cache.page, b0 + t);
+            if (!s.ok) bad[0] = 1;
+            n = blocks_of(p, s);
+        }
+        const int64_t before = block_scan(n, sums, total);
+        if (b0 + t < B) starts[b0 + t] = (int)(base + before);
+        base += total;
+    }
+    if (t == 0) {
+        starts[B] = (int)base;
+        *out = Walk{0, 0, 0, 0, 0};
+        p.cuts[blockIdx.x].first = 0;
+    }
+    __syncthreads();
+    const int items = (int)base, share = (items + threads - 1) / threads, j0 = min(items, t * share), j1 = min(items, j0 + share);
+    int b = 0, hi = B - 1;                  // the sequence of item j0: the last one that starts at or before it
+    while (b < hi) {
+        const int mid = (b + hi + 1) >> 1;
+        if (starts[mid] <= j0) b = mid;
+        else hi = mid - 1;
+    }
+    // visits the share's items until `stop` of their tiles are passed; returns the tiles
+    int seq = b, qt = 0;
+    auto visit = [&](int64_t stop) {
+        int64_t sum = 0;
+        seq = b;
+        for (int j = j0; j < j1; ++j) {
+            while (j >= starts[seq + 1]) ++seq;
+            qt = starts[seq + 1] - 1 - j;
+            const int tiles = item_of(p, load_seq(p.a.batch, p.a.cache.page, seq), seq, qt).tiles;
+            if (sum + tiles > stop) break;
+            sum += tiles;
+        }
+        return sum;
+    };
+    const int64_t mine = visit(INT64_MAX), before = block_scan(mine, sums, total);
+    const int64_t U = total * p.a.cache.H_kv;
+    const int P = (int)min((int64_t)p.P, U), c = blockIdx.x;
+    const int64_t u = cut(c, U, P), left = cut(c + 1, U, P) - u;
+    if (left > 0) {
+        const int g = (int)(u / total);
+        const int64_t r = u - g * total;
+        if (before <= r && r < before + mine) {
+            const int from = (int)(r - before - visit(r - before));
+            *out = Walk{(int)left, g, seq, qt, from};
+            if (from > 0 && cut(c - 1, U, P) <= u - from) {
+                const Item it = item_of(p, load_seq(p.a.batch, p.a.cache.page, seq), seq, qt);
+                p.cuts[c] = Cut{1, seq, g, it.t0, (int)(((u - from + it.tiles) * P - 1) / U)};
+            }
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");     // the scratch's place is the TMA's next
+    __syncthreads();
+}
 
 struct Kept {
     Walk walk;
@@ -255,14 +273,13 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
 }
 
 // mbar_wait in line: a call would cost the roles registers that their shares do not have.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, WsHeader* hdr, int where) {
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, int where) {
     if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = global_ns();
     while (!mbar_try_wait_suspend(bar, parity, 1000u)) {
         if (*abort_flag) return false;
         if (global_ns() - t0 > kTimeoutNs) {
-            record_error(hdr, SP_ETIMEOUT, where);
-            *abort_flag = 1;
+            *abort_flag = where;
             return false;
         }
     }
@@ -270,8 +287,8 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
 }
 
 // For a warp whose lanes go on together.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, WsHeader* hdr, int where) {
-    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, hdr, where));
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int where) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, where));
 }
 
 #define TMEM_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
@@ -440,7 +457,7 @@ struct Layout {
     static constexpr int kTileBytes = kKeys * D * 2;            // a tile of Q, K or V
     static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr int kQ = 0, kRing = 2 * kTileBytes, kBars = kRing + kStages * kTileBytes;
-    static constexpr int kKeep = kBars + 8 * (3 * kStages + 14), kEnd = kKeep + 8 * (int)sizeof(Kept);
+    static constexpr int kKeep = kBars + 8 * (3 * kStages + 14), kBad = kKeep + 8 * (int)sizeof(Kept), kEnd = kBad + 8 + (int)sizeof(Walk);
     static_assert(kEnd <= kSmem, "");
     // TMEM columns
     static constexpr int kS(int w) { return w * 128; }
@@ -456,7 +473,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
     extern __shared__ __align__(1024) uint8_t raw[];
     uint8_t* smem = raw;
     if (smem_u32(smem) & 1023) {            // the swizzle goes by addresses: not met, as there is no other shared memory
-        if (threadIdx.x == 0) record_error(p.hdr, SP_EDEVICE, 9);
+        if (threadIdx.x == 0) p.err[blockIdx.x] = 4 | 9 << 8, p.cuts[blockIdx.x].first = 0;
         return;
     }
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
@@ -471,12 +488,18 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
     uint64_t* turn = o_full + 2;            // [2] this row tile's MMAs may be issued
     uint64_t* final_bar = turn + 2;
     volatile uint32_t* tmem_sh = reinterpret_cast<volatile uint32_t*>(final_bar + 1);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_sh + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_sh + 1);    // the wait that gave up, or 0
+    int* bad = reinterpret_cast<int*>(smem + L::kBad);                          // [2] impossible lengths; a page index out of range
+    Walk* start = reinterpret_cast<Walk*>(bad + 2);
     Kept* keep = reinterpret_cast<Kept*>(smem + L::kKeep);      // [8] a softmax warp's place in its run
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     using W = Roles<kKind>;
     constexpr int kMma = W::kMma, kTma = W::kTma, kClean = W::kClean;
+    if (threadIdx.x == 32) {
+        const CUtensorMap* m[3] = {&maps.q, &maps.k, &maps.v};
+        for (int i = 0; i < (kSame ? 3 : 1); ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m[i])) : "memory");
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(smem_u32(&full[i]), kSame ? 1 : W::kMma - W::kSoftmax);
@@ -494,6 +517,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
         }
         mbar_init(smem_u32(final_bar), 2);
         *abort_flag = 0;
+        bad[0] = bad[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMma) {
@@ -506,9 +530,9 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_sh;
-    cudaGridDependencySynchronize();        // the plan
     cudaTriggerProgrammaticLaunchCompletion();
-    Walk walk(p, blockIdx.x);
+    plan(p, reinterpret_cast<int*>(smem + L::kRing), reinterpret_cast<int64_t*>(smem + L::kRing + 4 * (kMaxSeqs + 2)), start, bad);
+    Walk walk = *start;
     Segment sg;
     const int rows_tile = p.G * p.tpt;
 
@@ -538,7 +562,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
             const int n_tiles = sg.to - sg.from;
             int base = tile_of(sg, sg.from) * kKeys;
             for (int x = 0; x < n_tiles; ++x, base -= kKeys) {
-                ok = wait_warp(smem_u32(&s_full[w]), ph, abort_flag, p.hdr, 21);
+                ok = wait_warp(smem_u32(&s_full[w]), ph, abort_flag, 21);
                 ph ^= 1;
                 if (!ok) break;
                 tc_fence_after();
@@ -602,7 +626,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                 follow = __any_sync(0xffffffffu, grows);
             }
             if (!ok) break;
-            ok = wait_warp(smem_u32(&o_full[w]), ph_o, abort_flag, p.hdr, 22);
+            ok = wait_warp(smem_u32(&o_full[w]), ph_o, abort_flag, 22);
             ph_o ^= 1;
             if (!ok) break;
             tc_fence_after();
@@ -680,7 +704,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                     const int tok = tile_of(sg, x) * kKeys + r0 + (lane & 15);
                     if (tok >= sg.s.kv || tok < seen) return w;
                     if ((unsigned)pg >= (unsigned)c.pages) {
-                        record_error(p.hdr, SP_EDEVICE, 2);
+                        bad[1] = 1;
                         return w;
                     }
                     const int slot = (int)((unsigned)tok % (unsigned)c.page);
@@ -710,7 +734,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                             if (more) nxt = place(x + 1, next_page);
                             else nxt.at = -1;
                         }
-                        ok = wait_warp(smem_u32(&empty[st]), ph, abort_flag, p.hdr, 61);
+                        ok = wait_warp(smem_u32(&empty[st]), ph, abort_flag, 61);
                         if (!ok) break;
                         uint8_t* tile = smem + L::kRing + st * L::kTileBytes;
                         const uint32_t scale_lane = v ? cur.vs : cur.ks;
@@ -762,7 +786,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
             int st = 0;
             uint32_t ph = 0, ph_q = 0, ph_p = 0, ph_t = 1 - w;     // the first turn is A's
             bool ok = tmem == 0;
-            auto wait = [&](uint32_t bar, uint32_t parity, int where) { return wait_warp(bar, parity, abort_flag, p.hdr, where); };
+            auto wait = [&](uint32_t bar, uint32_t parity, int where) { return wait_warp(bar, parity, abort_flag, where); };
             auto step = [&] {
                 if (++st == NS) st = 0, ph ^= 1;
             };
@@ -829,15 +853,14 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                     step();
                 }
             }
-            if (tmem != 0 && lead) record_error(p.hdr, SP_EDEVICE, 8);
             // nothing of this warp's MMAs is in flight when TMEM is freed
             commit_if(lead, smem_u32(final_bar));
             if (lead) {
-                if (!ok) *abort_flag = 1;
+                if (tmem != 0) *abort_flag = 8;
                 const unsigned long long t0 = global_ns();
                 while (!mbar_try_wait_suspend(smem_u32(final_bar), 0, 1000u))
                     if (global_ns() - t0 > kTimeoutNs) {
-                        record_error(p.hdr, SP_ETIMEOUT, 36);
+                        *abort_flag = 36;
                         break;
                     }
             }
@@ -855,7 +878,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                 const int nw = two_tiles(p, sg) ? 2 : 1;
                 const int32_t* table = p.a.batch.table + (int64_t)sg.it.b * p.a.batch.table_stride;
                 const int seen = first_seen(sg.s, p.a.window);
-                ok = wait_warp(smem_u32(q_empty), ph_q, abort_flag, p.hdr, 41);
+                ok = wait_warp(smem_u32(q_empty), ph_q, abort_flag, 41);
                 ph_q ^= 1;
                 if (!ok) break;
                 if (lane == 0) {
@@ -873,7 +896,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                     if (lane >= boxes || tok >= sg.s.kv || tok + p.box <= seen) return (int)c.pages;
                     const int q = (int)((unsigned)tok / (unsigned)c.page), pg = table[q];
                     if (pg < 0 || pg >= c.pages) {
-                        record_error(p.hdr, SP_EDEVICE, 2);
+                        bad[1] = 1;
                         return (int)c.pages;
                     }
                     slot = tok - q * c.page;
@@ -885,7 +908,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                     if (x + 1 < sg.to) pg2 = page_of(x + 1, slot2);
                     const bool clean = !ragged(p, sg, tile_of(sg, x) * kKeys);
                     for (int v = 0; v < 2; ++v) {
-                        ok = wait_warp(smem_u32(&empty[st]), ph, abort_flag, p.hdr, 42);
+                        ok = wait_warp(smem_u32(&empty[st]), ph, abort_flag, 42);
                         if (!ok) break;
                         const bool wash = v == 1 && !clean;
                         const uint32_t bar = smem_u32(wash ? &landed[st] : &full[st]);
@@ -933,7 +956,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                     const int base = tile_of(sg, x) * kKeys, sv = st + 1 == NS ? 0 : st + 1;
                     st = sv + 1 == NS ? 0 : sv + 1;
                     if (!ragged(p, sg, base)) continue;
-                    ok = wait_warp(smem_u32(&landed[sv]), (ph >> sv) & 1, abort_flag, p.hdr, 51);
+                    ok = wait_warp(smem_u32(&landed[sv]), (ph >> sv) & 1, abort_flag, 51);
                     ph ^= 1u << sv;
                     if (!ok) break;
                     uint8_t* tile = smem + L::kRing + sv * L::kTileBytes;
@@ -952,29 +975,37 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (threadIdx.x == 0) p.err[blockIdx.x] = (bad[0] ? 1 : 0) | (bad[1] ? 2 : 0) | (*abort_flag ? 4 | *abort_flag << 8 : 0);
+    cudaGridDependencySynchronize();        // of a mixed batch: the step kernels, which ran beside this one, end before it does
     if (warp == kMma)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-// Adds up the parts of the items that were cut: block (c, y) takes the item
-// whose first cut is the one before CTA c, and 16 of its columns; a thread one row.
+// Adds up the parts of the items that were cut: block (c - 1, y) takes the item that CTA c's run begins in, and 16 of its columns;
+// a thread one row.  Block (0, 0) gathers the status as well: `alone` if no other kernel of the call has one.
 template <int D>
-__global__ void __launch_bounds__(kRowsItem) tc_join_kernel(const __grid_constant__ TcArgs p) {
+__global__ void __launch_bounds__(kRowsItem) tc_join_kernel(const __grid_constant__ TcArgs p, int alone) {
     cudaGridDependencySynchronize();
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        const int e = threadIdx.x < p.P ? p.err[threadIdx.x] : 0;
+        const bool bad = __syncthreads_or(e & 3), gone = __syncthreads_or(e & 4);
+        if (threadIdx.x == 0 && (alone || bad)) {
+            p.hdr->status = bad ? SP_EDEVICE : SP_OK;
+            p.hdr->where = 0;
+        }
+        __syncthreads();
+        if (bad && (e & 3)) p.hdr->where = e & 3;
+        if (gone && (e & 4)) {
+            p.hdr->status = SP_ETIMEOUT;
+            p.hdr->where = e >> 8;
+        }
+    }
     const int c = blockIdx.x + 1, row = threadIdx.x;
-    const int n = *p.n_items;
-    const int64_t per_head = p.pre[n], U = per_head * p.a.cache.H_kv;
-    const int P = (int)min((int64_t)p.P, U);
-    const int64_t u = cut(c, U, P);
-    if (u >= U) return;
-    const int g = (int)(u / per_head);
-    const int lo = find_item(p, n, u - g * per_head);
-    const int64_t begin = g * per_head + p.pre[lo];
-    if (u == begin || cut(c - 1, U, P) > begin) return;
-    const Item it = p.items[lo];
-    const Seq s = load_seq(p.a.batch, p.a.cache.page, it.b);
-    const int c1 = (int)(((begin + it.tiles) * P - 1) / U);        // the CTA of the item's last tile
-    const int w = row >> 7, r = row & 127, t_row = r / p.G, t = it.t0 + w * p.tpt + t_row;
+    const Cut q = p.cuts[c];
+    if (!q.first) return;
+    const Seq s = load_seq(p.a.batch, p.a.cache.page, q.b);
+    const int g = q.g, c1 = q.last;
+    const int w = row >> 7, r = row & 127, t_row = r / p.G, t = q.t0 + w * p.tpt + t_row;
     if (r >= p.G * p.tpt || t >= s.n) return;
     float m = -INFINITY;
     for (int k = c - 1; k <= c1; ++k) m = fmaxf(m, p.part_ml[((int64_t)k * 2 + (k == c - 1)) * kRowsItem + row].x);
@@ -1010,20 +1041,14 @@ __global__ void __launch_bounds__(kRowsItem) tc_join_kernel(const __grid_constan
 }
 
 struct Space {
-    size_t n_items, items, pre, part_o, part_ml, total;
+    size_t err, cuts, part_o, part_ml, total;
 };
 
-int max_items(const sp_batch& b, int tpt) {
-    return (int)std::min<int64_t>((int64_t)b.B + b.T / (2 * tpt), INT32_MAX / 2);
-}
-
-Space carve(const sp_batch& b, int d, int tpt, int P) {
+Space carve(int d, int P) {
     Space s;
     Carve c;
-    const size_t n = (size_t)max_items(b, tpt);
-    s.n_items = c.take(sizeof(int));
-    s.items = c.take(n * sizeof(Item));
-    s.pre = c.take((n + 1) * sizeof(int64_t));
+    s.err = c.take((size_t)P * sizeof(int));
+    s.cuts = c.take((size_t)P * sizeof(Cut));
     s.part_o = c.take((size_t)P * 2 * kRowsItem * d * sizeof(float));
     s.part_ml = c.take((size_t)P * 2 * kRowsItem * sizeof(float2));
     s.total = c.off;
@@ -1057,11 +1082,15 @@ sp_status encode(CUtensorMap* map, const void* data, int rank, const int64_t* ex
 template <int D, int kKind>
 sp_status launch(const Maps& maps, const TcArgs& p, cudaStream_t st) {
     SP_CUDA_TRY(cudaFuncSetAttribute(attend_tc_kernel<D, kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
-    plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
-    SP_LAUNCH_CHECK();
-    sp_status s = launch_early(attend_tc_kernel<D, kKind>, dim3((unsigned)p.P), Roles<kKind>::kThreads, (size_t)kSmem, st, maps, p);
-    if (s != SP_OK || p.P == 1) return s;
-    return launch_early(tc_join_kernel<D>, dim3((unsigned)p.P - 1, D / 16), kRowsItem, (size_t)0, st, p);
+    // after the step kernels of a mixed batch this one does not wait for them
+    if (p.min_rows > 0) {
+        const sp_status s = launch_early(attend_tc_kernel<D, kKind>, dim3((unsigned)p.P), Roles<kKind>::kThreads, (size_t)kSmem, st, maps, p);
+        if (s != SP_OK) return s;
+    } else {
+        attend_tc_kernel<D, kKind><<<p.P, Roles<kKind>::kThreads, kSmem, st>>>(maps, p);
+        SP_LAUNCH_CHECK();
+    }
+    return launch_early(tc_join_kernel<D>, dim3((unsigned)std::max(1, p.P - 1), D / 16), kRowsItem, (size_t)0, st, p, p.min_rows == 0 ? 1 : 0);
 }
 
 template <int D>
@@ -1072,7 +1101,8 @@ sp_status launch_codes(const Maps& maps, const TcArgs& p, cudaStream_t st) {
 }  // namespace
 
 // Whether the cache and the group of heads are within the kernel's layouts.
-bool attend_tc_supported(const sp_cache& c, int G) {
+bool attend_tc_supported(const sp_cache& c, const sp_batch& b, int G) {
+    if (b.B > kMaxSeqs || sm_count() < 2 || sm_count() > kRowsItem) return false;     // (the join looks at a CTA's status per thread)
     if (c.dtype != SP_BF16 || (c.d != 64 && c.d != 128) || G > 128) return false;
     if (c.kind != SP_CACHE_SAME)                                        // rows of codes are read 16 bytes at a time
         return (reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v) | (uintptr_t)c.stride_page |
@@ -1083,12 +1113,11 @@ bool attend_tc_supported(const sp_cache& c, int G) {
     return !(c.H_kv > 1 && c.stride_head == 0) && !(c.pages > 1 && c.stride_page == 0);
 }
 
-size_t attend_tc_ws_bytes(const sp_cache& c, const sp_batch& b, int G) {
-    return carve(b, c.d, 128 / G, sm_count()).total;
-}
+size_t attend_tc_ws_bytes(const sp_cache& c) { return carve(c.d, sm_count()).total; }
 
-// min_rows: sequences of at most that many rows per KV head have been taken by another kernel
-sp_status attend_tc_launch(const AttendProblem& a, int min_rows, void* ws, cudaStream_t st) {
+// min_rows: sequences of at most that many rows per KV head are taken by another kernel, whose workspace `ws` begins with; this
+// one's is `offset` bytes on.
+sp_status attend_tc_launch(const AttendProblem& a, int min_rows, void* ws, size_t offset, cudaStream_t st) {
     TcArgs p;
     p.a = a;
     p.G = a.H / a.cache.H_kv;
@@ -1096,14 +1125,11 @@ sp_status attend_tc_launch(const AttendProblem& a, int min_rows, void* ws, cudaS
     p.min_rows = min_rows;
     p.P = sm_count();
     p.box = std::min(128, a.cache.page & -a.cache.page);
-    p.clear = min_rows == 0;
-    p.max_items = max_items(a.batch, p.tpt);
-    char* base = static_cast<char*>(ws);
-    const Space s = carve(a.batch, a.cache.d, p.tpt, p.P);
-    p.hdr = reinterpret_cast<WsHeader*>(base);
-    p.n_items = reinterpret_cast<int*>(base + s.n_items);
-    p.items = reinterpret_cast<Item*>(base + s.items);
-    p.pre = reinterpret_cast<int64_t*>(base + s.pre);
+    char* base = static_cast<char*>(ws) + offset;
+    const Space s = carve(a.cache.d, p.P);
+    p.hdr = static_cast<WsHeader*>(ws);
+    p.err = reinterpret_cast<int*>(base + s.err);
+    p.cuts = reinterpret_cast<Cut*>(base + s.cuts);
     p.part_o = reinterpret_cast<float*>(base + s.part_o);
     p.part_ml = reinterpret_cast<float2*>(base + s.part_ml);
     Maps maps;
