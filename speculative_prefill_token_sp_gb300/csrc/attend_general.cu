@@ -85,9 +85,9 @@ __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(const __grid_co
     bool bad_seq = false, bad_page = false;
     cudaTriggerProgrammaticLaunchCompletion();
     const int64_t U = total_units(p, kUnit, bad_seq);
-    const int P = parts_of(p, U);
-    int64_t u = cut(blockIdx.x, U, P);
-    const int64_t u_end = cut(blockIdx.x + 1, U, P);
+    const Shares shares(U, p.P);
+    int64_t u = shares.at(blockIdx.x);
+    const int64_t u_end = shares.at(blockIdx.x + 1);
     int64_t begin = 0;
     int b = u < u_end ? find_unit(p, kUnit, u, begin) : 0;
     const float f = p.a.scale * 1.4426950408889634f;
@@ -101,8 +101,8 @@ __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(const __grid_co
             ++b;
             continue;
         }
-        const int64_t item = in_seq / span.units;
-        const int g = (int)(item / blocks), rb = (int)(item - (int64_t)g * blocks), from = (int)(in_seq - item * span.units);
+        const int64_t item = divide(in_seq, span.units);
+        const int g = (int)divide(item, blocks), rb = (int)(item - (int64_t)g * blocks), from = (int)(in_seq - item * span.units);
         const int to = (int)min((int64_t)span.units, from + (u_end - u));
         const int64_t r0 = (int64_t)rb * kGenRows;
         const int rows = (int)min((int64_t)kGenRows, (int64_t)s.n * p.G - r0);
@@ -244,8 +244,9 @@ template <typename T>
 __global__ void __launch_bounds__(32 * kGenRows) general_join_kernel(const __grid_constant__ SplitArgs p) {
     bool bad = false;
     const int64_t U = total_units(p, kUnit, bad);
-    const int P = parts_of(p, U), c = blockIdx.x + 1, r = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t u = cut(c, U, P);
+    const Shares shares(U, p.P);
+    const int c = blockIdx.x + 1, r = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t u = shares.at(c);
     int64_t begin = 0;
     const int b = u < U ? find_unit(p, kUnit, u, begin) : 0;
     cudaGridDependencySynchronize();        // the main kernel's parts
@@ -253,14 +254,14 @@ __global__ void __launch_bounds__(32 * kGenRows) general_join_kernel(const __gri
     if (u >= U) return;
     const Seq s = load_seq(p.a.batch, p.a.cache.page, b);
     const int units = span_of(s, p.a.window, kUnit).units, blocks = row_blocks(p, s);
-    const int64_t item = (u - begin) / units, first = begin + item * units;
-    if (u == first || cut(c - 1, U, P) > first) return;       // no cut, or not the item's first
-    const int g = (int)(item / blocks);
+    const int64_t item = divide(u - begin, units), first = begin + item * units;
+    if (u == first || shares.at(c - 1) > first) return;       // no cut, or not the item's first
+    const int g = (int)divide(item, blocks);
     const int64_t row = (item - (int64_t)g * blocks) * kGenRows + r;
     if (row >= (int64_t)s.n * p.G) return;
     const int e = lane * 8;
     float m = -INFINITY, z = 0.f, o[8] = {};
-    const int c1 = cta_of(first + units - 1, U, P);
+    const int c1 = shares.of(first + units - 1);
     for (int k = c - 1; k <= c1; ++k) {
         const int64_t slot = ((int64_t)k * 2 + (k == c - 1 ? 1 : 0)) * kRows + r;
         const float2 ml = p.part_ml[slot];

@@ -1,8 +1,7 @@
 // What the attention kernels that cut the keys (attend_step.cu, attend_general.cu)
 // share: an item is a block of query rows of one sequence and KV head; the items'
-// units of keys are laid end to end (sequence, KV head, row block, unit) and CTA c
-// takes the units [c U / P, (c + 1) U / P), P being the CTAs or the units, if those
-// are fewer, so that every part has a unit.  Each CTA works this out from the
+// units of keys are laid end to end (sequence, KV head, row block, unit) and each
+// CTA takes an equal run of them.  Each CTA works this out from the
 // batch's device arrays by itself.  An item that is cut leaves one part per
 // CTA in the workspace: slot 2 c + 1 if the part begins with the item's first
 // unit, 2 c otherwise (a CTA has at most one of each).
@@ -112,10 +111,6 @@ __device__ __forceinline__ int find_unit(const SplitArgs& p, int unit, int64_t u
     return p.a.batch.B;
 }
 
-// CTA c takes the units from cut(c) to cut(c + 1); the CTA of a unit is cta_of.
-__device__ __forceinline__ int parts_of(const SplitArgs& p, int64_t U) { return (int)min((int64_t)p.P, U); }
-__device__ __forceinline__ int64_t cut(int64_t c, int64_t U, int P) { return min(c, (int64_t)P) * U / max(P, 1); }
-__device__ __forceinline__ int cta_of(int64_t u, int64_t U, int P) { return (int)(((u + 1) * P - 1) / U); }
 // Gathers what the CTAs of the main kernel found wrong into the status; every thread of one block calls it.
 __device__ __forceinline__ void gather_status(const SplitArgs& p) {
     int one = 0, two = 0;

@@ -157,9 +157,9 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
     bool bad_seq = false, bad_page = false;
     cudaTriggerProgrammaticLaunchCompletion();      // the joining kernel may line up: it waits for this one's end
     const int64_t U = total_units(p, kUnit, bad_seq);
-    const int P = parts_of(p, U);
-    int64_t u = cut(blockIdx.x, U, P);
-    const int64_t u_end = cut(blockIdx.x + 1, U, P);
+    const Shares shares(U, p.P);
+    int64_t u = shares.at(blockIdx.x);
+    const int64_t u_end = shares.at(blockIdx.x + 1);
     int64_t begin = 0;
     int b = u < u_end ? find_unit(p, kUnit, u, begin) : 0;
     const float f = p.a.scale * 1.4426950408889634f;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
             ++b;
             continue;
         }
-        const int g = (int)(in_seq / span.units), from = (int)(in_seq - (int64_t)g * span.units);
+        const int g = (int)divide(in_seq, span.units), from = (int)(in_seq - (int64_t)g * span.units);
         const int to = (int)min((int64_t)span.units, from + (u_end - u));
         const int rows = s.n * p.G;
 
@@ -518,7 +518,8 @@ __global__ void __launch_bounds__(kJoinThreads) step_join_kernel(const __grid_co
     U *= p.a.cache.H_kv;
     const int units = span_of(s, p.a.window, kUnit).units;
     begin = begin * p.a.cache.H_kv + (int64_t)g * units;
-    const int P = parts_of(p, U), c0 = mine ? cta_of(begin, U, P) : 0, c1 = mine ? cta_of(begin + units - 1, U, P) : 0;
+    const Shares shares(U, p.P);
+    const int c0 = mine ? shares.of(begin) : 0, c1 = mine ? shares.of(begin + units - 1) : 0;
     cudaGridDependencySynchronize();        // the main kernel's partial sums
     if (i == 0 && r == 0) gather_status(p);
     if (c0 == c1) return;                   // not taken here, or written by the main kernel

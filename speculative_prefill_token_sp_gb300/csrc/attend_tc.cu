@@ -53,7 +53,7 @@ struct Roles {
     static constexpr bool kSame = kKind == SP_CACHE_SAME;
     static constexpr int kSoftmax = 8, kMma = kSame ? 8 : 16, kTma = kMma + 2, kClean = kMma + 3;
     static constexpr int kThreads = 32 * (kMma + 4);
-    static constexpr int kSoftmaxRegs = kSame ? 216 : 168, kConvertRegs = 48, kSingleRegs = kSame ? 72 : 48;
+    static constexpr int kSoftmaxRegs = kSame ? 216 : 136, kConvertRegs = 80, kSingleRegs = kSame ? 72 : 48;
     static_assert(kSoftmax * kSoftmaxRegs + (kMma - kSoftmax) * kConvertRegs + 4 * kSingleRegs <= (kMma + 4) * (kSame ? 168 : 96),
                   "the roles' registers");
 };
@@ -131,9 +131,6 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* warp_sums, int
     __syncthreads();
     return x - mine + (warp ? before : 0);
 }
-
-// CTA c takes the key tiles from cut(c) to cut(c + 1) of all U; P is the CTAs, or the tiles if those are fewer.
-__device__ __forceinline__ int64_t cut(int64_t c, int64_t U, int P) { return min(c, (int64_t)P) * U / max(P, 1); }
 
 // A CTA's run of key tiles, item by item: KV head, sequence, row block (from the last tokens, which see most keys, to the first),
 // key tile.  Every role walks it by itself; all lanes of a warp together.
@@ -225,17 +222,18 @@ __device__ __forceinline__ void plan(const TcArgs& p, int* starts, int64_t* sums
     };
     const int64_t mine = visit(INT64_MAX), before = block_scan(mine, sums, total);
     const int64_t U = total * p.a.cache.H_kv;
-    const int P = (int)min((int64_t)p.P, U), c = blockIdx.x;
-    const int64_t u = cut(c, U, P), left = cut(c + 1, U, P) - u;
+    const Shares shares(U, p.P);
+    const int c = blockIdx.x;
+    const int64_t u = shares.at(c), left = shares.at(c + 1) - u;
     if (left > 0) {
-        const int g = (int)(u / total);
+        const int g = (int)divide(u, total);
         const int64_t r = u - g * total;
         if (before <= r && r < before + mine) {
             const int from = (int)(r - before - visit(r - before));
             *out = Walk{(int)left, g, seq, qt, from};
-            if (from > 0 && cut(c - 1, U, P) <= u - from) {
+            if (from > 0 && shares.at(c - 1) <= u - from) {
                 const Item it = item_of(p, load_seq(p.a.batch, p.a.cache.page, seq), seq, qt);
-                p.cuts[c] = Cut{1, seq, g, it.t0, (int)(((u - from + it.tiles) * P - 1) / U)};
+                p.cuts[c] = Cut{1, seq, g, it.t0, shares.of(u - from + it.tiles - 1)};
             }
         }
     }
@@ -321,6 +319,11 @@ __device__ __forceinline__ void tmem_wait32(uint32_t* r) {
     for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// Keeps the uses of registers that an earlier wait was for below this point.
+__device__ __forceinline__ void keep32(uint32_t* r) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
 __device__ __forceinline__ void tmem_wait16(uint32_t* r) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
@@ -354,16 +357,25 @@ __device__ __forceinline__ void max_cols(const float* v, float (&mx)[4]) {
         for (int c = 0; c < 4; ++c) mx[c] = fmax3(mx[c], v[i + 2 * c], v[i + 2 * c + 1]);
 }
 
-// Weights 2^(f v - m) (nm = -m) of 32 logits as pairs of bf16, and their sums.
+// Weights 2^(f v - m) (nm = -m) of 32 logits as pairs of bf16, and their sums.  16 at a time and step by step: pair by pair, a warp
+// alone on its scheduler took 610 to 710 cycles for 96 weights, like this 495 (384 are the exponentials').
 __device__ __forceinline__ void weights32(const float* v, float f, float nm, float (&zs)[4], uint32_t* pk) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-        float a = v[i], b = v[i + 1];
-        fma2(a, b, f, nm);
-        a = ex2_approx(a);
-        b = ex2_approx(b);
-        add2(zs[i & 2], zs[(i & 2) + 1], a, b);
-        pk[i >> 1] = pack_bf16(a, b);
+    for (int c = 0; c < 32; c += 16) {
+        float w[16];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            w[i] = v[c + i];
+            w[i + 1] = v[c + i + 1];
+            fma2(w[i], w[i + 1], f, nm);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = ex2_approx(w[i]);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            add2(zs[i & 2], zs[(i & 2) + 1], w[i], w[i + 1]);
+            pk[(c + i) >> 1] = pack_bf16(w[i], w[i + 1]);
+        }
     }
 }
 
@@ -378,6 +390,30 @@ __device__ __forceinline__ void scale_o(uint32_t o_at, float a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * a);
         tmem_st16(o_at + 16 * c, ov);
+    }
+}
+
+// Lane 4k + j's piece i becomes lane 4k + i's piece j.
+__device__ __forceinline__ void transpose4(uint4 (&q)[4]) {
+    const int lane = threadIdx.x & 31;
+    auto swap = [](uint4 give, int with) {
+        give.x = __shfl_xor_sync(0xffffffffu, give.x, with);
+        give.y = __shfl_xor_sync(0xffffffffu, give.y, with);
+        give.z = __shfl_xor_sync(0xffffffffu, give.z, with);
+        give.w = __shfl_xor_sync(0xffffffffu, give.w, with);
+        return give;
+    };
+#pragma unroll
+    for (int with = 1; with <= 2; with *= 2) {
+        const bool up = lane & with;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & with) continue;
+            // the lower lane gives its piece i + with for the upper lane's piece i
+            const uint4 got = swap(up ? q[i] : q[i + with], with);
+            if (up) q[i] = got;
+            else q[i + with] = got;
+        }
     }
 }
 
@@ -554,11 +590,12 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
             const int p_first = sg.s.kv - sg.s.n + sg.it.t0 + w * p.tpt;
             const int p_last = sg.s.kv - sg.s.n + min(sg.s.n, sg.it.t0 + (w + 1) * p.tpt) - 1;
             const int pos = row < rows_tile ? min(p_first + row / p.G, p_last) : -1;
-            // z and O are sums of 2^(logit - m).  m is the row's maximum as it was some tiles ago: a tile's weights are worked out by
-            // it while its maximum is still being looked for, and m follows before the next tile if that is more than 2^8 above.
-            // Only if it is more than 2^24 above (or the row has no m yet) is the tile done again.
+            // z and O are sums of 2^(logit - m).  m need not be the row's maximum, only near it: it is the maximum of the first tile
+            // that the row sees, and where a tile's weights sum to more than 2^8, m grows by that sum's logarithm before the
+            // next one.  So the maximum of a tile is not looked for.  A tile is done again by its true maximum if its weights
+            // sum to more than 2^24, which is seen before they are handed over (of the last 32 keys by their maximum).
             float m = -INFINITY, z = 0.f, next_m = -INFINITY;
-            bool follow = false;
+            bool follow = false, fresh = true;
             const int n_tiles = sg.to - sg.from;
             int base = tile_of(sg, sg.from) * kKeys;
             for (int x = 0; x < n_tiles; ++x, base -= kKeys) {
@@ -576,54 +613,72 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                 }
                 uint32_t sr[kSame ? 128 : 32], pk[48];
                 float* sv = reinterpret_cast<float*>(sr);
-                float nm, top, zs[4];
+                float nm, zs[4];
                 for (;;) {
-                    nm = m == -INFINITY ? 0.f : -m;
-                    zs[0] = zs[1] = zs[2] = zs[3] = 0.f;
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    if constexpr (kSame) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, sr + 32 * c);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_wait32(sr + 32 * c);
-                        if (masked) mask_cols<128>(sv, 0, hi, lo);
-                        max_cols<32>(sv + 96, mx);
-                    }
-#pragma unroll
-                    for (int c = 0; c < 3; ++c) {
-                        float* v = kSame ? sv + 32 * c : sv;
-                        if constexpr (!kSame) {
+                    if (fresh) {            // the true maximum, for rows without an m or with one left far behind
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
                             tmem_ld32(s_at + 32 * c, sr);
                             tmem_wait32(sr);
                             if (masked) mask_cols<32>(sv, 32 * c, hi, lo);
+                            max_cols<32>(sv, mx);
                         }
-                        max_cols<32>(v, mx);
+                        const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * f;     // f > 0: f times the largest product
+                        // 16: a sum of 96 over 2^24 has a maximum over 2^17, and one pass is enough.  Also where there was no m
+                        const bool far = top > m + 16.f;
+                        const float a = far && m != -INFINITY ? ex2_approx(m - top) : 1.f;
+                        if (__any_sync(0xffffffffu, a != 1.f)) scale_o<D>(o_at, a);
+                        z *= a;
+                        if (far) m = top;
+                    }
+                    nm = m == -INFINITY ? 0.f : -m;
+                    zs[0] = zs[1] = zs[2] = zs[3] = 0.f;
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float* v3 = kSame ? sv + 96 : sv;
+                    tmem_ld32(s_at + 96, sr + (kSame ? 96 : 0));
+                    if constexpr (kSame) tmem_ld32(s_at, sr);
+                    tmem_wait32(sr + (kSame ? 96 : 0));
+                    if constexpr (kSame) {
+                        tmem_wait32(sr);
+                        tmem_ld32(s_at + 32, sr + 32);
+                        tmem_ld32(s_at + 64, sr + 64);
+                    }
+                    if (masked) mask_cols<32>(v3, 96, hi, lo);
+                    max_cols<32>(v3, mx);
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) {
+                        float* v = kSame ? sv + 32 * c : sv;
+                        if constexpr (!kSame) tmem_ld32(s_at + 32 * c, sr);
+                        if (!kSame || c == 1) tmem_wait32(reinterpret_cast<uint32_t*>(v));
+                        if (kSame && c == 2) keep32(sr + 64);
+                        if (masked) mask_cols<32>(v, 32 * c, hi, lo);
                         weights32(v, f, nm, zs, pk + 16 * c);
                     }
-                    if constexpr (!kSame) {
-                        tmem_ld32(s_at + 96, sr);
-                        tmem_wait32(sr);
-                        if (masked) mask_cols<32>(sv, 96, hi, lo);
-                        max_cols<32>(sv, mx);
-                    }
-                    top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * f;     // f > 0: f times the largest product
-                    const bool lost = pos >= 0 && (m == -INFINITY ? top > -INFINITY : top > m + 24.f);
-                    if (!__any_sync(0xffffffffu, lost)) break;
-                    const float a = lost && m != -INFINITY ? ex2_approx(m - top) : 1.f;
-                    if (__any_sync(0xffffffffu, a != 1.f)) scale_o<D>(o_at, a);
-                    z *= a;
-                    if (lost) m = top;
+                    const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * f;
+                    // (a NaN or infinite sum of a row with an infinite m stays: it is the row's result)
+                    const float sum = (zs[0] + zs[1]) + (zs[2] + zs[3]);
+                    const bool lost = pos >= 0 && (sum > 16777216.f || top > m + 24.f) && m != INFINITY;
+                    fresh = __any_sync(0xffffffffu, lost);
+                    if (!fresh) break;
                 }
 #pragma unroll
                 for (int c = 0; c < 3; ++c) tmem_st16(s_at + 16 * c, pk + 16 * c);
                 hand_over(&p_full[2 * w]);          // 96 keys' weights, then the last 32: the product with V begins meanwhile
+                if constexpr (!kSame) {
+                    tmem_ld32(s_at + 96, sr);
+                    tmem_wait32(sr);
+                    if (masked) mask_cols<32>(sv, 96, hi, lo);
+                }
                 weights32(kSame ? sv + 96 : sv, f, nm, zs, pk);
                 tmem_st16(s_at + 48, pk);
                 hand_over(&p_full[2 * w + 1]);
-                z += (zs[0] + zs[1]) + (zs[2] + zs[3]);
-                const bool grows = pos >= 0 && top > m + 8.f;
-                next_m = grows ? top : m;
+                const float sum = (zs[0] + zs[1]) + (zs[2] + zs[3]);
+                z += sum;
+                const bool grows = pos >= 0 && sum > 256.f && sum < INFINITY;
+                next_m = grows ? m + log2f(sum) : m;
                 follow = __any_sync(0xffffffffu, grows);
+                fresh = __any_sync(0xffffffffu, pos >= 0 && m == -INFINITY);
             }
             if (!ok) break;
             ok = wait_warp(smem_u32(&o_full[w]), ph_o, abort_flag, 22);
@@ -638,7 +693,10 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
             const float inv = z == 0.f ? 0.f : 1.f / z;
             const int64_t r = sg.s.row0 + t;
             const int h = sg.g * p.G + row - t_row * p.G;
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.a.out.data) + r * p.a.out.stride_row + h * p.a.out.stride_head;
+            int64_t row_at[4];          // where the rows of this lane's group of four begin (-1: not a row)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                row_at[i] = __shfl_sync(0xffffffffu, real ? r * p.a.out.stride_row + h * p.a.out.stride_head : -1, (lane & ~3) + i);
             const int64_t slot = (int64_t)blockIdx.x * 2 + (sg.from == 0 ? 1 : 0);
             float* po = p.part_o + slot * kRowsItem * D + (w * 128 + row) * 4;
 #pragma unroll 1
@@ -647,15 +705,24 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                 tmem_ld32(o_at + 32 * c, ov);
                 tmem_wait32(ov);
                 if (whole) {
-                    if (real) {
+                    // pieces of 16 bytes are exchanged among four lanes, so that a store writes 64 bytes of each of eight rows
+                    // (16 of each of 32 took the load/store unit four times as long)
+                    uint4 q[4];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            float v[8];
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t o4[4];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) v[k] = z == 0.f ? 0.f : __uint_as_float(ov[i + k]) * inv;
-                            store8(dst + 32 * c + i, v);
+                        for (int k = 0; k < 4; ++k) {
+                            const float a = __uint_as_float(ov[8 * i + 2 * k]) * inv, b = __uint_as_float(ov[8 * i + 2 * k + 1]) * inv;
+                            o4[k] = z == 0.f ? 0u : pack_bf16(a, b);
                         }
+                        q[i] = make_uint4(o4[0], o4[1], o4[2], o4[3]);
                     }
+                    transpose4(q);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (row_at[i] >= 0)
+                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out.data) + row_at[i] + 32 * c + 8 * (lane & 3)) = q[i];
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)

@@ -32,6 +32,26 @@ __device__ __forceinline__ int first_seen(const Seq& s, int window) {
     return window ? (int)max((int64_t)0, (int64_t)s.kv - s.n - window + 1) : 0;
 }
 
+// U units laid end to end, in `parts` runs whose lengths differ by one at most: run c has the units [at(c), at(c + 1)).  One
+// division makes it (32 bits wide where that suffices: 64-bit divisions cost hundreds of cycles), one finds the run of a unit.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+struct Shares {
+    int64_t each;       // units of a run; the first `extra` have one more
+    int parts, extra;
+    __device__ __forceinline__ Shares(int64_t U, int most) {
+        parts = (int)max((int64_t)1, min((int64_t)most, U));        // so that every run has a unit, unless there is none at all
+        each = divide(U, parts);
+        extra = (int)(U - each * parts);
+    }
+    __device__ __forceinline__ int64_t at(int c) const { return (int64_t)min(c, parts) * each + min(c, extra); }
+    __device__ __forceinline__ int of(int64_t u) const {
+        const int64_t big = (each + 1) * extra;
+        return (int)(u < big ? divide(u, each + 1) : extra + divide(u - big, each));
+    }
+};
+
 // The sequence that row r is a new token of: the last b with cu_new[b] <= r
 // (so empty sequences are passed over), or -1.
 __device__ __forceinline__ int seq_of_row(const sp_batch& b, int64_t r) {
