@@ -319,6 +319,9 @@ sp_status sp_attend(const sp_rows* q, const sp_cache* cache, const sp_batch* bat
     AttendProblem p;
     p.q = *q; p.out = *out; p.cache = *cache; p.batch = *batch; p.H = H; p.scale = (float)scale;
     p.window = window >= (int64_t)1 << 30 ? 0 : (int)window;       // kv_len is at most 2^30: no limit at all
+    p.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (cache->page == 1 << i) p.page_shift = i;
     p.lse = lse; p.lse_stride_row = lse_stride_row; p.lse_stride_head = lse_stride_head;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     switch (path_of(*cache, *batch, H)) {

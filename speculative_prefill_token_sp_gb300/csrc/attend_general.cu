@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(const __grid_co
             const int tok = span.first + (from + k) * kUnit + warp * kWarpKeys + off;
             return j < n_keys && off < kWarpKeys && tok <= item_last && tok < s.kv ? tok : -1;
         };
-        auto page_of = [&](int tok) { return tok >= 0 ? table[(unsigned)tok / (unsigned)c.page] : 0; };
+        auto page_of = [&](int tok) { return tok >= 0 ? table[p.a.page_of(tok)] : 0; };
         Row8<T, kKind> k0, v0, k1, v1;
         auto request = [&](int& tok, int pg, Row8<T, kKind>& k, Row8<T, kKind>& v) {
             if (tok < 0) return;
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(const __grid_co
                 return;
             }
             if (!act) return;
-            const int slot = (int)((unsigned)tok % (unsigned)c.page);
+            const int slot = tok - p.a.page_of(tok) * c.page;
             const int64_t at = row_offset(c, pg, g, slot) + sub * 8, sc = scale_offset(c, pg, g, slot);
             k.load(c.k, c.k_scale, at, sc);
             v.load(c.v, c.v_scale, at, sc);

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
         const int tok0 = span.first + warp * kTok + (lane & (kTok - 1));
         auto page_of = [&](int i) {
             const int tok = tok0 + i * kUnit;
-            return i < to && tok < s.kv ? table[(unsigned)tok / (unsigned)c.page] : 0;
+            return i < to && tok < s.kv ? table[p.a.page_of(tok)] : 0;
         };
         // requests piece i of the run into its place in the ring
         auto request = [&](int i, int pg) {
@@ -196,12 +196,12 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
                 const uint32_t at = ring_at + ((i - from) % R::kStages) * R::kStage;
                 int64_t mine = -1;
                 if (tok < s.kv) {
-                    if ((unsigned)pg < (unsigned)c.pages) mine = row_offset(c, pg, g, (int)((unsigned)tok % (unsigned)c.page));
+                    if ((unsigned)pg < (unsigned)c.pages) mine = row_offset(c, pg, g, tok - p.a.page_of(tok) * c.page);
                     else bad_page = true;
                 }
                 if constexpr (!kSame) {
                     if (lane < kTok) {
-                        const int64_t sc = mine >= 0 ? scale_offset(c, pg, g, (int)((unsigned)tok % (unsigned)c.page)) : 0;
+                        const int64_t sc = mine >= 0 ? scale_offset(c, pg, g, tok - p.a.page_of(tok) * c.page) : 0;
                         copy_async<4>(at + R::kScales + lane * 8, c.k_scale + sc, mine >= 0);
                         copy_async<4>(at + R::kScales + lane * 8 + 4, c.v_scale + sc, mine >= 0);
                     }

@@ -60,6 +60,9 @@ struct Roles {
 constexpr int kRowsItem = 256;
 constexpr int kKeys = 128;              // keys of a tile
 constexpr int kSmem = 227 * 1024;
+// What an item costs beside its key tiles (queries, first maximum, output), in key tiles: it counts so many more in the division
+// of the work.  Seven requests of 192 to 650 new tokens, 5 to 33 tiles an item: KOVER_NOTE
+constexpr int kExtra = 2;
 constexpr int kMaxSeqs = 16384;         // their item counts are laid out in the (still empty) ring of key tiles
 
 struct Item {
@@ -141,19 +144,22 @@ struct Segment {
 };
 
 struct Walk {
-    int left, g, b, qt, from;       // tiles left; the next item and its first tile
+    int left, g, b, qt, from;       // units (tiles and kExtra an item) left; the next item and its first unit
 
     __device__ __forceinline__ bool next(const TcArgs& p, Segment& o) {
-        if (left == 0) return false;
-        o.s = load_seq(p.a.batch, p.a.cache.page, b);
-        o.it = item_of(p, o.s, b, qt);
-        o.g = g;
-        o.from = from;
-        o.to = min(o.it.tiles, from + left);
-        left -= o.to - from;
-        from = 0;
-        if (left > 0 && --qt < 0) next_seq(p);
-        return true;
+        while (left > 0) {
+            o.s = load_seq(p.a.batch, p.a.cache.page, b);
+            o.it = item_of(p, o.s, b, qt);
+            o.g = g;
+            o.from = from;
+            const int to = min(o.it.tiles + kExtra, from + left);
+            o.to = min(o.it.tiles, to);
+            left -= to - from;
+            from = 0;
+            if (left > 0 && --qt < 0) next_seq(p);
+            if (o.from < o.to) return true;         // else the run begins behind the item's last tile
+        }
+        return false;
     }
     // the next sequence that has rows here (there is one, as tiles are left), 32 of them at a time
     __device__ __forceinline__ void next_seq(const TcArgs& p) {
@@ -214,7 +220,7 @@ __device__ __forceinline__ void plan(const TcArgs& p, int* starts, int64_t* sums
         for (int j = j0; j < j1; ++j) {
             while (j >= starts[seq + 1]) ++seq;
             qt = starts[seq + 1] - 1 - j;
-            const int tiles = item_of(p, load_seq(p.a.batch, p.a.cache.page, seq), seq, qt).tiles;
+            const int tiles = item_of(p, load_seq(p.a.batch, p.a.cache.page, seq), seq, qt).tiles + kExtra;
             if (sum + tiles > stop) break;
             sum += tiles;
         }
@@ -231,8 +237,8 @@ __device__ __forceinline__ void plan(const TcArgs& p, int* starts, int64_t* sums
         if (before <= r && r < before + mine) {
             const int from = (int)(r - before - visit(r - before));
             *out = Walk{(int)left, g, seq, qt, from};
-            if (from > 0 && shares.at(c - 1) <= u - from) {
-                const Item it = item_of(p, load_seq(p.a.batch, p.a.cache.page, seq), seq, qt);
+            const Item it = item_of(p, load_seq(p.a.batch, p.a.cache.page, seq), seq, qt);
+            if (from > 0 && from < it.tiles && shares.at(c - 1) <= u - from) {
                 p.cuts[c] = Cut{1, seq, g, it.t0, shares.of(u - from + it.tiles - 1)};
             }
         }
@@ -743,94 +749,96 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
     } else if (!kSame && warp < kMma) {
       if constexpr (!kSame) {
         // ------------------------------ conversion of 8-bit rows ------------------------------
-        // A warp takes 16 rows of each tile; a lane 16 entries of a row, so that a row's lanes read it whole.  A
-        // piece is requested for the next tile as soon as it is converted for this one.
+        // A warp takes 16 rows of each tile, a lane 16 entries of each 64 of two rows (rl and rl + 8): eight lanes then store to eight
+        // different banks, and a row is read 64 bytes at a time.  A piece is requested for the next tile as soon as it is
+        // converted for this one.
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kConvertRegs));
         {
-            constexpr int kLanes = D / 16, kPass = kLanes / 2;          // lanes of a row; times to have 16 rows
+            constexpr int kBlocks = D / 64;
             const sp_cache& c = p.a.cache;
-            const int r0 = (warp - W::kSoftmax) * 16, lp = lane % kLanes, rl = lane / kLanes;
-            const uint32_t swap = D == 128 ? (lp >> 2) & 1 : 0;        // the two column blocks' stores take other banks
+            const int r0 = (warp - W::kSoftmax) * 16, sub = lane & 3, rl = lane >> 2;
+            const uint32_t dst0 = (r0 + rl) * 128 + (((2 * sub) ^ rl) << 4), dst1 = (r0 + rl) * 128 + (((2 * sub + 1) ^ rl) << 4);
             int st = 0;
             uint32_t ph = 1;
             bool ok = true;
             while (ok && walk.next(p, sg)) {
                 const int32_t* table = p.a.batch.table + (int64_t)sg.it.b * p.a.batch.table_stride;
                 const int seen = first_seen(sg.s, p.a.window);
-                // this lane's row of a tile: where it is (-1: nowhere) and its scales as pairs of bf16
+                // this lane's rows of a tile: where they are (-1: nowhere) and their scales as pairs of bf16
                 struct Where {
                     int64_t at;
                     uint32_t ks, vs;
                 };
-                auto page_of = [&](int x) {
-                    const int tok = tile_of(sg, x) * kKeys + r0 + (lane & 15);
-                    return tok < sg.s.kv && tok >= seen ? table[(unsigned)tok / (unsigned)c.page] : -1;
-                };
-                auto place = [&](int x, int pg) {
+                auto token = [&](int x, int y) { return tile_of(sg, x) * kKeys + r0 + rl + 8 * y; };
+                auto page_of = [&](int tok) { return tok < sg.s.kv && tok >= seen ? table[p.a.page_of(tok)] : -1; };
+                auto place = [&](int tok, int pg) {
                     Where w{-1, 0x3f803f80u, 0x3f803f80u};
-                    const int tok = tile_of(sg, x) * kKeys + r0 + (lane & 15);
                     if (tok >= sg.s.kv || tok < seen) return w;
                     if ((unsigned)pg >= (unsigned)c.pages) {
                         bad[1] = 1;
                         return w;
                     }
-                    const int slot = (int)((unsigned)tok % (unsigned)c.page);
-                    w.at = row_offset(c, pg, sg.g, slot);
+                    const int slot = tok - p.a.page_of(tok) * c.page;
+                    w.at = row_offset(c, pg, sg.g, slot) + sub * 16;
                     const int64_t sc = scale_offset(c, pg, sg.g, slot);
                     // a power of two (or NaN) is its upper half
                     w.ks = __byte_perm(__float_as_uint(__ldg(c.k_scale + sc)), 0, 0x3232);
                     w.vs = __byte_perm(__float_as_uint(__ldg(c.v_scale + sc)), 0, 0x3232);
                     return w;
                 };
-                auto fetch = [&](const void* data, int64_t at_lane, int ps) {
-                    const int64_t at = __shfl_sync(0xffffffffu, at_lane, ps * (32 / kLanes) + rl);
-                    return at >= 0 ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(data) + at + lp * 16))
+                auto fetch = [&](const void* data, int64_t at, int h) {
+                    return at >= 0 ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(data) + at + h * 64))
                                    : make_uint4(0, 0, 0, 0);
                 };
-                Where cur = place(sg.from, page_of(sg.from));
-                uint4 raw_codes[kPass];
+                Where cur[2], nxt[2];
+                int next_page[2];
+                uint4 codes[2][kBlocks];
 #pragma unroll
-                for (int ps = 0; ps < kPass; ++ps) raw_codes[ps] = fetch(c.k, cur.at, ps);
+                for (int y = 0; y < 2; ++y) {
+                    cur[y] = place(token(sg.from, y), page_of(token(sg.from, y)));
+#pragma unroll
+                    for (int h = 0; h < kBlocks; ++h) codes[y][h] = fetch(c.k, cur[y].at, h);
+                }
                 for (int x = sg.from; x < sg.to && ok; ++x) {
                     const bool more = x + 1 < sg.to;
-                    const int next_page = more ? page_of(x + 1) : -1;
-                    Where nxt = cur;
-#pragma unroll 1
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) next_page[y] = more ? page_of(token(x + 1, y)) : -1;
+#pragma unroll
                     for (int v = 0; v < 2; ++v) {
                         if (v == 1) {
-                            if (more) nxt = place(x + 1, next_page);
-                            else nxt.at = -1;
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                if (more) nxt[y] = place(token(x + 1, y), next_page[y]);
+                                else nxt[y].at = -1;
+                            }
                         }
                         ok = wait_warp(smem_u32(&empty[st]), ph, abort_flag, 61);
                         if (!ok) break;
                         uint8_t* tile = smem + L::kRing + st * L::kTileBytes;
-                        const uint32_t scale_lane = v ? cur.vs : cur.ks;
-                        const void* next_data = v ? c.k : c.v;
-                        const int64_t next_at = v ? nxt.at : cur.at;
 #pragma unroll
-                        for (int ps = 0; ps < kPass; ++ps) {
-                            const int rr = ps * (32 / kLanes) + rl, row = r0 + rr;
-                            const uint32_t scale = __shfl_sync(0xffffffffu, scale_lane, rr);
-                            const uint32_t w4[4] = {raw_codes[ps].x, raw_codes[ps].y, raw_codes[ps].z, raw_codes[ps].w};
-                            uint32_t o[8];
+                        for (int y = 0; y < 2; ++y)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                o[2 * i] = mul_bf16x2(pair_of<kKind>(__byte_perm(w4[i], 0, 0x1404)), scale);
-                                o[2 * i + 1] = mul_bf16x2(pair_of<kKind>(__byte_perm(w4[i], 0, 0x3424)), scale);
+                            for (int h = 0; h < kBlocks; ++h) {
+                                const uint32_t scale = v ? cur[y].vs : cur[y].ks;
+                                const uint32_t w4[4] = {codes[y][h].x, codes[y][h].y, codes[y][h].z, codes[y][h].w};
+                                uint32_t o[8];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    o[2 * i] = mul_bf16x2(pair_of<kKind>(__byte_perm(w4[i], 0, 0x1404)), scale);
+                                    o[2 * i + 1] = mul_bf16x2(pair_of<kKind>(__byte_perm(w4[i], 0, 0x3424)), scale);
+                                }
+                                codes[y][h] = v ? fetch(c.k, nxt[y].at, h) : fetch(c.v, cur[y].at, h);
+                                uint8_t* at = tile + y * 1024 + h * (kKeys * 128);
+                                *reinterpret_cast<uint4*>(at + dst0) = make_uint4(o[0], o[1], o[2], o[3]);
+                                *reinterpret_cast<uint4*>(at + dst1) = make_uint4(o[4], o[5], o[6], o[7]);
                             }
-                            raw_codes[ps] = fetch(next_data, next_at, ps);
-                            uint8_t* at = tile + (lp >> 2) * (kKeys * 128) + row * 128;
-                            const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
-                            const uint32_t p0 = (lp & 3) * 2;
-                            *reinterpret_cast<uint4*>(at + (((p0 + swap) ^ (row & 7)) << 4)) = swap ? b : a;
-                            *reinterpret_cast<uint4*>(at + (((p0 + 1 - swap) ^ (row & 7)) << 4)) = swap ? a : b;
-                        }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_u32(&full[st]));
                         if (++st == NS) st = 0, ph ^= 1;
                     }
-                    cur = nxt;
+                    cur[0] = nxt[0];
+                    cur[1] = nxt[1];
                 }
             }
         }
@@ -961,7 +969,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                     const int tok = tile_of(sg, x) * kKeys + lane * p.box;
                     slot = 0;
                     if (lane >= boxes || tok >= sg.s.kv || tok + p.box <= seen) return (int)c.pages;
-                    const int q = (int)((unsigned)tok / (unsigned)c.page), pg = table[q];
+                    const int q = p.a.page_of(tok), pg = table[q];
                     if (pg < 0 || pg >= c.pages) {
                         bad[1] = 1;
                         return (int)c.pages;

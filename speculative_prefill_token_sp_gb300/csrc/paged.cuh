@@ -253,6 +253,10 @@ struct AttendProblem {
     int H;
     float scale;
     int window;             // 0: none
+    int page_shift;         // log2 of the page, or -1: it is not a power of two
+    __device__ __forceinline__ int page_of(int tok) const {
+        return page_shift >= 0 ? tok >> page_shift : (int)((unsigned)tok / (unsigned)cache.page);
+    }
     float* lse;             // may be null
     int64_t lse_stride_row, lse_stride_head;
 };
