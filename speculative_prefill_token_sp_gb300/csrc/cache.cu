@@ -2,137 +2,241 @@
 // reading tokens back.
 //
 // Both directions move each row once and compute next to nothing, so they are
-// bound by memory, or by the launch for a decode step's few rows.  A group of
-// 2^g lanes (the smallest power of two that covers d / 8) holds one row, eight
-// entries a lane; the row's largest magnitude is a shuffle maximum over the
-// group, so a row is read once and quantised in registers.  The last block
-// checks what the batch's arrays say and is the only writer of the status.
+// bound by memory, or by the launch for a decode step's few rows.  A block takes
+// some tokens (of one head to read, so that its rows lie side by side on both
+// sides; of all heads to write, as the new rows come token by token) and works
+// out their places once, into shared memory.  A row is then held by a group of
+// 2^g lanes, kE entries a lane (16 codes of an 8-bit cache, 8 entries otherwise),
+// and a thread has several rows' loads, keys and values, under way at once.  A
+// row's largest magnitude is a shuffle maximum over its group, so it is read
+// once and quantised in registers.  The last block checks what the batch's
+// arrays say and is the only writer of the status.
 #include "paged.cuh"
+
+#include <algorithm>
 
 namespace sp {
 namespace {
 
 constexpr int kCacheThreads = 256;
+constexpr int kAhead = 2;           // rows whose loads a thread has under way
+constexpr int kMaxTokens = 256;     // tokens of a block
 
 struct MoveArgs {
     sp_cache c;
     sp_batch b;
     sp_rows k, v;           // data may be null (read)
     int lg;                 // log2 of the lanes of a row
+    int tokens;             // of a block
     WsHeader* hdr;
 };
 
-template <typename T, int kKind>
-__device__ __forceinline__ void write_row(const MoveArgs& p, const float (&x)[8], void* data, float* scales, int64_t at,
-                                          int64_t scale_at, int lane, bool act, bool there) {
+// kE entries as fp32.
+template <typename T, int kE>
+__device__ __forceinline__ void load_entries(const T* p, float (&x)[kE]) {
+#pragma unroll
+    for (int i = 0; i < kE; i += 8) load8(p + i, *reinterpret_cast<float(*)[8]>(x + i));
+}
+template <typename T, int kE>
+__device__ __forceinline__ void store_entries(T* p, const float (&x)[kE]) {
+#pragma unroll
+    for (int i = 0; i < kE; i += 8) store8(p + i, *reinterpret_cast<const float(*)[8]>(x + i));
+}
+
+// One side (keys or values) of a row on its way into the cache.
+template <typename T, int kKind, int kE>
+__device__ __forceinline__ void write_row(const MoveArgs& p, const float (&x)[kE], void* data, float* scales, int64_t at,
+                                          int64_t scale_at, int lane, bool there) {
     if constexpr (kKind == SP_CACHE_SAME) {
-        if (act && there) store8(static_cast<T*>(data) + at + lane * 8, x);
+        if (there) store_entries(static_cast<T*>(data) + at + lane * kE, x);
     } else {
         float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(x[i]));
+        for (int i = 0; i < kE; ++i) top = max_nan(top, fabsf(x[i]));
         for (int o = 1; o < (1 << p.lg); o <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (!there) return;
         const float scale = row_scale<kKind>(top);
-        if (!act || !there) return;
+        // 1 / scale, exact as the scale is a power of two; the codes of a row with a NaN or an infinity are 0
         const bool fine = scale == scale;
-        const uint2 u = fine ? encode8<kKind>(x, __int_as_float(0x7f000000 - __float_as_int(scale))) : make_uint2(0, 0);
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(data) + at + lane * 8) = u;
+        const float inv = __int_as_float(0x7f000000 - __float_as_int(scale));
+        uint2 u[kE / 8];
+#pragma unroll
+        for (int i = 0; i < kE; i += 8)
+            u[i / 8] = fine ? encode8<kKind>(*reinterpret_cast<const float(*)[8]>(x + i), inv) : make_uint2(0, 0);
+        uint8_t* dst = static_cast<uint8_t*>(data) + at + lane * kE;
+        if constexpr (kE == 16) *reinterpret_cast<uint4*>(dst) = make_uint4(u[0].x, u[0].y, u[1].x, u[1].y);
+        else *reinterpret_cast<uint2*>(dst) = u[0];
         if (lane == 0) scales[scale_at] = scale;
     }
 }
 
-template <typename T, int kKind>
+template <typename T, int kKind, int kE>
 __global__ void __launch_bounds__(kCacheThreads) write_kernel(const __grid_constant__ MoveArgs p) {
     if (blockIdx.x == gridDim.x - 1) {
         check_batch(p.b, p.c, p.hdr);
         return;
     }
-    const int64_t i = ((int64_t)blockIdx.x * kCacheThreads + threadIdx.x) >> p.lg;
-    const int lane = threadIdx.x & ((1 << p.lg) - 1);
-    const bool act = i < p.b.T * p.c.H_kv && lane * 8 < p.c.d;
-    const int64_t r = act ? i / p.c.H_kv : 0;
-    const int h = act ? (int)(i - r * p.c.H_kv) : 0;
-    float x[8] = {}, y[8] = {};
-    if (act) {
-        load8(static_cast<const T*>(p.k.data) + r * p.k.stride_row + h * p.k.stride_head + lane * 8, x);
-        load8(static_cast<const T*>(p.v.data) + r * p.v.stride_row + h * p.v.stride_head + lane * 8, y);
+    __shared__ int2 places[kMaxTokens];
+    const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
+    const int n = (int)min((int64_t)p.tokens, p.b.T - t0);
+    for (int t = threadIdx.x; t < n; t += kCacheThreads) {
+        const Place pl = place_of_row(p.b, p.c, t0 + t);
+        places[t] = make_int2(pl.page, pl.slot);
     }
-    const Place pl = act ? place_of_row(p.b, p.c, r) : Place{-1, 0, false};
-    const bool there = pl.page >= 0;
-    const int64_t at = row_offset(p.c, pl.page, h, pl.slot), sat = scale_offset(p.c, pl.page, h, pl.slot);
-    write_row<T, kKind>(p, x, p.c.k, p.c.k_scale, at, sat, lane, act, there);
-    write_row<T, kKind>(p, y, p.c.v, p.c.v_scale, at, sat, lane, act, there);
-}
-
-template <typename T, int kKind>
-__device__ __forceinline__ void read_row(const void* data, const float* scales, int64_t at, int64_t scale_at, int lane,
-                                         bool there, T* dst) {
-    float x[8] = {};
-    if (there) {
-        if constexpr (kKind == SP_CACHE_SAME) {
-            load8(static_cast<const T*>(data) + at + lane * 8, x);
-        } else {
-            decode8<kKind>(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(data) + at + lane * 8), x);
-            const float s = scales[scale_at];
+    __syncthreads();
+    const int lane = threadIdx.x & ((1 << p.lg) - 1), rows = n * p.c.H_kv, step = kCacheThreads >> p.lg;
+    const bool act = lane * kE < p.c.d;
+    // all lanes of a warp go round together: the rows' maxima are shuffles
+    for (int r0 = threadIdx.x >> p.lg; r0 - (int)(threadIdx.x >> p.lg) < rows; r0 += kAhead * step) {
+        float x[kAhead][kE], y[kAhead][kE];
+        int t[kAhead], h[kAhead];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] *= s;
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = r0 + i * step;
+            t[i] = r < rows ? r / p.c.H_kv : -1;
+            h[i] = r - t[i] * p.c.H_kv;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) x[i][e] = y[i][e] = 0.f;
+            if (t[i] >= 0 && act) {
+                load_entries(static_cast<const T*>(p.k.data) + (t0 + t[i]) * p.k.stride_row + h[i] * p.k.stride_head + lane * kE, x[i]);
+                load_entries(static_cast<const T*>(p.v.data) + (t0 + t[i]) * p.v.stride_row + h[i] * p.v.stride_head + lane * kE, y[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int2 pl = t[i] >= 0 ? places[t[i]] : make_int2(-1, 0);
+            const bool there = pl.x >= 0 && act;
+            const int64_t at = row_offset(p.c, pl.x, h[i], pl.y), sat = scale_offset(p.c, pl.x, h[i], pl.y);
+            write_row<T, kKind, kE>(p, x[i], p.c.k, p.c.k_scale, at, sat, lane, there);
+            write_row<T, kKind, kE>(p, y[i], p.c.v, p.c.v_scale, at, sat, lane, there);
         }
     }
-    store8(dst + lane * 8, x);
 }
 
-template <typename T, int kKind>
+// One side of a row in the cache, as it is loaded, and its entries.
+template <typename T, int kKind, int kE>
+struct Held {
+    static constexpr int kWords = kKind == SP_CACHE_SAME ? kE * (int)sizeof(T) / 4 : kE / 4;
+    uint32_t w[kWords];
+    float scale;
+    __device__ __forceinline__ void load(const void* data, const float* scales, int64_t at, int64_t scale_at, int lane) {
+        const char* src = static_cast<const char*>(data) + (at + lane * kE) * (kKind == SP_CACHE_SAME ? (int)sizeof(T) : 1);
+        if constexpr (kWords == 2) {
+            const uint2 u = *reinterpret_cast<const uint2*>(src);
+            w[0] = u.x; w[1] = u.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) {
+                const uint4 u = reinterpret_cast<const uint4*>(src)[i / 4];
+                w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
+            }
+        }
+        if constexpr (kKind != SP_CACHE_SAME) scale = scales[scale_at];
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+        scale = 1.f;
+    }
+    __device__ __forceinline__ void store(T* dst) const {
+        if constexpr (kKind == SP_CACHE_SAME) {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) reinterpret_cast<uint4*>(dst)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        } else {
+            float x[kE];
+#pragma unroll
+            for (int i = 0; i < kE; i += 8) {
+                float(&v)[8] = *reinterpret_cast<float(*)[8]>(x + i);
+                decode8<kKind>(make_uint2(w[i / 4], w[i / 4 + 1]), v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] *= scale;
+            }
+            store_entries(dst, x);
+        }
+    }
+};
+
+template <typename T, int kKind, int kE>
 __global__ void __launch_bounds__(kCacheThreads) read_kernel(const __grid_constant__ MoveArgs p) {
     if (blockIdx.x == gridDim.x - 1) {
         if (blockIdx.y == 0) check_batch(p.b, p.c, p.hdr);
         return;
     }
-    const int64_t r = ((int64_t)blockIdx.x * kCacheThreads + threadIdx.x) >> p.lg;
-    const int lane = threadIdx.x & ((1 << p.lg) - 1), h = blockIdx.y;
-    if (r >= p.b.T || lane * 8 >= p.c.d) return;
-    const Place pl = place_of_row(p.b, p.c, r);
-    if (!pl.token) return;
-    const bool there = pl.page >= 0;
-    const int64_t at = row_offset(p.c, pl.page, h, pl.slot), sat = scale_offset(p.c, pl.page, h, pl.slot);
-    if (p.k.data)
-        read_row<T, kKind>(p.c.k, p.c.k_scale, at, sat, lane, there,
-                           static_cast<T*>(p.k.data) + r * p.k.stride_row + h * p.k.stride_head);
-    if (p.v.data)
-        read_row<T, kKind>(p.c.v, p.c.v_scale, at, sat, lane, there,
-                           static_cast<T*>(p.v.data) + r * p.v.stride_row + h * p.v.stride_head);
+    __shared__ int2 places[kMaxTokens];         // page (-1: zeros, -2: no token) and slot
+    const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
+    const int n = (int)min((int64_t)p.tokens, p.b.T - t0);
+    for (int t = threadIdx.x; t < n; t += kCacheThreads) {
+        const Place pl = place_of_row(p.b, p.c, t0 + t);
+        places[t] = make_int2(pl.token ? pl.page : -2, pl.slot);
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & ((1 << p.lg) - 1), h = blockIdx.y, step = kCacheThreads >> p.lg;
+    if (lane * kE >= p.c.d) return;
+    T* out_k = static_cast<T*>(p.k.data);
+    T* out_v = static_cast<T*>(p.v.data);
+    for (int r0 = threadIdx.x >> p.lg; r0 < n; r0 += kAhead * step) {
+        Held<T, kKind, kE> x[kAhead], y[kAhead];
+        int2 pl[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            pl[i] = r0 + i * step < n ? places[r0 + i * step] : make_int2(-2, 0);
+            x[i].zero();
+            y[i].zero();
+            if (pl[i].x < 0) continue;
+            const int64_t at = row_offset(p.c, pl[i].x, h, pl[i].y), sat = scale_offset(p.c, pl[i].x, h, pl[i].y);
+            if (out_k) x[i].load(p.c.k, p.c.k_scale, at, sat, lane);
+            if (out_v) y[i].load(p.c.v, p.c.v_scale, at, sat, lane);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (pl[i].x == -2) continue;
+            const int64_t r = t0 + r0 + i * step;
+            if (out_k) x[i].store(out_k + r * p.k.stride_row + h * p.k.stride_head + lane * kE);
+            if (out_v) y[i].store(out_v + r * p.v.stride_row + h * p.v.stride_head + lane * kE);
+        }
+    }
+}
+
+template <typename T, int kKind, int kE>
+void launch_one(bool write, MoveArgs a, cudaStream_t st) {
+    while ((kE << a.lg) < a.c.d) ++a.lg;
+    // about kAhead rows a thread, and few enough tokens for every SM to have a block
+    const int per_token = (write ? a.c.H_kv : 1) << a.lg;
+    const int64_t all = write ? a.b.T : a.b.T * a.c.H_kv;
+    const int64_t want = std::min<int64_t>((int64_t)kAhead * kCacheThreads / per_token, (all + 2 * sm_count() - 1) / (2 * sm_count()));
+    a.tokens = (int)std::max<int64_t>(1, std::min<int64_t>(want, kMaxTokens));
+    const dim3 grid((unsigned)((a.b.T + a.tokens - 1) / a.tokens + 1), write ? 1u : (unsigned)a.c.H_kv);
+    if (write) write_kernel<T, kKind, kE><<<grid, kCacheThreads, 0, st>>>(a);
+    else read_kernel<T, kKind, kE><<<grid, kCacheThreads, 0, st>>>(a);
 }
 
 template <typename T>
-void launch_kind(bool write, const MoveArgs& a, dim3 grid, cudaStream_t st) {
+void launch_kind(bool write, const MoveArgs& a, cudaStream_t st) {
+    const bool wide = a.c.d % 16 == 0 &&
+                      (reinterpret_cast<uintptr_t>(a.c.k) | reinterpret_cast<uintptr_t>(a.c.v) | (uintptr_t)a.c.stride_page |
+                       (uintptr_t)a.c.stride_head | (uintptr_t)a.c.stride_slot) % 16 == 0;
     switch (a.c.kind) {
-        case SP_CACHE_SAME:
-            if (write) write_kernel<T, SP_CACHE_SAME><<<grid, kCacheThreads, 0, st>>>(a);
-            else read_kernel<T, SP_CACHE_SAME><<<grid, kCacheThreads, 0, st>>>(a);
-            break;
+        case SP_CACHE_SAME: launch_one<T, SP_CACHE_SAME, 8>(write, a, st); break;
         case SP_CACHE_E4M3:
-            if (write) write_kernel<T, SP_CACHE_E4M3><<<grid, kCacheThreads, 0, st>>>(a);
-            else read_kernel<T, SP_CACHE_E4M3><<<grid, kCacheThreads, 0, st>>>(a);
+            if (wide) launch_one<T, SP_CACHE_E4M3, 16>(write, a, st);
+            else launch_one<T, SP_CACHE_E4M3, 8>(write, a, st);
             break;
         case SP_CACHE_INT8:
-            if (write) write_kernel<T, SP_CACHE_INT8><<<grid, kCacheThreads, 0, st>>>(a);
-            else read_kernel<T, SP_CACHE_INT8><<<grid, kCacheThreads, 0, st>>>(a);
+            if (wide) launch_one<T, SP_CACHE_INT8, 16>(write, a, st);
+            else launch_one<T, SP_CACHE_INT8, 8>(write, a, st);
             break;
     }
 }
 
 sp_status move_launch(bool write, const sp_cache& c, const sp_batch& b, const sp_rows& k, const sp_rows& v, void* ws,
                       cudaStream_t st) {
-    MoveArgs a{c, b, k, v, 0, static_cast<WsHeader*>(ws)};
-    while ((8 << a.lg) < c.d) ++a.lg;
-    const int64_t rows = write ? b.T * c.H_kv : b.T;
-    const int64_t blocks = ((rows << a.lg) + kCacheThreads - 1) / kCacheThreads + 1;
-    if (blocks > INT32_MAX) {
-        set_error("%s: %lld rows are too many for one call", write ? "sp_cache_write" : "sp_cache_read", (long long)rows);
+    const MoveArgs a{c, b, k, v, 0, 0, static_cast<WsHeader*>(ws)};
+    if (!write && c.H_kv > 65535) {
+        set_error("sp_cache_read: at most 65535 KV heads (got %d)", c.H_kv);
         return SP_EUNSUPPORTED;
     }
-    const dim3 grid((unsigned)blocks, write ? 1u : (unsigned)c.H_kv);
-    if (c.dtype == SP_BF16) launch_kind<__nv_bfloat16>(write, a, grid, st);
-    else launch_kind<float>(write, a, grid, st);
+    if (c.dtype == SP_BF16) launch_kind<__nv_bfloat16>(write, a, st);
+    else launch_kind<float>(write, a, st);
     SP_LAUNCH_CHECK();
     return SP_OK;
 }
