@@ -27,23 +27,31 @@ struct RotArgs {
 };
 
 // Rotates eight pairs: x0/x1 hold the pairs' entries (half layout: the two
-// halves' entries; interleaved: 16 consecutive entries).
-__device__ __forceinline__ void rotate8(float (&x0)[8], float (&x1)[8], const float2* cs, float sign, bool inter) {
+// halves' entries; interleaved: 16 consecutive entries).  cs: cosines and sines of
+// two pairs each, `stride` apart.
+__device__ __forceinline__ void rotate8(float (&x0)[8], float (&x1)[8], const float4* cs, int stride, float sign, bool inter) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float c = cs[i].x, s = cs[i].y * sign;
-        float& a = inter ? (i < 4 ? x0[(2 * i) & 7] : x1[(2 * i) & 7]) : x0[i];
-        float& b = inter ? (i < 4 ? x0[(2 * i + 1) & 7] : x1[(2 * i + 1) & 7]) : x1[i];
-        const float u = a, v = b;
-        a = u * c - v * s;
-        b = v * c + u * s;
+    for (int k = 0; k < 4; ++k) {
+        const float4 v = cs[k * stride];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int i = 2 * k + y;
+            const float c = y ? v.z : v.x, s = (y ? v.w : v.y) * sign;
+            float& a = inter ? (i < 4 ? x0[(2 * i) & 7] : x1[(2 * i) & 7]) : x0[i];
+            float& b = inter ? (i < 4 ? x0[(2 * i + 1) & 7] : x1[(2 * i + 1) & 7]) : x1[i];
+            const float u = a, w = b;
+            a = u * c - w * s;
+            b = w * c + u * s;
+        }
     }
 }
 
 template <typename T, bool kInter>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotArgs p) {
-    extern __shared__ float2 cs[];      // [tokens][pairs]: cosine, sine
-    const int pairs = p.plan.rot / 2;
+    // [tokens][4][pairs / 8] cosine, sine of pairs 8c + 2k and 8c + 2k + 1 at (k, c): a warp's lanes have consecutive c, so
+    // they read consecutive 16 bytes
+    extern __shared__ float4 cs[];
+    const int pairs = p.plan.rot / 2, rc = pairs / 8;
     const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
     const int nt = (int)min((int64_t)p.tokens, p.T - t0);
     for (int i = threadIdx.x; i < nt * pairs; i += kRotThreads) {
@@ -52,22 +60,26 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
         const int32_t half_turns = (int32_t)(((uint64_t)at * p.plan.turns[j]) >> 32);
         float s, c;
         sincospif((float)half_turns * 0x1p-31f, &s, &c);
-        cs[i] = make_float2(c, s);
+        reinterpret_cast<float2*>(cs)[((t * 4 + ((j & 7) >> 1)) * rc + (j >> 3)) * 2 + (j & 1)] = make_float2(c, s);
     }
     __syncthreads();
-    // an item: one head's chunk of eight pairs, or of eight entries past rot
-    const int rc = pairs / 8, chunks = rc + (p.d - p.plan.rot) / 8;
-    const int heads = p.H + p.Hk, per = heads * chunks;
-    for (int i = blockIdx.y * kRotThreads + threadIdx.x; i < nt * per; i += gridDim.y * kRotThreads) {
-        const int t = i / per, r = i - t * per;
-        int h = r / chunks;
-        const int c = r - h * chunks;
+    // a thread has one chunk, of eight pairs or of eight entries past rot, of every so many heads
+    const int chunks = rc + (p.d - p.plan.rot) / 8, heads = p.H + p.Hk, sweep = kRotThreads / chunks;
+    const int c = threadIdx.x % chunks, first = threadIdx.x / chunks;
+    if (first >= sweep) return;
+    int h = first + blockIdx.y * sweep, t = 0;
+    for (;; h += sweep * gridDim.y) {
+        while (h >= heads) {
+            h -= heads;
+            ++t;
+        }
+        if (t >= nt) return;
         const bool isq = h < p.H;
-        if (!isq) h -= p.H;
         const sp_rows& in = isq ? p.q : p.k;
         const sp_rows& out = isq ? p.qo : p.ko;
-        const T* src = static_cast<const T*>(in.data) + (t0 + t) * in.stride_row + h * in.stride_head;
-        T* dst = static_cast<T*>(out.data) + (t0 + t) * out.stride_row + h * out.stride_head;
+        const int hh = isq ? h : h - p.H;
+        const T* src = static_cast<const T*>(in.data) + (t0 + t) * in.stride_row + hh * in.stride_head;
+        T* dst = static_cast<T*>(out.data) + (t0 + t) * out.stride_row + hh * out.stride_head;
         float x0[8], x1[8];
         if (c >= rc) {
             const int e = p.plan.rot + (c - rc) * 8;
@@ -78,7 +90,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
         const int e0 = kInter ? c * 16 : c * 8, e1 = kInter ? c * 16 + 8 : pairs + c * 8;
         load8(src + e0, x0);
         load8(src + e1, x1);
-        rotate8(x0, x1, cs + t * pairs + c * 8, p.sign, kInter);
+        rotate8(x0, x1, cs + t * 4 * rc + c, rc, p.sign, kInter);
         store8(dst + e0, x0);
         store8(dst + e1, x1);
     }
@@ -95,7 +107,7 @@ sp_status rotary_launch(const sp_rotary_plan& plan, const int32_t* pos, int64_t 
     a.pos = pos; a.pos_stride = pos_stride; a.T = T; a.d = d; a.H = H; a.Hk = Hk;
     a.sign = inverse ? -1.f : 1.f;
     a.q = q; a.qo = qo; a.k = k; a.ko = ko;
-    a.tokens = 4;
+    a.tokens = 2;
     const int64_t blocks = (T + a.tokens - 1) / a.tokens;
     const int per = (H + Hk) * (plan.rot / 16 + (d - plan.rot) / 8) * a.tokens;
     // few tokens: several blocks share a token's heads
