@@ -11,13 +11,20 @@
 // then runs over all the heads of q and k with 16-byte loads and stores.
 #include "paged.cuh"
 
+#include <algorithm>
+
 namespace sp {
 namespace {
 
 constexpr int kRotThreads = 256;
 
+// What the kernel takes of a plan of at most kPairs pairs: a launch's cost on the host grows with its arguments (1.4 KB of them
+// took LAUNCH_NOTE).
+template <int kPairs>
 struct RotArgs {
-    sp_rotary_plan plan;
+    int rot;
+    uint64_t turns[kPairs];
+    uint8_t axis[kPairs];
     const int32_t* pos;
     int64_t pos_stride, T;
     int d, H, Hk;
@@ -46,25 +53,25 @@ __device__ __forceinline__ void rotate8(float (&x0)[8], float (&x1)[8], const fl
     }
 }
 
-template <typename T, bool kInter>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotArgs p) {
+template <typename T, bool kInter, int kPairs>
+__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotArgs<kPairs> p) {
     // [tokens][4][pairs / 8] cosine, sine of pairs 8c + 2k and 8c + 2k + 1 at (k, c): a warp's lanes have consecutive c, so
     // they read consecutive 16 bytes
     extern __shared__ float4 cs[];
-    const int pairs = p.plan.rot / 2, rc = pairs / 8;
+    const int pairs = p.rot / 2, rc = pairs / 8;
     const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
     const int nt = (int)min((int64_t)p.tokens, p.T - t0);
     for (int i = threadIdx.x; i < nt * pairs; i += kRotThreads) {
         const int t = i / pairs, j = i - t * pairs;
-        const int64_t at = p.pos[p.plan.axis[j] * p.pos_stride + t0 + t];
-        const int32_t half_turns = (int32_t)(((uint64_t)at * p.plan.turns[j]) >> 32);
+        const int64_t at = p.pos[p.axis[j] * p.pos_stride + t0 + t];
+        const int32_t half_turns = (int32_t)(((uint64_t)at * p.turns[j]) >> 32);
         float s, c;
         sincospif((float)half_turns * 0x1p-31f, &s, &c);
         reinterpret_cast<float2*>(cs)[((t * 4 + ((j & 7) >> 1)) * rc + (j >> 3)) * 2 + (j & 1)] = make_float2(c, s);
     }
     __syncthreads();
     // a thread has one chunk, of eight pairs or of eight entries past rot, of every so many heads
-    const int chunks = rc + (p.d - p.plan.rot) / 8, heads = p.H + p.Hk, sweep = kRotThreads / chunks;
+    const int chunks = rc + (p.d - p.rot) / 8, heads = p.H + p.Hk, sweep = kRotThreads / chunks;
     const int c = threadIdx.x % chunks, first = threadIdx.x / chunks;
     if (first >= sweep) return;
     int h = first + blockIdx.y * sweep, t = 0;
@@ -82,7 +89,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
         T* dst = static_cast<T*>(out.data) + (t0 + t) * out.stride_row + hh * out.stride_head;
         float x0[8], x1[8];
         if (c >= rc) {
-            const int e = p.plan.rot + (c - rc) * 8;
+            const int e = p.rot + (c - rc) * 8;
             load8(src + e, x0);
             store8(dst + e, x0);
             continue;
@@ -96,33 +103,46 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
     }
 }
 
+template <typename T, int kPairs>
+sp_status launch(const sp_rotary_plan& plan, RotArgs<kPairs> a, cudaStream_t st) {
+    const int rot = plan.rot;
+    a.rot = rot;
+    for (int i = 0; i < rot / 2; ++i) {
+        a.turns[i] = plan.turns[i];
+        a.axis[i] = plan.axis[i];
+    }
+    a.tokens = 2;
+    const int64_t blocks = (a.T + a.tokens - 1) / a.tokens;
+    const int per = (a.H + a.Hk) * (rot / 16 + (a.d - rot) / 8) * a.tokens;
+    // few tokens: several blocks share a token's heads
+    const int split = blocks >= 608 ? 1 : (int)std::min<int64_t>((per + kRotThreads - 1) / kRotThreads, (608 + blocks - 1) / blocks);
+    const size_t smem = (size_t)a.tokens * (rot / 2) * sizeof(float2);
+    const dim3 grid((unsigned)blocks, (unsigned)std::max(1, split));
+    if (plan.interleaved) rotary_kernel<T, true, kPairs><<<grid, kRotThreads, smem, st>>>(a);
+    else rotary_kernel<T, false, kPairs><<<grid, kRotThreads, smem, st>>>(a);
+    SP_LAUNCH_CHECK();
+    return SP_OK;
+}
+
+template <int kPairs>
+sp_status fill(const sp_rotary_plan& plan, const int32_t* pos, int64_t pos_stride, int64_t T, int d, sp_dtype dtype, bool inverse,
+               const sp_rows& q, const sp_rows& qo, int H, const sp_rows& k, const sp_rows& ko, int Hk, cudaStream_t st) {
+    RotArgs<kPairs> a;
+    a.pos = pos; a.pos_stride = pos_stride; a.T = T; a.d = d; a.H = H; a.Hk = Hk;
+    a.sign = inverse ? -1.f : 1.f;
+    a.q = q; a.qo = qo; a.k = k; a.ko = ko;
+    return dtype == SP_BF16 ? launch<__nv_bfloat16>(plan, a, st) : launch<float>(plan, a, st);
+}
+
 }  // namespace
 
 sp_status rotary_launch(const sp_rotary_plan& plan, const int32_t* pos, int64_t pos_stride, int64_t T, int d,
                         sp_dtype dtype, bool inverse, const sp_rows& q, const sp_rows& qo, int H, const sp_rows& k,
                         const sp_rows& ko, int Hk, cudaStream_t st) {
     if (T == 0 || H + Hk == 0) return SP_OK;
-    RotArgs a;
-    a.plan = plan;
-    a.pos = pos; a.pos_stride = pos_stride; a.T = T; a.d = d; a.H = H; a.Hk = Hk;
-    a.sign = inverse ? -1.f : 1.f;
-    a.q = q; a.qo = qo; a.k = k; a.ko = ko;
-    a.tokens = 2;
-    const int64_t blocks = (T + a.tokens - 1) / a.tokens;
-    const int per = (H + Hk) * (plan.rot / 16 + (d - plan.rot) / 8) * a.tokens;
-    // few tokens: several blocks share a token's heads
-    const int split = blocks >= 608 ? 1 : (int)std::min<int64_t>((per + kRotThreads - 1) / kRotThreads, (608 + blocks - 1) / blocks);
-    const size_t smem = (size_t)a.tokens * (plan.rot / 2) * sizeof(float2);
-    const dim3 grid((unsigned)blocks, (unsigned)std::max(1, split));
-    if (dtype == SP_BF16) {
-        if (plan.interleaved) rotary_kernel<__nv_bfloat16, true><<<grid, kRotThreads, smem, st>>>(a);
-        else rotary_kernel<__nv_bfloat16, false><<<grid, kRotThreads, smem, st>>>(a);
-    } else {
-        if (plan.interleaved) rotary_kernel<float, true><<<grid, kRotThreads, smem, st>>>(a);
-        else rotary_kernel<float, false><<<grid, kRotThreads, smem, st>>>(a);
-    }
-    SP_LAUNCH_CHECK();
-    return SP_OK;
+    return plan.rot <= 64    ? fill<32>(plan, pos, pos_stride, T, d, dtype, inverse, q, qo, H, k, ko, Hk, st)
+           : plan.rot <= 128 ? fill<64>(plan, pos, pos_stride, T, d, dtype, inverse, q, qo, H, k, ko, Hk, st)
+                             : fill<128>(plan, pos, pos_stride, T, d, dtype, inverse, q, qo, H, k, ko, Hk, st);
 }
 
 }  // namespace sp
