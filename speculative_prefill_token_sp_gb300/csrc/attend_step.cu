@@ -417,9 +417,7 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
                             if constexpr (kSame) {
                                 a[y] = __byte_perm(vr[i2].w[w], vr[i2 + 1].w[w], y & 1 ? 0x7632 : 0x5410);
                             } else {
-                                // the first token's byte to bits 8-15, the second's to bits 24-31
-                                const uint32_t i4 = (e + (y & 1)) & 3, sel = 0x4000u + (i4 << 12) + (i4 << 4);
-                                a[y] = pair_of<kKind>(__byte_perm(vr[i2].w[w], vr[i2 + 1].w[w], sel));
+                                a[y] = codes_of<kKind>(vr[i2].w[w], vr[i2 + 1].w[w], (e + (y & 1)) & 3);
                             }
                         }
 #pragma unroll

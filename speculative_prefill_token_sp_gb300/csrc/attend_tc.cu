@@ -764,15 +764,16 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
             while (ok && walk.next(p, sg)) {
                 const int32_t* table = p.a.batch.table + (int64_t)sg.it.b * p.a.batch.table_stride;
                 const int seen = first_seen(sg.s, p.a.window);
-                // this lane's rows of a tile: where they are (-1: nowhere) and their scales as pairs of bf16
+                // this lane's rows of a tile: where they are (-1: nowhere) and their scales, which are not touched before the
+                // tile's turn (waiting for them here took a third of the warps' time)
                 struct Where {
                     int64_t at;
-                    uint32_t ks, vs;
+                    float ks, vs;
                 };
                 auto token = [&](int x, int y) { return tile_of(sg, x) * kKeys + r0 + rl + 8 * y; };
                 auto page_of = [&](int tok) { return tok < sg.s.kv && tok >= seen ? table[p.a.page_of(tok)] : -1; };
                 auto place = [&](int tok, int pg) {
-                    Where w{-1, 0x3f803f80u, 0x3f803f80u};
+                    Where w{-1, 1.f, 1.f};
                     if (tok >= sg.s.kv || tok < seen) return w;
                     if ((unsigned)pg >= (unsigned)c.pages) {
                         bad[1] = 1;
@@ -781,9 +782,8 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                     const int slot = tok - p.a.page_of(tok) * c.page;
                     w.at = row_offset(c, pg, sg.g, slot) + sub * 16;
                     const int64_t sc = scale_offset(c, pg, sg.g, slot);
-                    // a power of two (or NaN) is its upper half
-                    w.ks = __byte_perm(__float_as_uint(__ldg(c.k_scale + sc)), 0, 0x3232);
-                    w.vs = __byte_perm(__float_as_uint(__ldg(c.v_scale + sc)), 0, 0x3232);
+                    w.ks = __ldg(c.k_scale + sc);
+                    w.vs = __ldg(c.v_scale + sc);
                     return w;
                 };
                 auto fetch = [&](const void* data, int64_t at, int h) {
@@ -816,22 +816,24 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                         if (!ok) break;
                         uint8_t* tile = smem + L::kRing + st * L::kTileBytes;
 #pragma unroll
-                        for (int y = 0; y < 2; ++y)
+                        for (int y = 0; y < 2; ++y) {
+                            // as a pair of bf16: a power of two (or NaN) is its upper half
+                            const uint32_t scale = __byte_perm(__float_as_uint(v ? cur[y].vs : cur[y].ks), 0, 0x3232);
 #pragma unroll
                             for (int h = 0; h < kBlocks; ++h) {
-                                const uint32_t scale = v ? cur[y].vs : cur[y].ks;
                                 const uint32_t w4[4] = {codes[y][h].x, codes[y][h].y, codes[y][h].z, codes[y][h].w};
                                 uint32_t o[8];
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
-                                    o[2 * i] = mul_bf16x2(pair_of<kKind>(__byte_perm(w4[i], 0, 0x1404)), scale);
-                                    o[2 * i + 1] = mul_bf16x2(pair_of<kKind>(__byte_perm(w4[i], 0, 0x3424)), scale);
+                                    o[2 * i] = mul_bf16x2(codes_of<kKind>(w4[i], 0), scale);
+                                    o[2 * i + 1] = mul_bf16x2(codes_of<kKind>(w4[i], 1), scale);
                                 }
                                 codes[y][h] = v ? fetch(c.k, nxt[y].at, h) : fetch(c.v, cur[y].at, h);
                                 uint8_t* at = tile + y * 1024 + h * (kKeys * 128);
                                 *reinterpret_cast<uint4*>(at + dst0) = make_uint4(o[0], o[1], o[2], o[3]);
                                 *reinterpret_cast<uint4*>(at + dst1) = make_uint4(o[4], o[5], o[6], o[7]);
                             }
+                        }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_u32(&full[st]));

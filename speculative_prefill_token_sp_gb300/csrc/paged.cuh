@@ -136,8 +136,8 @@ __device__ __forceinline__ void decode8(uint2 u, float (&x)[8]) {
     }
 }
 
-// Two 8-bit codes, in bits 8-15 and 24-31 of y (the other bits are ignored),
-// as a pair of bf16 (their values before the scale, exactly).
+// Two 8-bit codes as a pair of bf16 (their values before the scale, exactly).  The codes are brought to where they are needed
+// by a byte permute: bits 8-15 and 24-31 of y for e4m3, bits 0-7 and 16-23 for int8; the other bits are ignored.
 template <int kKind>
 __device__ __forceinline__ uint32_t pair_of(uint32_t y) {
     uint32_t r;
@@ -148,10 +148,19 @@ __device__ __forceinline__ uint32_t pair_of(uint32_t y) {
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(0x7b807b80u));
     } else {
         // 0x4300 + (7 bits) is 128 + those bits; minus 128, or minus 256 (0x4380) where the sign bit is set
-        const uint32_t lo = ((y >> 8) & 0x007f007fu) | 0x43004300u, off = ((y >> 8) & 0x00800080u) | 0x43004300u;
+        const uint32_t lo = (y & 0x007f007fu) | 0x43004300u, off = (y & 0x00800080u) | 0x43004300u;
         asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(lo), "r"(off));
     }
     return r;
+}
+// Codes 2j and 2j + 1 of a word, and code i of one word with code i of another.
+template <int kKind>
+__device__ __forceinline__ uint32_t codes_of(uint32_t w, int j) {
+    return pair_of<kKind>(__byte_perm(w, 0, kKind == SP_CACHE_E4M3 ? (j ? 0x3424 : 0x1404) : (j ? 0x4342 : 0x4140)));
+}
+template <int kKind>
+__device__ __forceinline__ uint32_t codes_of(uint32_t a, uint32_t b, int i) {
+    return pair_of<kKind>(__byte_perm(a, b, kKind == SP_CACHE_E4M3 ? 0x4000 + (i << 12) + (i << 4) : 0x0400 + (i << 8) + i));
 }
 
 // The scale of a row whose largest magnitude is `top` (NaN or infinite if an
