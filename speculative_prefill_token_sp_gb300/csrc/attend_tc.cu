@@ -61,8 +61,9 @@ constexpr int kRowsItem = 256;
 constexpr int kKeys = 128;              // keys of a tile
 constexpr int kSmem = 227 * 1024;
 // What an item costs beside its key tiles (queries, first maximum, output), in key tiles: it counts so many more in the division
-// of the work.  Seven requests of 192 to 650 new tokens, 5 to 33 tiles an item: KOVER_NOTE
-constexpr int kExtra = 2;
+// of the work.  Seven requests of 192 to 650 new tokens, 5 to 33 tiles an item, took 162, 142, 132, 128, 126 us with 0 to 4 (bf16) and
+// 203, 189, 175, 169, 173 us (int8).
+constexpr int kExtra = 3;
 constexpr int kMaxSeqs = 16384;         // their item counts are laid out in the (still empty) ring of key tiles
 
 struct Item {
@@ -72,7 +73,8 @@ struct Item {
 
 // What the joining kernel has to know of CTA c: whether its run begins inside an item that no CTA before has cut.
 struct Cut {
-    int first, b, g, t0;
+    int first, g, t0, n;    // KV head, first new token, new tokens of the sequence
+    int64_t row0;           // first row of the sequence
     int last;               // the CTA of the item's last tile
 };
 
@@ -237,9 +239,10 @@ __device__ __forceinline__ void plan(const TcArgs& p, int* starts, int64_t* sums
         if (before <= r && r < before + mine) {
             const int from = (int)(r - before - visit(r - before));
             *out = Walk{(int)left, g, seq, qt, from};
-            const Item it = item_of(p, load_seq(p.a.batch, p.a.cache.page, seq), seq, qt);
+            const Seq s = load_seq(p.a.batch, p.a.cache.page, seq);
+            const Item it = item_of(p, s, seq, qt);
             if (from > 0 && from < it.tiles && shares.at(c - 1) <= u - from) {
-                p.cuts[c] = Cut{1, seq, g, it.t0, shares.of(u - from + it.tiles - 1)};
+                p.cuts[c] = Cut{1, g, it.t0, s.n, s.row0, shares.of(u - from + it.tiles - 1)};
             }
         }
     }
@@ -657,7 +660,9 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                         float* v = kSame ? sv + 32 * c : sv;
                         if constexpr (!kSame) tmem_ld32(s_at + 32 * c, sr);
                         if (!kSame || c == 1) tmem_wait32(reinterpret_cast<uint32_t*>(v));
-                        if (kSame && c == 2) keep32(sr + 64);
+                        if constexpr (kSame) {
+                            if (c == 2) keep32(sr + 64);
+                        }
                         if (masked) mask_cols<32>(v, 32 * c, hi, lo);
                         weights32(v, f, nm, zs, pk + 16 * c);
                     }
@@ -1080,29 +1085,45 @@ __global__ void __launch_bounds__(kRowsItem) tc_join_kernel(const __grid_constan
     const int c = blockIdx.x + 1, row = threadIdx.x;
     const Cut q = p.cuts[c];
     if (!q.first) return;
-    const Seq s = load_seq(p.a.batch, p.a.cache.page, q.b);
     const int g = q.g, c1 = q.last;
     const int w = row >> 7, r = row & 127, t_row = r / p.G, t = q.t0 + w * p.tpt + t_row;
-    if (r >= p.G * p.tpt || t >= s.n) return;
-    float m = -INFINITY;
-    for (int k = c - 1; k <= c1; ++k) m = fmaxf(m, p.part_ml[((int64_t)k * 2 + (k == c - 1)) * kRowsItem + row].x);
-    float z = 0.f, v[16] = {};
-    for (int k = c - 1; k <= c1; ++k) {
-        const int64_t slot = (int64_t)k * 2 + (k == c - 1);     // the first part begins with the item's first tile
-        const float2 ml = p.part_ml[slot * kRowsItem + row];
-        // without a maximum the part has summed nothing, or NaN alone: it counts as it is
-        const float a = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);
-        z += ml.y * a;
+    if (r >= p.G * p.tpt || t >= q.n) return;
+    // Part after part with a running maximum; the next part is on its way while one is added.  (The first part begins with the item's
+    // first tile: slot 2 k + 1, the others 2 k.)
+    struct Part {
+        float2 ml;
+        float4 o[4];
+    };
+    auto fetch = [&](int k) {
+        const int64_t slot = (int64_t)k * 2 + (k == c - 1);
+        Part x;
+        x.ml = p.part_ml[slot * kRowsItem + row];
         const float4* src = reinterpret_cast<const float4*>(p.part_o) + (slot * (D / 4) + blockIdx.y * 4) * kRowsItem + row;
 #pragma unroll
+        for (int i = 0; i < 4; ++i) x.o[i] = src[i * kRowsItem];
+        return x;
+    };
+    float m = -INFINITY, z = 0.f, v[16] = {};
+    Part next = fetch(c - 1);
+    for (int k = c - 1; k <= c1; ++k) {
+        const Part x = next;
+        if (k < c1) next = fetch(k + 1);
+        const float top = fmaxf(m, x.ml.x);
+        // a side without a maximum has summed nothing, or NaN alone: it counts as it is
+        const float a = x.ml.x == -INFINITY ? 1.f : ex2_approx(x.ml.x - top), b = m == -INFINITY ? 1.f : ex2_approx(m - top);
+        m = top;
+        z = z * b + x.ml.y * a;
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float4 o = src[i * kRowsItem];
-            v[4 * i] += o.x * a; v[4 * i + 1] += o.y * a; v[4 * i + 2] += o.z * a; v[4 * i + 3] += o.w * a;
+            v[4 * i] = v[4 * i] * b + x.o[i].x * a;
+            v[4 * i + 1] = v[4 * i + 1] * b + x.o[i].y * a;
+            v[4 * i + 2] = v[4 * i + 2] * b + x.o[i].z * a;
+            v[4 * i + 3] = v[4 * i + 3] * b + x.o[i].w * a;
         }
     }
     const float inv = z == 0.f ? 0.f : 1.f / z;
     const int h = g * p.G + r - t_row * p.G;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.a.out.data) + (s.row0 + t) * p.a.out.stride_row +
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.a.out.data) + (q.row0 + t) * p.a.out.stride_row +
                          h * p.a.out.stride_head + blockIdx.y * 16;
     float o0[8], o1[8];
 #pragma unroll
@@ -1113,7 +1134,7 @@ __global__ void __launch_bounds__(kRowsItem) tc_join_kernel(const __grid_constan
     store8(dst, o0);
     store8(dst + 8, o1);
     if (p.a.lse && blockIdx.y == 0)
-        p.a.lse[(s.row0 + t) * p.a.lse_stride_row + h * p.a.lse_stride_head] =
+        p.a.lse[(q.row0 + t) * p.a.lse_stride_row + h * p.a.lse_stride_head] =
             z == 0.f ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
 }
 

@@ -18,8 +18,8 @@ namespace {
 
 constexpr int kRotThreads = 256;
 
-// What the kernel takes of a plan of at most kPairs pairs: a launch's cost on the host grows with its arguments (1.4 KB of them
-// took LAUNCH_NOTE).
+// What the kernel takes of a plan of at most kPairs pairs: a launch's time on the host grows with its arguments (with room for
+// 128 pairs, 1.4 KB of them, a call for heads of 64 took 2 us more).
 template <int kPairs>
 struct RotArgs {
     int rot;
