@@ -383,7 +383,8 @@ sp_status sp_rotary(const sp_rotary_plan* plan, const int32_t* positions, int64_
  * zeros), and round x / 2^k to the nearest code, ties to even.  With a power
  * of two the division is exact, and code * scale is a bf16 value, so reading
  * a cache back rounds nothing (for codes * scale above bf16's smallest normal).  A row that holds a NaN or an infinity gets
- * the scale NaN and reads back as NaN. */
+ * the scale NaN and reads back as NaN.  The NaN codes of e4m3 (0x7f, 0xff) are never written; sp_attend
+ * takes them for +-480 in values. */
 typedef enum { SP_CACHE_SAME = 0, SP_CACHE_E4M3 = 1, SP_CACHE_INT8 = 2 } sp_cache_kind;
 
 /* One layer's keys and values in pages of `page` tokens: the row of (page p,
@@ -420,7 +421,7 @@ typedef struct {
  * [0, pages) is never followed: SP_EDEVICE is recorded, its tokens are not
  * written, read back as zeros, and are attended as if they were zeros or left out. */
 typedef struct {
-    int32_t        B;          /* >= 1 */
+    int32_t        B;          /* 1 .. 65535 */
     int32_t        max_new;    /* at least the largest number of new tokens of a sequence */
     int64_t        T;          /* rows of the call's tensors, at most 2^31 - 1 */
     const int64_t* cu_new;     /* device [B + 1] */
@@ -436,7 +437,7 @@ size_t sp_cache_workspace_size(void);
 /* Writes the new tokens' keys and values, k_new and v_new [T, H_kv, d], to
  * their places in the cache, quantising as the cache's kind says.  A new
  * token whose place would be negative (kv_len below the number of new tokens) is
- * skipped.  No other slot of the cache is touched. */
+ * skipped.  No other slot of the cache is touched.  No two new tokens may have the same place. */
 sp_status sp_cache_write(const sp_cache* cache, const sp_batch* batch, const sp_rows* k_new, const sp_rows* v_new,
                          void* ws, size_t ws_bytes, void* stream);
 
@@ -466,13 +467,15 @@ size_t sp_attend_workspace_size(const sp_cache* cache, const sp_batch* batch, in
  * same bits; in another batch a sequence's sums may be added in another order.  The lse of the
  * look-ahead decode steps is what sp_score_lse takes.
  *
- *   q, out   [T, H, d] in the cache's dtype; out must not overlap q
+ *   q, out   [T, H, d] in the cache's dtype; out must not overlap q, and rows of neither may overlap
+ *            each other
  *   lse      fp32, lse[r * lse_stride_row + h * lse_stride_head], or NULL.  Step j of N
  *            look-ahead steps of one request (T = 1, layer l of sp_score_lse's lse [L, H, N]):
  *            pointer lse + l * H * N + j, lse_stride_head = N
  *
  * Requirements: 8 <= d <= 256, d % 8 == 0, H % H_kv == 0, scale > 0 and
- * finite.  What unwritten slots hold (NaN too) has no effect, nor have rows
+ * finite.  Before a call of a kind is captured into a graph, one of that kind should have run,
+ * as CUDA may load a kernel at its first launch.  What unwritten slots hold (NaN too) has no effect, nor have rows
  * that are not a token of the batch.  A NaN or an infinity in a key or value of a token that
  * some rows of the sequence see may reach its other rows as well.
  * Statistics and sums are fp32; bf16 softmax weights are rounded to bf16 for

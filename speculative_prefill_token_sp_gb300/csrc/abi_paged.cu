@@ -57,6 +57,17 @@ sp_status check_rows(const char* fn, const char* what, const sp_rows* r, sp_dtyp
     return SP_OK;
 }
 
+// Rows that are written, or that a tensor map describes, must not overlap.
+sp_status check_apart(const char* fn, const char* what, const sp_rows* r, int64_t rows, int heads, int d) {
+    const int64_t most = (int64_t)1 << 38;
+    if (rows == 0) return SP_OK;
+    if ((rows > 1 && (r->stride_row < d || r->stride_row > most)) || (heads > 1 && (r->stride_head < d || r->stride_head > most))) {
+        set_error("%s: the rows of %s must not overlap, and its strides must be at most 2^38", fn, what);
+        return SP_EINVAL;
+    }
+    return SP_OK;
+}
+
 sp_status check_workspace(const char* fn, const void* ws, size_t have, size_t need) {
     if (!ws || reinterpret_cast<uintptr_t>(ws) % 16) {
         set_error("%s: null or misaligned workspace", fn);
@@ -78,6 +89,7 @@ enum Path {
 };
 Path path_of(const sp_cache& c, const sp_batch& b, int H) {
     const int G = H / c.H_kv;
+    if (b.T == 0) return kGeneral;          // nothing to do but the check
     const bool step = attend_step_supported(c);
     if (step && (int64_t)b.max_new * G <= 16) return kStep;
     if (!attend_tc_supported(c, b, G)) return kGeneral;
@@ -112,6 +124,10 @@ sp_status check_cache(const char* fn, const sp_cache* c) {
     }
     sp_status s = check_dim(fn, c->d, c->dtype);
     if (s != SP_OK) return s;
+    if (c->H_kv > 65535) {
+        set_error("%s: at most 65535 KV heads (got %d)", fn, c->H_kv);
+        return SP_EUNSUPPORTED;
+    }
     if (c->H_kv < 1 || c->page < 1 || c->pages < 1 || c->pages > INT32_MAX) {
         set_error("%s: the cache needs H_kv, page and pages >= 1 (got %d, %d, %lld)", fn, c->H_kv, c->page,
                   (long long)c->pages);
@@ -149,6 +165,10 @@ sp_status check_batch_args(const char* fn, const sp_batch* b) {
                   "(got %d, %d, %lld, %d, %lld)", fn, b->B, b->table_width, (long long)b->T, b->max_new,
                   (long long)b->table_stride);
         return SP_EINVAL;
+    }
+    if (b->B > 65535) {
+        set_error("%s: at most 65535 sequences (got %d)", fn, b->B);
+        return SP_EUNSUPPORTED;
     }
     if (!b->cu_new || !b->kv_len || !b->table) {
         set_error("%s: null cu_new, kv_len or table", fn);
@@ -231,10 +251,12 @@ sp_status sp_rotary(const sp_rotary_plan* plan, const int32_t* positions, int64_
             set_error("%s: null or misaligned positions", fn);
             return SP_EINVAL;
         }
-        if (H > 0 && ((s = check_rows(fn, "q", q, dtype, T)) != SP_OK || (s = check_rows(fn, "q_out", q_out, dtype, T)) != SP_OK))
+        if (H > 0 && ((s = check_rows(fn, "q", q, dtype, T)) != SP_OK || (s = check_rows(fn, "q_out", q_out, dtype, T)) != SP_OK ||
+                      (s = check_apart(fn, "q_out", q_out, T, H, d)) != SP_OK))
             return s;
         if (H_kv > 0 &&
-            ((s = check_rows(fn, "k", k, dtype, T)) != SP_OK || (s = check_rows(fn, "k_out", k_out, dtype, T)) != SP_OK))
+            ((s = check_rows(fn, "k", k, dtype, T)) != SP_OK || (s = check_rows(fn, "k_out", k_out, dtype, T)) != SP_OK ||
+             (s = check_apart(fn, "k_out", k_out, T, H_kv, d)) != SP_OK))
             return s;
     }
     s = rotary_launch(*plan, positions, pos_stride, T, d, dtype, inverse != 0, H > 0 && q ? *q : none,
@@ -270,7 +292,9 @@ sp_status sp_cache_read(const sp_cache* cache, const sp_batch* batch, const sp_r
         return SP_EINVAL;
     }
     if ((out_k && (s = check_rows(fn, "out_k", out_k, cache->dtype, batch->T)) != SP_OK) ||
-        (out_v && (s = check_rows(fn, "out_v", out_v, cache->dtype, batch->T)) != SP_OK))
+        (out_v && (s = check_rows(fn, "out_v", out_v, cache->dtype, batch->T)) != SP_OK) ||
+        (out_k && (s = check_apart(fn, "out_k", out_k, batch->T, cache->H_kv, cache->d)) != SP_OK) ||
+        (out_v && (s = check_apart(fn, "out_v", out_v, batch->T, cache->H_kv, cache->d)) != SP_OK))
         return s;
     if ((s = check_workspace(fn, ws, ws_bytes, sizeof(WsHeader))) != SP_OK) return s;
     const sp_rows none{nullptr, 0, 0};
@@ -314,6 +338,8 @@ sp_status sp_attend(const sp_rows* q, const sp_cache* cache, const sp_batch* bat
         set_error("%s: lse must be 4-byte aligned", fn);
         return SP_EINVAL;
     }
+    if ((s = check_apart(fn, "q", q, batch->T, H, cache->d)) != SP_OK || (s = check_apart(fn, "out", out, batch->T, H, cache->d)) != SP_OK)
+        return s;
     const size_t need = sp_attend_workspace_size(cache, batch, H);
     if ((s = check_workspace(fn, ws, ws_bytes, need)) != SP_OK) return s;
     AttendProblem p;

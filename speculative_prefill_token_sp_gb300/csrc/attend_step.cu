@@ -577,7 +577,7 @@ sp_status launch(const SplitArgs& p, cudaStream_t st) {
     kern<<<p.P, kThreads, smem, st>>>(p);
     SP_LAUNCH_CHECK();
     const int64_t rows = std::min<int64_t>(p.rows, (int64_t)p.a.batch.max_new * p.G);
-    const dim3 grid((unsigned)(p.a.batch.B * p.a.cache.H_kv), (unsigned)std::max<int64_t>(1, rows));
+    const dim3 grid((unsigned)p.a.batch.B * (unsigned)p.a.cache.H_kv, (unsigned)std::max<int64_t>(1, rows));
     return launch_early(step_join_kernel<D, kKind>, grid, kJoinThreads, (size_t)0, st, p);
 }
 

@@ -237,10 +237,6 @@ void launch_kind(bool write, const MoveArgs& a, cudaStream_t st) {
 sp_status move_launch(bool write, const sp_cache& c, const sp_batch& b, const sp_rows& k, const sp_rows& v, void* ws,
                       cudaStream_t st) {
     const MoveArgs a{c, b, k, v, 0, 0, static_cast<WsHeader*>(ws)};
-    if (!write && c.H_kv > 65535) {
-        set_error("sp_cache_read: at most 65535 KV heads (got %d)", c.H_kv);
-        return SP_EUNSUPPORTED;
-    }
     if (c.dtype == SP_BF16) launch_kind<__nv_bfloat16>(write, a, st);
     else launch_kind<float>(write, a, st);
     SP_LAUNCH_CHECK();

@@ -339,6 +339,94 @@ def test_unwritten_slots_have_no_effect(sp, fill, new):
     check_attend(sp, H=4, H_kv=2, d=128, page=64, new=new, kv=[205], junk=fill)
 
 
+@pytest.mark.parametrize("kind", ["same", "e4m3"])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (64, "f32")])
+@pytest.mark.parametrize("n", [1, 6, 150])
+@pytest.mark.parametrize("shape", ["up", "down", "late", "spike"])
+def test_logits_that_leave_the_running_maximum_behind(sp, shape, n, d, dtype, kind):
+    """Logits that climb or fall by hundreds from one end of the cache to the other, or jump in one place."""
+    import torch
+    rng = np.random.default_rng(21)
+    td = torch_dtype(dtype)
+    H, H_kv, page, kv = 4, 2, 16, 700
+    along = np.arange(kv) / kv
+    level = {"up": 300 * along, "down": 300 - 300 * along, "late": np.where(np.arange(kv) % 128 == 127, 40.0, -40.0),
+             "spike": np.where(np.arange(kv) == 250, 90.0, 0.0)}[shape]
+    cache, table, kval, vval = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=[kv], dtype=td, kind=kind)
+    k = rng.standard_normal((kv, H_kv, d)) * 0.3
+    k[:, :, 0] = level[:, None] * 4         # times q[0] = 4 and the scale 1 / 16
+    new = torch.from_numpy(k).to(td)
+    v = torch.from_numpy(rng.standard_normal((kv, H_kv, d))).to(td)
+    fill, _ = make_batch(sp, [kv], [kv], table)
+    sp.cache_write(cache, fill, new.cuda(), v.cuda(), check=True)
+    kk, vv = sp.cache_read(cache, fill, check=True)
+    q = torch.from_numpy(rng.standard_normal((n, H, d))).to(td)
+    q[:, :, 0] = 4
+    batch, _ = make_batch(sp, [n], [kv], table)
+    out, lse = sp.attend(q.cuda(), cache, batch, scale=1 / 16, check=True)
+    ref, ref_lse, top, spread = oracle.paged.attend(q.double().numpy(), f64(kk), f64(vv), 1 / 16)
+    bound, lse_bound = attend_bounds(dtype, d, kv, ref, spread, top, ref_lse)
+    assert np.all(np.abs(f64(out) - ref) <= bound) and np.all(np.abs(f64(lse) - ref_lse) <= lse_bound)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (40, "f32")])
+def test_a_batch_without_rows(sp, d, dtype):
+    import torch
+    cache = sp.cache_alloc(2, 1, 16, d, dtype=torch_dtype(dtype))
+    batch, _ = make_batch(sp, [0, 0], [5, 0], np.array([[0], [1]]), rows=0, max_new=700)
+    empty = torch.empty(0, 2, d, dtype=torch_dtype(dtype), device="cuda")
+    out, lse = sp.attend(empty, cache, batch, check=True)
+    assert out.shape == (0, 2, d) and lse.shape == (2, 0)
+    sp.cache_write(cache, batch, empty[:, :1], empty[:, :1], check=True)
+    assert sp.cache_read(cache, batch, check=True)[0].shape == (1, 0, d)
+
+
+@pytest.mark.parametrize("kind", ["same", "int8"])
+def test_many_sequences_of_all_kinds_at_once(sp, kind):
+    rng = np.random.default_rng(22)
+    new = [int(x) for x in rng.choice([0, 1, 1, 1, 2, 4, 5, 33, 70], 90)]
+    kv = [n + int(rng.integers(0, 300)) for n in new]
+    kv[3] = 0
+    check_attend(sp, H=4, H_kv=1, d=64, page=16, new=new, kv=kv, kind=kind, behind=4)
+
+
+@pytest.mark.parametrize("n", [1, 100])
+def test_two_streams_at_once(sp, n):
+    import torch
+    rng = np.random.default_rng(23)
+    runs = []
+    for i in range(2):
+        cache, table, _, _ = make_cache(sp, rng, H_kv=2, d=128, page=16, kv=[3000 + n])
+        batch, _ = make_batch(sp, [n], [3000 + n], table)
+        q = torch.from_numpy(rng.standard_normal((n, 8, 128))).to(torch.bfloat16).cuda()
+        runs.append((cache, batch, q, sp.attend(q, cache, batch, check=True)[0], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(8):
+        for i, (cache, batch, q, _, stream) in enumerate(runs):
+            outs[i].append(sp.attend(q, cache, batch, stream=stream)[0])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in outs[i]:
+            assert torch.equal(o, runs[i][3])
+
+
+def test_a_chunk_over_a_cache_beyond_2_31_entries(sp):
+    import torch
+    far = 3 * (1 << 30)         # entries between two pages
+    buf = torch.zeros(far + 8192, dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(24)
+    pages = [buf.as_strided((2, 1, 64, 64), (far, 4096, 64, 1), at) for at in (0, 4096)]
+    cache = sp.Cache(*pages)
+    x, y = (torch.from_numpy(rng.standard_normal((100, 1, 64))).to(torch.bfloat16) for _ in range(2))
+    batch, _ = make_batch(sp, [100], [100], np.array([[1, 0]], np.int32))
+    sp.cache_write(cache, batch, x.cuda(), y.cuda(), check=True)
+    out, lse = sp.attend(x.cuda(), cache, batch, check=True)
+    ref = oracle.paged.attend(x.double().numpy(), x.double().numpy().transpose(1, 0, 2), y.double().numpy().transpose(1, 0, 2), 0.125)
+    bound, lse_bound = attend_bounds("bf16", 64, 100, ref[0], ref[3], ref[2], ref[1])
+    assert np.all(np.abs(f64(out) - ref[0]) <= bound) and np.all(np.abs(f64(lse) - ref[1]) <= lse_bound)
+
+
 @pytest.mark.parametrize("d,dtype,n", [(64, "bf16", 1), (128, "bf16", 3), (64, "f32", 2), (128, "bf16", 90), (40, "bf16", 5)])
 def test_pages_behind_the_window_may_be_gone(sp, d, dtype, n):
     import torch

@@ -41,7 +41,7 @@ BAD_CACHES = [
     (dict(d=0), "SP_EINVAL"), (dict(dtype=3), "SP_EINVAL"), (dict(kind=5), "SP_EINVAL"), (dict(kind=1), "SP_EINVAL"),
     (dict(kind=2, k_scale=64), "SP_EINVAL"), (dict(page=0), "SP_EINVAL"), (dict(pages=0), "SP_EINVAL"), (dict(H_kv=0), "SP_EINVAL"),
     (dict(k=4104), "SP_EINVAL"), (dict(stride_slot=68), "SP_EINVAL"), (dict(stride_slot=32), "SP_EINVAL"),
-    (dict(stride_page=-2048), "SP_EINVAL"), (dict(stride_head=1028), "SP_EINVAL"), (dict(pages=1 << 31), "SP_EINVAL"),
+    (dict(stride_page=-2048), "SP_EINVAL"), (dict(H_kv=65536), "SP_EUNSUPPORTED"), (dict(stride_head=1028), "SP_EINVAL"), (dict(pages=1 << 31), "SP_EINVAL"),
 ]
 BAD_BATCHES = [dict(B=0), dict(T=-1), dict(T=1 << 31), dict(max_new=-1), dict(table_width=0), dict(cu_new=None), dict(kv_len=None),
                dict(table=None), dict(cu_new=68), dict(table=258), dict(table_stride=-4)]
@@ -80,6 +80,19 @@ def test_bad_rows_are_refused(sp, over):
         assert sp.sp_cache_read(c, b, good, bad, 65536, big, 0) == sp.SP_EINVAL
     assert sp.sp_attend(bad, c, b, 4, 0.125, 0, good, None, 0, 0, 65536, big, 0) == sp.SP_EINVAL
     assert sp.sp_attend(good, c, b, 4, 0.125, 0, bad, None, 0, 0, 65536, big, 0) == sp.SP_EINVAL
+
+
+def test_overlapping_rows_are_refused(sp):
+    c, b, good = cache_of(sp), batch_of(sp), rows_of(sp)
+    big = 1 << 40
+    for over in (dict(stride_row=0), dict(stride_head=0), dict(stride_head=32), dict(stride_row=-256), dict(stride_row=1 << 39)):
+        bad = rows_of(sp, **over)
+        assert sp.sp_attend(bad, c, b, 4, 0.125, 0, good, None, 0, 0, 65536, big, 0) == sp.SP_EINVAL
+        assert sp.sp_attend(good, c, b, 4, 0.125, 0, bad, None, 0, 0, 65536, big, 0) == sp.SP_EINVAL
+        assert sp.sp_cache_read(c, b, bad, None, 65536, big, 0) == sp.SP_EINVAL
+        assert sp.sp_cache_read(c, b, None, bad, 65536, big, 0) == sp.SP_EINVAL
+    s = sp.sp_cache_write(c, batch_of(sp, B=65536), good, good, 65536, big, 0)
+    assert s == sp.SP_EUNSUPPORTED
 
 
 def test_other_arguments_that_are_refused(sp):
