@@ -187,11 +187,11 @@ def _code_only(text: str) -> str:
 
 
 def kernel_source_digest() -> str:
-    """sha256 of the scoring kernels' code (comments and whitespace ignored)."""
+    """sha256 of the code of the scoring kernels and the headers they share (comments and whitespace ignored)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "speculative_prefill_token_sp_gb300", "csrc")
     for name in sorted(os.listdir(csrc)):
-        if name.startswith("score") or name.endswith(".cuh"):
+        if name.startswith("score") or name in ("sp_common.cuh", "tc_ptx.cuh"):
             with open(os.path.join(csrc, name), encoding="utf-8") as f:
                 h.update(name.encode())
                 h.update(_code_only(f.read()).encode())
