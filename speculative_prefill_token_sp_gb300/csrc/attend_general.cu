@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(const __grid_co
     int64_t begin = 0;
     int b = u < u_end ? find_unit(p, kUnit, u, begin) : 0;
     const float f = p.a.scale * 1.4426950408889634f;
-    while (u < u_end) {
+    while (u < u_end && b < p.a.batch.B) {         // (b: should the arrays be changed while the kernel runs)
         const Seq s = load_seq(p.a.batch, c.page, b);
         const Span span = span_of(s, p.a.window, kUnit);
         const int blocks = row_blocks(p, s);

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
     const float f = p.a.scale * 1.4426950408889634f;
     auto piece = [&](int j) { return kJ == 1 ? q4 : (j >> 1) * 8 + 2 * q4 + (j & 1); };
 
-    while (u < u_end) {
+    while (u < u_end && b < p.a.batch.B) {         // (b: should the arrays be changed while the kernel runs)
         const Seq s = load_seq(bt, c.page, b);
         if (row_blocks(p, s) == 0) {
             ++b;

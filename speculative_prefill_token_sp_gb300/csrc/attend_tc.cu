@@ -166,10 +166,14 @@ struct Walk {
     // the next sequence that has rows here (there is one, as tiles are left), 32 of them at a time
     __device__ __forceinline__ void next_seq(const TcArgs& p) {
         const int lane = threadIdx.x & 31;
-        for (int first = b + 1;; first += 32) {
+        for (int first = b + 1, rounds = 0;; first += 32) {
             if (first >= p.a.batch.B) {
                 first = 0;
                 ++g;
+                if (++rounds > 1) {         // the arrays were changed while the kernel ran
+                    left = 0;
+                    return;
+                }
             }
             int n = 0;
             if (first + lane < p.a.batch.B) n = blocks_of(p, load_seq(p.a.batch, p.a.cache.page, first + lane));
@@ -366,6 +370,28 @@ __device__ __forceinline__ void max_cols(const float* v, float (&mx)[4]) {
         for (int c = 0; c < 4; ++c) mx[c] = fmax3(mx[c], v[i + 2 * c], v[i + 2 * c + 1]);
 }
 
+// Takes out the columns from `first` on that the row does not see.
+template <int N>
+__device__ __forceinline__ void mask_cols(float* v, int first, int hi, int lo) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (first + i > hi || first + i < lo) v[i] = -INFINITY;
+}
+
+// The largest logit (before the factor f) of a tile that the row sees, read once more from TMEM.
+__device__ __forceinline__ float top_of_row(uint32_t s_at, uint32_t* sr, bool masked, int hi, int lo) {
+    float* sv = reinterpret_cast<float*>(sr);
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        tmem_ld32(s_at + 32 * c, sr);
+        tmem_wait32(sr);
+        if (masked) mask_cols<32>(sv, 32 * c, hi, lo);
+        max_cols<32>(sv, mx);
+    }
+    return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+}
+
 // Weights 2^(f v - m) (nm = -m) of 32 logits as pairs of bf16, and their sums.  16 at a time and step by step: pair by pair, a warp
 // alone on its scheduler took 610 to 710 cycles for 96 weights, like this 495 (384 are the exponentials').
 __device__ __forceinline__ void weights32(const float* v, float f, float nm, float (&zs)[4], uint32_t* pk) {
@@ -432,14 +458,6 @@ __device__ __forceinline__ void hand_over(uint64_t* bar) {
     tc_fence_before();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(bar));
-}
-
-// Takes out the columns from `first` on that the row does not see.
-template <int N>
-__device__ __forceinline__ void mask_cols(float* v, int first, int hi, int lo) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (first + i > hi || first + i < lo) v[i] = -INFINITY;
 }
 
 // The MMA warps run with all lanes and issue from one (`lead`): descriptors, addresses and loop counters are then warp-uniform for
@@ -604,7 +622,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
             // next one.  So the maximum of a tile is not looked for.  A tile is done again by its true maximum if its weights
             // sum to more than 2^24, which is seen before they are handed over (of the last 32 keys by their maximum).
             float m = -INFINITY, z = 0.f, next_m = -INFINITY;
-            bool follow = false, fresh = true;
+            bool follow = false, fresh = true, huge = false;
             const int n_tiles = sg.to - sg.from;
             int base = tile_of(sg, sg.from) * kKeys;
             for (int x = 0; x < n_tiles; ++x, base -= kKeys) {
@@ -623,23 +641,18 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                 uint32_t sr[kSame ? 128 : 32], pk[48];
                 float* sv = reinterpret_cast<float*>(sr);
                 float nm, zs[4];
-                for (;;) {
+                // twice at most: after a pass by the true maximum nothing is lost
+                for (int pass = 0; pass < 2; ++pass) {
                     if (fresh) {            // the true maximum, for rows without an m or with one left far behind
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            tmem_ld32(s_at + 32 * c, sr);
-                            tmem_wait32(sr);
-                            if (masked) mask_cols<32>(sv, 32 * c, hi, lo);
-                            max_cols<32>(sv, mx);
-                        }
-                        const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * f;     // f > 0: f times the largest product
-                        // 16: a sum of 96 over 2^24 has a maximum over 2^17, and one pass is enough.  Also where there was no m
-                        const bool far = top > m + 16.f;
+                        const float top = top_of_row(s_at, sr, masked, hi, lo) * f;         // f > 0: f times the largest product
+                        // 16: a sum of 96 over 2^24 has a maximum over 2^17.  Also where there was no m
+                        const bool far = top > m + (huge ? 0.f : 16.f);
                         const float a = far && m != -INFINITY ? ex2_approx(m - top) : 1.f;
                         if (__any_sync(0xffffffffu, a != 1.f)) scale_o<D>(o_at, a);
                         z *= a;
                         if (far) m = top;
+                        huge = __any_sync(0xffffffffu, pos >= 0 && fabsf(m) > 1048576.f && m != -INFINITY);
+                        if (huge) break;
                     }
                     nm = m == -INFINITY ? 0.f : -m;
                     zs[0] = zs[1] = zs[2] = zs[3] = 0.f;
@@ -667,29 +680,45 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                         weights32(v, f, nm, zs, pk + 16 * c);
                     }
                     const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * f;
-                    // (a NaN or infinite sum of a row with an infinite m stays: it is the row's result)
                     const float sum = (zs[0] + zs[1]) + (zs[2] + zs[3]);
-                    const bool lost = pos >= 0 && (sum > 16777216.f || top > m + 24.f) && m != INFINITY;
-                    fresh = __any_sync(0xffffffffu, lost);
+                    fresh = __any_sync(0xffffffffu, pos >= 0 && (sum > 16777216.f || top > m + 24.f));
                     if (!fresh) break;
                 }
+                if (huge) {
+                    // Logits of more than 2^20: f v - m, rounded once, would differ from f v and m, each rounded, by more than the
+                    // weights can stand (and a row's own maximum have a weight that overflows or vanishes).  Rounded first, they
+                    // are off by what the products' own rounding is.
+                    zs[0] = zs[1] = zs[2] = zs[3] = 0.f;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld32(s_at + 32 * c, sr);
+                        tmem_wait32(sr);
+                        if (masked) mask_cols<32>(sv, 32 * c, hi, lo);
 #pragma unroll
-                for (int c = 0; c < 3; ++c) tmem_st16(s_at + 16 * c, pk + 16 * c);
-                hand_over(&p_full[2 * w]);          // 96 keys' weights, then the last 32: the product with V begins meanwhile
-                if constexpr (!kSame) {
-                    tmem_ld32(s_at + 96, sr);
-                    tmem_wait32(sr);
-                    if (masked) mask_cols<32>(sv, 96, hi, lo);
+                        for (int i = 0; i < 32; ++i) sv[i] = __fmul_rn(sv[i], f);
+                        weights32(sv, 1.f, m == -INFINITY ? 0.f : -m, zs, pk);
+                        tmem_st16(s_at + 16 * c, pk);
+                    }
+                    hand_over(&p_full[2 * w]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 3; ++c) tmem_st16(s_at + 16 * c, pk + 16 * c);
+                    hand_over(&p_full[2 * w]);      // 96 keys' weights, then the last 32: the product with V begins meanwhile
+                    if constexpr (!kSame) {
+                        tmem_ld32(s_at + 96, sr);
+                        tmem_wait32(sr);
+                        if (masked) mask_cols<32>(sv, 96, hi, lo);
+                    }
+                    weights32(kSame ? sv + 96 : sv, f, nm, zs, pk);
+                    tmem_st16(s_at + 48, pk);
                 }
-                weights32(kSame ? sv + 96 : sv, f, nm, zs, pk);
-                tmem_st16(s_at + 48, pk);
                 hand_over(&p_full[2 * w + 1]);
                 const float sum = (zs[0] + zs[1]) + (zs[2] + zs[3]);
                 z += sum;
-                const bool grows = pos >= 0 && sum > 256.f && sum < INFINITY;
+                const bool grows = !huge && pos >= 0 && sum > 256.f && sum < INFINITY;
                 next_m = grows ? m + log2f(sum) : m;
                 follow = __any_sync(0xffffffffu, grows);
-                fresh = __any_sync(0xffffffffu, pos >= 0 && m == -INFINITY);
+                fresh = huge || __any_sync(0xffffffffu, pos >= 0 && m == -INFINITY);
             }
             if (!ok) break;
             ok = wait_warp(smem_u32(&o_full[w]), ph_o, abort_flag, 22);

@@ -369,6 +369,59 @@ def test_logits_that_leave_the_running_maximum_behind(sp, shape, n, d, dtype, ki
     assert np.all(np.abs(f64(out) - ref) <= bound) and np.all(np.abs(f64(lse) - ref_lse) <= lse_bound)
 
 
+@pytest.mark.parametrize("kind", ["same", "e4m3", "int8"])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (64, "f32")])
+@pytest.mark.parametrize("n", [1, 150])
+@pytest.mark.parametrize("size", [2.0 ** 9, 2.0 ** 14, 2.0 ** 40, -2.0 ** 12, -2.0 ** 40])
+def test_logits_beyond_single_precision_steps(sp, size, n, d, dtype, kind):
+    """Logits of 2^18 to 2^88, where neighbouring fp32 values are up to 2^64 apart: the largest one takes all (tokens
+    whose keys are equal share it)."""
+    import torch
+    rng = np.random.default_rng(25)
+    td = torch_dtype(dtype)
+    H, H_kv, page, kv = 4, 2, 16, 200
+    cache, table, _, _ = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=[kv], dtype=td, kind=kind)
+    k = torch.zeros(kv, H_kv, d, dtype=td)
+    k[:, :, 0] = ((torch.arange(kv) + 1) * abs(size))[:, None].to(td)
+    v = torch.from_numpy(rng.standard_normal((kv, H_kv, d))).to(td)
+    fill, _ = make_batch(sp, [kv], [kv], table)
+    sp.cache_write(cache, fill, k.cuda(), v.cuda(), check=True)
+    kk, vv = sp.cache_read(cache, fill, check=True)
+    q = torch.zeros(n, H, d, dtype=td)
+    q[:, :, 0] = size
+    batch, _ = make_batch(sp, [n], [kv], table)
+    out, lse = sp.attend(q.cuda(), cache, batch, scale=1.0, check=True)
+    ref, ref_lse, _, spread = oracle.paged.attend(q.double().numpy(), f64(kk), f64(vv), 1.0)
+    # the keys are 2^-8 apart or equal, so a weight is 0 or 1 exactly; sums of equal weights as fp32 and bf16 allow
+    assert np.all(np.abs(f64(out) - ref) <= (2.0 ** -7 if dtype == "bf16" else 2.0 ** -20) * spread)
+    assert np.all(np.abs(f64(lse) - ref_lse) <= 2.0 ** -20 * np.abs(ref_lse))
+
+
+@pytest.mark.parametrize("kind", ["same", "e4m3", "int8"])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (64, "f32")])
+@pytest.mark.parametrize("n", [1, 150])
+@pytest.mark.parametrize("spread", [1e4, 1e10, 1e30])
+def test_rows_of_all_sizes_stay_finite(sp, spread, n, d, dtype, kind):
+    """Keys whose sizes spread over many decades: every output is a mean of values."""
+    import torch
+    rng = np.random.default_rng(26)
+    td = torch_dtype(dtype)
+    H, H_kv, page, kv = 4, 2, 16, 400
+    cache, table, _, _ = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=[kv], dtype=td, kind=kind)
+    size = spread ** rng.uniform(-1, 1, (kv, H_kv, 1))
+    k = torch.from_numpy(rng.standard_normal((kv, H_kv, d)) * size).to(td)
+    v = torch.from_numpy(rng.standard_normal((kv, H_kv, d))).to(td)
+    fill, _ = make_batch(sp, [kv], [kv], table)
+    sp.cache_write(cache, fill, k.cuda(), v.cuda(), check=True)
+    _, vv = sp.cache_read(cache, fill, check=True)
+    q = torch.from_numpy(rng.standard_normal((n, H, d))).to(td)
+    batch, _ = make_batch(sp, [n], [kv], table)
+    out, lse = sp.attend(q.cuda(), cache, batch, check=True)
+    got = f64(out)
+    assert np.all(np.isfinite(got)) and np.all(np.isfinite(f64(lse)))
+    assert np.abs(got).max() <= np.abs(f64(vv)).max() * (1 + 2.0 ** -7)
+
+
 @pytest.mark.parametrize("d,dtype", [(64, "bf16"), (40, "f32")])
 def test_a_batch_without_rows(sp, d, dtype):
     import torch
