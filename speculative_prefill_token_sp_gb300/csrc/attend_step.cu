@@ -31,6 +31,12 @@
 // equal runs, one per resident CTA, so a batch of any mixture of lengths keeps
 // every SM busy to the end; a pair that is cut leaves partial sums in the
 // workspace, and a second kernel, launched early, joins them in a fixed order.
+//
+// In a graph, one token each of 16 requests of 2K to 32K (bf16, 16 query heads on 4 of
+// 64) takes 49.5 us (5.3 TB/s), one over 131072 (e4m3, 32 on 8 of 128) 57 us (4.9 TB/s).
+// Bound by memory but for some 10 us of start, first loads and join, the 8-bit
+// kinds also by the integer pipe (56% busy).  The second
+// case with operands loaded from global memory into registers 117 us, then with the rings 83 us.
 #include "attend_split.cuh"
 
 #include <cuda_fp16.h>

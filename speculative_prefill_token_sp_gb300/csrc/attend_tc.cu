@@ -36,6 +36,11 @@
 // end, and each CTA takes an equal run of key tiles, so that the SMs end
 // together whatever the lengths.  An item that is cut leaves its sums in the
 // workspace and a joining kernel adds them up in a fixed order.
+//
+// A chunk of 4096 over 32768 (bf16, 32 query heads on 8 of 128) takes 1.13 ms,
+// 1.83 PFLOP/s or 95% of the rate of a large library product; in a long loop the board's
+// power limit makes it 1.30 to 1.34 ms.  Seven requests of 192 to 650 new tokens with
+// a window of 4096 take 161 us from an int8 cache, 126 us from bf16.
 #include "paged.cuh"
 #include "tc_ptx.cuh"
 

@@ -9,6 +9,8 @@
 // Bound by memory: each entry is read once and written once.  A block takes a
 // few tokens, works out their sines and cosines once into shared memory, and
 // then runs over all the heads of q and k with 16-byte loads and stores.
+// 8192 tokens of 32 + 8 heads of 128 in bf16 take 28.6 us in a graph (5.9 TB/s); 16
+// tokens 2.1 us.
 #include "paged.cuh"
 
 #include <algorithm>
