@@ -368,7 +368,7 @@ sp_status sp_rotary_plan_init(sp_rotary_plan* plan, int rot, const double* inv_f
  *   q, q_out    [T, H, d]     in and out may be the same rows, and must not overlap otherwise
  *   k, k_out    [T, H_kv, d]  H or H_kv may be 0: that pair of tensors is left out
  *
- * Requirements: T >= 0, 8 <= d <= 256, d % 8 == 0, rot <= d.  No workspace.
+ * Requirements: T >= 0, 8 <= d <= 256, d % 8 == 0, rot <= d, at most 65535 heads each.  No workspace.
  * Products and sums are fp32, rounded once. */
 sp_status sp_rotary(const sp_rotary_plan* plan, const int32_t* positions, int64_t pos_stride, int64_t T, int d,
                     sp_dtype dtype, int inverse, const sp_rows* q, const sp_rows* q_out, int H, const sp_rows* k,
@@ -382,7 +382,7 @@ sp_status sp_rotary(const sp_rotary_plan* plan, const int32_t* positions, int64_
  * smallest 2^k, k >= -100, with max|x| / 2^k <= 448 or 127 (1 for a row of
  * zeros), and round x / 2^k to the nearest code, ties to even.  With a power
  * of two the division is exact, and code * scale is a bf16 value, so reading
- * a cache back rounds nothing (for codes * scale above bf16's smallest normal).  A row that holds a NaN or an infinity gets
+ * a cache back rounds nothing (but an entry whose code rounds up to 2^128 reads back as infinity).  A row that holds a NaN or an infinity gets
  * the scale NaN and reads back as NaN.  The NaN codes of e4m3 (0x7f, 0xff) are never written; sp_attend
  * takes them for +-480 in values. */
 typedef enum { SP_CACHE_SAME = 0, SP_CACHE_E4M3 = 1, SP_CACHE_INT8 = 2 } sp_cache_kind;

@@ -593,10 +593,16 @@ def rotary_plan(rot, *, base=10000.0, inv_freq=None, sections=None, axis_of_pair
 
 
 def _rows(t, heads_first=False):
-    """sp_rows of a tensor [rows, heads, d] (heads_first: [heads, rows, d]) whose last axis is contiguous."""
+    """sp_rows of a tensor [rows, heads, d] (heads_first: [heads, rows, d]) whose last axis is contiguous.  The stride
+    of an axis with one entry may be anything in torch: d takes its place."""
     s0, s1, s2 = t.stride()
     if s2 != 1:
         raise ValueError("the last axis must be contiguous")
+    n0, n1, d = t.shape
+    if n0 == 1:
+        s0 = d
+    if n1 == 1:
+        s1 = d
     return SpRows(t.data_ptr(), s1, s0) if heads_first else SpRows(t.data_ptr(), s0, s1)
 
 
@@ -733,7 +739,10 @@ def cache_alloc(pages, H_kv, page, d, *, dtype=None, kind="same", device="cuda")
     """A Cache of uninitialised pages.  kind: "same" (rows held in dtype), "e4m3" or "int8"."""
     import torch
     dtype = dtype or torch.bfloat16
-    held = {"same": dtype, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}[kind]
+    kinds = {"same": dtype, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+    if kind not in kinds:
+        raise ValueError(f"kind must be one of {sorted(kinds)} (got {kind!r})")
+    held = kinds[kind]
     new = lambda: torch.empty(pages, H_kv, page, d, dtype=held, device=device)          # noqa: E731
     scale = lambda: None if kind == "same" else torch.empty(pages, H_kv, page, dtype=torch.float32, device=device)  # noqa: E731
     return Cache(new(), new(), scale(), scale(), dtype=dtype)

@@ -142,6 +142,10 @@ sp_status check_cache(const char* fn, const sp_cache* c) {
         set_error("%s: a cache of 8-bit codes needs k_scale and v_scale", fn);
         return SP_EINVAL;
     }
+    if (!same && (reinterpret_cast<uintptr_t>(c->k_scale) % 4 || reinterpret_cast<uintptr_t>(c->v_scale) % 4)) {
+        set_error("%s: k_scale and v_scale must be 4-byte aligned", fn);
+        return SP_EINVAL;
+    }
     const int64_t align = same ? 16 : 8, step = same ? 16 / esize(c->dtype) : 8;
     if (reinterpret_cast<uintptr_t>(c->k) % align || reinterpret_cast<uintptr_t>(c->v) % align ||
         c->stride_page % step || c->stride_head % step || c->stride_slot % step) {
@@ -244,6 +248,10 @@ sp_status sp_rotary(const sp_rotary_plan* plan, const int32_t* positions, int64_
     if (T < 0 || H < 0 || H_kv < 0 || T > INT32_MAX) {
         set_error("%s: T, H and H_kv must be >= 0, T at most 2^31-1 (got %lld, %d, %d)", fn, (long long)T, H, H_kv);
         return SP_EINVAL;
+    }
+    if (H > 65535 || H_kv > 65535) {
+        set_error("%s: at most 65535 heads (got %d, %d)", fn, H, H_kv);
+        return SP_EUNSUPPORTED;
     }
     const sp_rows none{nullptr, 0, 0};
     if (T > 0 && H + H_kv > 0) {

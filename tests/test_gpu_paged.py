@@ -712,3 +712,31 @@ def test_from_the_speculators_cache_to_the_targets_sparse_prefill(sp, kind):
     ref, ref_l, top, spread = oracle.paged.attend(f64(q[:n]), kk, vv, d ** -0.5)
     bound, _ = attend_bounds("bf16", d, n, ref, spread, top, ref_l)
     assert np.all(np.abs(f64(out[:n]) - ref) <= bound)
+
+
+@pytest.mark.parametrize("T,H", [(1, 4), (1, 32), (5, 1)])
+def test_the_stride_of_one_row_or_head_is_not_looked_at(sp, T, H):
+    """Every operator on tensors whose stride is odd along an axis with one entry, against the same rows contiguous."""
+    import torch
+    d, page = 64, 16
+    stride = (3, d, 1) if T == 1 else (d, 3, 1)
+    odd = lambda like: torch.zeros(like.numel(), dtype=like.dtype, device="cuda").as_strided(like.shape, stride)  # noqa: E731
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, v = (torch.randn(T, H, d, dtype=torch.bfloat16, device="cuda", generator=g) for _ in range(2))
+    q2, v2 = odd(q), odd(v)
+    q2.copy_(q)
+    v2.copy_(v)
+    plan, pos = sp.rotary_plan(d), torch.arange(7, 7 + T, dtype=torch.int32, device="cuda")
+    want, _ = sp.rotary(q, None, pos, plan)
+    got, _ = sp.rotary(q2, None, pos, plan, q_out=odd(q))
+    assert torch.equal(got, want)
+    H_kv = 1 if H == 32 else H
+    cu, kv = (torch.tensor(x, dtype=torch.int64, device="cuda") for x in ([0, T], [T]))
+    table = torch.tensor([[1]], dtype=torch.int32, device="cuda")
+    batch = sp.Batch(cu, kv, table, rows=T)
+    outs = []
+    for a, b in ((q, v), (q2, v2)):
+        cache = sp.cache_alloc(2, H_kv, page, d)
+        sp.cache_write(cache, batch, a[:, :H_kv], b[:, :H_kv], check=True)
+        outs.append(sp.attend(a, cache, batch, out=None if a is q else odd(q), check=True))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])

@@ -196,3 +196,15 @@ def test_oracle_of_the_cache_and_the_attention():
     out, lse, _, _ = oracle.paged.attend(q, np.zeros((1, 3, 8)), v, 1.0)
     assert np.allclose(out[0, 0], v[0, :2].mean(0)) and np.allclose(out[1, 0], v[0].mean(0))
     assert np.allclose(lse, np.log([[2.0, 3.0]]))
+
+
+def test_many_heads_and_misaligned_scales_are_refused(sp):
+    plan, r = sp.SpRotaryPlan(), rows_of(sp)
+    assert sp.sp_rotary_plan_init(plan, 64, [1.0] * 32, None, 1, 0) == sp.SP_OK
+    for H, H_kv in ((65536, 1), (1, 65536), ((1 << 31) - 1, (1 << 31) - 1)):
+        assert sp.sp_rotary(plan, 64, 0, 4, 64, 0, 0, r, r, H, r, r, H_kv, 0) == sp.SP_EUNSUPPORTED
+    for over in (dict(k_scale=66, v_scale=64), dict(k_scale=64, v_scale=66)):
+        for name, s in calls(sp, cache_of(sp, kind=sp.SP_CACHE_INT8, **over), batch_of(sp), r):
+            assert s == sp.SP_EINVAL, name
+    with pytest.raises(ValueError):
+        sp.cache_alloc(1, 1, 16, 64, kind="int4", device="cpu")
