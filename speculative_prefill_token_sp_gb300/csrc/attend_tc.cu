@@ -375,12 +375,19 @@ __device__ __forceinline__ void max_cols(const float* v, float (&mx)[4]) {
         for (int c = 0; c < 4; ++c) mx[c] = fmax3(mx[c], v[i + 2 * c], v[i + 2 * c + 1]);
 }
 
-// Takes out the columns from `first` on that the row does not see.
-template <int N>
+// The lowest n bits (none if n < 0).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    uint32_t r;
+    asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(r) : "r"(max(n, 0)));
+    return r;
+}
+
+// Takes out those of 32 columns from `first` on that the row does not see (all but lo to hi).
 __device__ __forceinline__ void mask_cols(float* v, int first, int hi, int lo) {
+    const uint32_t seen = low_bits(hi - first + 1) & ~low_bits(lo - first);
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (first + i > hi || first + i < lo) v[i] = -INFINITY;
+    for (int i = 0; i < 32; ++i)
+        if (!(seen >> i & 1)) v[i] = -INFINITY;
 }
 
 // The largest logit (before the factor f) of a tile that the row sees, read once more from TMEM.
@@ -391,7 +398,7 @@ __device__ __forceinline__ float top_of_row(uint32_t s_at, uint32_t* sr, bool ma
     for (int c = 0; c < 4; ++c) {
         tmem_ld32(s_at + 32 * c, sr);
         tmem_wait32(sr);
-        if (masked) mask_cols<32>(sv, 32 * c, hi, lo);
+        if (masked) mask_cols(sv, 32 * c, hi, lo);
         max_cols<32>(sv, mx);
     }
     return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
@@ -671,7 +678,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                         tmem_ld32(s_at + 32, sr + 32);
                         tmem_ld32(s_at + 64, sr + 64);
                     }
-                    if (masked) mask_cols<32>(v3, 96, hi, lo);
+                    if (masked) mask_cols(v3, 96, hi, lo);
                     max_cols<32>(v3, mx);
 #pragma unroll
                     for (int c = 0; c < 3; ++c) {
@@ -681,7 +688,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                         if constexpr (kSame) {
                             if (c == 2) keep32(sr + 64);
                         }
-                        if (masked) mask_cols<32>(v, 32 * c, hi, lo);
+                        if (masked) mask_cols(v, 32 * c, hi, lo);
                         weights32(v, f, nm, zs, pk + 16 * c);
                     }
                     const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * f;
@@ -698,7 +705,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                     for (int c = 0; c < 4; ++c) {
                         tmem_ld32(s_at + 32 * c, sr);
                         tmem_wait32(sr);
-                        if (masked) mask_cols<32>(sv, 32 * c, hi, lo);
+                        if (masked) mask_cols(sv, 32 * c, hi, lo);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) sv[i] = __fmul_rn(sv[i], f);
                         weights32(sv, 1.f, m == -INFINITY ? 0.f : -m, zs, pk);
@@ -712,7 +719,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                     if constexpr (!kSame) {
                         tmem_ld32(s_at + 96, sr);
                         tmem_wait32(sr);
-                        if (masked) mask_cols<32>(sv, 96, hi, lo);
+                        if (masked) mask_cols(sv, 96, hi, lo);
                     }
                     weights32(kSame ? sv + 96 : sv, f, nm, zs, pk);
                     tmem_st16(s_at + 48, pk);
