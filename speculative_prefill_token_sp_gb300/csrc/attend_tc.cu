@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
             while (ok && walk.next(p, sg)) {
                 const int32_t* table = p.a.batch.table + (int64_t)sg.it.b * p.a.batch.table_stride;
                 const int seen = first_seen(sg.s, p.a.window);
-                // this lane's rows of a tile: where they are (-1: nowhere) and their scales, which are not touched before the
+                // this lane's rows of a tile: where they are and their scales, which are not touched before the
                 // tile's turn (waiting for them here took a third of the warps' time)
                 struct Where {
                     int64_t at;
@@ -819,7 +819,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                 auto token = [&](int x, int y) { return tile_of(sg, x) * kKeys + r0 + rl + 8 * y; };
                 auto page_of = [&](int tok) { return tok < sg.s.kv && tok >= seen ? table[p.a.page_of(tok)] : -1; };
                 auto place = [&](int tok, int pg) {
-                    Where w{-1, 1.f, 1.f};
+                    Where w{sub * 16, 0.f, 0.f};        // nowhere: some row, times 0
                     if (tok >= sg.s.kv || tok < seen) return w;
                     if ((unsigned)pg >= (unsigned)c.pages) {
                         bad[1] = 1;
@@ -833,8 +833,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                     return w;
                 };
                 auto fetch = [&](const void* data, int64_t at, int h) {
-                    return at >= 0 ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(data) + at + h * 64))
-                                   : make_uint4(0, 0, 0, 0);
+                    return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(data) + at + h * 64));
                 };
                 Where cur[2], nxt[2];
                 int next_page[2];
@@ -855,7 +854,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 if (more) nxt[y] = place(token(x + 1, y), next_page[y]);
-                                else nxt[y].at = -1;
+                                else nxt[y].at = sub * 16;
                             }
                         }
                         ok = wait_warp(smem_u32(&empty[st]), ph, abort_flag, 61);

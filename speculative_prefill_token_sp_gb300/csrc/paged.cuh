@@ -153,11 +153,21 @@ __device__ __forceinline__ uint32_t pair_of(uint32_t y) {
     }
     return r;
 }
-// Codes 2j and 2j + 1 of a word, and code i of one word with code i of another.
+// Codes 2j and 2j + 1 of a word.
 template <int kKind>
 __device__ __forceinline__ uint32_t codes_of(uint32_t w, int j) {
-    return pair_of<kKind>(__byte_perm(w, 0, kKind == SP_CACHE_E4M3 ? (j ? 0x3424 : 0x1404) : (j ? 0x4342 : 0x4140)));
+    if (kKind == SP_CACHE_E4M3) return pair_of<kKind>(__byte_perm(w, 0, j ? 0x3424 : 0x1404));
+    // With the sign bit flipped a code is u = code + 128, and y = 0x4300 + u as a bf16 is 128 + u below u = 128 and 2 u from there
+    // on.  So the code is y - 256 below, and the half of that above: y - 256 - max(y / 2 - 128, 0).  (With the two masks of
+    // pair_of the integer pipe bounds the conversion.)
+    const uint32_t y = __byte_perm(w ^ 0x80808080u, 0x43434343u, j ? 0x4342 : 0x4140);
+    uint32_t t, r;
+    asm("fma.rn.relu.bf16x2 %0, %1, %2, %3;" : "=r"(t) : "r"(y), "r"(0x3f003f00u), "r"(0xc300c300u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x43804380u));
+    asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(t));
+    return r;
 }
+// Code i of one word with code i of another.
 template <int kKind>
 __device__ __forceinline__ uint32_t codes_of(uint32_t a, uint32_t b, int i) {
     return pair_of<kKind>(__byte_perm(a, b, kKind == SP_CACHE_E4M3 ? 0x4000 + (i << 12) + (i << 4) : 0x0400 + (i << 8) + i));
