@@ -416,14 +416,16 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
                                                 (cc * 8 + n) * kVB);
 #pragma unroll
                     for (int e = 0; e < kEv; e += 2) {
-                        uint32_t a[4];
+                        uint32_t a[4];              // entries e and e + 1 of tokens 2q, 2q + 1, then of 2q + 8, 2q + 9
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {       // entry e + (y & 1) of tokens 2q, 2q + 1 (+ 8 for y >= 2)
-                            const int w = (e + (y & 1)) * kSize / 4, i2 = (y >> 1) * 2;
+                        for (int y = 0; y < 4; y += 2) {
+                            const int w = e * kSize / 4;
+                            const uint32_t t0 = vr[y].w[w], t1 = vr[y + 1].w[w];
                             if constexpr (kSame) {
-                                a[y] = __byte_perm(vr[i2].w[w], vr[i2 + 1].w[w], y & 1 ? 0x7632 : 0x5410);
+                                a[y] = __byte_perm(t0, t1, 0x5410);
+                                a[y + 1] = __byte_perm(t0, t1, 0x7632);
                             } else {
-                                a[y] = codes_of<kKind>(vr[i2].w[w], vr[i2 + 1].w[w], (e + (y & 1)) & 3);
+                                pairs_of<kKind, false>(__byte_perm(t0, t1, e & 2 ? 0x7632 : 0x5410), a[y], a[y + 1]);
                             }
                         }
 #pragma unroll

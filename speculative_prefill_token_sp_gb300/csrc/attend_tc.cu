@@ -870,8 +870,10 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                                 uint32_t o[8];
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
-                                    o[2 * i] = mul_bf16x2(codes_of<kKind>(w4[i], 0), scale);
-                                    o[2 * i + 1] = mul_bf16x2(codes_of<kKind>(w4[i], 1), scale);
+                                    uint32_t lo, hi;
+                                    pairs_of<kKind, true>(w4[i], lo, hi);
+                                    o[2 * i] = mul_bf16x2(lo, scale);
+                                    o[2 * i + 1] = mul_bf16x2(hi, scale);
                                 }
                                 codes[y][h] = v ? fetch(c.k, nxt[y].at, h) : fetch(c.v, cur[y].at, h);
                                 uint8_t* at = tile + y * 1024 + h * (kKeys * 128);

@@ -136,41 +136,31 @@ __device__ __forceinline__ void decode8(uint2 u, float (&x)[8]) {
     }
 }
 
-// Two 8-bit codes as a pair of bf16 (their values before the scale, exactly).  The codes are brought to where they are needed
-// by a byte permute: bits 8-15 and 24-31 of y for e4m3, bits 0-7 and 16-23 for int8; the other bits are ignored.
-template <int kKind>
-__device__ __forceinline__ uint32_t pair_of(uint32_t y) {
-    uint32_t r;
-    if (kKind == SP_CACHE_E4M3) {
+// The four codes of a word as two pairs of bf16 (their values before the scale, exactly): codes 0, 1 and 2, 3 (kNext), or codes 0, 2
+// and 1, 3.  The integer pipe bounds what uses this, so it has few masks and permutes, and the rest is left to the FMA pipe.
+template <int kKind, bool kNext>
+__device__ __forceinline__ void pairs_of(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if constexpr (kKind == SP_CACHE_E4M3) {
         // exponent and mantissa moved to bf16's place mean the value * 2^-120 (biases 7 and 127), also
         // for e4m3's subnormals; the product with 2^120 is exact.  0x7f is NaN in e4m3, never written, and 480 here
-        const uint32_t b = ((y >> 4) & 0x07f007f0u) | (y & 0x80008000u);
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(b), "r"(0x7b807b80u));
+        if (kNext) w = __byte_perm(w, 0, 0x3120);
+        const uint32_t b0 = ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u), b1 = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(b0), "r"(0x7b807b80u));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(b1), "r"(0x7b807b80u));
     } else {
-        // 0x4300 + (7 bits) is 128 + those bits; minus 128, or minus 256 (0x4380) where the sign bit is set
-        const uint32_t lo = (y & 0x007f007fu) | 0x43004300u, off = (y & 0x00800080u) | 0x43004300u;
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(lo), "r"(off));
+        // With the sign bit flipped a code is u = code + 128, and y = 0x4300 + u as a bf16 is 128 + u below u = 128 and 2 u from
+        // there on.  So the code is y - 256 below, and the half of that above: y - 256 - max(y / 2 - 128, 0).
+        auto value = [](uint32_t y) {
+            uint32_t t, r;
+            asm("fma.rn.relu.bf16x2 %0, %1, %2, %3;" : "=r"(t) : "r"(y), "r"(0x3f003f00u), "r"(0xc300c300u));
+            asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x43804380u));
+            asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(t));
+            return r;
+        };
+        w ^= 0x80808080u;
+        lo = value(__byte_perm(w, 0x43434343u, kNext ? 0x4140 : 0x4240));
+        hi = value(__byte_perm(w, 0x43434343u, kNext ? 0x4342 : 0x4341));
     }
-    return r;
-}
-// Codes 2j and 2j + 1 of a word.
-template <int kKind>
-__device__ __forceinline__ uint32_t codes_of(uint32_t w, int j) {
-    if (kKind == SP_CACHE_E4M3) return pair_of<kKind>(__byte_perm(w, 0, j ? 0x3424 : 0x1404));
-    // With the sign bit flipped a code is u = code + 128, and y = 0x4300 + u as a bf16 is 128 + u below u = 128 and 2 u from there
-    // on.  So the code is y - 256 below, and the half of that above: y - 256 - max(y / 2 - 128, 0).  (With the two masks of
-    // pair_of the integer pipe bounds the conversion.)
-    const uint32_t y = __byte_perm(w ^ 0x80808080u, 0x43434343u, j ? 0x4342 : 0x4140);
-    uint32_t t, r;
-    asm("fma.rn.relu.bf16x2 %0, %1, %2, %3;" : "=r"(t) : "r"(y), "r"(0x3f003f00u), "r"(0xc300c300u));
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x43804380u));
-    asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(t));
-    return r;
-}
-// Code i of one word with code i of another.
-template <int kKind>
-__device__ __forceinline__ uint32_t codes_of(uint32_t a, uint32_t b, int i) {
-    return pair_of<kKind>(__byte_perm(a, b, kKind == SP_CACHE_E4M3 ? 0x4000 + (i << 12) + (i << 4) : 0x0400 + (i << 8) + i));
 }
 
 // The scale of a row whose largest magnitude is `top` (NaN or infinite if an
