@@ -64,6 +64,17 @@ __device__ __forceinline__ void join(float& m, float& z, float (&o)[8], float m2
     m = top;
 }
 
+// Adds up the sums of a warp's groups of `lanes` lanes.
+__device__ __forceinline__ void join_groups(float& m, float& z, float (&o)[8], int lanes) {
+    for (int w = lanes; w < 32; w <<= 1) {
+        float o2[8];
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, w), z2 = __shfl_xor_sync(0xffffffffu, z, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o2[e] = __shfl_xor_sync(0xffffffffu, o[e], w);
+        join(m, z, o, m2, z2, o2);
+    }
+}
+
 template <typename T>
 __device__ __forceinline__ void write_out(const SplitArgs& p, int64_t row, int h, int e, float m, float z, float (&o)[8]) {
     const float inv = z == 0.f ? 0.f : 1.f / z;
@@ -119,7 +130,7 @@ __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(const __grid_co
 #pragma unroll
             for (int e = 0; e < 8; ++e) q[i][e] = o[i][e] = 0.f;
             if (i >= rows) continue;
-            const int t = (int)((r0 + i) / p.G), h = g * p.G + (int)(r0 + i - (int64_t)t * p.G);
+            const int t = (int)divide(r0 + i, p.G), h = g * p.G + (int)(r0 + i - (int64_t)t * p.G);
             if (act) load8(static_cast<const T*>(p.a.q.data) + (s.row0 + t) * p.a.q.stride_row + h * p.a.q.stride_head + sub * 8, q[i]);
             last[i] = s.kv - s.n + t;
             item_last = max(item_last, last[i]);
@@ -198,13 +209,8 @@ __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(const __grid_co
         // join the groups of the warp, then the warps
 #pragma unroll
         for (int i = 0; i < kGenRows; ++i) {
-            for (int w = lanes; w < 32; w <<= 1) {
-                float o2[8];
-                const float m2 = __shfl_xor_sync(0xffffffffu, m[i], w), z2 = __shfl_xor_sync(0xffffffffu, z[i], w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o2[e] = __shfl_xor_sync(0xffffffffu, o[i][e], w);
-                join(m[i], z[i], o[i], m2, z2, o2);
-            }
+            if (i >= rows) break;
+            join_groups(m[i], z[i], o[i], lanes);
             if (grp == 0) {
                 if (sub == 0) sm_ml[warp][i] = make_float2(m[i], z[i]);
                 if (act) store8(&sm_o[warp][i][sub * 8], o[i]);
@@ -224,7 +230,7 @@ __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(const __grid_co
                 join(mm, zz, v, sm_ml[w][r].x, sm_ml[w][r].y, o2);
             }
             if (whole) {
-                const int64_t t = (r0 + r) / p.G;
+                const int64_t t = divide(r0 + r, p.G);
                 write_out<T>(p, s.row0 + t, g * p.G + (int)(r0 + r - t * p.G), e, mm, zz, v);
             } else {
                 const int64_t slot = ((int64_t)blockIdx.x * 2 + (from == 0 ? 1 : 0)) * kRows + r;
@@ -239,39 +245,71 @@ __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(const __grid_co
     if (threadIdx.x == 0) p.err[blockIdx.x] = any;
 }
 
-// Joins the parts of the items that were cut: block i takes the item whose
-// first cut is the one before CTA i + 1, a warp one of its rows.
+constexpr int kJoinWarps = 8;
+
+// Joins the parts of the items that were cut: block (i, r) takes row r of the item whose first cut is the one before CTA i + 1.  Each
+// group of 2^lg lanes has eight entries a lane of every so many parts, the next of them on the way while one is added: an
+// item may be cut into hundreds (one after the other they took 0.4 us each).
 template <typename T>
-__global__ void __launch_bounds__(32 * kGenRows) general_join_kernel(const __grid_constant__ SplitArgs p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) general_join_kernel(const __grid_constant__ SplitArgs p, int lg) {
+    __shared__ float sm_o[kJoinWarps][256];
+    __shared__ float2 sm_ml[kJoinWarps];
     bool bad = false;
     const int64_t U = total_units(p, kUnit, bad);
     const Shares shares(U, p.P);
-    const int c = blockIdx.x + 1, r = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x + 1, r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t u = shares.at(c);
     int64_t begin = 0;
-    const int b = u < U ? find_unit(p, kUnit, u, begin) : 0;
+    const int b = u < U ? find_unit(p, kUnit, u, begin) : p.a.batch.B;
+    const Seq s = b < p.a.batch.B ? load_seq(p.a.batch, p.a.cache.page, b) : Seq{0, 0, 0, true};
     cudaGridDependencySynchronize();        // the main kernel's parts
-    if (blockIdx.x == 0) gather_status(p);
-    if (u >= U) return;
-    const Seq s = load_seq(p.a.batch, p.a.cache.page, b);
+    if (blockIdx.x == 0 && r == 0) gather_status(p);
+    if (b >= p.a.batch.B) return;
     const int units = span_of(s, p.a.window, kUnit).units, blocks = row_blocks(p, s);
     const int64_t item = divide(u - begin, units), first = begin + item * units;
     if (u == first || shares.at(c - 1) > first) return;       // no cut, or not the item's first
     const int g = (int)divide(item, blocks);
     const int64_t row = (item - (int64_t)g * blocks) * kGenRows + r;
     if (row >= (int64_t)s.n * p.G) return;
-    const int e = lane * 8;
-    float m = -INFINITY, z = 0.f, o[8] = {};
+    const int lanes = 1 << lg, e = (lane & (lanes - 1)) * 8, groups = 32 * kJoinWarps >> lg;
+    const bool act = e < p.a.cache.d;
     const int c1 = shares.of(first + units - 1);
-    for (int k = c - 1; k <= c1; ++k) {
+    struct Part {
+        float2 ml;
+        float o[8];
+    };
+    auto fetch = [&](int k) {
+        Part x = {make_float2(-INFINITY, 0.f), {}};
+        if (k > c1) return x;
         const int64_t slot = ((int64_t)k * 2 + (k == c - 1 ? 1 : 0)) * kRows + r;
-        const float2 ml = p.part_ml[slot];
-        float o2[8] = {};
-        if (e < p.a.cache.d) load8(p.part_o + slot * p.a.cache.d + e, o2);
-        join(m, z, o, ml.x, ml.y, o2);
+        x.ml = p.part_ml[slot];
+        if (act) load8(p.part_o + slot * p.a.cache.d + e, x.o);
+        return x;
+    };
+    float m = -INFINITY, z = 0.f, o[8] = {};
+    const int k0 = c - 1 + (threadIdx.x >> lg);
+    Part next = fetch(k0);
+    for (int k = k0; k <= c1; k += groups) {
+        const Part x = next;
+        next = fetch(k + groups);
+        join(m, z, o, x.ml.x, x.ml.y, x.o);
     }
-    const int64_t t = row / p.G;
-    if (e < p.a.cache.d) write_out<T>(p, s.row0 + t, g * p.G + (int)(row - t * p.G), e, m, z, o);
+    __syncwarp();
+    join_groups(m, z, o, lanes);
+    if (lane < lanes) {
+        if (lane == 0) sm_ml[warp] = make_float2(m, z);
+        if (act) store8(&sm_o[warp][e], o);
+    }
+    __syncthreads();
+    if (warp > 0 || lane >= lanes || !act) return;
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) {
+        float o2[8];
+        load8(&sm_o[w][e], o2);
+        join(m, z, o, sm_ml[w].x, sm_ml[w].y, o2);
+    }
+    const int64_t t = divide(row, p.G);
+    write_out<T>(p, s.row0 + t, g * p.G + (int)(row - t * p.G), e, m, z, o);
 }
 
 int general_ctas() { return sm_count() * 3; }
@@ -286,7 +324,9 @@ sp_status launch(const SplitArgs& p, cudaStream_t st) {
         default: general_kernel<T, SP_CACHE_INT8><<<p.P, kGenThreads, 0, st>>>(p, lg); break;
     }
     SP_LAUNCH_CHECK();
-    return launch_early(general_join_kernel<T>, dim3((unsigned)p.P - 1), 32 * kGenRows, (size_t)0, st, p);
+    const int64_t rows = std::min<int64_t>(kGenRows, (int64_t)p.a.batch.max_new * p.G);
+    const dim3 grid((unsigned)p.P - 1, (unsigned)std::max<int64_t>(1, rows));
+    return launch_early(general_join_kernel<T>, grid, 32 * kJoinWarps, (size_t)0, st, p, lg);
 }
 
 }  // namespace
