@@ -598,11 +598,12 @@ def _rows(t, heads_first=False):
     s0, s1, s2 = t.stride()
     if s2 != 1:
         raise ValueError("the last axis must be contiguous")
-    n0, n1, d = t.shape
-    if n0 == 1:
-        s0 = d
-    if n1 == 1:
-        s1 = d
+    if (s0 | s1) & 7:
+        n0, n1, d = t.shape
+        if n0 == 1:
+            s0 = d
+        if n1 == 1:
+            s1 = d
     return SpRows(t.data_ptr(), s1, s0) if heads_first else SpRows(t.data_ptr(), s0, s1)
 
 
