@@ -596,7 +596,7 @@ def _rows(t, heads_first=False):
     """sp_rows of a tensor [rows, heads, d] (heads_first: [heads, rows, d]) whose last axis is contiguous.  The stride
     of an axis with one entry may be anything in torch: d takes its place."""
     s0, s1, s2 = t.stride()
-    if s2 != 1:
+    if s2 != 1 and t.numel():
         raise ValueError("the last axis must be contiguous")
     if (s0 | s1) & 7:
         n0, n1, d = t.shape

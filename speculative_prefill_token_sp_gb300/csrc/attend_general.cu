@@ -12,7 +12,7 @@
 // multiply-adds, g shuffles and about ten other instructions, which bounds the
 // kernel for many rows; for few it is bound by the latency of its loads, so the
 // keys are cut over all the CTAs that the SMs hold.  One fp32 token over 512 (4 query
-// heads on 2 of 64) takes 12.5 us with the joining kernel.
+// heads on 2 of 64) takes 10.6 us with the joining kernel, over 8192 13.3 us.
 #include "attend_split.cuh"
 
 #include <algorithm>

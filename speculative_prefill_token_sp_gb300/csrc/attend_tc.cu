@@ -39,8 +39,11 @@
 //
 // A chunk of 4096 over 32768 (bf16, 32 query heads on 8 of 128) takes 1.13 ms,
 // 1.83 PFLOP/s or 95% of the rate of a large library product; in a long loop the board's
-// power limit makes it 1.30 to 1.34 ms.  Seven requests of 192 to 650 new tokens with
-// a window of 4096 take 161 us from an int8 cache, 126 us from bf16.
+// power limit makes it 1.29 to 1.37 ms.  Seven requests of 192 to 650 new tokens with
+// a window of 4096 take 136 us from an int8 cache, 111 us from bf16: 51 key tiles a CTA
+// of 1.45 us (int8: about 2, the conversion's warps share the schedulers with
+// the softmax's), 10 us until the first logits, 5 us more for each of an SM's two
+// or three items, 5 us of step kernels without work and as much of joining.
 #include "paged.cuh"
 #include "tc_ptx.cuh"
 
@@ -66,8 +69,8 @@ constexpr int kRowsItem = 256;
 constexpr int kKeys = 128;              // keys of a tile
 constexpr int kSmem = 227 * 1024;
 // What an item costs beside its key tiles (queries, first maximum, output), in key tiles: it counts so many more in the division
-// of the work.  Seven requests of 192 to 650 new tokens, 5 to 33 tiles an item, took 162, 142, 132, 128, 126 us with 0 to 4 (bf16) and
-// 203, 189, 175, 169, 173 us (int8).
+// of the work.  Seven requests of 192 to 650 new tokens, 3 to 34 tiles an item, take 111, 111, 113 us with 2, 3, 4 (bf16) and
+// 135, 135, 138 us (int8); before the items' ends were made faster they took 162, 142, 132, 128, 126 us with 0 to 4 (bf16).
 constexpr int kExtra = 3;
 constexpr int kMaxSeqs = 16384;         // their item counts are laid out in the (still empty) ring of key tiles
 

@@ -740,3 +740,19 @@ def test_the_stride_of_one_row_or_head_is_not_looked_at(sp, T, H):
         sp.cache_write(cache, batch, a[:, :H_kv], b[:, :H_kv], check=True)
         outs.append(sp.attend(a, cache, batch, out=None if a is q else odd(q), check=True))
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("stride", [(0, 0, 0), (3, 5, 7)])
+def test_the_strides_of_an_empty_tensor_are_not_looked_at(sp, stride):
+    import torch
+    H, d = 4, 64
+    none = torch.empty(0, dtype=torch.bfloat16, device="cuda").as_strided((0, H, d), stride)
+    cache = sp.cache_alloc(2, H, 16, d)
+    batch = sp.Batch(torch.zeros(2, dtype=torch.int64, device="cuda"), torch.tensor([5], device="cuda"),
+                     torch.zeros(1, 1, dtype=torch.int32, device="cuda"), rows=0)
+    sp.cache_write(cache, batch, none, none, check=True)
+    sp.cache_read(cache, batch, out_k=none.transpose(0, 1), check=True)
+    out, lse = sp.attend(none, cache, batch, check=True)
+    assert out.shape == (0, H, d) and lse.shape == (H, 0)
+    q, k = sp.rotary(none, none, torch.empty(0, dtype=torch.int32, device="cuda"), sp.rotary_plan(d), q_out=none)
+    assert q.shape == k.shape == (0, H, d)
