@@ -12,10 +12,12 @@
 // multiply-adds, g shuffles and about ten other instructions, which bounds the
 // kernel for many rows; for few it is bound by the latency of its loads, so the
 // keys are cut over all the CTAs that the SMs hold.  One fp32 token over 512 (4 query
-// heads on 2 of 64) takes 10.6 us with the joining kernel, over 8192 13.3 us.
+// heads on 2 of 64) takes 10.1 us with the joining kernel, over 8192 13 us;
+// one token each of 16 requests over 32768 (16 on 4 heads of 64, fp32) 340 us (3.2 TB/s).
 #include "attend_split.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace sp {
 namespace {
@@ -160,34 +162,56 @@ __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(const __grid_co
             k.load(c.k, c.k_scale, at, sc);
             v.load(c.v, c.v_scale, at, sc);
         };
+        // Adds a key.  The first R rows at once and without branches between them, so that their shuffles and exponentials overlap.
+        auto add = [&](auto R, int tok, const float (&k)[8], const float (&v)[8]) {
+            constexpr int kR = decltype(R)::value;
+            float x[kR];
+            bool seen[kR], grows = false;
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {
+                x[i] = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[i] += q[i][e] * k[e];
+            }
+            for (int w = 1; w < lanes; w <<= 1) {
+#pragma unroll
+                for (int i = 0; i < kR; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], w);
+            }
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {
+                seen[i] = tok >= 0 && tok <= last[i] && (!p.a.window || tok > last[i] - p.a.window);
+                x[i] = seen[i] ? x[i] * f : -INFINITY;
+                grows |= x[i] > m[i];
+            }
+            if (grows) {
+#pragma unroll
+                for (int i = 0; i < kR; ++i) {
+                    const float top = fmaxf(m[i], x[i]), a = m[i] == top ? 1.f : ex2(m[i] - top);
+                    m[i] = top;
+                    z[i] *= a;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[i][e] *= a;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {
+                const float w2 = ex2(x[i] - (m[i] == -INFINITY ? 0.f : m[i]));
+                z[i] += w2;
+                if (seen[i]) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[i][e] += w2 * v[e];
+                }
+            }
+        };
         auto use = [&](int tok, const Row8<T, kKind>& kr, const Row8<T, kKind>& vr) {
             float k[8] = {}, v[8] = {};
             if (tok >= 0 && act) {
                 kr.get(k);
                 vr.get(v);
             }
-#pragma unroll
-            for (int i = 0; i < kGenRows; ++i) {
-                if (i >= rows) break;
-                float x = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x += q[i][e] * k[e];
-                for (int w = 1; w < lanes; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-                x *= f;
-                const int lo = p.a.window ? last[i] - p.a.window + 1 : 0;
-                if (tok < 0 || tok > last[i] || tok < lo) continue;
-                if (x > m[i]) {
-                    const float a = ex2(m[i] - x);
-                    m[i] = x;
-                    z[i] *= a;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[i][e] *= a;
-                }
-                const float w2 = ex2(x - (m[i] == -INFINITY ? 0.f : m[i]));
-                z[i] += w2;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[i][e] += w2 * v[e];
-            }
+            if (rows > 2) add(std::integral_constant<int, 4>{}, tok, k, v);
+            else if (rows == 2) add(std::integral_constant<int, 2>{}, tok, k, v);
+            else add(std::integral_constant<int, 1>{}, tok, k, v);
         };
         int t0 = token(0), t1 = token(1);
         int pg0 = page_of(t0), pg1 = page_of(t1);
