@@ -503,6 +503,12 @@ def test_a_long_cache(sp):
     check_attend(sp, H=2, H_kv=1, d=64, page=16, new=[1, 17], kv=[70001, 9001])
 
 
+@pytest.mark.parametrize("H,H_kv,d,page", [(4, 2, 64, 16), (3, 1, 256, 7), (2, 1, 8, 32)])
+@pytest.mark.parametrize("kind", ["same", "int8"])
+def test_items_cut_into_hundreds_of_parts(sp, H, H_kv, d, page, kind):
+    check_attend(sp, H=H, H_kv=H_kv, d=d, page=page, new=[1, 2], kv=[20000, 9000], dtype="f32", kind=kind)
+
+
 @pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (48, "bf16"), (64, "f32")])
 @pytest.mark.parametrize("n", [1, 150])
 def test_strided_queries_and_outputs(sp, d, dtype, n):
