@@ -349,9 +349,9 @@ typedef struct {
     uint8_t  axis[128];
 } sp_rotary_plan;
 
-/* Fills `plan` (host memory).  rot: even, 2 .. 256, a multiple of 16.  Pair i
+/* Fills `plan` (host memory).  rot: a multiple of 16, 16 .. 256.  Pair i
  * (i < rot / 2) is entries (i, i + rot / 2) of a head, or (2i, 2i + 1) if
- * `interleaved`; it turns by inv_freq_host[i] radians a position (finite) of
+ * `interleaved`; it turns by inv_freq_host[i] radians a position (at most 2^40 either way) of
  * axis axis_of_pair_host[i] (< axes <= 8; NULL: axis 0).  Several axes are the
  * positions of image and video tokens: time, height, width. */
 sp_status sp_rotary_plan_init(sp_rotary_plan* plan, int rot, const double* inv_freq_host,

@@ -80,6 +80,17 @@ sp_status check_workspace(const char* fn, const void* ws, size_t have, size_t ne
     return SP_OK;
 }
 
+// f / 2 pi modulo 1 in units of 2^-64, to one and a half of them for |f| <= 2^40: a position of 2^31 multiplies the error.  1 / 2 pi is
+// the sum of two doubles, and so is the product; taken of |f|, since the fraction of a small negative number would be rounded.
+uint64_t fraction_of_turn(double f) {
+    constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+    const double x = fabs(f);
+    const volatile double rounded = x * kHi;        // volatile: a compiler may fuse the product with what follows, and count lo twice
+    const double hi = rounded, lo = fma(x, kHi, -hi) + x * kLo;
+    const uint64_t u = (uint64_t)ldexp(hi - floor(hi), 64) + (uint64_t)llrint(ldexp(lo, 64));
+    return f < 0 ? 0 - u : u;
+}
+
 // Which kernels a call takes.
 enum Path {
     kGeneral,       // the general one
@@ -213,13 +224,16 @@ sp_status sp_rotary_plan_init(sp_rotary_plan* plan, int rot, const double* inv_f
     p.interleaved = interleaved != 0;
     p.axes = axes;
     for (int i = 0; i < rot / 2; ++i) {
-        const double turns = inv_freq_host[i] / 6.283185307179586476925286766559;
-        if (!isfinite(turns)) {
+        const double f = inv_freq_host[i];
+        if (!isfinite(f)) {
             set_error("%s: frequency %d is not finite", fn, i);
             return SP_EINVAL;
         }
-        const double f = turns - floor(turns);          // in [0, 1]: 1 where a tiny negative rounds up
-        p.turns[i] = f < 1.0 ? (uint64_t)ldexp(f, 64) : 0;
+        if (fabs(f) > 0x1p40) {
+            set_error("%s: frequency %d is above 2^40 radians a position (%g)", fn, i, f);
+            return SP_EUNSUPPORTED;
+        }
+        p.turns[i] = fraction_of_turn(f);
         p.axis[i] = axis_of_pair_host ? axis_of_pair_host[i] : 0;
         if (p.axis[i] >= axes) {
             set_error("%s: pair %d has axis %d of %d", fn, i, (int)p.axis[i], axes);

@@ -1,6 +1,7 @@
 """Rotary positions, the paged cache and the attention over it: what is refused, and what the host works out (no GPU)."""
 import ctypes
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -208,3 +209,27 @@ def test_many_heads_and_misaligned_scales_are_refused(sp):
             assert s == sp.SP_EINVAL, name
     with pytest.raises(ValueError):
         sp.cache_alloc(1, 1, 16, 64, kind="int4", device="cpu")
+
+
+PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+
+
+@pytest.mark.parametrize("freq", [
+    [1.0, -1.0, 0.1, -0.1, 1e-5, -1e-5, 3e-9, -3e-9], [6.0, -6.0, 7.0, 100.0, -1000.0, 1e6, 2.0 ** 40, -2.0 ** 40],
+    [2 * math.pi, -2 * math.pi, 0.0, -0.0, 1e-300, -1e-300, 5e-324, -5e-324],
+])
+def test_rotary_plan_is_exact_for_fast_and_negative_frequencies(sp, freq):
+    """A position of 2^31 multiplies the error of a fraction: at 2^-62 of a turn the angle is off by 2^-31 of one."""
+    plan = sp.rotary_plan(16, inv_freq=freq)
+    for i, f in enumerate(freq):
+        turns = Fraction(f) / (2 * PI)          # off by 2^-256 of itself
+        off = (Fraction(plan.turns[i], 1 << 64) - turns) % 1
+        # cut off once and rounded once, to 2^-64 of a turn each; the product with 1 / 2 pi in two doubles is off by 2^-105 of it
+        assert min(off, 1 - off) <= Fraction(3, 1 << 65) + abs(turns) / (1 << 105), f
+
+
+def test_rotary_frequencies_beyond_2_40_are_refused(sp):
+    plan = sp.SpRotaryPlan()
+    for f in (2.0 ** 40 * (1 + 2.0 ** -52), -1e300):
+        assert sp.sp_rotary_plan_init(plan, 16, [1.0] * 7 + [f], None, 1, 0) == sp.SP_EUNSUPPORTED
+        assert sp.sp_last_error()
