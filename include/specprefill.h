@@ -473,8 +473,8 @@ size_t sp_attend_workspace_size(const sp_cache* cache, const sp_batch* batch, in
  *            look-ahead steps of one request (T = 1, layer l of sp_score_lse's lse [L, H, N]):
  *            pointer lse + l * H * N + j, lse_stride_head = N
  *
- * Requirements: 8 <= d <= 256, d % 8 == 0, H % H_kv == 0, scale > 0 and
- * finite.  Before a call of a kind is captured into a graph, one of that kind should have run,
+ * Requirements: 8 <= d <= 256, d % 8 == 0, H % H_kv == 0, scale in 8.2e-39 .. 2.3e38
+ * (scale * log2(e) is a normal fp32 number).  Before a call of a kind is captured into a graph, one of that kind should have run,
  * as CUDA may load a kernel at its first launch.  What unwritten slots hold (NaN too) has no effect, nor have rows
  * that are not a token of the batch.  A NaN or an infinity in a key or value of a token that
  * some rows of the sequence see may reach its other rows as well.

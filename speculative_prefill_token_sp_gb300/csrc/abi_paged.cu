@@ -3,6 +3,7 @@
 // here, before anything is enqueued.
 #include "paged.cuh"
 
+#include <float.h>
 #include <string.h>
 
 #include <algorithm>
@@ -346,8 +347,9 @@ sp_status sp_attend(const sp_rows* q, const sp_cache* cache, const sp_batch* bat
         set_error("%s: H (%d) must be a multiple of H_kv (%d)", fn, H, cache->H_kv);
         return SP_EINVAL;
     }
-    if (!(scale > 0.0) || !isfinite((float)scale)) {
-        set_error("%s: scale must be positive and finite (got %g)", fn, scale);
+    const float factor = (float)scale * 1.4426950408889634f;        // the kernels': logits to base 2
+    if (!(factor >= FLT_MIN) || !isfinite(factor)) {
+        set_error("%s: scale must be positive, and a normal fp32 number times log2(e) (got %g)", fn, scale);
         return SP_EINVAL;
     }
     if (window < 0) {

@@ -233,3 +233,11 @@ def test_rotary_frequencies_beyond_2_40_are_refused(sp):
     for f in (2.0 ** 40 * (1 + 2.0 ** -52), -1e300):
         assert sp.sp_rotary_plan_init(plan, 16, [1.0] * 7 + [f], None, 1, 0) == sp.SP_EUNSUPPORTED
         assert sp.sp_last_error()
+
+
+def test_scales_that_single_precision_does_not_hold_are_refused(sp):
+    """The kernels take logits to base 2: scale * log2(e) has to be a normal fp32 number."""
+    c, b, r = cache_of(sp), batch_of(sp), rows_of(sp)
+    for scale in (5e-324, 1e-46, 1e-40, 8.1e-39, 2.4e38, 3e38, 1e39):
+        assert sp.sp_attend(r, c, b, 4, scale, 0, r, None, 0, 0, 65536, 1 << 40, 0) == sp.SP_EINVAL, scale
+        assert "scale" in sp.sp_last_error()
