@@ -58,11 +58,29 @@ sp_status check_rows(const char* fn, const char* what, const sp_rows* r, sp_dtyp
     return SP_OK;
 }
 
+// Whether places i0 * stride0 + i1 * stride1 + ... of `width` entries each lie apart, as in every tensor that slices and permutations
+// make of a contiguous one: the steps of each axis pass over all that the axes of smaller steps span.
+struct Axis {
+    int64_t extent, stride;
+};
+template <int N>
+bool apart(Axis (&axis)[N], int width) {
+    std::sort(axis, axis + N, [](const Axis& a, const Axis& b) { return a.stride < b.stride; });
+    __int128 span = width;
+    for (const Axis& a : axis) {
+        if (a.extent <= 1) continue;
+        if (a.stride < span) return false;
+        span += (__int128)(a.extent - 1) * a.stride;
+    }
+    return true;
+}
+
 // Rows that are written, or that a tensor map describes, must not overlap.
 sp_status check_apart(const char* fn, const char* what, const sp_rows* r, int64_t rows, int heads, int d) {
     const int64_t most = (int64_t)1 << 38;
+    Axis axis[2] = {{rows, r->stride_row}, {heads, r->stride_head}};
     if (rows == 0) return SP_OK;
-    if ((rows > 1 && (r->stride_row < d || r->stride_row > most)) || (heads > 1 && (r->stride_head < d || r->stride_head > most))) {
+    if ((rows > 1 && r->stride_row > most) || (heads > 1 && r->stride_head > most) || !apart(axis, d)) {
         set_error("%s: the rows of %s must not overlap, and its strides must be at most 2^38", fn, what);
         return SP_EINVAL;
     }

@@ -241,3 +241,33 @@ def test_scales_that_single_precision_does_not_hold_are_refused(sp):
     for scale in (5e-324, 1e-46, 1e-40, 8.1e-39, 2.4e38, 3e38, 1e39):
         assert sp.sp_attend(r, c, b, 4, scale, 0, r, None, 0, 0, 65536, 1 << 40, 0) == sp.SP_EINVAL, scale
         assert "scale" in sp.sp_last_error()
+
+
+# 10 rows of 4 (H) or 2 (H_kv) heads of 64; each stride by itself is at least a row
+CROSSED = [dict(stride_row=64, stride_head=64), dict(stride_row=128, stride_head=64), dict(stride_row=64, stride_head=576),
+           dict(stride_row=120, stride_head=64), dict(stride_row=(1 << 38), stride_head=(1 << 38))]
+
+
+@pytest.mark.parametrize("over", CROSSED)
+def test_rows_of_one_head_that_meet_those_of_another_are_refused(sp, over):
+    c, b, good, bad = cache_of(sp), batch_of(sp), rows_of(sp), rows_of(sp, **over)
+    big = 1 << 40
+    assert sp.sp_attend(good, c, b, 4, 0.125, 0, bad, None, 0, 0, 65536, big, 0) == sp.SP_EINVAL
+    assert "overlap" in sp.sp_last_error()
+    assert sp.sp_attend(bad, c, b, 4, 0.125, 0, good, None, 0, 0, 65536, big, 0) == sp.SP_EINVAL
+    plan = sp.SpRotaryPlan()
+    assert sp.sp_rotary_plan_init(plan, 64, [1.0] * 32, None, 1, 0) == sp.SP_OK
+    assert sp.sp_rotary(plan, 64, 0, 10, 64, 0, 0, good, bad, 4, None, None, 0, 0) == sp.SP_EINVAL
+    assert sp.sp_rotary(plan, 64, 0, 10, 64, 0, 0, None, None, 0, good, bad, 4, 0) == sp.SP_EINVAL
+    if over["stride_row"] != 128:       # two heads of 64 do fit there
+        assert sp.sp_cache_read(c, b, bad, None, 65536, big, 0) == sp.SP_EINVAL
+        assert sp.sp_cache_read(c, b, None, bad, 65536, big, 0) == sp.SP_EINVAL
+
+
+@pytest.mark.parametrize("over", [dict(stride_row=256, stride_head=64), dict(stride_row=64, stride_head=640),
+                                  dict(stride_row=1 << 38, stride_head=64), dict(stride_row=264, stride_head=64)])
+def test_rows_apart_are_taken(sp, over):
+    """An empty workspace is refused behind the rows: that is how far these calls come."""
+    c, b, r = cache_of(sp), batch_of(sp), rows_of(sp, **over)
+    assert sp.sp_attend(r, c, b, 4, 0.125, 0, r, None, 0, 0, 65536, 0, 0) == sp.SP_ENOMEM
+    assert sp.sp_cache_read(c, b, r, r, 65536, 0, 0) == sp.SP_ENOMEM
