@@ -437,7 +437,9 @@ size_t sp_cache_workspace_size(void);
 /* Writes the new tokens' keys and values, k_new and v_new [T, H_kv, d], to
  * their places in the cache, quantising as the cache's kind says.  A new
  * token whose place would be negative (kv_len below the number of new tokens) is
- * skipped.  No other slot of the cache is touched.  No two new tokens may have the same place. */
+ * skipped.  No other slot of the cache is touched.  No two new tokens may have the same place, nor
+ * two pages, heads or slots of the cache (checked: each stride passes over what the smaller ones
+ * span).  A cache that is only read may be expanded along pages or heads. */
 sp_status sp_cache_write(const sp_cache* cache, const sp_batch* batch, const sp_rows* k_new, const sp_rows* v_new,
                          void* ws, size_t ws_bytes, void* stream);
 

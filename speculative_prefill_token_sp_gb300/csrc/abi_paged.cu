@@ -314,6 +314,11 @@ sp_status sp_cache_write(const sp_cache* cache, const sp_batch* batch, const sp_
     const char* fn = "sp_cache_write";
     sp_status s;
     if ((s = check_cache(fn, cache)) != SP_OK || (s = check_batch_args(fn, batch)) != SP_OK) return s;
+    Axis axis[3] = {{cache->pages, cache->stride_page}, {cache->H_kv, cache->stride_head}, {cache->page, cache->stride_slot}};
+    if (!apart(axis, cache->d)) {
+        set_error("%s: pages, heads or slots of the cache overlap", fn);
+        return SP_EINVAL;
+    }
     if ((s = check_rows(fn, "k_new", k_new, cache->dtype, batch->T)) != SP_OK ||
         (s = check_rows(fn, "v_new", v_new, cache->dtype, batch->T)) != SP_OK)
         return s;

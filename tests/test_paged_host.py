@@ -271,3 +271,27 @@ def test_rows_apart_are_taken(sp, over):
     c, b, r = cache_of(sp), batch_of(sp), rows_of(sp, **over)
     assert sp.sp_attend(r, c, b, 4, 0.125, 0, r, None, 0, 0, 65536, 0, 0) == sp.SP_ENOMEM
     assert sp.sp_cache_read(c, b, r, r, 65536, 0, 0) == sp.SP_ENOMEM
+
+
+def test_a_cache_whose_places_overlap_is_not_written(sp):
+    """Two heads, pages or slots in one place: reading such a cache is fine, writing it is refused."""
+    b, r = batch_of(sp), rows_of(sp)
+    slot, head, page = 64, 16 * 64, 2 * 16 * 64
+    for over in (dict(stride_head=0), dict(stride_page=0), dict(stride_page=page - 8), dict(stride_head=head - 8),
+                 dict(stride_slot=slot, stride_head=slot), dict(stride_slot=head, stride_head=slot, stride_page=page - 8),
+                 dict(stride_page=slot, stride_head=10 * slot, stride_slot=slot),
+                 dict(kind=sp.SP_CACHE_INT8, k_scale=64, v_scale=64, stride_head=0)):
+        c = cache_of(sp, **over)
+        assert sp.sp_cache_write(c, b, r, r, 65536, 1 << 40, 0) == sp.SP_EINVAL, over
+        assert "overlap" in sp.sp_last_error()
+        assert sp.sp_cache_read(c, b, r, r, 65536, 0, 0) == sp.SP_ENOMEM, over         # an empty workspace
+        assert sp.sp_attend(r, c, b, 4, 0.125, 0, r, None, 0, 0, 65536, 0, 0) == sp.SP_ENOMEM, over
+
+
+def test_caches_of_every_order_are_written(sp):
+    """Pages, heads and slots in any order of their strides, with gaps; and a stride along an axis with one entry."""
+    b, r = batch_of(sp), rows_of(sp)
+    for over in (dict(stride_slot=64, stride_head=1024, stride_page=2048), dict(stride_slot=128, stride_head=64, stride_page=2048),
+                 dict(stride_page=64, stride_head=640, stride_slot=1280), dict(stride_slot=136, stride_head=64, stride_page=4096),
+                 dict(H_kv=1, stride_head=0, stride_page=1024), dict(pages=1, stride_page=0), dict(page=1, stride_slot=64, stride_head=64)):
+        assert sp.sp_cache_write(cache_of(sp, **over), b, r, r, 65536, 0, 0) == sp.SP_ENOMEM, over
