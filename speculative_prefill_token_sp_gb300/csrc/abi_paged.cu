@@ -120,7 +120,8 @@ enum Path {
 Path path_of(const sp_cache& c, const sp_batch& b, int H) {
     const int G = H / c.H_kv;
     if (b.T == 0) return kGeneral;          // nothing to do but the check
-    const bool step = attend_step_supported(c);
+    // (its join has a block for each sequence and KV head)
+    const bool step = attend_step_supported(c) && (int64_t)b.B * c.H_kv <= INT32_MAX;
     if (step && (int64_t)b.max_new * G <= 16) return kStep;
     if (!attend_tc_supported(c, b, G)) return kGeneral;
     return step && b.B > 1 ? kMixed : kChunks;

@@ -762,3 +762,36 @@ def test_the_strides_of_an_empty_tensor_are_not_looked_at(sp, stride):
     assert out.shape == (0, H, d) and lse.shape == (H, 0)
     q, k = sp.rotary(none, none, torch.empty(0, dtype=torch.int32, device="cuda"), sp.rotary_plan(d), q_out=none)
     assert q.shape == k.shape == (0, H, d)
+
+
+def test_more_pairs_of_sequence_and_head_than_a_grid_has_blocks(sp):
+    """65535 sequences of 40000 KV heads, two of which have a new token each."""
+    import torch
+    B, H, d = 65535, 40000, 64
+    assert B * H > 2 ** 31
+    rng = np.random.default_rng(31)
+    cache = sp.cache_alloc(2, H, 2, d)
+    x = [torch.from_numpy(rng.standard_normal((3, H, d))).to(torch.bfloat16) for _ in range(2)]
+    i64 = lambda a: torch.tensor(a, dtype=torch.int64, device="cuda")                          # noqa: E731
+    table = torch.zeros(B, 1, dtype=torch.int32, device="cuda")
+    table[B - 1] = 1
+    fill = sp.Batch(i64([0, 1, 3]), i64([1, 2]), table[[0, B - 1]], rows=3)
+    sp.cache_write(cache, fill, x[0].cuda(), x[1].cuda(), check=True)
+    new, kv = np.zeros(B, np.int64), np.zeros(B, np.int64)
+    new[[0, -1]], kv[[0, -1]] = 1, [1, 2]
+    batch = sp.Batch(i64(np.concatenate([[0], np.cumsum(new)])), i64(kv), table, rows=2, max_new=1)
+    q = torch.from_numpy(rng.standard_normal((2, H, d))).to(torch.bfloat16)
+    out, lse = sp.attend(q.cuda(), cache, batch, check=True)
+    # the first token sees itself alone, the last one two keys: every head by itself, so the heads are the oracle's rows
+    k, v = f64(x[0]), f64(x[1])
+    assert np.array_equal(f64(out[0]), v[0])
+    logits = np.einsum("hd,khd->hk", f64(q[1]), k[1:]) / 8
+    top = np.einsum("hd,khd->hk", np.abs(f64(q[1])), np.abs(k[1:])).max(1) / 8
+    m = logits.max(1)
+    w = np.exp(logits - m[:, None])
+    z = w.sum(1)
+    w /= z[:, None]
+    ref, spread = np.einsum("hk,khd->hd", w, v[1:]), np.einsum("hk,khd->hd", w, np.abs(v[1:]))
+    ref_lse = m + np.log(z)
+    bound, lse_bound = attend_bounds("bf16", d, 2, ref, spread, top, ref_lse)
+    assert np.all(np.abs(f64(out[1]) - ref) <= bound) and np.all(np.abs(f64(lse[:, 1]) - ref_lse) <= lse_bound)
