@@ -383,7 +383,11 @@ sp_status sp_rotary(const sp_rotary_plan* plan, const int32_t* positions, int64_
  * zeros), and round x / 2^k to the nearest code, ties to even.  With a power
  * of two the division is exact, and code * scale is a bf16 value, so reading
  * a cache back rounds nothing (but an entry whose code rounds up to 2^128 reads back as infinity).  A row that holds a NaN or an infinity gets
- * the scale NaN and reads back as NaN.  The NaN codes of e4m3 (0x7f, 0xff) are never written; sp_attend
+ * the scale NaN and reads back as NaN.
+ * A cache that another program has filled may have any fp32 scales: code * scale is then rounded once to `dtype` when
+ * it is read back, and sp_attend takes it as read back in its kernel for bf16 chunks (d = 64 and 128, sequences of more
+ * than 16 query rows per KV head) and unrounded elsewhere.
+ * The NaN codes of e4m3 (0x7f, 0xff) are never written; sp_attend
  * takes them for +-480 in values. */
 typedef enum { SP_CACHE_SAME = 0, SP_CACHE_E4M3 = 1, SP_CACHE_INT8 = 2 } sp_cache_kind;
 
@@ -395,7 +399,7 @@ typedef enum { SP_CACHE_SAME = 0, SP_CACHE_E4M3 = 1, SP_CACHE_INT8 = 2 } sp_cach
 typedef struct {
     void*         k;
     void*         v;
-    float*        k_scale;     /* 8-bit kinds: [pages, H_kv, page], contiguous, powers of two or NaN; else NULL */
+    float*        k_scale;     /* 8-bit kinds: [pages, H_kv, page], contiguous (see sp_cache_kind); else NULL */
     float*        v_scale;
     int64_t       stride_page, stride_head, stride_slot;
     int64_t       pages;

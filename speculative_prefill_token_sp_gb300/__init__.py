@@ -704,7 +704,8 @@ def rotary(q, k, positions, plan, *, inverse=False, q_out=None, k_out=None, stre
 class Cache:
     """One layer's paged keys and values: k and v [pages, H_kv, page, d] (any strides with the last axis contiguous;
     the same for both), of `dtype` (bf16 or f32) or, for an 8-bit cache, float8_e4m3fn or int8 with k_scale and
-    v_scale fp32 [pages, H_kv, page].  dtype: of the rows that are written and read (default: k's)."""
+    v_scale fp32 [pages, H_kv, page].  cache_write makes the scales powers of two; those of a cache that was filled
+    elsewhere may be any.  dtype: of the rows that are written and read (default: k's)."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None, *, dtype=None):
         torch = _torch or _load_torch()

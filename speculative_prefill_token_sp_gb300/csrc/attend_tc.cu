@@ -50,6 +50,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace sp {
 namespace {
@@ -847,51 +848,67 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
 #pragma unroll
                     for (int h = 0; h < kBlocks; ++h) codes[y][h] = fetch(c.k, cur[y].at, h);
                 }
-                for (int x = sg.from; x < sg.to && ok; ++x) {
-                    const bool more = x + 1 < sg.to;
+                // Converts tiles [x, sg.to).  A power of two is its upper half, and so a bf16.  Scales that are none, of a cache that
+                // another program has filled: the product is rounded to bf16 as sp_cache_read rounds it (kAny).  Without kAny it
+                // returns at the first tile with such a scale.  Seven ragged requests take 136 us from powers of two (172 with
+                // a branch for each 16 codes), 174 (int8) and 169 us (e4m3) from others.
+                auto tiles = [&](auto kAny, int x) {
+                    for (; x < sg.to && ok; ++x) {
+                        if constexpr (!kAny) {
+                            const uint32_t all = __float_as_uint(cur[0].ks) | __float_as_uint(cur[1].ks) | __float_as_uint(cur[0].vs) |
+                                                 __float_as_uint(cur[1].vs);
+                            if (__any_sync(0xffffffffu, all & 0xffffu)) return x;
+                        }
+                        const bool more = x + 1 < sg.to;
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) next_page[y] = more ? page_of(token(x + 1, y)) : -1;
+                        for (int y = 0; y < 2; ++y) next_page[y] = more ? page_of(token(x + 1, y)) : -1;
 #pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        if (v == 1) {
+                        for (int v = 0; v < 2; ++v) {
+                            if (v == 1) {
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    if (more) nxt[y] = place(token(x + 1, y), next_page[y]);
+                                    else nxt[y].at = sub * 16;
+                                }
+                            }
+                            ok = wait_warp(smem_u32(&empty[st]), ph, abort_flag, 61);
+                            if (!ok) break;
+                            uint8_t* tile = smem + L::kRing + st * L::kTileBytes;
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
-                                if (more) nxt[y] = place(token(x + 1, y), next_page[y]);
-                                else nxt[y].at = sub * 16;
-                            }
-                        }
-                        ok = wait_warp(smem_u32(&empty[st]), ph, abort_flag, 61);
-                        if (!ok) break;
-                        uint8_t* tile = smem + L::kRing + st * L::kTileBytes;
+                                const float own = v ? cur[y].vs : cur[y].ks;
+                                const uint32_t scale = __byte_perm(__float_as_uint(own), 0, 0x3232);     // a pair of bf16
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            // as a pair of bf16: a power of two (or NaN) is its upper half
-                            const uint32_t scale = __byte_perm(__float_as_uint(v ? cur[y].vs : cur[y].ks), 0, 0x3232);
+                                for (int h = 0; h < kBlocks; ++h) {
+                                    const uint32_t w4[4] = {codes[y][h].x, codes[y][h].y, codes[y][h].z, codes[y][h].w};
+                                    uint32_t o[8];
 #pragma unroll
-                            for (int h = 0; h < kBlocks; ++h) {
-                                const uint32_t w4[4] = {codes[y][h].x, codes[y][h].y, codes[y][h].z, codes[y][h].w};
-                                uint32_t o[8];
+                                    for (int i = 0; i < 4; ++i) {
+                                        uint32_t pair[2];
+                                        pairs_of<kKind, true>(w4[i], pair[0], pair[1]);
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    uint32_t lo, hi;
-                                    pairs_of<kKind, true>(w4[i], lo, hi);
-                                    o[2 * i] = mul_bf16x2(lo, scale);
-                                    o[2 * i + 1] = mul_bf16x2(hi, scale);
+                                        for (int k = 0; k < 2; ++k)
+                                            o[2 * i + k] = kAny ? pack_bf16(__uint_as_float(pair[k] << 16) * own,
+                                                                            __uint_as_float(pair[k] & 0xffff0000u) * own)
+                                                                : mul_bf16x2(pair[k], scale);
+                                    }
+                                    codes[y][h] = v ? fetch(c.k, nxt[y].at, h) : fetch(c.v, cur[y].at, h);
+                                    uint8_t* at = tile + y * 1024 + h * (kKeys * 128);
+                                    *reinterpret_cast<uint4*>(at + dst0) = make_uint4(o[0], o[1], o[2], o[3]);
+                                    *reinterpret_cast<uint4*>(at + dst1) = make_uint4(o[4], o[5], o[6], o[7]);
                                 }
-                                codes[y][h] = v ? fetch(c.k, nxt[y].at, h) : fetch(c.v, cur[y].at, h);
-                                uint8_t* at = tile + y * 1024 + h * (kKeys * 128);
-                                *reinterpret_cast<uint4*>(at + dst0) = make_uint4(o[0], o[1], o[2], o[3]);
-                                *reinterpret_cast<uint4*>(at + dst1) = make_uint4(o[4], o[5], o[6], o[7]);
                             }
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(&full[st]));
+                            if (++st == NS) st = 0, ph ^= 1;
                         }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&full[st]));
-                        if (++st == NS) st = 0, ph ^= 1;
+                        cur[0] = nxt[0];
+                        cur[1] = nxt[1];
                     }
-                    cur[0] = nxt[0];
-                    cur[1] = nxt[1];
-                }
+                    return x;
+                };
+                tiles(std::true_type{}, tiles(std::false_type{}, sg.from));
             }
         }
       }

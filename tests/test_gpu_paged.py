@@ -795,3 +795,44 @@ def test_more_pairs_of_sequence_and_head_than_a_grid_has_blocks(sp):
     ref_lse = m + np.log(z)
     bound, lse_bound = attend_bounds("bf16", d, 2, ref, spread, top, ref_lse)
     assert np.all(np.abs(f64(out[1]) - ref) <= bound) and np.all(np.abs(f64(lse[:, 1]) - ref_lse) <= lse_bound)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("factor", ["any", "some", 1 + (2 ** 16 - 1) * 2.0 ** -23, 1.5, -1.25])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (40, "bf16"), (64, "f32")])
+def test_scales_of_another_cache_that_are_no_powers_of_two(sp, kind, factor, d, dtype):
+    """A cache that another program has filled, with scales of largest magnitude / 127 for instance."""
+    import torch
+    rng = np.random.default_rng(32)
+    td = torch_dtype(dtype)
+    H, H_kv, page = 4, 2, 16
+    new, kv = [1, 150, 6], [300, 400, 6]
+    cache, table, _, _ = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=kv, dtype=td, kind=kind)
+    rows = []
+    for codes, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        times = 1 + rng.integers(0, 1 << 23, tuple(scale.shape)) * 2.0 ** -23 if factor in ("any", "some") else factor
+        if factor == "some":        # one slot of the long sequences
+            rest = times != 1
+            rest[table[0, 7], :, 3] = rest[table[1, 9], 0, 15] = False
+            times[rest] = 1
+        scale.copy_(torch.from_numpy(scale.double().cpu().numpy() * times))
+        rows.append(f64(codes.float()) * f64(scale)[..., None])
+    sequence = lambda x, b: np.stack([x[table[b, i // page], :, i % page] for i in range(kv[b])], 1)       # noqa: E731
+    whole, cu = make_batch(sp, kv, kv, table)
+    read = sp.cache_read(cache, whole, check=True)
+    batch, at = make_batch(sp, new, kv, table, max_new=max(new))
+    q = torch.from_numpy(rng.standard_normal((sum(new), H, d))).to(td)
+    out, lse = sp.attend(q.cuda(), cache, batch, check=True)
+    for b in range(len(kv)):
+        held = [sequence(x, b) for x in rows]
+        got = [f64(x[:, cu[b]:cu[b + 1]]) for x in read]
+        for x, y in zip(held, got):
+            # rounded once to the type; as a product in fp32 first, whose own half step moves a rounding by 2^-24 at most
+            assert np.all(np.abs(y - x) <= ((2.0 ** -8 if dtype == "bf16" else 0) + 2.0 ** -24) * np.abs(x))
+        # chunks attend the rows as they are read back, the other kernels as they are held
+        if d in (64, 128) and dtype == "bf16" and new[b] * H // H_kv > 16:
+            held = got
+        ref, ref_lse, top, spread = oracle.paged.attend(f64(q[at[b]:at[b + 1]]), *held, d ** -0.5)
+        bound, lse_bound = attend_bounds(dtype, d, kv[b], ref, spread, top, ref_lse)
+        assert np.all(np.abs(f64(out[at[b]:at[b + 1]]) - ref) <= bound)
+        assert np.all(np.abs(f64(lse[:, at[b]:at[b + 1]]) - ref_lse) <= lse_bound)
