@@ -387,8 +387,8 @@ sp_status sp_rotary(const sp_rotary_plan* plan, const int32_t* positions, int64_
  * A cache that another program has filled may have any fp32 scales: code * scale is then rounded once to `dtype` when
  * it is read back, and sp_attend takes it as read back in its kernel for bf16 chunks (d = 64 and 128, sequences of more
  * than 16 query rows per KV head) and unrounded elsewhere.
- * The NaN codes of e4m3 (0x7f, 0xff) are never written; sp_attend
- * takes them for +-480 in values. */
+ * The NaN codes of e4m3 (0x7f, 0xff) are never written, and a cache must not hold them: sp_cache_read makes NaN of
+ * them, and sp_attend NaN or +-480, as the kernel that the call takes has it.  (A row that is to be NaN has the scale NaN.) */
 typedef enum { SP_CACHE_SAME = 0, SP_CACHE_E4M3 = 1, SP_CACHE_INT8 = 2 } sp_cache_kind;
 
 /* One layer's keys and values in pages of `page` tokens: the row of (page p,
