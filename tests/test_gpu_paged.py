@@ -836,3 +836,103 @@ def test_scales_of_another_cache_that_are_no_powers_of_two(sp, kind, factor, d, 
         bound, lse_bound = attend_bounds(dtype, d, kv[b], ref, spread, top, ref_lse)
         assert np.all(np.abs(f64(out[at[b]:at[b + 1]]) - ref) <= bound)
         assert np.all(np.abs(f64(lse[:, at[b]:at[b + 1]]) - ref_lse) <= lse_bound)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (40, "bf16"), (64, "f32")])
+@pytest.mark.parametrize("n", [1, 6, 150])
+def test_the_smallest_codes_in_attention(sp, kind, d, dtype, n):
+    """Caches that hold nothing but e4m3's subnormal codes, -7 to 7 times 2^-9, or int8's -7 to 7: keys, values, or both."""
+    import torch
+    rng = np.random.default_rng(33)
+    td = torch_dtype(dtype)
+    H, H_kv, page, kv = 4, 2, 16, 300
+    for small in ("k", "v", "kv"):
+        cache, table, kval, vval = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=[kv], dtype=td, kind=kind)
+        held = [kval[0], vval[0]]
+        for i, (name, codes, scale) in enumerate((("k", cache.k, cache.k_scale), ("v", cache.v, cache.v_scale))):
+            if name not in small:
+                continue
+            c = rng.integers(-7, 8, tuple(codes.shape))
+            bits = np.where(c < 0, 128 - c, c) if kind == "e4m3" else c & 255       # sign and magnitude, or two's complement
+            codes.view(torch.uint8).copy_(torch.from_numpy(bits.astype(np.uint8)))
+            size = 2.0 ** 7 if kind == "e4m3" else 2.0 ** -2        # values up to 7 / 4
+            scale.fill_(size)
+            x = c * (2.0 ** -9 if kind == "e4m3" else 1.0) * size
+            held[i] = np.stack([x[table[0, t // page], :, t % page] for t in range(kv)], 1)
+        batch, _ = make_batch(sp, [n], [kv], table)
+        q = torch.from_numpy(rng.standard_normal((n, H, d))).to(td)
+        out, lse = sp.attend(q.cuda(), cache, batch, check=True)
+        ref, ref_lse, top, spread = oracle.paged.attend(f64(q), *held, d ** -0.5)
+        bound, lse_bound = attend_bounds(dtype, d, kv, ref, spread, top, ref_lse)
+        assert np.all(np.abs(f64(out) - ref) <= bound) and np.all(np.abs(f64(lse) - ref_lse) <= lse_bound), small
+
+
+@pytest.mark.parametrize("kind", ["same", "e4m3", "int8"])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (40, "bf16"), (64, "f32")])
+@pytest.mark.parametrize("new", [[1, 140, 2], [140, 1, 150], [1, 2, 1], [150, 130, 140]])
+@pytest.mark.parametrize("bad", [0, 1, 2])
+def test_a_bad_page_of_any_sequence_harms_no_other(sp, kind, d, dtype, new, bad):
+    """Steps and chunks in one batch, over every kind of cache; the sequence with the bad page among them."""
+    import torch
+    rng = np.random.default_rng(34)
+    td = torch_dtype(dtype)
+    H, H_kv, page = 4, 2, 16
+    kv = [n + 60 for n in new]
+    cache, table, kval, vval = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=kv, dtype=td, kind=kind, junk=float("nan"))
+    T = sum(new)
+    q = torch.from_numpy(rng.standard_normal((T, H, d))).to(td).cuda()
+    x = torch.from_numpy(rng.standard_normal((T, H_kv, d))).to(td).cuda()
+    wrong = table.copy()
+    wrong[bad, 1] = 0                           # (make_batch takes negative entries for unused ones)
+    batch, cu = make_batch(sp, new, kv, wrong, max_new=max(new))
+    batch.table[bad, 1] = (cache.pages, -1, 0x7fffffff)[bad]
+    out = torch.full((T, H, d), 7.0, dtype=td, device="cuda")
+    lse = torch.full((H, T), 7.0, device="cuda")
+    ws = torch.empty(sp.attend_workspace_size(q, cache, batch), dtype=torch.uint8, device="cuda")
+    sp.attend(q, cache, batch, out=out, lse=lse, ws=ws)
+    assert sp.sp_workspace_status(ws) == sp.SP_EDEVICE
+    for b in range(3):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        k, v = kval[b].copy(), vval[b].copy()
+        sides = [(k, v)]
+        if b == bad:                            # its page's tokens count as zeros, or not at all
+            k[:, page:2 * page] = v[:, page:2 * page] = 0
+            there = np.arange(kv[b]) // page != 1
+            sides.append((k[:, there], v[:, there]))
+        fits = []
+        for k, v in sides:
+            ref, ref_lse, top, spread = oracle.paged.attend(f64(q[rows]), k, v, d ** -0.5)
+            bound, lse_bound = attend_bounds(dtype, d, kv[b], ref, spread, top, ref_lse)
+            fits.append(np.all(np.abs(f64(out[rows]) - ref) <= bound) and np.all(np.abs(f64(lse[:, rows]) - ref_lse) <= lse_bound))
+        assert any(fits), b
+    # the bad page among the tokens that are written and read back
+    last = (kv[bad] - 1) // page
+    wrong = table.copy()
+    wrong[bad, last] = 0x7ffffff0
+    batch, cu = make_batch(sp, new, kv, wrong, max_new=max(new))
+    sides = [(cache.k, cache.k_scale), (cache.v, cache.v_scale)]
+    raw = lambda t: t.contiguous().view(torch.uint8 if kind != "same" else t.dtype).cpu().clone()         # noqa: E731
+    old = [(raw(t), None if s is None else s.cpu().clone()) for t, s in sides]
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    sp.cache_write(cache, batch, x, -x, ws=ws)
+    assert sp.sp_workspace_status(ws) == sp.SP_EDEVICE
+    touched = torch.zeros(cache.k.shape[:3], dtype=torch.bool)
+    places = oracle.paged.places(cu, kv)
+    for b, i in places:
+        if wrong[b, i // page] < cache.pages:
+            touched[wrong[b, i // page], :, i % page] = True
+    for (t, s), (was, was_scale) in zip(sides, old):
+        assert np.array_equal(f64(raw(t)[~touched]), f64(was[~touched]), equal_nan=True)
+        if s is not None:
+            assert np.array_equal(f64(s.cpu()[~touched]), f64(was_scale[~touched]), equal_nan=True)
+    k, v = sp.cache_read(cache, batch, ws=ws)
+    assert sp.sp_workspace_status(ws) == sp.SP_EDEVICE
+    for r, (b, i) in enumerate(places):
+        row = f64(x[r])
+        if wrong[b, i // page] >= cache.pages:
+            row = row * 0
+        elif kind != "same":
+            codes, scale = oracle.paged.quantise(row, kind)
+            row = f64(torch.from_numpy(codes * scale[:, None]).to(td))
+        assert np.array_equal(f64(k[:, r]), row) and np.array_equal(f64(v[:, r]), -row)
