@@ -116,8 +116,9 @@ sp_status launch(const sp_rotary_plan& plan, RotArgs<kPairs> a, cudaStream_t st)
     a.tokens = 2;
     const int64_t blocks = (a.T + a.tokens - 1) / a.tokens;
     const int per = (a.H + a.Hk) * (rot / 16 + (a.d - rot) / 8) * a.tokens;
-    // few tokens: several blocks share a token's heads
-    const int split = blocks >= 608 ? 1 : (int)std::min<int64_t>((per + kRotThreads - 1) / kRotThreads, (608 + blocks - 1) / blocks);
+    // few tokens: several blocks share a token's heads, so that an SM has four
+    const int64_t want = 4 * sm_count();
+    const int split = blocks >= want ? 1 : (int)std::min<int64_t>((per + kRotThreads - 1) / kRotThreads, (want + blocks - 1) / blocks);
     const size_t smem = (size_t)a.tokens * (rot / 2) * sizeof(float2);
     const dim3 grid((unsigned)blocks, (unsigned)std::max(1, split));
     if (plan.interleaved) rotary_kernel<T, true, kPairs><<<grid, kRotThreads, smem, st>>>(a);
