@@ -485,7 +485,11 @@ size_t sp_attend_workspace_size(const sp_cache* cache, const sp_batch* batch, in
  * that are not a token of the batch.  A NaN or an infinity in a key or value of a token that
  * some rows of the sequence see may reach its other rows as well.
  * Statistics and sums are fp32; bf16 softmax weights are rounded to bf16 for
- * the product with the values. */
+ * the product with the values.
+ * The tensor cores are used for bf16 with d = 64 or 128, where no sequence has more than 16 query rows per KV head or the cache's
+ * pages are a multiple of 8 tokens (any page for the 8-bit kinds, 16-byte aligned with such strides), H / H_kv is at most 128 and
+ * B at most 16384.  All else is right, but runs on the
+ * CUDA cores: a chunk of 256 over 4096 takes 30 us at d = 128 and 2.1 ms at d = 96. */
 sp_status sp_attend(const sp_rows* q, const sp_cache* cache, const sp_batch* batch, int H, double scale,
                     int64_t window, const sp_rows* out, float* lse, int64_t lse_stride_row,
                     int64_t lse_stride_head, void* ws, size_t ws_bytes, void* stream);

@@ -32,10 +32,14 @@
 // every SM busy to the end; a pair that is cut leaves partial sums in the
 // workspace, and a second kernel, launched early, joins them in a fixed order.
 //
+// The weights are rounded to bf16 (2^-8 of each; z sums them unrounded), the operand type of the second product.
+//
 // In a graph, one token each of 16 requests of 2K to 32K (bf16, 16 query heads on 4 of
-// 64) takes 49.5 us (5.3 TB/s), one over 131072 (e4m3, 32 on 8 of 128) 57 us (4.9 TB/s).
-// Bound by memory but for some 10 us of start, first loads and join, the 8-bit
-// kinds also by the integer pipe (56% busy).  The second
+// 64) takes 49.5 us (5.3 TB/s), one over 131072 (e4m3, 32 on 8 of 128) 56.5 us (4.9 TB/s).  One
+// over 131072, 262144, 524288 and 1048576 takes 56, 102, 193, 366 us (e4m3) and 92, 173, 333,
+// 656 us (bf16): 6.25 and 6.66 TB/s along the length, 92 and 98% of the copy rate, and 12 us
+// that do not grow with it, nearly all of them in this kernel (start, first loads, the last units).
+// The integer pipe is 56% busy with the 8-bit kinds.  The e4m3
 // case with operands loaded from global memory into registers 117 us, then with the rings 83 us.
 #include "attend_split.cuh"
 
