@@ -936,3 +936,34 @@ def test_a_bad_page_of_any_sequence_harms_no_other(sp, kind, d, dtype, new, bad)
             codes, scale = oracle.paged.quantise(row, kind)
             row = f64(torch.from_numpy(codes * scale[:, None]).to(td))
         assert np.array_equal(f64(k[:, r]), row) and np.array_equal(f64(v[:, r]), -row)
+
+
+@pytest.mark.parametrize("kind", ["same", "e4m3", "int8"])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (40, "bf16"), (64, "f32")])
+@pytest.mark.parametrize("n,kv,at", [(1, 300, 5), (6, 300, 297), (150, 700, 620), (150, 5000, 4990), (40, 3000, 100)])
+def test_a_key_that_is_nan_reaches_the_rows_that_see_it(sp, kind, d, dtype, n, kv, at):
+    """And no others: neither the tokens before it nor another sequence."""
+    import torch
+    rng = np.random.default_rng(35)
+    td = torch_dtype(dtype)
+    H, H_kv, page = 4, 2, 16
+    new, lens = [n, 2], [kv, 90]
+    cache, table, kval, vval = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=lens, dtype=td, kind=kind)
+    one, _ = make_batch(sp, [1], [at + 1], table[:1])
+    x = torch.from_numpy(rng.standard_normal((1, H_kv, d))).to(td)
+    x[:, :, d // 3] = float("nan")
+    v = torch.from_numpy(vval[0][:, at][None]).to(td)           # what is there already
+    sp.cache_write(cache, one, x.cuda(), v.cuda(), check=True)
+    batch, cu = make_batch(sp, new, lens, table, max_new=max(new))
+    q = torch.from_numpy(rng.standard_normal((n + 2, H, d))).to(td)
+    out, lse = (f64(t) for t in sp.attend(q.cuda(), cache, batch, check=True))
+    sees = np.arange(kv - n, kv) >= at
+    assert np.all(np.isnan(out[:n][sees])) and np.all(np.isnan(lse[:, :n][:, sees]))
+    for b, rows in ((0, np.flatnonzero(~sees)), (1, np.arange(n, n + 2))):
+        if len(rows) == 0:
+            continue
+        # the rows before the NaN are the last ones of a sequence that ends there
+        end = lens[1] if b else at
+        ref, ref_lse, top, spread = oracle.paged.attend(f64(q[rows]), kval[b][:, :end], vval[b][:, :end], d ** -0.5)
+        bound, lse_bound = attend_bounds(dtype, d, end, ref, spread, top, ref_lse)
+        assert np.all(np.abs(out[rows] - ref) <= bound) and np.all(np.abs(lse[:, rows] - ref_lse) <= lse_bound)
