@@ -967,3 +967,28 @@ def test_a_key_that_is_nan_reaches_the_rows_that_see_it(sp, kind, d, dtype, n, k
         ref, ref_lse, top, spread = oracle.paged.attend(f64(q[rows]), kval[b][:, :end], vval[b][:, :end], d ** -0.5)
         bound, lse_bound = attend_bounds(dtype, d, end, ref, spread, top, ref_lse)
         assert np.all(np.abs(out[rows] - ref) <= bound) and np.all(np.abs(lse[:, rows] - ref_lse) <= lse_bound)
+
+
+def test_scoring_steps_and_chunks_on_streams_of_their_own(sp):
+    """A mixed batch, a decode step, a single-precision call and a scoring call, each again and again beside the others."""
+    import torch
+    rng = np.random.default_rng(36)
+    dev = lambda *s, t=torch.bfloat16: torch.from_numpy(rng.standard_normal(s)).to(t).cuda()            # noqa: E731
+    calls = []
+    for new, kv, dtype, kind in (([1, 200, 3], [3000, 2500, 700], "bf16", "e4m3"), ([1] * 5, [9000, 20, 4000, 1, 600], "bf16", "same"),
+                                 ([2, 30], [900, 1000], "f32", "int8")):
+        cache, table, _, _ = make_cache(sp, rng, H_kv=2, d=64, page=16, kv=kv, dtype=torch_dtype(dtype), kind=kind)
+        batch, _ = make_batch(sp, new, kv, table, max_new=max(new))
+        q = dev(sum(new), 8, 64, t=torch_dtype(dtype))
+        calls.append(lambda s=None, q=q, c=cache, b=batch: sp.attend(q, c, b, stream=s))
+    Q, K, K_la = dev(8, 2, 32, 128), dev(2, 8, 8192, 128), dev(2, 8, 8, 128)
+    ws = torch.empty(sp.sp_score_workspace_size(2, 32, 8, 128, 8192, 8, sp.SP_BF16), dtype=torch.uint8, device="cuda")
+    calls.append(lambda s=None: (sp.score(Q, K, K_la, ws=ws, stream=s),))
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[call(s) for call, s in zip(calls, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for one in got:
+        for mine, right in zip(one, want):
+            assert all(torch.equal(a, b) for a, b in zip(mine, right))
