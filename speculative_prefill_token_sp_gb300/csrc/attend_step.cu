@@ -35,7 +35,7 @@
 // The weights are rounded to bf16 (2^-8 of each; z sums them unrounded), the operand type of the second product.
 //
 // In a graph, one token each of 16 requests of 2K to 32K (bf16, 16 query heads on 4 of
-// 64) takes 49.5 us (5.3 TB/s), one over 131072 (e4m3, 32 on 8 of 128) 56.5 us (4.9 TB/s).  One
+// 64) takes 49.5 us (5.3 TB/s), one over 131072 (e4m3, 32 on 8 of 128) 56.5 to 57.8 us (4.8 TB/s).  One
 // over 131072, 262144, 524288 and 1048576 takes 56, 102, 193, 366 us (e4m3) and 92, 173, 333,
 // 656 us (bf16): 6.25 and 6.66 TB/s along the length, 92 and 98% of the copy rate, and 12 us
 // that do not grow with it, nearly all of them in this kernel (start, first loads, the last units).
