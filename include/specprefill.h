@@ -495,6 +495,120 @@ sp_status sp_attend(const sp_rows* q, const sp_cache* cache, const sp_batch* bat
                     int64_t lse_stride_head, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Trees of drafted tokens                                                  */
+/* ------------------------------------------------------------------------ */
+
+/* The new tokens of a batch's sequences may be drafted ones that form a tree: parent[r] says on which new token of its own
+ * sequence row r hangs, counted from the sequence's first (so parent[r] < its own number), or -1 for a root, which hangs on
+ * the cached tokens.  A round: sp_tree_seen, sp_rotary at its positions, sp_cache_write, sp_attend_tree in each layer, then
+ * sp_tree_accept and sp_cache_keep (drafted != 0) in each layer. */
+
+/* Workspace bytes of sp_tree_seen and sp_tree_accept (they keep their status there). */
+size_t sp_tree_workspace_size(void);
+
+/* From the parents, what sp_attend_tree and sp_rotary take.
+ *
+ *   parent     device int32 [T]
+ *   seen       device, or NULL: bit u % 32 of word seen[r * seen_stride + u / 32] is set if row r is new token u of its
+ *              sequence or hangs on it, directly or over others.  All seen_words words are written; 32 * seen_words >= max_new
+ *   positions  device int32 [T], or NULL: kv_len - (new tokens) + the number of tokens that row r hangs on
+ *
+ * Rows that are not a token of the batch are not written.  The batch's table is not read.  A parent that is not a token before
+ * its row counts as -1, and SP_EDEVICE is recorded in the workspace. */
+sp_status sp_tree_seen(const sp_batch* batch, const int32_t* parent, uint32_t* seen, int64_t seen_stride, int seen_words,
+                       int32_t* positions, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of sp_attend_tree (0 if the arguments are invalid). */
+size_t sp_attend_tree_workspace_size(const sp_cache* cache, const sp_batch* batch, int H);
+
+/* sp_attend where a row sees the cached tokens before the new ones, and of the new ones those whose bits are set (as
+ * sp_tree_seen lays them out; any bits will do, also none, or such of later tokens; bits of tokens that the sequence does not
+ * have are ignored).  A row's place, which a window > 0 goes by, is kv_len - (new tokens) + max(bits set, 1) - 1; the window
+ * hides tokens before the new ones only.  A row that sees nothing gets out = 0 and lse = -inf.
+ * All else as sp_attend: types, layouts, kernels and their speed. */
+sp_status sp_attend_tree(const sp_rows* q, const sp_cache* cache, const sp_batch* batch, int H, double scale,
+                         int64_t window, const uint32_t* seen, int64_t seen_stride, int seen_words, const sp_rows* out,
+                         float* lse, int64_t lse_stride_row, int64_t lse_stride_head, void* ws, size_t ws_bytes, void* stream);
+
+/* The drafted tokens that the target agrees with, by its choice after each of them (draft and target device int32 [T]:
+ * the token that row r is, and the one that the target chooses after it).  The first new token of a sequence is accepted (it
+ * is the target's own choice of the round before); after an accepted token r its first child c with draft[c] == target[r] is.
+ *
+ *   path    device int32: path[b * path_stride + i] is the i-th accepted new token of sequence b, ascending, counted from the
+ *           sequence's first; -1 behind the last one, up to max_new
+ *   n_path  device int64 [B]: how many (0 for a sequence without new tokens)
+ *   next    device int32 [B] or NULL: the target's choice after the last accepted token (-1 without one)
+ *
+ * Parents as for sp_tree_seen.  path and n_path are what sp_cache_keep takes with drafted != 0 and heads = 1. */
+sp_status sp_tree_accept(const sp_batch* batch, const int32_t* parent, const int32_t* draft, const int32_t* target, int32_t* path,
+                         int64_t path_stride, int64_t* n_path, int32_t* next, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Cutting a cache                                                          */
+/* ------------------------------------------------------------------------ */
+
+/* Workspace bytes of sp_attend_weights for this cache, batch and number of query heads on the current device (0 if they
+ * are invalid).  Does not depend on the contents of the batch's device arrays. */
+size_t sp_attend_weights_workspace_size(const sp_cache* cache, const sp_batch* batch, int H);
+
+/* Adds the attention weights that the new tokens' queries give their sequences' cached tokens to what these have gathered:
+ *
+ *   weights[i, g] = decay * weights[i, g] + sum over rows r that see i, heads h of KV head g of exp(scale * q[r, h] . k_i - lse[r, h])
+ *
+ * for token i of the sequence and KV head g, with the new tokens, visibility (causal, window) and lse of sp_attend.  A new
+ * token's weight starts from 0; with decay = 0 every token's does, and what was there is not read.  Weights of tokens that
+ * no row sees (outside every row's window, or of a sequence without new tokens) are not touched.  A row whose lse is -inf saw
+ * nothing and adds nothing.
+ *
+ *   q        [T, H, d]   lse  fp32, lse[r * lse_stride_row + h * lse_stride_head], as sp_attend writes it
+ *   weights  device fp32 [pages, H_kv, page], contiguous: of the token in slot s of page p, KV head g
+ *
+ * Requirements as sp_attend; 0 <= decay <= 1.  A token whose page index is out of range is left out, and SP_EDEVICE recorded.
+ * No two tokens of the batch may have the same place.  Sums are fp32 in a fixed order: the same call gives the same bits. */
+sp_status sp_attend_weights(const sp_rows* q, const sp_cache* cache, const sp_batch* batch, int H, double scale, int64_t window,
+                            const float* lse, int64_t lse_stride_row, int64_t lse_stride_head, double decay, float* weights,
+                            void* ws, size_t ws_bytes, void* stream);
+
+/* Which of its tokens each sequence keeps: all if it has at most `budget`, else the first `first`, the last `last`, and of those
+ * between the budget - first - last with the largest weights, ties to the lower token.  -0 equals 0, and NaN ranks below all
+ * else.  The batch's kv_len and table say where the tokens are; its new tokens count like the others.
+ *
+ *   shared  0: a list for every KV head, by its own weights; otherwise one list a sequence, by the maximum over the KV heads
+ *   kept    device int32: kept[b * kept_stride_seq + g * kept_stride_head + i] is the i-th kept token of sequence b and KV head
+ *           g (0 if shared), ascending; -1 behind the last one, up to `budget`
+ *   n_kept  device int64 [B]: min(kv_len[b], budget)
+ *
+ * 0 <= first + last <= budget <= 2^30.  Workspace: sp_cache_workspace_size().  A sequence whose lengths are impossible keeps
+ * nothing (n_kept 0); a token whose page index is out of range ranks lowest; either records SP_EDEVICE. */
+sp_status sp_cache_choose(const sp_cache* cache, const sp_batch* batch, const float* weights, int shared, int64_t budget,
+                          int64_t first, int64_t last, int32_t* kept, int64_t kept_stride_seq, int64_t kept_stride_head,
+                          int64_t* n_kept, void* ws, size_t ws_bytes, void* stream);
+
+/* Keeps the listed tokens of each sequence and drops the others: the i-th listed token's keys, values, scales and (unless
+ * NULL) weights become those of token i, and kv_out[b] = n_kept[b].  The lists are ascending.  They are sp_cache_choose's, the
+ * kept positions of a prompt that sp_select has cut, or any others.  With drafted != 0 they count from the sequence's first new
+ * token, as sp_tree_accept's do, the i-th becomes new token i, and kv_out[b] = kv_len[b] - (new tokens) + n_kept[b]:
+ * the tokens before the new ones stay.
+ *
+ *   kept    device int32, kept[b * kept_stride_seq + g * kept_stride_head + i]; heads = H_kv lists a sequence, or 1 for all heads
+ *   n_kept  device int64 [B], each at most `most`
+ *   to      NULL: the rows move within the sequence's own pages, whose last ones fall free.  Otherwise device int32
+ *           [B, to_width], rows to_stride apart: new token i is in slot i % page of page to[b * to_stride + i / page], and
+ *           what was there before stays as it was.  No page of `to` may be one that holds a listed token of the batch
+ *   weights [pages, H_kv, page], as sp_attend_weights gathers them, or NULL
+ *   kv_out  device int64 [B], not the batch's kv_len itself
+ *
+ * Keys keep the positions that they were rotated at, so attention over the kept tokens is what it was without the others; a
+ * window counts kept tokens.  Nothing is quantised again.  Slots from kv_out on hold what they held.  Workspace:
+ * sp_cache_workspace_size().  SP_EDEVICE is recorded, and the sequence is left as it was with kv_out[b] = kv_len[b], where
+ * lengths or counts are impossible (also a `to` too narrow for them); an entry that is out of range is passed over, and one that
+ * is not above the entry before it is recorded as well (the sequence's rows are then not determined).  No two sequences may
+ * have a page in common that either has rows moved in. */
+sp_status sp_cache_keep(const sp_cache* cache, const sp_batch* batch, const int32_t* kept, int heads, int64_t kept_stride_seq,
+                        int64_t kept_stride_head, const int64_t* n_kept, int64_t most, int drafted, const int32_t* to, int to_width,
+                        int64_t to_stride, float* weights, int64_t* kv_out, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Status                                                                   */
 /* ------------------------------------------------------------------------ */
 

@@ -41,3 +41,4 @@ from .select import (  # noqa: F401
 )
 from .gather import gather_kept  # noqa: F401,E402
 from . import paged  # noqa: F401,E402
+from . import kept  # noqa: F401,E402

@@ -31,6 +31,10 @@ __all__ = [
     "sp_attend_workspace_size", "sp_attend",
     "rotary_plan", "rotary", "Cache", "Batch", "cache_alloc", "cache_write", "cache_read", "attend_workspace_size",
     "attend",
+    "sp_tree_workspace_size", "sp_tree_seen", "sp_attend_tree_workspace_size", "sp_attend_tree", "sp_tree_accept",
+    "sp_attend_weights_workspace_size", "sp_attend_weights", "sp_cache_choose", "sp_cache_keep",
+    "tree_seen", "attend_tree_workspace_size", "attend_tree", "tree_accept", "weights_alloc", "attend_weights_workspace_size",
+    "attend_weights", "cache_choose", "cache_keep",
 ]
 
 SP_OK, SP_EINVAL, SP_ENOMEM, SP_ECUDA, SP_EDEVICE, SP_ETIMEOUT, SP_EUNSUPPORTED = range(7)
@@ -125,6 +129,15 @@ _SIGS = {
     "sp_cache_read": (_i32, [_vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "sp_attend_workspace_size": (_sz, [_vp, _vp, _i32]),
     "sp_attend": (_i32, [_vp, _vp, _vp, _i32, _dbl, _i64, _vp, _vp, _i64, _i64, _vp, _sz, _vp]),
+    "sp_tree_workspace_size": (_sz, []),
+    "sp_tree_seen": (_i32, [_vp, _vp, _vp, _i64, _i32, _vp, _vp, _sz, _vp]),
+    "sp_attend_tree_workspace_size": (_sz, [_vp, _vp, _i32]),
+    "sp_attend_tree": (_i32, [_vp, _vp, _vp, _i32, _dbl, _i64, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _vp, _sz, _vp]),
+    "sp_tree_accept": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "sp_attend_weights_workspace_size": (_sz, [_vp, _vp, _i32]),
+    "sp_attend_weights": (_i32, [_vp, _vp, _vp, _i32, _dbl, _i64, _vp, _i64, _i64, _dbl, _vp, _vp, _sz, _vp]),
+    "sp_cache_choose": (_i32, [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _sz, _vp]),
+    "sp_cache_keep": (_i32, [_vp, _vp, _vp, _i32, _i64, _i64, _vp, _i64, _i32, _vp, _i32, _i64, _vp, _vp, _vp, _sz, _vp]),
     "sp_workspace_status": (_i32, [_vp, _vp]),
     "sp_last_error": (_c.c_char_p, []),
     "sp_status_string": (_c.c_char_p, [_i32]),
@@ -337,6 +350,54 @@ def sp_attend(q, cache, batch, H, scale, window, out, lse, lse_stride_row, lse_s
               stream=None) -> int:
     return lib().sp_attend(_struct(q), _struct(cache), _struct(batch), H, scale, window, _struct(out), _ptr(lse),
                            lse_stride_row, lse_stride_head, _ptr(ws), ws_bytes, _stream(stream))
+
+
+def sp_tree_workspace_size() -> int:
+    return lib().sp_tree_workspace_size()
+
+
+def sp_tree_seen(batch, parent, seen, seen_stride, seen_words, positions, ws, ws_bytes, stream=None) -> int:
+    return lib().sp_tree_seen(_struct(batch), _ptr(parent), _ptr(seen), seen_stride, seen_words, _ptr(positions), _ptr(ws),
+                              ws_bytes, _stream(stream))
+
+
+def sp_attend_tree_workspace_size(cache, batch, H) -> int:
+    return lib().sp_attend_tree_workspace_size(_struct(cache), _struct(batch), H)
+
+
+def sp_attend_tree(q, cache, batch, H, scale, window, seen, seen_stride, seen_words, out, lse, lse_stride_row,
+                   lse_stride_head, ws, ws_bytes, stream=None) -> int:
+    return lib().sp_attend_tree(_struct(q), _struct(cache), _struct(batch), H, scale, window, _ptr(seen), seen_stride,
+                                seen_words, _struct(out), _ptr(lse), lse_stride_row, lse_stride_head, _ptr(ws), ws_bytes,
+                                _stream(stream))
+
+
+def sp_tree_accept(batch, parent, draft, target, path, path_stride, n_path, next, ws, ws_bytes, stream=None) -> int:
+    return lib().sp_tree_accept(_struct(batch), _ptr(parent), _ptr(draft), _ptr(target), _ptr(path), path_stride,
+                                _ptr(n_path), _ptr(next), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def sp_attend_weights_workspace_size(cache, batch, H) -> int:
+    return lib().sp_attend_weights_workspace_size(_struct(cache), _struct(batch), H)
+
+
+def sp_attend_weights(q, cache, batch, H, scale, window, lse, lse_stride_row, lse_stride_head, decay, weights, ws, ws_bytes,
+                      stream=None) -> int:
+    return lib().sp_attend_weights(_struct(q), _struct(cache), _struct(batch), H, scale, window, _ptr(lse), lse_stride_row,
+                                   lse_stride_head, decay, _ptr(weights), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def sp_cache_choose(cache, batch, weights, shared, budget, first, last, kept, kept_stride_seq, kept_stride_head, n_kept, ws,
+                    ws_bytes, stream=None) -> int:
+    return lib().sp_cache_choose(_struct(cache), _struct(batch), _ptr(weights), shared, budget, first, last, _ptr(kept),
+                                 kept_stride_seq, kept_stride_head, _ptr(n_kept), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def sp_cache_keep(cache, batch, kept, heads, kept_stride_seq, kept_stride_head, n_kept, most, drafted, to, to_width,
+                  to_stride, weights, kv_out, ws, ws_bytes, stream=None) -> int:
+    return lib().sp_cache_keep(_struct(cache), _struct(batch), _ptr(kept), heads, kept_stride_seq, kept_stride_head,
+                               _ptr(n_kept), most, drafted, _ptr(to), to_width, to_stride, _ptr(weights), _ptr(kv_out),
+                               _ptr(ws), ws_bytes, _stream(stream))
 
 
 def sp_workspace_status(ws, stream=None) -> int:
@@ -837,6 +898,10 @@ def attend(q, cache, batch, *, scale=None, window=0, out=None, lse=None, ws=None
     among them): (out [rows, H, d], lse fp32 [H, rows]).  scale: default 1 / sqrt(d).  window > 0: each token sees
     itself and the window - 1 tokens before it.  lse may be any strided fp32 [H, rows], such as [l, :, j:j+1] of
     score_lse's [L, H, N].  out must not overlap q.  Rows that are not a token of the batch are not written."""
+    return _attend(q, cache, batch, None, scale, window, out, lse, ws, stream, check)
+
+
+def _attend(q, cache, batch, seen, scale, window, out, lse, ws, stream, check):
     device, rows = cache.device, batch.rows
     H = q.shape[1] if q.dim() == 3 else 0
     _check_rows_of(q, "q", rows, H, cache.d, cache.dtype, device)
@@ -855,13 +920,240 @@ def attend(q, cache, batch, *, scale=None, window=0, out=None, lse=None, ws=None
         w, size = _space(sp_attend_workspace_size(cache.c, batch.c, H) if ws is None else 0, device, ws)
         zh, zr = z.stride()
         qr, outr = _rows(q), _rows(o)
-        status = lib().sp_attend(ctypes.addressof(qr), cache.at, batch.at, H,
-                                 cache.d ** -0.5 if scale is None else float(scale), int(window),
-                                 ctypes.addressof(outr), z.data_ptr(), zr, zh, w.data_ptr(), size, handle)
+        scale_ = cache.d ** -0.5 if scale is None else float(scale)
+        if seen is None:
+            status = lib().sp_attend(ctypes.addressof(qr), cache.at, batch.at, H, scale_, int(window),
+                                     ctypes.addressof(outr), z.data_ptr(), zr, zh, w.data_ptr(), size, handle)
+        else:
+            status = lib().sp_attend_tree(ctypes.addressof(qr), cache.at, batch.at, H, scale_, int(window), seen.data_ptr(),
+                                          _row_stride(seen), seen.shape[1], ctypes.addressof(outr), z.data_ptr(), zr, zh,
+                                          w.data_ptr(), size, handle)
         if status:
             _check(status)
         if check:
             _check(sp_workspace_status(w, handle))
         return o, z
+
+    return _on(device, stream, call)
+
+
+# ----------------------------------------------------------------------------
+# Trees of drafted tokens
+# ----------------------------------------------------------------------------
+
+def _check_ints(t, name, shape, device, dtype=None):
+    """An integer tensor of this shape (None: any extent) whose last axis is contiguous."""
+    dtype = dtype or _torch.int32
+    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        want = ", ".join("*" if n is None else str(n) for n in shape)
+        raise ValueError(f"{name} must be {str(dtype)[6:]} [{want}]: got {t.dtype} {list(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+
+
+def _row_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[-1]
+
+
+def tree_seen(batch, parent, *, seen=None, positions=None, ws=None, stream=None, check=False):
+    """What the batch's new tokens see if they are drafted ones that form a tree: parent int32 [rows], the new token of the
+    same sequence that each hangs on, counted from the sequence's first and before its child, or -1.  Returns (seen int32
+    [rows, words], the bits that attend_tree takes, and positions int32 [rows], which rotary takes).  Rows that are not
+    a token of the batch are not written."""
+    device, rows = batch.device, batch.rows
+    words = max(1, -(-batch.max_new // 32))
+    _check_ints(parent, "parent", (rows,), device)
+    if seen is not None:
+        _check_ints(seen, "seen", (rows, None), device)
+    if positions is not None:
+        _check_ints(positions, "positions", (rows,), device)
+
+    def call(handle):
+        s, p = seen, positions
+        if s is None:
+            s = _torch.empty(rows, words, dtype=_torch.int32, device=device)
+        if p is None:
+            p = _torch.empty(rows, dtype=_torch.int32, device=device)
+        w, size = _space(sp_tree_workspace_size() if ws is None else 0, device, ws)
+        status = lib().sp_tree_seen(batch.at, parent.data_ptr(), s.data_ptr(), _row_stride(s), s.shape[1], p.data_ptr(),
+                                    w.data_ptr(), size, handle)
+        if status:
+            _check(status)
+        if check:
+            _check(sp_workspace_status(w, handle))
+        return s, p
+
+    return _on(device, stream, call)
+
+
+def attend_tree_workspace_size(q, cache, batch):
+    """Workspace bytes of attend_tree for these arguments."""
+    return _on(cache.device, None, lambda handle: sp_attend_tree_workspace_size(cache.c, batch.c, q.shape[1]))
+
+
+def attend_tree(q, cache, batch, seen, *, scale=None, window=0, out=None, lse=None, ws=None, stream=None, check=False):
+    """Attention of drafted tokens: as attend, but of the new tokens each row sees those whose bits are set in seen int32
+    [rows, words], as tree_seen makes them (word u // 32, bit u % 32 for the sequence's new token u).  A window counts from
+    a row's place, behind the cached tokens and the new ones that it sees, and hides cached tokens only."""
+    _check_ints(seen, "seen", (batch.rows, None), cache.device)
+    return _attend(q, cache, batch, seen, scale, window, out, lse, ws, stream, check)
+
+
+def tree_accept(batch, parent, draft, target, *, path=None, n_path=None, next_token=None, ws=None, stream=None, check=False):
+    """The drafted tokens that the target agrees with.  draft and target int32 [rows]: the token that each row is, and the
+    target's choice after it.  A sequence's first new token is accepted, and after an accepted token its first child that is
+    the target's choice.  Returns (path int32 [B, max_new], the accepted ones of each sequence counted from its first, then -1;
+    n_path int64 [B]; next_token int32 [B], the target's choice after the last).  path and n_path go to cache_keep."""
+    device, rows, B = batch.device, batch.rows, batch.c.B
+    for t, name in ((parent, "parent"), (draft, "draft"), (target, "target")):
+        _check_ints(t, name, (rows,), device)
+    if path is not None:
+        _check_ints(path, "path", (B, batch.max_new), device)
+    if n_path is not None:
+        _check_ints(n_path, "n_path", (B,), device, _torch.int64)
+    if next_token is not None:
+        _check_ints(next_token, "next_token", (B,), device)
+
+    def call(handle):
+        p, n, x = path, n_path, next_token
+        if p is None:
+            p = _torch.empty(B, batch.max_new, dtype=_torch.int32, device=device)
+        if n is None:
+            n = _torch.empty(B, dtype=_torch.int64, device=device)
+        if x is None:
+            x = _torch.empty(B, dtype=_torch.int32, device=device)
+        w, size = _space(sp_tree_workspace_size() if ws is None else 0, device, ws)
+        status = lib().sp_tree_accept(batch.at, parent.data_ptr(), draft.data_ptr(), target.data_ptr(), p.data_ptr(),
+                                      _row_stride(p), n.data_ptr(), x.data_ptr(), w.data_ptr(), size, handle)
+        if status:
+            _check(status)
+        if check:
+            _check(sp_workspace_status(w, handle))
+        return p, n, x
+
+    return _on(device, stream, call)
+
+
+# ----------------------------------------------------------------------------
+# Cutting a cache
+# ----------------------------------------------------------------------------
+
+def weights_alloc(cache):
+    """Weights of a cache's tokens, fp32 [pages, H_kv, page], for attend_weights (uninitialised: a new token's starts from 0)."""
+    torch = _torch or _load_torch()
+    return torch.empty(cache.pages, cache.H_kv, cache.page, dtype=torch.float32, device=cache.device)
+
+
+def _check_weights(weights, cache):
+    if weights.shape != (cache.pages, cache.H_kv, cache.page) or weights.dtype != _torch.float32 or \
+            not weights.is_contiguous() or weights.device != cache.device:
+        raise ValueError(f"weights must be contiguous fp32 [{cache.pages}, {cache.H_kv}, {cache.page}] on {cache.device}")
+
+
+def attend_weights_workspace_size(q, cache, batch):
+    """Workspace bytes of attend_weights for these arguments."""
+    return _on(cache.device, None, lambda handle: sp_attend_weights_workspace_size(cache.c, batch.c, q.shape[1]))
+
+
+def attend_weights(q, cache, batch, lse, weights, *, scale=None, window=0, decay=1.0, ws=None, stream=None, check=False):
+    """Adds the attention weights that the batch's new tokens give their sequences' cached tokens to weights fp32 [pages, H_kv,
+    page], summed over new tokens and the query heads of a KV head: weights = decay * weights + the sum.  q, scale and window
+    as given to attend, lse fp32 [H, rows] as it returned it.  New tokens start from 0; with decay=0 all do (the weights that
+    the last tokens of a prompt give it, say).  Returns weights."""
+    device, rows = cache.device, batch.rows
+    H = q.shape[1] if q.dim() == 3 else 0
+    _check_rows_of(q, "q", rows, H, cache.d, cache.dtype, device)
+    if lse.shape != (H, rows) or lse.dtype != _torch.float32 or lse.device != device:
+        raise ValueError(f"lse must be fp32 [{H}, {rows}] on {device}")
+    _check_weights(weights, cache)
+    _same_device(device, batch)
+
+    def call(handle):
+        w, size = _space(sp_attend_weights_workspace_size(cache.c, batch.c, H) if ws is None else 0, device, ws)
+        zh, zr = lse.stride()
+        qr = _rows(q)
+        status = lib().sp_attend_weights(ctypes.addressof(qr), cache.at, batch.at, H,
+                                         cache.d ** -0.5 if scale is None else float(scale), int(window), lse.data_ptr(), zr, zh,
+                                         float(decay), weights.data_ptr(), w.data_ptr(), size, handle)
+        if status:
+            _check(status)
+        if check:
+            _check(sp_workspace_status(w, handle))
+        return weights
+
+    return _on(device, stream, call)
+
+
+def cache_choose(cache, batch, weights, budget, *, first=0, last=0, shared=False, kept=None, n_kept=None, ws=None, stream=None,
+                 check=False):
+    """Which `budget` tokens each sequence keeps: its first and last ones, and of those between the ones with the largest
+    weights (ties to the lower token); all if it has no more.  Returns (kept int32 [B, H_kv, budget], ascending and then -1, and
+    n_kept int64 [B]).  shared=True: one list for all heads, kept [B, 1, budget], by the maximum of their weights."""
+    device, B, budget = cache.device, batch.c.B, int(budget)
+    heads = 1 if shared else cache.H_kv
+    _check_weights(weights, cache)
+    _same_device(device, batch)
+    if kept is not None:
+        _check_ints(kept, "kept", (B, heads, budget), device)
+    if n_kept is not None:
+        _check_ints(n_kept, "n_kept", (B,), device, _torch.int64)
+
+    def call(handle):
+        k, n = kept, n_kept
+        if k is None:
+            k = _torch.empty(B, heads, max(budget, 0), dtype=_torch.int32, device=device)
+        if n is None:
+            n = _torch.empty(B, dtype=_torch.int64, device=device)
+        w, size = _space(cache.ws_bytes, device, ws)
+        status = lib().sp_cache_choose(cache.at, batch.at, weights.data_ptr(), 1 if shared else 0, budget, int(first), int(last),
+                                       k.data_ptr(), k.stride(0), k.stride(1), n.data_ptr(), w.data_ptr(), size, handle)
+        if status:
+            _check(status)
+        if check:
+            _check(sp_workspace_status(w, handle))
+        return k, n
+
+    return _on(device, stream, call)
+
+
+def cache_keep(cache, batch, kept, n_kept, *, drafted=False, to=None, weights=None, kv_len=None, ws=None, stream=None,
+               check=False):
+    """Keeps the listed tokens of each sequence, in order, and drops the others: kept int32 [B, most], or [B, H_kv, most] for a list
+    a head, ascending, of which n_kept int64 [B] count (cache_choose's; select's positions of one prompt as [1, M]).  Returns
+    the sequences' new lengths, int64 [B].  drafted=True: the lists count from the first new token, as tree_accept's, and the
+    tokens before stay.  to int32 [B, width]: the kept tokens go to these pages, which are none of the listed tokens' own
+    (default: to the front of their own, in place).  weights: the tokens' weights, moved along with them."""
+    device, B = cache.device, batch.c.B
+    if kept.dim() == 3:
+        _check_ints(kept, "kept", (B, None, None), device)
+        heads, most, seq, head = kept.shape[1], kept.shape[2], kept.stride(0), kept.stride(1)
+    else:
+        _check_ints(kept, "kept", (B, None), device)
+        heads, most, seq, head = 1, kept.shape[1], kept.stride(0), 0
+    _check_ints(n_kept, "n_kept", (B,), device, _torch.int64)
+    if to is not None:
+        _check_ints(to, "to", (B, None), device)
+    if weights is not None:
+        _check_weights(weights, cache)
+    if kv_len is not None:
+        _check_ints(kv_len, "kv_len", (B,), device, _torch.int64)
+    _same_device(device, batch)
+
+    def call(handle):
+        n = kv_len
+        if n is None:
+            n = _torch.empty(B, dtype=_torch.int64, device=device)
+        w, size = _space(cache.ws_bytes, device, ws)
+        status = lib().sp_cache_keep(cache.at, batch.at, kept.data_ptr(), heads, seq, head, n_kept.data_ptr(), most,
+                                     1 if drafted else 0, None if to is None else to.data_ptr(),
+                                     0 if to is None else to.shape[1], 0 if to is None else _row_stride(to),
+                                     None if weights is None else weights.data_ptr(), n.data_ptr(), w.data_ptr(), size, handle)
+        if status:
+            _check(status)
+        if check:
+            _check(sp_workspace_status(w, handle))
+        return n
 
     return _on(device, stream, call)

@@ -27,6 +27,18 @@ sp_status attend_step_launch(const AttendProblem& p, void* ws, cudaStream_t st);
 bool attend_tc_supported(const sp_cache& c, const sp_batch& b, int G);
 size_t attend_tc_ws_bytes(const sp_cache& c);
 sp_status attend_tc_launch(const AttendProblem& p, int min_rows, void* ws, size_t offset, cudaStream_t st);
+// Implemented in weights_*.cu, tree.cu and evict.cu.
+sp_status weights_general_launch(const WeightsProblem& w, void* ws, cudaStream_t st);
+sp_status tree_seen_launch(const sp_batch& b, const int32_t* parent, uint32_t* seen, int64_t stride, int words, int32_t* positions,
+                           void* ws, cudaStream_t st);
+sp_status tree_accept_launch(const sp_batch& b, const int32_t* parent, const int32_t* draft, const int32_t* target, int32_t* path,
+                             int64_t stride, int64_t* n_path, int32_t* next, void* ws, cudaStream_t st);
+sp_status cache_choose_launch(const sp_cache& c, const sp_batch& b, const float* weights, bool shared, int64_t budget, int64_t first,
+                              int64_t last, int32_t* kept, int64_t stride_seq, int64_t stride_head, int64_t* n_kept, void* ws,
+                              cudaStream_t st);
+sp_status cache_keep_launch(const sp_cache& c, const sp_batch& b, const int32_t* kept, int heads, int64_t stride_seq,
+                            int64_t stride_head, const int64_t* n_kept, int64_t most, bool drafted, const int32_t* to, int to_width,
+                            int64_t to_stride, float* weights, int64_t* kv_out, void* ws, cudaStream_t st);
 
 namespace {
 
@@ -134,6 +146,117 @@ size_t path_bytes(Path path, const sp_cache& c) {
         case kMixed: return attend_step_ws_bytes(c) + attend_tc_ws_bytes(c);
         default: return attend_general_ws_bytes(c);
     }
+}
+
+// Pages, heads and slots of a cache that is written lie apart.
+sp_status check_no_overlap(const char* fn, const sp_cache* c) {
+    Axis axis[3] = {{c->pages, c->stride_page}, {c->H_kv, c->stride_head}, {c->page, c->stride_slot}};
+    if (apart(axis, c->d)) return SP_OK;
+    set_error("%s: pages, heads or slots of the cache overlap", fn);
+    return SP_EINVAL;
+}
+
+sp_status check_heads(const char* fn, const sp_cache* c, int H) {
+    if (H >= 1 && H % c->H_kv == 0) return SP_OK;
+    set_error("%s: H (%d) must be a multiple of H_kv (%d)", fn, H, c->H_kv);
+    return SP_EINVAL;
+}
+
+sp_status check_ints(const char* fn, const char* what, const void* p) {
+    if (p && reinterpret_cast<uintptr_t>(p) % 4 == 0) return SP_OK;
+    set_error("%s: null or misaligned %s", fn, what);
+    return SP_EINVAL;
+}
+
+sp_status check_counts(const char* fn, const char* what, const void* p) {
+    if (p && reinterpret_cast<uintptr_t>(p) % 8 == 0) return SP_OK;
+    set_error("%s: null or misaligned %s", fn, what);
+    return SP_EINVAL;
+}
+
+sp_status check_weights(const char* fn, const float* w) { return check_ints(fn, "weights", w); }
+
+// A kernel has a cluster of up to 8 CTAs for each.
+sp_status check_items(const char* fn, int64_t items) {
+    if (items < (int64_t)1 << 27) return SP_OK;
+    set_error("%s: too many sequences and KV heads (%lld)", fn, (long long)items);
+    return SP_EUNSUPPORTED;
+}
+
+sp_status check_words(const char* fn, const sp_batch* b, const uint32_t* seen, int64_t stride, int words) {
+    if (b->T == 0) return SP_OK;
+    sp_status s = check_ints(fn, "seen", seen);
+    if (s != SP_OK) return s;
+    if (words < 1 || (int64_t)32 * words < b->max_new || stride < 0) {
+        set_error("%s: %d words a row do not hold %d tokens (row stride %lld)", fn, words, b->max_new, (long long)stride);
+        return SP_EINVAL;
+    }
+    return SP_OK;
+}
+
+size_t attend_bytes(const char* fn, const sp_cache* cache, const sp_batch* batch, int H) {
+    if (check_cache(fn, cache) != SP_OK || check_batch_args(fn, batch) != SP_OK || check_heads(fn, cache, H) != SP_OK) return 0;
+    return path_bytes(path_of(*cache, *batch, H), *cache);
+}
+
+// What sp_attend, sp_attend_tree and sp_attend_weights have in common: checks it and fills in the problem.
+sp_status attend_problem(const char* fn, const sp_rows* q, const sp_cache* cache, const sp_batch* batch, int H, double scale,
+                         int64_t window, AttendProblem* out) {
+    sp_status s;
+    if ((s = check_cache(fn, cache)) != SP_OK || (s = check_batch_args(fn, batch)) != SP_OK || (s = check_heads(fn, cache, H)) != SP_OK)
+        return s;
+    const float factor = (float)scale * 1.4426950408889634f;        // the kernels': logits to base 2
+    if (!(factor >= FLT_MIN) || !isfinite(factor)) {
+        set_error("%s: scale must be positive, and a normal fp32 number times log2(e) (got %g)", fn, scale);
+        return SP_EINVAL;
+    }
+    if (window < 0) {
+        set_error("%s: window must be >= 0 (got %lld)", fn, (long long)window);
+        return SP_EINVAL;
+    }
+    if ((s = check_rows(fn, "q", q, cache->dtype, batch->T)) != SP_OK || (s = check_apart(fn, "q", q, batch->T, H, cache->d)) != SP_OK)
+        return s;
+    AttendProblem p;
+    memset(&p, 0, sizeof(p));
+    if (q) p.q = *q;
+    p.cache = *cache; p.batch = *batch; p.H = H; p.scale = (float)scale;
+    p.window = window >= (int64_t)1 << 30 ? 0 : (int)window;       // kv_len is at most 2^30: no limit at all
+    p.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (cache->page == 1 << i) p.page_shift = i;
+    *out = p;
+    return SP_OK;
+}
+
+// seen: null for causal attention.
+sp_status attend(const char* fn, const sp_rows* q, const sp_cache* cache, const sp_batch* batch, int H, double scale, int64_t window,
+                 const uint32_t* seen, int64_t seen_stride, const sp_rows* out, float* lse, int64_t lse_stride_row,
+                 int64_t lse_stride_head, void* ws, size_t ws_bytes, void* stream) {
+    AttendProblem p;
+    sp_status s;
+    if ((s = attend_problem(fn, q, cache, batch, H, scale, window, &p)) != SP_OK) return s;
+    if ((s = check_rows(fn, "out", out, cache->dtype, batch->T)) != SP_OK) return s;
+    if (reinterpret_cast<uintptr_t>(lse) % 4) {
+        set_error("%s: lse must be 4-byte aligned", fn);
+        return SP_EINVAL;
+    }
+    if ((s = check_apart(fn, "out", out, batch->T, H, cache->d)) != SP_OK) return s;
+    if ((s = check_workspace(fn, ws, ws_bytes, attend_bytes(fn, cache, batch, H))) != SP_OK) return s;
+    if (out) p.out = *out;
+    p.lse = lse; p.lse_stride_row = lse_stride_row; p.lse_stride_head = lse_stride_head;
+    p.seen = seen; p.seen_stride = seen_stride;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    switch (path_of(*cache, *batch, H)) {
+        case kGeneral: s = attend_general_launch(p, ws, st); break;
+        case kStep: s = attend_step_launch(p, ws, st); break;
+        case kChunks: s = attend_tc_launch(p, 0, ws, 0, st); break;
+        case kMixed:
+            s = attend_step_launch(p, ws, st);
+            if (s == SP_OK) s = attend_tc_launch(p, 16, ws, attend_step_ws_bytes(*cache), st);
+            break;
+    }
+    if (s == SP_OK) clear_error();
+    return s;
 }
 
 }  // namespace
@@ -315,11 +438,7 @@ sp_status sp_cache_write(const sp_cache* cache, const sp_batch* batch, const sp_
     const char* fn = "sp_cache_write";
     sp_status s;
     if ((s = check_cache(fn, cache)) != SP_OK || (s = check_batch_args(fn, batch)) != SP_OK) return s;
-    Axis axis[3] = {{cache->pages, cache->stride_page}, {cache->H_kv, cache->stride_head}, {cache->page, cache->stride_slot}};
-    if (!apart(axis, cache->d)) {
-        set_error("%s: pages, heads or slots of the cache overlap", fn);
-        return SP_EINVAL;
-    }
+    if ((s = check_no_overlap(fn, cache)) != SP_OK) return s;
     if ((s = check_rows(fn, "k_new", k_new, cache->dtype, batch->T)) != SP_OK ||
         (s = check_rows(fn, "v_new", v_new, cache->dtype, batch->T)) != SP_OK)
         return s;
@@ -352,61 +471,176 @@ sp_status sp_cache_read(const sp_cache* cache, const sp_batch* batch, const sp_r
 }
 
 size_t sp_attend_workspace_size(const sp_cache* cache, const sp_batch* batch, int H) {
-    const char* fn = "sp_attend_workspace_size";
-    if (check_cache(fn, cache) != SP_OK || check_batch_args(fn, batch) != SP_OK) return 0;
-    if (H < 1 || H % cache->H_kv) {
-        set_error("%s: H (%d) must be a multiple of H_kv (%d)", fn, H, cache->H_kv);
-        return 0;
-    }
-    return path_bytes(path_of(*cache, *batch, H), *cache);
+    return attend_bytes("sp_attend_workspace_size", cache, batch, H);
+}
+
+size_t sp_attend_tree_workspace_size(const sp_cache* cache, const sp_batch* batch, int H) {
+    return attend_bytes("sp_attend_tree_workspace_size", cache, batch, H);
 }
 
 sp_status sp_attend(const sp_rows* q, const sp_cache* cache, const sp_batch* batch, int H, double scale,
                     int64_t window, const sp_rows* out, float* lse, int64_t lse_stride_row,
                     int64_t lse_stride_head, void* ws, size_t ws_bytes, void* stream) {
-    const char* fn = "sp_attend";
+    return attend("sp_attend", q, cache, batch, H, scale, window, nullptr, 0, out, lse, lse_stride_row, lse_stride_head, ws, ws_bytes,
+                  stream);
+}
+
+sp_status sp_attend_tree(const sp_rows* q, const sp_cache* cache, const sp_batch* batch, int H, double scale,
+                         int64_t window, const uint32_t* seen, int64_t seen_stride, int seen_words, const sp_rows* out, float* lse,
+                         int64_t lse_stride_row, int64_t lse_stride_head, void* ws, size_t ws_bytes, void* stream) {
+    const char* fn = "sp_attend_tree";
     sp_status s;
-    if ((s = check_cache(fn, cache)) != SP_OK || (s = check_batch_args(fn, batch)) != SP_OK) return s;
-    if (H < 1 || H % cache->H_kv) {
-        set_error("%s: H (%d) must be a multiple of H_kv (%d)", fn, H, cache->H_kv);
+    if ((s = check_batch_args(fn, batch)) != SP_OK || (s = check_words(fn, batch, seen, seen_stride, seen_words)) != SP_OK) return s;
+    static const uint32_t none = 0;         // of an empty batch: never read
+    return attend(fn, q, cache, batch, H, scale, window, seen ? seen : &none, seen_stride, out, lse, lse_stride_row, lse_stride_head, ws,
+                  ws_bytes, stream);
+}
+
+size_t sp_tree_workspace_size(void) { return sizeof(WsHeader); }
+
+sp_status sp_tree_seen(const sp_batch* batch, const int32_t* parent, uint32_t* seen, int64_t seen_stride, int seen_words,
+                       int32_t* positions, void* ws, size_t ws_bytes, void* stream) {
+    const char* fn = "sp_tree_seen";
+    sp_status s;
+    if ((s = check_batch_args(fn, batch)) != SP_OK) return s;
+    if (!seen && !positions) {
+        set_error("%s: neither seen nor positions are asked for", fn);
         return SP_EINVAL;
     }
-    const float factor = (float)scale * 1.4426950408889634f;        // the kernels': logits to base 2
-    if (!(factor >= FLT_MIN) || !isfinite(factor)) {
-        set_error("%s: scale must be positive, and a normal fp32 number times log2(e) (got %g)", fn, scale);
+    if (seen && (s = check_words(fn, batch, seen, seen_stride, seen_words)) != SP_OK) return s;
+    if (seen && batch->T > 1 && seen_stride < seen_words) {
+        set_error("%s: the rows of seen overlap (stride %lld of %d words)", fn, (long long)seen_stride, seen_words);
         return SP_EINVAL;
     }
-    if (window < 0) {
-        set_error("%s: window must be >= 0 (got %lld)", fn, (long long)window);
+    if (batch->T > 0 && (s = check_ints(fn, "parent", parent)) != SP_OK) return s;
+    if (reinterpret_cast<uintptr_t>(positions) % 4) {
+        set_error("%s: misaligned positions", fn);
         return SP_EINVAL;
     }
-    if ((s = check_rows(fn, "q", q, cache->dtype, batch->T)) != SP_OK || (s = check_rows(fn, "out", out, cache->dtype, batch->T)) != SP_OK)
+    if ((s = check_workspace(fn, ws, ws_bytes, sizeof(WsHeader))) != SP_OK) return s;
+    s = tree_seen_launch(*batch, parent, seen, seen_stride, seen ? seen_words : 1, positions, ws, static_cast<cudaStream_t>(stream));
+    if (s == SP_OK) clear_error();
+    return s;
+}
+
+sp_status sp_tree_accept(const sp_batch* batch, const int32_t* parent, const int32_t* draft, const int32_t* target, int32_t* path,
+                         int64_t path_stride, int64_t* n_path, int32_t* next, void* ws, size_t ws_bytes, void* stream) {
+    const char* fn = "sp_tree_accept";
+    sp_status s;
+    if ((s = check_batch_args(fn, batch)) != SP_OK) return s;
+    if (batch->T > 0 && ((s = check_ints(fn, "parent", parent)) != SP_OK || (s = check_ints(fn, "draft", draft)) != SP_OK ||
+                         (s = check_ints(fn, "target", target)) != SP_OK))
         return s;
+    if ((batch->max_new > 0 && (s = check_ints(fn, "path", path)) != SP_OK) || (s = check_counts(fn, "n_path", n_path)) != SP_OK) return s;
+    if (batch->B > 1 && path_stride < batch->max_new) {
+        set_error("%s: the sequences' paths overlap (stride %lld for %d tokens)", fn, (long long)path_stride, batch->max_new);
+        return SP_EINVAL;
+    }
+    if (reinterpret_cast<uintptr_t>(next) % 4) {
+        set_error("%s: misaligned next", fn);
+        return SP_EINVAL;
+    }
+    if ((s = check_workspace(fn, ws, ws_bytes, sizeof(WsHeader))) != SP_OK) return s;
+    s = tree_accept_launch(*batch, parent, draft, target, path, path_stride, n_path, next, ws, static_cast<cudaStream_t>(stream));
+    if (s == SP_OK) clear_error();
+    return s;
+}
+
+size_t sp_attend_weights_workspace_size(const sp_cache* cache, const sp_batch* batch, int H) {
+    const char* fn = "sp_attend_weights_workspace_size";
+    if (check_cache(fn, cache) != SP_OK || check_batch_args(fn, batch) != SP_OK || check_heads(fn, cache, H) != SP_OK) return 0;
+    return sizeof(WsHeader);
+}
+
+sp_status sp_attend_weights(const sp_rows* q, const sp_cache* cache, const sp_batch* batch, int H, double scale, int64_t window,
+                            const float* lse, int64_t lse_stride_row, int64_t lse_stride_head, double decay, float* weights,
+                            void* ws, size_t ws_bytes, void* stream) {
+    const char* fn = "sp_attend_weights";
+    sp_status s;
+    AttendProblem a;
+    if ((s = attend_problem(fn, q, cache, batch, H, scale, window, &a)) != SP_OK) return s;
+    if (batch->T > 0 && !lse) {
+        set_error("%s: null lse", fn);
+        return SP_EINVAL;
+    }
+    if ((s = check_weights(fn, weights)) != SP_OK) return s;
     if (reinterpret_cast<uintptr_t>(lse) % 4) {
         set_error("%s: lse must be 4-byte aligned", fn);
         return SP_EINVAL;
     }
-    if ((s = check_apart(fn, "q", q, batch->T, H, cache->d)) != SP_OK || (s = check_apart(fn, "out", out, batch->T, H, cache->d)) != SP_OK)
-        return s;
-    const size_t need = sp_attend_workspace_size(cache, batch, H);
-    if ((s = check_workspace(fn, ws, ws_bytes, need)) != SP_OK) return s;
-    AttendProblem p;
-    p.q = *q; p.out = *out; p.cache = *cache; p.batch = *batch; p.H = H; p.scale = (float)scale;
-    p.window = window >= (int64_t)1 << 30 ? 0 : (int)window;       // kv_len is at most 2^30: no limit at all
-    p.page_shift = -1;
-    for (int i = 0; i < 31; ++i)
-        if (cache->page == 1 << i) p.page_shift = i;
-    p.lse = lse; p.lse_stride_row = lse_stride_row; p.lse_stride_head = lse_stride_head;
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    switch (path_of(*cache, *batch, H)) {
-        case kGeneral: s = attend_general_launch(p, ws, st); break;
-        case kStep: s = attend_step_launch(p, ws, st); break;
-        case kChunks: s = attend_tc_launch(p, 0, ws, 0, st); break;
-        case kMixed:
-            s = attend_step_launch(p, ws, st);
-            if (s == SP_OK) s = attend_tc_launch(p, 16, ws, attend_step_ws_bytes(*cache), st);
-            break;
+    if (!(decay >= 0 && decay <= 1)) {
+        set_error("%s: decay must be in [0, 1] (got %g)", fn, decay);
+        return SP_EINVAL;
     }
+    if ((s = check_workspace(fn, ws, ws_bytes, sp_attend_weights_workspace_size(cache, batch, H))) != SP_OK) return s;
+    a.lse = const_cast<float*>(lse);        // read only
+    a.lse_stride_row = lse_stride_row;
+    a.lse_stride_head = lse_stride_head;
+    const WeightsProblem w{a, (float)decay, weights};
+    s = weights_general_launch(w, ws, static_cast<cudaStream_t>(stream));
+    if (s == SP_OK) clear_error();
+    return s;
+}
+
+sp_status sp_cache_choose(const sp_cache* cache, const sp_batch* batch, const float* weights, int shared, int64_t budget,
+                          int64_t first, int64_t last, int32_t* kept, int64_t kept_stride_seq, int64_t kept_stride_head,
+                          int64_t* n_kept, void* ws, size_t ws_bytes, void* stream) {
+    const char* fn = "sp_cache_choose";
+    sp_status s;
+    if ((s = check_cache(fn, cache)) != SP_OK || (s = check_batch_args(fn, batch)) != SP_OK || (s = check_weights(fn, weights)) != SP_OK)
+        return s;
+    if (budget < 0 || budget > (int64_t)1 << 30 || first < 0 || last < 0 || first > budget || last > budget - first) {
+        set_error("%s: 0 <= first + last <= budget <= 2^30 (got %lld, %lld, %lld)", fn, (long long)first, (long long)last,
+                  (long long)budget);
+        return SP_EINVAL;
+    }
+    const int heads = shared ? 1 : cache->H_kv;
+    if ((s = check_items(fn, (int64_t)batch->B * heads)) != SP_OK) return s;
+    if ((budget > 0 && (s = check_ints(fn, "kept", kept)) != SP_OK) || (s = check_counts(fn, "n_kept", n_kept)) != SP_OK) return s;
+    Axis axis[2] = {{batch->B, kept_stride_seq}, {heads, kept_stride_head}};
+    if (budget > 0 && !apart(axis, (int)budget)) {
+        set_error("%s: the lists of kept overlap", fn);
+        return SP_EINVAL;
+    }
+    if ((s = check_workspace(fn, ws, ws_bytes, sizeof(WsHeader))) != SP_OK) return s;
+    s = cache_choose_launch(*cache, *batch, weights, shared != 0, budget, first, last, kept, kept_stride_seq, kept_stride_head, n_kept,
+                            ws, static_cast<cudaStream_t>(stream));
+    if (s == SP_OK) clear_error();
+    return s;
+}
+
+sp_status sp_cache_keep(const sp_cache* cache, const sp_batch* batch, const int32_t* kept, int heads, int64_t kept_stride_seq,
+                        int64_t kept_stride_head, const int64_t* n_kept, int64_t most, int drafted, const int32_t* to, int to_width,
+                        int64_t to_stride, float* weights, int64_t* kv_out, void* ws, size_t ws_bytes, void* stream) {
+    const char* fn = "sp_cache_keep";
+    sp_status s;
+    if ((s = check_cache(fn, cache)) != SP_OK || (s = check_batch_args(fn, batch)) != SP_OK || (s = check_no_overlap(fn, cache)) != SP_OK)
+        return s;
+    if (heads != 1 && heads != cache->H_kv) {
+        set_error("%s: a list for every KV head (%d) or 1 that they share (got %d)", fn, cache->H_kv, heads);
+        return SP_EINVAL;
+    }
+    if ((s = check_items(fn, 2 * (int64_t)batch->B * cache->H_kv)) != SP_OK) return s;
+    if (most < 0 || most > (int64_t)1 << 30) {
+        set_error("%s: lists of 0 to 2^30 entries (got %lld)", fn, (long long)most);
+        return SP_EINVAL;
+    }
+    if ((most > 0 && (s = check_ints(fn, "kept", kept)) != SP_OK) || (s = check_counts(fn, "n_kept", n_kept)) != SP_OK ||
+        (s = check_counts(fn, "kv_out", kv_out)) != SP_OK)
+        return s;
+    if (kv_out == batch->kv_len || kv_out == n_kept) {
+        set_error("%s: kv_out must be neither kv_len nor n_kept, which are read meanwhile", fn);
+        return SP_EINVAL;
+    }
+    if (reinterpret_cast<uintptr_t>(to) % 4 || (to && (to_width < 1 || to_stride < 0))) {
+        set_error("%s: to must be 4-byte aligned, with to_width >= 1 and to_stride >= 0", fn);
+        return SP_EINVAL;
+    }
+    if (to == batch->table) to = nullptr;       // the same places
+    if (weights && (s = check_weights(fn, weights)) != SP_OK) return s;
+    if ((s = check_workspace(fn, ws, ws_bytes, sizeof(WsHeader))) != SP_OK) return s;
+    s = cache_keep_launch(*cache, *batch, kept, heads, kept_stride_seq, kept_stride_head, n_kept, most, drafted != 0, to, to_width,
+                          to_stride, weights, kv_out, ws, static_cast<cudaStream_t>(stream));
     if (s == SP_OK) clear_error();
     return s;
 }

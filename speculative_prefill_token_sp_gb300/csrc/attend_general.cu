@@ -91,7 +91,8 @@ __device__ __forceinline__ void write_out(const SplitArgs& p, int64_t row, int h
             z == 0.f ? -INFINITY : (m + log2f(z)) * 0.6931471805599453f;
 }
 
-template <typename T, int kKind>
+// kTree: the new tokens are drafted ones, and p.a.seen says which of them each sees.
+template <typename T, int kKind, bool kTree>
 __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(const __grid_constant__ SplitArgs p, int lg) {
     __shared__ float sm_o[kGenWarps][kGenRows][256];
     __shared__ float2 sm_ml[kGenWarps][kGenRows];
@@ -125,20 +126,26 @@ __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(const __grid_co
         const int rows = (int)min((int64_t)kGenRows, (int64_t)s.n * p.G - r0);
 
         float q[kGenRows][8], o[kGenRows][8], m[kGenRows], z[kGenRows];
-        int last[kGenRows];
-        int item_last = -1;
+        int last[kGenRows], drafted[kGenRows];      // drafted tokens: `last` is the row's place, which the window goes by
+        int item_last = kTree ? s.kv - 1 : -1;
 #pragma unroll
         for (int i = 0; i < kGenRows; ++i) {
             m[i] = -INFINITY;
             z[i] = 0.f;
             last[i] = -1;
+            drafted[i] = -1;
 #pragma unroll
             for (int e = 0; e < 8; ++e) q[i][e] = o[i][e] = 0.f;
             if (i >= rows) continue;
             const int t = (int)divide(r0 + i, p.G), h = g * p.G + (int)(r0 + i - (int64_t)t * p.G);
             if (act) load8(static_cast<const T*>(p.a.q.data) + (s.row0 + t) * p.a.q.stride_row + h * p.a.q.stride_head + sub * 8, q[i]);
-            last[i] = s.kv - s.n + t;
-            item_last = max(item_last, last[i]);
+            if constexpr (kTree) {
+                drafted[i] = t;
+                last[i] = p.a.window ? place_of_drafted(p.a, s, t) : 0;
+            } else {
+                last[i] = s.kv - s.n + t;
+                item_last = max(item_last, last[i]);
+            }
         }
 
         // this group's keys: of each unit's share of the warp, every step-th
@@ -182,7 +189,14 @@ __global__ void __launch_bounds__(kGenThreads, 3) general_kernel(const __grid_co
             }
 #pragma unroll
             for (int i = 0; i < kR; ++i) {
-                seen[i] = tok >= 0 && tok <= last[i] && (!p.a.window || tok > last[i] - p.a.window);
+                if constexpr (kTree) {
+                    const int u = tok - (s.kv - s.n);
+                    if (tok < 0 || drafted[i] < 0) seen[i] = false;
+                    else if (u < 0) seen[i] = !p.a.window || tok > last[i] - p.a.window;
+                    else seen[i] = seen_word(p.a, s, drafted[i], u >> 5) >> (u & 31) & 1;
+                } else {
+                    seen[i] = tok >= 0 && tok <= last[i] && (!p.a.window || tok > last[i] - p.a.window);
+                }
                 x[i] = seen[i] ? x[i] * f : -INFINITY;
                 grows |= x[i] > m[i];
             }
@@ -341,15 +355,25 @@ __global__ void __launch_bounds__(32 * kJoinWarps) general_join_kernel(const __g
 
 int general_ctas() { return sm_count() * 3; }
 
+template <typename T, int kKind>
+void launch_kind(const SplitArgs& p, int lg, cudaStream_t st, bool tree) {
+    if (tree) general_kernel<T, kKind, true><<<p.P, kGenThreads, 0, st>>>(p, lg);
+    else general_kernel<T, kKind, false><<<p.P, kGenThreads, 0, st>>>(p, lg);
+}
+template <typename T>
+void launch_main(const SplitArgs& p, int lg, cudaStream_t st, bool tree) {
+    switch (p.a.cache.kind) {
+        case SP_CACHE_SAME: launch_kind<T, SP_CACHE_SAME>(p, lg, st, tree); break;
+        case SP_CACHE_E4M3: launch_kind<T, SP_CACHE_E4M3>(p, lg, st, tree); break;
+        default: launch_kind<T, SP_CACHE_INT8>(p, lg, st, tree); break;
+    }
+}
+
 template <typename T>
 sp_status launch(const SplitArgs& p, cudaStream_t st) {
     int lg = 0;
     while ((8 << lg) < p.a.cache.d) ++lg;
-    switch (p.a.cache.kind) {
-        case SP_CACHE_SAME: general_kernel<T, SP_CACHE_SAME><<<p.P, kGenThreads, 0, st>>>(p, lg); break;
-        case SP_CACHE_E4M3: general_kernel<T, SP_CACHE_E4M3><<<p.P, kGenThreads, 0, st>>>(p, lg); break;
-        default: general_kernel<T, SP_CACHE_INT8><<<p.P, kGenThreads, 0, st>>>(p, lg); break;
-    }
+    launch_main<T>(p, lg, st, p.a.seen != nullptr);
     SP_LAUNCH_CHECK();
     const int64_t rows = std::min<int64_t>(kGenRows, (int64_t)p.a.batch.max_new * p.G);
     const dim3 grid((unsigned)p.P - 1, (unsigned)std::max<int64_t>(1, rows));

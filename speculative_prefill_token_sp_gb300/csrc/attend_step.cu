@@ -141,8 +141,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// kN: tiles of 8 query rows (1 or 2).
-template <int D, int kKind, int kN>
+// kN: tiles of 8 query rows (1 or 2).  kTree: the new tokens are drafted ones, and p.a.seen says which of them each sees.
+template <int D, int kKind, int kN, bool kTree>
 __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const __grid_constant__ SplitArgs p) {
     constexpr bool kSame = kKind == SP_CACHE_SAME;
     using R = Ring<D, kKind, kN>;
@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
         uint32_t qb[kN][2 * kJ * (kE / 8)][2];
         float fq[kN][2];            // the logits' factor (8-bit caches: with the query rows' own)
         int last[kN][2], first[kN][2];
+        uint32_t drafted[kN][2];    // the new tokens that the rows see: at most 16 of them
 #pragma unroll
         for (int h = 0; h < kN; ++h) {
             const int r = n + 8 * h, t = r / p.G;
@@ -278,11 +279,17 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 const int ry = 8 * h + 2 * q4 + y;
-                last[h][y] = ry < rows ? s.kv - s.n + ry / p.G : -1;
-                first[h][y] = p.a.window ? last[h][y] - p.a.window + 1 : 0;
+                if constexpr (kTree) {
+                    drafted[h][y] = ry < rows ? seen_word(p.a, s, ry / p.G, 0) : 0u;
+                    last[h][y] = ry < rows ? s.kv - s.n - 1 : -1;
+                    first[h][y] = p.a.window ? s.kv - s.n + max(__popc(drafted[h][y]), 1) - p.a.window : 0;
+                } else {
+                    last[h][y] = ry < rows ? s.kv - s.n + ry / p.G : -1;
+                    first[h][y] = p.a.window ? last[h][y] - p.a.window + 1 : 0;
+                }
             }
         }
-        const int all_last = s.kv - s.n, all_first = p.a.window ? s.kv - p.a.window : 0;  // tokens that every row sees
+        const int all_last = s.kv - s.n - kTree, all_first = p.a.window ? s.kv - p.a.window : 0;  // tokens that every row sees
 
         float o[kN][kO][4];
         float m[kN][2], z[kN][2];
@@ -356,7 +363,13 @@ __global__ void __launch_bounds__(kThreads, kN == 1 ? 3 : 2) step_kernel(const _
                         for (int y = 0; y < 2; ++y) {
                             float& v = x[h][t][2 * e + y];
                             v *= kSame ? f : fq[h][y] * sc.x;
-                            if (masked && (tok > last[h][y] || tok < first[h][y])) v = -INFINITY;
+                            if constexpr (kTree) {
+                                const int u = tok - (s.kv - s.n);
+                                const bool seen = u < 0 ? tok <= last[h][y] && tok >= first[h][y] : (drafted[h][y] >> min(u, 31)) & 1;
+                                if (masked && !seen) v = -INFINITY;
+                            } else {
+                                if (masked && (tok > last[h][y] || tok < first[h][y])) v = -INFINITY;
+                            }
                             top[h][y] = fmaxf(top[h][y], v);
                         }
                 }
@@ -584,7 +597,8 @@ int ctas(int rows) { return sm_count() * (rows <= 8 ? 3 : 2); }
 template <int D, int kKind>
 sp_status launch(const SplitArgs& p, cudaStream_t st) {
     const int smem = p.rows <= 8 ? Ring<D, kKind, 1>::kSmem : Ring<D, kKind, 2>::kSmem;
-    void (*kern)(SplitArgs) = p.rows <= 8 ? step_kernel<D, kKind, 1> : step_kernel<D, kKind, 2>;
+    void (*kern)(SplitArgs) = p.a.seen ? (p.rows <= 8 ? step_kernel<D, kKind, 1, true> : step_kernel<D, kKind, 2, true>)
+                                       : (p.rows <= 8 ? step_kernel<D, kKind, 1, false> : step_kernel<D, kKind, 2, false>);
     SP_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     kern<<<p.P, kThreads, smem, st>>>(p);
     SP_LAUNCH_CHECK();

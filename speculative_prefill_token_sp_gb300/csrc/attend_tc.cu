@@ -120,8 +120,9 @@ __device__ __forceinline__ Item item_of(const TcArgs& p, const Seq& s, int b, in
     Item it;
     it.b = b;
     it.t0 = qt * 2 * p.tpt;
-    const int last = min(s.n, it.t0 + 2 * p.tpt) - 1 + s.kv - s.n;      // place of the item's last token
-    const int first = p.a.window ? max(0, s.kv - s.n + it.t0 - p.a.window + 1) : 0;
+    // place of the item's last token; a drafted one may see any of the new tokens, and be anywhere among them
+    const int last = p.a.seen ? s.kv - 1 : min(s.n, it.t0 + 2 * p.tpt) - 1 + s.kv - s.n;
+    const int first = p.a.window ? max(0, s.kv - s.n + (p.a.seen ? 0 : it.t0) - p.a.window + 1) : 0;
     it.lo = first / kKeys;
     it.tiles = last < 0 ? 1 : last / kKeys + 1 - it.lo;
     return it;
@@ -383,30 +384,35 @@ __device__ __forceinline__ void max_cols(const float* v, float (&mx)[4]) {
         for (int c = 0; c < 4; ++c) mx[c] = fmax3(mx[c], v[i + 2 * c], v[i + 2 * c + 1]);
 }
 
-// The lowest n bits (none if n < 0).
-__device__ __forceinline__ uint32_t low_bits(int n) {
-    uint32_t r;
-    asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(r) : "r"(max(n, 0)));
-    return r;
-}
+// The columns of a tile that a row sees: lo to hi, and of drafted tokens (kTree) those whose bits are set.
+template <bool kTree>
+struct Cols {
+    int hi, lo;
+    uint32_t drafted[kTree ? 4 : 1];
+    __device__ __forceinline__ uint32_t word(int c) const {         // columns 32 c to 32 c + 31
+        uint32_t r = low_bits(hi - 32 * c + 1) & ~low_bits(lo - 32 * c);
+        if constexpr (kTree) r |= c == 0 ? drafted[0] : c == 1 ? drafted[1] : c == 2 ? drafted[2] : drafted[3];
+        return r;
+    }
+};
 
-// Takes out those of 32 columns from `first` on that the row does not see (all but lo to hi).
-__device__ __forceinline__ void mask_cols(float* v, int first, int hi, int lo) {
-    const uint32_t seen = low_bits(hi - first + 1) & ~low_bits(lo - first);
+// Takes out those of 32 columns that the row does not see.
+__device__ __forceinline__ void mask_cols(float* v, uint32_t seen) {
 #pragma unroll
     for (int i = 0; i < 32; ++i)
         if (!(seen >> i & 1)) v[i] = -INFINITY;
 }
 
 // The largest logit (before the factor f) of a tile that the row sees, read once more from TMEM.
-__device__ __forceinline__ float top_of_row(uint32_t s_at, uint32_t* sr, bool masked, int hi, int lo) {
+template <bool kTree>
+__device__ __forceinline__ float top_of_row(uint32_t s_at, uint32_t* sr, bool masked, const Cols<kTree>& cols) {
     float* sv = reinterpret_cast<float*>(sr);
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         tmem_ld32(s_at + 32 * c, sr);
         tmem_wait32(sr);
-        if (masked) mask_cols(sv, 32 * c, hi, lo);
+        if (masked) mask_cols(sv, cols.word(c));
         max_cols<32>(sv, mx);
     }
     return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
@@ -547,7 +553,8 @@ struct Layout {
     static constexpr int kO(int w) { return 256 + w * D; }
 };
 
-template <int D, int kKind>
+// kTree: the new tokens are drafted ones, and p.a.seen says which of them each sees.
+template <int D, int kKind, bool kTree>
 __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(const __grid_constant__ Maps maps,
                                                                 const __grid_constant__ TcArgs p) {
     using L = Layout<D>;
@@ -636,7 +643,9 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
             // places of the tile's first and last rows, for whether a key tile needs a mask at all, and of this one
             const int p_first = sg.s.kv - sg.s.n + sg.it.t0 + w * p.tpt;
             const int p_last = sg.s.kv - sg.s.n + min(sg.s.n, sg.it.t0 + (w + 1) * p.tpt) - 1;
-            const int pos = row < rows_tile ? min(p_first + row / p.G, p_last) : -1;
+            const int pos = row >= rows_tile ? -1 : kTree ? 0 : min(p_first + row / p.G, p_last);     // below 0: not a row
+            const int ctx = sg.s.kv - sg.s.n, drafted = kTree ? min(sg.it.t0 + w * p.tpt + row / p.G, sg.s.n - 1) : 0;
+            const int place = kTree && p.a.window && row < rows_tile ? place_of_drafted(p.a, sg.s, drafted) : 0;
             // z and O are sums of 2^(logit - m).  m need not be the row's maximum, only near it: it is the maximum of the first tile
             // that the row sees, and where a tile's weights sum to more than 2^8, m grows by that sum's logarithm before the
             // next one.  So the maximum of a tile is not looked for.  A tile is done again by its true maximum if its weights
@@ -646,12 +655,30 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
             const int n_tiles = sg.to - sg.from;
             int base = tile_of(sg, sg.from) * kKeys;
             for (int x = 0; x < n_tiles; ++x, base -= kKeys) {
+                const bool masked = kTree ? base + kKeys > ctx || (p.a.window && base < sg.s.kv - p.a.window)
+                                          : base + kKeys - 1 > p_first || (p.a.window && base <= p_last - p.a.window);
+                Cols<kTree> cols;
+                if constexpr (kTree) {
+                    cols.hi = row < rows_tile ? ctx - 1 - base : -1;
+                    cols.lo = p.a.window ? place - p.a.window + 1 - base : -1;
+                    if (masked) {           // (the loads are done before the wait ends)
+                        const int k = (base - ctx) >> 5, sh = (base - ctx) & 31;
+                        uint32_t prev = row < rows_tile ? seen_word(p.a, sg.s, drafted, k) : 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t next = row < rows_tile ? seen_word(p.a, sg.s, drafted, k + i + 1) : 0;
+                            cols.drafted[i] = __funnelshift_r(prev, next, sh);
+                            prev = next;
+                        }
+                    }
+                } else {
+                    cols.hi = pos - base;
+                    cols.lo = p.a.window ? cols.hi - p.a.window + 1 : -1;
+                }
                 ok = wait_warp(smem_u32(&s_full[w]), ph, abort_flag, 21);
                 ph ^= 1;
                 if (!ok) break;
                 tc_fence_after();
-                const bool masked = base + kKeys - 1 > p_first || (p.a.window && base <= p_last - p.a.window);
-                const int hi = pos - base, lo = p.a.window ? hi - p.a.window + 1 : -1;      // columns this row sees
                 if (follow) {
                     const float a = next_m > m ? ex2_approx(m - next_m) : 1.f;
                     m = next_m;
@@ -664,7 +691,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                 // twice at most: after a pass by the true maximum nothing is lost
                 for (int pass = 0; pass < 2; ++pass) {
                     if (fresh) {            // the true maximum, for rows without an m or with one left far behind
-                        const float top = top_of_row(s_at, sr, masked, hi, lo) * f;         // f > 0: f times the largest product
+                        const float top = top_of_row(s_at, sr, masked, cols) * f;         // f > 0: f times the largest product
                         // 16: a sum of 96 over 2^24 has a maximum over 2^17.  Also where there was no m
                         const bool far = top > m + (huge ? 0.f : 16.f);
                         const float a = far && m != -INFINITY ? ex2_approx(m - top) : 1.f;
@@ -686,7 +713,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                         tmem_ld32(s_at + 32, sr + 32);
                         tmem_ld32(s_at + 64, sr + 64);
                     }
-                    if (masked) mask_cols(v3, 96, hi, lo);
+                    if (masked) mask_cols(v3, cols.word(3));
                     max_cols<32>(v3, mx);
 #pragma unroll
                     for (int c = 0; c < 3; ++c) {
@@ -696,7 +723,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                         if constexpr (kSame) {
                             if (c == 2) keep32(sr + 64);
                         }
-                        if (masked) mask_cols(v, 32 * c, hi, lo);
+                        if (masked) mask_cols(v, cols.word(c));
                         weights32(v, f, nm, zs, pk + 16 * c);
                     }
                     const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * f;
@@ -713,7 +740,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                     for (int c = 0; c < 4; ++c) {
                         tmem_ld32(s_at + 32 * c, sr);
                         tmem_wait32(sr);
-                        if (masked) mask_cols(sv, 32 * c, hi, lo);
+                        if (masked) mask_cols(sv, cols.word(c));
 #pragma unroll
                         for (int i = 0; i < 32; ++i) sv[i] = __fmul_rn(sv[i], f);
                         weights32(sv, 1.f, m == -INFINITY ? 0.f : -m, zs, pk);
@@ -727,7 +754,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) attend_tc_kernel(co
                     if constexpr (!kSame) {
                         tmem_ld32(s_at + 96, sr);
                         tmem_wait32(sr);
-                        if (masked) mask_cols(sv, 96, hi, lo);
+                        if (masked) mask_cols(sv, cols.word(3));
                     }
                     weights32(kSame ? sv + 96 : sv, f, nm, zs, pk);
                     tmem_st16(s_at + 48, pk);
@@ -1245,13 +1272,14 @@ sp_status encode(CUtensorMap* map, const void* data, int rank, const int64_t* ex
 
 template <int D, int kKind>
 sp_status launch(const Maps& maps, const TcArgs& p, cudaStream_t st) {
-    SP_CUDA_TRY(cudaFuncSetAttribute(attend_tc_kernel<D, kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+    void (*kern)(Maps, TcArgs) = p.a.seen ? attend_tc_kernel<D, kKind, true> : attend_tc_kernel<D, kKind, false>;
+    SP_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
     // after the step kernels of a mixed batch this one does not wait for them
     if (p.min_rows > 0) {
-        const sp_status s = launch_early(attend_tc_kernel<D, kKind>, dim3((unsigned)p.P), Roles<kKind>::kThreads, (size_t)kSmem, st, maps, p);
+        const sp_status s = launch_early(kern, dim3((unsigned)p.P), Roles<kKind>::kThreads, (size_t)kSmem, st, maps, p);
         if (s != SP_OK) return s;
     } else {
-        attend_tc_kernel<D, kKind><<<p.P, Roles<kKind>::kThreads, kSmem, st>>>(maps, p);
+        kern<<<p.P, Roles<kKind>::kThreads, kSmem, st>>>(maps, p);
         SP_LAUNCH_CHECK();
     }
     return launch_early(tc_join_kernel<D>, dim3((unsigned)std::max(1, p.P - 1), D / 16), kRowsItem, (size_t)0, st, p, p.min_rows == 0 ? 1 : 0);

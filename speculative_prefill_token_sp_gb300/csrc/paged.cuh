@@ -230,6 +230,30 @@ __device__ __forceinline__ void check_batch(const sp_batch& b, const sp_cache& c
     }
 }
 
+// The same for calls that go over all tokens that a sequence's new ones see (with `idle`: of every sequence, also without new ones).
+__device__ __forceinline__ void check_tokens(const sp_batch& b, const sp_cache& c, int window, bool idle, WsHeader* hdr) {
+    __shared__ int bad;
+    if (threadIdx.x == 0) bad = 0;
+    __syncthreads();
+    int mine = 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    for (int i = warp; i < b.B; i += warps) {
+        const Seq s = load_seq(b, c.page, i);
+        if (!s.ok) mine = max(mine, 1);
+        if (s.kv == 0 || (s.n == 0 && !idle)) continue;
+        for (int q = first_seen(s, window) / c.page + lane; q <= (s.kv - 1) / c.page; q += 32) {
+            const int pg = b.table[(int64_t)i * b.table_stride + q];
+            if (pg < 0 || pg >= c.pages) mine = 2;
+        }
+    }
+    if (mine) atomicMax(&bad, mine);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        hdr->status = bad ? SP_EDEVICE : SP_OK;
+        hdr->where = bad;
+    }
+}
+
 // Argument checks shared by the entry points (defined in abi_paged.cu).
 sp_status check_cache(const char* fn, const sp_cache* c);
 sp_status check_batch_args(const char* fn, const sp_batch* b);
@@ -268,6 +292,35 @@ struct AttendProblem {
     }
     float* lse;             // may be null
     int64_t lse_stride_row, lse_stride_head;
+    const uint32_t* seen;   // sp_attend_tree: the new tokens that a row sees, as bits; null: those up to its own
+    int64_t seen_stride;
 };
+
+// The attention weight that cached tokens gather (weights_*.cu): a.q, a.lse (read), and the tokens' weights [pages, H_kv, page].
+struct WeightsProblem {
+    AttendProblem a;
+    float decay;
+    float* weights;
+};
+
+// The lowest n bits (none if n < 0).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    uint32_t r;
+    asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(r) : "r"(max(n, 0)));
+    return r;
+}
+
+// Of drafted tokens: word k of the new tokens that new token t of the sequence sees (0 behind the last one).
+__device__ __forceinline__ uint32_t seen_word(const AttendProblem& a, const Seq& s, int t, int k) {
+    if (k < 0 || 32 * k >= s.n) return 0;
+    return __ldg(a.seen + (s.row0 + t) * a.seen_stride + k) & low_bits(s.n - 32 * k);
+}
+
+// And its place: behind the cached tokens, and as many of the new ones as it sees, itself among them.
+__device__ __forceinline__ int place_of_drafted(const AttendProblem& a, const Seq& s, int t) {
+    int sees = 0;
+    for (int k = 0; 32 * k < s.n; ++k) sees += __popc(seen_word(a, s, t, k));
+    return s.kv - s.n + max(sees, 1) - 1;
+}
 
 }  // namespace sp
