@@ -1,0 +1,178 @@
+// What the tensor-core kernels over the paged cache share (attend_tc.cu, weights_tc.cu): the layout of a tile, bounded waits, TMEM
+// loads, packed fp32 arithmetic, the issue of MMAs and copies, tensor maps, and a scan over a block.
+//
+// A tile is 128 rows of 64 or 128 bf16: column blocks of 64 entries (128 bytes), each [128 rows][128 bytes] with 128-byte swizzle.
+#pragma once
+
+#include "paged.cuh"
+#include "tc_ptx.cuh"
+
+namespace sp {
+namespace {
+
+// Sum over the block's threads before this one's; `total` over all of them.
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* warp_sums, int64_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t mine = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int64_t w = lane < warps ? warp_sums[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+    }
+    total = __shfl_sync(0xffffffffu, w, 31);
+    const int64_t before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    __syncthreads();
+    return x - mine + (warp ? before : 0);
+}
+
+constexpr uint32_t instr_desc(int n, bool b_mn) {
+    return (1u << 4)                                // fp32 accumulator
+           | (1u << 7) | (1u << 10)                 // bf16 operands
+           | (b_mn ? 1u << 16 : 0u)                 // B stored with its N index contiguous (V), or its K index (K)
+           | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+// mbar_wait in line: a call would cost the roles registers that their shares do not have.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, int where) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try_wait_suspend(bar, parity, 1000u)) {
+        if (*abort_flag) return false;
+        if (global_ns() - t0 > kTimeoutNs) {
+            *abort_flag = where;
+            return false;
+        }
+    }
+    return true;
+}
+
+// For a warp whose lanes go on together.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int where) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, where));
+}
+
+#define TMEM_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
+#define TMEM_W8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
+
+// 32 columns of this thread's TMEM lane; the registers may be used after tmem_wait32 (16).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : TMEM_R8(r, 0), TMEM_R8(r, 8), TMEM_R8(r, 16), TMEM_R8(r, 24)
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : TMEM_R8(r, 0), TMEM_R8(r, 8)
+        : "r"(taddr));
+}
+// Waits for this thread's TMEM loads; taking the registers as operands keeps their uses below it.
+__device__ __forceinline__ void tmem_wait32(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Keeps the uses of registers that an earlier wait was for below this point.
+__device__ __forceinline__ void keep32(uint32_t* r) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// (a, b) * (x, x) + (y, y), two fp32 at once
+__device__ __forceinline__ void fma2(float& a, float& b, float x, float y) {
+    asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %2};\n\tmov.b64 w, {%3, %3};\n\t"
+        "fma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
+    asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\t"
+        "add.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+
+// The MMA warps run with all lanes and issue from one (`lead`): descriptors, addresses and loop counters are then warp-uniform for
+// the compiler, which keeps them in uniform registers.  Issued from inside `if (lane == 0)`, an MMA took so many instructions
+// that the softmax warps beside it on the scheduler held the tensor cores up (chunk of 4096 over 32768: 1.35 ms).
+// A descriptor's upper half is constant, its lower half an address that no stage carries out of.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ void mma_ss(bool lead, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}\n"
+        ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)acc), "r"((uint32_t)lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(bool lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar), "r"((uint32_t)lead)
+        : "memory");
+}
+__device__ __forceinline__ void arrive_if(bool lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}\n" ::"r"(bar), "r"((uint32_t)lead)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// A tensor map of bf16 rows; strides in entries.  An extent of 1 has no stride of its own.
+sp_status encode(CUtensorMap* map, const void* data, int rank, const int64_t* extent, const int64_t* stride, const int* box) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    if (!enc) {
+        set_error("cuTensorMapEncodeTiled is unavailable from the driver");
+        return SP_ECUDA;
+    }
+    cuuint64_t dim[4], step[3];
+    cuuint32_t bx[4], one[4] = {1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        dim[i] = (cuuint64_t)extent[i];
+        bx[i] = (cuuint32_t)box[i];
+        if (i) step[i - 1] = extent[i] == 1 ? 16 : (cuuint64_t)stride[i] * 2;
+    }
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(data), dim, step, bx, one,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        set_error("cuTensorMapEncodeTiled failed (%d)", (int)r);
+        return SP_ECUDA;
+    }
+    return SP_OK;
+}
+
+}  // namespace
+}  // namespace sp
