@@ -22,6 +22,7 @@ namespace sp {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBatch = 8;                   // tokens whose weights a thread has under way
 constexpr int kMostHeld = 48 * 1024;        // tokens that a CTA holds in shared memory; more are read again in each pass
 
 struct ChooseArgs {
@@ -34,6 +35,7 @@ struct ChooseArgs {
     int64_t stride_seq, stride_head;
     int64_t* n_kept;
     int held;                   // keys of shared memory
+    int page_shift;             // log2 of the page, or -1
     WsHeader* hdr;
 };
 
@@ -76,18 +78,47 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant_
     const int all = s.kv - p.first - p.last, per = (all + C - 1) / C;
     const int lo = min(all, r * per), m = min(all, lo + per) - lo;          // this CTA's run
     const int32_t* table = p.b.table + (int64_t)b * p.b.table_stride;
-    auto load = [&](int i) {
-        const int tok = p.first + lo + i, q = (int)((unsigned)tok / (unsigned)p.c.page), pg = table[q], slot = tok - q * p.c.page;
-        if (pg < 0 || pg >= p.c.pages) return 0u;
-        if (p.heads > 1 || p.c.H_kv == 1) return key_of(p.weights[scale_offset(p.c, pg, h, slot)]);
-        uint32_t top = 0;
-        for (int g = 0; g < p.c.H_kv; ++g) top = max(top, key_of(p.weights[scale_offset(p.c, pg, g, slot)]));
-        return top;
+    // The keys of tokens i, i + kThreads, ... (kBatch of them) of the run, their loads under way together: one after the other, a table
+    // entry and a weight each, they took most of the kernel's time.
+    auto load = [&](int i, uint32_t (&x)[kBatch]) {
+        int pg[kBatch], slot[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int tok = p.first + lo + i + u * kThreads;
+            const int q = p.page_shift >= 0 ? tok >> p.page_shift : (int)((unsigned)tok / (unsigned)p.c.page);
+            pg[u] = i + u * kThreads < m ? __ldg(table + q) : -1;
+            slot[u] = tok - q * p.c.page;
+            x[u] = 0;
+        }
+        const bool one = p.heads > 1 || p.c.H_kv == 1;
+        for (int g = one ? h : 0; g < (one ? h + 1 : p.c.H_kv); ++g) {
+            float w[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                w[u] = (unsigned)pg[u] < (unsigned)p.c.pages ? __ldg(p.weights + scale_offset(p.c, pg[u], g, slot[u])) : __int_as_float(0x7fffffff);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) x[u] = max(x[u], key_of(w[u]));
+        }
     };
     const bool in_shared = m <= p.held;
-    auto key = [&](int i) { return in_shared ? held[i] : load(i); };
-    if (in_shared)
-        for (int i = threadIdx.x; i < m; i += kThreads) held[i] = load(i);
+    if (in_shared) {
+        for (int i = threadIdx.x; i < m; i += kBatch * kThreads) {
+            uint32_t x[kBatch];
+            load(i, x);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (i + u * kThreads < m) held[i + u * kThreads] = x[u];
+        }
+    }
+    auto key = [&](int i) {
+        if (in_shared) return held[i];
+        const int tok = p.first + lo + i, q = (int)((unsigned)tok / (unsigned)p.c.page), pg = __ldg(table + q), slot = tok - q * p.c.page;
+        if ((unsigned)pg >= (unsigned)p.c.pages) return 0u;
+        if (p.heads > 1 || p.c.H_kv == 1) return key_of(__ldg(p.weights + scale_offset(p.c, pg, h, slot)));
+        uint32_t top = 0;
+        for (int g = 0; g < p.c.H_kv; ++g) top = max(top, key_of(__ldg(p.weights + scale_offset(p.c, pg, g, slot))));
+        return top;
+    };
 
     uint32_t prefix = 0;                        // of the k-th largest: its bits above `shift`
     int shift = 32;
@@ -194,9 +225,13 @@ struct KeepArgs {
     float* weights;             // may be null
     int64_t* kv_out;
     int ctas;                   // of an item
+    int page_shift;             // log2 of the page, or -1
     int lg, segs;               // log2 of the lanes of a row, and how many pieces of its a lane has (1 or 2)
     int ahead;                  // rows under way: ahead * (32 >> lg) / segs of a warp
     WsHeader* hdr;
+    __device__ __forceinline__ int page_of(int tok) const {
+        return page_shift >= 0 ? tok >> page_shift : (int)((unsigned)tok / (unsigned)c.page);
+    }
 };
 
 // How many tokens of the sequence are kept, and the token that the list and the new places count from.
@@ -214,36 +249,54 @@ __device__ __forceinline__ Kept kept_of(const KeepArgs& p, const Seq& s, int b) 
     return k;
 }
 
-__device__ __forceinline__ int page_at(const sp_cache& c, const int32_t* table, int tok, int& slot) {
-    const int q = (int)((unsigned)tok / (unsigned)c.page), pg = table[q];
-    slot = tok - q * c.page;
-    return pg >= 0 && pg < c.pages ? pg : -1;
+__device__ __forceinline__ int page_at(const KeepArgs& p, const int32_t* table, int tok, int& slot) {
+    const int q = p.page_of(tok), pg = __ldg(table + q);
+    slot = tok - q * p.c.page;
+    return (unsigned)pg < (unsigned)p.c.pages ? pg : -1;
 }
 
-// One block's check of everything that the device arrays say.
+// A cluster's check of everything that the device arrays say: its threads take the entries of all lists in turn, several of them
+// under way at once (one warp a list, an entry after the other, it took ten times as long as the moving).
 __device__ __forceinline__ void check_kept(const KeepArgs& p) {
     __shared__ int bad;
+    cg::cluster_group cluster = cg::this_cluster();
     if (threadIdx.x == 0) bad = 0;
-    __syncthreads();
+    cluster.sync();
     int mine = 0;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int64_t i = warp; i < (int64_t)p.b.B * p.heads; i += kMoveWarps) {
-        const int b = (int)(i / p.heads), h = (int)(i - (int64_t)b * p.heads);
-        const Seq s = load_seq(p.b, p.c.page, b);
-        const Kept k = kept_of(p, s, b);
-        if (!k.ok) mine = max(mine, 1);
-        const int32_t* list = p.kept + b * p.stride_seq + h * p.stride_head;
-        const int32_t *table = p.b.table + b * p.b.table_stride, *to = p.to ? p.to + b * p.to_stride : table;
-        for (int j = lane; j < k.n; j += 32) {
-            const int e = list[j], before = j ? list[j - 1] : -1;
-            int slot;
-            if (e <= before || e >= k.from) mine = max(mine, 3);
-            else if (page_at(p.c, table, k.base + e, slot) < 0 || page_at(p.c, to, k.base + j, slot) < 0) mine = max(mine, 2);
+    const int64_t lists = (int64_t)p.b.B * p.heads, step = (int64_t)cluster.num_blocks() * kMoveThreads;
+    const int64_t me = (int64_t)cluster.block_rank() * kMoveThreads + threadIdx.x;
+    for (int64_t b = me; b < p.b.B; b += step)
+        if (!kept_of(p, load_seq(p.b, p.c.page, (int)b), (int)b).ok) mine = 1;
+    constexpr int kBatch = 8;
+    for (int64_t i0 = me; i0 < lists * p.most; i0 += kBatch * step) {
+        int e[kBatch], before[kBatch], from[kBatch], pg[kBatch], pg2[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t i = i0 + u * step, l = divide(i, p.most);
+            const int b = (int)divide(l, p.heads), h = (int)(l - (int64_t)b * p.heads), j = (int)(i - l * p.most);
+            from[u] = -1;
+            if (i >= lists * p.most) continue;
+            const Seq s = load_seq(p.b, p.c.page, b);
+            const Kept k = kept_of(p, s, b);
+            if (j >= k.n) continue;
+            const int32_t* list = p.kept + b * p.stride_seq + h * p.stride_head;
+            from[u] = k.from;
+            e[u] = __ldg(list + j);
+            before[u] = j ? __ldg(list + j - 1) : -1;
+            const int32_t *table = p.b.table + b * p.b.table_stride, *to = p.to ? p.to + b * p.to_stride : table;
+            pg2[u] = __ldg(to + p.page_of(k.base + j));
+            pg[u] = e[u] >= 0 && e[u] < k.from ? __ldg(table + p.page_of(k.base + e[u])) : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (from[u] < 0) continue;
+            if (e[u] <= before[u] || e[u] >= from[u]) mine = max(mine, 3);
+            else if ((unsigned)pg[u] >= (unsigned)p.c.pages || (unsigned)pg2[u] >= (unsigned)p.c.pages) mine = max(mine, 2);
         }
     }
-    if (mine) atomicMax(&bad, mine);
-    __syncthreads();
-    if (threadIdx.x == 0) {
+    if (mine) atomicMax(cluster.map_shared_rank(&bad, 0), mine);
+    cluster.sync();
+    if (me == 0) {
         p.hdr->status = bad ? SP_EDEVICE : SP_OK;
         p.hdr->where = bad;     // 1: impossible lengths or counts, 2: a page index out of range, 3: a list that is not ascending
     }
@@ -251,12 +304,13 @@ __device__ __forceinline__ void check_kept(const KeepArgs& p) {
 
 template <typename Piece, bool kInPlace>
 __global__ void __launch_bounds__(kMoveThreads) keep_kernel(const __grid_constant__ KeepArgs p) {
-    const int item = blockIdx.x / p.ctas, r = blockIdx.x - item * p.ctas;
-    const int side = item & 1, bh = item >> 1, b = bh / p.c.H_kv, h = bh - b * p.c.H_kv;
-    if (b >= p.b.B) {
-        if (item == 2 * p.b.B * p.c.H_kv && r == 0) check_kept(p);
+    const unsigned clusters = gridDim.x / cg::this_cluster().num_blocks();
+    if (blockIdx.x / cg::this_cluster().num_blocks() == clusters - 1) {
+        check_kept(p);
         return;
     }
+    const int item = blockIdx.x / p.ctas, r = blockIdx.x - item * p.ctas;
+    const int side = item & 1, bh = item >> 1, b = bh / p.c.H_kv, h = bh - b * p.c.H_kv;
     const Seq s = load_seq(p.b, p.c.page, b);
     const Kept k = kept_of(p, s, b);
     if (h == 0 && side == 0 && r == 0 && threadIdx.x == 0) p.kv_out[b] = k.ok ? k.base + k.n : p.b.kv_len[b];
@@ -277,7 +331,7 @@ __global__ void __launch_bounds__(kMoveThreads) keep_kernel(const __grid_constan
             const int e = list[j];
             if (e >= 0 && e < k.from && (!kInPlace || e > j)) {
                 int slot, slot2;
-                const int pg = page_at(p.c, table, k.base + e, slot), pg2 = page_at(p.c, to, k.base + j, slot2);
+                const int pg = page_at(p, table, k.base + e, slot), pg2 = page_at(p, to, k.base + j, slot2);
                 if (pg >= 0 && pg2 >= 0) {
                     src = row_offset(p.c, pg, h, slot) * esize;
                     dst = row_offset(p.c, pg2, h, slot2) * esize;
@@ -334,6 +388,12 @@ sp_status launch_cluster(void (*kern)(A...), unsigned grid, int threads, int clu
     return SP_OK;
 }
 
+int page_shift_of(int page) {
+    for (int i = 0; i < 31; ++i)
+        if (page == 1 << i) return i;
+    return -1;
+}
+
 // Largest power of two that is at most x (1 .. most).
 int power_below(int64_t x, int most) {
     int c = 1;
@@ -347,7 +407,7 @@ sp_status cache_choose_launch(const sp_cache& c, const sp_batch& b, const float*
                               int64_t last, int32_t* kept, int64_t stride_seq, int64_t stride_head, int64_t* n_kept, void* ws,
                               cudaStream_t st) {
     ChooseArgs a{c, b, weights, shared ? 1 : c.H_kv, (int)budget, (int)first, (int)last, kept, stride_seq, stride_head, n_kept, 0,
-                 static_cast<WsHeader*>(ws)};
+                 page_shift_of(c.page), static_cast<WsHeader*>(ws)};
     const int64_t items = (int64_t)b.B * a.heads, tokens = std::min<int64_t>((int64_t)b.table_width * c.page, (int64_t)1 << 30);
     const int cluster = power_below(std::min<int64_t>((tokens + 2047) / 2048, std::max<int64_t>(1, 2 * sm_count() / items)), 8);
     a.held = (int)std::min<int64_t>(kMostHeld, (tokens + cluster - 1) / cluster);
@@ -360,7 +420,7 @@ sp_status cache_keep_launch(const sp_cache& c, const sp_batch& b, const int32_t*
                             int64_t stride_head, const int64_t* n_kept, int64_t most, bool drafted, const int32_t* to, int to_width,
                             int64_t to_stride, float* weights, int64_t* kv_out, void* ws, cudaStream_t st) {
     KeepArgs a{c, b, kept, heads, stride_seq, stride_head, n_kept, (int)most, drafted, to, to_width, to_stride, weights, kv_out,
-               1, 0, 1, kAhead, static_cast<WsHeader*>(ws)};
+               1, page_shift_of(c.page), 0, 1, kAhead, static_cast<WsHeader*>(ws)};
     const int bytes = c.d * (c.kind != SP_CACHE_SAME ? 1 : c.dtype == SP_BF16 ? 2 : 4);
     // the kinds of 8 bits may have rows at multiples of 8 bytes only
     const bool wide = bytes % 16 == 0 && (reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v)) % 16 == 0 &&
@@ -371,19 +431,15 @@ sp_status cache_keep_launch(const sp_cache& c, const sp_batch& b, const int32_t*
     a.ahead = std::min(kAhead, a.segs << a.lg);         // a lane has the places of one row
     const int rows_cta = kMoveWarps * (32 >> a.lg) * a.ahead / a.segs;
     const int64_t items = 2 * (int64_t)b.B * c.H_kv;
-    const int64_t useful = std::max<int64_t>(1, (most + rows_cta - 1) / rows_cta), fill = std::max<int64_t>(1, 4 * sm_count() / items);
-    if (!to) {
-        a.ctas = power_below(std::min(useful, fill), 8);
-        const unsigned grid = (unsigned)((items + 1) * a.ctas);
-        return wide ? launch_cluster(keep_kernel<uint4, true>, grid, kMoveThreads, a.ctas, 0, st, a)
-                    : launch_cluster(keep_kernel<uint2, true>, grid, kMoveThreads, a.ctas, 0, st, a);
-    }
-    a.ctas = (int)std::min(useful, fill);
-    const unsigned grid = (unsigned)((items + 1) * a.ctas);
-    if (wide) keep_kernel<uint4, false><<<grid, kMoveThreads, 0, st>>>(a);
-    else keep_kernel<uint2, false><<<grid, kMoveThreads, 0, st>>>(a);
-    SP_LAUNCH_CHECK();
-    return SP_OK;
+    const int64_t useful = std::max<int64_t>(1, (most + rows_cta - 1) / rows_cta);
+    // In place one cluster an item.  To other pages as many CTAs as there are rounds: the rows of a round are read at once, but one
+    // round follows the other.
+    const int cluster = power_below(to && (int64_t)b.B * heads * most > 4096 ? 8 : std::min<int64_t>(useful, std::max<int64_t>(1, 4 * sm_count() / items)), 8);
+    a.ctas = to ? (int)std::min<int64_t>((useful + cluster - 1) / cluster, std::max<int64_t>(1, (1 << 24) / items)) * cluster : cluster;
+    const unsigned grid = (unsigned)(items * a.ctas + cluster);
+    void (*kern)(KeepArgs) = to ? (wide ? keep_kernel<uint4, false> : keep_kernel<uint2, false>)
+                                : (wide ? keep_kernel<uint4, true> : keep_kernel<uint2, true>);
+    return launch_cluster(kern, grid, kMoveThreads, cluster, 0, st, a);
 }
 
 }  // namespace sp

@@ -26,12 +26,13 @@ __device__ __forceinline__ void check_tree(const sp_batch& b, const int32_t* par
     if (threadIdx.x == 0) bad = 0;
     __syncthreads();
     int mine = 0;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    for (int i = warp; i < b.B; i += warps) {
+    // eight lanes a sequence: the sequences' loads depend on each other, so many of them are under way
+    for (int i = threadIdx.x >> 3; i < b.B; i += kThreads / 8) {
         const Seq s = load_drafted(b, i);
         if (!s.ok) mine = max(mine, 1);
-        for (int t = lane; t < s.n; t += 32) {
-            const int u = parent[s.row0 + t];
+#pragma unroll 4
+        for (int t = threadIdx.x & 7; t < s.n; t += 8) {
+            const int u = __ldg(parent + s.row0 + t);
             if (u < -1 || u >= t) mine = 3;
         }
     }
