@@ -944,6 +944,8 @@ def _attend(q, cache, batch, seen, scale, window, out, lse, ws, stream, check):
 def _check_ints(t, name, shape, device, dtype=None):
     """An integer tensor of this shape (None: any extent) whose last axis is contiguous."""
     dtype = dtype or _torch.int32
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device.index:
+        return                  # nearly every call's: the rest takes four times as long
     if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
         want = ", ".join("*" if n is None else str(n) for n in shape)
         raise ValueError(f"{name} must be {str(dtype)[6:]} [{want}]: got {t.dtype} {list(t.shape)}")

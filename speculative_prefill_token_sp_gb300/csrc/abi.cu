@@ -8,6 +8,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <vector>
 
@@ -487,6 +488,10 @@ sp_status sp_workspace_status(const void* ws, void* stream) {
     if (e != cudaSuccess) {
         set_error("sp_workspace_status: %s", cudaGetErrorString(e));
         return SP_ECUDA;
+    }
+    if (h.status > kSpread && h.status <= kSpread + (int)(sizeof(h.aux) / sizeof(h.aux[0]))) {
+        h.where = *std::max_element(h.aux, h.aux + (h.status - kSpread));
+        h.status = h.where ? SP_EDEVICE : SP_OK;
     }
     if (h.status != SP_OK) {
         set_error("device-side status %d recorded at check %d", h.status, h.where);

@@ -1,10 +1,10 @@
 // Cutting a cache: which tokens to keep, by the weight they have gathered, and moving those to the front of their pages.
 //
 // Choosing is a selection of the k largest of a sequence's weights.  A cluster of CTAs has one (sequence, KV head), each CTA an equal
-// run of the tokens, in shared memory as integers of the same order.  Four passes over 8 bits each find the k-th largest: a histogram
-// in each CTA, added up over the cluster through distributed shared memory.  The tokens above it, and the first of
-// those that equal it, are written in order: every warp counts its run, and the counts' prefix sums say where it writes.
-// The weights are read from memory once.
+// run of the tokens, whose weights its threads hold in registers as integers of the same order.  At most four passes over 8 bits each
+// find the k-th largest: a histogram in each CTA, added up over the cluster through distributed shared memory.  The tokens above it,
+// and the first of those that equal it, are written in order: every warp counts its part of the run, and the counts' prefix
+// sums say where it writes.  The weights are read from memory once (again in each pass by a cluster that does not hold them).
 //
 // Moving reads each kept row once and writes it once.  In place a row's new slot may be another's old one.  The list is ascending, so
 // a row never moves back, and all rows of a round may be written once the rows of that round and of the ones before it have
@@ -21,9 +21,7 @@ namespace cg = cooperative_groups;
 namespace sp {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBatch = 8;                   // tokens whose weights a thread has under way
-constexpr int kMostHeld = 48 * 1024;        // tokens that a CTA holds in shared memory; more are read again in each pass
+constexpr int kThreads = 512, kWarps = kThreads / 32, kMostCtas = 8;
 
 struct ChooseArgs {
     sp_cache c;
@@ -34,28 +32,34 @@ struct ChooseArgs {
     int32_t* kept;
     int64_t stride_seq, stride_head;
     int64_t* n_kept;
-    int held;                   // keys of shared memory
-    int page_shift;             // log2 of the page, or -1
+    int skip_pages, skip_slots; // 32 tokens on: 32 / page and 32 % page
     WsHeader* hdr;
 };
 
-// What the choice goes by: integers in the order of the weights, 0 for NaN, which ranks below all of them.
+// What the choice goes by: integers in the order of the weights, 1 for NaN, which ranks below all of them, as does a token without a page
+// (0 is none of the tokens).
 __device__ __forceinline__ uint32_t key_of(float w) {
     const uint32_t u = __float_as_uint(w + 0.f);        // -0 is 0
-    if (w != w) return 0;
-    return u >> 31 ? ~u : u | 0x80000000u;
+    return w != w ? 1u : u >> 31 ? ~u : u | 0x80000000u;
 }
 
+// One more in a bin, if `there`: a branch for each of a thread's weights took longer than the counting.
+__device__ __forceinline__ void count_if(bool there, uint32_t bin) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p red.shared.add.u32 [%1], 1;\n\t}\n" ::"r"((uint32_t)there), "r"(bin)
+                 : "memory");
+}
+
+// kPer: weights that a thread holds.  Token i of a piece of the run is warp i / (32 kPer)'s, so a warp's tokens are consecutive.
+template <int kPer>
 __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant__ ChooseArgs p) {
-    extern __shared__ uint32_t held[];
-    __shared__ uint32_t hist[2][256];
-    __shared__ uint32_t found[2];               // the digit, and how many keys are above it
-    __shared__ uint32_t found_equal;
+    constexpr int kPiece = kThreads * kPer;
+    __shared__ uint32_t hist[2][256], totals[256];
+    __shared__ uint32_t found[3];               // the digit, how many keys are above it, and how many have it
     __shared__ uint2 counts[kWarps], mine_all;  // keys above the threshold and equal to it, of each warp and of the CTA
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), r = (int)cluster.block_rank();
-    const int item = blockIdx.x / C;
-    if (item == p.b.B * p.heads) {
+    const int item = (int)(blockIdx.x / C) - 1;
+    if (item < 0) {
         if (r == 0) check_tokens(p.b, p.c, 0, true, p.hdr);
         return;
     }
@@ -76,67 +80,74 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant_
     if (k == 0) return;
 
     const int all = s.kv - p.first - p.last, per = (all + C - 1) / C;
-    const int lo = min(all, r * per), m = min(all, lo + per) - lo;          // this CTA's run
+    const int lo = min(all, r * per), m = min(all, lo + per) - lo, pieces = (m + kPiece - 1) / kPiece;     // this CTA's run
     const int32_t* table = p.b.table + (int64_t)b * p.b.table_stride;
-    // The keys of tokens i, i + kThreads, ... (kBatch of them) of the run, their loads under way together: one after the other, a table
-    // entry and a weight each, they took most of the kernel's time.
-    auto load = [&](int i, uint32_t (&x)[kBatch]) {
-        int pg[kBatch], slot[kBatch];
+    uint32_t x[kPer];
+    // The keys of this thread's tokens of a piece (0 behind the run's end).  Sixteen loads of a kind are under way at once, without
+    // branches: one token after the other, a table entry and a weight each, took most of the kernel's time.
+    const int64_t per_page = (int64_t)p.c.H_kv * p.c.page;
+    const bool one = p.heads > 1 || p.c.H_kv == 1;
+    auto load = [&](int piece) {
+        constexpr int kBatch = kPer < 16 ? kPer : 16;
+        int i = piece * kPiece + warp * 32 * kPer + lane;
+        int q = (int)((unsigned)(p.first + lo + i) / (unsigned)p.c.page), slot = p.first + lo + i - q * p.c.page;
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int tok = p.first + lo + i + u * kThreads;
-            const int q = p.page_shift >= 0 ? tok >> p.page_shift : (int)((unsigned)tok / (unsigned)p.c.page);
-            pg[u] = i + u * kThreads < m ? __ldg(table + q) : -1;
-            slot[u] = tok - q * p.c.page;
-            x[u] = 0;
-        }
-        const bool one = p.heads > 1 || p.c.H_kv == 1;
-        for (int g = one ? h : 0; g < (one ? h + 1 : p.c.H_kv); ++g) {
-            float w[kBatch];
+        for (int u0 = 0; u0 < kPer; u0 += kBatch) {
+            int pg[kBatch], at[kBatch];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                w[u] = (unsigned)pg[u] < (unsigned)p.c.pages ? __ldg(p.weights + scale_offset(p.c, pg[u], g, slot[u])) : __int_as_float(0x7fffffff);
+            for (int u = 0; u < kBatch; ++u) {
+                pg[u] = __ldg(table + (i + 32 * u < m ? q : 0));
+                at[u] = slot;
+                q += p.skip_pages;
+                slot += p.skip_slots;
+                if (slot >= p.c.page) slot -= p.c.page, ++q;
+            }
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) x[u] = max(x[u], key_of(w[u]));
+            for (int u = 0; u < kBatch; ++u) {
+                if (i + 32 * u >= m || (unsigned)pg[u] >= (unsigned)p.c.pages) pg[u] = 0, at[u] = -1;       // reads another's weight
+                x[u0 + u] = i + 32 * u < m ? 1u : 0u;
+            }
+            for (int g = one ? h : 0; g < (one ? h + 1 : p.c.H_kv); ++g) {
+                const float* from = p.weights + (int64_t)g * p.c.page;
+                float w[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) w[u] = __ldg(from + (pg[u] * per_page + max(at[u], 0)));
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    if (at[u] >= 0) x[u0 + u] = max(x[u0 + u], key_of(w[u]));
+            }
+            i += 32 * kBatch;
         }
     };
-    const bool in_shared = m <= p.held;
-    if (in_shared) {
-        for (int i = threadIdx.x; i < m; i += kBatch * kThreads) {
-            uint32_t x[kBatch];
-            load(i, x);
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                if (i + u * kThreads < m) held[i + u * kThreads] = x[u];
-        }
-    }
-    auto key = [&](int i) {
-        if (in_shared) return held[i];
-        const int tok = p.first + lo + i, q = (int)((unsigned)tok / (unsigned)p.c.page), pg = __ldg(table + q), slot = tok - q * p.c.page;
-        if ((unsigned)pg >= (unsigned)p.c.pages) return 0u;
-        if (p.heads > 1 || p.c.H_kv == 1) return key_of(__ldg(p.weights + scale_offset(p.c, pg, h, slot)));
-        uint32_t top = 0;
-        for (int g = 0; g < p.c.H_kv; ++g) top = max(top, key_of(__ldg(p.weights + scale_offset(p.c, pg, g, slot))));
-        return top;
-    };
+    if (pieces == 1) load(0);
 
     uint32_t prefix = 0;                        // of the k-th largest: its bits above `shift`
     int shift = 32;
     for (int pass = 0; pass < 4; ++pass) {
-        uint32_t* mine = hist[pass & 1];
-        if (threadIdx.x < 256) mine[threadIdx.x] = 0;
+        uint32_t* bins = hist[pass & 1];
+        const uint32_t at_bins = (uint32_t)__cvta_generic_to_shared(bins);
+        if (threadIdx.x < 256) bins[threadIdx.x] = 0;
         __syncthreads();
-        for (int i = threadIdx.x; i < m; i += kThreads) {
-            const uint32_t x = key(i);
-            if (pass == 0 || x >> shift == prefix) atomicAdd(&mine[(x >> (shift - 8)) & 255], 1u);
+        for (int q = 0; q < pieces; ++q) {
+            if (pieces > 1) load(q);
+#pragma unroll
+            for (int u = 0; u < kPer; ++u)
+                count_if(pass == 0 || x[u] >> shift == prefix, at_bins + 4 * ((x[u] >> (shift - 8)) & 255));
         }
-        cluster.sync();
-        uint32_t sum = 0;
-        if (threadIdx.x < 256)
-            for (int c = 0; c < C; ++c) sum += cluster.map_shared_rank(mine, c)[threadIdx.x];
+        if (C > 1) cluster.sync();
+        else __syncthreads();
+        if (threadIdx.x < 256) {
+            uint32_t sum = 0;
+            if (C > 1) {
+                uint32_t of[kMostCtas];         // all on their way at once
+#pragma unroll
+                for (int c = 0; c < kMostCtas; ++c) of[c] = c < C ? cluster.map_shared_rank(bins, c)[threadIdx.x] : 0;
+#pragma unroll
+                for (int c = 0; c < kMostCtas; ++c) sum += of[c];
+            }
+            totals[threadIdx.x] = C > 1 ? sum : bins[threadIdx.x];
+        }
         // (the other histogram is written next, and this one again only after all have met once more)
-        __shared__ uint32_t totals[256];
-        if (threadIdx.x < 256) totals[threadIdx.x] = sum;
         __syncthreads();
         if (warp == 0) {                        // lane l: digits 255 - 8 l and the seven below it
             uint32_t of[8], sub = 0;
@@ -162,49 +173,91 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant_
                     }
                 found[0] = 255 - 8 * lane - i;
                 found[1] = above;
-                found_equal = totals[255 - 8 * lane - i];
+                found[2] = totals[255 - 8 * lane - i];
             }
         }
         __syncthreads();
         prefix = prefix << 8 | found[0];
         k -= (int)found[1];
         shift -= 8;
-        if (found_equal == (uint32_t)k) break;      // all that begin like this are kept: no need to tell them apart
+        if (found[2] == (uint32_t)k) break;         // all that begin like this are kept: no need to tell them apart
     }
 
-    // keys above the threshold are kept, and the first k that equal it; a warp has a run of its own
-    const int seg = (((m + kWarps - 1) / kWarps) + 31) & ~31, from = min(m, warp * seg), to = min(m, from + seg);
-    uint2 cnt = make_uint2(0, 0);
-    for (int i = from + lane; i - lane < to; i += 32) {
-        const uint32_t x = i < to ? key(i) >> shift : 0;
-        cnt.x += __popc(__ballot_sync(0xffffffffu, i < to && x > prefix));
-        cnt.y += __popc(__ballot_sync(0xffffffffu, i < to && x == prefix));
+    // keys above the threshold are kept, and the first k that equal it (all of them, if there are no more: then they count as above)
+    const bool alike = found[2] == (uint32_t)k;
+    const uint32_t least = alike ? prefix : prefix + 1;
+    auto flags = [&](int u, unsigned& gt, unsigned& eq) {
+        gt = __ballot_sync(0xffffffffu, x[u] >> shift >= least);
+        eq = alike ? 0 : __ballot_sync(0xffffffffu, x[u] >> shift == prefix);
+    };
+    auto count = [&] {
+        uint2 c = make_uint2(0, 0);
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            unsigned gt, eq;
+            flags(u, gt, eq);
+            c.x += __popc(gt);
+            c.y += __popc(eq);
+        }
+        return c;
+    };
+    uint2 mine = make_uint2(0, 0);              // of this warp
+    for (int q = 0; q < pieces; ++q) {
+        if (pieces > 1) load(q);
+        const uint2 c = count();
+        mine.x += c.x, mine.y += c.y;
     }
-    if (lane == 0) counts[warp] = cnt;
+    if (lane == 0) counts[warp] = mine;
     __syncthreads();
-    uint2 before = make_uint2(0, 0), total = make_uint2(0, 0);
-    for (int w = 0; w < kWarps; ++w) {
-        const uint2 c = counts[w];
-        if (w < warp) before.x += c.x, before.y += c.y;
-        total.x += c.x, total.y += c.y;
+    // of the warps before this one, and of all
+    auto scan = [&](uint2& before, uint2& total) {
+        before = total = make_uint2(0, 0);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const uint2 c = counts[w];
+            if (w < warp) before.x += c.x, before.y += c.y;
+            total.x += c.x, total.y += c.y;
+        }
+    };
+    uint2 before, total, base = make_uint2(0, 0);
+    scan(before, total);
+    if (C > 1) {
+        if (threadIdx.x == 0) mine_all = total;
+        cluster.sync();
+        if (lane < r) base = *cluster.map_shared_rank(&mine_all, lane);
+#pragma unroll
+        for (int o = kMostCtas / 2; o; o >>= 1) {
+            base.x += __shfl_xor_sync(0xffffffffu, base.x, o);
+            base.y += __shfl_xor_sync(0xffffffffu, base.y, o);
+        }
+        base.x = __shfl_sync(0xffffffffu, base.x, 0);
+        base.y = __shfl_sync(0xffffffffu, base.y, 0);
+        cluster.barrier_arrive();       // (waited for at the end: no CTA leaves while another reads its counts)
     }
-    if (threadIdx.x == 0) mine_all = total;
-    cluster.sync();
-    for (int c = 0; c < r; ++c) {
-        const uint2 o = *cluster.map_shared_rank(&mine_all, c);
-        before.x += o.x, before.y += o.y;
-    }
-    for (int i = from + lane; i - lane < to; i += 32) {
-        const uint32_t x = i < to ? key(i) >> shift : 0;
-        const unsigned gt = __ballot_sync(0xffffffffu, i < to && x > prefix), eq = __ballot_sync(0xffffffffu, i < to && x == prefix);
+    for (int q = 0; q < pieces; ++q) {
+        if (pieces > 1) {                       // one piece after the other
+            load(q);
+            const uint2 c = count();
+            __syncthreads();
+            if (lane == 0) counts[warp] = c;
+            __syncthreads();
+            scan(before, total);
+        }
+        uint32_t above = base.x + before.x, equal = base.y + before.y;
         const unsigned below = (1u << lane) - 1;
-        const uint32_t eq_rank = before.y + __popc(eq & below);
-        if ((gt >> lane & 1) || ((eq >> lane & 1) && eq_rank < (uint32_t)k))
-            kept[p.first + before.x + __popc(gt & below) + min(eq_rank, (uint32_t)k)] = p.first + lo + i;
-        before.x += __popc(gt);
-        before.y += __popc(eq);
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            unsigned gt, eq;
+            flags(u, gt, eq);
+            const uint32_t rank = equal + __popc(eq & below);
+            if ((gt >> lane & 1) || ((eq >> lane & 1) && rank < (uint32_t)k))
+                kept[p.first + above + __popc(gt & below) + min(rank, (uint32_t)k)] = p.first + lo + q * kPiece + warp * 32 * kPer + 32 * u + lane;
+            above += __popc(gt);
+            equal += __popc(eq);
+        }
+        base.x += total.x, base.y += total.y;
     }
-    cluster.sync();             // no CTA leaves while another reads its counts
+    if (C > 1) cluster.barrier_wait();
 }
 
 constexpr int kMoveThreads = 256, kMoveWarps = kMoveThreads / 32;
@@ -224,7 +277,9 @@ struct KeepArgs {
     int64_t to_stride;
     float* weights;             // may be null
     int64_t* kv_out;
+    int pairs;                  // (head, side) pairs of an item
     int ctas;                   // of an item
+    int checkers;               // CTAs in front of the others that check the lists
     int page_shift;             // log2 of the page, or -1
     int lg, segs;               // log2 of the lanes of a row, and how many pieces of its a lane has (1 or 2)
     int ahead;                  // rows under way: ahead * (32 >> lg) / segs of a warp
@@ -255,19 +310,16 @@ __device__ __forceinline__ int page_at(const KeepArgs& p, const int32_t* table, 
     return (unsigned)pg < (unsigned)p.c.pages ? pg : -1;
 }
 
-// A cluster's check of everything that the device arrays say: its threads take the entries of all lists in turn, several of them
-// under way at once (one warp a list, an entry after the other, it took ten times as long as the moving).
+// The check of everything that the device arrays say, by the first CTAs, each of which records what it found: threads take the entries
+// of all lists in turn, several of them under way at once.  (One CTA took 20 us for 64 lists of 1024 to 8192 entries, longer than the moving.)
+constexpr int kMostCheckers = 48;
 __device__ __forceinline__ void check_kept(const KeepArgs& p) {
-    __shared__ int bad;
-    cg::cluster_group cluster = cg::this_cluster();
-    if (threadIdx.x == 0) bad = 0;
-    cluster.sync();
     int mine = 0;
-    const int64_t lists = (int64_t)p.b.B * p.heads, step = (int64_t)cluster.num_blocks() * kMoveThreads;
-    const int64_t me = (int64_t)cluster.block_rank() * kMoveThreads + threadIdx.x;
+    const int64_t lists = (int64_t)p.b.B * p.heads, step = (int64_t)p.checkers * kMoveThreads;
+    const int64_t me = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x;
     for (int64_t b = me; b < p.b.B; b += step)
         if (!kept_of(p, load_seq(p.b, p.c.page, (int)b), (int)b).ok) mine = 1;
-    constexpr int kBatch = 8;
+    constexpr int kBatch = 4;
     for (int64_t i0 = me; i0 < lists * p.most; i0 += kBatch * step) {
         int e[kBatch], before[kBatch], from[kBatch], pg[kBatch], pg2[kBatch];
 #pragma unroll
@@ -294,49 +346,51 @@ __device__ __forceinline__ void check_kept(const KeepArgs& p) {
             else if ((unsigned)pg[u] >= (unsigned)p.c.pages || (unsigned)pg2[u] >= (unsigned)p.c.pages) mine = max(mine, 2);
         }
     }
-    if (mine) atomicMax(cluster.map_shared_rank(&bad, 0), mine);
-    cluster.sync();
-    if (me == 0) {
-        p.hdr->status = bad ? SP_EDEVICE : SP_OK;
-        p.hdr->where = bad;     // 1: impossible lengths or counts, 2: a page index out of range, 3: a list that is not ascending
+    // 1: impossible lengths or counts, 2: a page index out of range, 3: a list that is not ascending
+    const bool three = __syncthreads_or(mine == 3), two = __syncthreads_or(mine == 2), one = __syncthreads_or(mine == 1);
+    if (threadIdx.x == 0) {
+        p.hdr->aux[blockIdx.x] = three ? 3 : two ? 2 : one ? 1 : 0;
+        if (blockIdx.x == 0) p.hdr->status = kSpread + p.checkers;
     }
 }
 
 template <typename Piece, bool kInPlace>
 __global__ void __launch_bounds__(kMoveThreads) keep_kernel(const __grid_constant__ KeepArgs p) {
-    const unsigned clusters = gridDim.x / cg::this_cluster().num_blocks();
-    if (blockIdx.x / cg::this_cluster().num_blocks() == clusters - 1) {
+    if (blockIdx.x < p.checkers) {
         check_kept(p);
         return;
     }
-    const int item = blockIdx.x / p.ctas, r = blockIdx.x - item * p.ctas;
-    const int side = item & 1, bh = item >> 1, b = bh / p.c.H_kv, h = bh - b * p.c.H_kv;
+    const int cta = blockIdx.x - p.checkers, item = cta / p.ctas, r = cta - item * p.ctas;
+    const int per_seq = (2 * p.c.H_kv + p.pairs - 1) / p.pairs, b = item / per_seq, first = (item - b * per_seq) * p.pairs;
     const Seq s = load_seq(p.b, p.c.page, b);
     const Kept k = kept_of(p, s, b);
-    if (h == 0 && side == 0 && r == 0 && threadIdx.x == 0) p.kv_out[b] = k.ok ? k.base + k.n : p.b.kv_len[b];
+    if (first == 0 && r == 0 && threadIdx.x == 0) p.kv_out[b] = k.ok ? k.base + k.n : p.b.kv_len[b];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & ((1 << p.lg) - 1), grp = lane >> p.lg;
     const int rows_at_once = 32 >> p.lg, rows_w = rows_at_once * p.ahead / p.segs, rows_cta = kMoveWarps * rows_w;
     const int esize = p.c.kind == SP_CACHE_SAME ? (p.c.dtype == SP_BF16 ? 2 : 4) : 1, pieces = p.c.d * esize / (int)sizeof(Piece);
-    char* data = static_cast<char*>(side ? p.c.v : p.c.k);
-    float* scales = p.c.kind == SP_CACHE_SAME ? nullptr : side ? p.c.v_scale : p.c.k_scale;
-    float* weights = side ? nullptr : p.weights;
-    const int32_t* list = p.kept + b * p.stride_seq + (p.heads > 1 ? h : 0) * p.stride_head;
     const int32_t *table = p.b.table + b * p.b.table_stride, *to = p.to ? p.to + b * p.to_stride : table;
-
-    for (int j0 = 0; j0 < k.n; j0 += p.ctas * rows_cta) {
+    // the item's rows, pair after pair (more than one pair only where their rows are few)
+    const int rows = min(p.pairs, 2 * p.c.H_kv - first) * k.n;
+    for (int j0 = 0; j0 < rows; j0 += p.ctas * rows_cta) {
         // this lane's row of the warp's: where it is and where it goes
-        const int j = j0 + (r * kMoveWarps + warp) * rows_w + lane;
-        int64_t src = -1, dst = -1, src_s = 0, dst_s = 0;
-        if (lane < rows_w && j < k.n) {
-            const int e = list[j];
+        const int row = j0 + (r * kMoveWarps + warp) * rows_w + lane;
+        char *src = nullptr, *dst = nullptr;
+        float *scales = nullptr, *weights = nullptr;
+        int64_t src_s = 0, dst_s = 0;
+        if (lane < rows_w && row < rows) {
+            const int pair = p.pairs > 1 ? row / k.n : 0, j = row - pair * k.n, side = (first + pair) & 1, h = (first + pair) >> 1;
+            const int e = __ldg(p.kept + b * p.stride_seq + (p.heads > 1 ? h : 0) * p.stride_head + j);
             if (e >= 0 && e < k.from && (!kInPlace || e > j)) {
                 int slot, slot2;
                 const int pg = page_at(p, table, k.base + e, slot), pg2 = page_at(p, to, k.base + j, slot2);
                 if (pg >= 0 && pg2 >= 0) {
-                    src = row_offset(p.c, pg, h, slot) * esize;
-                    dst = row_offset(p.c, pg2, h, slot2) * esize;
+                    char* data = static_cast<char*>(side ? p.c.v : p.c.k);
+                    src = data + row_offset(p.c, pg, h, slot) * esize;
+                    dst = data + row_offset(p.c, pg2, h, slot2) * esize;
                     src_s = scale_offset(p.c, pg, h, slot);
                     dst_s = scale_offset(p.c, pg2, h, slot2);
+                    if (p.c.kind != SP_CACHE_SAME) scales = side ? p.c.v_scale : p.c.k_scale;
+                    if (!side) weights = p.weights;
                 }
             }
         }
@@ -345,28 +399,24 @@ __global__ void __launch_bounds__(kMoveThreads) keep_kernel(const __grid_constan
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (u < p.ahead) {
-                const int q = u * rows_at_once + grp, row = p.segs == 2 ? q >> 1 : q, piece = sub + (p.segs == 2 ? (q & 1) << p.lg : 0);
-                const int64_t at = __shfl_sync(0xffffffffu, src, row);
-                if (at >= 0 && piece < pieces) x[u] = *reinterpret_cast<const Piece*>(data + at + piece * sizeof(Piece));
+                const int q = u * rows_at_once + grp, of = p.segs == 2 ? q >> 1 : q, piece = sub + (p.segs == 2 ? (q & 1) << p.lg : 0);
+                const char* at = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), of));
+                if (at && piece < pieces) x[u] = *reinterpret_cast<const Piece*>(at + piece * sizeof(Piece));
             }
         }
-        if (src >= 0) {
-            if (scales) scale = scales[src_s];
-            if (weights) weight = weights[src_s];
-        }
+        if (scales) scale = scales[src_s];
+        if (weights) weight = weights[src_s];
         if (kInPlace) cg::this_cluster().sync();
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (u < p.ahead) {
-                const int q = u * rows_at_once + grp, row = p.segs == 2 ? q >> 1 : q, piece = sub + (p.segs == 2 ? (q & 1) << p.lg : 0);
-                const int64_t at = __shfl_sync(0xffffffffu, dst, row);
-                if (at >= 0 && piece < pieces) *reinterpret_cast<Piece*>(data + at + piece * sizeof(Piece)) = x[u];
+                const int q = u * rows_at_once + grp, of = p.segs == 2 ? q >> 1 : q, piece = sub + (p.segs == 2 ? (q & 1) << p.lg : 0);
+                char* at = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), of));
+                if (at && piece < pieces) *reinterpret_cast<Piece*>(at + piece * sizeof(Piece)) = x[u];
             }
         }
-        if (src >= 0) {
-            if (scales) scales[dst_s] = scale;
-            if (weights) weights[dst_s] = weight;
-        }
+        if (scales) scales[dst_s] = scale;
+        if (weights) weights[dst_s] = weight;
     }
 }
 
@@ -406,21 +456,21 @@ int power_below(int64_t x, int most) {
 sp_status cache_choose_launch(const sp_cache& c, const sp_batch& b, const float* weights, bool shared, int64_t budget, int64_t first,
                               int64_t last, int32_t* kept, int64_t stride_seq, int64_t stride_head, int64_t* n_kept, void* ws,
                               cudaStream_t st) {
-    ChooseArgs a{c, b, weights, shared ? 1 : c.H_kv, (int)budget, (int)first, (int)last, kept, stride_seq, stride_head, n_kept, 0,
-                 page_shift_of(c.page), static_cast<WsHeader*>(ws)};
+    ChooseArgs a{c, b, weights, shared ? 1 : c.H_kv, (int)budget, (int)first, (int)last, kept, stride_seq, stride_head, n_kept,
+                 32 / c.page, 32 % c.page, static_cast<WsHeader*>(ws)};
     const int64_t items = (int64_t)b.B * a.heads, tokens = std::min<int64_t>((int64_t)b.table_width * c.page, (int64_t)1 << 30);
-    const int cluster = power_below(std::min<int64_t>((tokens + 2047) / 2048, std::max<int64_t>(1, 2 * sm_count() / items)), 8);
-    a.held = (int)std::min<int64_t>(kMostHeld, (tokens + cluster - 1) / cluster);
-    const size_t smem = (size_t)a.held * 4;
-    SP_CUDA_TRY(cudaFuncSetAttribute(choose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld * 4));
-    return launch_cluster(choose_kernel, (unsigned)((items + 1) * cluster), kThreads, cluster, smem, st, a);
+    // (clusters of 16, of which the GPU does not hold eight at a time: 30 us for 20.5, eight lists of 131072)
+    const int cluster = power_below(std::min<int64_t>((tokens + 2047) / 2048, std::max<int64_t>(1, 2 * sm_count() / items)), kMostCtas);
+    void (*kern)(ChooseArgs) = tokens <= (int64_t)cluster * kThreads * 8 ? choose_kernel<8>
+                               : tokens <= (int64_t)cluster * kThreads * 16 ? choose_kernel<16> : choose_kernel<32>;
+    return launch_cluster(kern, (unsigned)((items + 1) * cluster), kThreads, cluster, 0, st, a);
 }
 
 sp_status cache_keep_launch(const sp_cache& c, const sp_batch& b, const int32_t* kept, int heads, int64_t stride_seq,
                             int64_t stride_head, const int64_t* n_kept, int64_t most, bool drafted, const int32_t* to, int to_width,
                             int64_t to_stride, float* weights, int64_t* kv_out, void* ws, cudaStream_t st) {
     KeepArgs a{c, b, kept, heads, stride_seq, stride_head, n_kept, (int)most, drafted, to, to_width, to_stride, weights, kv_out,
-               1, page_shift_of(c.page), 0, 1, kAhead, static_cast<WsHeader*>(ws)};
+               1, 1, 1, page_shift_of(c.page), 0, 1, kAhead, static_cast<WsHeader*>(ws)};
     const int bytes = c.d * (c.kind != SP_CACHE_SAME ? 1 : c.dtype == SP_BF16 ? 2 : 4);
     // the kinds of 8 bits may have rows at multiples of 8 bytes only
     const bool wide = bytes % 16 == 0 && (reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v)) % 16 == 0 &&
@@ -430,16 +480,18 @@ sp_status cache_keep_launch(const sp_cache& c, const sp_batch& b, const int32_t*
     a.segs = pieces > 32 ? 2 : 1;
     a.ahead = std::min(kAhead, a.segs << a.lg);         // a lane has the places of one row
     const int rows_cta = kMoveWarps * (32 >> a.lg) * a.ahead / a.segs;
-    const int64_t items = 2 * (int64_t)b.B * c.H_kv;
-    const int64_t useful = std::max<int64_t>(1, (most + rows_cta - 1) / rows_cta);
+    // short lists share a CTA, as long as the rows of all fit into a round
+    a.pairs = (int)std::min<int64_t>(2 * c.H_kv, std::max<int64_t>(1, rows_cta / std::max<int64_t>(1, most)));
+    const int64_t items = (int64_t)b.B * ((2 * c.H_kv + a.pairs - 1) / a.pairs), useful = std::max<int64_t>(1, (most + rows_cta - 1) / rows_cta);
     // In place one cluster an item.  To other pages as many CTAs as there are rounds: the rows of a round are read at once, but one
     // round follows the other.
-    const int cluster = power_below(to && (int64_t)b.B * heads * most > 4096 ? 8 : std::min<int64_t>(useful, std::max<int64_t>(1, 4 * sm_count() / items)), 8);
-    a.ctas = to ? (int)std::min<int64_t>((useful + cluster - 1) / cluster, std::max<int64_t>(1, (1 << 24) / items)) * cluster : cluster;
-    const unsigned grid = (unsigned)(items * a.ctas + cluster);
+    const int cluster = to ? 1 : power_below(std::min<int64_t>(useful, std::max<int64_t>(1, 4 * sm_count() / items)), 8);
+    a.ctas = to ? (int)std::min<int64_t>(useful, std::max<int64_t>(1, (1 << 28) / items)) : cluster;
+    const int64_t entries = (int64_t)b.B * heads * most;
+    a.checkers = (int)std::min<int64_t>(kMostCheckers, (entries + 4 * kMoveThreads - 1) / (4 * kMoveThreads) + cluster) / cluster * cluster;
     void (*kern)(KeepArgs) = to ? (wide ? keep_kernel<uint4, false> : keep_kernel<uint2, false>)
                                 : (wide ? keep_kernel<uint4, true> : keep_kernel<uint2, true>);
-    return launch_cluster(kern, grid, kMoveThreads, cluster, 0, st, a);
+    return launch_cluster(kern, (unsigned)(items * a.ctas + a.checkers), kMoveThreads, cluster, 0, st, a);
 }
 
 }  // namespace sp

@@ -18,6 +18,8 @@ struct WsHeader {
     int32_t aux[62];
 };
 static_assert(sizeof(WsHeader) == 256, "workspace header is 256 bytes");
+// A status of kSpread + n: n CTAs have each written what they found to aux[i] (0: nothing), and sp_workspace_status puts it together.
+constexpr int kSpread = 0x100;
 
 constexpr size_t kAlign = 256;
 inline size_t align_up(size_t x, size_t a = kAlign) { return (x + a - 1) / a * a; }
