@@ -29,6 +29,7 @@ size_t attend_tc_ws_bytes(const sp_cache& c);
 sp_status attend_tc_launch(const AttendProblem& p, int min_rows, void* ws, size_t offset, cudaStream_t st);
 // Implemented in weights_*.cu, tree.cu and evict.cu.
 sp_status weights_general_launch(const WeightsProblem& w, void* ws, cudaStream_t st);
+sp_status weights_step_launch(const WeightsProblem& w, void* ws, cudaStream_t st);
 bool weights_tc_supported(const sp_cache& c, const sp_batch& b, int G);
 size_t weights_tc_ws_bytes();
 sp_status weights_tc_launch(const WeightsProblem& w, void* ws, cudaStream_t st);
@@ -151,8 +152,12 @@ size_t path_bytes(Path path, const sp_cache& c) {
     }
 }
 
-// Which kernel sp_attend_weights takes.
-bool weights_on_tc(const sp_cache& c, const sp_batch& b, int H) { return b.T > 0 && weights_tc_supported(c, b, H / c.H_kv); }
+// Which kernel sp_attend_weights takes: as sp_attend, but a mixed batch goes to the tensor cores' kernel as a whole.
+Path weights_path(const sp_cache& c, const sp_batch& b, int H) {
+    const Path path = path_of(c, b, H);
+    if (path == kGeneral || path == kStep) return path;
+    return weights_tc_supported(c, b, H / c.H_kv) ? kChunks : kGeneral;
+}
 
 // Pages, heads and slots of a cache that is written lie apart.
 sp_status check_no_overlap(const char* fn, const sp_cache* c) {
@@ -555,7 +560,7 @@ sp_status sp_tree_accept(const sp_batch* batch, const int32_t* parent, const int
 size_t sp_attend_weights_workspace_size(const sp_cache* cache, const sp_batch* batch, int H) {
     const char* fn = "sp_attend_weights_workspace_size";
     if (check_cache(fn, cache) != SP_OK || check_batch_args(fn, batch) != SP_OK || check_heads(fn, cache, H) != SP_OK) return 0;
-    return weights_on_tc(*cache, *batch, H) ? weights_tc_ws_bytes() : sizeof(WsHeader);
+    return weights_path(*cache, *batch, H) == kChunks ? weights_tc_ws_bytes() : sizeof(WsHeader);
 }
 
 sp_status sp_attend_weights(const sp_rows* q, const sp_cache* cache, const sp_batch* batch, int H, double scale, int64_t window,
@@ -584,7 +589,11 @@ sp_status sp_attend_weights(const sp_rows* q, const sp_cache* cache, const sp_ba
     a.lse_stride_head = lse_stride_head;
     const WeightsProblem w{a, (float)decay, weights};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    s = weights_on_tc(*cache, *batch, H) ? weights_tc_launch(w, ws, st) : weights_general_launch(w, ws, st);
+    switch (weights_path(*cache, *batch, H)) {
+        case kStep: s = weights_step_launch(w, ws, st); break;
+        case kChunks: s = weights_tc_launch(w, ws, st); break;
+        default: s = weights_general_launch(w, ws, st); break;
+    }
     if (s == SP_OK) clear_error();
     return s;
 }
