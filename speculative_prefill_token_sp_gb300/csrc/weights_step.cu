@@ -3,8 +3,8 @@
 //
 //   w[i] = decay * w[i] + sum over the rows that see token i of 2^(f q . k_i - l),  f = scale * log2(e), l = lse * log2(e)
 //
-// The work is bound by the keys' bytes, each read once.  Each warp copies the rows of its next pieces (32 tokens, 64 where a row has at
-// most 128 bytes), their scales and the weights that are there into its own ring in shared memory with cp.async while it works
+// The work is bound by the keys' bytes, each read once.  Each warp copies the rows of its next pieces (32 tokens), their
+// scales and the weights that are there into its own ring in shared memory with cp.async while it works
 // on the piece before, with no barrier with another warp.  The products are mma.sync, transposed (S^T = K Q^T): the tokens
 // are the long side, the query rows (8 a tile) the narrow one, and a token's weights lie in four neighbouring lanes.  The order of
 // the entries of a head is chosen such that a lane's operand registers are 16 consecutive bytes of a row.
@@ -24,10 +24,10 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 template <int D, int kKind>
 struct Ring {
     static constexpr int kRow = D * (kKind == SP_CACHE_SAME ? 2 : 1), kPitch = kRow + 16;
-    static constexpr int kTok = kRow > 128 ? 32 : 64, kUnit = kWarps * kTok;
+    static constexpr int kTok = 32, kUnit = kWarps * kTok;
     static constexpr int kAt = kTok * kPitch, kOld = kAt + 8 * kTok, kScale = kOld + 4 * kTok;
     static constexpr int kStage = kScale + (kKind == SP_CACHE_SAME ? 0 : 4 * kTok);
-    static constexpr int kStages = 3;
+    static constexpr int kStages = 2;
     static constexpr int kSmem = kWarps * kStages * kStage;
     static constexpr int kMost = 227 * 1024 / (kSmem + 1024), kCtas = kMost < 4 ? kMost : 4;        // resident on an SM
 };
