@@ -150,8 +150,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// A tensor map of bf16 rows; strides in entries.  An extent of 1 has no stride of its own.
-sp_status encode(CUtensorMap* map, const void* data, int rank, const int64_t* extent, const int64_t* stride, const int* box) {
+// A tensor map of rows of bf16, or of codes as they lie; strides in entries.  An extent of 1 has no stride of its own.
+sp_status encode(CUtensorMap* map, const void* data, int rank, const int64_t* extent, const int64_t* stride, const int* box,
+                 bool codes = false) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
     if (!enc) {
         set_error("cuTensorMapEncodeTiled is unavailable from the driver");
@@ -162,10 +163,10 @@ sp_status encode(CUtensorMap* map, const void* data, int rank, const int64_t* ex
     for (int i = 0; i < rank; ++i) {
         dim[i] = (cuuint64_t)extent[i];
         bx[i] = (cuuint32_t)box[i];
-        if (i) step[i - 1] = extent[i] == 1 ? 16 : (cuuint64_t)stride[i] * 2;
+        if (i) step[i - 1] = extent[i] == 1 ? 16 : (cuuint64_t)stride[i] * (codes ? 1 : 2);
     }
-    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(data), dim, step, bx, one,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const CUresult r = enc(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(data), dim, step, bx, one,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         set_error("cuTensorMapEncodeTiled failed (%d)", (int)r);

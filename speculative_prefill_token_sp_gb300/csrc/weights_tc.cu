@@ -35,12 +35,15 @@ constexpr int kSmem = 227 * 1024;
 constexpr int kExtra = 1;               // what an item costs beside its row tiles, in row tiles
 constexpr int kMaxSeqs = 16384;         // their item counts are laid out in the (still empty) rings
 
+// Warps of a CTA by role.  setmaxnreg shares out the registers that the block was launched with: 384 threads of 168, or 640 of 96.
 template <int kKind>
 struct Roles {
     static constexpr bool kSame = kKind == SP_CACHE_SAME;
-    static constexpr int kHalves = kSame ? 2 : 1;               // threads that share a key
-    static constexpr int kAdd = 8 * kHalves, kMma = kAdd + (kSame ? 0 : 8), kTma = kMma + 1, kLse = kMma + 2;
+    static constexpr int kAdd = 8, kMma = kAdd + (kSame ? 0 : 8), kTma = kMma + 1, kLse = kMma + 2;
     static constexpr int kThreads = 32 * (kMma + 4);
+    static constexpr int kAddRegs = kSame ? 216 : 136, kConvertRegs = 80, kSingleRegs = kSame ? 72 : 48;
+    static_assert(kAdd * kAddRegs + (kMma - kAdd) * kConvertRegs + 4 * kSingleRegs <= (kMma + 4) * (kSame ? 168 : 96),
+                  "the roles' registers");
 };
 
 struct Cut {
@@ -53,6 +56,7 @@ struct TcArgs {
     int G, tpt;             // query heads of a KV head; new tokens of a row tile
     int P;                  // CTAs
     int box;                // rows of a TMA box
+    int k_stages, q_stages; // of the rings
     WsHeader* hdr;
     int* err;               // [P]: 1 impossible lengths, 2 a page index out of range, 4 a wait that gave up (in bits 8-15)
     Cut* cuts;              // [P]
@@ -209,51 +213,69 @@ __device__ __forceinline__ void plan(const TcArgs& p, int* starts, int64_t* sums
     __syncthreads();
 }
 
-template <int D>
+// Shared memory: rings of key tiles, of row tiles and, of an 8-bit cache, of tiles of codes in what is left of 224 KB; then the
+// normalisers beside S, what the halves of the adding warps exchange, and the barriers.
+template <int D, int kKind>
 struct Layout {
     static constexpr int kChunks = D / 64;
-    static constexpr int kTileBytes = kKeys * D * 2;            // a tile of K or Q
-    static constexpr int kKs = D == 128 ? 4 : 8, kQs = D == 128 ? 3 : 5;
-    static constexpr int kK = 0, kQ = kKs * kTileBytes, kL = kQ + kQs * kTileBytes, kHalf = kL + kQs * 128 * 4,
-                         kBars = kHalf + kBlock * 4;
-    static constexpr int kBarCount = 2 * kKs + 4 * kQs + 8 + 4 + 1;
+    static constexpr int kTileBytes = kKeys * D * 2, kCodeBytes = kKeys * D;       // a tile of K or Q; of codes
+    static constexpr int kRings = 224 * 1024, kTiles = kRings / kTileBytes;
+    static constexpr int kL = kRings, kHalf = kL + 2 * 128 * 4, kBars = kHalf + kBlock * 4;
+    static constexpr int kMostStages = kKind == SP_CACHE_SAME ? kTiles : 2 * kTiles;        // of all rings together
+    static constexpr int kBarCount = 2 * kMostStages + 4 + 4 + 1;
     static constexpr int kBad = kBars + 8 * (kBarCount + 1), kEnd = kBad + 8 + (int)sizeof(Walk);
     static_assert(kEnd <= kSmem, "");
-    static_assert(kL >= 4 * (kMaxSeqs + 2) + 8 * 32, "the plan's scratch");
-    static constexpr int kS(int w, int buf) { return (2 * w + buf) * 128; }     // TMEM columns
+    static_assert(kRings >= 4 * (kMaxSeqs + 2) + 8 * 32, "the plan's scratch");
+    static constexpr int kS(int w, int buf) { return (2 * buf + w) * 128; }         // TMEM columns
 };
 
-// 32 logits of a key's to weights 2^(f v - l) (nl = -l, of each column), those of the rows that see it added to zs.  (What is hidden
-// is taken out last: a column of no row holds anything, and f is 0 or NaN where a row's scale is.)
-template <bool kMasked>
-__device__ __forceinline__ void add_weights32(const float* v, float f, const float* nl, uint32_t seen, float (&zs)[4]) {
+// (a, b) = (x, y) * (f, f) + (n, m), two fp32 at once
+__device__ __forceinline__ void fma2n(float& a, float& b, float x, float y, float f, float n, float m) {
+    asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %4};\n\tmov.b64 w, {%5, %6};\n\t"
+        "fma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "=f"(a), "=f"(b) : "f"(x), "f"(y), "f"(f), "f"(n), "f"(m));
+}
+
+// kCols logits each of two keys to weights 2^(f v - l) (nl = -l, of each column), those of the rows that see them added to za and zb.
+// (What is hidden is taken out last: a column of no row holds anything, and f is 0 or NaN where a row's scale is.)
+template <bool kMasked, int kCols>
+__device__ __forceinline__ void add_weights(const float* va, const float* vb, float fa, float fb, const float* nl, uint32_t sees_a,
+                                            uint32_t sees_b, float (&za)[4], float (&zb)[4]) {
 #pragma unroll
-    for (int c = 0; c < 32; c += 16) {
-        float x[16];
+    for (int c = 0; c < kCols; c += 16) {
+        float n[16], xa[16], xb[16];
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-            const float4 n = *reinterpret_cast<const float4*>(nl + c + i);
-            x[i] = n.x, x[i + 1] = n.y, x[i + 2] = n.z, x[i + 3] = n.w;
+            const float4 x = *reinterpret_cast<const float4*>(nl + c + i);
+            n[i] = x.x, n[i + 1] = x.y, n[i + 2] = x.z, n[i + 3] = x.w;
         }
 #pragma unroll
-        for (int i = 0; i < 16; i += 2)
-            asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 w, {%4, %4};\n\t"
-                "fma.rn.f32x2 u, v, w, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
-                : "+f"(x[i]), "+f"(x[i + 1]) : "f"(v[c + i]), "f"(v[c + i + 1]), "f"(f));
+        for (int i = 0; i < 16; i += 2) {
+            fma2n(xa[i], xa[i + 1], va[c + i], va[c + i + 1], fa, n[i], n[i + 1]);
+            fma2n(xb[i], xb[i + 1], vb[c + i], vb[c + i + 1], fb, n[i], n[i + 1]);
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            x[i] = ex2_approx(x[i]);
-            if (kMasked && !(seen >> (c + i) & 1)) x[i] = 0.f;
+            xa[i] = ex2_approx(xa[i]);
+            if (kMasked && !(sees_a >> (c + i) & 1)) xa[i] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) add2(zs[i & 2], zs[(i & 2) + 1], x[i], x[i + 1]);
+        for (int i = 0; i < 16; ++i) {
+            xb[i] = ex2_approx(xb[i]);
+            if (kMasked && !(sees_b >> (c + i) & 1)) xb[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            add2(za[i & 2], za[(i & 2) + 1], xa[i], xa[i + 1]);
+            add2(zb[i & 2], zb[(i & 2) + 1], xb[i], xb[i + 1]);
+        }
     }
 }
 
 template <int D, int kKind>
 __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(const __grid_constant__ Maps maps,
                                                                  const __grid_constant__ TcArgs p) {
-    using L = Layout<D>;
+    using L = Layout<D, kKind>;
     using W = Roles<kKind>;
     constexpr bool kSame = W::kSame;
     extern __shared__ __align__(1024) uint8_t raw[];
@@ -263,46 +285,43 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
         return;
     }
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
-    uint64_t* k_full = bars;                    // [kKs] a key tile is ready
-    uint64_t* k_empty = k_full + L::kKs;        // the MMAs have read it
-    uint64_t* q_full = k_empty + L::kKs;        // [kQs] a row tile
-    uint64_t* q_empty = q_full + L::kQs;
-    uint64_t* l_full = q_empty + L::kQs;        // [kQs] its normalisers
-    uint64_t* l_empty = l_full + L::kQs;
-    uint64_t* s_full = l_empty + L::kQs;        // [2][2] S of key tile A or B, buffer 0 or 1
-    uint64_t* s_empty = s_full + 4;
-    uint64_t* h_full = s_empty + 4;             // [2] the second half's sums of key tile A or B are there
-    uint64_t* h_empty = h_full + 2;
-    uint64_t* final_bar = h_empty + 2;
+    const int ks = p.k_stages, qs = p.q_stages, rs = kSame ? 0 : (L::kTiles - ks - qs) * 2;
+    uint64_t* k_full = bars;                    // [ks] a key tile is ready
+    uint64_t* q_full = k_full + ks;             // [qs] a row tile
+    uint64_t* r_full = q_full + qs;             // [rs] a tile of codes
+    uint64_t* k_empty = bars + L::kMostStages;  // the MMAs have read it
+    uint64_t* q_empty = k_empty + ks;
+    uint64_t* r_empty = q_empty + qs;           // it is converted
+    uint64_t* s_full = bars + 2 * L::kMostStages;       // [2] S of both key tiles, and the rows' normalisers, in buffer 0 or 1
+    uint64_t* s_empty = s_full + 2;
+    uint64_t* x_full = s_empty + 2;             // [2] the sums of key tile A or B that the other half has are there
+    uint64_t* x_empty = x_full + 2;
+    uint64_t* final_bar = x_empty + 2;
+    uint8_t *k_ring = smem, *q_ring = smem + ks * L::kTileBytes, *r_ring = q_ring + qs * L::kTileBytes;
     volatile uint32_t* tmem_sh = reinterpret_cast<volatile uint32_t*>(final_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_sh + 1);
     int* bad = reinterpret_cast<int*>(smem + L::kBad);                          // [2] impossible lengths; a page index out of range
     Walk* start = reinterpret_cast<Walk*>(bad + 2);
-    float* ls = reinterpret_cast<float*>(smem + L::kL);                         // [kQs][128] -l
-    float* halves = reinterpret_cast<float*>(smem + L::kHalf);                  // [2][128] the second half's sums of A and B
+    float* ls = reinterpret_cast<float*>(smem + L::kL);                         // [2][128] -l
+    float* halves = reinterpret_cast<float*>(smem + L::kHalf);                  // [2][128] tile A's sums of the second half, tile B's of the first
 
     const AttendProblem& a = p.w.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 32) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.q)) : "memory");
-        if (kSame) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < L::kKs; ++i) {
-            mbar_init(smem_u32(&k_full[i]), kSame ? 1 : 8);
-            mbar_init(smem_u32(&k_empty[i]), 1);
+        for (int i = 0; i < ks + qs + rs; ++i) {
+            mbar_init(smem_u32(&bars[i]), !kSame && i < ks ? 8 : 1);
+            mbar_init(smem_u32(&bars[L::kMostStages + i]), i < ks + qs ? 1 : 8);
         }
-        for (int i = 0; i < L::kQs; ++i) {
-            mbar_init(smem_u32(&q_full[i]), 1);
-            mbar_init(smem_u32(&q_empty[i]), 1);
-            mbar_init(smem_u32(&l_full[i]), 1);
-            mbar_init(smem_u32(&l_empty[i]), W::kAdd);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&s_full[i]), 2);             // the MMAs and the normalisers
+            mbar_init(smem_u32(&s_empty[i]), W::kAdd);
+            mbar_init(smem_u32(&x_full[i]), 4);
+            mbar_init(smem_u32(&x_empty[i]), 4);
         }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(smem_u32(&s_full[i]), 1);
-            mbar_init(smem_u32(&s_empty[i]), 4 * W::kHalves);
-        }
-        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&h_full[i]), 4);         // (and h_empty)
         mbar_init(smem_u32(final_bar), 1);
         *abort_flag = 0;
         bad[0] = bad[1] = 0;
@@ -326,110 +345,135 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
 
     if (warp < W::kAdd) {
         // ------------------------------ weights ------------------------------
-        // warps 0-3: tile A, 4-7: tile B, and the same again for the second half of the columns' blocks
-        const int w = (warp >> 2) & 1, h = warp >> 3, row = (warp & 3) * 32 + lane;        // key of the tile = TMEM lane
-        const uint32_t lane_at = (uint32_t)((warp & 3) * 32) << 16;
+        // A warp has 32 keys of each tile, and every other block of 32 columns: a thread's two keys share what it reads of a column
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(W::kAddRegs));
+        const int h = warp >> 2, row = (warp & 3) * 32 + lane;      // half of the blocks; key of the tile = TMEM lane
+        const uint32_t s_at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float f = a.scale * 1.4426950408889634f;
-        int buf = 0, qst = 0;
-        uint32_t ph_h = 0;
-        uint32_t ph_s = 0, ph_l = 0;            // per buffer; of the ring of normalisers
-        bool ok = true, first = true;
-        // this thread's key of an item: the place of its weight (-1: none), what is there, and the scale of its row
+        int buf = 0;
+        uint32_t ph_s = 0, ph_x = 0;
+        bool ok = true;
+        // this thread's keys of an item: the place of their weights (-1: none), what is there (of the key that it writes: the first half
+        // tile A's, the second tile B's), and the scale of their rows
         struct Place {
             int64_t at;
-            float old, scale;
+            float old, scale[2];
         };
         auto place = [&](const Segment& x) {
-            Place r{-1, 0.f, 1.f};
-            const int key = x.it.k0 + w * kKeys + row;
-            if (key >= x.s.kv || key < first_seen(x.s, a.window) || (kSame && h == 1)) return r;
-            const int q = a.page_of(key), pg = __ldg(a.batch.table + (int64_t)x.b * a.batch.table_stride + q);
-            if ((unsigned)pg >= (unsigned)a.cache.pages) {
-                bad[1] = 1;
-                return r;
+            Place r{-1, 0.f, {1.f, 1.f}};
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int key = x.it.k0 + w * kKeys + row;
+                if (key >= x.s.kv || key < first_seen(x.s, a.window) || (kSame && w != h)) continue;
+                const int q = a.page_of(key), pg = __ldg(a.batch.table + (int64_t)x.b * a.batch.table_stride + q);
+                if ((unsigned)pg >= (unsigned)a.cache.pages) {
+                    bad[1] = 1;
+                    continue;
+                }
+                const int64_t at = scale_offset(a.cache, pg, x.g, key - q * a.cache.page);
+                if constexpr (!kSame) r.scale[w] = __ldg(a.cache.k_scale + at);
+                if (w != h) continue;
+                r.at = at;
+                if (key < x.s.kv - x.s.n && p.w.decay != 0.f && x.to == x.it.tiles && x.from == 0) r.old = p.w.weights[at];
             }
-            r.at = scale_offset(a.cache, pg, x.g, key - q * a.cache.page);
-            if (key < x.s.kv - x.s.n && p.w.decay != 0.f && x.to == x.it.tiles && x.from == 0) r.old = p.w.weights[r.at];
-            if constexpr (!kSame) r.scale = __ldg(a.cache.k_scale + r.at);
             return r;
         };
         bool more = walk.next(p, sg);
-        Place cur = {-1, 0.f, 1.f};
+        Place cur = {-1, 0.f, {1.f, 1.f}};
         if (more) cur = place(sg);
         while (more && ok) {
             Segment next;
             const bool then = walk.next(p, next);
-            Place ahead = {-1, 0.f, 1.f};
+            Place ahead = {-1, 0.f, {1.f, 1.f}};
             if (then) ahead = place(next);
-            const int ctx = sg.s.kv - sg.s.n, base = sg.it.k0 + w * kKeys, key = base + row;
-            const bool mine = w == 0 || two_of(sg);
-            const float fk = kSame ? f : f * cur.scale;
-            float total = 0.f;
-            // the last tile's normalisers are kept for an item that has the same
-            if (!first && !sg.same) {
-                if (lane == 0) mbar_arrive(smem_u32(&l_empty[qst]));
-                if (++qst == L::kQs) qst = 0, ph_l ^= 1;
-            }
-            for (int i = sg.from; i < sg.to; ++i) {
-                const int t0 = sg.it.ta + i * p.tpt, tokens = min(p.tpt, sg.it.tb - t0), rows = tokens * p.G;
-                if (!(sg.same && i == sg.from)) {
-                    ok = wait_warp(smem_u32(&l_full[qst]), ph_l, abort_flag, 21);
-                    if (!ok) break;
-                }
-                if (mine) {
-                    ok = wait_warp(smem_u32(&s_full[2 * w + buf]), ph_s >> buf & 1, abort_flag, 22);
-                    ph_s ^= 1u << buf;
-                    if (!ok) break;
-                    tc_fence_after();
-                    const bool masked = base + kKeys - 1 > ctx + t0 || (a.window && base <= ctx + t0 + tokens - 1 - a.window) || rows % 32;
-                    // the columns that see this key
-                    const int hi = a.window ? min(max(key - ctx - t0 + a.window, 0), tokens) * p.G : rows;
-                    const int lo = min(max(key - ctx - t0, 0), tokens) * p.G;
-                    const uint32_t s_at = tmem + lane_at + L::kS(w, buf);
-                    const float* nl = ls + qst * 128;
-                    float zs[4] = {0.f, 0.f, 0.f, 0.f};
-                    uint32_t sr[32];
-                    float* sv = reinterpret_cast<float*>(sr);
-#pragma unroll 1
-                    for (int c = h; c * 32 < rows; c += W::kHalves) {
-                        tmem_ld32(s_at + 32 * c, sr);
+            const int ctx = sg.s.kv - sg.s.n;
+            const float fa = kSame ? f : f * cur.scale[0], fb = kSame ? f : f * cur.scale[1];
+            float total[2] = {0.f, 0.f};
+            int t0 = sg.it.ta + sg.from * p.tpt;
+            for (int i = sg.from; i < sg.to; ++i, t0 += p.tpt) {
+                const int tokens = min(p.tpt, sg.it.tb - t0), rows = tokens * p.G;
+                ok = wait_warp(smem_u32(&s_full[buf]), ph_s, abort_flag, 22);
+                if (!ok) break;
+                tc_fence_after();
+                const bool masked = sg.it.k0 + kBlock - 1 > ctx + t0 || (a.window && sg.it.k0 <= ctx + t0 + tokens - 1 - a.window) || rows % 32;
+                const uint32_t at = s_at + buf * 256;
+                const float* nl = ls + buf * 128;
+                float za[4] = {0.f, 0.f, 0.f, 0.f}, zb[4] = {0.f, 0.f, 0.f, 0.f};
+                // the columns of block c that see each key
+                auto sees = [&](int w, int c) {
+                    const int ahead_of = sg.it.k0 + w * kKeys + row - ctx - t0;
+                    const int hi = a.window ? min(max(ahead_of + a.window, 0), tokens) * p.G : rows, lo = min(max(ahead_of, 0), tokens) * p.G;
+                    return low_bits(hi - 32 * c) & ~low_bits(lo - 32 * c);
+                };
+                if constexpr (kSame) {
+                    auto load = [&](uint32_t* sr, int c) {
+                        tmem_ld32(at + 32 * c, sr);
+                        tmem_ld32(at + 128 + 32 * c, sr + 32);
+                    };
+                    auto wait = [&](uint32_t* sr) {
                         tmem_wait32(sr);
-                        if (masked) add_weights32<true>(sv, fk, nl + 32 * c, low_bits(hi - 32 * c) & ~low_bits(lo - 32 * c), zs);
-                        else add_weights32<false>(sv, fk, nl + 32 * c, 0u, zs);
+                        keep32(sr + 32);
+                    };
+                    auto use = [&](uint32_t* sr, int c) {
+                        const float* v = reinterpret_cast<const float*>(sr);
+                        if (masked) add_weights<true, 32>(v, v + 32, fa, fb, nl + 32 * c, sees(0, c), sees(1, c), za, zb);
+                        else add_weights<false, 32>(v, v + 32, fa, fb, nl + 32 * c, 0u, 0u, za, zb);
+                    };
+                    // the second block is on its way while the first is worked on
+                    uint32_t s0[64], s1[64];
+                    const bool b1 = 32 * (h + 2) < rows;
+                    if (32 * h < rows) {
+                        load(s0, h);
+                        wait(s0);
+                        if (b1) load(s1, h + 2);
+                        use(s0, h);
+                        if (b1) {
+                            wait(s1);
+                            use(s1, h + 2);
+                        }
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&s_empty[2 * w + buf]));
-                    total += (zs[0] + zs[1]) + (zs[2] + zs[3]);
-                    buf ^= 1;
+                } else {                // with fewer registers 16 columns at a time
+#pragma unroll 1
+                    for (int c = 2 * h; c * 16 < rows; c += (c & 1) ? 3 : 1) {
+                        uint32_t sr[32];
+                        tmem_ld16(at + 16 * c, sr);
+                        tmem_ld16(at + 128 + 16 * c, sr + 16);
+                        tmem_wait32(sr);
+                        const float* v = reinterpret_cast<const float*>(sr);
+                        if (masked) {
+                            const int by = 16 * (c & 1);
+                            add_weights<true, 16>(v, v + 16, fa, fb, nl + 16 * c, sees(0, c >> 1) >> by, sees(1, c >> 1) >> by, za, zb);
+                        } else {
+                            add_weights<false, 16>(v, v + 16, fa, fb, nl + 16 * c, 0u, 0u, za, zb);
+                        }
+                    }
                 }
-                if (i + 1 < sg.to) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&l_empty[qst]));
-                    if (++qst == L::kQs) qst = 0, ph_l ^= 1;
-                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&s_empty[buf]));
+                total[0] += (za[0] + za[1]) + (za[2] + za[3]);
+                total[1] += (zb[0] + zb[1]) + (zb[2] + zb[3]);
+                ph_s ^= buf;
+                buf ^= 1;
             }
             if (!ok) break;
-            first = false;
-            if constexpr (kSame) {
-                // (no named barrier: a warp that gives up a wait would leave the others at it)
-                if (mine) {
-                    float* there = halves + w * kKeys + row;
-                    ok = wait_warp(smem_u32(h ? &h_empty[w] : &h_full[w]), ph_h ^ h, abort_flag, 23);
-                    if (!ok) break;
-                    ph_h ^= 1;
-                    if (h) *there = total;
-                    else total += *there;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(h ? &h_full[w] : &h_empty[w]));
-                }
-            }
-            if (h == 0 && mine) {
-                if (sg.from == 0 && sg.to == sg.it.tiles) {
-                    if (cur.at >= 0) p.w.weights[cur.at] = p.w.decay != 0.f ? total + p.w.decay * cur.old : total;
-                } else {
-                    p.parts[((int64_t)blockIdx.x * 2 + (sg.from == 0 ? 1 : 0)) * kBlock + w * kKeys + row] = total;
-                }
+            // The halves exchange their sums: the first half of the warps writes tile A's keys and the second half tile B's.  (No named
+            // barrier: a warp that gives up a wait would leave the others at it.)
+            ok = wait_warp(smem_u32(&x_empty[1 - h]), ph_x ^ 1, abort_flag, 23);
+            if (!ok) break;
+            halves[(1 - h) * kKeys + row] = total[1 - h];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&x_full[1 - h]));
+            ok = wait_warp(smem_u32(&x_full[h]), ph_x, abort_flag, 24);
+            if (!ok) break;
+            const float sum = h ? halves[kKeys + row] + total[1] : total[0] + halves[row];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&x_empty[h]));
+            ph_x ^= 1;
+            if (sg.from == 0 && sg.to == sg.it.tiles) {
+                if (cur.at >= 0) p.w.weights[cur.at] = p.w.decay != 0.f ? sum + p.w.decay * cur.old : sum;
+            } else {
+                p.parts[((int64_t)blockIdx.x * 2 + (sg.from == 0 ? 1 : 0)) * kBlock + h * kKeys + row] = sum;
             }
             __syncwarp();
             sg = next;
@@ -439,114 +483,102 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
     } else if (!kSame && warp < W::kMma) {
       if constexpr (!kSame) {
         // ------------------------------ conversion of 8-bit rows ------------------------------
-        // A warp takes 16 rows of each tile, a lane 16 entries of each 64 of two rows (rl and rl + 8); the next tile's codes are
-        // requested as soon as this one's are converted.
-        constexpr int kBlocks = D / 64;
-        const sp_cache& c = a.cache;
-        const int r0 = (warp - W::kAdd) * 16, sub = lane & 3, rl = lane >> 2;
-        const uint32_t dst0 = (r0 + rl) * 128 + (((2 * sub) ^ rl) << 4), dst1 = (r0 + rl) * 128 + (((2 * sub + 1) ^ rl) << 4);
-        int st = 0;
-        uint32_t ph = 1;
+        // A warp takes 16 rows of each tile.  Eight lanes read 128 bytes of codes, and a lane's 16 codes become two pieces of 16 bytes of
+        // the bf16 tile; half of the lanes store their second piece first, so that eight of them meet eight different banks.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kConvertRegs));
+        constexpr int kPieces = D / 16, kRounds = 16 * kPieces / 32;        // 16-byte pieces of a row of codes; of a lane
+        const int r0 = (warp - W::kAdd) * 16;
+        int st = 0, rst = 0;
+        uint32_t ph = 1, ph_r = 0;
         bool ok = true;
-        uint4 codes[2][kBlocks];
-        auto fetch = [&](const Segment& x, int w) {
-            const int seen = first_seen(x.s, a.window);
+        while (ok && walk.next(p, sg)) {
+            for (int w = 0; w < (two_of(sg) ? 2 : 1); ++w) {
+                ok = wait_warp(smem_u32(&r_full[rst]), ph_r, abort_flag, 62);
+                if (!ok) break;
+                uint4 codes[kRounds];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int tok = x.it.k0 + w * kKeys + r0 + rl + 8 * y;
-                int64_t at = 0;         // no token: some row, which no one's weight is of
-                if (tok < x.s.kv && tok >= seen) {
-                    const int q = a.page_of(tok), pg = __ldg(a.batch.table + (int64_t)x.b * a.batch.table_stride + q);
-                    if ((unsigned)pg < (unsigned)c.pages) at = row_offset(c, pg, x.g, tok - q * c.page);
+                for (int y = 0; y < kRounds; ++y) {
+                    const int i = y * 32 + lane;
+                    codes[y] = *reinterpret_cast<const uint4*>(r_ring + rst * L::kCodeBytes + (r0 * kPieces + i) * 16);
                 }
-#pragma unroll
-                for (int h = 0; h < kBlocks; ++h)
-                    codes[y][h] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.k) + at + sub * 16 + h * 64));
-            }
-        };
-        bool more = walk.next(p, sg);
-        if (more) fetch(sg, 0);
-        while (more && ok) {
-            const bool two = two_of(sg);
-            Segment next;
-            const bool then = walk.next(p, next);
-            for (int w = 0; w < (two ? 2 : 1); ++w) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&r_empty[rst]));
+                if (++rst == rs) rst = 0, ph_r ^= 1;
                 ok = wait_warp(smem_u32(&k_empty[st]), ph, abort_flag, 61);
                 if (!ok) break;
-                uint8_t* tile = smem + L::kK + st * L::kTileBytes;
+                uint8_t* tile = k_ring + st * L::kTileBytes;
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
+                for (int y = 0; y < kRounds; ++y) {
+                    const int i = y * 32 + lane, rr = r0 + i / kPieces, piece = i % kPieces;
+                    const uint32_t w4[4] = {codes[y].x, codes[y].y, codes[y].z, codes[y].w};
+                    uint32_t o[8];
 #pragma unroll
-                    for (int h = 0; h < kBlocks; ++h) {
-                        const uint32_t w4[4] = {codes[y][h].x, codes[y][h].y, codes[y][h].z, codes[y][h].w};
-                        uint32_t o[8];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) pairs_of<kKind, true>(w4[i], o[2 * i], o[2 * i + 1]);
-                        uint8_t* at = tile + y * 1024 + h * (kKeys * 128);
-                        *reinterpret_cast<uint4*>(at + dst0) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4*>(at + dst1) = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
-                if (w == 0 && two) fetch(sg, 1);
-                else if (then) fetch(next, 0);
+                    for (int k = 0; k < 4; ++k) pairs_of<kKind, true>(w4[k], o[2 * k], o[2 * k + 1]);
+                    uint8_t* at = tile + (piece >> 2) * (kKeys * 128) + rr * 128;
+                    const int c0 = 2 * (piece & 3), flip = D == 128 ? piece >> 2 : 0;
+                    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                    *reinterpret_cast<uint4*>(at + (((c0 + flip) ^ (rr & 7)) << 4)) = flip ? hi : lo;
+                    *reinterpret_cast<uint4*>(at + (((c0 + 1 - flip) ^ (rr & 7)) << 4)) = flip ? lo : hi;
+                }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&k_full[st]));
-                if (++st == L::kKs) st = 0, ph ^= 1;
+                if (++st == ks) st = 0, ph ^= 1;
             }
-            sg = next;
-            more = then;
         }
       }
-    } else if (warp == W::kMma) {
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kSingleRegs));
+      if (warp == W::kMma) {
         // ------------------------------ MMAs ------------------------------
         const bool lead = elect_one();
-        const uint64_t k_desc = smem_desc(smem_u32(smem + L::kK)), q_desc = smem_desc(smem_u32(smem + L::kQ));
+        const uint64_t k_desc = smem_desc(smem_u32(k_ring)), q_desc = smem_desc(smem_u32(q_ring));
         const uint32_t k_lo = (uint32_t)k_desc, q_lo = (uint32_t)q_desc, d_hi = (uint32_t)(k_desc >> 32);
         int kst = 0, qst = 0;
-        uint32_t ph_k = 0, ph_q = 0, buf[2] = {0, 0}, ph_s[2] = {3, 3};      // a fresh barrier counts as completed for the odd parity
+        uint32_t ph_k = 0, ph_q = 0, buf = 0, ph_s = 1;         // a fresh barrier counts as completed for the odd parity
         bool ok = tmem == 0, first = true;
         while (ok && walk.next(p, sg)) {
             const bool two = two_of(sg);
+            // the last tile's place is given back now: it is used again by an item that has the same
             if (!first && !sg.same) {
                 commit_if(lead, smem_u32(&q_empty[qst]));
-                if (++qst == L::kQs) qst = 0, ph_q ^= 1;
+                if (++qst == qs) qst = 0, ph_q ^= 1;
             }
             first = false;
-            const int k1 = kst + 1 == L::kKs ? 0 : kst + 1;
-            for (int i = sg.from; i < sg.to && ok; ++i) {
-                const int tokens = min(p.tpt, sg.it.tb - (sg.it.ta + i * p.tpt));
-                const uint32_t idesc = instr_desc((tokens * p.G + 15) & ~15, false);
+            const int k1 = kst + 1 == ks ? 0 : kst + 1;
+            ok = wait_warp(smem_u32(&k_full[kst]), ph_k, abort_flag, 32) &&
+                 (!two || wait_warp(smem_u32(&k_full[k1]), ph_k ^ (k1 == 0), abort_flag, 32));
+            if (!ok) break;
+            int left = sg.it.tb - (sg.it.ta + sg.from * p.tpt);
+            for (int i = sg.from; i < sg.to; ++i, left -= p.tpt) {
+                const uint32_t idesc = instr_desc((min(p.tpt, left) * p.G + 15) & ~15, false);
                 if (!(sg.same && i == sg.from)) ok = wait_warp(smem_u32(&q_full[qst]), ph_q, abort_flag, 31);
+                ok = ok && wait_warp(smem_u32(&s_empty[buf]), ph_s, abort_flag, 33);
                 if (!ok) break;
+                tc_fence_after();
+                const uint32_t qb = q_lo + qst * (L::kTileBytes >> 4);
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     if (w == 1 && !two) break;
-                    const int ks = w ? k1 : kst;
-                    if (i == sg.from) ok = ok && wait_warp(smem_u32(&k_full[ks]), ph_k ^ (w && k1 == 0), abort_flag, 32);
-                    ok = ok && wait_warp(smem_u32(&s_empty[2 * w + buf[w]]), ph_s[w] >> buf[w] & 1, abort_flag, 33);
-                    if (!ok) break;
-                    ph_s[w] ^= 1u << buf[w];
-                    tc_fence_after();
-                    const uint32_t ka = k_lo + ks * (L::kTileBytes >> 4), qb = q_lo + qst * (L::kTileBytes >> 4);
-                    const uint32_t d = L::kS(w, 0) + buf[w] * 128;
+                    const uint32_t ka = k_lo + (w ? k1 : kst) * (L::kTileBytes >> 4), d = L::kS(w, 0) + buf * 256;
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t off = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
                         mma_ss(lead, d, ka + off, qb + off, d_hi, idesc, k > 0);
                     }
-                    commit_if(lead, smem_u32(&s_full[2 * w + buf[w]]));
-                    buf[w] ^= 1;
                 }
-                if (!ok) break;
+                commit_if(lead, smem_u32(&s_full[buf]));
+                ph_s ^= buf;
+                buf ^= 1;
                 if (i + 1 < sg.to) {
                     commit_if(lead, smem_u32(&q_empty[qst]));
-                    if (++qst == L::kQs) qst = 0, ph_q ^= 1;
+                    if (++qst == qs) qst = 0, ph_q ^= 1;
                 }
             }
             if (!ok) break;
             for (int w = 0; w < (two ? 2 : 1); ++w) {
                 commit_if(lead, smem_u32(&k_empty[kst]));
-                if (++kst == L::kKs) kst = 0, ph_k ^= 1;
+                if (++kst == ks) kst = 0, ph_k ^= 1;
             }
         }
         // nothing of this warp's MMAs is in flight when TMEM is freed
@@ -561,43 +593,49 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
                 }
         }
         __syncwarp();
-    } else if (warp == W::kTma) {
+      } else if (warp == W::kTma) {
         // ------------------------------ TMA ------------------------------
+        // key tiles to their ring, codes to a ring of their own
         const sp_cache& c = a.cache;
         const int rows_tile = p.G * p.tpt, boxes = kKeys / p.box;
+        uint64_t *t_full = kSame ? k_full : r_full, *t_empty = kSame ? k_empty : r_empty;
+        uint8_t* t_ring = kSame ? k_ring : r_ring;
+        constexpr int kBytes = kSame ? L::kTileBytes : L::kCodeBytes;
+        const int ts = kSame ? ks : rs;
         int kst = 0, qst = 0, k_loads = 0, q_loads = 0;
         uint32_t ph_k = 1, ph_q = 1;
         bool ok = true, first = true;
         while (ok && walk.next(p, sg)) {
-            const bool two = two_of(sg);
-            if constexpr (kSame) {
-                const int32_t* table = a.batch.table + (int64_t)sg.b * a.batch.table_stride;
-                const int seen = first_seen(sg.s, a.window);
-                for (int w = 0; w < (two ? 2 : 1); ++w) {
-                    // this lane's box: its page (pages: none, which loads zeros) and its first slot
-                    const int tok = sg.it.k0 + w * kKeys + lane * p.box;
-                    int slot = 0, pg = (int)c.pages;
-                    if (lane < boxes && tok < sg.s.kv && tok + p.box > seen) {
-                        const int q = a.page_of(tok), t = __ldg(table + q);
-                        if (t >= 0 && t < c.pages) pg = t, slot = tok - q * c.page;
-                        else bad[1] = 1;
-                    }
-                    ok = wait_warp(smem_u32(&k_empty[kst]), ph_k, abort_flag, 41);
-                    if (!ok) break;
-                    const uint32_t bar = smem_u32(&k_full[kst]);
-                    if (lane == 0) mbar_expect_tx(bar, L::kTileBytes);
-                    __syncwarp();
-                    if (lane < boxes)
+            const int32_t* table = a.batch.table + (int64_t)sg.b * a.batch.table_stride;
+            const int seen = first_seen(sg.s, a.window);
+            for (int w = 0; w < (two_of(sg) ? 2 : 1); ++w) {
+                // this lane's box: its page (pages: none, which loads zeros) and its first slot
+                const int tok = sg.it.k0 + w * kKeys + lane * p.box;
+                int slot = 0, pg = (int)c.pages;
+                if (lane < boxes && tok < sg.s.kv && tok + p.box > seen) {
+                    const int q = a.page_of(tok), t = __ldg(table + q);
+                    if (t >= 0 && t < c.pages) pg = t, slot = tok - q * c.page;
+                    else bad[1] = 1;
+                }
+                ok = wait_warp(smem_u32(&t_empty[kst]), ph_k, abort_flag, 41);
+                if (!ok) break;
+                const uint32_t bar = smem_u32(&t_full[kst]), at = smem_u32(t_ring) + kst * kBytes;
+                if (lane == 0) mbar_expect_tx(bar, kBytes);
+                __syncwarp();
+                if (lane < boxes) {
+                    if constexpr (kSame) {
 #pragma unroll
                         for (int ch = 0; ch < L::kChunks; ++ch)
-                            tma_load_4d(smem_u32(smem + L::kK) + kst * L::kTileBytes + ch * (kKeys * 128) + lane * p.box * 128, &maps.k,
-                                        ch * 64, slot, sg.g, pg, bar);
-                    ++k_loads;
-                    if (++kst == L::kKs) kst = 0, ph_k ^= 1;
+                            tma_load_4d(at + ch * (kKeys * 128) + lane * p.box * 128, &maps.k, ch * 64, slot, sg.g, pg, bar);
+                    } else {
+                        tma_load_4d(at + lane * p.box * D, &maps.k, 0, slot, sg.g, pg, bar);
+                    }
                 }
-                if (!ok) break;
+                ++k_loads;
+                if (++kst == ts) kst = 0, ph_k ^= 1;
             }
-            if (!first && !sg.same && ++qst == L::kQs) qst = 0, ph_q ^= 1;
+            if (!ok) break;
+            if (!first && !sg.same && ++qst == qs) qst = 0, ph_q ^= 1;
             first = false;
             for (int i = sg.from; i < sg.to; ++i) {
                 if (!(sg.same && i == sg.from)) {
@@ -607,56 +645,54 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
                         const uint32_t bar = smem_u32(&q_full[qst]);
                         mbar_expect_tx(bar, (uint32_t)(rows_tile * D * 2));
                         for (int ch = 0; ch < L::kChunks; ++ch)
-                            tma_load_3d(smem_u32(smem + L::kQ) + qst * L::kTileBytes + ch * (kKeys * 128), &maps.q, ch * 64, sg.g * p.G,
+                            tma_load_3d(smem_u32(q_ring) + qst * L::kTileBytes + ch * (kKeys * 128), &maps.q, ch * 64, sg.g * p.G,
                                         (int)(sg.s.row0 + sg.it.ta + i * p.tpt), bar);
                     }
                     ++q_loads;
                 }
-                if (i + 1 < sg.to && ++qst == L::kQs) qst = 0, ph_q ^= 1;
+                if (i + 1 < sg.to && ++qst == qs) qst = 0, ph_q ^= 1;
             }
         }
         // an aborted CTA's copies land before it leaves: the last ones of each ring, one phase of a stage's barrier each
         if (lane == 0 && *abort_flag) {
             const unsigned long long t0 = global_ns();
-            for (int k = 1; k <= min(k_loads, L::kKs); ++k) {
+            for (int k = 1; k <= min(k_loads, ts); ++k) {
                 const int n = k_loads - k;
-                while (!mbar_try_wait_suspend(smem_u32(&k_full[n % L::kKs]), (uint32_t)(n / L::kKs) & 1, 1000u) && global_ns() - t0 < kTimeoutNs) {}
+                while (!mbar_try_wait_suspend(smem_u32(&t_full[n % ts]), (uint32_t)(n / ts) & 1, 1000u) && global_ns() - t0 < kTimeoutNs) {}
             }
-            for (int k = 1; k <= min(q_loads, L::kQs); ++k) {
+            for (int k = 1; k <= min(q_loads, qs); ++k) {
                 const int n = q_loads - k;
-                while (!mbar_try_wait_suspend(smem_u32(&q_full[n % L::kQs]), (uint32_t)(n / L::kQs) & 1, 1000u) && global_ns() - t0 < kTimeoutNs) {}
+                while (!mbar_try_wait_suspend(smem_u32(&q_full[n % qs]), (uint32_t)(n / qs) & 1, 1000u) && global_ns() - t0 < kTimeoutNs) {}
             }
         }
         __syncwarp();
-    } else if (warp == W::kLse) {
+      } else if (warp == W::kLse) {
         // ------------------------------ normalisers ------------------------------
-        int qst = 0;
-        uint32_t ph = 1;
-        bool ok = true, first = true;
+        // they lie beside S: the same barriers say when the place is free and that they are there
+        uint32_t buf = 0, ph_s = 1;
+        bool ok = true;
         while (ok && walk.next(p, sg)) {
-            if (!first && !sg.same && ++qst == L::kQs) qst = 0, ph ^= 1;
-            first = false;
             for (int i = sg.from; i < sg.to; ++i) {
-                if (!(sg.same && i == sg.from)) {
-                    const int t0 = sg.it.ta + i * p.tpt, rows = min(p.tpt, sg.it.tb - t0) * p.G;
-                    float l[4];
+                const int t0 = sg.it.ta + i * p.tpt, rows = min(p.tpt, sg.it.tb - t0) * p.G;
+                float l[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int r = lane + 32 * k, t = r / p.G;
-                        l[k] = 0.f;         // columns of no row are masked
-                        if (r < rows) l[k] = a.lse[(sg.s.row0 + t0 + t) * a.lse_stride_row + (sg.g * p.G + r - t * p.G) * a.lse_stride_head];
-                    }
-                    ok = wait_warp(smem_u32(&l_empty[qst]), ph, abort_flag, 51);
-                    if (!ok) break;
-                    // a row that saw no token has the sum 0, whose logarithm is -inf, and gives nothing
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) ls[qst * 128 + lane + 32 * k] = l[k] == -INFINITY ? -INFINITY : l[k] * -1.4426950408889634f;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&l_full[qst]));
+                for (int k = 0; k < 4; ++k) {
+                    const int r = lane + 32 * k, t = r / p.G;
+                    l[k] = 0.f;         // columns of no row are masked
+                    if (r < rows) l[k] = a.lse[(sg.s.row0 + t0 + t) * a.lse_stride_row + (sg.g * p.G + r - t * p.G) * a.lse_stride_head];
                 }
-                if (i + 1 < sg.to && ++qst == L::kQs) qst = 0, ph ^= 1;
+                ok = wait_warp(smem_u32(&s_empty[buf]), ph_s, abort_flag, 51);
+                if (!ok) break;
+                // a row that saw no token has the sum 0, whose logarithm is -inf, and gives nothing
+#pragma unroll
+                for (int k = 0; k < 4; ++k) ls[buf * 128 + lane + 32 * k] = l[k] == -INFINITY ? -INFINITY : l[k] * -1.4426950408889634f;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&s_full[buf]));
+                ph_s ^= buf;
+                buf ^= 1;
             }
         }
+      }
     }
     tc_fence_before();
     __syncthreads();
@@ -717,8 +753,8 @@ Space carve(int P) {
 
 template <int D, int kKind>
 sp_status launch(const Maps& maps, const TcArgs& p, cudaStream_t st) {
-    SP_CUDA_TRY(cudaFuncSetAttribute(weights_tc_kernel<D, kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kEnd));
-    weights_tc_kernel<D, kKind><<<p.P, Roles<kKind>::kThreads, Layout<D>::kEnd, st>>>(maps, p);
+    SP_CUDA_TRY(cudaFuncSetAttribute(weights_tc_kernel<D, kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize, (Layout<D, kKind>::kEnd)));
+    weights_tc_kernel<D, kKind><<<p.P, Roles<kKind>::kThreads, (Layout<D, kKind>::kEnd), st>>>(maps, p);
     SP_LAUNCH_CHECK();
     return launch_early(weights_join_kernel, dim3((unsigned)std::max(1, p.P - 1)), kBlock, (size_t)0, st, p);
 }
@@ -739,8 +775,9 @@ bool weights_tc_supported(const sp_cache& c, const sp_batch& b, int G) {
     // (the join looks at a CTA's status per thread; the plan counts key blocks in 32 bits)
     if (b.B > kMaxSeqs || sm_count() < 2 || sm_count() > kBlock || (int64_t)b.B * b.table_width > ((int64_t)1 << 38) / c.page) return false;
     if (c.dtype != SP_BF16 || (c.d != 64 && c.d != 128) || G > 128) return false;
-    if (c.kind != SP_CACHE_SAME)                                        // rows of codes are read 16 bytes at a time
-        return (reinterpret_cast<uintptr_t>(c.k) | (uintptr_t)c.stride_page | (uintptr_t)c.stride_head | (uintptr_t)c.stride_slot) % 16 == 0;
+    if (c.kind != SP_CACHE_SAME &&
+        (reinterpret_cast<uintptr_t>(c.k) | (uintptr_t)c.stride_page | (uintptr_t)c.stride_head | (uintptr_t)c.stride_slot) % 16 != 0)
+        return false;                                                   // a tensor map wants multiples of 16 bytes
     if (c.page % 8 != 0) return false;                                  // boxes of 8 rows at least
     const int64_t limit = (int64_t)1 << 39;                             // tensor-map strides are below 2^40 bytes
     if (c.stride_slot >= limit / 2 || c.stride_head >= limit / 2 || c.stride_page >= limit / 2) return false;
@@ -757,6 +794,10 @@ sp_status weights_tc_launch(const WeightsProblem& w, void* ws, cudaStream_t st) 
     p.tpt = 128 / p.G;
     p.P = sm_count();
     p.box = std::min(128, a.cache.page & -a.cache.page);
+    const bool same = a.cache.kind == SP_CACHE_SAME;
+    const int tiles = 224 * 1024 / (kKeys * a.cache.d * 2);
+    p.k_stages = same ? (a.cache.d == 128 ? 4 : 8) : (a.cache.d == 128 ? 3 : 6);
+    p.q_stages = same ? tiles - p.k_stages : (a.cache.d == 128 ? 2 : 4);
     const Space s = carve(p.P);
     char* base = static_cast<char*>(ws);
     p.hdr = static_cast<WsHeader*>(ws);
@@ -772,7 +813,9 @@ sp_status weights_tc_launch(const WeightsProblem& w, void* ws, cudaStream_t st) 
     sp_status e;
     memset(&maps, 0, sizeof(maps));
     if ((e = encode(&maps.q, a.q.data, 3, q_ext, q_str, q_box)) != SP_OK) return e;
-    if (a.cache.kind == SP_CACHE_SAME && (e = encode(&maps.k, a.cache.k, 4, c_ext, c_str, c_box)) != SP_OK) return e;
+    const int r_box[4] = {a.cache.d, p.box, 1, 1};          // whole rows of codes, as they lie
+    if ((e = same ? encode(&maps.k, a.cache.k, 4, c_ext, c_str, c_box) : encode(&maps.k, a.cache.k, 4, c_ext, c_str, r_box, true)) != SP_OK)
+        return e;
     return a.cache.d == 64 ? launch_kind<64>(maps, p, st) : launch_kind<128>(maps, p, st);
 }
 
