@@ -98,6 +98,37 @@ def test_weights_layouts_scales_and_normalisers(sp, new, kv, layout, scale, shif
     check_weights(sp, H=4, H_kv=2, d=d, page=page, new=new, kv=kv, layout=layout, scale=scale, lse_shift=shift, kind=kind)
 
 
+@pytest.mark.parametrize("d,kind,n,kv", [(128, "e4m3", 32, 60000), (64, "same", 24, 90000), (128, "same", 700, 30000), (64, "int8", 1, 120000),
+                                         (128, "int8", 90, 50000)])
+def test_weights_of_a_long_cache(sp, d, kind, n, kv):
+    """Every CTA has dozens of items: all tokens' weights against 64-bit products of the rows as they read back."""
+    import torch
+    H, H_kv, page = 16, 4, 64
+    g = torch.Generator(device="cuda").manual_seed(n)
+    pages = -(-kv // page)
+    cache = sp.cache_alloc(pages, H_kv, page, d, kind=kind)
+    table = torch.randperm(pages, generator=g, device="cuda").int()[None]
+    i64 = lambda *v: torch.tensor(v, dtype=torch.int64, device="cuda")                          # noqa: E731
+    full = sp.Batch(i64(0, kv), i64(kv), table, rows=kv)
+    new = lambda h, m: torch.randn(m, h, d, generator=g, device="cuda").to(torch.bfloat16)      # noqa: E731
+    sp.cache_write(cache, full, new(H_kv, kv), new(H_kv, kv), check=True)
+    k, _ = sp.cache_read(cache, full, check=True)
+    q = new(H, n)
+    batch = sp.Batch(i64(0, n), i64(kv), table, rows=n)
+    lse = np.log(kv) + 0.5 + 0.1 * torch.randn(H, n, generator=g, device="cuda")
+    w = sp.attend_weights(q, cache, batch, lse, sp.weights_alloc(cache).fill_(3.0), decay=0.5, check=True)
+    i = torch.arange(kv, device="cuda")
+    got = w[table[0].long()[i // page], :, i % page].double().T                                  # [H_kv, kv]
+    seen = i <= torch.arange(kv - n, kv, device="cuda")[:, None]
+    for h in range(H_kv):
+        want = torch.where(i < kv - n, 1.5, 0.0).double()
+        for f in range(4 * h, 4 * h + 4):
+            x = q[:, f].double() @ k[h].double().T * d ** -0.5 - lse[f].double()[:, None]
+            want += torch.where(seen, x.exp(), 0.0).sum(0)
+        # |logits| below 12, of products that sum to at most 100: each weight within 2^-17 (oracle.kept.weights' bound), and sums of n * 4
+        assert torch.all((got[h] - want).abs() <= want * (2.0 ** -17 + 4 * n * 2.0 ** -24))
+
+
 def test_weights_sum_to_the_rows(sp):
     """With lse as attend returns it, the weights of a sequence add up to its rows, whatever the batch."""
     import torch
