@@ -8,18 +8,15 @@
 // tiles of 128 query rows that see any of them come by, each read for both key tiles: with one key tile an item the
 // query rows' traffic would be 64 bytes a clock and SM, which L2 does not give.
 //
-// Per 256 x 128 logits the MMAs take 1024 cycles (d = 128; 512 at d = 64), the exponentials as many (32 a clock and SM), and the loads
-// from TMEM too (128 bytes a clock), so all three are to be under way at the same time: S has two buffers, and an adding warp
-// has its next block of S on the way to its registers while it works on the one before.
+// Per 256 x 128 logits the MMAs take 1024 cycles (d = 128; 512 at d = 64) and the exponentials as many (32 a clock and SM), so
+// both units are to be busy at the same time: S has two buffers for each key tile, and 16 warps (8 where an 8-bit cache's
+// conversion takes the registers) work on them.
 //
 // Warp roles of a CTA (one per SM):
-//  * eight warps add up weights: 32 keys of both key tiles each, half of them one half of the columns' blocks and half the other;
+//  * 16 (8) warps add up weights: those of tiles A and B, each 32 keys, and with 16 each half of the columns' blocks of 32;
 //  * eight warps, for an 8-bit cache only: make bf16 of its codes in the shared-memory tiles (their scales are factors of
 //    a thread's logits);
-//  * one walks the CTA's run and tells the others each item, one issues the MMAs, one makes the TMA loads of keys (codes), page by
-//    page, and of query rows, one reads the rows' normalisers;
-//  * four look up the places of the keys' weights and what is there, items ahead, and write the sums, an item each in turn.  (Done by the adding
-//    warps themselves, the lookups took longer than the adding where a key is seen by few rows.)
+//  * one issues the MMAs, one makes the TMA loads of keys, page by page, and of query rows, one reads the rows' normalisers.
 //
 // The items of the call are laid end to end and each CTA takes an equal run of (key block, row tile) pairs.  An item that is cut
 // leaves its sums in the workspace and a joining kernel adds them up in a fixed order.
@@ -39,15 +36,15 @@ constexpr int kSmem = 227 * 1024;
 constexpr int kExtra = 1;               // what an item costs beside its row tiles, in row tiles
 constexpr int kMaxSeqs = 16384;         // their item counts are laid out in the (still empty) rings
 
-// Warps of a CTA by role.  setmaxnreg shares out the registers that the block was launched with: 512 threads of 128, or 768 of 80.
+// Warps of a CTA by role.  setmaxnreg shares out the registers that the block was launched with: 384 threads of 168, or 640 of 96.
 template <int kKind>
 struct Roles {
     static constexpr bool kSame = kKind == SP_CACHE_SAME;
-    static constexpr int kAdd = 8, kMma = kAdd + (kSame ? 0 : 8), kTma = kMma + 1, kLse = kMma + 2, kWalk = kMma + 3, kPlace = kMma + 4;
-    static constexpr int kWarps = kPlace + 4, kThreads = 32 * kWarps;
-    static constexpr int kAddRegs = kSame ? 176 : 128, kConvertRegs = 64, kOtherRegs = kSame ? 80 : 48;
-    static_assert(kAdd * kAddRegs + (kMma - kAdd) * kConvertRegs + 8 * kOtherRegs <= kWarps * (kSame ? 128 : 80), "the roles' registers");
-    static constexpr int kReaders = kWarps - 1;                 // warps that are told the items
+    static constexpr int kAdd = 8, kMma = kAdd + (kSame ? 0 : 8), kTma = kMma + 1, kLse = kMma + 2;
+    static constexpr int kThreads = 32 * (kMma + 4);
+    static constexpr int kAddRegs = kSame ? 216 : 136, kConvertRegs = 80, kSingleRegs = kSame ? 72 : 48;
+    static_assert(kAdd * kAddRegs + (kMma - kAdd) * kConvertRegs + 4 * kSingleRegs <= (kMma + 4) * (kSame ? 168 : 96),
+                  "the roles' registers");
 };
 
 struct Cut {
@@ -60,7 +57,7 @@ struct TcArgs {
     int G, tpt;             // query heads of a KV head; new tokens of a row tile
     int P;                  // CTAs
     int box;                // rows of a TMA box
-    int k_stages, q_stages, r_stages;       // of the rings
+    int k_stages, q_stages; // of the rings
     WsHeader* hdr;
     int* err;               // [P]: 1 impossible lengths, 2 a page index out of range, 4 a wait that gave up (in bits 8-15)
     Cut* cuts;              // [P]
@@ -91,67 +88,54 @@ __device__ __forceinline__ Item item_of(const TcArgs& p, const Seq& s, int j) {
     return it;
 }
 
-// What the walking warp tells the others of an item.
 struct Segment {
-    int k0, ta, tb, tiles;  // as Item
-    int n, kv, b, g;        // new tokens and length of the sequence; sequence, KV head
-    int from, to;           // row tiles [from, to) of the item; from < 0: there is no more
-    int same;               // its one row tile is the one before
-    int pad;
-    int64_t row0;
-    int64_t pad2;
+    Item it;
+    Seq s;
+    int b, g, from, to;     // sequence, KV head; row tiles [from, to) of the item
+    bool same;              // its one row tile is the one before
 };
-static_assert(sizeof(Segment) == 64, "four words of 16 bytes");
 
-// A CTA's run, item by item: KV head, sequence, key block, row tile.  All lanes of the walking warp go together.
+// A CTA's run, item by item: KV head, sequence, key block, row tile.  Every role walks it by itself; all lanes of a warp together.
 struct Walk {
     int left, g, b, j, from;            // units (row tiles and kExtra an item) left; the next item and its first unit
-};
-struct Walker {
-    Walk w;
-    Seq s;
-    int have, blocks;                   // the sequence that s is of
     int was_b, was_g, was_ta;           // the last item, if it had one row tile
 
-    __device__ __forceinline__ Walker(const Walk& from) : w(from), have(-1), was_b(-1), was_g(0), was_ta(0) {}
-
     __device__ __forceinline__ bool next(const TcArgs& p, Segment& o) {
-        while (w.left > 0) {
-            if (have != w.b) {
-                s = load_seq(p.w.a.batch, p.w.a.cache.page, w.b);
-                blocks = blocks_of(p, s);
-                have = w.b;
-            }
-            if (w.j >= blocks) {        // the arrays were changed while the kernel ran
-                w.left = 0;
+        while (left > 0) {
+            o.s = load_seq(p.w.a.batch, p.w.a.cache.page, b);
+            const int blocks = blocks_of(p, o.s);
+            if (j >= blocks) {          // the arrays were changed while the kernel ran
+                left = 0;
                 break;
             }
-            const Item it = item_of(p, s, w.j);
-            o = Segment{it.k0, it.ta, it.tb, it.tiles, s.n, s.kv, w.b, w.g, w.from, 0, 0, 0, s.row0, 0};
-            const int to = min(it.tiles + kExtra, w.from + w.left);
-            o.to = min(it.tiles, to);
-            w.left -= to - w.from;
-            w.from = 0;
-            if (w.left > 0 && ++w.j >= blocks) next_seq(p);
+            o.it = item_of(p, o.s, j);
+            o.b = b;
+            o.g = g;
+            o.from = from;
+            const int to = min(o.it.tiles + kExtra, from + left);
+            o.to = min(o.it.tiles, to);
+            left -= to - from;
+            from = 0;
+            if (left > 0 && ++j >= blocks) next_seq(p);
             if (o.from >= o.to) continue;       // the run begins behind the item's last tile
-            const bool one = it.tiles == 1;
-            o.same = one && was_b == o.b && was_g == o.g && was_ta == it.ta;
+            const bool one = o.it.tiles == 1;
+            o.same = one && was_b == o.b && was_g == o.g && was_ta == o.it.ta;
             was_b = one ? o.b : -1;
             was_g = o.g;
-            was_ta = it.ta;
+            was_ta = o.it.ta;
             return true;
         }
         return false;
     }
     __device__ __forceinline__ void next_seq(const TcArgs& p) {
         const int lane = threadIdx.x & 31;
-        w.j = 0;
-        for (int first = w.b + 1, rounds = 0;; first += 32) {
+        j = 0;
+        for (int first = b + 1, rounds = 0;; first += 32) {
             if (first >= p.w.a.batch.B) {
                 first = 0;
-                ++w.g;
+                ++g;
                 if (++rounds > 1) {
-                    w.left = 0;
+                    left = 0;
                     return;
                 }
             }
@@ -159,7 +143,7 @@ struct Walker {
             if (first + lane < p.w.a.batch.B) n = blocks_of(p, load_seq(p.w.a.batch, p.w.a.cache.page, first + lane));
             const unsigned some = __ballot_sync(0xffffffffu, n > 0);
             if (some) {
-                w.b = first + __ffs(some) - 1;
+                b = first + __ffs(some) - 1;
                 return;
             }
         }
@@ -184,7 +168,7 @@ __device__ __forceinline__ void plan(const TcArgs& p, int* starts, int64_t* sums
     }
     if (t == 0) {
         starts[B] = (int)base;
-        *out = Walk{0, 0, 0, 0, 0};
+        *out = Walk{0, 0, 0, 0, 0, -1, 0, 0};
         p.cuts[blockIdx.x].first = 0;
     }
     __syncthreads();
@@ -220,7 +204,7 @@ __device__ __forceinline__ void plan(const TcArgs& p, int* starts, int64_t* sums
         const int64_t r = u - g * total;
         if (before <= r && r < before + mine) {
             const int from = (int)(r - before - visit(r - before));
-            *out = Walk{(int)left, g, seq, blk, from};
+            *out = Walk{(int)left, g, seq, blk, from, -1, 0, 0};
             const Item it = item_of(p, load_seq(p.w.a.batch, page, seq), blk);
             if (from > 0 && from < it.tiles && shares.at(c - 1) <= u - from)
                 p.cuts[c] = Cut{1, seq, g, it.k0, shares.of(u - from + it.tiles - 1)};
@@ -230,22 +214,20 @@ __device__ __forceinline__ void plan(const TcArgs& p, int* starts, int64_t* sums
     __syncthreads();
 }
 
-// Shared memory: rings of key tiles, of row tiles and, of an 8-bit cache, of tiles of codes; then the normalisers, the sums of the two
-// halves of the adding warps, the scales of an item's keys, the items, and the barriers.
+// Shared memory: rings of key tiles, of row tiles and, of an 8-bit cache, of tiles of codes in what is left of 224 KB; then the
+// normalisers beside S, what the halves of the adding warps exchange, and the barriers.
 template <int D, int kKind>
 struct Layout {
-    static constexpr bool kSame = kKind == SP_CACHE_SAME;
     static constexpr int kChunks = D / 64;
     static constexpr int kTileBytes = kKeys * D * 2, kCodeBytes = kKeys * D;       // a tile of K or Q; of codes
-    static constexpr int kRings = 208 * 1024 / (kSame ? kTileBytes : kCodeBytes) * (kSame ? kTileBytes : kCodeBytes);
-    static constexpr int kLs = 2, kOuts = 4, kScales = kSame ? 0 : 4, kSegs = 8;
-    static constexpr int kL = kRings, kOut = kL + kLs * 128 * 4, kScale = kOut + kOuts * 2 * kBlock * 4, kSeg = kScale + kScales * kBlock * 4,
-                         kBars = kSeg + kSegs * (int)sizeof(Segment);
-    static constexpr int kMostStages = kRings / (kSame ? kTileBytes : kCodeBytes);         // of all rings together
-    static constexpr int kBarCount = 2 * kMostStages + 4 + 2 * kOuts + 2 * 4 + 2 * kSegs + 1;
+    static constexpr int kRings = 224 * 1024, kTiles = kRings / kTileBytes;
+    static constexpr int kL = kRings, kHalf = kL + 2 * 128 * 4, kBars = kHalf + kBlock * 4;
+    static constexpr int kMostStages = kKind == SP_CACHE_SAME ? kTiles : 2 * kTiles;        // of all rings together
+    static constexpr int kBarCount = 2 * kMostStages + 4 + 4 + 1;
     static constexpr int kBad = kBars + 8 * (kBarCount + 1), kEnd = kBad + 8 + (int)sizeof(Walk);
     static_assert(kEnd <= kSmem, "");
     static_assert(kRings >= 4 * (kMaxSeqs + 2) + 8 * 32, "the plan's scratch");
+    static constexpr int kS(int w, int buf) { return (2 * buf + w) * 128; }         // TMEM columns
 };
 
 // (a, b) = (x, y) * (f, f) + (n, m), two fp32 at once
@@ -255,43 +237,37 @@ __device__ __forceinline__ void fma2n(float& a, float& b, float x, float y, floa
         : "=f"(a), "=f"(b) : "f"(x), "f"(y), "f"(f), "f"(n), "f"(m));
 }
 
-// kCols logits each of two keys to weights 2^(f v - l) (nl = -l, of each column).  The weights of a step are added to za and zb in the
-// next one (x has the last step's): added at once, each pair was waited for, which took three times as long as the rest.
-struct Sums {
-    float za[4], zb[4], xa[8], xb[8];
-};
+// kCols logits each of two keys to weights 2^(f v - l) (nl = -l, of each column), added to za and zb.
 template <int kCols>
-__device__ __forceinline__ void add_weights(const float* va, const float* vb, float fa, float fb, const float* nl, Sums& s) {
+__device__ __forceinline__ void add_weights(const float* va, const float* vb, float fa, float fb, const float* nl, float (&za)[4],
+                                            float (&zb)[4]) {
 #pragma unroll
-    for (int c = 0; c < kCols; c += 8) {
-        float n[8], ya[8], yb[8];
+    for (int c = 0; c < kCols; c += 16) {
+        float n[16], xa[16], xb[16];
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
+        for (int i = 0; i < 16; i += 4) {
             const float4 x = *reinterpret_cast<const float4*>(nl + c + i);
             n[i] = x.x, n[i + 1] = x.y, n[i + 2] = x.z, n[i + 3] = x.w;
         }
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            fma2n(ya[i], ya[i + 1], va[c + i], va[c + i + 1], fa, n[i], n[i + 1]);
-            fma2n(yb[i], yb[i + 1], vb[c + i], vb[c + i + 1], fb, n[i], n[i + 1]);
+        for (int i = 0; i < 16; i += 2) {
+            fma2n(xa[i], xa[i + 1], va[c + i], va[c + i + 1], fa, n[i], n[i + 1]);
+            fma2n(xb[i], xb[i + 1], vb[c + i], vb[c + i + 1], fb, n[i], n[i + 1]);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            ya[i] = ex2_approx(ya[i]);
-            yb[i] = ex2_approx(yb[i]);
-        }
+        for (int i = 0; i < 16; ++i) xa[i] = ex2_approx(xa[i]);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            add2(s.za[i & 2], s.za[(i & 2) + 1], s.xa[i], s.xa[i + 1]);
-            add2(s.zb[i & 2], s.zb[(i & 2) + 1], s.xb[i], s.xb[i + 1]);
-        }
+        for (int i = 0; i < 16; ++i) xb[i] = ex2_approx(xb[i]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s.xa[i] = ya[i], s.xb[i] = yb[i];
+        for (int i = 0; i < 16; i += 2) {
+            add2(za[i & 2], za[(i & 2) + 1], xa[i], xa[i + 1]);
+            add2(zb[i & 2], zb[(i & 2) + 1], xb[i], xb[i + 1]);
+        }
     }
 }
 
-// A wait of few instructions, as there are some twenty of them: with wait_bar's clock at each, the roles' loops no longer fitted into the
-// instruction cache (58% hits).  It gives up after 2^26 looks, which take seconds.
+// A wait of few instructions, as there are some twenty of them: with wait_bar's clock at each, the roles' loops fit less well into the
+// instruction cache.  It gives up after 2^26 looks, which take seconds.
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag, int where) {
     bool ok = true;
     for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
@@ -316,33 +292,26 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
         if (threadIdx.x == 0) p.err[blockIdx.x] = 4 | 9 << 8, p.cuts[blockIdx.x].first = 0;
         return;
     }
-    const int ks = p.k_stages, qs = p.q_stages, rs = p.r_stages;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+    const int ks = p.k_stages, qs = p.q_stages, rs = kSame ? 0 : (L::kTiles - ks - qs) * 2;
     uint64_t* k_full = bars;                    // [ks] a key tile is ready
     uint64_t* q_full = k_full + ks;             // [qs] a row tile
     uint64_t* r_full = q_full + qs;             // [rs] a tile of codes
     uint64_t* k_empty = bars + L::kMostStages;  // the MMAs have read it
     uint64_t* q_empty = k_empty + ks;
     uint64_t* r_empty = q_empty + qs;           // it is converted
-    uint64_t* s_full = bars + 2 * L::kMostStages;       // [2] S of both key tiles is in TMEM, and the rows' normalisers are there
-    uint64_t* s_empty = s_full + 2;             // the adding warps have used it
-    uint64_t* o_full = s_empty + 2;             // [4] the sums of an item's keys, a place for each warp that writes them: two warps waiting
-                                                // for phases of one barrier might be more than a phase apart
-    uint64_t* o_empty = o_full + L::kOuts;
-    uint64_t* c_full = o_empty + L::kOuts;      // [4] the scales of an item's keys
-    uint64_t* c_empty = c_full + 4;
-    uint64_t* g_full = c_empty + 4;             // [8] an item
-    uint64_t* g_empty = g_full + L::kSegs;
-    uint64_t* final_bar = g_empty + L::kSegs;
+    uint64_t* s_full = bars + 2 * L::kMostStages;       // [2] S of both key tiles, and the rows' normalisers, in buffer 0 or 1
+    uint64_t* s_empty = s_full + 2;
+    uint64_t* x_full = s_empty + 2;             // [2] the sums of key tile A or B that the other half has are there
+    uint64_t* x_empty = x_full + 2;
+    uint64_t* final_bar = x_empty + 2;
     uint8_t *k_ring = smem, *q_ring = smem + ks * L::kTileBytes, *r_ring = q_ring + qs * L::kTileBytes;
     volatile uint32_t* tmem_sh = reinterpret_cast<volatile uint32_t*>(final_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_sh + 1);
     int* bad = reinterpret_cast<int*>(smem + L::kBad);                          // [2] impossible lengths; a page index out of range
     Walk* start = reinterpret_cast<Walk*>(bad + 2);
     float* ls = reinterpret_cast<float*>(smem + L::kL);                         // [2][128] -l
-    float* outs = reinterpret_cast<float*>(smem + L::kOut);                     // [4][half][256]
-    float* scales = reinterpret_cast<float*>(smem + L::kScale);                 // [4][256]
-    Segment* segs = reinterpret_cast<Segment*>(smem + L::kSeg);
+    float* halves = reinterpret_cast<float*>(smem + L::kHalf);                  // [2][128] tile A's sums of the second half, tile B's of the first
 
     const AttendProblem& a = p.w.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -358,16 +327,8 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&s_full[i]), 2);             // the MMAs and the normalisers
             mbar_init(smem_u32(&s_empty[i]), W::kAdd);
-        }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(smem_u32(&o_full[i]), W::kAdd);
-            mbar_init(smem_u32(&o_empty[i]), 1);
-            mbar_init(smem_u32(&c_full[i]), 1);
-            mbar_init(smem_u32(&c_empty[i]), W::kAdd);
-        }
-        for (int i = 0; i < L::kSegs; ++i) {
-            mbar_init(smem_u32(&g_full[i]), 1);
-            mbar_init(smem_u32(&g_empty[i]), W::kReaders);
+            mbar_init(smem_u32(&x_full[i]), 4);
+            mbar_init(smem_u32(&x_empty[i]), 4);
         }
         mbar_init(smem_u32(final_bar), 1);
         *abort_flag = 0;
@@ -386,132 +347,129 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
     const uint32_t tmem = *tmem_sh;
     cudaTriggerProgrammaticLaunchCompletion();
     plan(p, reinterpret_cast<int*>(smem), reinterpret_cast<int64_t*>(smem + 4 * (kMaxSeqs + 2)), start, bad);
-
-    // the next item as the walking warp tells it; false: there is none, or the kernel gives up
-    int seg_at = 0;
-    uint32_t seg_ph = 0;
-    Segment sg{};
-    auto two_of = [&] { return sg.k0 + kKeys < sg.kv; };            // tile B has keys
-    auto next_segment = [&] {
-        if (!wait_all(smem_u32(&g_full[seg_at]), seg_ph, abort_flag, 11)) return false;
-        sg = segs[seg_at];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&g_empty[seg_at]));
-        if (++seg_at == L::kSegs) seg_at = 0, seg_ph ^= 1;
-        return sg.from >= 0;
-    };
+    Walk walk = *start;
+    Segment sg;
+    auto two_of = [&](const Segment& x) { return x.it.k0 + kKeys < x.s.kv; };       // tile B has keys
 
     if (warp < W::kAdd) {
         // ------------------------------ weights ------------------------------
-        // A warp has 32 keys of each tile, and every other block of kB columns: a thread's two keys share what it reads of a column.
-        // Blocks go through two sets of registers; a tile's last one is worked on when the next tile's first is on its way.
+        // A warp has 32 keys of each tile, and every other block of 32 columns: a thread's two keys share what it reads of a column
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(W::kAddRegs));
-        constexpr int kB = kSame ? 32 : 16;
         const int h = warp >> 2, row = (warp & 3) * 32 + lane;      // half of the blocks; key of the tile = TMEM lane
         const uint32_t s_at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float f = a.scale * 1.4426950408889634f;
-        uint32_t buf = 0, ph_s = 0, lst = 0, out = 0, ph_o = 1, cst = 0, ph_c = 0;
-        float fa = f, fb = f, total[2] = {0.f, 0.f};
-        Sums sums = {};
-        uint32_t r0[2 * kB];
-        auto load = [&](uint32_t* sr, uint32_t at) {
-            if constexpr (kB == 32) {
-                tmem_ld32(at, sr);
-                tmem_ld32(at + 128, sr + kB);
-            } else {
-                tmem_ld16(at, sr);
-                tmem_ld16(at + 128, sr + kB);
-            }
+        constexpr int kB = kSame ? 32 : 16;     // columns of a block
+        int buf = 0;
+        uint32_t ph_s = 0, ph_x = 0;
+        bool ok = true;
+        // this thread's keys of an item: the place of their weights (-1: none), what is there (of the key that it writes: the first half
+        // tile A's, the second tile B's), and the scale of their rows
+        struct Place {
+            int64_t at;
+            float old, scale[2];
         };
-        auto loaded = [&](uint32_t* sr) {
-            tmem_wait32(sr);
-            if constexpr (kB == 32) keep32(sr + 32);
-        };
-        auto use = [&](const uint32_t* sr, int nl) {
-            const float* v = reinterpret_cast<const float*>(sr);
-            add_weights<kB>(v, v + kB, fa, fb, ls + nl, sums);
-        };
-        auto flush = [&] {              // a tile's sums to the item's
+        auto place = [&](const Segment& x) {
+            Place r{-1, 0.f, {1.f, 1.f}};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                sums.za[i & 3] += sums.xa[i];
-                sums.zb[i & 3] += sums.xb[i];
-            }
-            total[0] += (sums.za[0] + sums.za[1]) + (sums.za[2] + sums.za[3]);
-            total[1] += (sums.zb[0] + sums.zb[1]) + (sums.zb[2] + sums.zb[3]);
-            sums = {};
-        };
-        auto finish = [&] {             // an item's sums to the warps that write them
-            if (!wait_all(smem_u32(&o_empty[out]), ph_o, abort_flag, 23)) return false;
-            float* o = outs + (out * 2 + h) * kBlock + row;
-            o[0] = total[0];
-            o[kKeys] = total[1];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&o_full[out]));
-            if (++out == L::kOuts) out = 0, ph_o ^= 1;
-            total[0] = total[1] = 0.f;
-            return true;
-        };
-        // takes out the columns that do not see a key (one that no row has holds anything)
-        auto hide = [&](uint32_t* sr, uint32_t sees, float f) {
-            const uint32_t gone = __float_as_uint(f < 0.f ? INFINITY : -INFINITY);
-#pragma unroll
-            for (int k = 0; k < kB; ++k)
-                if (!(sees >> k & 1)) sr[k] = gone;
-        };
-        bool ok = true, open = false;       // an item still to be finished
-        int i = 0, t0 = 0;
-        sg.to = 0;
-        while (ok) {
-            const bool begins = i == sg.to;
-            if (begins) {
-                if (open) ok = finish();
-                open = true;
-                if (!ok || !next_segment()) break;
-                i = sg.from;
-                t0 = sg.ta + i * p.tpt;
-                if constexpr (!kSame) {
-                    ok = wait_all(smem_u32(&c_full[cst]), ph_c, abort_flag, 24);
-                    if (!ok) break;
-                    fa = f * scales[cst * kBlock + row];
-                    fb = f * scales[cst * kBlock + kKeys + row];
-                    if (fa == 0.f) fa = FLT_MIN;        // so that what is hidden vanishes
-                    if (fb == 0.f) fb = FLT_MIN;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&c_empty[cst]));
-                    if (++cst == 4) cst = 0, ph_c ^= 1;
+            for (int w = 0; w < 2; ++w) {
+                const int key = x.it.k0 + w * kKeys + row;
+                if (key >= x.s.kv || key < first_seen(x.s, a.window) || (kSame && w != h)) continue;
+                const int q = a.page_of(key), pg = __ldg(a.batch.table + (int64_t)x.b * a.batch.table_stride + q);
+                if ((unsigned)pg >= (unsigned)a.cache.pages) {
+                    bad[1] = 1;
+                    continue;
                 }
+                const int64_t at = scale_offset(a.cache, pg, x.g, key - q * a.cache.page);
+                if constexpr (!kSame) r.scale[w] = __ldg(a.cache.k_scale + at);
+                if (w != h) continue;
+                r.at = at;
+                if (key < x.s.kv - x.s.n && p.w.decay != 0.f && x.to == x.it.tiles && x.from == 0) r.old = p.w.weights[at];
             }
-            const int ctx = sg.kv - sg.n, tokens = min(p.tpt, sg.tb - t0), rows = tokens * p.G;
-            ok = wait_all(smem_u32(&s_full[buf]), ph_s, abort_flag, 22);
-            if (!ok) break;
-            tc_fence_after();
-            const bool masked = sg.k0 + kBlock - 1 > ctx + t0 || (a.window && sg.k0 <= ctx + t0 + tokens - 1 - a.window) || rows % kB;
-            const uint32_t at = s_at + buf * 256 + h * kB;
-            const int nl = lst * 128 + h * kB;
+            return r;
+        };
+        bool more = walk.next(p, sg);
+        Place cur = {-1, 0.f, {1.f, 1.f}};
+        if (more) cur = place(sg);
+        while (more && ok) {
+            Segment next;
+            const bool then = walk.next(p, next);
+            Place ahead = {-1, 0.f, {1.f, 1.f}};
+            if (then) ahead = place(next);
+            const int ctx = sg.s.kv - sg.s.n;
+            // (a row of scale 0 has the smallest one, so that what is hidden vanishes)
+            const float fa = kSame ? f : cur.scale[0] == 0.f ? FLT_MIN : f * cur.scale[0], fb = kSame ? f : cur.scale[1] == 0.f ? FLT_MIN : f * cur.scale[1];
+            float total[2] = {0.f, 0.f};
+            int t0 = sg.it.ta + sg.from * p.tpt;
+            for (int i = sg.from; i < sg.to; ++i, t0 += p.tpt) {
+                const int tokens = min(p.tpt, sg.it.tb - t0), rows = tokens * p.G;
+                ok = wait_all(smem_u32(&s_full[buf]), ph_s, abort_flag, 22);
+                if (!ok) break;
+                tc_fence_after();
+                const bool masked = sg.it.k0 + kBlock - 1 > ctx + t0 || (a.window && sg.it.k0 <= ctx + t0 + tokens - 1 - a.window) || rows % kB;
+                const uint32_t at = s_at + buf * 256;
+                const float* nl = ls + buf * 128;
+                float za[4] = {0.f, 0.f, 0.f, 0.f}, zb[4] = {0.f, 0.f, 0.f, 0.f};
+                // 32 columns at a time, or 16 with fewer registers.  (The next ones on their way meanwhile took more registers than there
+                // are: a chunk of 4096 over 32768 903 us for 812.)
 #pragma unroll 1
-            for (int c = 0; c < 128 && c + h * kB < rows; c += 2 * kB) {
-                load(r0, at + c);
-                loaded(r0);
-                if (masked) {
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const int ahead = sg.k0 + w * kKeys + row - ctx - t0, c0 = h * kB + c;
-                        const int hi = a.window ? min(max(ahead + a.window, 0), tokens) * p.G : rows, lo = min(max(ahead, 0), tokens) * p.G;
-                        hide(r0 + w * kB, low_bits(hi - c0) & ~low_bits(lo - c0), w ? fb : fa);
+                for (int c = h * kB; c < rows; c += 2 * kB) {
+                    uint32_t sr[2 * kB];
+                    if constexpr (kB == 32) {
+                        tmem_ld32(at + c, sr);
+                        tmem_ld32(at + 128 + c, sr + kB);
+                        tmem_wait32(sr);
+                        keep32(sr + 32);
+                    } else {
+                        tmem_ld16(at + c, sr);
+                        tmem_ld16(at + 128 + c, sr + kB);
+                        tmem_wait32(sr);
                     }
+                    if (masked) {           // takes out the columns that do not see a key; one that no row has holds anything
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            const int ahead_of = sg.it.k0 + w * kKeys + row - ctx - t0;
+                            const int hi = a.window ? min(max(ahead_of + a.window, 0), tokens) * p.G : rows, lo = min(max(ahead_of, 0), tokens) * p.G;
+                            const uint32_t sees = low_bits(hi - c) & ~low_bits(lo - c);
+                            const uint32_t gone = __float_as_uint((w ? fb : fa) < 0.f ? INFINITY : -INFINITY);
+#pragma unroll
+                            for (int k = 0; k < kB; ++k)
+                                if (!(sees >> k & 1)) sr[w * kB + k] = gone;
+                        }
+                    }
+                    const float* v = reinterpret_cast<const float*>(sr);
+                    add_weights<kB>(v, v + kB, fa, fb, nl + c, za, zb);
                 }
-                use(r0, nl + c);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&s_empty[buf]));
+                total[0] += (za[0] + za[1]) + (za[2] + za[3]);
+                total[1] += (zb[0] + zb[1]) + (zb[2] + zb[3]);
+                ph_s ^= buf;
+                buf ^= 1;
             }
-            flush();
-            tc_fence_before();
+            if (!ok) break;
+            // The halves exchange their sums: the first half of the warps writes tile A's keys and the second half tile B's.  (No named
+            // barrier: a warp that gives up a wait would leave the others at it.)
+            ok = wait_all(smem_u32(&x_empty[1 - h]), ph_x ^ 1, abort_flag, 23);
+            if (!ok) break;
+            halves[(1 - h) * kKeys + row] = total[1 - h];
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&s_empty[buf]));
-            ph_s ^= buf;
-            buf ^= 1;
-            if (++lst == L::kLs) lst = 0;
-            ++i;
-            t0 += p.tpt;
+            if (lane == 0) mbar_arrive(smem_u32(&x_full[1 - h]));
+            ok = wait_all(smem_u32(&x_full[h]), ph_x, abort_flag, 24);
+            if (!ok) break;
+            const float sum = h ? halves[kKeys + row] + total[1] : total[0] + halves[row];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&x_empty[h]));
+            ph_x ^= 1;
+            if (sg.from == 0 && sg.to == sg.it.tiles) {
+                if (cur.at >= 0) p.w.weights[cur.at] = p.w.decay != 0.f ? sum + p.w.decay * cur.old : sum;
+            } else {
+                p.parts[((int64_t)blockIdx.x * 2 + (sg.from == 0 ? 1 : 0)) * kBlock + h * kKeys + row] = sum;
+            }
+            __syncwarp();
+            sg = next;
+            cur = ahead;
+            more = then;
         }
     } else if (!kSame && warp < W::kMma) {
       if constexpr (!kSame) {
@@ -524,8 +482,8 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
         int st = 0, rst = 0;
         uint32_t ph = 1, ph_r = 0;
         bool ok = true;
-        while (ok && next_segment()) {
-            for (int w = 0; w < (two_of() ? 2 : 1); ++w) {
+        while (ok && walk.next(p, sg)) {
+            for (int w = 0; w < (two_of(sg) ? 2 : 1); ++w) {
                 ok = wait_all(smem_u32(&r_full[rst]), ph_r, abort_flag, 62);
                 if (!ok) break;
                 uint4 codes[kRounds];
@@ -548,10 +506,9 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
 #pragma unroll
                     for (int k = 0; k < 4; ++k) pairs_of<kKind, true>(w4[k], o[2 * k], o[2 * k + 1]);
                     uint8_t* at = tile + (piece >> 2) * (kKeys * 128) + rr * 128;
-                    const int c0 = 2 * (piece & 3), flip = D == 128 ? piece >> 2 : 0;
-                    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-                    *reinterpret_cast<uint4*>(at + (((c0 + flip) ^ (rr & 7)) << 4)) = flip ? hi : lo;
-                    *reinterpret_cast<uint4*>(at + (((c0 + 1 - flip) ^ (rr & 7)) << 4)) = flip ? lo : hi;
+                    const int c0 = 2 * (piece & 3);
+                    *reinterpret_cast<uint4*>(at + ((c0 ^ (rr & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(at + (((c0 + 1) ^ (rr & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -561,7 +518,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
         }
       }
     } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kOtherRegs));
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kSingleRegs));
       if (warp == W::kMma) {
         // ------------------------------ MMAs ------------------------------
         const bool lead = elect_one();
@@ -570,8 +527,8 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
         int kst = 0, qst = 0;
         uint32_t ph_k = 0, ph_q = 0, buf = 0, ph_s = 1;         // a fresh barrier counts as completed for the odd parity
         bool ok = tmem == 0, first = true;
-        while (ok && next_segment()) {
-            const bool two = two_of();
+        while (ok && walk.next(p, sg)) {
+            const bool two = two_of(sg);
             // the last tile's place is given back now: it is used again by an item that has the same
             if (!first && !sg.same) {
                 commit_if(lead, smem_u32(&q_empty[qst]));
@@ -582,7 +539,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
             ok = wait_all(smem_u32(&k_full[kst]), ph_k, abort_flag, 32) &&
                  (!two || wait_all(smem_u32(&k_full[k1]), ph_k ^ (k1 == 0), abort_flag, 32));
             if (!ok) break;
-            int left = sg.tb - (sg.ta + sg.from * p.tpt);
+            int left = sg.it.tb - (sg.it.ta + sg.from * p.tpt);
             for (int i = sg.from; i < sg.to; ++i, left -= p.tpt) {
                 const uint32_t idesc = instr_desc((min(p.tpt, left) * p.G + 15) & ~15, false);
                 if (!(sg.same && i == sg.from)) ok = wait_all(smem_u32(&q_full[qst]), ph_q, abort_flag, 31);
@@ -593,7 +550,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     if (w == 1 && !two) break;
-                    const uint32_t ka = k_lo + (w ? k1 : kst) * (L::kTileBytes >> 4), d = w * 128 + buf * 256;
+                    const uint32_t ka = k_lo + (w ? k1 : kst) * (L::kTileBytes >> 4), d = L::kS(w, 0) + buf * 256;
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t off = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
@@ -638,38 +595,30 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
         int kst = 0, qst = 0, k_loads = 0, q_loads = 0;
         uint32_t ph_k = 1, ph_q = 1;
         bool ok = true, first = true;
-        while (ok && next_segment()) {
+        while (ok && walk.next(p, sg)) {
             const int32_t* table = a.batch.table + (int64_t)sg.b * a.batch.table_stride;
-            const int seen = a.window ? max(0, sg.kv - sg.n - a.window + 1) : 0;
-            // this lane's boxes: their pages (pages: none, which loads zeros) and first slots
-            int slot[2], pg[2];
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const int tok = sg.k0 + w * kKeys + lane * p.box;
-                slot[w] = 0, pg[w] = -1;
-                if (lane < boxes && tok < sg.kv && tok + p.box > seen) {
-                    const int q = a.page_of(tok);
-                    pg[w] = __ldg(table + q);
-                    slot[w] = tok - q * c.page;
-                    if ((unsigned)pg[w] >= (unsigned)c.pages) bad[1] = 1;
+            const int seen = first_seen(sg.s, a.window);
+            for (int w = 0; w < (two_of(sg) ? 2 : 1); ++w) {
+                // this lane's box: its page (pages: none, which loads zeros) and its first slot
+                const int tok = sg.it.k0 + w * kKeys + lane * p.box;
+                int slot = 0, pg = (int)c.pages;
+                if (lane < boxes && tok < sg.s.kv && tok + p.box > seen) {
+                    const int q = a.page_of(tok), t = __ldg(table + q);
+                    if (t >= 0 && t < c.pages) pg = t, slot = tok - q * c.page;
+                    else bad[1] = 1;
                 }
-            }
-            for (int w = 0; w < (two_of() ? 2 : 1); ++w) {
                 ok = wait_all(smem_u32(&t_empty[kst]), ph_k, abort_flag, 41);
                 if (!ok) break;
                 const uint32_t bar = smem_u32(&t_full[kst]), at = smem_u32(t_ring) + kst * kBytes;
                 if (lane == 0) mbar_expect_tx(bar, kBytes);
                 __syncwarp();
                 if (lane < boxes) {
-                    const int page = w ? pg[1] : pg[0], from = w ? slot[1] : slot[0];
-                    const bool there = (unsigned)page < (unsigned)c.pages;
                     if constexpr (kSame) {
 #pragma unroll
                         for (int ch = 0; ch < L::kChunks; ++ch)
-                            tma_load_4d(at + ch * (kKeys * 128) + lane * p.box * 128, &maps.k, ch * 64, there ? from : 0, sg.g,
-                                        there ? page : (int)c.pages, bar);
+                            tma_load_4d(at + ch * (kKeys * 128) + lane * p.box * 128, &maps.k, ch * 64, slot, sg.g, pg, bar);
                     } else {
-                        tma_load_4d(at + lane * p.box * D, &maps.k, 0, there ? from : 0, sg.g, there ? page : (int)c.pages, bar);
+                        tma_load_4d(at + lane * p.box * D, &maps.k, 0, slot, sg.g, pg, bar);
                     }
                 }
                 ++k_loads;
@@ -687,7 +636,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
                         mbar_expect_tx(bar, (uint32_t)(rows_tile * D * 2));
                         for (int ch = 0; ch < L::kChunks; ++ch)
                             tma_load_3d(smem_u32(q_ring) + qst * L::kTileBytes + ch * (kKeys * 128), &maps.q, ch * 64, sg.g * p.G,
-                                        (int)(sg.row0 + sg.ta + i * p.tpt), bar);
+                                        (int)(sg.s.row0 + sg.it.ta + i * p.tpt), bar);
                     }
                     ++q_loads;
                 }
@@ -710,99 +659,27 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
       } else if (warp == W::kLse) {
         // ------------------------------ normalisers ------------------------------
         // they lie beside S: the same barriers say when the place is free and that they are there
-        uint32_t buf = 0, ph_s = 1, lst = 0;
+        uint32_t buf = 0, ph_s = 1;
         bool ok = true;
-        while (ok && next_segment()) {
+        while (ok && walk.next(p, sg)) {
             for (int i = sg.from; i < sg.to; ++i) {
-                const int t0 = sg.ta + i * p.tpt, rows = min(p.tpt, sg.tb - t0) * p.G;
+                const int t0 = sg.it.ta + i * p.tpt, rows = min(p.tpt, sg.it.tb - t0) * p.G;
                 float l[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int r = lane + 32 * k, t = r / p.G;
                     l[k] = 0.f;         // columns of no row are masked
-                    if (r < rows) l[k] = __ldg(a.lse + (sg.row0 + t0 + t) * a.lse_stride_row + (sg.g * p.G + r - t * p.G) * a.lse_stride_head);
+                    if (r < rows) l[k] = a.lse[(sg.s.row0 + t0 + t) * a.lse_stride_row + (sg.g * p.G + r - t * p.G) * a.lse_stride_head];
                 }
                 ok = wait_all(smem_u32(&s_empty[buf]), ph_s, abort_flag, 51);
                 if (!ok) break;
                 // a row that saw no token has the sum 0, whose logarithm is -inf, and gives nothing
 #pragma unroll
-                for (int k = 0; k < 4; ++k) ls[lst * 128 + lane + 32 * k] = l[k] == -INFINITY ? -INFINITY : l[k] * -1.4426950408889634f;
+                for (int k = 0; k < 4; ++k) ls[buf * 128 + lane + 32 * k] = l[k] == -INFINITY ? -INFINITY : l[k] * -1.4426950408889634f;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&s_full[buf]));
                 ph_s ^= buf;
                 buf ^= 1;
-                if (++lst == L::kLs) lst = 0;
-            }
-        }
-      } else if (warp == W::kWalk) {
-        // ------------------------------ the items ------------------------------
-        Walker walker(*start);
-        uint32_t ph = 1;
-        for (bool more = true; more;) {
-            more = walker.next(p, sg);
-            if (!more) sg.from = -1;
-            if (!wait_all(smem_u32(&g_empty[seg_at]), ph, abort_flag, 12)) break;
-            if (lane == 0) {
-                segs[seg_at] = sg;
-                mbar_arrive(smem_u32(&g_full[seg_at]));
-            }
-            __syncwarp();
-            if (++seg_at == L::kSegs) seg_at = 0, ph ^= 1;
-        }
-      } else {
-        // ------------------------------ places ------------------------------
-        // Each warp has every fourth item, eight of its keys a lane: it looks their places, scales and old weights up well ahead, and
-        // writes their sums when they are there.
-        const int mine = warp - W::kPlace;
-        uint32_t item = 0;              // of the CTA's run
-        for (bool ok = true; ok && next_segment(); ++item) {
-            if ((item & 3) != mine) continue;
-            const int seen = a.window ? max(0, sg.kv - sg.n - a.window + 1) : 0;
-            const int32_t* table = a.batch.table + (int64_t)sg.b * a.batch.table_stride;
-            const bool whole = sg.from == 0 && sg.to == sg.tiles;
-            int64_t at[8];              // -1: no key, or no page
-            float old[8];
-            int pg[8];
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-                const int key = sg.k0 + lane + 32 * y;
-                pg[y] = key < sg.kv && key >= seen ? __ldg(table + a.page_of(key)) : -1;
-            }
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-                const int key = sg.k0 + lane + 32 * y;
-                const bool there = (unsigned)pg[y] < (unsigned)a.cache.pages;
-                if (!there && key < sg.kv && key >= seen) bad[1] = 1;
-                at[y] = there ? scale_offset(a.cache, pg[y], sg.g, key - a.page_of(key) * a.cache.page) : -1;
-                old[y] = 0.f;
-                if (there && key < sg.kv - sg.n && p.w.decay != 0.f && whole) old[y] = p.w.weights[at[y]];
-            }
-            if constexpr (!kSame) {
-                float scale[8];
-#pragma unroll
-                for (int y = 0; y < 8; ++y) scale[y] = at[y] >= 0 ? __ldg(a.cache.k_scale + at[y]) : 1.f;
-                ok = wait_all(smem_u32(&c_empty[mine]), (item >> 2 & 1) ^ 1, abort_flag, 72);
-                if (!ok) break;
-#pragma unroll
-                for (int y = 0; y < 8; ++y) scales[mine * kBlock + lane + 32 * y] = scale[y];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&c_full[mine]));
-            }
-            ok = wait_all(smem_u32(&o_full[mine]), item >> 2 & 1, abort_flag, 71);
-            if (!ok) break;
-            float sum[8];
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-                const float* o = outs + mine * 2 * kBlock + lane + 32 * y;
-                sum[y] = o[0] + o[kBlock];
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&o_empty[mine]));
-            float* part = p.parts + ((int64_t)blockIdx.x * 2 + (sg.from == 0 ? 1 : 0)) * kBlock + lane;
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-                if (!whole) part[32 * y] = sum[y];
-                else if (at[y] >= 0) p.w.weights[at[y]] = p.w.decay != 0.f ? sum[y] + p.w.decay * old[y] : sum[y];
             }
         }
       }
@@ -908,12 +785,9 @@ sp_status weights_tc_launch(const WeightsProblem& w, void* ws, cudaStream_t st) 
     p.P = sm_count();
     p.box = std::min(128, a.cache.page & -a.cache.page);
     const bool same = a.cache.kind == SP_CACHE_SAME;
-    // 208 KB: six tiles of keys and query rows at d = 128 (twice as many at d = 64), more of keys where the rows stay; or of an 8-bit
-    // cache three, two, and three of codes
-    const int twice = a.cache.d == 64 ? 2 : 1;
-    p.k_stages = (same && a.batch.max_new <= p.tpt ? 4 : 3) * twice;
-    p.q_stages = (same ? 6 * twice - p.k_stages : 2 * twice);
-    p.r_stages = same ? 0 : 3 * twice;
+    const int tiles = 224 * 1024 / (kKeys * a.cache.d * 2);
+    p.k_stages = same ? (a.cache.d == 128 ? 4 : 8) : (a.cache.d == 128 ? 3 : 6);
+    p.q_stages = same ? tiles - p.k_stages : (a.cache.d == 128 ? 2 : 4);
     const Space s = carve(p.P);
     char* base = static_cast<char*>(ws);
     p.hdr = static_cast<WsHeader*>(ws);
