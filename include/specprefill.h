@@ -514,7 +514,8 @@ size_t sp_tree_workspace_size(void);
  *   positions  device int32 [T], or NULL: kv_len - (new tokens) + the number of tokens that row r hangs on
  *
  * Rows that are not a token of the batch are not written.  The batch's table is not read.  A parent that is not a token before
- * its row counts as -1, and SP_EDEVICE is recorded in the workspace. */
+ * its row counts as -1, and SP_EDEVICE is recorded in the workspace; a sequence of more than 4096 new tokens is left out, and
+ * SP_EDEVICE recorded as well. */
 sp_status sp_tree_seen(const sp_batch* batch, const int32_t* parent, uint32_t* seen, int64_t seen_stride, int seen_words,
                        int32_t* positions, void* ws, size_t ws_bytes, void* stream);
 

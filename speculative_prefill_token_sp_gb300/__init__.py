@@ -963,7 +963,7 @@ def tree_seen(batch, parent, *, seen=None, positions=None, ws=None, stream=None,
     """What the batch's new tokens see if they are drafted ones that form a tree: parent int32 [rows], the new token of the
     same sequence that each hangs on, counted from the sequence's first and before its child, or -1.  Returns (seen int32
     [rows, words], the bits that attend_tree takes, and positions int32 [rows], which rotary takes).  Rows that are not
-    a token of the batch are not written."""
+    a token of the batch are not written.  At most 4096 new tokens a sequence."""
     device, rows = batch.device, batch.rows
     words = max(1, -(-batch.max_new // 32))
     _check_ints(parent, "parent", (rows,), device)

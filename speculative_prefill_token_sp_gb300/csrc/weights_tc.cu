@@ -22,7 +22,6 @@
 // leaves its sums in the workspace and a joining kernel adds them up in a fixed order.
 #include "tc_tiles.cuh"
 
-#include <float.h>
 #include <string.h>
 
 #include <algorithm>
@@ -237,10 +236,11 @@ __device__ __forceinline__ void fma2n(float& a, float& b, float x, float y, floa
         : "=f"(a), "=f"(b) : "f"(x), "f"(y), "f"(f), "f"(n), "f"(m));
 }
 
-// kCols logits each of two keys to weights 2^(f v - l) (nl = -l, of each column), added to za and zb.
-template <int kCols>
-__device__ __forceinline__ void add_weights(const float* va, const float* vb, float fa, float fb, const float* nl, float (&za)[4],
-                                            float (&zb)[4]) {
+// kCols logits each of two keys to weights 2^(f v - l) (nl = -l, of each column), those of the rows that see them added to za and zb.
+// What is hidden is taken out last: a column of no row holds anything, and l or the scale in f may be NaN.
+template <bool kMasked, int kCols>
+__device__ __forceinline__ void add_weights(const float* va, const float* vb, float fa, float fb, const float* nl, uint32_t sees_a,
+                                            uint32_t sees_b, float (&za)[4], float (&zb)[4]) {
 #pragma unroll
     for (int c = 0; c < kCols; c += 16) {
         float n[16], xa[16], xb[16];
@@ -255,9 +255,15 @@ __device__ __forceinline__ void add_weights(const float* va, const float* vb, fl
             fma2n(xb[i], xb[i + 1], vb[c + i], vb[c + i + 1], fb, n[i], n[i + 1]);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) xa[i] = ex2_approx(xa[i]);
+        for (int i = 0; i < 16; ++i) {
+            xa[i] = ex2_approx(xa[i]);
+            if (kMasked && !(sees_a >> (c + i) & 1)) xa[i] = 0.f;
+        }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) xb[i] = ex2_approx(xb[i]);
+        for (int i = 0; i < 16; ++i) {
+            xb[i] = ex2_approx(xb[i]);
+            if (kMasked && !(sees_b >> (c + i) & 1)) xb[i] = 0.f;
+        }
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
             add2(za[i & 2], za[(i & 2) + 1], xa[i], xa[i + 1]);
@@ -396,8 +402,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
             Place ahead = {-1, 0.f, {1.f, 1.f}};
             if (then) ahead = place(next);
             const int ctx = sg.s.kv - sg.s.n;
-            // (a row of scale 0 has the smallest one, so that what is hidden vanishes)
-            const float fa = kSame ? f : cur.scale[0] == 0.f ? FLT_MIN : f * cur.scale[0], fb = kSame ? f : cur.scale[1] == 0.f ? FLT_MIN : f * cur.scale[1];
+            const float fa = kSame ? f : f * cur.scale[0], fb = kSame ? f : f * cur.scale[1];
             float total[2] = {0.f, 0.f};
             int t0 = sg.it.ta + sg.from * p.tpt;
             for (int i = sg.from; i < sg.to; ++i, t0 += p.tpt) {
@@ -424,20 +429,19 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
                         tmem_ld16(at + 128 + c, sr + kB);
                         tmem_wait32(sr);
                     }
-                    if (masked) {           // takes out the columns that do not see a key; one that no row has holds anything
+                    const float* v = reinterpret_cast<const float*>(sr);
+                    if (masked) {
+                        uint32_t sees[2];           // the columns that see each key
 #pragma unroll
                         for (int w = 0; w < 2; ++w) {
                             const int ahead_of = sg.it.k0 + w * kKeys + row - ctx - t0;
                             const int hi = a.window ? min(max(ahead_of + a.window, 0), tokens) * p.G : rows, lo = min(max(ahead_of, 0), tokens) * p.G;
-                            const uint32_t sees = low_bits(hi - c) & ~low_bits(lo - c);
-                            const uint32_t gone = __float_as_uint((w ? fb : fa) < 0.f ? INFINITY : -INFINITY);
-#pragma unroll
-                            for (int k = 0; k < kB; ++k)
-                                if (!(sees >> k & 1)) sr[w * kB + k] = gone;
+                            sees[w] = low_bits(hi - c) & ~low_bits(lo - c);
                         }
+                        add_weights<true, kB>(v, v + kB, fa, fb, nl + c, sees[0], sees[1], za, zb);
+                    } else {
+                        add_weights<false, kB>(v, v + kB, fa, fb, nl + c, 0u, 0u, za, zb);
                     }
-                    const float* v = reinterpret_cast<const float*>(sr);
-                    add_weights<kB>(v, v + kB, fa, fb, nl + c, za, zb);
                 }
                 tc_fence_before();
                 __syncwarp();

@@ -129,6 +129,80 @@ def test_weights_of_a_long_cache(sp, d, kind, n, kv):
         assert torch.all((got[h] - want).abs() <= want * (2.0 ** -17 + 4 * n * 2.0 ** -24))
 
 
+@pytest.mark.parametrize("n,d,dtype,page", [(1, 64, "bf16", 16), (1, 128, "bf16", 16), (40, 64, "bf16", 16), (40, 128, "bf16", 64), (5, 64, "f32", 16),
+                                            (3, 64, "bf16", 7), (30, 128, "bf16", 7)])
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_weights_over_a_cache_of_any_scales(sp, kind, n, d, dtype, page):
+    """Scales that are no powers of two, tiny, negative and zero ones, as another program may have filled them in."""
+    import torch
+    rng = np.random.default_rng(18)
+    kv, H, H_kv = 200, 4, 2
+    cache, table, _, _ = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=[kv], kind=kind, dtype=torch_dtype(dtype))
+    scale = rng.uniform(0.5, 1.5, cache.k_scale.shape) * (1 / 64 if kind == "int8" else 1 / 128)
+    scale[rng.random(scale.shape) < 0.1] = 0
+    scale[rng.random(scale.shape) < 0.1] *= -1
+    scale[rng.random(scale.shape) < 0.1] *= 1e-20
+    cache.k_scale.copy_(torch.from_numpy(scale))
+    i = np.arange(kv)
+    codes = f64(cache.k.float())[table[0, i // page], :, i % page]
+    k = (codes * f64(cache.k_scale)[table[0, i // page], :, i % page][..., None]).transpose(1, 0, 2)
+    batch, _ = make_batch(sp, [n], [kv], table)
+    q = torch.from_numpy(rng.standard_normal((n, H, d))).to(torch_dtype(dtype)).cuda()
+    lse = torch.from_numpy(rng.uniform(4, 6, (H, n))).float().cuda()
+    w = sp.attend_weights(q, cache, batch, lse, sp.weights_alloc(cache), decay=0, check=True)
+    want, bound = oracle.kept.weights(f64(q), k, f64(lse), d ** -0.5, oracle.kept.visible(n, kv))
+    got = f64(w)[table[0, i // page], :, i % page].T
+    assert np.all(np.abs(got - want) <= bound + 2.0 ** -23 * want)
+
+
+@pytest.mark.parametrize("kind", ["same", "int8"])
+@pytest.mark.parametrize("n,d,dtype", [(1, 64, "bf16"), (40, 64, "bf16"), (40, 128, "bf16"), (2, 64, "f32")])
+def test_a_key_that_is_nan_has_a_weight_that_is_nan(sp, n, d, dtype, kind):
+    """And no other token's weight knows of it; a row whose normaliser is NaN reaches all that it sees."""
+    import torch
+    rng = np.random.default_rng(19)
+    kv, H, H_kv, page = 300, 4, 2, 16
+    cache, table, kval, _ = make_cache(sp, rng, H_kv=H_kv, d=d, page=page, kv=[kv], kind=kind, dtype=torch_dtype(dtype))
+    at = [5, 130, kv - 1]
+    for i in at:
+        if kind == "same":
+            cache.k[int(table[0, i // page]), 1, i % page, 3] = float("nan")
+        else:
+            cache.k_scale[int(table[0, i // page]), 1, i % page] = float("nan")
+    batch, _ = make_batch(sp, [n], [kv], table)
+    q = torch.from_numpy(rng.standard_normal((n, H, d))).to(torch_dtype(dtype)).cuda()
+    lse = torch.full((H, n), 6.0, device="cuda")
+    i = np.arange(kv)
+    got = f64(sp.attend_weights(q, cache, batch, lse, sp.weights_alloc(cache), decay=0, check=True))[table[0, i // page], :, i % page].T
+    nan = np.isnan(got)
+    assert not nan[0].any() and np.flatnonzero(nan[1]).tolist() == at
+    want, bound = oracle.kept.weights(f64(q), kval[0], f64(lse), d ** -0.5, oracle.kept.visible(n, kv))
+    assert np.all((np.abs(got - want) <= bound + 2.0 ** -23 * want) | nan)
+    lse[0, 0] = float("nan")
+    got = f64(sp.attend_weights(q, cache, batch, lse, sp.weights_alloc(cache), decay=0, check=True))[table[0, i // page], :, i % page].T
+    assert np.isnan(got[0, :kv - n + 1]).all() and not np.isnan(got[0, kv - n + 1:]).any()
+
+
+def test_weights_of_a_cache_beyond_2_31_entries(sp):
+    import torch
+    for d, n in ((64, 2), (128, 40), (96, 3)):
+        far = 5 * (1 << 29)
+        buf = torch.zeros(far + 8192 * 8, dtype=torch.bfloat16, device="cuda")
+        shape, stride = (2, 1, 64, d), (far, 64 * d, d, 1)
+        k, v = buf.as_strided(shape, stride), buf.as_strided(shape, stride, 64 * d)
+        g = torch.Generator(device="cuda").manual_seed(d)
+        k.copy_(torch.randn(shape, generator=g, device="cuda"))
+        batch, _ = make_batch(sp, [n], [110], np.array([[1, 0]], np.int32))
+        q = torch.randn(n, 2, d, generator=g, device="cuda").to(torch.bfloat16)
+        lse = torch.full((2, n), 5.0, device="cuda")
+        w = sp.attend_weights(q, sp.Cache(k, v), batch, lse, torch.full((2, 1, 64), 2.0, device="cuda"), check=True)
+        kk = f64(torch.cat([k[1], k[0]], 1))[:, :110]
+        want, bound = oracle.kept.weights(f64(q), kk, f64(lse), d ** -0.5, oracle.kept.visible(n, 110))
+        want[:, :110 - n] += 2
+        got = f64(torch.cat([w[1], w[0]], 1))
+        assert np.all(np.abs(got[:, :110] - want) <= bound + 2.0 ** -23 * want) and np.all(got[:, 110:] == 2)
+
+
 def test_weights_sum_to_the_rows(sp):
     """With lse as attend returns it, the weights of a sequence add up to its rows, whatever the batch."""
     import torch

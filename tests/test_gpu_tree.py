@@ -104,6 +104,23 @@ def test_bad_parents_are_roots_and_reported(sp):
     assert n.tolist() == [0, 2] and path.tolist() == [[-1, -1], [0, 1]] and nxt.tolist() == [-1, 1]
 
 
+def test_the_longest_chain_and_one_more(sp):
+    import torch
+    batch, cu = plain_batch(sp, [4096, 4097, 2], [5000, 4097, 9])
+    parent = np.concatenate([np.arange(n) - 1 for n in (4096, 4097, 2)])
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    seen = torch.full((batch.rows, 129), 7, dtype=torch.int32, device="cuda")
+    pos = torch.full((batch.rows,), 7, dtype=torch.int32, device="cuda")
+    sp.tree_seen(batch, i32(parent), seen=seen, positions=pos, ws=ws)
+    assert sp.sp_workspace_status(ws) == sp.SP_EDEVICE
+    assert pos[:4096].tolist() == list(range(904, 5000)) and torch.all(pos[4096:8193] == 7) and pos[8193:].tolist() == [7, 8]
+    assert torch.all(seen[4096:8193] == 7) and seen[8193:, 0].tolist() == [1, 3] and not seen[8193:, 1:].any()
+    bits = seen[:4096, :128].cpu().numpy().view(np.uint32)
+    t = np.arange(4096)[:, None]
+    inside = np.clip(t + 1 - 32 * np.arange(128), 0, 32).astype(np.uint64)
+    assert np.array_equal(bits, ((np.uint64(1) << inside) - np.uint64(1)).astype(np.uint32))
+
+
 @pytest.mark.parametrize("new", [[1], [0, 7, 33, 64, 0], [1, 31, 32, 100], [1000], [24] * 40])
 @pytest.mark.parametrize("agree", [0.0, 0.5, 1.0])
 def test_tree_accept(sp, new, agree):
@@ -291,3 +308,55 @@ def test_a_captured_tree_follows_its_bits(sp, n, dtype):
                 assert np.all(np.abs(f64(o["out"][rows]) - ref[0]) <= bound)
                 want, then = oracle.kept.accept(p[rows], draft[rows].tolist(), target[rows].tolist())
                 assert o["path"][b].tolist() == want + [-1] * (n - len(want)) and o["next"][b].item() == then
+
+
+def test_a_tree_over_a_cache_beyond_2_31_entries(sp):
+    import torch
+    for d, n in ((64, 4), (128, 70), (96, 5)):
+        far = 5 * (1 << 29)
+        buf = torch.zeros(far + 8192 * 8, dtype=torch.bfloat16, device="cuda")
+        shape, stride = (2, 1, 64, d), (far, 64 * d, d, 1)
+        k, v = buf.as_strided(shape, stride), buf.as_strided(shape, stride, 64 * d)
+        g = torch.Generator(device="cuda").manual_seed(d)
+        for t in (k, v):
+            t.copy_(torch.randn(shape, generator=g, device="cuda"))
+        cache = sp.Cache(k, v)
+        batch, _ = make_batch(sp, [n], [110], np.array([[1, 0]], np.int32))
+        q = torch.randn(n, 2, d, generator=g, device="cuda").to(torch.bfloat16)
+        parent = tree(np.random.default_rng(d), n, "random")
+        seen, _ = sp.tree_seen(batch, i32(parent), check=True)
+        out, _ = sp.attend_tree(q, cache, batch, seen, check=True)
+        kk, vv = (f64(torch.cat([t[1], t[0]], 1))[:, :110] for t in (k, v))
+        see = oracle.kept.tree_seen(parent)[0]
+        ref, ref_lse, top, spread = oracle.kept.attend(f64(q), kk, vv, d ** -0.5, oracle.kept.visible(n, 110, 0, see))
+        bound, _ = attend_bounds("bf16", d, 110, ref, spread, top, ref_lse)
+        assert np.all(np.abs(f64(out) - ref) <= bound)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_a_round_on_another_stream(sp, handle):
+    """All calls of a round on a stream of their own, by object and by handle, give what they give on the current one."""
+    import torch
+    rng = np.random.default_rng(16)
+    cache, table, _, _ = make_cache(sp, rng, H_kv=2, d=64, page=16, kv=[300, 90])
+    batch, _ = make_batch(sp, [6, 20], [300, 90], table, max_new=20)
+    q = torch.from_numpy(rng.standard_normal((26, 4, 64))).to(torch.bfloat16).cuda()
+    parent = i32(np.concatenate([tree(rng, 6, "random"), tree(rng, 20, "random")]))
+    tok = i32(rng.integers(0, 2, 26))
+
+    def round_(stream):
+        c = sp.Cache(cache.k.clone(), cache.v.clone())
+        torch.cuda.synchronize()
+        a = dict(stream=stream)
+        seen, pos = sp.tree_seen(batch, parent, **a)
+        out, lse = sp.attend_tree(q, c, batch, seen, **a)
+        w = sp.attend_weights(q, c, batch, lse, torch.zeros(c.pages, 2, 16, device="cuda"), **a)
+        path, n, nxt = sp.tree_accept(batch, parent, tok, tok, **a)
+        length = sp.cache_keep(c, batch, path, n, drafted=True, weights=w, **a)
+        kept, m = sp.cache_choose(c, batch, w, 40, first=2, last=3, **a)
+        torch.cuda.synchronize()
+        return [seen, pos, out, lse, w, path, n, nxt, length, kept, m, c.k, c.v]
+
+    s = torch.cuda.Stream()
+    for a, b in zip(round_(None), round_(s.cuda_stream if handle else s)):
+        assert torch.equal(a, b)
