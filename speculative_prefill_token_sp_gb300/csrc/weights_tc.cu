@@ -9,11 +9,15 @@
 // query rows' traffic would be 64 bytes a clock and SM, which L2 does not give.
 //
 // Per 256 x 128 logits the MMAs take 1024 cycles (d = 128; 512 at d = 64) and the exponentials as many (32 a clock and SM), so
-// both units are to be busy at the same time: S has two buffers for each key tile, and 16 warps (8 where an 8-bit cache's
-// conversion takes the registers) work on them.
+// both units are to be busy at the same time: S has two buffers for each key tile, and the eight adding warps empty one while
+// the MMAs fill the other.  What bounds it is neither unit: an adding warp issues an FMA and an ADD on pairs of weights and an
+// exponential a weight, about two cycles of its scheduler each, which is 1.2 times the exponentials' own time.
+// A chunk of 4096 tokens over 32768 (bf16, 32/8 heads of 128): 830 us, 1.24 PFLOP/s, of which reading the normalisers from shared
+// memory is some 60.  The last 32 of 131072 tokens from e4m3 (one row tile an item): 88 us, 1.5 TB/s of codes; there half of
+// the adding is 14 us, the conversion of codes 2.5, and an item's start, exchange and write the rest.
 //
 // Warp roles of a CTA (one per SM):
-//  * 16 (8) warps add up weights: those of tiles A and B, each 32 keys, and with 16 each half of the columns' blocks of 32;
+//  * eight warps add up weights: four of them 64 keys of both tiles for half of the columns' blocks of 32, four the other half;
 //  * eight warps, for an 8-bit cache only: make bf16 of its codes in the shared-memory tiles (their scales are factors of
 //    a thread's logits);
 //  * one issues the MMAs, one makes the TMA loads of keys, page by page, and of query rows, one reads the rows' normalisers.
@@ -41,7 +45,7 @@ struct Roles {
     static constexpr bool kSame = kKind == SP_CACHE_SAME;
     static constexpr int kAdd = 8, kMma = kAdd + (kSame ? 0 : 8), kTma = kMma + 1, kLse = kMma + 2;
     static constexpr int kThreads = 32 * (kMma + 4);
-    static constexpr int kAddRegs = kSame ? 216 : 136, kConvertRegs = 80, kSingleRegs = kSame ? 72 : 48;
+    static constexpr int kAddRegs = kSame ? 192 : 112, kConvertRegs = 80, kSingleRegs = kSame ? 120 : 96;
     static_assert(kAdd * kAddRegs + (kMma - kAdd) * kConvertRegs + 4 * kSingleRegs <= (kMma + 4) * (kSame ? 168 : 96),
                   "the roles' registers");
 };
@@ -98,16 +102,25 @@ struct Segment {
 struct Walk {
     int left, g, b, j, from;            // units (row tiles and kExtra an item) left; the next item and its first unit
     int was_b, was_g, was_ta;           // the last item, if it had one row tile
+    int have, blocks, tiles;            // the sequence that these are of: its key blocks, and the row tiles of all its new tokens
+    Seq s;
 
+    // (Nearly all items are seen by all new tokens of the sequence before: for these there is little to do, as every warp does it.)
     __device__ __forceinline__ bool next(const TcArgs& p, Segment& o) {
         while (left > 0) {
-            o.s = load_seq(p.w.a.batch, p.w.a.cache.page, b);
-            const int blocks = blocks_of(p, o.s);
+            if (have != b) {
+                s = load_seq(p.w.a.batch, p.w.a.cache.page, b);
+                blocks = blocks_of(p, s);
+                tiles = (s.n + p.tpt - 1) / p.tpt;
+                have = b;
+            }
+            o.s = s;
             if (j >= blocks) {          // the arrays were changed while the kernel ran
                 left = 0;
                 break;
             }
-            o.it = item_of(p, o.s, j);
+            if (!p.w.a.window && j * kBlock <= s.kv - s.n) o.it = Item{j * kBlock, 0, s.n, tiles};
+            else o.it = item_of(p, s, j);
             o.b = b;
             o.g = g;
             o.from = from;
@@ -167,7 +180,7 @@ __device__ __forceinline__ void plan(const TcArgs& p, int* starts, int64_t* sums
     }
     if (t == 0) {
         starts[B] = (int)base;
-        *out = Walk{0, 0, 0, 0, 0, -1, 0, 0};
+        *out = Walk{0, 0, 0, 0, 0, -1, 0, 0, -1, 0, 0, {}};
         p.cuts[blockIdx.x].first = 0;
     }
     __syncthreads();
@@ -203,7 +216,7 @@ __device__ __forceinline__ void plan(const TcArgs& p, int* starts, int64_t* sums
         const int64_t r = u - g * total;
         if (before <= r && r < before + mine) {
             const int from = (int)(r - before - visit(r - before));
-            *out = Walk{(int)left, g, seq, blk, from, -1, 0, 0};
+            *out = Walk{(int)left, g, seq, blk, from, -1, 0, 0, -1, 0, 0, {}};
             const Item it = item_of(p, load_seq(p.w.a.batch, page, seq), blk);
             if (from > 0 && from < it.tiles && shares.at(c - 1) <= u - from)
                 p.cuts[c] = Cut{1, seq, g, it.k0, shares.of(u - from + it.tiles - 1)};
@@ -479,7 +492,7 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
       if constexpr (!kSame) {
         // ------------------------------ conversion of 8-bit rows ------------------------------
         // A warp takes 16 rows of each tile.  Eight lanes read 128 bytes of codes, and a lane's 16 codes become two pieces of 16 bytes of
-        // the bf16 tile; half of the lanes store their second piece first, so that eight of them meet eight different banks.
+        // the bf16 tile.
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kConvertRegs));
         constexpr int kPieces = D / 16, kRounds = 16 * kPieces / 32;        // 16-byte pieces of a row of codes; of a lane
         const int r0 = (warp - W::kAdd) * 16;
@@ -490,22 +503,16 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
             for (int w = 0; w < (two_of(sg) ? 2 : 1); ++w) {
                 ok = wait_all(smem_u32(&r_full[rst]), ph_r, abort_flag, 62);
                 if (!ok) break;
-                uint4 codes[kRounds];
-#pragma unroll
-                for (int y = 0; y < kRounds; ++y) {
-                    const int i = y * 32 + lane;
-                    codes[y] = *reinterpret_cast<const uint4*>(r_ring + rst * L::kCodeBytes + (r0 * kPieces + i) * 16);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&r_empty[rst]));
-                if (++rst == rs) rst = 0, ph_r ^= 1;
                 ok = wait_all(smem_u32(&k_empty[st]), ph, abort_flag, 61);
                 if (!ok) break;
+                const uint8_t* from = r_ring + rst * L::kCodeBytes + (r0 * kPieces + lane) * 16;
                 uint8_t* tile = k_ring + st * L::kTileBytes;
-#pragma unroll
+                // (not unrolled: the roles' loops together do not fit into the instruction cache as it is)
+#pragma unroll 1
                 for (int y = 0; y < kRounds; ++y) {
                     const int i = y * 32 + lane, rr = r0 + i / kPieces, piece = i % kPieces;
-                    const uint32_t w4[4] = {codes[y].x, codes[y].y, codes[y].z, codes[y].w};
+                    const uint4 codes = *reinterpret_cast<const uint4*>(from + y * 512);
+                    const uint32_t w4[4] = {codes.x, codes.y, codes.z, codes.w};
                     uint32_t o[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) pairs_of<kKind, true>(w4[k], o[2 * k], o[2 * k + 1]);
@@ -514,6 +521,9 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
                     *reinterpret_cast<uint4*>(at + ((c0 ^ (rr & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                     *reinterpret_cast<uint4*>(at + (((c0 + 1) ^ (rr & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&r_empty[rst]));
+                if (++rst == rs) rst = 0, ph_r ^= 1;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&k_full[st]));
