@@ -12,13 +12,14 @@
 // both units are to be busy at the same time: S has two buffers for each key tile, and the eight adding warps empty one while
 // the MMAs fill the other.  What bounds it is neither unit: an adding warp issues an FMA and an ADD on pairs of weights and an
 // exponential a weight, about two cycles of its scheduler each, which is 1.2 times the exponentials' own time.
-// A chunk of 4096 tokens over 32768 (bf16, 32/8 heads of 128): 830 us, 1.24 PFLOP/s, of which reading the normalisers from shared
-// memory is some 60.  The last 32 of 131072 tokens from e4m3 (one row tile an item): 88 us, 1.5 TB/s of codes; there half of
-// the adding is 14 us, the conversion of codes 2.5, and an item's start, exchange and write the rest.
+// A chunk of 4096 tokens over 32768 (32/8 heads of 128): 825 us from bf16, 1.25 PFLOP/s, of which reading the normalisers from shared
+// memory is some 60, and 951 from e4m3.  The last 32 of 131072 tokens (one row tile an item): 68 us from e4m3, 59 from bf16; the adding
+// is 20 of them beside the rest, the conversion of codes 2, and 50 stay without either: starts, waits and the keys' way in.
 //
 // Warp roles of a CTA (one per SM):
-//  * eight warps add up weights: four of them 64 keys of both tiles for half of the columns' blocks of 32, four the other half;
-//  * eight warps, for an 8-bit cache only: make bf16 of its codes in the shared-memory tiles (their scales are factors of
+//  * eight warps add up weights: of a bf16 cache each has 64 keys of both tiles and every other 32 columns, of an 8-bit one 32 keys of
+//    one tile and all columns;
+//  * four warps, for an 8-bit cache only: make bf16 of its codes in the shared-memory tiles (their scales are factors of
 //    a thread's logits);
 //  * one issues the MMAs, one makes the TMA loads of keys, page by page, and of query rows, one reads the rows' normalisers.
 //
@@ -39,14 +40,15 @@ constexpr int kSmem = 227 * 1024;
 constexpr int kExtra = 1;               // what an item costs beside its row tiles, in row tiles
 constexpr int kMaxSeqs = 16384;         // their item counts are laid out in the (still empty) rings
 
-// Warps of a CTA by role.  setmaxnreg shares out the registers that the block was launched with: 384 threads of 168, or 640 of 96.
+// Warps of a CTA by role.  setmaxnreg shares out the registers that the block was launched with: 384 threads of 168, or 512 of 128 (eight converting
+// warps left the adding ones 112 registers: 72 us for 68, the last 32 of 131072 tokens).
 template <int kKind>
 struct Roles {
     static constexpr bool kSame = kKind == SP_CACHE_SAME;
-    static constexpr int kAdd = 8, kMma = kAdd + (kSame ? 0 : 8), kTma = kMma + 1, kLse = kMma + 2;
+    static constexpr int kAdd = 8, kConvert = kSame ? 0 : 4, kMma = kAdd + kConvert, kTma = kMma + 1, kLse = kMma + 2;
     static constexpr int kThreads = 32 * (kMma + 4);
-    static constexpr int kAddRegs = kSame ? 192 : 112, kConvertRegs = 80, kSingleRegs = kSame ? 120 : 96;
-    static_assert(kAdd * kAddRegs + (kMma - kAdd) * kConvertRegs + 4 * kSingleRegs <= (kMma + 4) * (kSame ? 168 : 96),
+    static constexpr int kAddRegs = kSame ? 192 : 168, kConvertRegs = 80, kSingleRegs = kSame ? 120 : 96;
+    static_assert(kAdd * kAddRegs + (kMma - kAdd) * kConvertRegs + 4 * kSingleRegs <= (kMma + 4) * (kSame ? 168 : 128),
                   "the roles' registers");
 };
 
@@ -249,39 +251,33 @@ __device__ __forceinline__ void fma2n(float& a, float& b, float x, float y, floa
         : "=f"(a), "=f"(b) : "f"(x), "f"(y), "f"(f), "f"(n), "f"(m));
 }
 
-// kCols logits each of two keys to weights 2^(f v - l) (nl = -l, of each column), those of the rows that see them added to za and zb.
+// 32 logits each of kN keys to weights 2^(f v - l) (nl = -l, of each column), those of the rows that see them added to z.
 // What is hidden is taken out last: a column of no row holds anything, and l or the scale in f may be NaN.
-template <bool kMasked, int kCols>
-__device__ __forceinline__ void add_weights(const float* va, const float* vb, float fa, float fb, const float* nl, uint32_t sees_a,
-                                            uint32_t sees_b, float (&za)[4], float (&zb)[4]) {
+template <bool kMasked, int kN>
+__device__ __forceinline__ void add_weights(const float* v, const float (&f)[kN], const float* nl, const uint32_t (&sees)[kN], float (&z)[kN][4]) {
 #pragma unroll
-    for (int c = 0; c < kCols; c += 16) {
-        float n[16], xa[16], xb[16];
+    for (int c = 0; c < 32; c += 16) {
+        float n[16], x[kN][16];
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(nl + c + i);
-            n[i] = x.x, n[i + 1] = x.y, n[i + 2] = x.z, n[i + 3] = x.w;
+            const float4 y = *reinterpret_cast<const float4*>(nl + c + i);
+            n[i] = y.x, n[i + 1] = y.y, n[i + 2] = y.z, n[i + 3] = y.w;
         }
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            fma2n(xa[i], xa[i + 1], va[c + i], va[c + i + 1], fa, n[i], n[i + 1]);
-            fma2n(xb[i], xb[i + 1], vb[c + i], vb[c + i + 1], fb, n[i], n[i + 1]);
-        }
+        for (int i = 0; i < 16; i += 2)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            xa[i] = ex2_approx(xa[i]);
-            if (kMasked && !(sees_a >> (c + i) & 1)) xa[i] = 0.f;
-        }
+            for (int w = 0; w < kN; ++w) fma2n(x[w][i], x[w][i + 1], v[32 * w + c + i], v[32 * w + c + i + 1], f[w], n[i], n[i + 1]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            xb[i] = ex2_approx(xb[i]);
-            if (kMasked && !(sees_b >> (c + i) & 1)) xb[i] = 0.f;
-        }
+        for (int w = 0; w < kN; ++w)
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            add2(za[i & 2], za[(i & 2) + 1], xa[i], xa[i + 1]);
-            add2(zb[i & 2], zb[(i & 2) + 1], xb[i], xb[i + 1]);
-        }
+            for (int i = 0; i < 16; ++i) {
+                x[w][i] = ex2_approx(x[w][i]);
+                if (kMasked && !(sees[w] >> (c + i) & 1)) x[w][i] = 0.f;
+            }
+#pragma unroll
+        for (int i = 0; i < 16; i += 2)
+#pragma unroll
+            for (int w = 0; w < kN; ++w) add2(z[w][i & 2], z[w][(i & 2) + 1], x[w][i], x[w][i + 1]);
     }
 }
 
@@ -340,8 +336,8 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < ks + qs + rs; ++i) {
-            mbar_init(smem_u32(&bars[i]), !kSame && i < ks ? 8 : 1);
-            mbar_init(smem_u32(&bars[L::kMostStages + i]), i < ks + qs ? 1 : 8);
+            mbar_init(smem_u32(&bars[i]), !kSame && i < ks ? W::kConvert : 1);
+            mbar_init(smem_u32(&bars[L::kMostStages + i]), i < ks + qs ? 1 : W::kConvert);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&s_full[i]), 2);             // the MMAs and the normalisers
@@ -372,112 +368,118 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
 
     if (warp < W::kAdd) {
         // ------------------------------ weights ------------------------------
-        // A warp has 32 keys of each tile, and every other block of 32 columns: a thread's two keys share what it reads of a column
+        // bf16: a warp has 32 keys of each tile, and every other block of 32 columns, since a thread's two keys share what it reads of a
+        // column.  8 bits: 32 keys of one tile and all columns, with nothing to exchange (whose items are mostly short: the last 32 of
+        // 131072 tokens 88 us with the exchange, 77 without)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(W::kAddRegs));
-        const int h = warp >> 2, row = (warp & 3) * 32 + lane;      // half of the blocks; key of the tile = TMEM lane
-        const uint32_t s_at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        constexpr int kN = kSame ? 2 : 1;       // keys of a thread
+        const int h = warp >> 2, row = (warp & 3) * 32 + lane;      // half of the blocks, or tile; key of the tile = TMEM lane
+        const uint32_t s_at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (kSame ? 0 : h * 128);
         const float f = a.scale * 1.4426950408889634f;
-        constexpr int kB = kSame ? 32 : 16;     // columns of a block
         int buf = 0;
         uint32_t ph_s = 0, ph_x = 0;
         bool ok = true;
-        // this thread's keys of an item: the place of their weights (-1: none), what is there (of the key that it writes: the first half
-        // tile A's, the second tile B's), and the scale of their rows
+        // the key of an item whose weight this thread writes (the first half tile A's, the second tile B's): the weight's place (-1:
+        // none), what is there, and the scale of its row
         struct Place {
             int64_t at;
-            float old, scale[2];
+            float old, scale;
         };
+        // the page that the next item will want, if it is of the same sequence
+        int then_b = -1, then_q = 0, then_pg = 0;
         auto place = [&](const Segment& x) {
-            Place r{-1, 0.f, {1.f, 1.f}};
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const int key = x.it.k0 + w * kKeys + row;
-                if (key >= x.s.kv || key < first_seen(x.s, a.window) || (kSame && w != h)) continue;
-                const int q = a.page_of(key), pg = __ldg(a.batch.table + (int64_t)x.b * a.batch.table_stride + q);
-                if ((unsigned)pg >= (unsigned)a.cache.pages) {
-                    bad[1] = 1;
-                    continue;
-                }
-                const int64_t at = scale_offset(a.cache, pg, x.g, key - q * a.cache.page);
-                if constexpr (!kSame) r.scale[w] = __ldg(a.cache.k_scale + at);
-                if (w != h) continue;
-                r.at = at;
-                if (key < x.s.kv - x.s.n && p.w.decay != 0.f && x.to == x.it.tiles && x.from == 0) r.old = p.w.weights[at];
+            Place r{-1, 0.f, 1.f};
+            const int key = x.it.k0 + h * kKeys + row;
+            if (key >= x.s.kv || key < first_seen(x.s, a.window)) return r;
+            const int32_t* table = a.batch.table + (int64_t)x.b * a.batch.table_stride;
+            const int q = a.page_of(key), pg = x.b == then_b && q == then_q ? then_pg : __ldg(table + q);
+            if (key + kBlock < x.s.kv) {
+                then_b = x.b;
+                then_q = a.page_of(key + kBlock);
+                then_pg = __ldg(table + then_q);
             }
+            if ((unsigned)pg >= (unsigned)a.cache.pages) {
+                bad[1] = 1;
+                return r;
+            }
+            r.at = scale_offset(a.cache, pg, x.g, key - q * a.cache.page);
+            if constexpr (!kSame) r.scale = __ldg(a.cache.k_scale + r.at);
+            if (key < x.s.kv - x.s.n && p.w.decay != 0.f && x.to == x.it.tiles && x.from == 0) r.old = p.w.weights[r.at];
             return r;
         };
         bool more = walk.next(p, sg);
-        Place cur = {-1, 0.f, {1.f, 1.f}};
+        Place cur = {-1, 0.f, 1.f};
         if (more) cur = place(sg);
         while (more && ok) {
             Segment next;
             const bool then = walk.next(p, next);
-            Place ahead = {-1, 0.f, {1.f, 1.f}};
+            Place ahead = {-1, 0.f, 1.f};
             if (then) ahead = place(next);
             const int ctx = sg.s.kv - sg.s.n;
-            const float fa = kSame ? f : f * cur.scale[0], fb = kSame ? f : f * cur.scale[1];
-            float total[2] = {0.f, 0.f};
+            float fs[kN], total[kN];
+#pragma unroll
+            for (int w = 0; w < kN; ++w) fs[w] = kSame ? f : f * cur.scale, total[w] = 0.f;
             int t0 = sg.it.ta + sg.from * p.tpt;
             for (int i = sg.from; i < sg.to; ++i, t0 += p.tpt) {
                 const int tokens = min(p.tpt, sg.it.tb - t0), rows = tokens * p.G;
                 ok = wait_all(smem_u32(&s_full[buf]), ph_s, abort_flag, 22);
                 if (!ok) break;
                 tc_fence_after();
-                const bool masked = sg.it.k0 + kBlock - 1 > ctx + t0 || (a.window && sg.it.k0 <= ctx + t0 + tokens - 1 - a.window) || rows % kB;
+                const bool masked = sg.it.k0 + kBlock - 1 > ctx + t0 || (a.window && sg.it.k0 <= ctx + t0 + tokens - 1 - a.window) || rows % 32;
                 const uint32_t at = s_at + buf * 256;
                 const float* nl = ls + buf * 128;
-                float za[4] = {0.f, 0.f, 0.f, 0.f}, zb[4] = {0.f, 0.f, 0.f, 0.f};
-                // 32 columns at a time, or 16 with fewer registers.  (The next ones on their way meanwhile took more registers than there
-                // are: a chunk of 4096 over 32768 903 us for 812.)
-#pragma unroll 1
-                for (int c = h * kB; c < rows; c += 2 * kB) {
-                    uint32_t sr[2 * kB];
-                    if constexpr (kB == 32) {
-                        tmem_ld32(at + c, sr);
-                        tmem_ld32(at + 128 + c, sr + kB);
-                        tmem_wait32(sr);
-                        keep32(sr + 32);
-                    } else {
-                        tmem_ld16(at + c, sr);
-                        tmem_ld16(at + 128 + c, sr + kB);
-                        tmem_wait32(sr);
-                    }
-                    const float* v = reinterpret_cast<const float*>(sr);
-                    if (masked) {
-                        uint32_t sees[2];           // the columns that see each key
+                float z[kN][4];
 #pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            const int ahead_of = sg.it.k0 + w * kKeys + row - ctx - t0;
+                for (int w = 0; w < kN; ++w)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) z[w][k] = 0.f;
+                // (The next columns on their way meanwhile took more registers than there are: a chunk of 4096 over 32768 903 us for 812.)
+#pragma unroll 1
+                for (int c = kSame ? h * 32 : 0; c < rows; c += 32 * kN) {
+                    uint32_t sr[32 * kN];
+                    tmem_ld32(at + c, sr);
+                    if constexpr (kN == 2) tmem_ld32(at + 128 + c, sr + 32);
+                    tmem_wait32(sr);
+                    if constexpr (kN == 2) keep32(sr + 32);
+                    const float* v = reinterpret_cast<const float*>(sr);
+                    uint32_t sees[kN];              // the columns that see each key
+                    if (masked) {
+#pragma unroll
+                        for (int w = 0; w < kN; ++w) {
+                            const int ahead_of = sg.it.k0 + (kSame ? w : h) * kKeys + row - ctx - t0;
                             const int hi = a.window ? min(max(ahead_of + a.window, 0), tokens) * p.G : rows, lo = min(max(ahead_of, 0), tokens) * p.G;
                             sees[w] = low_bits(hi - c) & ~low_bits(lo - c);
                         }
-                        add_weights<true, kB>(v, v + kB, fa, fb, nl + c, sees[0], sees[1], za, zb);
+                        add_weights<true, kN>(v, fs, nl + c, sees, z);
                     } else {
-                        add_weights<false, kB>(v, v + kB, fa, fb, nl + c, 0u, 0u, za, zb);
+                        add_weights<false, kN>(v, fs, nl + c, sees, z);
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&s_empty[buf]));
-                total[0] += (za[0] + za[1]) + (za[2] + za[3]);
-                total[1] += (zb[0] + zb[1]) + (zb[2] + zb[3]);
+#pragma unroll
+                for (int w = 0; w < kN; ++w) total[w] += (z[w][0] + z[w][1]) + (z[w][2] + z[w][3]);
                 ph_s ^= buf;
                 buf ^= 1;
             }
             if (!ok) break;
-            // The halves exchange their sums: the first half of the warps writes tile A's keys and the second half tile B's.  (No named
-            // barrier: a warp that gives up a wait would leave the others at it.)
-            ok = wait_all(smem_u32(&x_empty[1 - h]), ph_x ^ 1, abort_flag, 23);
-            if (!ok) break;
-            halves[(1 - h) * kKeys + row] = total[1 - h];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&x_full[1 - h]));
-            ok = wait_all(smem_u32(&x_full[h]), ph_x, abort_flag, 24);
-            if (!ok) break;
-            const float sum = h ? halves[kKeys + row] + total[1] : total[0] + halves[row];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&x_empty[h]));
-            ph_x ^= 1;
+            float sum = total[0];
+            if constexpr (kSame) {
+                // The halves exchange their sums: the first half of the warps writes tile A's keys and the second half tile B's.  (No named
+                // barrier: a warp that gives up a wait would leave the others at it.)
+                ok = wait_all(smem_u32(&x_empty[1 - h]), ph_x ^ 1, abort_flag, 23);
+                if (!ok) break;
+                halves[(1 - h) * kKeys + row] = total[1 - h];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&x_full[1 - h]));
+                ok = wait_all(smem_u32(&x_full[h]), ph_x, abort_flag, 24);
+                if (!ok) break;
+                sum = h ? halves[kKeys + row] + total[1] : total[0] + halves[row];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&x_empty[h]));
+                ph_x ^= 1;
+            }
             if (sg.from == 0 && sg.to == sg.it.tiles) {
                 if (cur.at >= 0) p.w.weights[cur.at] = p.w.decay != 0.f ? sum + p.w.decay * cur.old : sum;
             } else {
@@ -491,11 +493,11 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
     } else if (!kSame && warp < W::kMma) {
       if constexpr (!kSame) {
         // ------------------------------ conversion of 8-bit rows ------------------------------
-        // A warp takes 16 rows of each tile.  Eight lanes read 128 bytes of codes, and a lane's 16 codes become two pieces of 16 bytes of
+        // A warp takes 32 rows of each tile.  Eight lanes read 128 bytes of codes, and a lane's 16 codes become two pieces of 16 bytes of
         // the bf16 tile.
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kConvertRegs));
-        constexpr int kPieces = D / 16, kRounds = 16 * kPieces / 32;        // 16-byte pieces of a row of codes; of a lane
-        const int r0 = (warp - W::kAdd) * 16;
+        constexpr int kPieces = D / 16, kRounds = kPieces;        // 16-byte pieces of a row of codes; of a lane
+        const int r0 = (warp - W::kAdd) * 32;
         int st = 0, rst = 0;
         uint32_t ph = 1, ph_r = 0;
         bool ok = true;
@@ -507,8 +509,8 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
                 if (!ok) break;
                 const uint8_t* from = r_ring + rst * L::kCodeBytes + (r0 * kPieces + lane) * 16;
                 uint8_t* tile = k_ring + st * L::kTileBytes;
-                // (not unrolled: the roles' loops together do not fit into the instruction cache as it is)
-#pragma unroll 1
+                // (two rounds at a time: the roles' loops together do not fit into the instruction cache as it is)
+#pragma unroll 2
                 for (int y = 0; y < kRounds; ++y) {
                     const int i = y * 32 + lane, rr = r0 + i / kPieces, piece = i % kPieces;
                     const uint4 codes = *reinterpret_cast<const uint4*>(from + y * 512);
@@ -601,7 +603,9 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
         // ------------------------------ TMA ------------------------------
         // key tiles to their ring, codes to a ring of their own
         const sp_cache& c = a.cache;
-        const int rows_tile = p.G * p.tpt, boxes = kKeys / p.box;
+        const int rows_tile = p.G * p.tpt, boxes = kKeys / p.box, mine = lane & 15;
+        static_assert(kKeys / 8 <= 16, "boxes of a tile");
+        int then_b = -1, then_q = 0, then_pg = 0;       // the page that the next item will want, if it is of the same sequence
         uint64_t *t_full = kSame ? k_full : r_full, *t_empty = kSame ? k_empty : r_empty;
         uint8_t* t_ring = kSame ? k_ring : r_ring;
         constexpr int kBytes = kSame ? L::kTileBytes : L::kCodeBytes;
@@ -611,28 +615,34 @@ __global__ void __launch_bounds__(Roles<kKind>::kThreads, 1) weights_tc_kernel(c
         bool ok = true, first = true;
         while (ok && walk.next(p, sg)) {
             const int32_t* table = a.batch.table + (int64_t)sg.b * a.batch.table_stride;
-            const int seen = first_seen(sg.s, a.window);
-            for (int w = 0; w < (two_of(sg) ? 2 : 1); ++w) {
-                // this lane's box: its page (pages: none, which loads zeros) and its first slot
-                const int tok = sg.it.k0 + w * kKeys + lane * p.box;
-                int slot = 0, pg = (int)c.pages;
-                if (lane < boxes && tok < sg.s.kv && tok + p.box > seen) {
-                    const int q = a.page_of(tok), t = __ldg(table + q);
+            // this lane's box (lanes 0..15: of tile A, 16..31: of tile B): its page (pages: none, which loads zeros) and its first slot
+            const int tok = sg.it.k0 + (lane >> 4) * kKeys + mine * p.box;
+            int slot = 0, pg = (int)c.pages;
+            if (mine < boxes && tok < sg.s.kv) {
+                const int q = a.page_of(tok), t = sg.b == then_b && q == then_q ? then_pg : __ldg(table + q);
+                if (tok + kBlock < sg.s.kv) {
+                    then_b = sg.b;
+                    then_q = a.page_of(tok + kBlock);
+                    then_pg = __ldg(table + then_q);
+                }
+                if (tok + p.box > first_seen(sg.s, a.window)) {
                     if (t >= 0 && t < c.pages) pg = t, slot = tok - q * c.page;
                     else bad[1] = 1;
                 }
+            }
+            for (int w = 0; w < (two_of(sg) ? 2 : 1); ++w) {
                 ok = wait_all(smem_u32(&t_empty[kst]), ph_k, abort_flag, 41);
                 if (!ok) break;
                 const uint32_t bar = smem_u32(&t_full[kst]), at = smem_u32(t_ring) + kst * kBytes;
                 if (lane == 0) mbar_expect_tx(bar, kBytes);
                 __syncwarp();
-                if (lane < boxes) {
+                if (mine < boxes && lane >> 4 == w) {
                     if constexpr (kSame) {
 #pragma unroll
                         for (int ch = 0; ch < L::kChunks; ++ch)
-                            tma_load_4d(at + ch * (kKeys * 128) + lane * p.box * 128, &maps.k, ch * 64, slot, sg.g, pg, bar);
+                            tma_load_4d(at + ch * (kKeys * 128) + mine * p.box * 128, &maps.k, ch * 64, slot, sg.g, pg, bar);
                     } else {
-                        tma_load_4d(at + lane * p.box * D, &maps.k, 0, slot, sg.g, pg, bar);
+                        tma_load_4d(at + mine * p.box * D, &maps.k, 0, slot, sg.g, pg, bar);
                     }
                 }
                 ++k_loads;
