@@ -942,9 +942,11 @@ def _attend(q, cache, batch, seen, scale, window, out, lse, ws, stream, check):
 # ----------------------------------------------------------------------------
 
 def _check_ints(t, name, shape, device, dtype=None):
-    """An integer tensor of this shape (None: any extent) whose last axis is contiguous."""
+    """An integer tensor of this shape (None: any extent, of all axes but the first) whose last axis is contiguous."""
     dtype = dtype or _torch.int32
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device.index:
+    have = t.shape
+    if t.dtype is dtype and t.is_contiguous() and t.get_device() == device.index and \
+            (have == shape or (shape[-1] is None and len(have) == len(shape) and have[0] == shape[0])):
         return                  # nearly every call's: the rest takes four times as long
     if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
         want = ", ".join("*" if n is None else str(n) for n in shape)

@@ -5,11 +5,15 @@
 // find the k-th largest: a histogram in each CTA, added up over the cluster through distributed shared memory.  The tokens above it,
 // and the first of those that equal it, are written in order: every warp counts its part of the run, and the counts' prefix
 // sums say where it writes.  The weights are read from memory once (again in each pass by a cluster that does not hold them).
+// Eight lists of 131072 tokens cut to 8192: 20.5 us, 16 requests of 1K to 32K tokens with a list for all heads 12.1.  4 MB of weights are 1 us
+// of it: the rest is latency, of the loads (table, then weight), of four exchanges over the cluster, and of the writing.
 //
 // Moving reads each kept row once and writes it once.  In place a row's new slot may be another's old one.  The list is ascending, so
 // a row never moves back, and all rows of a round may be written once the rows of that round and of the ones before it have
 // been read: the cluster that has a (sequence, KV head, side) reads a round into registers, meets at its barrier and writes.
 // To other pages there is nothing to wait for.
+// 8192 of 131072 tokens, 8 heads of 128, bf16: 13.8 us (67 MB moved: 4.9 TB/s); 16 requests of int8 11.6; the accepted tokens of 64
+// trees 7.0, of which half is the check of the lists.
 #include "paged.cuh"
 
 #include <cooperative_groups.h>

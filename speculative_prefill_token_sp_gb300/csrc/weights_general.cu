@@ -7,7 +7,8 @@
 // once for all of them, goes through the lanes' registers while the next one is on its way.  A CTA's warps have different
 // keys; its unit is all keys that they hold at a time, and the units of all (sequence, KV head) pairs are cut into equal
 // runs.  Nothing is added up across threads but the dot products, so the same call gives the same bits.
-// Arithmetic is fp32 on the CUDA cores, and bounds the kernel for many rows.
+// Arithmetic is fp32 on the CUDA cores, and bounds the kernel for many rows: a chunk of 4096 tokens over 32768 (bf16, 32/8 heads of
+// 128), which the tensor-core kernel takes in 0.83 ms, is 143 ms here, and a step of 16 requests of 2K to 32K tokens 165 us for 27.
 #include "attend_split.cuh"
 
 #include <type_traits>

@@ -315,8 +315,7 @@ def test_cache_choose_of_long_caches(sp, kv, budget):
     page = 64
     per = [-(-c // page) for c in kv]
     pages = sum(per)
-    k = torch.zeros(1, dtype=torch.bfloat16, device="cuda").expand(pages * page * 8).as_strided((pages, 1, page, 8), (0, 0, 8, 1)) \
-        if False else torch.zeros(pages, 1, page, 8, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(pages, 1, page, 8, dtype=torch.bfloat16, device="cuda")
     cache = sp.Cache(k, k)
     table = np.zeros((len(kv), max(per)), np.int32)
     order = np.random.default_rng(3).permutation(pages)

@@ -168,10 +168,9 @@ def test_python_checks(sp):  # noqa: F811
         # on the CPU all along
         lambda: sp.tree_seen(batch, ids), lambda: sp.cache_choose(cache, batch, w, 8), lambda: sp.attend_weights(q, cache, batch, lse, w),
     ]
-    for i, call in enumerate(bad):
+    for call in bad:
         with pytest.raises(ValueError):
             call()
-            print(i)
 
 
 def test_oracle_of_a_tree():
