@@ -282,12 +282,12 @@ __device__ __forceinline__ void add_weights(const float* v, const float (&f)[kN]
 }
 
 // A wait of few instructions, as there are some twenty of them: with wait_bar's clock at each, the roles' loops fit less well into the
-// instruction cache.  It gives up after 2^26 looks, which take seconds.
+// instruction cache.  It gives up after 2^22 looks, of some 1.4 us each while nothing comes: 6 s.
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag, int where) {
     bool ok = true;
     for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
         if (n & 1023) continue;
-        if (*abort_flag == 0 && n >> 26 == 0) continue;
+        if (*abort_flag == 0 && n >> 22 == 0) continue;
         if (*abort_flag == 0) *abort_flag = where;
         ok = false;
         break;
