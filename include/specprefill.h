@@ -577,7 +577,7 @@ sp_status sp_attend_weights(const sp_rows* q, const sp_cache* cache, const sp_ba
  *   shared  0: a list for every KV head, by its own weights; otherwise one list a sequence, by the maximum over the KV heads
  *   kept    device int32: kept[b * kept_stride_seq + g * kept_stride_head + i] is the i-th kept token of sequence b and KV head
  *           g (0 if shared), ascending; -1 behind the last one, up to `budget`
- *   n_kept  device int64 [B]: min(kv_len[b], budget)
+ *   n_kept  device int64 [B]: min(kv_len[b], budget); not the batch's kv_len itself
  *
  * 0 <= first + last <= budget <= 2^30.  Workspace: sp_cache_workspace_size().  A sequence whose lengths are impossible keeps
  * nothing (n_kept 0); a token whose page index is out of range ranks lowest; either records SP_EDEVICE. */

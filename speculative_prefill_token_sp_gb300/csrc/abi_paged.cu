@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 
 namespace sp {
 
@@ -183,6 +184,28 @@ sp_status check_counts(const char* fn, const char* what, const void* p) {
     if (p && reinterpret_cast<uintptr_t>(p) % 8 == 0) return SP_OK;
     set_error("%s: null or misaligned %s", fn, what);
     return SP_EINVAL;
+}
+
+// An output that is written while the inputs are read is in none of their places.
+struct Span {
+    const void* p;
+    int64_t bytes;
+};
+sp_status check_apart(const char* fn, const char* what, Span out, std::initializer_list<Span> inputs) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(out.p);
+    for (const Span& in : inputs) {
+        const uintptr_t b = reinterpret_cast<uintptr_t>(in.p);
+        if (!a || !b || a >= b + (uintptr_t)in.bytes || b >= a + (uintptr_t)out.bytes) continue;
+        set_error("%s: %s is in the place of an array that is read meanwhile", fn, what);
+        return SP_EINVAL;
+    }
+    return SP_OK;
+}
+Span starts_of(const sp_batch* b) { return {b->cu_new, 8 * ((int64_t)b->B + 1)}; }
+Span lengths_of(const sp_batch* b) { return {b->kv_len, 8 * (int64_t)b->B}; }
+// n rows of `wide` words
+Span words_of(const void* p, int64_t n, int64_t stride, int64_t wide) {
+    return {p, n > 0 ? 4 * ((n - 1) * std::min<int64_t>(n > 1 ? stride : 0, (int64_t)1 << 28) + wide) : 0};
 }
 
 sp_status check_weights(const char* fn, const float* w) { return check_ints(fn, "weights", w); }
@@ -528,6 +551,10 @@ sp_status sp_tree_seen(const sp_batch* batch, const int32_t* parent, uint32_t* s
         set_error("%s: misaligned positions", fn);
         return SP_EINVAL;
     }
+    const Span parents = words_of(parent, batch->T, 1, 1);
+    if ((s = check_apart(fn, "seen", words_of(seen, batch->T, seen_stride, seen_words), {parents, starts_of(batch), lengths_of(batch)})) != SP_OK ||
+        (s = check_apart(fn, "positions", words_of(positions, batch->T, 1, 1), {parents, starts_of(batch), lengths_of(batch)})) != SP_OK)
+        return s;
     if ((s = check_workspace(fn, ws, ws_bytes, sizeof(WsHeader))) != SP_OK) return s;
     s = tree_seen_launch(*batch, parent, seen, seen_stride, seen ? seen_words : 1, positions, ws, static_cast<cudaStream_t>(stream));
     if (s == SP_OK) clear_error();
@@ -551,6 +578,12 @@ sp_status sp_tree_accept(const sp_batch* batch, const int32_t* parent, const int
         set_error("%s: misaligned next", fn);
         return SP_EINVAL;
     }
+    const Span p = words_of(parent, batch->T, 1, 1), d = words_of(draft, batch->T, 1, 1), t = words_of(target, batch->T, 1, 1);
+    const Span starts = starts_of(batch), lengths = lengths_of(batch);
+    if ((s = check_apart(fn, "path", words_of(path, batch->B, path_stride, batch->max_new), {p, d, t, starts, lengths})) != SP_OK ||
+        (s = check_apart(fn, "n_path", {n_path, 8 * (int64_t)batch->B}, {p, d, t, starts, lengths})) != SP_OK ||
+        (s = check_apart(fn, "next", words_of(next, batch->B, 1, 1), {p, d, t, starts, lengths})) != SP_OK)
+        return s;
     if ((s = check_workspace(fn, ws, ws_bytes, sizeof(WsHeader))) != SP_OK) return s;
     s = tree_accept_launch(*batch, parent, draft, target, path, path_stride, n_path, next, ws, static_cast<cudaStream_t>(stream));
     if (s == SP_OK) clear_error();
@@ -618,6 +651,7 @@ sp_status sp_cache_choose(const sp_cache* cache, const sp_batch* batch, const fl
         set_error("%s: the lists of kept overlap", fn);
         return SP_EINVAL;
     }
+    if ((s = check_apart(fn, "n_kept", {n_kept, 8 * (int64_t)batch->B}, {starts_of(batch), lengths_of(batch)})) != SP_OK) return s;
     if ((s = check_workspace(fn, ws, ws_bytes, sizeof(WsHeader))) != SP_OK) return s;
     s = cache_choose_launch(*cache, *batch, weights, shared != 0, budget, first, last, kept, kept_stride_seq, kept_stride_head, n_kept,
                             ws, static_cast<cudaStream_t>(stream));
@@ -644,10 +678,8 @@ sp_status sp_cache_keep(const sp_cache* cache, const sp_batch* batch, const int3
     if ((most > 0 && (s = check_ints(fn, "kept", kept)) != SP_OK) || (s = check_counts(fn, "n_kept", n_kept)) != SP_OK ||
         (s = check_counts(fn, "kv_out", kv_out)) != SP_OK)
         return s;
-    if (kv_out == batch->kv_len || kv_out == n_kept) {
-        set_error("%s: kv_out must be neither kv_len nor n_kept, which are read meanwhile", fn);
-        return SP_EINVAL;
-    }
+    if ((s = check_apart(fn, "kv_out", {kv_out, 8 * (int64_t)batch->B}, {starts_of(batch), lengths_of(batch), {n_kept, 8 * (int64_t)batch->B}})) != SP_OK)
+        return s;
     if (reinterpret_cast<uintptr_t>(to) % 4 || (to && (to_width < 1 || to_stride < 0))) {
         set_error("%s: to must be 4-byte aligned, with to_width >= 1 and to_stride >= 0", fn);
         return SP_EINVAL;

@@ -141,6 +141,16 @@ def test_tree_accept_refusals(sp, over):  # noqa: F811
     assert accept(sp, batch_of(sp), size=64) == sp.SP_ENOMEM
 
 
+def test_outputs_in_the_place_of_what_is_read_are_refused(sp):  # noqa: F811
+    c, b = cache_of(sp), batch_of(sp)           # cu_new at 64 (24 bytes), kv_len at 128 (16), rows of 40 bytes
+    for s in (choose(sp, c, b, n=128), choose(sp, c, b, n=136), choose(sp, c, b, n=120), choose(sp, c, b, n=80),
+              keep(sp, c, b, out=128), keep(sp, c, b, out=136), keep(sp, c, b, out=8200), keep(sp, c, b, out=8184), keep(sp, c, b, out=64),
+              seen(sp, b, pos=512), seen(sp, b, pos=548), seen(sp, b, seen=476), seen(sp, b, seen=None, pos=128),
+              accept(sp, b, path=512), accept(sp, b, path=1024), accept(sp, b, path=1572), accept(sp, b, path=1500), accept(sp, b, n=128),
+              accept(sp, b, n=1568), accept(sp, b, next=1024), accept(sp, b, next=80)):
+        assert s == sp.SP_EINVAL and "read meanwhile" in sp.sp_last_error()
+
+
 def test_python_checks(sp):  # noqa: F811
     import torch
     i64 = lambda *v: torch.tensor(v, dtype=torch.int64)                                         # noqa: E731
