@@ -13,7 +13,7 @@
 // the MMAs fill the other.  What bounds it is neither unit: an adding warp issues an FMA and an ADD on pairs of weights and an
 // exponential a weight, about two cycles of its scheduler each, which is 1.2 times the exponentials' own time.
 // A chunk of 4096 tokens over 32768 (32/8 heads of 128): 825 us from bf16, 1.25 PFLOP/s, of which reading the normalisers from shared
-// memory is some 60, and 951 from e4m3.  The last 32 of 131072 tokens (one row tile an item): 68 us from e4m3, 59 from bf16; the adding
+// memory is some 60, and 940 from e4m3.  The last 32 of 131072 tokens (one row tile an item): 68 us from e4m3, 59 from bf16; the adding
 // is 20 of them beside the rest, the conversion of codes 2, and 50 stay without either: starts, waits and the keys' way in.
 //
 // Warp roles of a CTA (one per SM):
@@ -811,7 +811,9 @@ sp_status weights_tc_launch(const WeightsProblem& w, void* ws, cudaStream_t st) 
     const bool same = a.cache.kind == SP_CACHE_SAME;
     const int tiles = 224 * 1024 / (kKeys * a.cache.d * 2);
     p.k_stages = same ? (a.cache.d == 128 ? 4 : 8) : (a.cache.d == 128 ? 3 : 6);
-    p.q_stages = same ? tiles - p.k_stages : (a.cache.d == 128 ? 2 : 4);
+    // (what is left of an 8-bit cache's 224 KB are tiles of codes, two in the place of one; a second row tile in theirs: a chunk of 4096
+    // over 32768 951 us for 940.  Two key tiles instead of three: the last 32 of 131072 81 us for 68.)
+    p.q_stages = same ? tiles - p.k_stages : (a.cache.d == 128 ? 1 : 2);
     const Space s = carve(p.P);
     char* base = static_cast<char*>(ws);
     p.hdr = static_cast<WsHeader*>(ws);
